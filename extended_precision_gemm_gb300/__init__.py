@@ -38,6 +38,8 @@ __all__ = [
     "qd_slice_gemm_tc", "qd_recombine_tc",
     "MD_TC_PARTS", "md_gemm_tc", "md_tc_layout", "md_tc_workspace_size", "md_split_bf16", "md_slice_gemm_tc",
     "md_recombine_tc",
+    "MX4", "MX4_FORMATS", "mx4_layout", "mx4_quantize", "mx4_dequantize", "mx4_tile_scales", "mx4_gemm",
+    "mx4_ff_weights", "mx4_ff_gated", "ACTIVATIONS", "ff_gated", "ff_gated_backward", "ff_gated_saved_size",
 ]
 
 SLICES = 8
@@ -125,6 +127,18 @@ _SIGNATURES = {
     "md_split_bf16": ([_int, _i64, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr, _ptr, _ptr, _ptr, _ptr], _int),
     "md_slice_gemm_tc": ([_int, _i64, _i64, _i64, _ptr, _ptr, _int, _ptr, _ptr], _int),
     "md_recombine_tc": ([_int, _i64, _i64, _ptr, _int, _ptr, _ptr, _ptr, _i64, _ptr], _int),
+    "dd_mx4_layout": ([_int, _i64, _i64, _ptr, _ptr], _int),
+    "dd_mx4_quantize": ([_int, _int, _int, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr, _ptr, _ptr], _int),
+    "dd_mx4_dequantize": ([_int, _int, _i64, _i64, _ptr, _i64, _ptr, _ptr, _ptr, _i64, _ptr], _int),
+    "dd_mx4_gemm": ([_int, _i64, _i64, _i64, _ptr, _i64, _ptr, _ptr, _ptr, _i64, _ptr, _ptr, ctypes.c_float, _int,
+                     _ptr, _i64, _ptr], _int),
+    "dd_mx4_ff_gated": ([_int, _int, _int, _i64, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr, _ptr, _ptr, _i64, _ptr,
+                         _ptr, _ptr, _i64, _ptr], _int),
+    "dd_ff_gated_saved_size": ([_int, _i64, _i64, _ptr], _int),
+    "dd_ff_gated": ([_int, _int, _i64, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr,
+                     ctypes.c_size_t, _ptr], _int),
+    "dd_ff_gated_backward": ([_int, _i64, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64,
+                              _ptr, ctypes.c_size_t, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr], _int),
 }
 
 
@@ -1006,3 +1020,10 @@ def md_recombine_tc(nparts: int, M: int, N: int, P, e, f, splits=None, C=None, s
     _check("md_recombine_tc", load().md_recombine_tc(nparts, M, N, P.data_ptr(), splits, e.data_ptr(), f.data_ptr(),
                                                      _vp(pc), _ld(C[0]), _stream_handle(stream)))
     return C
+
+
+# ---- 4-bit microscaled products and the gated feed-forward block ----
+
+from .low_precision import (  # noqa: E402
+    ACTIVATIONS, MX4, MX4_FORMATS, ff_gated, ff_gated_backward, ff_gated_saved_size, mx4_dequantize, mx4_ff_gated,
+    mx4_ff_weights, mx4_gemm, mx4_layout, mx4_quantize, mx4_tile_scales)

@@ -243,13 +243,16 @@ cudaError_t library_pool(cudaMemPool_t* pool, bool create) {
     return cudaSuccess;
 }
 
-// Stream-ordered allocation from the library's pool (cudaFreeAsync returns it).
-cudaError_t pool_alloc(void** ptr, size_t bytes, cudaStream_t st) {
+}  // namespace
+
+cudaError_t ddg::pool_alloc(void** ptr, size_t bytes, cudaStream_t st) {
     cudaMemPool_t pool = nullptr;
     cudaError_t err = library_pool(&pool, true);
     if (err != cudaSuccess) return err;
     return cudaMallocFromPoolAsync(ptr, bytes, pool, st);
 }
+
+namespace {
 
 // `peek` reads the slice GEMM's count of bounded waits that gave up: a count
 // that grew during the call makes it return DDGEMM_ERR_CUDA.
@@ -520,8 +523,11 @@ ddgemm_status dd_wait_timeouts(unsigned int* count) {
     if (s == DDGEMM_OK) s = from_cuda(read_and_reset_wait_timeouts_qd(&c));
     unsigned int m = 0;
     if (s == DDGEMM_OK) s = from_cuda(read_and_reset_wait_timeouts_tc(&d));
+    unsigned int f = 0, x = 0;
     if (s == DDGEMM_OK) s = from_cuda(read_and_reset_wait_timeouts_tc_md(&m));
-    *count = a + b + c + d + m;
+    if (s == DDGEMM_OK) s = from_cuda(read_and_reset_wait_timeouts_ff(&f));
+    if (s == DDGEMM_OK) s = from_cuda(read_and_reset_wait_timeouts_mx4(&x));
+    *count = a + b + c + d + m + f + x;
     return s;
 }
 

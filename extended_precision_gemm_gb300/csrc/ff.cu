@@ -1,0 +1,229 @@
+// ff.cu -- the gated feed-forward block in 16 bits,
+//   y = h Wd^T,  h = act(x Wg^T) * (x Wu^T)      (Wg, Wu: F x D, Wd: D x F)
+// and its gradients
+//   dh = dy Wd,  dg = dh * u * act'(g),  du = dh * act(g),
+//   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dWd = dy^T h,
+// as products on CTA pairs (tile_gemm.cuh) with the elementwise work in their
+// epilogues.  The training form keeps h (16 bits), a = act(g) and
+// b = u * act'(g): the backward pass is then dg = dh b, du = dh a and needs
+// neither g and u nor the activation again.
+#include "activation.cuh"
+#include "mx4.cuh"
+#include "tile_gemm.cuh"
+
+namespace ddg {
+namespace {
+
+// C = accumulators, rounded once.
+template <typename T>
+struct EpiStore {
+    static constexpr int GROUPS = 2;
+    T* C;
+    int64_t ldc, M, N;
+    bool vec;
+    template <class Release>
+    __device__ __forceinline__ void run(uint32_t acc, int64_t row, int nt, int group, int, Release release) const {
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+            const int c = group * 128 + j * 32;
+            uint32_t v[32];
+            tc5::ld32(acc + c, v);
+            if (j == 3) release();
+            float f[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+            if (row < M) store32(C + row * ldc, (int64_t)nt * 256 + c, N, vec, f);
+        }
+    }
+};
+
+// h = act(g) * u from accumulators of 128 columns of g and 128 of u, rounded to
+// 16 bits (the operand of the next product); SAVE: a = act(g), b = u act'(g).
+template <typename T, bool SAVE>
+struct EpiGate {
+    static constexpr int GROUPS = 2;
+    T* h;
+    float *a, *b;
+    int64_t ld, M, N;  // N: F rounded up to 64 (the planes' rows, ld)
+    int act;
+    template <class Release>
+    __device__ __forceinline__ void run(uint32_t acc, int64_t row, int nt, int group, int, Release release) const {
+#pragma unroll 1
+        for (int j = 0; j < 2; ++j) {
+            const int c = group * 64 + j * 32;
+            uint32_t g[32], u[32];
+            tc5::ld32(acc + c, g);
+            tc5::ld32(acc + 128 + c, u);
+            if (j == 1) release();
+            const int64_t col = (int64_t)nt * 128 + c;
+            if (row >= M || col >= N) continue;
+            float hv[32], av[32], bv[32];
+            with_activation(act, [&](auto tag) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    float da = 0.0f;
+                    activation<decltype(tag)::value, SAVE>(__uint_as_float(g[i]), av[i], da);
+                    hv[i] = av[i] * __uint_as_float(u[i]);
+                    bv[i] = __uint_as_float(u[i]) * da;
+                }
+            });
+            store32(h + row * ld, col, N, true, hv);
+            if (SAVE) {
+                store32(a + row * ld, col, N, true, av);
+                store32(b + row * ld, col, N, true, bv);
+            }
+        }
+    }
+};
+
+// dg = dh b, du = dh a, rounded to 16 bits (operands of the next products).
+template <typename T>
+struct EpiGateBackward {
+    static constexpr int GROUPS = 2;
+    const float *a, *b;
+    T *dg, *du;
+    int64_t ld, M, N;
+    template <class Release>
+    __device__ __forceinline__ void run(uint32_t acc, int64_t row, int nt, int group, int, Release release) const {
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+            const int c = group * 128 + j * 32;
+            uint32_t v[32];
+            tc5::ld32(acc + c, v);
+            if (j == 3) release();
+            const int64_t col = (int64_t)nt * 256 + c;
+            if (row >= M || col >= N) continue;
+#pragma unroll
+            for (int i = 0; i < 32; i += 16) {
+                uint32_t wa[2][8], wb[2][8], pg[8], pu[8];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    load_v8(a + row * ld + col + i + 8 * k, wa[k]);
+                    load_v8(b + row * ld + col + i + 8 * k, wb[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float d0 = __uint_as_float(v[i + 2 * k]), d1 = __uint_as_float(v[i + 2 * k + 1]);
+                    const uint32_t* qa = &wa[k / 4][2 * k % 8];
+                    const uint32_t* qb = &wb[k / 4][2 * k % 8];
+                    pg[k] = pack2<T>(d0 * __uint_as_float(qb[0]), d1 * __uint_as_float(qb[1]));
+                    pu[k] = pack2<T>(d0 * __uint_as_float(qa[0]), d1 * __uint_as_float(qa[1]));
+                }
+                store_v8(dg + row * ld + col + i, pg);
+                store_v8(du + row * ld + col + i, pu);
+            }
+        }
+    }
+};
+
+// Rows of `cols` 16-bit elements to a 16-byte aligned leading dimension.
+__global__ void __launch_bounds__(256) realign_kernel(const uint16_t* src, int64_t ld, int64_t rows, int64_t cols,
+                                                      uint16_t* dst, int64_t ldd) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t n = rows * cols;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / cols, c = i - r * cols;
+        dst[r * ldd + c] = src[r * ld + c];
+    }
+}
+
+cudaError_t map16(CUtensorMap* m, const Matrix16& x, bool mn_major) {
+    const int64_t ld = x.rows > 1 ? x.ld : round_up(x.cols, 8);
+    return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, x.p, x.cols, x.rows, ld * 2, 64, mn_major ? 64 : 128, true);
+}
+
+TileArgs tile_args(int64_t M, int64_t N, int64_t per_tile, int64_t K, int segs) {
+    TileArgs g = {};
+    g.mt = (int)((M + 255) / 256);
+    g.nt = (int)((N + per_tile - 1) / per_tile);
+    g.nk = (int)((K + 63) / 64);
+    g.segs = segs;
+    g.last_steps = (int)((K - (int64_t)(g.nk - 1) * 64 + 15) / 16);
+    return g;
+}
+
+// sum over segments of A_s B_s^T; A_MN: A is K x M, B_MN: B is K x N.
+template <int KIND, bool A_MN, bool B_MN, bool GATED, class Epi>
+cudaError_t product16(int64_t M, int64_t N, int64_t K, int segs, const Matrix16& A0, const Matrix16& A1,
+                      const Matrix16& B0, const Matrix16& B1, const Epi& epi, cudaStream_t st) {
+    TileMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    cudaError_t err = map16(&maps.a[0], A0, A_MN);
+    if (err == cudaSuccess) err = map16(&maps.b[0], B0, B_MN);
+    if (err == cudaSuccess && segs == 2) err = map16(&maps.a[1], A1, A_MN);
+    if (err == cudaSuccess && (segs == 2 || GATED)) err = map16(&maps.b[1], B1, B_MN);
+    if (err != cudaSuccess) return err;
+    return launch_tile_gemm<KIND, A_MN, B_MN, GATED>(tile_args(M, N, GATED ? 128 : 256, K, segs), maps, epi, st);
+}
+
+template <typename T>
+EpiStore<T> store_to(void* C, int64_t ldc, int64_t M, int64_t N) {
+    return EpiStore<T>{static_cast<T*>(C), ldc, M, N, (uintptr_t)C % 32 == 0 && (ldc * sizeof(T)) % 32 == 0};
+}
+
+template <int KIND, typename T>
+cudaError_t forward_typed(const FfForward& f, cudaStream_t st) {
+    const Matrix16 h{f.h, f.T, f.F, f.ld};
+    cudaError_t err;
+    if (f.a != nullptr)
+        err = product16<KIND, false, false, true>(
+            f.T, f.F, f.D, 1, f.x, f.x, f.wg, f.wu,
+            EpiGate<T, true>{static_cast<T*>(f.h), f.a, f.b, f.ld, f.T, round_up(f.F, 64), f.act}, st);
+    else
+        err = product16<KIND, false, false, true>(
+            f.T, f.F, f.D, 1, f.x, f.x, f.wg, f.wu,
+            EpiGate<T, false>{static_cast<T*>(f.h), nullptr, nullptr, f.ld, f.T, round_up(f.F, 64), f.act}, st);
+    if (err == cudaSuccess)
+        err = product16<KIND, false, false, false>(f.T, f.D, f.F, 1, h, h, f.wd, f.wd, store_to<T>(f.y, f.ldy, f.T, f.D),
+                                                   st);
+    return err;
+}
+
+template <int KIND, typename T>
+cudaError_t backward_typed(const FfBackward& f, cudaStream_t st) {
+    const Matrix16 h{const_cast<void*>(f.h), f.T, f.F, f.ld}, dg{f.dg, f.T, f.F, f.ld}, du{f.du, f.T, f.F, f.ld};
+    // dh = dy Wd: B is Wd, D x F (K x N)
+    cudaError_t err = product16<KIND, false, true, false>(
+        f.T, f.F, f.D, 1, f.dy, f.dy, f.wd, f.wd,
+        EpiGateBackward<T>{f.a, f.b, static_cast<T*>(f.dg), static_cast<T*>(f.du), f.ld, f.T, round_up(f.F, 64)}, st);
+    // dx = dg Wg + du Wu
+    if (err == cudaSuccess && f.dx != nullptr)
+        err = product16<KIND, false, true, false>(f.T, f.D, f.F, 2, dg, du, f.wg, f.wu,
+                                                  store_to<T>(f.dx, f.lddx, f.T, f.D), st);
+    // the weights' gradients: sums over the T rows of both operands
+    if (err == cudaSuccess && f.dwg != nullptr)
+        err = product16<KIND, true, true, false>(f.F, f.D, f.T, 1, dg, dg, f.x, f.x,
+                                                 store_to<T>(f.dwg, f.lddwg, f.F, f.D), st);
+    if (err == cudaSuccess && f.dwu != nullptr)
+        err = product16<KIND, true, true, false>(f.F, f.D, f.T, 1, du, du, f.x, f.x,
+                                                 store_to<T>(f.dwu, f.lddwu, f.F, f.D), st);
+    if (err == cudaSuccess && f.dwd != nullptr)
+        err = product16<KIND, true, true, false>(f.D, f.F, f.T, 1, f.dy, f.dy, h, h,
+                                                 store_to<T>(f.dwd, f.lddwd, f.D, f.F), st);
+    return err;
+}
+
+}  // namespace
+
+cudaError_t launch_realign(const Matrix16& src, const Matrix16& dst, cudaStream_t st) {
+    const int64_t n = src.rows * src.cols;
+    if (n == 0) return cudaSuccess;
+    const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 152 * 8);
+    return launch_pdl(realign_kernel, dim3(blocks), dim3(256), 0, st, static_cast<const uint16_t*>(src.p), src.ld,
+                      src.rows, src.cols, static_cast<uint16_t*>(dst.p), dst.ld);
+}
+
+cudaError_t launch_ff_forward(const FfForward& f, cudaStream_t st) {
+    return f.type == DDGEMM_BF16 ? forward_typed<kKindBF16, __nv_bfloat16>(f, st)
+                                 : forward_typed<kKindF16, __half>(f, st);
+}
+
+cudaError_t launch_ff_backward(const FfBackward& f, cudaStream_t st) {
+    return f.type == DDGEMM_BF16 ? backward_typed<kKindBF16, __nv_bfloat16>(f, st)
+                                 : backward_typed<kKindF16, __half>(f, st);
+}
+
+cudaError_t read_and_reset_wait_timeouts_ff(unsigned int* count) { return reset_tile_timeouts(count); }
+
+}  // namespace ddg

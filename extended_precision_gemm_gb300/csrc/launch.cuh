@@ -160,6 +160,97 @@ cudaError_t launch_recombine_tc_md(int nin, const int32_t* P, int splits, int64_
                                    cudaStream_t st);
 cudaError_t read_and_reset_wait_timeouts_tc_md(unsigned int* count);
 
+// ---- 4-bit microscaled matrices (mx4.cuh) and the gated block ----
+
+// rows x K: codes (ldq bytes a row), tiled scales, row exponents (nvfp4).
+struct Mx4Matrix {
+    const uint8_t* codes;
+    int64_t ldq;
+    const uint8_t* scales;
+    const int32_t* exponents;
+    int64_t rows, K;
+};
+// X (rows x K, or K x rows if cols) of type DDGEMM_F32 / _BF16 / _F16 into
+// codes, scales and (nvfp4) row exponents; column_max: `rows` words of
+// workspace, nvfp4 columns only.
+struct Mx4Quantize {
+    int fmt, type;
+    bool cols;
+    int64_t rows, K;
+    const void* X;
+    int64_t ldx;
+    uint8_t* codes;
+    int64_t ldq;
+    uint8_t* scales;
+    int32_t* exponents;
+    uint32_t* column_max;
+};
+cudaError_t launch_mx4_quantize(const Mx4Quantize& q, cudaStream_t st);
+cudaError_t launch_mx4_dequantize(int fmt, int type, int64_t rows, int64_t K, const uint8_t* codes, int64_t ldq,
+                                  const uint8_t* scales, const int32_t* exponents, void* X, int64_t ldx,
+                                  cudaStream_t st);
+// C (A.rows x B.rows) = alpha A B^T.
+struct Mx4Gemm {
+    int fmt, type;
+    Mx4Matrix A, B;
+    float alpha;
+    void* C;
+    int64_t ldc;
+};
+cudaError_t launch_mx4_gemm(const Mx4Gemm& g, cudaStream_t st);
+// act(x Wg^T) * (x Wu^T) with Wg and Wu in turn, 32 rows each, in W; into hq
+// (mxfp4) or h in 32 bits (nvfp4).
+struct Mx4Gate {
+    int fmt, act;
+    Mx4Matrix x, W, hq;
+    float* h;
+    int64_t ldh, F;
+};
+cudaError_t launch_mx4_gate(const Mx4Gate& g, cudaStream_t st);
+cudaError_t read_and_reset_wait_timeouts_mx4(unsigned int* count);
+
+// A row-major matrix of 16-bit elements.
+struct Matrix16 {
+    void* p;
+    int64_t rows, cols, ld;
+};
+cudaError_t launch_realign(const Matrix16& src, const Matrix16& dst, cudaStream_t st);
+// The gated block; operands 16-byte aligned with 16-byte rows.  h, a, b (and
+// dg, du): planes of T rows, ld elements apart (a multiple of 64, >= F).
+struct FfForward {
+    int type, act;
+    int64_t T, D, F;
+    Matrix16 x, wg, wu, wd;
+    void* h;
+    float *a, *b;  // null: no backward pass follows
+    int64_t ld;
+    void* y;
+    int64_t ldy;
+};
+cudaError_t launch_ff_forward(const FfForward& f, cudaStream_t st);
+struct FfBackward {
+    int type;
+    int64_t T, D, F;
+    Matrix16 dy, x, wg, wu, wd;
+    const void* h;
+    const float *a, *b;
+    void *dg, *du;
+    int64_t ld;
+    void* dx;  // any of the gradients may be null
+    int64_t lddx;
+    void* dwg;
+    int64_t lddwg;
+    void* dwu;
+    int64_t lddwu;
+    void* dwd;
+    int64_t lddwd;
+};
+cudaError_t launch_ff_backward(const FfBackward& f, cudaStream_t st);
+cudaError_t read_and_reset_wait_timeouts_ff(unsigned int* count);
+
+// Stream-ordered allocation from the library's pool (cudaFreeAsync returns it).
+cudaError_t pool_alloc(void** ptr, size_t bytes, cudaStream_t st);
+
 // The bounds-check records of the translation units with checks (all zero
 // unless the library was built with -DDDGEMM_CHECKED); each synchronises the
 // device, reads its record and clears it.

@@ -1,0 +1,187 @@
+// mx4.cuh -- the 4-bit microscaled matrix formats (declarations in ddgemm.h):
+// layout arithmetic shared by host and device, and the device routines that
+// turn 32-bit values into codes and scales.
+//
+// A matrix of `rows` rows of length K holds E2M1 codes, two to a byte along k
+// (the even k in the low nibble), and one scale byte per block of k:
+//   mxfp4: blocks of 32, scale 2^(byte - 127) (E8M0; 255 is NaN);
+//   nvfp4: blocks of 16, E4M3 scale, and an exponent e per row; a value is
+//          code * scale * 2^e.
+// The scales lie in tiles of 128 rows by 4 blocks (512 bytes), row r and block
+// b at (r % 32) * 16 + (r % 128 / 32) * 4 + b % 4: the order in which a tile
+// is copied into tensor memory, lane r % 32 and one 32-bit column for each 32
+// rows.  K is padded to MX4_TILE_K in the scales (byte 0) and to 32 in the
+// codes (code 0).
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace ddg {
+
+constexpr int MX4_TILE_K = 256;  // k of one 128-byte row of codes: a stage of the products
+
+constexpr int kMxfp4 = DDGEMM_MXFP4, kNvfp4 = DDGEMM_NVFP4;
+
+__host__ __device__ constexpr int mx4_block(int fmt) { return fmt == kMxfp4 ? 32 : 16; }
+// scale tiles (4 blocks of k) per MX4_TILE_K
+__host__ __device__ constexpr int mx4_tiles_per_k(int fmt) { return MX4_TILE_K / mx4_block(fmt) / 4; }
+__host__ __device__ inline int64_t mx4_scale_tiles(int fmt, int64_t K) {
+    return (K + MX4_TILE_K - 1) / MX4_TILE_K * mx4_tiles_per_k(fmt);
+}
+__host__ __device__ inline int64_t mx4_code_bytes(int64_t K) { return round_up(K, 32) / 2; }
+__host__ __device__ inline int64_t mx4_scale_bytes(int fmt, int64_t rows, int64_t K) {
+    return (rows + 127) / 128 * mx4_scale_tiles(fmt, K) * 512;
+}
+// Offset of the four scale bytes of row r in scale tile t of its 128 rows.
+__host__ __device__ inline int64_t mx4_scale_word(int64_t r, int64_t t, int64_t tiles) {
+    return ((r / 128) * tiles + t) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4;
+}
+
+#ifdef __CUDACC__
+
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+// 2^e as a float, -126 <= e <= 127.
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// x * 2^s for any |s| <= 252 in two steps of the same direction, so that no
+// partial result leaves the range before the whole does.
+__device__ __forceinline__ float scale_by_exp2(float x, int s) {
+    const int h = s / 2;
+    return x * exp2_int(h) * exp2_int(s - h);
+}
+
+// The E8M0 byte of a block whose largest magnitude has these bits:
+// floor(log2 max) - 2 (so that the largest value lies in [4, 8) before it
+// saturates at 6), 255 (NaN) where a value is infinite or NaN.
+__device__ __forceinline__ uint32_t mxfp4_scale_byte(uint32_t max_bits) {
+    if (max_bits >= kInfBits) return 255u;
+    const int b = (int)(max_bits >> 23) - 2;
+    return (uint32_t)(b > 0 ? b : 0);
+}
+// 1 / scale, a power of two; 0 for NaN.
+__device__ __forceinline__ float mxfp4_inverse(uint32_t byte) {
+    return byte == 255u ? 0.0f : __uint_as_float((254u - byte) << 23);
+}
+__device__ __forceinline__ float mxfp4_scale(uint32_t byte) {
+    return byte == 255u ? __uint_as_float(0x7fc00000u) : byte == 0u ? __uint_as_float(0x00400000u)
+                                                                    : __uint_as_float(byte << 23);
+}
+
+// The exponent of an nvfp4 row whose largest finite magnitude has these bits:
+// the least e >= -100 with max <= 6 * 448 * 2^e (2688 = 1.3125 * 2^11); 0 for
+// a zero row.
+__device__ __forceinline__ int nvfp4_row_exponent(uint32_t max_bits) {
+    if (max_bits == 0u) return 0;
+    const int e = (int)(max_bits >> 23) - 127 - ((max_bits & 0x7fffffu) <= 0x280000u ? 11 : 10);
+    return e > -100 ? e : -100;
+}
+
+__device__ __forceinline__ float e4m3_value(uint32_t byte) {
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((unsigned short)byte));
+    return __half2float(__ushort_as_half((unsigned short)(h2 & 0xffffu)));
+}
+
+// The E4M3 byte of an nvfp4 block: max / (6 * 2^e) rounded to nearest, at
+// least the smallest scale for a block that is not zero; 127 (NaN) where a
+// value is infinite or NaN.  `unit` is 2^-e.  The quotient of floats is
+// correctly rounded, and no quotient but a true tie of the E4M3 grid lands on
+// one (6 t has at most 8 significant bits, so max differs from it by at least
+// one of its own last places, more than half a last place of the quotient).
+__device__ __forceinline__ uint32_t nvfp4_scale_byte(uint32_t max_bits, float unit) {
+    if (max_bits >= kInfBits) return 127u;
+    if (max_bits == 0u) return 0u;
+    const float want = __fdiv_rn(__uint_as_float(max_bits) * unit, 6.0f);
+    unsigned short two;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.0f), "f"(want));
+    const uint32_t byte = two & 0xffu;
+    return byte > 0u ? byte : 1u;
+}
+
+// y / s with r = 1 / s correctly rounded: one residual correction of y * r
+// gives the correctly rounded quotient (Markstein's theorem), and rounding
+// that to E2M1 is the same as rounding the exact quotient: |y - t s| is at
+// least one last place of y for every tie point t (3 bits) but a true tie.
+__device__ __forceinline__ float quotient(float y, float s, float r) {
+    const float q = y * r;
+    return fmaf(fmaf(-q, s, y), r, q);
+}
+
+// Eight values (already divided by their scales) as eight E2M1 codes, the
+// first in the lowest nibble; to nearest, ties to even, saturating at 6.
+__device__ __forceinline__ uint32_t e2m1_pack8(const float (&y)[8]) {
+    uint32_t w;
+    asm("{\n"
+        " .reg .b8 t0, t1, t2, t3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 t0, %2, %1;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 t1, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 t2, %6, %5;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 t3, %8, %7;\n"
+        " mov.b32 %0, {t0, t1, t2, t3};\n"
+        "}\n"
+        : "=r"(w)
+        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+    return w;
+}
+
+__device__ __forceinline__ void e2m1_unpack8(uint32_t w, float (&y)[8]) {
+    uint32_t h[4];
+    asm("{\n"
+        " .reg .b8 t0, t1, t2, t3;\n"
+        " mov.b32 {t0, t1, t2, t3}, %4;\n"
+        " cvt.rn.f16x2.e2m1x2 %0, t0;\n"
+        " cvt.rn.f16x2.e2m1x2 %1, t1;\n"
+        " cvt.rn.f16x2.e2m1x2 %2, t2;\n"
+        " cvt.rn.f16x2.e2m1x2 %3, t3;\n"
+        "}\n"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        y[2 * i] = __half2float(__ushort_as_half((unsigned short)(h[i] & 0xffffu)));
+        y[2 * i + 1] = __half2float(__ushort_as_half((unsigned short)(h[i] >> 16)));
+    }
+}
+
+// ---- element types of inputs and outputs (DDGEMM_F32, _BF16, _F16) ----
+
+template <typename T> __device__ __forceinline__ float to_float(T v);
+template <> __device__ __forceinline__ float to_float<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <> __device__ __forceinline__ float to_float<__half>(__half v) { return __half2float(v); }
+template <typename T> __device__ __forceinline__ T from_float(float v);
+template <> __device__ __forceinline__ float from_float<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
+
+// Eight consecutive elements as floats; `vec`: the address is 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&y)[8]) {
+    constexpr int W = sizeof(T) * 8 / 16;
+    uint4 raw[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) raw[i] = reinterpret_cast<const uint4*>(p)[i];
+    const T* t = reinterpret_cast<const T*>(raw);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = to_float<T>(t[i]);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&y)[8]) {
+    constexpr int W = sizeof(T) * 8 / 16;
+    uint4 raw[W];
+    T* t = reinterpret_cast<T*>(raw);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = from_float<T>(y[i]);
+#pragma unroll
+    for (int i = 0; i < W; ++i) reinterpret_cast<uint4*>(p)[i] = raw[i];
+}
+
+#endif  // __CUDACC__
+
+}  // namespace ddg

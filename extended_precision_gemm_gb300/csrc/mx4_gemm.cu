@@ -1,0 +1,187 @@
+// mx4_gemm.cu -- products of matrices in 4-bit microscaled form
+// (C = alpha A B^T) and the two products of the 4-bit gated block.
+#include "activation.cuh"
+#include "mx4.cuh"
+#include "tile_gemm.cuh"
+
+namespace ddg {
+namespace {
+
+// The row exponents of an nvfp4 operand for 32 columns: lane i holds that of
+// column c + i (0 beyond N).
+__device__ __forceinline__ int column_exponent(const int32_t* f, int64_t c, int64_t N, int lane) {
+    return f != nullptr && c + lane < N ? f[c + lane] : 0;
+}
+
+// C = alpha * accumulators * 2^(e_i + f_j), rounded once.
+template <int KIND, typename T>
+struct EpiScale {
+    static constexpr int GROUPS = 3;
+    T* C;
+    int64_t ldc, M, N;
+    const int32_t *e, *f;
+    float alpha;
+    bool vec;
+    template <class Release>
+    __device__ __forceinline__ void run(uint32_t acc, int64_t row, int nt, int group, int lane, Release release) const {
+        const int er = KIND == kKindNv && row < M ? e[row] : 0;
+#pragma unroll 1
+        for (int j = 0; j < 2; ++j) {
+            const int c = group * 64 + j * 32;
+            const int64_t col = (int64_t)nt * 192 + c;
+            uint32_t v[32];
+            tc5::ld32(acc + c, v);
+            if (j == 1) release();
+            if (col >= N) continue;
+            float o[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(v[i]) * alpha;
+            if (KIND == kKindNv) {
+                const int fc = column_exponent(f, col, N, lane);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = scale_by_exp2(o[i], er + __shfl_sync(~0u, fc, i));
+            }
+            if (row < M) store32(C + row * ldc, col, N, vec, o);
+        }
+    }
+};
+
+// h = act(g) * u, both in 32 bits, from 32 columns of g and 32 of u in turn.
+// mxfp4: a thread holds a whole block of 32 of its row and writes its codes
+// and scale; the last tile also clears the scales of the padding of k.
+// nvfp4: h in 32 bits, for the row's exponent is not known yet.
+template <int KIND>
+struct EpiGate4 {
+    static constexpr int GROUPS = 3;
+    uint8_t *codes, *scales;
+    float* h;
+    int64_t ld;      // bytes of a row of codes (mxfp4), elements of a row of h (nvfp4)
+    int64_t M, F;
+    int nt;          // n tiles
+    const int32_t *e, *f;
+    int act;
+    template <class Release>
+    __device__ __forceinline__ void run(uint32_t acc, int64_t row, int n, int group, int lane, Release release) const {
+        uint32_t g[32], u[32];
+        tc5::ld32(acc + group * 64, g);
+        tc5::ld32(acc + group * 64 + 32, u);
+        release();
+        const int64_t c = (int64_t)n * 96 + group * 32;
+        float hv[32];
+        if (KIND == kKindNv) {
+            const int64_t wc = (int64_t)n * 192 + group * 64, W = round_up(F, 32) * 2;
+            const int er = row < M ? e[row] : 0;
+            const int fg = column_exponent(f, wc, W, lane), fu = column_exponent(f, wc + 32, W, lane);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                g[i] = __float_as_uint(scale_by_exp2(__uint_as_float(g[i]), er + __shfl_sync(~0u, fg, i)));
+                u[i] = __float_as_uint(scale_by_exp2(__uint_as_float(u[i]), er + __shfl_sync(~0u, fu, i)));
+            }
+        }
+        if (row >= M) return;
+        if (c < F) {
+            with_activation(act, [&](auto tag) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    float a, da;
+                    activation<decltype(tag)::value, false>(__uint_as_float(g[i]), a, da);
+                    hv[i] = a * __uint_as_float(u[i]);
+                }
+            });
+        }
+        if (KIND == kKindNv) {
+            if (c < F) store32(h + row * ld, c, F, true, hv);
+            return;
+        }
+        const int64_t tiles = mx4_scale_tiles(kMxfp4, F);
+        if (c < F) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(hv[i]) & 0x7fffffffu);
+            const uint32_t byte = mxfp4_scale_byte(m);
+            const float inv = mxfp4_inverse(byte);
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = hv[k * 8 + i] * inv;
+                w[k] = e2m1_pack8(y);
+            }
+            *reinterpret_cast<uint4*>(codes + row * ld + c / 2) = make_uint4(w[0], w[1], w[2], w[3]);
+            const int64_t b = c / 32;
+            scales[mx4_scale_word(row, b / 4, tiles) + b % 4] = (uint8_t)byte;
+        }
+        if (n == nt - 1 && group == 2)
+            for (int64_t b = (F + 31) / 32; b < tiles * 4; ++b) scales[mx4_scale_word(row, b / 4, tiles) + b % 4] = 0;
+    }
+};
+
+cudaError_t map_codes(CUtensorMap* m, const Mx4Matrix& x, int box_rows) {
+    const int64_t bytes = mx4_code_bytes(x.K), ld = x.rows > 1 ? x.ldq : round_up(bytes, 16);
+    return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, x.codes, bytes, x.rows, ld, 128, box_rows, true);
+}
+cudaError_t map_scales(CUtensorMap* m, int fmt, const Mx4Matrix& x) {
+    return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, x.scales, 128,
+                       (x.rows + 127) / 128 * mx4_scale_tiles(fmt, x.K), 512, 128, mx4_tiles_per_k(fmt), false);
+}
+
+template <int KIND, class Epi>
+cudaError_t product4(const Mx4Matrix& A, const Mx4Matrix& B, const Epi& epi, cudaStream_t st) {
+    constexpr int FMT = KIND == kKindMx ? kMxfp4 : kNvfp4;
+    TileMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    cudaError_t err = map_codes(&maps.a[0], A, 128);
+    if (err == cudaSuccess) err = map_codes(&maps.b[0], B, 96);
+    if (err == cudaSuccess) err = map_scales(&maps.sa, FMT, A);
+    if (err == cudaSuccess) err = map_scales(&maps.sb, FMT, B);
+    if (err != cudaSuccess) return err;
+    TileArgs g = {};
+    g.mt = (int)((A.rows + 255) / 256);
+    g.nt = (int)((B.rows + 191) / 192);
+    g.nk = (int)((A.K + MX4_TILE_K - 1) / MX4_TILE_K);
+    g.segs = 1;
+    g.last_steps = (int)((A.K - (int64_t)(g.nk - 1) * MX4_TILE_K + 63) / 64);
+    g.tiles_k = (int)mx4_scale_tiles(FMT, A.K);
+    return launch_tile_gemm<KIND, false, false, false>(g, maps, epi, st);
+}
+
+template <int KIND, typename T>
+cudaError_t gemm_typed(const Mx4Gemm& g, cudaStream_t st) {
+    T* C = static_cast<T*>(g.C);
+    const bool vec = (uintptr_t)C % 32 == 0 && (g.ldc * sizeof(T)) % 32 == 0;
+    return product4<KIND>(
+        g.A, g.B, EpiScale<KIND, T>{C, g.ldc, g.A.rows, g.B.rows, g.A.exponents, g.B.exponents, g.alpha, vec}, st);
+}
+
+template <int KIND>
+cudaError_t gemm_kind(const Mx4Gemm& g, cudaStream_t st) {
+    switch (g.type) {
+        case DDGEMM_F32: return gemm_typed<KIND, float>(g, st);
+        case DDGEMM_BF16: return gemm_typed<KIND, __nv_bfloat16>(g, st);
+        default: return gemm_typed<KIND, __half>(g, st);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_mx4_gemm(const Mx4Gemm& g, cudaStream_t st) {
+    return g.fmt == kMxfp4 ? gemm_kind<kKindMx>(g, st) : gemm_kind<kKindNv>(g, st);
+}
+
+cudaError_t launch_mx4_gate(const Mx4Gate& g, cudaStream_t st) {
+    const int nt = (int)((g.W.rows + 191) / 192);
+    if (g.fmt == kMxfp4)
+        return product4<kKindMx>(g.x, g.W,
+                                 EpiGate4<kKindMx>{const_cast<uint8_t*>(g.hq.codes), const_cast<uint8_t*>(g.hq.scales),
+                                                   nullptr, g.hq.ldq, g.x.rows, g.F, nt, nullptr, nullptr, g.act},
+                                 st);
+    return product4<kKindNv>(g.x, g.W,
+                             EpiGate4<kKindNv>{nullptr, nullptr, g.h, g.ldh, g.x.rows, g.F, nt, g.x.exponents,
+                                               g.W.exponents, g.act},
+                             st);
+}
+
+cudaError_t read_and_reset_wait_timeouts_mx4(unsigned int* count) { return reset_tile_timeouts(count); }
+
+}  // namespace ddg

@@ -1,0 +1,417 @@
+// tile_gemm.cuh -- matrix products on CTA pairs (tcgen05 cta_group::2) for the
+// 4-bit products and the gated feed-forward block: one persistent kernel,
+// templated on what its operands are and on the epilogue that takes the
+// accumulators.  Everything is in an unnamed namespace, so each including file
+// has its own count of bounded waits that gave up.
+//
+// D = sum over k of A[m, k] B[n, k].  A pair of CTAs on two SMs owns a tile of
+// 256 m by NT n: each CTA holds 128 rows of A, one half of the rows of B, and
+// 128 rows of the accumulators (f32, in tensor memory, twice: the MMAs of a
+// tile overlap the epilogue of the one before).  A stage of the shared-memory
+// ring is 128 bytes of k.  Warps: 0 copies (TMA), 1 issues the MMAs (even CTA
+// only), the others run the epilogue, four warps (128 rows) for each group of
+// columns.
+//
+// 16-bit operands: NT = 256, 64 k to a stage, either operand with k contiguous
+// or with its row index contiguous (64 x 64 blocks, the same swizzle); the
+// sum may run over two segments (A0 B0^T + A1 B1^T).
+// 4-bit operands: NT = 192, 256 k to a stage; two accumulators of 192 columns
+// leave 128 columns of tensor memory to the scales (16 for A's 128 rows, 32
+// for two tiles of 128 rows of B, twice).  A tile of B starts at a multiple of
+// 64 rows of a scale tile: its scales begin two columns into them.
+#pragma once
+
+#include <algorithm>
+
+#include "launch.cuh"
+#include "umma.cuh"
+
+namespace ddg {
+namespace {
+
+constexpr unsigned long long kTileWaitNs = 2000000000ULL;  // bounded waits: 2 s
+constexpr int kTileGroup = 8;  // m tiles that share their n tiles while these are in L2
+
+__device__ unsigned int g_tile_timeouts = 0;
+
+__device__ __forceinline__ void tile_timeout(volatile int* abort_flag) {
+    *abort_flag = 1;
+    atomicAdd(&g_tile_timeouts, 1u);
+}
+
+struct TileMaps {
+    CUtensorMap a[2], b[2];  // operands of the segments (gated: b[rank] by CTA)
+    CUtensorMap sa, sb;      // scales (4-bit kinds): tiles of 128 words
+};
+
+struct TileArgs {
+    int mt, nt;       // tiles along m and n
+    int pairs;        // CTA pairs in the grid
+    int nk, segs;     // stages of a segment, segments
+    int last_steps;   // MMAs in a segment's last stage
+    int tiles_k;      // 4-bit kinds: scale tiles in a row of 128
+};
+
+template <int KIND>
+struct TileShape {
+    static constexpr bool F4 = kind_is_4bit(KIND);
+    static constexpr int NT = F4 ? 192 : 256;
+    static constexpr int A_BYTES = 128 * 128, B_BYTES = NT / 2 * 128;
+    static constexpr int SCALE_TILES = F4 ? (KIND == kKindMx ? 2 : 4) : 0;  // per stage and 128 rows
+    static constexpr int SA_BYTES = SCALE_TILES * 512, SB_BYTES = 2 * SA_BYTES;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
+    static constexpr int STAGES = 6;
+    static constexpr int SMEM = STAGES * STAGE_BYTES + 1024;
+    static constexpr uint32_t SCALE_COL = 2 * NT, SCALE_COLS = 64;  // two sets
+    static_assert(STAGE_BYTES % 1024 == 0 && SMEM <= 227 * 1024, "shared memory");
+    static_assert(!F4 || SCALE_COL + 2 * SCALE_COLS <= 512, "tensor memory");
+};
+
+__device__ __forceinline__ void tile_of(const TileArgs& g, int64_t t, int& m, int& n) {
+    const int64_t per_group = (int64_t)kTileGroup * g.nt;
+    const int64_t group = t / per_group;
+    const int first = (int)group * kTileGroup, size = min(kTileGroup, g.mt - first);
+    m = first + (int)((t % per_group) % size);
+    n = (int)((t % per_group) / size);
+}
+
+// Epi: GROUPS, and run(acc, m row, n tile, group, lane, release): takes this
+// warp's 32 rows of the accumulators from column `acc` on (all lanes, also for
+// rows beyond the matrix) and calls release() after its last read of them.
+template <int KIND, bool A_MN, bool B_MN, bool GATED, class Epi>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROUPS, 1)
+    tile_gemm_kernel(const __grid_constant__ TileArgs g, const __grid_constant__ TileMaps maps,
+                     const __grid_constant__ Epi epi) {
+    using S = TileShape<KIND>;
+    constexpr int STAGES = S::STAGES, NT = S::NT;
+    constexpr bool F4 = S::F4;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[2 * STAGES + 5];
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int abort_flag;
+
+    const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int64_t pair = blockIdx.x >> 1;
+    const int64_t tiles = (int64_t)g.mt * g.nt;
+    const int per_tile = g.nk * g.segs;
+
+    const uint32_t full0 = smem_addr(&bars[0]), empty0 = smem_addr(&bars[STAGES]);
+    const uint32_t accf0 = smem_addr(&bars[2 * STAGES]), acce0 = smem_addr(&bars[2 * STAGES + 2]);
+    const uint32_t done_bar = smem_addr(&bars[2 * STAGES + 4]);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(full0 + 8 * i, 1);
+            mbar_init(empty0 + 8 * i, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(accf0 + 8 * b, 1);
+            mbar_init(acce0 + 8 * b, 2 * 4 * Epi::GROUPS);
+        }
+        mbar_init(done_bar, 1);
+        abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tc5::tmem_alloc_pair(smem_addr(&tmem_slot), 512);
+        tc5::tmem_relinquish_pair();
+    }
+    tc5::fence_before_sync();
+    cluster_sync();
+    tc5::fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+    pdl_launch_dependents();
+    pdl_wait();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---- copies; both CTAs' complete on the even CTA's barriers ----
+            const uint32_t full_lead0 = cluster_addr(full0, 0);
+            uint32_t stage = 0, phase = 0;
+            int64_t issued = 0;
+            for (int64_t t = pair; t < tiles && !abort_flag; t += g.pairs) {
+                int mt, nt;
+                tile_of(g, t, mt, nt);
+                const int a_row = (mt * 2 + (int)rank) * 128;
+                const int b_row = GATED ? nt * (NT / 2) : nt * NT + (int)rank * (NT / 2);
+                for (int it = 0; it < per_tile; ++it) {
+                    if (!mbar_wait_bounded(empty0 + 8 * stage, phase ^ 1, kTileWaitNs)) {
+                        tile_timeout(&abort_flag);
+                        break;
+                    }
+                    const int seg = it / g.nk, kb = it - seg * g.nk;
+                    const uint32_t dst = ring + stage * S::STAGE_BYTES, bar = full_lead0 + 8 * stage;
+                    const CUtensorMap* ma = &maps.a[seg];
+                    const CUtensorMap* mb = &maps.b[GATED ? rank : seg];
+                    if (leader) mbar_expect_tx(full0 + 8 * stage, 2u * S::STAGE_BYTES);
+                    constexpr int ROW = F4 ? 128 : 64;  // elements (bytes of codes) of a 128-byte row
+                    if (!A_MN) {
+                        tma_load_2d_group(dst, ma, kb * ROW, a_row, bar);
+                    } else {
+                        tma_load_2d_group(dst, ma, a_row, kb * 64, bar);
+                        tma_load_2d_group(dst + 8192, ma, a_row + 64, kb * 64, bar);
+                    }
+                    const uint32_t db = dst + S::A_BYTES;
+                    if (!B_MN) {
+                        tma_load_2d_group(db, mb, kb * ROW, b_row, bar);
+                    } else {
+                        tma_load_2d_group(db, mb, b_row, kb * 64, bar);
+                        tma_load_2d_group(db + 8192, mb, b_row + 64, kb * 64, bar);
+                    }
+                    if (F4) {
+                        const uint32_t ds = db + S::B_BYTES;
+                        const int t0 = kb * S::SCALE_TILES, rb = nt * NT / 128;
+                        tma_load_2d_group(ds, &maps.sa, 0, (mt * 2 + (int)rank) * g.tiles_k + t0, bar);
+                        tma_load_2d_group(ds + S::SA_BYTES, &maps.sb, 0, rb * g.tiles_k + t0, bar);
+                        tma_load_2d_group(ds + 2 * S::SA_BYTES, &maps.sb, 0, (rb + 1) * g.tiles_k + t0, bar);
+                    }
+                    ++issued;
+                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
+                }
+            }
+            // copies still in flight land before the CTA exits: the even CTA
+            // waits for its last stages to fill, the odd CTA (whose copies
+            // complete on the even CTA's barriers) for them to be consumed
+            const int64_t first = issued > STAGES ? issued - STAGES : 0;
+            for (int64_t j = first; j < issued; ++j) {
+                const uint32_t bar = (leader ? full0 : empty0) + 8 * (uint32_t)(j % STAGES);
+                if (!mbar_wait_bounded(bar, (uint32_t)((j / STAGES) & 1), kTileWaitNs)) {
+                    if (!abort_flag) tile_timeout(&abort_flag);
+                    break;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            // ---- MMAs ----
+            constexpr uint32_t IDESC = F4 ? tc5::idesc_e2m1(KIND == kKindMx, 256, NT)
+                                          : tc5::idesc_f16(KIND == kKindBF16, A_MN, B_MN, 256, NT);
+            constexpr uint64_t A_STEP = A_MN ? 2048 / 16 : 2, B_STEP = B_MN ? 2048 / 16 : 2;
+            const uint64_t ad0 = A_MN ? tc5::desc_mnmajor_sw128(ring, 8192) : tc5::desc_kmajor_sw128(ring);
+            const uint64_t bd0 = B_MN ? tc5::desc_mnmajor_sw128(ring + S::A_BYTES, 8192)
+                                      : tc5::desc_kmajor_sw128(ring + S::A_BYTES);
+            const uint64_t sd0 = tc5::desc_scale_tile(ring + S::A_BYTES + S::B_BYTES);
+            uint32_t stage = 0, phase = 0, count = 0;
+            bool ok = true, issued_any = false;
+            for (int64_t t = pair; t < tiles && ok; t += g.pairs, ++count) {
+                int mt, nt;
+                tile_of(g, t, mt, nt);
+                const uint32_t buf = count & 1;
+                const uint32_t d = tmem + buf * NT;
+                if (!mbar_wait_bounded(acce0 + 8 * buf, ((count >> 1) & 1) ^ 1, kTileWaitNs)) {
+                    if (!abort_flag) tile_timeout(&abort_flag);
+                    ok = false;
+                    break;
+                }
+                tc5::fence_after_sync();
+                int kb = 0;
+                for (int it = 0; it < per_tile; ++it) {
+                    if (!mbar_wait_bounded(full0 + 8 * stage, phase, kTileWaitNs)) {
+                        if (!abort_flag) tile_timeout(&abort_flag);
+                        ok = false;
+                        break;
+                    }
+                    tc5::fence_after_sync();
+                    const uint64_t off = (uint64_t)((stage * S::STAGE_BYTES) >> 4);
+                    const uint64_t ad = ad0 + off, bd = bd0 + off;
+                    const int steps = kb == g.nk - 1 ? g.last_steps : 4;
+                    if (++kb == g.nk) kb = 0;
+                    issued_any = true;
+                    if constexpr (F4) {
+                        const uint32_t sc = tmem + S::SCALE_COL + (it & 1) * S::SCALE_COLS;
+                        const uint64_t sd = sd0 + off;
+#pragma unroll
+                        for (int i = 0; i < S::SCALE_TILES; ++i) {
+                            tc5::cp_scales_pair(sc + i * 4, sd + i * 32);
+                            tc5::cp_scales_pair(sc + 16 + i * 8, sd + (S::SCALE_TILES + i) * 32);
+                            tc5::cp_scales_pair(sc + 16 + i * 8 + 4, sd + (2 * S::SCALE_TILES + i) * 32);
+                        }
+                        const uint32_t sbo = (uint32_t)(nt & 1) * 2;  // 192 nt is 64 rows into a tile for odd nt
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (j >= steps) break;
+                            const uint32_t acc = (it | j) != 0 ? 1u : 0u;
+                            if (KIND == kKindMx)
+                                tc5::mma_mx_pair(d, ad + A_STEP * j, bd + B_STEP * j,
+                                                 tc5::idesc_scale_byte(IDESC, (j & 1) * 2), sc + (j / 2) * 4,
+                                                 sc + 16 + (j / 2) * 8 + sbo, acc);
+                            else
+                                tc5::mma_nv_pair(d, ad + A_STEP * j, bd + B_STEP * j, IDESC, sc + j * 4,
+                                                 sc + 16 + j * 8 + sbo, acc);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (j >= steps) break;
+                            tc5::mma_f16_pair(d, ad + A_STEP * j, bd + B_STEP * j, IDESC, (it | j) != 0 ? 1u : 0u);
+                        }
+                    }
+                    tc5::commit_pair(empty0 + 8 * stage, 0x3);
+                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
+                }
+                if (!ok) break;
+                tc5::commit_pair(accf0 + 8 * buf, 0x3);
+            }
+            if (issued_any) {
+                tc5::commit_pair(done_bar, 0x3);
+                if (!mbar_wait_bounded(done_bar, 0, kTileWaitNs)) tile_timeout(&abort_flag);
+            }
+        } else if (lane == 0) {
+            // odd CTA: the MMAs read its shared memory and write its tensor memory
+            if (pair < tiles && !mbar_wait_bounded(done_bar, 0, kTileWaitNs * 4)) tile_timeout(&abort_flag);
+        }
+    } else {
+        // ---- epilogue ----
+        const int q = warp & 3, group = (warp - 2) >> 2;
+        uint32_t count = 0;
+        for (int64_t t = pair; t < tiles; t += g.pairs, ++count) {
+            int mt, nt;
+            tile_of(g, t, mt, nt);
+            const uint32_t buf = count & 1;
+            if (abort_flag || !mbar_wait_bounded(accf0 + 8 * buf, (count >> 1) & 1, kTileWaitNs)) {
+                if (!abort_flag) tile_timeout(&abort_flag);
+                break;
+            }
+            tc5::fence_after_sync();
+            const int64_t row = ((int64_t)mt * 2 + rank) * 128 + q * 32 + lane;
+            epi.run(tmem + buf * NT + ((uint32_t)(q * 32) << 16), row, nt, group, lane, [&]() {
+                tc5::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leader) mbar_arrive(acce0 + 8 * buf);
+                    else mbar_arrive_remote(acce0 + 8 * buf, 0);
+                }
+            });
+            __syncwarp();
+        }
+    }
+
+    // neither CTA leaves while its peer may still touch its shared memory
+    tc5::fence_before_sync();
+    cluster_sync();
+    tc5::fence_after_sync();
+    if (warp == 1) {
+        __syncwarp();
+        tc5::tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+int tile_sms() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 152;
+    return sms;
+}
+
+// Launch on as many CTA pairs as can be resident (never more than tiles).
+template <int KIND, bool A_MN, bool B_MN, bool GATED, class Epi>
+cudaError_t launch_tile_gemm(TileArgs g, const TileMaps& maps, const Epi& epi, cudaStream_t st) {
+    using S = TileShape<KIND>;
+    static std::atomic<int> cached[64];  // resident pairs per device; 0 = not asked yet
+    auto* kernel = tile_gemm_kernel<KIND, A_MN, B_MN, GATED, Epi>;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(64 + 128 * Epi::GROUPS);
+    cfg.dynamicSmemBytes = S::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    int pairs = cached[dev].load(std::memory_order_relaxed);
+    if (pairs <= 0) {
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        if (err != cudaSuccess) return err;
+        cfg.numAttrs = 1;
+        cfg.gridDim = dim3((unsigned)(2 * std::max(1, tile_sms() / 2)));
+        if (cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg) != cudaSuccess || pairs <= 0) {
+            (void)cudaGetLastError();
+            pairs = std::max(1, tile_sms() / 2);
+        } else {
+            cached[dev].store(pairs, std::memory_order_relaxed);
+        }
+    }
+    const int64_t tiles = (int64_t)g.mt * g.nt;
+    if (tiles <= 0) return cudaSuccess;
+    g.pairs = (int)std::min<int64_t>(pairs, tiles);
+    cfg.numAttrs = 2;
+    cfg.gridDim = dim3((unsigned)(2 * g.pairs));
+    return cudaLaunchKernelEx(&cfg, kernel, g, maps, epi);
+}
+
+cudaError_t reset_tile_timeouts(unsigned int* count) {
+    cudaError_t err = cudaDeviceSynchronize();
+    if (err != cudaSuccess) return err;
+    err = cudaMemcpyFromSymbol(count, g_tile_timeouts, sizeof(unsigned int));
+    if (err != cudaSuccess) return err;
+    const unsigned int zero = 0;
+    return cudaMemcpyToSymbol(g_tile_timeouts, &zero, sizeof(unsigned int));
+}
+
+// ---- pieces of epilogues ----
+
+__device__ __forceinline__ void store_v8(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+__device__ __forceinline__ void load_v8(const void* p, uint32_t (&w)[8]) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p)
+                 : "memory");
+}
+
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    uint32_t w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+    return w;
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+    uint32_t w;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+    return w;
+}
+
+// 32 values of a row from column c on, whole 32-byte sectors where the row is
+// 32-byte aligned (vec) and all 32 columns exist.
+template <typename T>
+__device__ __forceinline__ void store32(T* row, int64_t c, int64_t N, bool vec, const float (&v)[32]) {
+    if (vec && c + 32 <= N) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[i + j]);
+                store_v8(row + c + i, w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 16) {
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = pack2<T>(v[i + 2 * j], v[i + 2 * j + 1]);
+                store_v8(row + c + i, w);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (c + i < N) row[c + i] = from_float<T>(v[i]);
+    }
+}
+
+}  // namespace
+}  // namespace ddg

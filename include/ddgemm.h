@@ -673,12 +673,128 @@ int dd_checked_build(void);
 ddgemm_status dd_check_report(unsigned int* count, unsigned int* site, int64_t* index);
 
 /*
- * Number of times a slice-GEMM thread block (any variant) gave up waiting
+ * Number of times a slice-GEMM thread block (any variant), or one of the 4-bit
+ * products or of the gated block, gave up waiting
  * for its operand copies on the current device (each wait is bounded in time; a block that
  * gives up stops early and its P tile is incomplete).  Synchronises the
  * device, reads the counter and resets it to 0.  Zero in normal operation.
  */
 ddgemm_status dd_wait_timeouts(unsigned int* count);
+
+/* ------------------------------------------------------------------ */
+/* 4-bit microscaled matrices                                           */
+/* ------------------------------------------------------------------ */
+
+/*
+ * A matrix of `rows` rows of length K in 4-bit microscaled form: E2M1 codes
+ * (sign, then 0, 0.5, 1, 1.5, 2, 3, 4, 6) and one scale byte for every block
+ * of k, the blocks of a row sharing a power of two where the format says so.
+ *   DDGEMM_MXFP4: blocks of 32; scale 2^(byte - 127), byte - 127 =
+ *     floor(log2 max|x|) - 2 over the block (at least -127).
+ *   DDGEMM_NVFP4: blocks of 16; scale E4M3, max|x| / (6 2^e) rounded to
+ *     nearest (at least 2^-9 unless the block is zero), with an exponent e for
+ *     each row: the least e >= -100 with max|row| <= 2688 2^e, 0 for a zero
+ *     row.  A value is code * scale * 2^e.
+ * A value becomes the code nearest to x / scale, ties to the even code,
+ * saturating at 6.  A block that holds an infinity or a NaN gets the scale
+ * NaN (bytes 255 and 127) and its values are NaN; the exponent of an nvfp4
+ * row goes by its finite values.
+ *
+ * Layout.  codes: one row after the other, ld bytes apart (a multiple of 16,
+ * at least K / 2 rounded up to 16), two codes to a byte, the even k in the low
+ * nibble; codes from K up to the next multiple of 32 are 0.  scales: tiles of
+ * 128 rows by 4 blocks, 512 bytes each, all tiles of 128 rows one after the
+ * other; row r and block b at (r % 32) * 16 + (r % 128 / 32) * 4 + b % 4 of
+ * their tile.  A row's scales cover K rounded up to 256; those beyond K are 0.
+ * Scales of rows beyond the last are not read into any result and need not be
+ * set.  exponents: int32 per row (nvfp4; ignored, may be NULL, for mxfp4).
+ * codes and scales start on 16-byte boundaries.
+ */
+#define DDGEMM_MXFP4 0
+#define DDGEMM_NVFP4 1
+#define DDGEMM_MX4_MAX_K (1 << 22)
+#define DDGEMM_MX4_MAX_ROWS (1 << 28)
+
+/* Element types of plain matrices. */
+#define DDGEMM_F32 0
+#define DDGEMM_BF16 1
+#define DDGEMM_F16 2
+
+/* Bytes of a row of codes (the least ld) and of all scales. */
+ddgemm_status dd_mx4_layout(int format, int64_t rows, int64_t K, int64_t* code_row_bytes, int64_t* scale_bytes);
+
+/*
+ * Quantise X (of `type`): its rows (columns = 0: X is rows x K, ldx >= K), or
+ * its columns (columns = 1: X is K x rows, ldx >= rows; row i of the result is
+ * column i of X), like dd_split_rows and dd_split_cols.
+ */
+ddgemm_status dd_mx4_quantize(int format, int type, int columns, int64_t rows, int64_t K, const void* X, int64_t ldx,
+                              uint8_t* codes, int64_t ldq, uint8_t* scales, int32_t* exponents, void* stream);
+
+/* The values a 4-bit matrix stands for, rounded to `type` (exact in F32 and
+ * BF16 but for underflow): X is rows x K, ldx >= K. */
+ddgemm_status dd_mx4_dequantize(int format, int type, int64_t rows, int64_t K, const uint8_t* codes, int64_t ldq,
+                                const uint8_t* scales, const int32_t* exponents, void* X, int64_t ldx, void* stream);
+
+/*
+ * C = alpha * A * B^T for 4-bit matrices A (M x K) and B (N x K) of the same
+ * format, on the block-scaled tensor cores (tcgen05): products summed in 32
+ * bits, C rounded once to `type` (M x N, ldc >= N).  A K x N matrix B of the
+ * other entry points is quantised with columns = 1.  K = 0 writes zeros.
+ */
+ddgemm_status dd_mx4_gemm(int format, int64_t M, int64_t N, int64_t K, const uint8_t* A_codes, int64_t lda,
+                          const uint8_t* A_scales, const int32_t* A_exponents, const uint8_t* B_codes, int64_t ldb,
+                          const uint8_t* B_scales, const int32_t* B_exponents, float alpha, int type, void* C,
+                          int64_t ldc, void* stream);
+
+/* ------------------------------------------------------------------ */
+/* The gated feed-forward block                                         */
+/* ------------------------------------------------------------------ */
+
+#define DDGEMM_ACT_SILU 0       /* g / (1 + exp(-g)) */
+#define DDGEMM_ACT_GELU 1       /* g (1 + erf(g / sqrt 2)) / 2 */
+#define DDGEMM_ACT_GELU_TANH 2  /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+#define DDGEMM_ACT_RELU 3       /* max(g, 0) */
+#define DDGEMM_FF_MAX (1 << 28) /* bound on T, D and F */
+
+/*
+ * y = h Wd^T with h = act(x Wg^T) * (x Wu^T): x T x D, Wg and Wu F x D, Wd
+ * D x F, y T x D, all of `type` (DDGEMM_BF16 or DDGEMM_F16), any leading
+ * dimensions.  Sums, the activation and the product are in 32 bits; h is
+ * rounded to `type` between the two products.  `saved`, if not NULL, receives
+ * what the backward pass needs (dd_ff_gated_saved_size bytes, 256-byte
+ * aligned; opaque, of the library's version that wrote it).
+ */
+ddgemm_status dd_ff_gated_saved_size(int type, int64_t T, int64_t F, size_t* bytes);
+ddgemm_status dd_ff_gated(int type, int activation, int64_t T, int64_t D, int64_t F, const void* x, int64_t ldx,
+                          const void* Wg, int64_t ldwg, const void* Wu, int64_t ldwu, const void* Wd, int64_t ldwd,
+                          void* y, int64_t ldy, void* saved, size_t saved_bytes, void* stream);
+
+/*
+ * The gradients of the block from dy (T x D): dx (T x D), dWg and dWu (F x D)
+ * and dWd (D x F), each written (not added to); one that is NULL is not
+ * computed.  dh = dy Wd; dg = dh u act'(g) and du = dh act(g) are rounded to
+ * `type` before the products they enter.  `saved` is that of dd_ff_gated on
+ * the same T, F and type.
+ */
+ddgemm_status dd_ff_gated_backward(int type, int64_t T, int64_t D, int64_t F, const void* dy, int64_t lddy,
+                                   const void* x, int64_t ldx, const void* Wg, int64_t ldwg, const void* Wu,
+                                   int64_t ldwu, const void* Wd, int64_t ldwd, const void* saved, size_t saved_bytes,
+                                   void* dx, int64_t lddx, void* dWg, int64_t lddwg, void* dWu, int64_t lddwu,
+                                   void* dWd, int64_t lddwd, void* stream);
+
+/*
+ * The block on 4-bit operands, for serving: x (T x D, of `type`) is quantised
+ * along D, h along F (from its 32-bit values), both products run as
+ * dd_mx4_gemm, y is of `type`.  W_in holds Wg and Wu in turn, 32 rows of Wg
+ * then the same 32 of Wu, the last groups filled up with zero rows: 2 *
+ * (F rounded up to 32) rows of length D.  W_out is Wd: D rows of length F.
+ */
+ddgemm_status dd_mx4_ff_gated(int format, int type, int activation, int64_t T, int64_t D, int64_t F, const void* x,
+                              int64_t ldx, const uint8_t* in_codes, int64_t ld_in, const uint8_t* in_scales,
+                              const int32_t* in_exponents, const uint8_t* out_codes, int64_t ld_out,
+                              const uint8_t* out_scales, const int32_t* out_exponents, void* y, int64_t ldy,
+                              void* stream);
 
 #ifdef __cplusplus
 }
