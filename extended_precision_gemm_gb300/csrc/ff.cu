@@ -9,6 +9,7 @@
 // neither g and u nor the activation again.
 #include "activation.cuh"
 #include "mx4.cuh"
+#include "split_gemm.cuh"
 #include "tile_gemm.cuh"
 
 namespace ddg {
@@ -116,6 +117,38 @@ struct EpiGateBackward {
     }
 };
 
+// The same two epilogues for the split kernel: one value per lane.
+template <typename T>
+struct EpiSplitStore {
+    static constexpr int UNITS = 1;
+    T* C;
+    int64_t ldc, N;
+    __device__ __forceinline__ void emit(float v, float, int64_t m, int unit, int lane, int tile) const {
+        const int64_t n = (int64_t)tile * 128 + unit * 32 + lane;
+        if (n < N) C[m * ldc + n] = from_float<T>(v);
+    }
+};
+
+template <typename T>
+struct EpiSplitGate {
+    static constexpr int UNITS = 2;
+    T* h;
+    float *a, *b;  // null: no backward pass follows
+    int64_t ld, N;
+    int act;
+    __device__ __forceinline__ void emit(float g, float u, int64_t m, int unit, int lane, int tile) const {
+        const int64_t n = (int64_t)tile * 64 + unit * 32 + lane;
+        if (n >= N) return;
+        float av = 0.0f, da = 0.0f;
+        with_activation(act, [&](auto tag) { activation<decltype(tag)::value, true>(g, av, da); });
+        h[m * ld + n] = from_float<T>(av * u);
+        if (a != nullptr) {
+            a[m * ld + n] = av;
+            b[m * ld + n] = u * da;
+        }
+    }
+};
+
 // Rows of `cols` 16-bit elements to a 16-byte aligned leading dimension.
 __global__ void __launch_bounds__(256) realign_kernel(const uint16_t* src, int64_t ld, int64_t rows, int64_t cols,
                                                       uint16_t* dst, int64_t ldd) {
@@ -128,9 +161,9 @@ __global__ void __launch_bounds__(256) realign_kernel(const uint16_t* src, int64
     }
 }
 
-cudaError_t map16(CUtensorMap* m, const Matrix16& x, bool mn_major) {
+cudaError_t map16(CUtensorMap* m, const Matrix16& x, int box_rows) {
     const int64_t ld = x.rows > 1 ? x.ld : round_up(x.cols, 8);
-    return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, x.p, x.cols, x.rows, ld * 2, 64, mn_major ? 64 : 128, true);
+    return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, x.p, x.cols, x.rows, ld * 2, 64, box_rows, true);
 }
 
 TileArgs tile_args(int64_t M, int64_t N, int64_t per_tile, int64_t K, int segs) {
@@ -149,13 +182,36 @@ cudaError_t product16(int64_t M, int64_t N, int64_t K, int segs, const Matrix16&
                       const Matrix16& B0, const Matrix16& B1, const Epi& epi, cudaStream_t st) {
     TileMaps maps;
     memset(&maps, 0, sizeof(maps));
-    cudaError_t err = map16(&maps.a[0], A0, A_MN);
-    if (err == cudaSuccess) err = map16(&maps.b[0], B0, B_MN);
-    if (err == cudaSuccess && segs == 2) err = map16(&maps.a[1], A1, A_MN);
-    if (err == cudaSuccess && (segs == 2 || GATED)) err = map16(&maps.b[1], B1, B_MN);
+    constexpr int A_BOX = A_MN ? 64 : 128, B_BOX = B_MN ? 64 : 128;
+    cudaError_t err = map16(&maps.a[0], A0, A_BOX);
+    if (err == cudaSuccess) err = map16(&maps.b[0], B0, B_BOX);
+    if (err == cudaSuccess && segs == 2) err = map16(&maps.a[1], A1, A_BOX);
+    if (err == cudaSuccess && (segs == 2 || GATED)) err = map16(&maps.b[1], B1, B_BOX);
     if (err != cudaSuccess) return err;
     return launch_tile_gemm<KIND, A_MN, B_MN, GATED>(tile_args(M, N, GATED ? 128 : 256, K, segs), maps, epi, st);
 }
+
+// x (tokens x K) times the rows of W0 (and W1, 64 rows of each to a tile).
+template <int KIND, bool PAIRED, class Epi>
+cudaError_t split16(const Matrix16& x, const Matrix16& W0, const Matrix16& W1, bool early, const Epi& epi,
+                    cudaStream_t st) {
+    constexpr int ROWS = PAIRED ? 64 : 128;
+    SplitMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    cudaError_t err = map16(&maps.p[0], W0, ROWS);
+    if (err == cudaSuccess && PAIRED) err = map16(&maps.p[1], W1, ROWS);
+    if (err == cudaSuccess) err = map16(&maps.q, x, split_nq(x.rows));
+    if (err != cudaSuccess) return err;
+    SplitArgs g = {};
+    g.nt = (int)((W0.rows + ROWS - 1) / ROWS);
+    g.nk = (int)((x.cols + 63) / 64);
+    g.last_steps = (int)((x.cols - (int64_t)(g.nk - 1) * 64 + 15) / 16);
+    g.early = early;
+    g.M = x.rows;
+    return launch_split_gemm<KIND, PAIRED>(g, maps, epi, st);
+}
+
+int64_t pair_tiles(int64_t M, int64_t N, int64_t per_tile) { return (M + 255) / 256 * ((N + per_tile - 1) / per_tile); }
 
 template <typename T>
 EpiStore<T> store_to(void* C, int64_t ldc, int64_t M, int64_t N) {
@@ -166,7 +222,10 @@ template <int KIND, typename T>
 cudaError_t forward_typed(const FfForward& f, cudaStream_t st) {
     const Matrix16 h{f.h, f.T, f.F, f.ld};
     cudaError_t err;
-    if (f.a != nullptr)
+    if (split_takes(f.T, pair_tiles(f.T, f.F, 128)))
+        err = split16<KIND, true>(f.x, f.wg, f.wu, false,
+                                  EpiSplitGate<T>{static_cast<T*>(f.h), f.a, f.b, f.ld, f.F, f.act}, st);
+    else if (f.a != nullptr)
         err = product16<KIND, false, false, true>(
             f.T, f.F, f.D, 1, f.x, f.x, f.wg, f.wu,
             EpiGate<T, true>{static_cast<T*>(f.h), f.a, f.b, f.ld, f.T, round_up(f.F, 64), f.act}, st);
@@ -174,7 +233,11 @@ cudaError_t forward_typed(const FfForward& f, cudaStream_t st) {
         err = product16<KIND, false, false, true>(
             f.T, f.F, f.D, 1, f.x, f.x, f.wg, f.wu,
             EpiGate<T, false>{static_cast<T*>(f.h), nullptr, nullptr, f.ld, f.T, round_up(f.F, 64), f.act}, st);
-    if (err == cudaSuccess)
+    if (err != cudaSuccess) return err;
+    // Wd was complete before the launch above could end its own wait
+    if (split_takes(f.T, pair_tiles(f.T, f.D, 256)))
+        err = split16<KIND, false>(h, f.wd, f.wd, true, EpiSplitStore<T>{static_cast<T*>(f.y), f.ldy, f.D}, st);
+    else
         err = product16<KIND, false, false, false>(f.T, f.D, f.F, 1, h, h, f.wd, f.wd, store_to<T>(f.y, f.ldy, f.T, f.D),
                                                    st);
     return err;

@@ -196,6 +196,7 @@ struct Mx4Gemm {
     float alpha;
     void* C;
     int64_t ldc;
+    bool early;  // B was complete before the launch before this one began
 };
 cudaError_t launch_mx4_gemm(const Mx4Gemm& g, cudaStream_t st);
 // act(x Wg^T) * (x Wu^T) with Wg and Wu in turn, 32 rows each, in W; into hq

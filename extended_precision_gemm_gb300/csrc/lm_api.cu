@@ -212,7 +212,7 @@ ddgemm_status dd_mx4_gemm(int format, int64_t M, int64_t N, int64_t K, const uin
     if (overlaps_mx4(format, A, C, cb) || overlaps_mx4(format, B, C, cb)) return DDGEMM_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (K == 0) return status_of(zero16(C, M, N, ldc, es, st));
-    return status_of(launch_mx4_gemm(Mx4Gemm{format, type, A, B, alpha, C, ldc}, st));
+    return status_of(launch_mx4_gemm(Mx4Gemm{format, type, A, B, alpha, C, ldc, false}, st));
 }
 
 ddgemm_status dd_ff_gated_saved_size(int type, int64_t T, int64_t F, size_t* bytes) {
@@ -354,7 +354,7 @@ ddgemm_status dd_mx4_ff_gated(int format, int type, int activation, int64_t T, i
         err = launch_mx4_quantize(Mx4Quantize{format, DDGEMM_F32, false, T, F, h, ldh, ws.at<uint8_t>(hc), hl,
                                               ws.at<uint8_t>(hs), ws.at<int32_t>(he), nullptr},
                                   st);
-    if (err == cudaSuccess) err = launch_mx4_gemm(Mx4Gemm{format, type, hq, W2, 1.0f, y, ldy}, st);
+    if (err == cudaSuccess) err = launch_mx4_gemm(Mx4Gemm{format, type, hq, W2, 1.0f, y, ldy, true}, st);
     return status_of(err);
 }
 

@@ -134,17 +134,48 @@ __global__ void __launch_bounds__(QWARPS * 32) nvfp4_rows_kernel(const T* X, int
     }
 }
 
-// Two consecutive elements of a row of X as floats (zero beyond R).
-template <typename T>
-__device__ __forceinline__ void load_pair(const T* row, int64_t c, int64_t R, bool vec, float& a, float& b) {
-    if (vec && c + 2 <= R) {
-        struct alignas(2 * sizeof(T)) Two { T a, b; };
-        const Two t = *reinterpret_cast<const Two*>(row + c);
-        a = to_float<T>(t.a);
-        b = to_float<T>(t.b);
+// Two consecutive elements, as they lie in memory.
+template <typename T> struct Two;
+template <> struct Two<float> {
+    using raw = uint2;
+    static __device__ __forceinline__ void split(uint2 r, float& a, float& b) { a = __uint_as_float(r.x), b = __uint_as_float(r.y); }
+    static __device__ __forceinline__ uint2 join(float a, float b) { return make_uint2(__float_as_uint(a), __float_as_uint(b)); }
+};
+template <> struct Two<__nv_bfloat16> {
+    using raw = uint32_t;
+    static __device__ __forceinline__ void split(uint32_t r, float& a, float& b) {
+        a = __uint_as_float(r << 16), b = __uint_as_float(r & 0xffff0000u);
+    }
+    static __device__ __forceinline__ uint32_t join(__nv_bfloat16 a, __nv_bfloat16 b) {
+        return (uint32_t)__bfloat16_as_ushort(a) | (uint32_t)__bfloat16_as_ushort(b) << 16;
+    }
+};
+template <> struct Two<__half> {
+    using raw = uint32_t;
+    static __device__ __forceinline__ void split(uint32_t r, float& a, float& b) {
+        a = __half2float(__ushort_as_half((unsigned short)(r & 0xffffu)));
+        b = __half2float(__ushort_as_half((unsigned short)(r >> 16)));
+    }
+    static __device__ __forceinline__ uint32_t join(__half a, __half b) {
+        return (uint32_t)__half_as_ushort(a) | (uint32_t)__half_as_ushort(b) << 16;
+    }
+};
+
+// Columns c and c + 1 of N consecutive rows from k on (zero beyond R and K).
+// The whole rows of a full tile are loaded without a branch between them, so
+// that all N loads are in flight together.
+template <typename T, int N>
+__device__ __forceinline__ void load_columns(const T* X, int64_t ldx, int64_t k, int64_t c, int64_t K, int64_t R, bool vec,
+                                             typename Two<T>::raw (&raw)[N]) {
+    const T* p = X + k * ldx + c;
+    if (vec && k + N <= K && c + 2 <= R) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) raw[i] = *reinterpret_cast<const typename Two<T>::raw*>(p + i * ldx);
     } else {
-        a = c < R ? to_float<T>(row[c]) : 0.0f;
-        b = c + 1 < R ? to_float<T>(row[c + 1]) : 0.0f;
+        const T zero = from_float<T>(0.0f);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            raw[i] = Two<T>::join(k + i < K && c < R ? p[i * ldx] : zero, k + i < K && c + 1 < R ? p[i * ldx + 1] : zero);
     }
 }
 
@@ -159,10 +190,12 @@ __global__ void __launch_bounds__(256) column_max_kernel(const T* X, int64_t ldx
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 64 + lane * 2, k0 = (int64_t)blockIdx.y * 256 + warp * 32;
     uint32_t m0 = 0, m1 = 0;
-#pragma unroll 16
+    typename Two<T>::raw raw[32];
+    load_columns<T, 32>(X, ldx, k0, c, K, R, vec, raw);
+#pragma unroll
     for (int i = 0; i < 32; ++i) {
-        float a = 0.0f, b = 0.0f;
-        if (k0 + i < K) load_pair(X + (k0 + i) * ldx, c, R, vec, a, b);
+        float a, b;
+        Two<T>::split(raw[i], a, b);
         const uint32_t x = abs_bits(a), y = abs_bits(b);
         m0 = max(m0, x < kInfBits ? x : 0u);
         m1 = max(m1, y < kInfBits ? y : 0u);
@@ -181,60 +214,70 @@ __global__ void __launch_bounds__(256) column_max_kernel(const T* X, int64_t ldx
 // Columns of X (K x R) as rows of the result: a block takes 64 columns and 256
 // k.  Warp w reads rows 32 w .. + 31, a lane two columns of them, so a lane
 // holds whole blocks of k and needs no exchange for their maxima; codes and
-// scales go through shared memory and leave as whole 128-byte rows.
+// scales go through shared memory (rows of 33 and 5 words: no bank conflicts)
+// and leave as whole 128-byte rows.  The blocks take k in descending order:
+// the maxima before read X upwards and leave its end in L2.
 template <typename T, int FMT>
 __global__ void __launch_bounds__(256) mx4_columns_kernel(const T* X, int64_t ldx, int64_t R, int64_t K, bool vec,
                                                           const uint32_t* most, uint8_t* codes, int64_t ldq,
                                                           uint8_t* scales, int32_t* exponents) {
     constexpr int BLOCK = mx4_block(FMT), WORDS = mx4_tiles_per_k(FMT);
-    __shared__ __align__(16) uint8_t code[64][128 + 16];
-    __shared__ __align__(16) uint8_t scale[64][4 * WORDS];
+    __shared__ uint32_t code[64][33];   // row p: column (p % 32) * 2 + p / 32 of the tile
+    __shared__ uint32_t scale[64][5];
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t r0 = (int64_t)blockIdx.x * 64, kt = blockIdx.y;
+    const int64_t r0 = (int64_t)blockIdx.x * 64, kt = gridDim.y - 1 - blockIdx.y;
     const int64_t c = r0 + lane * 2, k0 = kt * MX4_TILE_K + warp * 32;
-    float x[2][32];
+    typename Two<T>::raw raw[32];
+    load_columns<T, 32>(X, ldx, k0, c, K, R, vec, raw);
+    int e[2] = {0, 0};
+    if (FMT == kNvfp4) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        x[0][i] = x[1][i] = 0.0f;
-        if (k0 + i < K) load_pair(X + (k0 + i) * ldx, c, R, vec, x[0][i], x[1][i]);
+        for (int j = 0; j < 2; ++j)
+            if (c + j < R) {
+                e[j] = nvfp4_row_exponent(most[c + j]);
+                if (kt == 0 && warp == 0) exponents[c + j] = e[j];
+            }
     }
+    const float unit[2] = {exp2_int(-e[0]), exp2_int(-e[1])};
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int row = lane * 2 + j;
-        int e = 0;
-        if (FMT == kNvfp4 && r0 + row < R) {
-            e = nvfp4_row_exponent(most[r0 + row]);
-            if (kt == 0 && warp == 0) exponents[r0 + row] = e;
+    for (int b = 0; b < 32 / BLOCK; ++b) {
+        uint32_t m[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < BLOCK; ++i) {
+            float x, y;
+            Two<T>::split(raw[b * BLOCK + i], x, y);
+            m[0] = max(m[0], abs_bits(x));
+            m[1] = max(m[1], abs_bits(y));
         }
-        const float unit = exp2_int(-e);
+        float s[2] = {1.0f, 1.0f}, r[2];
 #pragma unroll
-        for (int b = 0; b < 32 / BLOCK; ++b) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < BLOCK; ++i) m = max(m, abs_bits(x[j][b * BLOCK + i]));
+        for (int j = 0; j < 2; ++j) {
             uint32_t byte;
-            float s = 1.0f, r;
             if (FMT == kMxfp4) {
-                byte = mxfp4_scale_byte(m);
-                r = mxfp4_inverse(byte);
+                byte = mxfp4_scale_byte(m[j]);
+                r[j] = mxfp4_inverse(byte);
             } else {
-                byte = nvfp4_scale_byte(m, unit);
-                s = e4m3_value(byte);
-                r = byte == 0u || byte == 127u ? 0.0f : __frcp_rn(s);
+                byte = nvfp4_scale_byte(m[j], unit[j]);
+                s[j] = e4m3_value(byte);
+                r[j] = byte == 0u || byte == 127u ? 0.0f : __frcp_rn(s[j]);
             }
-            scale[row][warp * (32 / BLOCK) + b] = (uint8_t)byte;
+            reinterpret_cast<uint8_t*>(&scale[j * 32 + lane][0])[warp * (32 / BLOCK) + b] = (uint8_t)byte;
+        }
 #pragma unroll
-            for (int q = 0; q < BLOCK / 8; ++q) {
-                float y[8];
+        for (int q = 0; q < BLOCK / 8; ++q) {
+            float y[2][8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float v = x[j][b * BLOCK + q * 8 + i];
-                    y[i] = FMT == kMxfp4 ? v * r : r == 0.0f ? 0.0f : quotient(v * unit, s, r);
-                }
-                *reinterpret_cast<uint32_t*>(&code[row][warp * 16 + b * (BLOCK / 2) + q * 4]) = e2m1_pack8(y);
+            for (int i = 0; i < 8; ++i) {
+                float v[2];
+                Two<T>::split(raw[b * BLOCK + q * 8 + i], v[0], v[1]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    y[j][i] = FMT == kMxfp4 ? v[j] * r[j] : r[j] == 0.0f ? 0.0f : quotient(v[j] * unit[j], s[j], r[j]);
             }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) code[j * 32 + lane][warp * 4 + b * (BLOCK / 8) + q] = e2m1_pack8(y[j]);
         }
     }
     __syncthreads();
@@ -242,21 +285,24 @@ __global__ void __launch_bounds__(256) mx4_columns_kernel(const T* X, int64_t ld
     const int64_t bytes = mx4_code_bytes(K);
 #pragma unroll
     for (int i = threadIdx.x; i < 64 * 8; i += 256) {
-        const int row = i / 8, at = i % 8 * 16;
-        if (r0 + row < R && kt * 128 + at < bytes)
-            *reinterpret_cast<uint4*>(codes + (r0 + row) * ldq + kt * 128 + at) =
-                *reinterpret_cast<const uint4*>(&code[row][at]);
+        const int p = i / 8, at = i % 8;
+        const int64_t row = r0 + p % 32 * 2 + p / 32;
+        if (row < R && kt * 128 + at * 16 < bytes)
+            *reinterpret_cast<uint4*>(codes + row * ldq + kt * 128 + at * 16) =
+                make_uint4(code[p][at * 4], code[p][at * 4 + 1], code[p][at * 4 + 2], code[p][at * 4 + 3]);
     }
     const int64_t tiles = mx4_scale_tiles(FMT, K);
-    for (int i = threadIdx.x; i < 64 * WORDS; i += 256) {
-        const int row = i % 64, w = i / 64;
-        if (r0 + row < R)
-            *reinterpret_cast<uint32_t*>(scales + mx4_scale_word(r0 + row, kt * WORDS + w, tiles)) =
-                *reinterpret_cast<const uint32_t*>(&scale[row][w * 4]);
+    if (threadIdx.x < 64 * WORDS) {
+        const int p = threadIdx.x % 64, w = threadIdx.x / 64;
+        const int64_t row = r0 + p % 32 * 2 + p / 32;
+        if (row < R) *reinterpret_cast<uint32_t*>(scales + mx4_scale_word(row, kt * WORDS + w, tiles)) = scale[p][w];
     }
 }
 
-// The values a matrix stands for: one warp for 256 k of a row, 8 codes a lane.
+// The values a matrix stands for: one warp for 1024 k of a row, in four steps
+// of 8 codes a lane (whole 512-byte runs of 16-bit values leave a warp at
+// once), all of their codes and scales loaded before the first conversion.
+constexpr int DSTEPS = 4;
 template <typename T, int FMT>
 __global__ void __launch_bounds__(QWARPS * 32) mx4_dequantize_kernel(const uint8_t* codes, int64_t ldq,
                                                                      const uint8_t* scales, const int32_t* exponents,
@@ -265,29 +311,41 @@ __global__ void __launch_bounds__(QWARPS * 32) mx4_dequantize_kernel(const uint8
     constexpr int LANES = mx4_block(FMT) / 8;
     pdl_wait();
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const int64_t kts = (K + MX4_TILE_K - 1) / MX4_TILE_K;
+    const int lane = threadIdx.x & 31, block = lane / LANES;
+    const int64_t kts = (K + MX4_TILE_K - 1) / MX4_TILE_K, steps = (kts + DSTEPS - 1) / DSTEPS;
     const int64_t item = (int64_t)blockIdx.x * QWARPS + (threadIdx.x >> 5);
-    if (item >= rows * kts) return;
-    const int64_t row = item / kts, kt = item % kts, k0 = kt * MX4_TILE_K + lane * 8;
-    if (k0 >= K) return;
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + row * ldq + k0 / 2);
-    const int block = lane / LANES;
-    const uint32_t byte = scales[mx4_scale_word(row, kt * mx4_tiles_per_k(FMT) + block / 4, mx4_scale_tiles(FMT, K)) +
-                                 block % 4];
-    float y[8];
-    e2m1_unpack8(w, y);
-    const float s = FMT == kMxfp4 ? mxfp4_scale(byte) : e4m3_value(byte);
+    if (item >= rows * steps) return;
+    const int64_t row = item / steps, kt0 = item % steps * DSTEPS;
+    const uint8_t* src = codes + row * ldq;
+    const uint8_t* sc = scales + mx4_scale_word(row, 0, mx4_scale_tiles(FMT, K)) + block % 4;
     const float unit = FMT == kMxfp4 ? 1.0f : exp2_int(exponents[row]);
+    uint32_t w[DSTEPS], byte[DSTEPS];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = y[i] * s * unit;
-    T* dst = X + row * ldx + k0;
-    if (vec && k0 + 8 <= K) {
-        store8(dst, y);
-    } else {
+    for (int j = 0; j < DSTEPS; ++j) {
+        const int64_t kt = kt0 + j, k0 = kt * MX4_TILE_K + lane * 8;
+        w[j] = byte[j] = 0;
+        if (k0 < K) {
+            w[j] = *reinterpret_cast<const uint32_t*>(src + k0 / 2);
+            byte[j] = sc[(kt * mx4_tiles_per_k(FMT) + block / 4) * 512];
+        }
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (k0 + i < K) dst[i] = from_float<T>(y[i]);
+    for (int j = 0; j < DSTEPS; ++j) {
+        const int64_t k0 = (kt0 + j) * MX4_TILE_K + lane * 8;
+        if (k0 >= K) return;
+        float y[8];
+        e2m1_unpack8(w[j], y);
+        const float s = FMT == kMxfp4 ? mxfp4_scale(byte[j]) : e4m3_value(byte[j]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = y[i] * s * unit;
+        T* dst = X + row * ldx + k0;
+        if (vec && k0 + 8 <= K) {
+            store8(dst, y);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (k0 + i < K) dst[i] = from_float<T>(y[i]);
+        }
     }
 }
 
@@ -323,7 +381,7 @@ cudaError_t quantize_typed(const Mx4Quantize& q, const T* X, cudaStream_t st) {
 template <typename T>
 cudaError_t dequantize_typed(int fmt, int64_t rows, int64_t K, const uint8_t* codes, int64_t ldq,
                              const uint8_t* scales, const int32_t* exponents, T* X, int64_t ldx, cudaStream_t st) {
-    const int64_t items = rows * ((K + MX4_TILE_K - 1) / MX4_TILE_K);
+    const int64_t items = rows * ((K + DSTEPS * MX4_TILE_K - 1) / (DSTEPS * MX4_TILE_K));
     const bool vec = (uintptr_t)X % 16 == 0 && ldx * sizeof(T) % 16 == 0;
     const dim3 grid((unsigned)((items + QWARPS - 1) / QWARPS)), block(QWARPS * 32);
     return fmt == kMxfp4 ? launch_pdl(mx4_dequantize_kernel<T, kMxfp4>, grid, block, 0, st, codes, ldq, scales,

@@ -2,6 +2,7 @@
 // (C = alpha A B^T) and the two products of the 4-bit gated block.
 #include "activation.cuh"
 #include "mx4.cuh"
+#include "split_gemm.cuh"
 #include "tile_gemm.cuh"
 
 namespace ddg {
@@ -117,6 +118,61 @@ struct EpiGate4 {
     }
 };
 
+// The same two epilogues for the split kernel: one value per lane.
+template <int KIND, typename T>
+struct EpiSplitScale {
+    static constexpr int UNITS = 1;
+    T* C;
+    int64_t ldc, N;
+    const int32_t *e, *f;
+    float alpha;
+    __device__ __forceinline__ void emit(float v, float, int64_t m, int unit, int lane, int tile) const {
+        const int64_t n = (int64_t)tile * 128 + unit * 32 + lane;
+        if (n >= N) return;
+        v *= alpha;
+        if (KIND == kKindNv) v = scale_by_exp2(v, e[m] + f[n]);
+        C[m * ldc + n] = from_float<T>(v);
+    }
+};
+
+template <int KIND>
+struct EpiSplitGate4 {
+    static constexpr int UNITS = 2;
+    uint8_t *codes, *scales;
+    float* h;
+    int64_t ld, F;
+    const int32_t *e, *f;
+    int act;
+    __device__ __forceinline__ void emit(float g, float u, int64_t m, int unit, int lane, int tile) const {
+        const int64_t b = (int64_t)tile * 2 + unit, n = b * 32 + lane;  // block of 32 hidden values
+        if (b * 32 >= F) return;
+        if (KIND == kKindNv) {
+            const int er = e[m];
+            g = scale_by_exp2(g, er + f[b * 64 + lane]);
+            u = scale_by_exp2(u, er + f[b * 64 + 32 + lane]);
+        }
+        float a = 0.0f, da;
+        with_activation(act, [&](auto tag) { activation<decltype(tag)::value, false>(g, a, da); });
+        const float hv = a * u;
+        if (KIND == kKindNv) {
+            if (n < F) h[m * ld + n] = hv;
+            return;
+        }
+        const uint32_t byte = mxfp4_scale_byte(__reduce_max_sync(~0u, __float_as_uint(hv) & 0x7fffffffu));
+        const float q = hv * mxfp4_inverse(byte);
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(~0u, q, (lane & 3) * 8 + i);
+        if (lane < 4) *reinterpret_cast<uint32_t*>(codes + m * ld + b * 16 + lane * 4) = e2m1_pack8(y);
+        const int64_t tiles = mx4_scale_tiles(kMxfp4, F);
+        if (lane == 0) {
+            scales[mx4_scale_word(m, b / 4, tiles) + b % 4] = (uint8_t)byte;
+            if (n + 32 >= F)  // the last block: the padding of k
+                for (int64_t p = b + 1; p < tiles * 4; ++p) scales[mx4_scale_word(m, p / 4, tiles) + p % 4] = 0;
+        }
+    }
+};
+
 cudaError_t map_codes(CUtensorMap* m, const Mx4Matrix& x, int box_rows) {
     const int64_t bytes = mx4_code_bytes(x.K), ld = x.rows > 1 ? x.ldq : round_up(bytes, 16);
     return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, x.codes, bytes, x.rows, ld, 128, box_rows, true);
@@ -146,9 +202,35 @@ cudaError_t product4(const Mx4Matrix& A, const Mx4Matrix& B, const Epi& epi, cud
     return launch_tile_gemm<KIND, false, false, false>(g, maps, epi, st);
 }
 
+// x (tokens x K) times the rows of W.
+template <int KIND, class Epi>
+cudaError_t split4(const Mx4Matrix& x, const Mx4Matrix& W, bool early, const Epi& epi, cudaStream_t st) {
+    constexpr int FMT = KIND == kKindMx ? kMxfp4 : kNvfp4;
+    SplitMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    cudaError_t err = map_codes(&maps.p[0], W, 128);
+    if (err == cudaSuccess) err = map_codes(&maps.q, x, split_nq(x.rows));
+    if (err == cudaSuccess) err = map_scales(&maps.sp, FMT, W);
+    if (err == cudaSuccess) err = map_scales(&maps.sq, FMT, x);
+    if (err != cudaSuccess) return err;
+    SplitArgs g = {};
+    g.nt = (int)((W.rows + 127) / 128);
+    g.nk = (int)((x.K + MX4_TILE_K - 1) / MX4_TILE_K);
+    g.last_steps = (int)((x.K - (int64_t)(g.nk - 1) * MX4_TILE_K + 63) / 64);
+    g.tiles_k = (int)mx4_scale_tiles(FMT, x.K);
+    g.early = early;
+    g.M = x.rows;
+    return launch_split_gemm<KIND, false>(g, maps, epi, st);
+}
+
+int64_t pair_tiles(const Mx4Matrix& A, const Mx4Matrix& B) { return (A.rows + 255) / 256 * ((B.rows + 191) / 192); }
+
 template <int KIND, typename T>
 cudaError_t gemm_typed(const Mx4Gemm& g, cudaStream_t st) {
     T* C = static_cast<T*>(g.C);
+    if (split_takes(g.A.rows, pair_tiles(g.A, g.B)))
+        return split4<KIND>(g.A, g.B, g.early,
+                            EpiSplitScale<KIND, T>{C, g.ldc, g.B.rows, g.A.exponents, g.B.exponents, g.alpha}, st);
     const bool vec = (uintptr_t)C % 32 == 0 && (g.ldc * sizeof(T)) % 32 == 0;
     return product4<KIND>(
         g.A, g.B, EpiScale<KIND, T>{C, g.ldc, g.A.rows, g.B.rows, g.A.exponents, g.B.exponents, g.alpha, vec}, st);
@@ -169,17 +251,24 @@ cudaError_t launch_mx4_gemm(const Mx4Gemm& g, cudaStream_t st) {
     return g.fmt == kMxfp4 ? gemm_kind<kKindMx>(g, st) : gemm_kind<kKindNv>(g, st);
 }
 
-cudaError_t launch_mx4_gate(const Mx4Gate& g, cudaStream_t st) {
+namespace {
+
+template <int KIND>
+cudaError_t gate_kind(const Mx4Gate& g, cudaStream_t st) {
+    uint8_t *codes = const_cast<uint8_t*>(g.hq.codes), *scales = const_cast<uint8_t*>(g.hq.scales);
+    const int64_t ld = KIND == kKindMx ? g.hq.ldq : g.ldh;
+    if (split_takes(g.x.rows, pair_tiles(g.x, g.W)))
+        return split4<KIND>(g.x, g.W, true,  // x was quantised by the launch before, which waited for all before it
+                            EpiSplitGate4<KIND>{codes, scales, g.h, ld, g.F, g.x.exponents, g.W.exponents, g.act}, st);
     const int nt = (int)((g.W.rows + 191) / 192);
-    if (g.fmt == kMxfp4)
-        return product4<kKindMx>(g.x, g.W,
-                                 EpiGate4<kKindMx>{const_cast<uint8_t*>(g.hq.codes), const_cast<uint8_t*>(g.hq.scales),
-                                                   nullptr, g.hq.ldq, g.x.rows, g.F, nt, nullptr, nullptr, g.act},
-                                 st);
-    return product4<kKindNv>(g.x, g.W,
-                             EpiGate4<kKindNv>{nullptr, nullptr, g.h, g.ldh, g.x.rows, g.F, nt, g.x.exponents,
-                                               g.W.exponents, g.act},
-                             st);
+    return product4<KIND>(
+        g.x, g.W, EpiGate4<KIND>{codes, scales, g.h, ld, g.x.rows, g.F, nt, g.x.exponents, g.W.exponents, g.act}, st);
+}
+
+}  // namespace
+
+cudaError_t launch_mx4_gate(const Mx4Gate& g, cudaStream_t st) {
+    return g.fmt == kMxfp4 ? gate_kind<kKindMx>(g, st) : gate_kind<kKindNv>(g, st);
 }
 
 cudaError_t read_and_reset_wait_timeouts_mx4(unsigned int* count) { return reset_tile_timeouts(count); }

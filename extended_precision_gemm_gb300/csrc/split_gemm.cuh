@@ -1,0 +1,332 @@
+// split_gemm.cuh -- matrix products of few rows (tokens) with a large matrix
+// (weights), for the 4-bit products and the gated block: bound by the bytes of
+// the weights, so the work is split over k as well until it covers the SMs.
+//
+// One CTA multiplies 128 rows of the weights (the M side of the MMA, so that
+// no tensor-core row is idle however few tokens there are) with NQ tokens over
+// its share of k; a cluster of CTAs shares one such tile, each with its own
+// part of k.  The partial sums meet in shared memory: every CTA leaves its
+// tile there, and after a cluster barrier each adds its part of the outputs
+// over the CTAs in order (no atomics: results do not depend on timing).
+// Warps: 0 copies, 1 issues MMAs, 2-5 read the accumulators; all take part in
+// the final sums.  Two CTAs fit an SM.
+//
+// With EARLY weights (nothing that the launch before this one writes), the
+// ring is filled with them before the wait for that launch.
+#pragma once
+
+#include "mx4.cuh"
+#include "tile_gemm.cuh"
+
+namespace ddg {
+namespace {
+
+constexpr int kSplitThreads = 192;
+constexpr int kSplitSmem = 108 * 1024;  // of the ring: two CTAs on an SM
+constexpr int kMaxCluster = 8;
+
+template <int KIND, int NQ>
+struct SplitShape {
+    static constexpr bool F4 = kind_is_4bit(KIND);
+    static constexpr int P_BYTES = 128 * 128, Q_BYTES = NQ * 128;
+    static constexpr int SCALE_TILES = F4 ? (KIND == kKindMx ? 2 : 4) : 0;
+    static constexpr int SCALE_BYTES = SCALE_TILES * 512;  // of each operand
+    static constexpr int STAGE_BYTES = P_BYTES + Q_BYTES + 2 * SCALE_BYTES;
+    static constexpr int STAGES = kSplitSmem / STAGE_BYTES;
+    static constexpr int SMEM = STAGES * STAGE_BYTES + 1024;
+    static constexpr uint32_t ACC_COLS = NQ < 32 ? 32 : NQ;
+    static constexpr uint32_t TMEM_COLS = !F4 ? ACC_COLS : NQ <= 64 ? 128 : 256;
+    static_assert(STAGE_BYTES % 1024 == 0 && STAGES >= 2, "ring");
+    static_assert(128 * NQ * 4 <= STAGES * STAGE_BYTES, "partial sums fit the ring");
+};
+
+struct SplitMaps {
+    CUtensorMap p[2], q, sp, sq;  // weights (gated 16-bit: Wg and Wu, 64 rows each), tokens, scales
+};
+
+struct SplitArgs {
+    int nt, mt;        // tiles of 128 weight rows, of NQ tokens
+    int nk, per;       // stages along k, and of one CTA
+    int last_steps;    // MMAs in the last stage
+    int tiles_k;       // 4-bit kinds: scale tiles in a row of 128
+    int splits;        // CTAs of a cluster
+    int early;         // the weights may be read before the wait
+    int64_t M;         // tokens
+};
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Epi: UNITS (1: a unit of work is 32 weight rows of one token, 4 units to a
+// tile and token; 2: it is 32 rows of g and 32 of u, 2 units) and
+// emit(v0, v1, token, unit, lane, tile): the whole warp, one row per lane.
+template <int KIND, int NQ, bool PAIRED16, class Epi>
+__global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __grid_constant__ SplitArgs g,
+                                                                   const __grid_constant__ SplitMaps maps,
+                                                                   const __grid_constant__ Epi epi) {
+    using S = SplitShape<KIND, NQ>;
+    constexpr int STAGES = S::STAGES;
+    constexpr bool F4 = S::F4;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[2 * STAGES + 1];
+    __shared__ uint32_t tmem_slot;
+
+    const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
+    const int z = (int)cluster_ctarank();
+    const int tile = blockIdx.x / g.splits;
+    const int nt = tile % g.nt, mt = tile / g.nt;
+    const int k0 = z * g.per, count = min(g.per, g.nk - k0);
+    const uint32_t full0 = smem_addr(&bars[0]), empty0 = smem_addr(&bars[STAGES]), done_bar = smem_addr(&bars[2 * STAGES]);
+
+    constexpr int ROW = F4 ? 128 : 64;
+    auto load_weights = [&](int i, uint32_t dst, uint32_t bar) {
+        const int kb = k0 + i;
+        if (PAIRED16) {
+            tma_load_2d(dst, &maps.p[0], kb * ROW, nt * 64, bar);
+            tma_load_2d(dst + S::P_BYTES / 2, &maps.p[1], kb * ROW, nt * 64, bar);
+        } else {
+            tma_load_2d(dst, &maps.p[0], kb * ROW, nt * 128, bar);
+        }
+        if (F4) tma_load_2d(dst + S::P_BYTES + S::Q_BYTES, &maps.sp, 0, nt * g.tiles_k + kb * S::SCALE_TILES, bar);
+    };
+    const int ahead = g.early ? min(count, STAGES) : 0;
+    if (warp == 0) {
+        if (elect_one()) {
+            for (int i = 0; i < STAGES; ++i) {
+                mbar_init(full0 + 8 * i, 1);
+                mbar_init(empty0 + 8 * i, 1);
+            }
+            mbar_init(done_bar, 1);
+            fence_barrier_init();
+            for (int i = 0; i < ahead; ++i) {
+                mbar_expect_tx(full0 + 8 * i, S::STAGE_BYTES);
+                load_weights(i, ring + i * S::STAGE_BYTES, full0 + 8 * i);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        tc5::tmem_alloc(smem_addr(&tmem_slot), S::TMEM_COLS);
+        tc5::tmem_relinquish();
+    }
+    tc5::fence_before_sync();
+    __syncthreads();
+    tc5::fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp == 0) {
+        pdl_wait();
+        pdl_launch_dependents();
+        uint32_t stage = 0, phase = 0;
+        int issued = ahead;
+        bool ok = true;
+        for (int i = 0; i < count; ++i) {
+            ok = warp_wait(empty0 + 8 * stage, phase ^ 1, kTileWaitNs);
+            if (!ok) break;
+            if (elect_one()) {
+                const uint32_t dst = ring + stage * S::STAGE_BYTES, bar = full0 + 8 * stage;
+                if (i >= ahead) {
+                    mbar_expect_tx(bar, S::STAGE_BYTES);
+                    load_weights(i, dst, bar);
+                }
+                const int kb = k0 + i;
+                tma_load_2d(dst + S::P_BYTES, &maps.q, kb * ROW, mt * NQ, bar);
+                if (F4)
+                    tma_load_2d(dst + S::P_BYTES + S::Q_BYTES + S::SCALE_BYTES, &maps.sq, 0,
+                                mt * g.tiles_k + kb * S::SCALE_TILES, bar);  // mt > 0 only with 128 tokens
+            }
+            __syncwarp();
+            issued = max(issued, i + 1);
+            if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        }
+        // copies still in flight land before the CTA exits
+        for (int j = max(0, issued - STAGES); j < issued; ++j) {
+            const bool landed = warp_wait(full0 + 8 * (uint32_t)(j % STAGES), (uint32_t)(j / STAGES & 1), kTileWaitNs);
+            ok = ok && landed;
+            if (!landed) break;
+        }
+        if (!ok && lane == 0) tile_timeout();
+    } else if (warp == 1) {
+        constexpr uint32_t IDESC = F4 ? tc5::idesc_e2m1(KIND == kKindMx, 128, NQ)
+                                      : tc5::idesc_f16(KIND == kKindBF16, false, false, 128, NQ);
+        const uint64_t pd0 = tc5::desc_kmajor_sw128(ring), qd0 = tc5::desc_kmajor_sw128(ring + S::P_BYTES);
+        const uint64_t sd0 = tc5::desc_scale_tile(ring + S::P_BYTES + S::Q_BYTES);
+        uint32_t stage = 0, phase = 0;
+        bool ok = true;
+        for (int i = 0; i < count; ++i) {
+            ok = warp_wait(full0 + 8 * stage, phase, kTileWaitNs);
+            if (!ok) break;
+            tc5::fence_after_sync();
+            if (elect_one()) {
+                const uint64_t off = (uint64_t)((stage * S::STAGE_BYTES) >> 4);
+                const int steps = k0 + i == g.nk - 1 ? g.last_steps : 4;
+                if constexpr (F4) {
+                    const uint32_t sc = tmem + S::ACC_COLS + (i & 1) * 32;
+                    const uint64_t sd = sd0 + off;
+#pragma unroll
+                    for (int t = 0; t < S::SCALE_TILES; ++t) {
+                        tc5::cp_scales_single(sc + t * 4, sd + t * 32);
+                        tc5::cp_scales_single(sc + 16 + t * 4, sd + (S::SCALE_TILES + t) * 32);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (j >= steps) break;
+                        const uint32_t acc = (i | j) != 0 ? 1u : 0u;
+                        if (KIND == kKindMx)
+                            tc5::mma_mx_single(tmem, pd0 + off + 2 * j, qd0 + off + 2 * j,
+                                               tc5::idesc_scale_byte(IDESC, (j & 1) * 2), sc + (j / 2) * 4,
+                                               sc + 16 + (j / 2) * 4, acc);
+                        else
+                            tc5::mma_nv_single(tmem, pd0 + off + 2 * j, qd0 + off + 2 * j, IDESC, sc + j * 4,
+                                               sc + 16 + j * 4, acc);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (j >= steps) break;
+                        tc5::mma_f16_single(tmem, pd0 + off + 2 * j, qd0 + off + 2 * j, IDESC, (i | j) != 0 ? 1u : 0u);
+                    }
+                }
+                tc5::commit(empty0 + 8 * stage);
+                if (i == count - 1) tc5::commit(done_bar);
+            }
+            __syncwarp();
+            if (++stage == STAGES) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) {  // what was issued still has to finish
+            if (elect_one()) tc5::commit(done_bar);
+            __syncwarp();
+            if (lane == 0) tile_timeout();
+        }
+    }
+    __syncwarp();
+
+    // partial sums to shared memory (the ring is no longer read or written
+    // once every MMA has finished): token m at m * 128, weight rows contiguous
+    const int tokens = (int)min((int64_t)NQ, g.M - (int64_t)mt * NQ);
+    if (!warp_wait(done_bar, 0, 2 * kTileWaitNs) && lane == 0) tile_timeout();
+    tc5::fence_after_sync();
+    if (warp >= 2) {
+        const int q = warp & 3;
+        const uint32_t base = ring + (uint32_t)(q * 32 + lane) * 4;
+#pragma unroll
+        for (int c = 0; c < NQ; c += 16) {
+            if (c >= tokens) break;
+            uint32_t v[16];
+            asm volatile(
+                "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+                "tcgen05.wait::ld.sync.aligned;\n"
+                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+                  "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+                : "r"(tmem + ((uint32_t)(q * 32) << 16) + c)
+                : "memory");
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (c + i < tokens)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + (uint32_t)(c + i) * 512), "r"(v[i]) : "memory");
+        }
+    }
+    tc5::fence_before_sync();
+    cluster_sync();
+    tc5::fence_after_sync();
+    if (warp == 1) tc5::tmem_dealloc(tmem, S::TMEM_COLS);
+
+    // this CTA's share of the outputs, added over the CTAs in their order
+    pdl_wait();  // the other warps' first access to global memory
+    constexpr int PER_TOKEN = Epi::UNITS == 2 ? 2 : 4;
+    // (in batches of units, so that the loads of several are in flight)
+    constexpr int BATCH = 4;
+    const int units = tokens * PER_TOKEN, stride = g.splits * (kSplitThreads / 32);
+    for (int w0 = z + warp * g.splits; w0 < units; w0 += stride * BATCH) {
+        float v0[BATCH], v1[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) v0[i] = v1[i] = 0.0f;
+        for (int c = 0; c < g.splits; ++c) {
+            const uint32_t at = cluster_addr(ring + (uint32_t)lane * 4, (uint32_t)c);
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const int w = w0 + i * stride, m = w / PER_TOKEN, unit = w % PER_TOKEN;
+                if (w >= units) break;
+                // rows of the tile: 32 unit, or g and u: 64-row halves (16 bits), 32-row groups in turn (4 bits)
+                const int r0 = Epi::UNITS == 1 || PAIRED16 ? unit * 32 : unit * 64;
+                const int r1 = PAIRED16 ? 64 + unit * 32 : unit * 64 + 32;
+                v0[i] += ld_cluster(at + (uint32_t)(m * 128 + r0) * 4);
+                if (Epi::UNITS == 2) v1[i] += ld_cluster(at + (uint32_t)(m * 128 + r1) * 4);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int w = w0 + i * stride;
+            if (w < units) epi.emit(v0[i], v1[i], (int64_t)mt * NQ + w / PER_TOKEN, w % PER_TOKEN, lane, nt);
+        }
+    }
+    cluster_sync();  // no CTA leaves while another reads its sums
+}
+
+template <int KIND, int NQ, bool PAIRED16, class Epi>
+cudaError_t launch_split_sized(SplitArgs g, const SplitMaps& maps, const Epi& epi, cudaStream_t st) {
+    using S = SplitShape<KIND, NQ>;
+    static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
+    auto* kernel = split_gemm_kernel<KIND, NQ, PAIRED16, Epi>;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        if (err != cudaSuccess) return err;
+        ready.fetch_or(1ULL << dev, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((int64_t)g.nt * g.mt * g.splits));
+    cfg.blockDim = dim3(kSplitThreads);
+    cfg.dynamicSmemBytes = S::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)g.splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, g, maps, epi);
+}
+
+// Tokens of a tile: the least of 16, 32, 64 and 128 that holds them all.
+inline int split_nq(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+
+// CTAs along k: as many as two to an SM give each tile, at most a cluster,
+// with at least two stages each.
+inline int split_count(int64_t tiles, int nk) {
+    const int64_t slots = 2 * (int64_t)tile_sms();
+    int64_t s = std::min<int64_t>(kMaxCluster, std::max<int64_t>(1, slots / std::max<int64_t>(1, tiles)));
+    s = std::min<int64_t>(s, std::max(1, nk / 2));
+    const int per = (int)((nk + s - 1) / s);
+    return (nk + per - 1) / per;
+}
+
+// Whether the split kernel takes a product of M tokens: see the callers.
+inline bool split_takes(int64_t M, int64_t pair_tiles) { return M <= 128 || pair_tiles * 4 <= tile_sms(); }
+
+template <int KIND, bool PAIRED16, class Epi>
+cudaError_t launch_split_gemm(SplitArgs g, const SplitMaps& maps, const Epi& epi, cudaStream_t st) {
+    const int nq = split_nq(g.M);
+    g.mt = (int)((g.M + nq - 1) / nq);
+    g.splits = split_count((int64_t)g.nt * g.mt, g.nk);
+    g.per = (g.nk + g.splits - 1) / g.splits;
+    switch (nq) {
+        case 16: return launch_split_sized<KIND, 16, PAIRED16>(g, maps, epi, st);
+        case 32: return launch_split_sized<KIND, 32, PAIRED16>(g, maps, epi, st);
+        case 64: return launch_split_sized<KIND, 64, PAIRED16>(g, maps, epi, st);
+        default: return launch_split_sized<KIND, 128, PAIRED16>(g, maps, epi, st);
+    }
+}
+
+}  // namespace
+}  // namespace ddg

@@ -34,10 +34,7 @@ constexpr int kTileGroup = 8;  // m tiles that share their n tiles while these a
 
 __device__ unsigned int g_tile_timeouts = 0;
 
-__device__ __forceinline__ void tile_timeout(volatile int* abort_flag) {
-    *abort_flag = 1;
-    atomicAdd(&g_tile_timeouts, 1u);
-}
+__device__ __forceinline__ void tile_timeout() { atomicAdd(&g_tile_timeouts, 1u); }
 
 struct TileMaps {
     CUtensorMap a[2], b[2];  // operands of the segments (gated: b[rank] by CTA)
@@ -88,10 +85,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[2 * STAGES + 5];
     __shared__ uint32_t tmem_slot;
-    __shared__ volatile int abort_flag;
 
     const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int64_t pair = blockIdx.x >> 1;
@@ -112,7 +108,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
             mbar_init(acce0 + 8 * b, 2 * 4 * Epi::GROUPS);
         }
         mbar_init(done_bar, 1);
-        abort_flag = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -123,26 +118,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
     cluster_sync();
     tc5::fence_after_sync();
     const uint32_t tmem = tmem_slot;
-    pdl_launch_dependents();
     pdl_wait();
+    pdl_launch_dependents();
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ---- copies; both CTAs' complete on the even CTA's barriers ----
-            const uint32_t full_lead0 = cluster_addr(full0, 0);
-            uint32_t stage = 0, phase = 0;
-            int64_t issued = 0;
-            for (int64_t t = pair; t < tiles && !abort_flag; t += g.pairs) {
-                int mt, nt;
-                tile_of(g, t, mt, nt);
-                const int a_row = (mt * 2 + (int)rank) * 128;
-                const int b_row = GATED ? nt * (NT / 2) : nt * NT + (int)rank * (NT / 2);
-                for (int it = 0; it < per_tile; ++it) {
-                    if (!mbar_wait_bounded(empty0 + 8 * stage, phase ^ 1, kTileWaitNs)) {
-                        tile_timeout(&abort_flag);
-                        break;
-                    }
-                    const int seg = it / g.nk, kb = it - seg * g.nk;
+        // ---- copies; both CTAs' complete on the even CTA's barriers ----
+        const uint32_t full_lead0 = cluster_addr(full0, 0);
+        uint32_t stage = 0, phase = 0;
+        int64_t issued = 0;
+        bool ok = true;
+        for (int64_t t = pair; t < tiles && ok; t += g.pairs) {
+            int mt, nt;
+            tile_of(g, t, mt, nt);
+            const int a_row = (mt * 2 + (int)rank) * 128;
+            const int b_row = GATED ? nt * (NT / 2) : nt * NT + (int)rank * (NT / 2);
+            int seg = 0, kb = 0;
+            for (int it = 0; it < per_tile; ++it) {
+                ok = warp_wait(empty0 + 8 * stage, phase ^ 1, kTileWaitNs);
+                if (!ok) break;
+                if (elect_one()) {
                     const uint32_t dst = ring + stage * S::STAGE_BYTES, bar = full_lead0 + 8 * stage;
                     const CUtensorMap* ma = &maps.a[seg];
                     const CUtensorMap* mb = &maps.b[GATED ? rank : seg];
@@ -168,24 +162,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
                         tma_load_2d_group(ds + S::SA_BYTES, &maps.sb, 0, rb * g.tiles_k + t0, bar);
                         tma_load_2d_group(ds + 2 * S::SA_BYTES, &maps.sb, 0, (rb + 1) * g.tiles_k + t0, bar);
                     }
-                    ++issued;
-                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
-            }
-            // copies still in flight land before the CTA exits: the even CTA
-            // waits for its last stages to fill, the odd CTA (whose copies
-            // complete on the even CTA's barriers) for them to be consumed
-            const int64_t first = issued > STAGES ? issued - STAGES : 0;
-            for (int64_t j = first; j < issued; ++j) {
-                const uint32_t bar = (leader ? full0 : empty0) + 8 * (uint32_t)(j % STAGES);
-                if (!mbar_wait_bounded(bar, (uint32_t)((j / STAGES) & 1), kTileWaitNs)) {
-                    if (!abort_flag) tile_timeout(&abort_flag);
-                    break;
-                }
+                __syncwarp();
+                if (++kb == g.nk) { kb = 0; ++seg; }
+                ++issued;
+                if (++stage == STAGES) { stage = 0; phase ^= 1; }
             }
         }
+        // copies still in flight land before the CTA exits: the even CTA
+        // waits for its last stages to fill, the odd CTA (whose copies
+        // complete on the even CTA's barriers) for them to be consumed
+        const int64_t first = issued > STAGES ? issued - STAGES : 0;
+        for (int64_t j = first; j < issued; ++j) {
+            const uint32_t bar = (leader ? full0 : empty0) + 8 * (uint32_t)(j % STAGES);
+            const bool landed = warp_wait(bar, (uint32_t)((j / STAGES) & 1), kTileWaitNs);
+            ok = ok && landed;
+            if (!landed) break;
+        }
+        if (!ok && lane == 0) tile_timeout();
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        bool ok = true;
+        if (leader) {
             // ---- MMAs ----
             constexpr uint32_t IDESC = F4 ? tc5::idesc_e2m1(KIND == kKindMx, 256, NT)
                                           : tc5::idesc_f16(KIND == kKindBF16, A_MN, B_MN, 256, NT);
@@ -195,74 +192,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
                                       : tc5::desc_kmajor_sw128(ring + S::A_BYTES);
             const uint64_t sd0 = tc5::desc_scale_tile(ring + S::A_BYTES + S::B_BYTES);
             uint32_t stage = 0, phase = 0, count = 0;
-            bool ok = true, issued_any = false;
             for (int64_t t = pair; t < tiles && ok; t += g.pairs, ++count) {
                 int mt, nt;
                 tile_of(g, t, mt, nt);
                 const uint32_t buf = count & 1;
                 const uint32_t d = tmem + buf * NT;
-                if (!mbar_wait_bounded(acce0 + 8 * buf, ((count >> 1) & 1) ^ 1, kTileWaitNs)) {
-                    if (!abort_flag) tile_timeout(&abort_flag);
-                    ok = false;
-                    break;
-                }
+                ok = warp_wait(acce0 + 8 * buf, ((count >> 1) & 1) ^ 1, kTileWaitNs);
+                if (!ok) break;
                 tc5::fence_after_sync();
                 int kb = 0;
                 for (int it = 0; it < per_tile; ++it) {
-                    if (!mbar_wait_bounded(full0 + 8 * stage, phase, kTileWaitNs)) {
-                        if (!abort_flag) tile_timeout(&abort_flag);
-                        ok = false;
-                        break;
-                    }
+                    ok = warp_wait(full0 + 8 * stage, phase, kTileWaitNs);
+                    if (!ok) break;
                     tc5::fence_after_sync();
-                    const uint64_t off = (uint64_t)((stage * S::STAGE_BYTES) >> 4);
-                    const uint64_t ad = ad0 + off, bd = bd0 + off;
-                    const int steps = kb == g.nk - 1 ? g.last_steps : 4;
-                    if (++kb == g.nk) kb = 0;
-                    issued_any = true;
-                    if constexpr (F4) {
-                        const uint32_t sc = tmem + S::SCALE_COL + (it & 1) * S::SCALE_COLS;
-                        const uint64_t sd = sd0 + off;
+                    if (elect_one()) {
+                        const uint64_t off = (uint64_t)((stage * S::STAGE_BYTES) >> 4);
+                        const uint64_t ad = ad0 + off, bd = bd0 + off;
+                        const int steps = kb == g.nk - 1 ? g.last_steps : 4;
+                        if constexpr (F4) {
+                            const uint32_t sc = tmem + S::SCALE_COL + (it & 1) * S::SCALE_COLS;
+                            const uint64_t sd = sd0 + off;
 #pragma unroll
-                        for (int i = 0; i < S::SCALE_TILES; ++i) {
-                            tc5::cp_scales_pair(sc + i * 4, sd + i * 32);
-                            tc5::cp_scales_pair(sc + 16 + i * 8, sd + (S::SCALE_TILES + i) * 32);
-                            tc5::cp_scales_pair(sc + 16 + i * 8 + 4, sd + (2 * S::SCALE_TILES + i) * 32);
-                        }
-                        const uint32_t sbo = (uint32_t)(nt & 1) * 2;  // 192 nt is 64 rows into a tile for odd nt
+                            for (int i = 0; i < S::SCALE_TILES; ++i) {
+                                tc5::cp_scales_pair(sc + i * 4, sd + i * 32);
+                                tc5::cp_scales_pair(sc + 16 + i * 8, sd + (S::SCALE_TILES + i) * 32);
+                                tc5::cp_scales_pair(sc + 16 + i * 8 + 4, sd + (2 * S::SCALE_TILES + i) * 32);
+                            }
+                            const uint32_t sbo = (uint32_t)(nt & 1) * 2;  // 192 nt is 64 rows into a tile for odd nt
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if (j >= steps) break;
-                            const uint32_t acc = (it | j) != 0 ? 1u : 0u;
-                            if (KIND == kKindMx)
-                                tc5::mma_mx_pair(d, ad + A_STEP * j, bd + B_STEP * j,
-                                                 tc5::idesc_scale_byte(IDESC, (j & 1) * 2), sc + (j / 2) * 4,
-                                                 sc + 16 + (j / 2) * 8 + sbo, acc);
-                            else
-                                tc5::mma_nv_pair(d, ad + A_STEP * j, bd + B_STEP * j, IDESC, sc + j * 4,
-                                                 sc + 16 + j * 8 + sbo, acc);
-                        }
-                    } else {
+                            for (int j = 0; j < 4; ++j) {
+                                if (j >= steps) break;
+                                const uint32_t acc = (it | j) != 0 ? 1u : 0u;
+                                if (KIND == kKindMx)
+                                    tc5::mma_mx_pair(d, ad + A_STEP * j, bd + B_STEP * j,
+                                                     tc5::idesc_scale_byte(IDESC, (j & 1) * 2), sc + (j / 2) * 4,
+                                                     sc + 16 + (j / 2) * 8 + sbo, acc);
+                                else
+                                    tc5::mma_nv_pair(d, ad + A_STEP * j, bd + B_STEP * j, IDESC, sc + j * 4,
+                                                     sc + 16 + j * 8 + sbo, acc);
+                            }
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if (j >= steps) break;
-                            tc5::mma_f16_pair(d, ad + A_STEP * j, bd + B_STEP * j, IDESC, (it | j) != 0 ? 1u : 0u);
+                            for (int j = 0; j < 4; ++j) {
+                                if (j >= steps) break;
+                                tc5::mma_f16_pair(d, ad + A_STEP * j, bd + B_STEP * j, IDESC, (it | j) != 0 ? 1u : 0u);
+                            }
                         }
+                        tc5::commit_pair(empty0 + 8 * stage, 0x3);
+                        if (it == per_tile - 1) tc5::commit_pair(accf0 + 8 * buf, 0x3);
                     }
-                    tc5::commit_pair(empty0 + 8 * stage, 0x3);
+                    __syncwarp();
+                    if (++kb == g.nk) kb = 0;
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
-                if (!ok) break;
-                tc5::commit_pair(accf0 + 8 * buf, 0x3);
             }
-            if (issued_any) {
-                tc5::commit_pair(done_bar, 0x3);
-                if (!mbar_wait_bounded(done_bar, 0, kTileWaitNs)) tile_timeout(&abort_flag);
+            if (pair < tiles) {
+                if (elect_one()) tc5::commit_pair(done_bar, 0x3);
+                __syncwarp();
             }
-        } else if (lane == 0) {
-            // odd CTA: the MMAs read its shared memory and write its tensor memory
-            if (pair < tiles && !mbar_wait_bounded(done_bar, 0, kTileWaitNs * 4)) tile_timeout(&abort_flag);
         }
+        // every MMA has finished before either CTA gives up its shared or
+        // tensor memory
+        if (pair < tiles) ok = warp_wait(done_bar, 0, leader ? kTileWaitNs : kTileWaitNs * 4) && ok;
+        if (!ok && lane == 0) tile_timeout();
     } else {
         // ---- epilogue ----
         const int q = warp & 3, group = (warp - 2) >> 2;
@@ -271,8 +263,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
             int mt, nt;
             tile_of(g, t, mt, nt);
             const uint32_t buf = count & 1;
-            if (abort_flag || !mbar_wait_bounded(accf0 + 8 * buf, (count >> 1) & 1, kTileWaitNs)) {
-                if (!abort_flag) tile_timeout(&abort_flag);
+            if (!warp_wait(accf0 + 8 * buf, (count >> 1) & 1, kTileWaitNs)) {
+                if (lane == 0) tile_timeout();
                 break;
             }
             tc5::fence_after_sync();

@@ -20,56 +20,93 @@ MX4_FORMATS = {"mxfp4": 0, "nvfp4": 1}
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 
 
+_types = _types16 = _uint8 = _int32 = _Tensor = _empty = _raw_stream = None
+
+
 def _torch():
-    return _ddg._torch()
+    """torch, imported on the first call (with the lookups that every call makes)."""
+    global _types, _types16, _uint8, _int32, _Tensor, _empty, _raw_stream
+    import torch
+    if _types is None:
+        _uint8, _int32, _Tensor, _empty = torch.uint8, torch.int32, torch.Tensor, torch.empty
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _types16 = {torch.bfloat16: 1, torch.float16: 2}
+        _types = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    return torch
+
+
+def _stream(stream, t):
+    """The handle of `stream`, or of the current stream of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return _torch().cuda.current_stream(t.device).cuda_stream
+
+
+def _call(name, *args):
+    status = getattr(_ddg._lib or _ddg.load(), name)(*args)
+    if status != 0:
+        raise _ddg.DDGemmError(name, status)
 
 
 def _lookup(table, key, name):
-    if key not in table:
+    value = table.get(key)
+    if value is None:
         raise ValueError(f"{name} must be one of {', '.join(table)}")
-    return table[key]
+    return value
 
 
 def _type(dtype, name, sixteen=False):
-    torch = _torch()
-    types = {torch.bfloat16: 1, torch.float16: 2} if sixteen else {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    if dtype not in types:
+    if _types is None:
+        _torch()
+    types = _types16 if sixteen else _types
+    code = types.get(dtype)
+    if code is None:
         raise TypeError(f"{name} must be {' or '.join(str(t) for t in types)}")
-    return types[dtype]
+    return code
 
 
 def _matrix(t, name, dtype=None):
-    """A 2-D CUDA tensor with unit column stride (of `dtype`)."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or (dtype is not None and t.dtype != dtype):
+    """(rows, columns, leading dimension) of a 2-D CUDA tensor with unit column
+    stride (of `dtype`)."""
+    if _types is None:
+        _torch()
+    if not isinstance(t, _Tensor) or t.dim() != 2 or (dtype is not None and t.dtype != dtype):
         raise TypeError(f"{name} must be a 2-D {dtype or 'torch'} tensor")
     if not t.is_cuda:
         raise TypeError(f"{name} must be on a CUDA device")
-    if t.numel() > 0 and t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if cols > 1 and rows > 0 and unit != 1:
         raise ValueError(f"{name} must be row-major with unit column stride")
-    if t.shape[0] > 1 and t.shape[1] > 0 and t.stride(0) < t.shape[1]:
+    if rows <= 1 or cols == 0:
+        ld = cols or 1
+    elif ld < cols:
         raise ValueError(f"{name} must have rows that do not overlap")
-    return t
+    return rows, cols, ld
 
 
-def _like(out, shape, dtype, device, name, stream):
-    """`out` checked, or a new tensor (recorded on `stream`, which may not be
-    the one it was allocated for)."""
-    torch = _torch()
+def _like(out, shape, dtype, like, name, stream):
+    """(`out` checked, or a new tensor on like's device, its leading
+    dimension); a new one is recorded on `stream`, which may not be the one it
+    was allocated for."""
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
+        out = _empty(shape, dtype=dtype, device=like.device)
         if stream is not None:
             out.record_stream(stream)
-        return out
-    _matrix(out, name, dtype)
-    if tuple(out.shape) != tuple(shape) or out.device != device:
-        raise ValueError(f"{name} must be {tuple(shape)} on {device}")
-    return out
+        return out, shape[1] or 1
+    rows, cols, ld = _matrix(out, name, dtype)
+    if (rows, cols) != tuple(shape) or out.device != like.device:
+        raise ValueError(f"{name} must be {tuple(shape)} on {like.device}")
+    return out, ld
 
 
 def _same_device(*tensors):
-    if any(t is not None and t.device != tensors[0].device for t in tensors):
-        raise ValueError("tensors must be on the same device")
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != index:
+            raise ValueError("tensors must be on the same device")
 
 
 # ---- 4-bit matrices ----
@@ -94,70 +131,81 @@ class MX4:
         return (self.rows, self.k)
 
     def _args(self, name):
-        torch = _torch()
+        """Format, pointers and leading dimension, checked."""
+        if _types is None:
+            _torch()
         fmt = _lookup(MX4_FORMATS, self.fmt, "fmt")
-        width, scale_bytes = mx4_layout(self.rows, self.k, self.fmt)
-        c, s, e = self.codes, self.scales, self.exponents
-        if not isinstance(c, torch.Tensor) or c.dtype != torch.uint8 or c.dim() != 2 or not c.is_cuda:
+        c, s, e, rows = self.codes, self.scales, self.exponents, self.rows
+        width, scale_bytes = _sizes(fmt, rows, self.k)
+        if not isinstance(c, _Tensor) or c.dtype != _uint8 or c.dim() != 2 or not c.is_cuda:
             raise TypeError(f"{name}.codes must be a 2-D uint8 CUDA tensor")
-        if c.shape[0] != self.rows or c.shape[1] < width or (c.numel() > 0 and c.stride(1) != 1):
-            raise ValueError(f"{name}.codes must be {self.rows} rows of at least {width} bytes")
-        if not isinstance(s, torch.Tensor) or s.dtype != torch.uint8 or not s.is_cuda:
+        have, bytes_ = c.shape
+        ld, unit = c.stride()
+        if have != rows or bytes_ < width or (bytes_ > 1 and rows > 0 and unit != 1):
+            raise ValueError(f"{name}.codes must be {rows} rows of at least {width} bytes")
+        if not isinstance(s, _Tensor) or s.dtype != _uint8 or not s.is_cuda:
             raise TypeError(f"{name}.scales must be a uint8 CUDA tensor")
         if s.numel() < scale_bytes or not s.is_contiguous():
             raise ValueError(f"{name}.scales must hold {scale_bytes} contiguous bytes")
+        pointer = None
         if fmt == 1:
-            if not isinstance(e, torch.Tensor) or e.dtype != torch.int32 or not e.is_cuda:
+            if not isinstance(e, _Tensor) or e.dtype != _int32 or not e.is_cuda:
                 raise TypeError(f"{name}.exponents must be an int32 CUDA tensor")
-            if e.numel() < self.rows or not e.is_contiguous():
-                raise ValueError(f"{name}.exponents must hold {self.rows} contiguous values")
+            if e.numel() < rows or not e.is_contiguous():
+                raise ValueError(f"{name}.exponents must hold {rows} contiguous values")
             _same_device(c, s, e)
-        _same_device(c, s)
-        ld = c.stride(0) if self.rows > 1 else -(-c.shape[1] // 16) * 16
-        return fmt, c.data_ptr(), ld, s.data_ptr(), (e.data_ptr() if fmt == 1 else None)
+            pointer = e.data_ptr()
+        else:
+            _same_device(c, s)
+        return fmt, c.data_ptr(), ld if rows > 1 else -(-bytes_ // 16) * 16, s.data_ptr(), pointer
+
+
+def _sizes(fmt, rows, k):
+    """dd_mx4_layout for sizes that a tensor can have."""
+    per_k = 8 if fmt == 0 else 16
+    return -(-k // 32) * 16, -(-rows // 128) * -(-k // 256) * per_k * 128
 
 
 def mx4_layout(rows: int, k: int, fmt: str = "mxfp4"):
     """(bytes of a row of codes, bytes of all scales) of a rows x k matrix."""
     width, scales = ctypes.c_int64(), ctypes.c_int64()
-    _ddg._check("dd_mx4_layout", _ddg.load().dd_mx4_layout(_lookup(MX4_FORMATS, fmt, "fmt"), rows, k,
-                                                          ctypes.byref(width), ctypes.byref(scales)))
+    _call("dd_mx4_layout", _lookup(MX4_FORMATS, fmt, "fmt"), rows, k, ctypes.byref(width), ctypes.byref(scales))
     return width.value, scales.value
 
 
 def mx4_quantize(x, fmt: str = "mxfp4", cols: bool = False, out: MX4 | None = None, stream=None) -> MX4:
     """The rows of x (float32, bfloat16 or float16), or with cols its columns,
     in 4-bit form.  A K x N right-hand side is quantised with cols=True."""
-    torch = _torch()
     f = _lookup(MX4_FORMATS, fmt, "fmt")
-    _matrix(x, "x")
+    rows, k, ld = _matrix(x, "x")
     t = _type(x.dtype, "x")
-    rows, k = (x.shape[1], x.shape[0]) if cols else (x.shape[0], x.shape[1])
+    if cols:
+        rows, k = k, rows
     if out is None:
-        width, scale_bytes = mx4_layout(rows, k, fmt)
-        new = lambda *shape, dtype=torch.uint8: torch.empty(shape, dtype=dtype, device=x.device)  # noqa: E731
-        out = MX4(new(rows, width), new(scale_bytes), new(rows, dtype=torch.int32) if f else None, rows, k, fmt)
+        width, scale_bytes = _sizes(f, rows, k)
+        codes, scales = _empty((rows, width), dtype=_uint8, device=x.device), _empty(scale_bytes, dtype=_uint8, device=x.device)
+        exponents = _empty(rows, dtype=_int32, device=x.device) if f else None
+        out = MX4(codes, scales, exponents, rows, k, fmt)
         if stream is not None:
-            for part in (out.codes, out.scales) + ((out.exponents,) if f else ()):
+            for part in (codes, scales) + ((exponents,) if f else ()):
                 part.record_stream(stream)
-    elif out.shape != (rows, k) or out.fmt != fmt:
-        raise ValueError(f"out must be a {rows} x {k} {fmt} matrix")
-    _, codes, ldq, scales, exponents = out._args("out")
-    _same_device(x, out.codes)
-    _ddg._check("dd_mx4_quantize", _ddg.load().dd_mx4_quantize(
-        f, t, int(cols), rows, k, x.data_ptr(), _ddg._ld(x), codes, ldq, scales, exponents, _ddg._stream_handle(stream)))
+        args = codes.data_ptr(), width, scales.data_ptr(), exponents.data_ptr() if f else None
+    else:
+        if out.shape != (rows, k) or out.fmt != fmt:
+            raise ValueError(f"out must be a {rows} x {k} {fmt} matrix")
+        args = out._args("out")[1:]
+        _same_device(x, out.codes)
+    _call("dd_mx4_quantize", f, t, int(cols), rows, k, x.data_ptr(), ld, *args, _stream(stream, x))
     return out
 
 
 def mx4_dequantize(q: MX4, dtype=None, out=None, stream=None):
     """The values q stands for, as a rows x k tensor (bfloat16 by default, which holds them exactly)."""
-    torch = _torch()
-    dtype = dtype or (out.dtype if out is not None else torch.bfloat16)
+    dtype = dtype or (out.dtype if out is not None else _torch().bfloat16)
     t = _type(dtype, "dtype")
-    f, codes, ldq, scales, exponents = q._args("q")
-    out = _like(out, q.shape, dtype, q.codes.device, "out", stream)
-    _ddg._check("dd_mx4_dequantize", _ddg.load().dd_mx4_dequantize(
-        f, t, q.rows, q.k, codes, ldq, scales, exponents, out.data_ptr(), _ddg._ld(out), _ddg._stream_handle(stream)))
+    args = q._args("q")
+    out, ld = _like(out, (q.rows, q.k), dtype, q.codes, "out", stream)
+    _call("dd_mx4_dequantize", args[0], t, q.rows, q.k, *args[1:], out.data_ptr(), ld, _stream(stream, out))
     return out
 
 
@@ -174,60 +222,55 @@ def mx4_tile_scales(scales, fmt: str = "mxfp4"):
 def mx4_gemm(a: MX4, b: MX4, dtype=None, out=None, alpha: float = 1.0, stream=None):
     """alpha a b^T for 4-bit matrices a (M x K) and b (N x K) of one format, as
     an M x N tensor (bfloat16 by default)."""
-    torch = _torch()
     if a.fmt != b.fmt or a.k != b.k:
         raise ValueError("a and b must share format and k")
-    dtype = dtype or (out.dtype if out is not None else torch.bfloat16)
+    dtype = dtype or (out.dtype if out is not None else _torch().bfloat16)
     t = _type(dtype, "dtype")
-    f, ac, lda, as_, ae = a._args("a")
-    _, bc, ldb, bs, be = b._args("b")
+    left, right = a._args("a"), b._args("b")
     _same_device(a.codes, b.codes)
-    out = _like(out, (a.rows, b.rows), dtype, a.codes.device, "out", stream)
-    _ddg._check("dd_mx4_gemm", _ddg.load().dd_mx4_gemm(
-        f, a.rows, b.rows, a.k, ac, lda, as_, ae, bc, ldb, bs, be, alpha, t, out.data_ptr(), _ddg._ld(out),
-        _ddg._stream_handle(stream)))
+    out, ld = _like(out, (a.rows, b.rows), dtype, a.codes, "out", stream)
+    _call("dd_mx4_gemm", left[0], a.rows, b.rows, a.k, *left[1:], *right[1:], alpha, t, out.data_ptr(), ld,
+          _stream(stream, out))
     return out
 
 
 # ---- the gated block ----
 
 def _ff_shapes(x, Wg, Wu, Wd):
-    for t, n in ((x, "x"), (Wg, "Wg"), (Wu, "Wu"), (Wd, "Wd")):
-        _matrix(t, n, x.dtype if n != "x" else None)
-    code = _type(x.dtype, "x", sixteen=True)
-    T, D = x.shape
-    F = Wg.shape[0]
-    if tuple(Wg.shape) != (F, D) or tuple(Wu.shape) != (F, D) or tuple(Wd.shape) != (D, F):
+    """(type, T, D, F, the operands' pointers and leading dimensions in turn)."""
+    T, D, ldx = _matrix(x, "x")
+    dtype = x.dtype
+    code = _type(dtype, "x", sixteen=True)
+    F, dg, ldg = _matrix(Wg, "Wg", dtype)
+    fu, du, ldu = _matrix(Wu, "Wu", dtype)
+    dd, fd, ldd = _matrix(Wd, "Wd", dtype)
+    if (dg, fu, du, dd, fd) != (D, F, D, D, F):
         raise ValueError("Wg and Wu must be F x D and Wd D x F for x of T x D")
     _same_device(x, Wg, Wu, Wd)
-    return code, T, D, F
+    return code, T, D, F, (x.data_ptr(), ldx, Wg.data_ptr(), ldg, Wu.data_ptr(), ldu, Wd.data_ptr(), ldd)
 
 
 def ff_gated_saved_size(T: int, F: int, dtype) -> int:
     """Bytes that ff_gated(save=True) keeps for the backward pass."""
     n = ctypes.c_size_t()
-    _ddg._check("dd_ff_gated_saved_size", _ddg.load().dd_ff_gated_saved_size(_type(dtype, "dtype", sixteen=True), T, F,
-                                                                            ctypes.byref(n)))
+    _call("dd_ff_gated_saved_size", _type(dtype, "dtype", sixteen=True), T, F, ctypes.byref(n))
     return n.value
 
 
 def ff_gated(x, Wg, Wu, Wd, act: str = "silu", save: bool = False, out=None, stream=None):
     """y = (act(x Wg^T) * (x Wu^T)) Wd^T in bfloat16 or float16 (x: T x D, Wg and
     Wu: F x D, Wd: D x F); with save=True (y, saved) for ff_gated_backward."""
-    torch = _torch()
-    code, T, D, F = _ff_shapes(x, Wg, Wu, Wd)
+    code, T, D, F, operands = _ff_shapes(x, Wg, Wu, Wd)
     a = _lookup(ACTIVATIONS, act, "act")
-    y = _like(out, (T, D), x.dtype, x.device, "out", stream)
+    y, ldy = _like(out, (T, D), x.dtype, x, "out", stream)
     saved, n = None, 0
     if save:
         n = ff_gated_saved_size(T, F, x.dtype)
-        saved = torch.empty(n, dtype=torch.uint8, device=x.device)
+        saved = _empty(n, dtype=_uint8, device=x.device)
         if stream is not None:
             saved.record_stream(stream)
-    ld = _ddg._ld
-    _ddg._check("dd_ff_gated", _ddg.load().dd_ff_gated(
-        code, a, T, D, F, x.data_ptr(), ld(x), Wg.data_ptr(), ld(Wg), Wu.data_ptr(), ld(Wu), Wd.data_ptr(), ld(Wd),
-        y.data_ptr(), ld(y), saved.data_ptr() if n else None, n, _ddg._stream_handle(stream)))
+    _call("dd_ff_gated", code, a, T, D, F, *operands, y.data_ptr(), ldy, saved.data_ptr() if n else None, n,
+          _stream(stream, x))
     return (y, saved) if save else y
 
 
@@ -235,26 +278,23 @@ def ff_gated_backward(dy, x, Wg, Wu, Wd, saved, dx=None, dWg=None, dWu=None, dWd
     """(dx, dWg, dWu, dWd) from dy and what ff_gated(save=True) kept; `need` says
     which of them are wanted (None in the place of the others).  Tensors that
     are given are overwritten."""
-    torch = _torch()
-    code, T, D, F = _ff_shapes(x, Wg, Wu, Wd)
-    _matrix(dy, "dy", x.dtype)
-    if tuple(dy.shape) != (T, D):
+    code, T, D, F, operands = _ff_shapes(x, Wg, Wu, Wd)
+    rows, cols, lddy = _matrix(dy, "dy", x.dtype)
+    if (rows, cols) != (T, D):
         raise ValueError("dy must be T x D")
-    if not isinstance(saved, torch.Tensor) or saved.dtype != torch.uint8 or not saved.is_cuda or not saved.is_contiguous():
+    if not isinstance(saved, _Tensor) or saved.dtype != _uint8 or not saved.is_cuda or not saved.is_contiguous():
         raise TypeError("saved must be the uint8 CUDA tensor that ff_gated returned")
-    if saved.numel() != ff_gated_saved_size(T, F, x.dtype):
+    n = saved.numel()
+    if n != ff_gated_saved_size(T, F, x.dtype):
         raise ValueError("saved is of another T, F or type")
     _same_device(x, dy, saved)
-    shapes = (("dx", dx, (T, D)), ("dWg", dWg, (F, D)), ("dWu", dWu, (F, D)), ("dWd", dWd, (D, F)))
-    outs = [_like(o, shape, x.dtype, x.device, n, stream) if want else None for (n, o, shape), want in zip(shapes, need)]
-    ld = _ddg._ld
-    args = []
-    for o, (_, _, shape) in zip(outs, shapes):
-        args += [o.data_ptr(), ld(o)] if o is not None else [None, max(shape[1], 1)]
-    _ddg._check("dd_ff_gated_backward", _ddg.load().dd_ff_gated_backward(
-        code, T, D, F, dy.data_ptr(), ld(dy), x.data_ptr(), ld(x), Wg.data_ptr(), ld(Wg), Wu.data_ptr(), ld(Wu),
-        Wd.data_ptr(), ld(Wd), saved.data_ptr() if saved.numel() else None, saved.numel(), *args,
-        _ddg._stream_handle(stream)))
+    outs, args = [], []
+    for name, o, shape, want in zip(("dx", "dWg", "dWu", "dWd"), (dx, dWg, dWu, dWd), ((T, D), (F, D), (F, D), (D, F)), need):
+        o, ld = _like(o, shape, x.dtype, x, name, stream) if want else (None, shape[1] or 1)
+        outs.append(o)
+        args += (o.data_ptr() if want else None, ld)
+    _call("dd_ff_gated_backward", code, T, D, F, dy.data_ptr(), lddy, *operands, saved.data_ptr() if n else None, n, *args,
+          _stream(stream, x))
     return tuple(outs)
 
 
@@ -267,27 +307,27 @@ def mx4_ff_weights(Wg, Wu, Wd, fmt: str = "mxfp4", stream=None):
     F, D = Wg.shape
     if tuple(Wu.shape) != (F, D) or tuple(Wd.shape) != (D, F):
         raise ValueError("Wg and Wu must be F x D and Wd D x F")
-    pair = [torch.nn.functional.pad(w, (0, 0, 0, -F % 32)).view(-1, 32, D) for w in (Wg, Wu)]
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mx4_ff_weights(Wg, Wu, Wd, fmt)
+    pair = [torch.nn.functional.pad(w, (0, 0, 0, -F % 32)).reshape(-1, 32, D) for w in (Wg, Wu)]
     both = torch.stack(pair, 1).view(-1, D)
-    return mx4_quantize(both, fmt, stream=stream), mx4_quantize(_matrix(Wd, "Wd"), fmt, stream=stream)
+    return mx4_quantize(both, fmt), mx4_quantize(Wd, fmt)
 
 
 def mx4_ff_gated(x, w_in: MX4, w_out: MX4, act: str = "silu", out=None, stream=None):
     """y = (act(x Wg^T) * (x Wu^T)) Wd^T with 4-bit operands: the weights as
     mx4_ff_weights lays them out, x and the hidden values quantised in the
     call.  x and y: float32, bfloat16 or float16, T x D."""
-    _matrix(x, "x")
+    T, D, ldx = _matrix(x, "x")
     t = _type(x.dtype, "x")
     a = _lookup(ACTIVATIONS, act, "act")
-    T, D = x.shape
     F = w_out.k
     if w_in.fmt != w_out.fmt or w_in.k != D or w_out.rows != D or w_in.rows != 2 * (-(-F // 32) * 32):
         raise ValueError("w_in must be 2 * (F rounded up to 32) x D and w_out D x F, of one format")
-    f, ic, ldi, is_, ie = w_in._args("w_in")
-    _, oc, ldo, os_, oe = w_out._args("w_out")
+    first, second = w_in._args("w_in"), w_out._args("w_out")
     _same_device(x, w_in.codes, w_out.codes)
-    y = _like(out, (T, D), x.dtype, x.device, "out", stream)
-    _ddg._check("dd_mx4_ff_gated", _ddg.load().dd_mx4_ff_gated(
-        f, t, a, T, D, F, x.data_ptr(), _ddg._ld(x), ic, ldi, is_, ie, oc, ldo, os_, oe, y.data_ptr(), _ddg._ld(y),
-        _ddg._stream_handle(stream)))
+    y, ldy = _like(out, (T, D), x.dtype, x, "out", stream)
+    _call("dd_mx4_ff_gated", first[0], t, a, T, D, F, x.data_ptr(), ldx, *first[1:], *second[1:], y.data_ptr(), ldy,
+          _stream(stream, x))
     return y
