@@ -15,48 +15,52 @@
 namespace ddg {
 namespace {
 
-// C = accumulators, rounded once.
-template <typename T>
+// C = accumulators, rounded once; of one product, or of each of three.
+template <typename T, int NT_, int P>
 struct EpiStore {
-    static constexpr int GROUPS = 2;
-    T* C;
-    int64_t ldc, M, N;
-    bool vec;
+    static constexpr int NT = NT_, GROUPS = 2;
+    T* C[P];
+    int64_t ldc[P], M[P], N[P];
+    bool vec[P];
     template <class Release>
-    __device__ __forceinline__ void run(uint32_t acc, int64_t row, int nt, int group, int, Release release) const {
+    __device__ __forceinline__ void run(uint32_t acc, int p, int64_t row, int nt, int group, int, Release release) const {
+        if (P == 1) p = 0;
+        constexpr int STEPS = NT / GROUPS / 32;
 #pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-            const int c = group * 128 + j * 32;
+        for (int j = 0; j < STEPS; ++j) {
+            const int c = (group * STEPS + j) * 32;
             uint32_t v[32];
             tc5::ld32(acc + c, v);
-            if (j == 3) release();
+            if (j == STEPS - 1) release();
             float f[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-            if (row < M) store32(C + row * ldc, (int64_t)nt * 256 + c, N, vec, f);
+            if (row < M[p]) store32(C[p] + row * ldc[p], (int64_t)nt * NT + c, N[p], vec[p], f);
         }
     }
 };
 
-// h = act(g) * u from accumulators of 128 columns of g and 128 of u, rounded to
-// 16 bits (the operand of the next product); SAVE: a = act(g), b = u act'(g).
-template <typename T, bool SAVE>
+// h = act(g) * u from accumulators of NT / 2 columns of g and as many of u,
+// rounded to 16 bits (the operand of the next product); SAVE: a = act(g),
+// b = u act'(g).
+template <typename T, int NT_, bool SAVE>
 struct EpiGate {
-    static constexpr int GROUPS = 2;
+    static constexpr int NT = NT_, GROUPS = 2;
     T* h;
     float *a, *b;
     int64_t ld, M, N;  // N: F rounded up to 64 (the planes' rows, ld)
     int act;
     template <class Release>
-    __device__ __forceinline__ void run(uint32_t acc, int64_t row, int nt, int group, int, Release release) const {
+    __device__ __forceinline__ void run(uint32_t acc, int, int64_t row, int nt, int group, int, Release release) const {
+        constexpr int STEPS = NT / 2 / GROUPS / 32;
 #pragma unroll 1
-        for (int j = 0; j < 2; ++j) {
-            const int c = group * 64 + j * 32;
+        for (int j = 0; j < STEPS; ++j) {
+            const int c = (group * STEPS + j) * 32;
             uint32_t g[32], u[32];
             tc5::ld32(acc + c, g);
-            tc5::ld32(acc + 128 + c, u);
-            if (j == 1) release();
-            const int64_t col = (int64_t)nt * 128 + c;
+            tc5::ld32(acc + NT / 2 + c, u);
+            if (j == STEPS - 1) release();
+            const int64_t col = (int64_t)nt * (NT / 2) + c;
             if (row >= M || col >= N) continue;
             float hv[32], av[32], bv[32];
             with_activation(act, [&](auto tag) {
@@ -78,21 +82,22 @@ struct EpiGate {
 };
 
 // dg = dh b, du = dh a, rounded to 16 bits (operands of the next products).
-template <typename T>
+template <typename T, int NT_>
 struct EpiGateBackward {
-    static constexpr int GROUPS = 2;
+    static constexpr int NT = NT_, GROUPS = 2;
     const float *a, *b;
     T *dg, *du;
     int64_t ld, M, N;
     template <class Release>
-    __device__ __forceinline__ void run(uint32_t acc, int64_t row, int nt, int group, int, Release release) const {
+    __device__ __forceinline__ void run(uint32_t acc, int, int64_t row, int nt, int group, int, Release release) const {
+        constexpr int STEPS = NT / GROUPS / 32;
 #pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-            const int c = group * 128 + j * 32;
+        for (int j = 0; j < STEPS; ++j) {
+            const int c = (group * STEPS + j) * 32;
             uint32_t v[32];
             tc5::ld32(acc + c, v);
-            if (j == 3) release();
-            const int64_t col = (int64_t)nt * 256 + c;
+            if (j == STEPS - 1) release();
+            const int64_t col = (int64_t)nt * NT + c;
             if (row >= M || col >= N) continue;
 #pragma unroll
             for (int i = 0; i < 32; i += 16) {
@@ -166,14 +171,24 @@ cudaError_t map16(CUtensorMap* m, const Matrix16& x, int box_rows) {
     return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, x.p, x.cols, x.rows, ld * 2, 64, box_rows, true);
 }
 
+// A product's depth and tiles; PER: columns of B under a tile (64 or 128 of
+// each matrix if gated).
 TileArgs tile_args(int64_t M, int64_t N, int64_t per_tile, int64_t K, int segs) {
     TileArgs g = {};
-    g.mt = (int)((M + 255) / 256);
-    g.nt = (int)((N + per_tile - 1) / per_tile);
+    g.products = 1;
+    g.mt[0] = (int)((M + 255) / 256);
+    g.nt[0] = (int)((N + per_tile - 1) / per_tile);
     g.nk = (int)((K + 63) / 64);
     g.segs = segs;
     g.last_steps = (int)((K - (int64_t)(g.nk - 1) * 64 + 15) / 16);
     return g;
+}
+
+int64_t pair_tiles(int64_t M, int64_t N, int64_t per_tile) { return (M + 255) / 256 * ((N + per_tile - 1) / per_tile); }
+
+constexpr double kNarrow16 = 0.6;  // see narrow_tiles
+bool narrow16(int64_t M, int64_t N, int64_t wide) {
+    return narrow_tiles(pair_tiles(M, N, wide), pair_tiles(M, N, wide / 2), kNarrow16);
 }
 
 // sum over segments of A_s B_s^T; A_MN: A is K x M, B_MN: B is K x N.
@@ -182,13 +197,13 @@ cudaError_t product16(int64_t M, int64_t N, int64_t K, int segs, const Matrix16&
                       const Matrix16& B0, const Matrix16& B1, const Epi& epi, cudaStream_t st) {
     TileMaps maps;
     memset(&maps, 0, sizeof(maps));
-    constexpr int A_BOX = A_MN ? 64 : 128, B_BOX = B_MN ? 64 : 128;
+    constexpr int A_BOX = A_MN ? 64 : 128, B_BOX = B_MN ? 64 : Epi::NT / 2;
     cudaError_t err = map16(&maps.a[0], A0, A_BOX);
     if (err == cudaSuccess) err = map16(&maps.b[0], B0, B_BOX);
     if (err == cudaSuccess && segs == 2) err = map16(&maps.a[1], A1, A_BOX);
     if (err == cudaSuccess && (segs == 2 || GATED)) err = map16(&maps.b[1], B1, B_BOX);
     if (err != cudaSuccess) return err;
-    return launch_tile_gemm<KIND, A_MN, B_MN, GATED>(tile_args(M, N, GATED ? 128 : 256, K, segs), maps, epi, st);
+    return launch_tile_gemm<KIND, A_MN, B_MN, GATED>(tile_args(M, N, GATED ? Epi::NT / 2 : Epi::NT, K, segs), maps, epi, st);
 }
 
 // x (tokens x K) times the rows of W0 (and W1, 64 rows of each to a tile).
@@ -211,60 +226,103 @@ cudaError_t split16(const Matrix16& x, const Matrix16& W0, const Matrix16& W1, b
     return launch_split_gemm<KIND, PAIRED>(g, maps, epi, st);
 }
 
-int64_t pair_tiles(int64_t M, int64_t N, int64_t per_tile) { return (M + 255) / 256 * ((N + per_tile - 1) / per_tile); }
+template <typename T, int NT, int P>
+void set_store(EpiStore<T, NT, P>& epi, int p, void* C, int64_t ldc, int64_t M, int64_t N) {
+    epi.C[p] = static_cast<T*>(C);
+    epi.ldc[p] = ldc;
+    epi.M[p] = M;
+    epi.N[p] = N;
+    epi.vec[p] = (uintptr_t)C % 32 == 0 && (ldc * sizeof(T)) % 32 == 0;
+}
 
-template <typename T>
-EpiStore<T> store_to(void* C, int64_t ldc, int64_t M, int64_t N) {
-    return EpiStore<T>{static_cast<T*>(C), ldc, M, N, (uintptr_t)C % 32 == 0 && (ldc * sizeof(T)) % 32 == 0};
+// C = sum over segments, with wide or narrow tiles.
+template <int KIND, typename T, bool B_MN>
+cudaError_t store16(int64_t M, int64_t N, int64_t K, int segs, const Matrix16& A0, const Matrix16& A1,
+                    const Matrix16& B0, const Matrix16& B1, void* C, int64_t ldc, cudaStream_t st) {
+    if (narrow16(M, N, 256)) {
+        EpiStore<T, 128, 1> epi;
+        set_store(epi, 0, C, ldc, M, N);
+        return product16<KIND, false, B_MN, false>(M, N, K, segs, A0, A1, B0, B1, epi, st);
+    }
+    EpiStore<T, 256, 1> epi;
+    set_store(epi, 0, C, ldc, M, N);
+    return product16<KIND, false, B_MN, false>(M, N, K, segs, A0, A1, B0, B1, epi, st);
+}
+
+template <int KIND, typename T, int NT, bool SAVE>
+cudaError_t gate16(const FfForward& f, cudaStream_t st) {
+    return product16<KIND, false, false, true>(
+        f.T, f.F, f.D, 1, f.x, f.x, f.wg, f.wu,
+        EpiGate<T, NT, SAVE>{static_cast<T*>(f.h), f.a, f.b, f.ld, f.T, round_up(f.F, 64), f.act}, st);
 }
 
 template <int KIND, typename T>
 cudaError_t forward_typed(const FfForward& f, cudaStream_t st) {
     const Matrix16 h{f.h, f.T, f.F, f.ld};
     cudaError_t err;
-    if (split_takes(f.T, pair_tiles(f.T, f.F, 128)))
+    if (split_takes(f.T, pair_tiles(f.T, f.F, 128))) {
         err = split16<KIND, true>(f.x, f.wg, f.wu, false,
                                   EpiSplitGate<T>{static_cast<T*>(f.h), f.a, f.b, f.ld, f.F, f.act}, st);
-    else if (f.a != nullptr)
-        err = product16<KIND, false, false, true>(
-            f.T, f.F, f.D, 1, f.x, f.x, f.wg, f.wu,
-            EpiGate<T, true>{static_cast<T*>(f.h), f.a, f.b, f.ld, f.T, round_up(f.F, 64), f.act}, st);
-    else
-        err = product16<KIND, false, false, true>(
-            f.T, f.F, f.D, 1, f.x, f.x, f.wg, f.wu,
-            EpiGate<T, false>{static_cast<T*>(f.h), nullptr, nullptr, f.ld, f.T, round_up(f.F, 64), f.act}, st);
+    } else {
+        const bool narrow = narrow16(f.T, f.F, 128), save = f.a != nullptr;
+        err = narrow ? (save ? gate16<KIND, T, 128, true>(f, st) : gate16<KIND, T, 128, false>(f, st))
+                     : (save ? gate16<KIND, T, 256, true>(f, st) : gate16<KIND, T, 256, false>(f, st));
+    }
     if (err != cudaSuccess) return err;
     // Wd was complete before the launch above could end its own wait
     if (split_takes(f.T, pair_tiles(f.T, f.D, 256)))
-        err = split16<KIND, false>(h, f.wd, f.wd, true, EpiSplitStore<T>{static_cast<T*>(f.y), f.ldy, f.D}, st);
-    else
-        err = product16<KIND, false, false, false>(f.T, f.D, f.F, 1, h, h, f.wd, f.wd, store_to<T>(f.y, f.ldy, f.T, f.D),
-                                                   st);
-    return err;
+        return split16<KIND, false>(h, f.wd, f.wd, true, EpiSplitStore<T>{static_cast<T*>(f.y), f.ldy, f.D}, st);
+    return store16<KIND, T, false>(f.T, f.D, f.F, 1, h, h, f.wd, f.wd, f.y, f.ldy, st);
+}
+
+template <int KIND, typename T, int NT>
+cudaError_t gate_backward16(const FfBackward& f, cudaStream_t st) {
+    return product16<KIND, false, true, false>(
+        f.T, f.F, f.D, 1, f.dy, f.dy, f.wd, f.wd,
+        EpiGateBackward<T, NT>{f.a, f.b, static_cast<T*>(f.dg), static_cast<T*>(f.du), f.ld, f.T, round_up(f.F, 64)}, st);
+}
+
+// The weights' gradients that are wanted, in one launch: sums over the T rows
+// of both operands.
+template <int KIND, typename T, int NT>
+cudaError_t weights16(const FfBackward& f, const Matrix16& h, const Matrix16& dg, const Matrix16& du, cudaStream_t st) {
+    TileMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    EpiStore<T, NT, kMaxProducts> epi = {};
+    TileArgs g = tile_args(f.F, f.D, NT, f.T, 1);
+    g.products = 0;
+    cudaError_t err = cudaSuccess;
+    auto add = [&](const Matrix16& A, const Matrix16& B, void* C, int64_t ldc) {
+        if (C == nullptr || err != cudaSuccess) return;
+        const int p = g.products++;
+        err = map16(&maps.a[p], A, 64);
+        if (err == cudaSuccess) err = map16(&maps.b[p], B, 64);
+        g.mt[p] = (int)((A.cols + 255) / 256);
+        g.nt[p] = (int)((B.cols + NT - 1) / NT);
+        set_store(epi, p, C, ldc, A.cols, B.cols);
+    };
+    add(dg, f.x, f.dwg, f.lddwg);
+    add(du, f.x, f.dwu, f.lddwu);
+    add(f.dy, h, f.dwd, f.lddwd);
+    if (err != cudaSuccess || g.products == 0) return err;
+    return launch_tile_gemm<KIND, true, true, false>(g, maps, epi, st);
 }
 
 template <int KIND, typename T>
 cudaError_t backward_typed(const FfBackward& f, cudaStream_t st) {
     const Matrix16 h{const_cast<void*>(f.h), f.T, f.F, f.ld}, dg{f.dg, f.T, f.F, f.ld}, du{f.du, f.T, f.F, f.ld};
-    // dh = dy Wd: B is Wd, D x F (K x N)
-    cudaError_t err = product16<KIND, false, true, false>(
-        f.T, f.F, f.D, 1, f.dy, f.dy, f.wd, f.wd,
-        EpiGateBackward<T>{f.a, f.b, static_cast<T*>(f.dg), static_cast<T*>(f.du), f.ld, f.T, round_up(f.F, 64)}, st);
+    cudaError_t err = cudaSuccess;
+    // dh = dy Wd (B is Wd, D x F: K x N), unless only dWd is wanted
+    if (f.dx != nullptr || f.dwg != nullptr || f.dwu != nullptr)
+        err = narrow16(f.T, f.F, 256) ? gate_backward16<KIND, T, 128>(f, st) : gate_backward16<KIND, T, 256>(f, st);
     // dx = dg Wg + du Wu
     if (err == cudaSuccess && f.dx != nullptr)
-        err = product16<KIND, false, true, false>(f.T, f.D, f.F, 2, dg, du, f.wg, f.wu,
-                                                  store_to<T>(f.dx, f.lddx, f.T, f.D), st);
-    // the weights' gradients: sums over the T rows of both operands
-    if (err == cudaSuccess && f.dwg != nullptr)
-        err = product16<KIND, true, true, false>(f.F, f.D, f.T, 1, dg, dg, f.x, f.x,
-                                                 store_to<T>(f.dwg, f.lddwg, f.F, f.D), st);
-    if (err == cudaSuccess && f.dwu != nullptr)
-        err = product16<KIND, true, true, false>(f.F, f.D, f.T, 1, du, du, f.x, f.x,
-                                                 store_to<T>(f.dwu, f.lddwu, f.F, f.D), st);
-    if (err == cudaSuccess && f.dwd != nullptr)
-        err = product16<KIND, true, true, false>(f.D, f.F, f.T, 1, f.dy, f.dy, h, h,
-                                                 store_to<T>(f.dwd, f.lddwd, f.D, f.F), st);
-    return err;
+        err = store16<KIND, T, true>(f.T, f.D, f.F, 2, dg, du, f.wg, f.wu, f.dx, f.lddx, st);
+    if (err != cudaSuccess) return err;
+    const int64_t wide = 2 * pair_tiles(f.F, f.D, 256) + pair_tiles(f.D, f.F, 256);
+    const int64_t narrow = 2 * pair_tiles(f.F, f.D, 128) + pair_tiles(f.D, f.F, 128);
+    return narrow_tiles(wide, narrow, kNarrow16) ? weights16<KIND, T, 128>(f, h, dg, du, st)
+                                                 : weights16<KIND, T, 256>(f, h, dg, du, st);
 }
 
 }  // namespace

@@ -11,23 +11,45 @@ namespace {
 
 constexpr int QWARPS = 8;  // warps per block of the row kernels
 
-// A lane's 8 values of a row, k = k0 .. k0 + 7 (zero beyond K).
-template <typename T>
-__device__ __forceinline__ void load_row8(const T* row, int64_t k0, int64_t K, bool vec, float (&x)[8]) {
-    if (vec && k0 + 8 <= K) {
-        load8(row + k0, x);
+// A lane's 8 values of each of N tiles of 256 k of a row, from tile kt on and
+// `step` tiles apart (zero beyond K).  Where the row is 16-byte aligned and a
+// multiple of 8 long, the loads are issued without a branch between them (an
+// address beyond the row is pulled back into it): all are in flight together.
+template <typename T, int N>
+__device__ __forceinline__ void load_tiles(const T* row, int64_t kt, int64_t step, int lane, int64_t K, bool vec,
+                                           float (&x)[N][8]) {
+    if (vec) {
+        constexpr int W = sizeof(T) / 2;
+        uint4 raw[N][W];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int64_t k0 = min((kt + j * step) * MX4_TILE_K + lane * 8, K - 8);
+#pragma unroll
+            for (int i = 0; i < W; ++i) raw[j][i] = reinterpret_cast<const uint4*>(row + k0)[i];
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const bool in = (kt + j * step) * MX4_TILE_K + lane * 8 < K;
+            const T* t = reinterpret_cast<const T*>(raw[j]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[j][i] = in ? to_float<T>(t[i]) : 0.0f;
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = k0 + i < K ? to_float<T>(row[k0 + i]) : 0.0f;
+        for (int j = 0; j < N; ++j) {
+            const int64_t k0 = (kt + j * step) * MX4_TILE_K + lane * 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[j][i] = k0 + i < K ? to_float<T>(row[k0 + i]) : 0.0f;
+        }
     }
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
-// A warp's 256 k of one row: codes and scale words.  `unit` is 2^-e of an
-// nvfp4 row.
+// A warp's 256 k of one row: codes and scale words.  `e` is the exponent of
+// an nvfp4 row.
 template <int FMT>
-__device__ __forceinline__ void quantize_tile(const float (&x)[8], float unit, int lane, int64_t row, int64_t kt,
+__device__ __forceinline__ void quantize_tile(const float (&x)[8], int e, int lane, int64_t row, int64_t kt,
                                               int64_t K, uint8_t* codes, int64_t ldq, uint8_t* scales) {
     constexpr int LANES = mx4_block(FMT) / 8;  // lanes that share a block
     uint32_t m = 0;
@@ -43,10 +65,10 @@ __device__ __forceinline__ void quantize_tile(const float (&x)[8], float unit, i
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = x[i] * inv;
     } else {
-        byte = nvfp4_scale_byte(m, unit);
-        const float s = e4m3_value(byte), r = byte == 0u || byte == 127u ? 0.0f : __frcp_rn(s);
+        byte = nvfp4_scale_byte(m, exp2_int(-e));
+        const float s = nvfp4_step(byte, e), r = nvfp4_inverse(byte, s);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = r == 0.0f ? 0.0f : quotient(x[i] * unit, s, r);
+        for (int i = 0; i < 8; ++i) y[i] = quotient(x[i], s, r);
     }
     if (kt * MX4_TILE_K + lane * 8 < round_up(K, 32))
         *reinterpret_cast<uint32_t*>(codes + row * ldq + kt * (MX4_TILE_K / 2) + lane * 4) = e2m1_pack8(y);
@@ -60,21 +82,24 @@ __device__ __forceinline__ void quantize_tile(const float (&x)[8], float unit, i
     }
 }
 
-// mxfp4 rows: one warp for 256 k of a row.
-template <typename T>
+// mxfp4 rows: one warp for TILES times 256 k of a row, all loaded before the
+// first is converted (one tile where there are few: latency counts then).
+template <typename T, int TILES>
 __global__ void __launch_bounds__(QWARPS * 32) mxfp4_rows_kernel(const T* X, int64_t ldx, int64_t rows, int64_t K,
                                                                  bool vec, uint8_t* codes, int64_t ldq,
                                                                  uint8_t* scales) {
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t kts = (K + MX4_TILE_K - 1) / MX4_TILE_K;
+    const int64_t kts = (K + MX4_TILE_K - 1) / MX4_TILE_K, steps = (kts + TILES - 1) / TILES;
     const int64_t item = (int64_t)blockIdx.x * QWARPS + (threadIdx.x >> 5);
-    if (item >= rows * kts) return;
-    const int64_t row = item / kts, kt = item % kts;
-    float x[8];
-    load_row8(X + row * ldx, kt * MX4_TILE_K + lane * 8, K, vec, x);
-    quantize_tile<kMxfp4>(x, 1.0f, lane, row, kt, K, codes, ldq, scales);
+    if (item >= rows * steps) return;
+    const int64_t row = item / steps, kt = item % steps * TILES;
+    float x[TILES][8];
+    load_tiles<T, TILES>(X + row * ldx, kt, 1, lane, K, vec, x);
+#pragma unroll
+    for (int j = 0; j < TILES; ++j)
+        if (kt + j < kts) quantize_tile<kMxfp4>(x[j], 0, lane, row, kt + j, K, codes, ldq, scales);
 }
 
 // nvfp4 rows: one block for a row.  The row's values stay in registers
@@ -101,18 +126,13 @@ __global__ void __launch_bounds__(QWARPS * 32) nvfp4_rows_kernel(const T* X, int
             m = max(m, b < kInfBits ? b : 0u);
         }
     };
+    load_tiles<T, KEEP>(src, warp, warps, lane, K, vec, keep);
 #pragma unroll
-    for (int j = 0; j < KEEP; ++j) {
-        const int64_t kt = warp + (int64_t)j * warps;
-        if (kt < kts) load_row8(src, kt * MX4_TILE_K + lane * 8, K, vec, keep[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < KEEP; ++j)
-        if (warp + (int64_t)j * warps < kts) take(keep[j]);
+    for (int j = 0; j < KEEP; ++j) take(keep[j]);
     for (int64_t kt = warp + (int64_t)KEEP * warps; kt < kts; kt += warps) {
-        float x[8];
-        load_row8(src, kt * MX4_TILE_K + lane * 8, K, vec, x);
-        take(x);
+        float x[1][8];
+        load_tiles<T, 1>(src, kt, 1, lane, K, vec, x);
+        take(x[0]);
     }
     m = __reduce_max_sync(~0u, m);
     if (lane == 0) part[warp] = m;
@@ -120,17 +140,16 @@ __global__ void __launch_bounds__(QWARPS * 32) nvfp4_rows_kernel(const T* X, int
     m = part[0];
     for (int w = 1; w < warps; ++w) m = max(m, part[w]);
     const int e = nvfp4_row_exponent(m);
-    const float unit = exp2_int(-e);
     if (threadIdx.x == 0) exponents[row] = e;
 #pragma unroll
     for (int j = 0; j < KEEP; ++j) {
         const int64_t kt = warp + (int64_t)j * warps;
-        if (kt < kts) quantize_tile<kNvfp4>(keep[j], unit, lane, row, kt, K, codes, ldq, scales);
+        if (kt < kts) quantize_tile<kNvfp4>(keep[j], e, lane, row, kt, K, codes, ldq, scales);
     }
     for (int64_t kt = warp + (int64_t)KEEP * warps; kt < kts; kt += warps) {
-        float x[8];
-        load_row8(src, kt * MX4_TILE_K + lane * 8, K, vec, x);
-        quantize_tile<kNvfp4>(x, unit, lane, row, kt, K, codes, ldq, scales);
+        float x[1][8];
+        load_tiles<T, 1>(src, kt, 1, lane, K, vec, x);
+        quantize_tile<kNvfp4>(x[0], e, lane, row, kt, K, codes, ldq, scales);
     }
 }
 
@@ -142,6 +161,7 @@ template <> struct Two<float> {
     static __device__ __forceinline__ uint2 join(float a, float b) { return make_uint2(__float_as_uint(a), __float_as_uint(b)); }
 };
 template <> struct Two<__nv_bfloat16> {
+    static constexpr bool kBrain = true;
     using raw = uint32_t;
     static __device__ __forceinline__ void split(uint32_t r, float& a, float& b) {
         a = __uint_as_float(r << 16), b = __uint_as_float(r & 0xffff0000u);
@@ -151,6 +171,7 @@ template <> struct Two<__nv_bfloat16> {
     }
 };
 template <> struct Two<__half> {
+    static constexpr bool kBrain = false;
     using raw = uint32_t;
     static __device__ __forceinline__ void split(uint32_t r, float& a, float& b) {
         a = __half2float(__ushort_as_half((unsigned short)(r & 0xffffu)));
@@ -160,6 +181,35 @@ template <> struct Two<__half> {
         return (uint32_t)__half_as_ushort(a) | (uint32_t)__half_as_ushort(b) << 16;
     }
 };
+
+// Largest magnitudes of two columns over N rows, as the bits of floats (with
+// infinities and NaN, which are larger than any finite value; FINITE: without).
+// 16-bit values are compared two at a time as integers.
+template <typename T, int N, bool FINITE>
+__device__ __forceinline__ void max_pair(const typename Two<T>::raw* raw, uint32_t& m0, uint32_t& m1) {
+    if constexpr (sizeof(T) == 4) {
+        m0 = m1 = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t x = raw[i].x & 0x7fffffffu, y = raw[i].y & 0x7fffffffu;
+            m0 = max(m0, !FINITE || x < kInfBits ? x : 0u);
+            m1 = max(m1, !FINITE || y < kInfBits ? y : 0u);
+        }
+    } else {
+        constexpr uint32_t inf = sizeof(T) == 2 && Two<T>::kBrain ? 0x7f807f80u : 0x7c007c00u;
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            uint32_t x = raw[i] & 0x7fff7fffu;
+            if (FINITE) x &= __vcmpltu2(x, inf);
+            m = __vmaxu2(m, x);
+        }
+        float a, b;
+        Two<T>::split(m, a, b);
+        m0 = __float_as_uint(a);
+        m1 = __float_as_uint(b);
+    }
+}
 
 // Columns c and c + 1 of N consecutive rows from k on (zero beyond R and K).
 // The whole rows of a full tile are loaded without a branch between them, so
@@ -189,17 +239,10 @@ __global__ void __launch_bounds__(256) column_max_kernel(const T* X, int64_t ldx
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 64 + lane * 2, k0 = (int64_t)blockIdx.y * 256 + warp * 32;
-    uint32_t m0 = 0, m1 = 0;
+    uint32_t m0, m1;
     typename Two<T>::raw raw[32];
     load_columns<T, 32>(X, ldx, k0, c, K, R, vec, raw);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        float a, b;
-        Two<T>::split(raw[i], a, b);
-        const uint32_t x = abs_bits(a), y = abs_bits(b);
-        m0 = max(m0, x < kInfBits ? x : 0u);
-        m1 = max(m1, y < kInfBits ? y : 0u);
-    }
+    max_pair<T, 32, true>(raw, m0, m1);
     part[warp][lane * 2] = m0;
     part[warp][lane * 2 + 1] = m1;
     __syncthreads();
@@ -240,18 +283,11 @@ __global__ void __launch_bounds__(256) mx4_columns_kernel(const T* X, int64_t ld
                 if (kt == 0 && warp == 0) exponents[c + j] = e[j];
             }
     }
-    const float unit[2] = {exp2_int(-e[0]), exp2_int(-e[1])};
 #pragma unroll
     for (int b = 0; b < 32 / BLOCK; ++b) {
-        uint32_t m[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < BLOCK; ++i) {
-            float x, y;
-            Two<T>::split(raw[b * BLOCK + i], x, y);
-            m[0] = max(m[0], abs_bits(x));
-            m[1] = max(m[1], abs_bits(y));
-        }
-        float s[2] = {1.0f, 1.0f}, r[2];
+        uint32_t m[2];
+        max_pair<T, BLOCK, false>(raw + b * BLOCK, m[0], m[1]);
+        float s[2] = {0.0f, 0.0f}, r[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             uint32_t byte;
@@ -259,12 +295,13 @@ __global__ void __launch_bounds__(256) mx4_columns_kernel(const T* X, int64_t ld
                 byte = mxfp4_scale_byte(m[j]);
                 r[j] = mxfp4_inverse(byte);
             } else {
-                byte = nvfp4_scale_byte(m[j], unit[j]);
-                s[j] = e4m3_value(byte);
-                r[j] = byte == 0u || byte == 127u ? 0.0f : __frcp_rn(s[j]);
+                byte = nvfp4_scale_byte(m[j], exp2_int(-e[j]));
+                s[j] = nvfp4_step(byte, e[j]);
+                r[j] = nvfp4_inverse(byte, s[j]);
             }
             reinterpret_cast<uint8_t*>(&scale[j * 32 + lane][0])[warp * (32 / BLOCK) + b] = (uint8_t)byte;
         }
+        const uint64_t rr = pack_pair(r[0], r[1]), ss = pack_pair(-s[0], -s[1]);
 #pragma unroll
         for (int q = 0; q < BLOCK / 8; ++q) {
             float y[2][8];
@@ -272,9 +309,8 @@ __global__ void __launch_bounds__(256) mx4_columns_kernel(const T* X, int64_t ld
             for (int i = 0; i < 8; ++i) {
                 float v[2];
                 Two<T>::split(raw[b * BLOCK + q * 8 + i], v[0], v[1]);
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    y[j][i] = FMT == kMxfp4 ? v[j] * r[j] : r[j] == 0.0f ? 0.0f : quotient(v[j] * unit[j], s[j], r[j]);
+                const uint64_t vv = pack_pair(v[0], v[1]);
+                unpack_pair(FMT == kMxfp4 ? mul_pair(vv, rr) : quotient_pair(vv, ss, rr), y[0][i], y[1][i]);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) code[j * 32 + lane][warp * 4 + b * (BLOCK / 8) + q] = e2m1_pack8(y[j]);
@@ -353,11 +389,14 @@ template <typename T>
 cudaError_t quantize_typed(const Mx4Quantize& q, const T* X, cudaStream_t st) {
     const int64_t kts = (q.K + MX4_TILE_K - 1) / MX4_TILE_K;
     if (!q.cols) {
-        const bool vec = (uintptr_t)X % 16 == 0 && q.ldx * sizeof(T) % 16 == 0;
+        const bool vec = (uintptr_t)X % 16 == 0 && q.ldx * sizeof(T) % 16 == 0 && q.K % 8 == 0;
         if (q.fmt == kMxfp4) {
-            const int64_t items = q.rows * kts;
-            return launch_pdl(mxfp4_rows_kernel<T>, dim3((unsigned)((items + QWARPS - 1) / QWARPS)),
-                              dim3(QWARPS * 32), 0, st, X, q.ldx, q.rows, q.K, vec, q.codes, q.ldq, q.scales);
+            // four tiles a warp once that leaves every SM its 64 warps
+            const bool many = q.rows * kts >= 4 * 64 * 152;
+            const int64_t items = many ? q.rows * ((kts + 3) / 4) : q.rows * kts;
+            return launch_pdl(many ? mxfp4_rows_kernel<T, 4> : mxfp4_rows_kernel<T, 1>,
+                              dim3((unsigned)((items + QWARPS - 1) / QWARPS)), dim3(QWARPS * 32), 0, st, X, q.ldx,
+                              q.rows, q.K, vec, q.codes, q.ldq, q.scales);
         }
         const unsigned warps = (unsigned)(kts < QWARPS ? kts : QWARPS);
         return launch_pdl(nvfp4_rows_kernel<T>, dim3((unsigned)q.rows), dim3(warps * 32), 0, st, X, q.ldx, q.K, vec,
@@ -369,13 +408,12 @@ cudaError_t quantize_typed(const Mx4Quantize& q, const T* X, cudaStream_t st) {
         return launch_pdl(mx4_columns_kernel<T, kMxfp4>, grid, dim3(256), 0, st, X, q.ldx, q.rows, q.K, vec,
                           (const uint32_t*)nullptr, q.codes, q.ldq, q.scales, (int32_t*)nullptr);
     cudaError_t err = cudaMemsetAsync(q.column_max, 0, (size_t)q.rows * 4, st);
-    if (err != cudaSuccess) return err;
-    // the maxima follow a memset, which is no kernel: an ordinary launch
-    column_max_kernel<T><<<grid, 256, 0, st>>>(X, q.ldx, q.rows, q.K, vec, q.column_max);
-    err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-    return launch_pdl(mx4_columns_kernel<T, kNvfp4>, grid, dim3(256), 0, st, X, q.ldx, q.rows, q.K, vec,
-                      (const uint32_t*)q.column_max, q.codes, q.ldq, q.scales, q.exponents);
+    if (err == cudaSuccess)
+        err = launch_pdl(column_max_kernel<T>, grid, dim3(256), 0, st, X, q.ldx, q.rows, q.K, vec, q.column_max);
+    if (err == cudaSuccess)
+        err = launch_pdl(mx4_columns_kernel<T, kNvfp4>, grid, dim3(256), 0, st, X, q.ldx, q.rows, q.K, vec,
+                         (const uint32_t*)q.column_max, q.codes, q.ldq, q.scales, q.exponents);
+    return err;
 }
 
 template <typename T>

@@ -104,6 +104,16 @@ __device__ __forceinline__ uint32_t nvfp4_scale_byte(uint32_t max_bits, float un
     return byte > 0u ? byte : 1u;
 }
 
+// The scale of an nvfp4 block and its row's power of two in one: exact and
+// normal (2^-109 .. 2^126), as is the reciprocal.  Both 0 for a zero block and
+// for NaN: quotients of finite values are then 0.
+__device__ __forceinline__ float nvfp4_step(uint32_t byte, int e) {
+    return byte == 127u ? 0.0f : e4m3_value(byte) * exp2_int(e);
+}
+__device__ __forceinline__ float nvfp4_inverse(uint32_t byte, float step) {
+    return byte == 0u || byte == 127u ? 0.0f : __frcp_rn(step);
+}
+
 // y / s with r = 1 / s correctly rounded: one residual correction of y * r
 // gives the correctly rounded quotient (Markstein's theorem), and rounding
 // that to E2M1 is the same as rounding the exact quotient: |y - t s| is at
@@ -111,6 +121,31 @@ __device__ __forceinline__ uint32_t nvfp4_scale_byte(uint32_t max_bits, float un
 __device__ __forceinline__ float quotient(float y, float s, float r) {
     const float q = y * r;
     return fmaf(fmaf(-q, s, y), r, q);
+}
+
+// The same for two values with scales of their own, on packed 32-bit pairs.
+__device__ __forceinline__ uint64_t pack_pair(float a, float b) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a), "f"(b));
+    return p;
+}
+__device__ __forceinline__ void unpack_pair(uint64_t p, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+// `minus_s`: the scales negated.
+__device__ __forceinline__ uint64_t quotient_pair(uint64_t y, uint64_t minus_s, uint64_t r) {
+    const uint64_t q = mul_pair(y, r);
+    return fma_pair(fma_pair(q, minus_s, y), r, q);
 }
 
 // Eight values (already divided by their scales) as eight E2M1 codes, the

@@ -15,21 +15,21 @@ __device__ __forceinline__ int column_exponent(const int32_t* f, int64_t c, int6
 }
 
 // C = alpha * accumulators * 2^(e_i + f_j), rounded once.
-template <int KIND, typename T>
+template <int KIND, typename T, int NT_>
 struct EpiScale {
-    static constexpr int GROUPS = 3;
+    static constexpr int NT = NT_, GROUPS = NT / 64;
     T* C;
     int64_t ldc, M, N;
     const int32_t *e, *f;
     float alpha;
     bool vec;
     template <class Release>
-    __device__ __forceinline__ void run(uint32_t acc, int64_t row, int nt, int group, int lane, Release release) const {
+    __device__ __forceinline__ void run(uint32_t acc, int, int64_t row, int nt, int group, int lane, Release release) const {
         const int er = KIND == kKindNv && row < M ? e[row] : 0;
 #pragma unroll 1
         for (int j = 0; j < 2; ++j) {
             const int c = group * 64 + j * 32;
-            const int64_t col = (int64_t)nt * 192 + c;
+            const int64_t col = (int64_t)nt * NT + c;
             uint32_t v[32];
             tc5::ld32(acc + c, v);
             if (j == 1) release();
@@ -51,9 +51,9 @@ struct EpiScale {
 // mxfp4: a thread holds a whole block of 32 of its row and writes its codes
 // and scale; the last tile also clears the scales of the padding of k.
 // nvfp4: h in 32 bits, for the row's exponent is not known yet.
-template <int KIND>
+template <int KIND, int NT_>
 struct EpiGate4 {
-    static constexpr int GROUPS = 3;
+    static constexpr int NT = NT_, GROUPS = NT / 64;
     uint8_t *codes, *scales;
     float* h;
     int64_t ld;      // bytes of a row of codes (mxfp4), elements of a row of h (nvfp4)
@@ -62,15 +62,15 @@ struct EpiGate4 {
     const int32_t *e, *f;
     int act;
     template <class Release>
-    __device__ __forceinline__ void run(uint32_t acc, int64_t row, int n, int group, int lane, Release release) const {
+    __device__ __forceinline__ void run(uint32_t acc, int, int64_t row, int n, int group, int lane, Release release) const {
         uint32_t g[32], u[32];
         tc5::ld32(acc + group * 64, g);
         tc5::ld32(acc + group * 64 + 32, u);
         release();
-        const int64_t c = (int64_t)n * 96 + group * 32;
+        const int64_t c = (int64_t)n * (NT / 2) + group * 32;
         float hv[32];
         if (KIND == kKindNv) {
-            const int64_t wc = (int64_t)n * 192 + group * 64, W = round_up(F, 32) * 2;
+            const int64_t wc = (int64_t)n * NT + group * 64, W = round_up(F, 32) * 2;
             const int er = row < M ? e[row] : 0;
             const int fg = column_exponent(f, wc, W, lane), fu = column_exponent(f, wc + 32, W, lane);
 #pragma unroll
@@ -113,7 +113,7 @@ struct EpiGate4 {
             const int64_t b = c / 32;
             scales[mx4_scale_word(row, b / 4, tiles) + b % 4] = (uint8_t)byte;
         }
-        if (n == nt - 1 && group == 2)
+        if (n == nt - 1 && group == GROUPS - 1)
             for (int64_t b = (F + 31) / 32; b < tiles * 4; ++b) scales[mx4_scale_word(row, b / 4, tiles) + b % 4] = 0;
     }
 };
@@ -188,13 +188,14 @@ cudaError_t product4(const Mx4Matrix& A, const Mx4Matrix& B, const Epi& epi, cud
     TileMaps maps;
     memset(&maps, 0, sizeof(maps));
     cudaError_t err = map_codes(&maps.a[0], A, 128);
-    if (err == cudaSuccess) err = map_codes(&maps.b[0], B, 96);
+    if (err == cudaSuccess) err = map_codes(&maps.b[0], B, Epi::NT / 2);
     if (err == cudaSuccess) err = map_scales(&maps.sa, FMT, A);
     if (err == cudaSuccess) err = map_scales(&maps.sb, FMT, B);
     if (err != cudaSuccess) return err;
     TileArgs g = {};
-    g.mt = (int)((A.rows + 255) / 256);
-    g.nt = (int)((B.rows + 191) / 192);
+    g.products = 1;
+    g.mt[0] = (int)((A.rows + 255) / 256);
+    g.nt[0] = (int)((B.rows + Epi::NT - 1) / Epi::NT);
     g.nk = (int)((A.K + MX4_TILE_K - 1) / MX4_TILE_K);
     g.segs = 1;
     g.last_steps = (int)((A.K - (int64_t)(g.nk - 1) * MX4_TILE_K + 63) / 64);
@@ -223,17 +224,25 @@ cudaError_t split4(const Mx4Matrix& x, const Mx4Matrix& W, bool early, const Epi
     return launch_split_gemm<KIND, false>(g, maps, epi, st);
 }
 
-int64_t pair_tiles(const Mx4Matrix& A, const Mx4Matrix& B) { return (A.rows + 255) / 256 * ((B.rows + 191) / 192); }
+int64_t pair_tiles(const Mx4Matrix& A, const Mx4Matrix& B, int nt) { return (A.rows + 255) / 256 * ((B.rows + nt - 1) / nt); }
+
+constexpr double kNarrow4 = 0.75;  // see narrow_tiles
+bool narrow4(const Mx4Matrix& A, const Mx4Matrix& B) {
+    return narrow_tiles(pair_tiles(A, B, 192), pair_tiles(A, B, 128), kNarrow4);
+}
 
 template <int KIND, typename T>
 cudaError_t gemm_typed(const Mx4Gemm& g, cudaStream_t st) {
     T* C = static_cast<T*>(g.C);
-    if (split_takes(g.A.rows, pair_tiles(g.A, g.B)))
+    if (split_takes(g.A.rows, pair_tiles(g.A, g.B, 192)))
         return split4<KIND>(g.A, g.B, g.early,
                             EpiSplitScale<KIND, T>{C, g.ldc, g.B.rows, g.A.exponents, g.B.exponents, g.alpha}, st);
     const bool vec = (uintptr_t)C % 32 == 0 && (g.ldc * sizeof(T)) % 32 == 0;
+    if (narrow4(g.A, g.B))
+        return product4<KIND>(
+            g.A, g.B, EpiScale<KIND, T, 128>{C, g.ldc, g.A.rows, g.B.rows, g.A.exponents, g.B.exponents, g.alpha, vec}, st);
     return product4<KIND>(
-        g.A, g.B, EpiScale<KIND, T>{C, g.ldc, g.A.rows, g.B.rows, g.A.exponents, g.B.exponents, g.alpha, vec}, st);
+        g.A, g.B, EpiScale<KIND, T, 192>{C, g.ldc, g.A.rows, g.B.rows, g.A.exponents, g.B.exponents, g.alpha, vec}, st);
 }
 
 template <int KIND>
@@ -257,12 +266,15 @@ template <int KIND>
 cudaError_t gate_kind(const Mx4Gate& g, cudaStream_t st) {
     uint8_t *codes = const_cast<uint8_t*>(g.hq.codes), *scales = const_cast<uint8_t*>(g.hq.scales);
     const int64_t ld = KIND == kKindMx ? g.hq.ldq : g.ldh;
-    if (split_takes(g.x.rows, pair_tiles(g.x, g.W)))
+    if (split_takes(g.x.rows, pair_tiles(g.x, g.W, 192)))
         return split4<KIND>(g.x, g.W, true,  // x was quantised by the launch before, which waited for all before it
                             EpiSplitGate4<KIND>{codes, scales, g.h, ld, g.F, g.x.exponents, g.W.exponents, g.act}, st);
-    const int nt = (int)((g.W.rows + 191) / 192);
-    return product4<KIND>(
-        g.x, g.W, EpiGate4<KIND>{codes, scales, g.h, ld, g.x.rows, g.F, nt, g.x.exponents, g.W.exponents, g.act}, st);
+    const auto nt = [&](int n) { return (int)((g.W.rows + n - 1) / n); };
+    if (narrow4(g.x, g.W))
+        return product4<KIND>(g.x, g.W, EpiGate4<KIND, 128>{codes, scales, g.h, ld, g.x.rows, g.F, nt(128), g.x.exponents,
+                                                            g.W.exponents, g.act}, st);
+    return product4<KIND>(g.x, g.W, EpiGate4<KIND, 192>{codes, scales, g.h, ld, g.x.rows, g.F, nt(192), g.x.exponents,
+                                                        g.W.exponents, g.act}, st);
 }
 
 }  // namespace

@@ -4,21 +4,23 @@
 // accumulators.  Everything is in an unnamed namespace, so each including file
 // has its own count of bounded waits that gave up.
 //
-// D = sum over k of A[m, k] B[n, k].  A pair of CTAs on two SMs owns a tile of
-// 256 m by NT n: each CTA holds 128 rows of A, one half of the rows of B, and
+// D = sum over k of A[m, k] B[n, k], for up to three products of the same kind
+// and depth in one launch.  A pair of CTAs on two SMs owns a tile of 256 m by
+// NT n: each CTA holds 128 rows of A, one half of the rows of B, and
 // 128 rows of the accumulators (f32, in tensor memory, twice: the MMAs of a
 // tile overlap the epilogue of the one before).  A stage of the shared-memory
 // ring is 128 bytes of k.  Warps: 0 copies (TMA), 1 issues the MMAs (even CTA
 // only), the others run the epilogue, four warps (128 rows) for each group of
 // columns.
 //
-// 16-bit operands: NT = 256, 64 k to a stage, either operand with k contiguous
+// 16-bit operands: NT = 256 (128 where that fills the SMs better), 64 k to a stage, either operand with k contiguous
 // or with its row index contiguous (64 x 64 blocks, the same swizzle); the
 // sum may run over two segments (A0 B0^T + A1 B1^T).
-// 4-bit operands: NT = 192, 256 k to a stage; two accumulators of 192 columns
-// leave 128 columns of tensor memory to the scales (16 for A's 128 rows, 32
-// for two tiles of 128 rows of B, twice).  A tile of B starts at a multiple of
-// 64 rows of a scale tile: its scales begin two columns into them.
+// 4-bit operands: NT = 192 (or 128), 256 k to a stage; two accumulators of 192
+// columns leave 128 columns of tensor memory to the scales (16 for A's 128
+// rows, 32 for two tiles of 128 rows of B, twice).  192 rows of B start at a
+// multiple of 64 rows of a scale tile: their scales begin two columns into it
+// for every other tile.
 #pragma once
 
 #include <algorithm>
@@ -36,50 +38,58 @@ __device__ unsigned int g_tile_timeouts = 0;
 
 __device__ __forceinline__ void tile_timeout() { atomicAdd(&g_tile_timeouts, 1u); }
 
+constexpr int kMaxProducts = 3;
+
 struct TileMaps {
-    CUtensorMap a[2], b[2];  // operands of the segments (gated: b[rank] by CTA)
-    CUtensorMap sa, sb;      // scales (4-bit kinds): tiles of 128 words
+    CUtensorMap a[kMaxProducts], b[kMaxProducts];  // by product, by segment, or (gated) b by CTA
+    CUtensorMap sa, sb;                            // scales (4-bit kinds): tiles of 128 words
 };
 
 struct TileArgs {
-    int mt, nt;       // tiles along m and n
-    int pairs;        // CTA pairs in the grid
-    int nk, segs;     // stages of a segment, segments
-    int last_steps;   // MMAs in a segment's last stage
-    int tiles_k;      // 4-bit kinds: scale tiles in a row of 128
+    int mt[kMaxProducts], nt[kMaxProducts];  // tiles along m and n
+    int64_t first[kMaxProducts];             // first tile of each product
+    int64_t tiles;
+    int products;
+    int pairs;       // CTA pairs in the grid
+    int nk, segs;    // stages of a segment, segments (more than one: a single product)
+    int last_steps;  // MMAs in a segment's last stage
+    int tiles_k;     // 4-bit kinds: scale tiles in a row of 128
 };
 
-template <int KIND>
+template <int KIND, int NT_>
 struct TileShape {
     static constexpr bool F4 = kind_is_4bit(KIND);
-    static constexpr int NT = F4 ? 192 : 256;
+    static constexpr int NT = NT_;
     static constexpr int A_BYTES = 128 * 128, B_BYTES = NT / 2 * 128;
     static constexpr int SCALE_TILES = F4 ? (KIND == kKindMx ? 2 : 4) : 0;  // per stage and 128 rows
-    static constexpr int SA_BYTES = SCALE_TILES * 512, SB_BYTES = 2 * SA_BYTES;
+    static constexpr int SB_BLOCKS = NT % 128 == 0 ? NT / 128 : 2;          // 128-row blocks under a tile of B
+    static constexpr int SA_BYTES = SCALE_TILES * 512, SB_BYTES = SB_BLOCKS * SA_BYTES;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
-    static constexpr int STAGES = 6;
+    static constexpr int STAGES = 208 * 1024 / STAGE_BYTES;  // the rest is L1, for the epilogue's loads
     static constexpr int SMEM = STAGES * STAGE_BYTES + 1024;
     static constexpr uint32_t SCALE_COL = 2 * NT, SCALE_COLS = 64;  // two sets
-    static_assert(STAGE_BYTES % 1024 == 0 && SMEM <= 227 * 1024, "shared memory");
+    static_assert(STAGE_BYTES % 1024 == 0 && SMEM + 1024 <= 227 * 1024, "shared memory");
     static_assert(!F4 || SCALE_COL + 2 * SCALE_COLS <= 512, "tensor memory");
 };
 
-__device__ __forceinline__ void tile_of(const TileArgs& g, int64_t t, int& m, int& n) {
-    const int64_t per_group = (int64_t)kTileGroup * g.nt;
+__device__ __forceinline__ void tile_of(const TileArgs& g, int64_t t, int& p, int& m, int& n) {
+    p = g.products > 2 && t >= g.first[2] ? 2 : g.products > 1 && t >= g.first[1] ? 1 : 0;
+    t -= g.first[p];
+    const int64_t per_group = (int64_t)kTileGroup * g.nt[p];
     const int64_t group = t / per_group;
-    const int first = (int)group * kTileGroup, size = min(kTileGroup, g.mt - first);
+    const int first = (int)group * kTileGroup, size = min(kTileGroup, g.mt[p] - first);
     m = first + (int)((t % per_group) % size);
     n = (int)((t % per_group) / size);
 }
 
-// Epi: GROUPS, and run(acc, m row, n tile, group, lane, release): takes this
+// Epi: NT, GROUPS, and run(acc, product, m row, n tile, group, lane, release): takes this
 // warp's 32 rows of the accumulators from column `acc` on (all lanes, also for
 // rows beyond the matrix) and calls release() after its last read of them.
 template <int KIND, bool A_MN, bool B_MN, bool GATED, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROUPS, 1)
     tile_gemm_kernel(const __grid_constant__ TileArgs g, const __grid_constant__ TileMaps maps,
                      const __grid_constant__ Epi epi) {
-    using S = TileShape<KIND>;
+    using S = TileShape<KIND, Epi::NT>;
     constexpr int STAGES = S::STAGES, NT = S::NT;
     constexpr bool F4 = S::F4;
     extern __shared__ uint8_t smem_raw[];
@@ -91,7 +101,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int64_t pair = blockIdx.x >> 1;
-    const int64_t tiles = (int64_t)g.mt * g.nt;
+    const int64_t tiles = g.tiles;
     const int per_tile = g.nk * g.segs;
 
     const uint32_t full0 = smem_addr(&bars[0]), empty0 = smem_addr(&bars[STAGES]);
@@ -128,8 +138,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
         int64_t issued = 0;
         bool ok = true;
         for (int64_t t = pair; t < tiles && ok; t += g.pairs) {
-            int mt, nt;
-            tile_of(g, t, mt, nt);
+            int p, mt, nt;
+            tile_of(g, t, p, mt, nt);
             const int a_row = (mt * 2 + (int)rank) * 128;
             const int b_row = GATED ? nt * (NT / 2) : nt * NT + (int)rank * (NT / 2);
             int seg = 0, kb = 0;
@@ -138,8 +148,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
                 if (!ok) break;
                 if (elect_one()) {
                     const uint32_t dst = ring + stage * S::STAGE_BYTES, bar = full_lead0 + 8 * stage;
-                    const CUtensorMap* ma = &maps.a[seg];
-                    const CUtensorMap* mb = &maps.b[GATED ? rank : seg];
+                    const CUtensorMap* ma = &maps.a[p + seg];
+                    const CUtensorMap* mb = &maps.b[GATED ? rank : p + seg];
                     if (leader) mbar_expect_tx(full0 + 8 * stage, 2u * S::STAGE_BYTES);
                     constexpr int ROW = F4 ? 128 : 64;  // elements (bytes of codes) of a 128-byte row
                     if (!A_MN) {
@@ -152,15 +162,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
                     if (!B_MN) {
                         tma_load_2d_group(db, mb, kb * ROW, b_row, bar);
                     } else {
-                        tma_load_2d_group(db, mb, b_row, kb * 64, bar);
-                        tma_load_2d_group(db + 8192, mb, b_row + 64, kb * 64, bar);
+                        static_assert(!B_MN || NT % 128 == 0, "whole blocks of 64");
+#pragma unroll
+                        for (int i = 0; i < NT / 128; ++i)
+                            tma_load_2d_group(db + i * 8192, mb, b_row + i * 64, kb * 64, bar);
                     }
                     if (F4) {
                         const uint32_t ds = db + S::B_BYTES;
                         const int t0 = kb * S::SCALE_TILES, rb = nt * NT / 128;
                         tma_load_2d_group(ds, &maps.sa, 0, (mt * 2 + (int)rank) * g.tiles_k + t0, bar);
                         tma_load_2d_group(ds + S::SA_BYTES, &maps.sb, 0, rb * g.tiles_k + t0, bar);
-                        tma_load_2d_group(ds + 2 * S::SA_BYTES, &maps.sb, 0, (rb + 1) * g.tiles_k + t0, bar);
+                        if (S::SB_BLOCKS == 2)
+                            tma_load_2d_group(ds + 2 * S::SA_BYTES, &maps.sb, 0, (rb + 1) * g.tiles_k + t0, bar);
                     }
                 }
                 __syncwarp();
@@ -193,8 +206,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
             const uint64_t sd0 = tc5::desc_scale_tile(ring + S::A_BYTES + S::B_BYTES);
             uint32_t stage = 0, phase = 0, count = 0;
             for (int64_t t = pair; t < tiles && ok; t += g.pairs, ++count) {
-                int mt, nt;
-                tile_of(g, t, mt, nt);
+                int p, mt, nt;
+                tile_of(g, t, p, mt, nt);
                 const uint32_t buf = count & 1;
                 const uint32_t d = tmem + buf * NT;
                 ok = warp_wait(acce0 + 8 * buf, ((count >> 1) & 1) ^ 1, kTileWaitNs);
@@ -212,13 +225,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
                         if constexpr (F4) {
                             const uint32_t sc = tmem + S::SCALE_COL + (it & 1) * S::SCALE_COLS;
                             const uint64_t sd = sd0 + off;
+                            constexpr int SB = 4 * S::SB_BLOCKS;  // columns of B's scales for 4 blocks of k
 #pragma unroll
                             for (int i = 0; i < S::SCALE_TILES; ++i) {
                                 tc5::cp_scales_pair(sc + i * 4, sd + i * 32);
-                                tc5::cp_scales_pair(sc + 16 + i * 8, sd + (S::SCALE_TILES + i) * 32);
-                                tc5::cp_scales_pair(sc + 16 + i * 8 + 4, sd + (2 * S::SCALE_TILES + i) * 32);
+                                tc5::cp_scales_pair(sc + 16 + i * SB, sd + (S::SCALE_TILES + i) * 32);
+                                if (S::SB_BLOCKS == 2)
+                                    tc5::cp_scales_pair(sc + 16 + i * SB + 4, sd + (2 * S::SCALE_TILES + i) * 32);
                             }
-                            const uint32_t sbo = (uint32_t)(nt & 1) * 2;  // 192 nt is 64 rows into a tile for odd nt
+                            const uint32_t sbo = NT == 192 ? (uint32_t)(nt & 1) * 2 : 0u;
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 if (j >= steps) break;
@@ -226,10 +241,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
                                 if (KIND == kKindMx)
                                     tc5::mma_mx_pair(d, ad + A_STEP * j, bd + B_STEP * j,
                                                      tc5::idesc_scale_byte(IDESC, (j & 1) * 2), sc + (j / 2) * 4,
-                                                     sc + 16 + (j / 2) * 8 + sbo, acc);
+                                                     sc + 16 + (j / 2) * SB + sbo, acc);
                                 else
                                     tc5::mma_nv_pair(d, ad + A_STEP * j, bd + B_STEP * j, IDESC, sc + j * 4,
-                                                     sc + 16 + j * 8 + sbo, acc);
+                                                     sc + 16 + j * SB + sbo, acc);
                             }
                         } else {
 #pragma unroll
@@ -260,8 +275,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
         const int q = warp & 3, group = (warp - 2) >> 2;
         uint32_t count = 0;
         for (int64_t t = pair; t < tiles; t += g.pairs, ++count) {
-            int mt, nt;
-            tile_of(g, t, mt, nt);
+            int p, mt, nt;
+            tile_of(g, t, p, mt, nt);
             const uint32_t buf = count & 1;
             if (!warp_wait(accf0 + 8 * buf, (count >> 1) & 1, kTileWaitNs)) {
                 if (lane == 0) tile_timeout();
@@ -269,7 +284,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
             }
             tc5::fence_after_sync();
             const int64_t row = ((int64_t)mt * 2 + rank) * 128 + q * 32 + lane;
-            epi.run(tmem + buf * NT + ((uint32_t)(q * 32) << 16), row, nt, group, lane, [&]() {
+            epi.run(tmem + buf * NT + ((uint32_t)(q * 32) << 16), p, row, nt, group, lane, [&]() {
                 tc5::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
@@ -301,7 +316,7 @@ int tile_sms() {
 // Launch on as many CTA pairs as can be resident (never more than tiles).
 template <int KIND, bool A_MN, bool B_MN, bool GATED, class Epi>
 cudaError_t launch_tile_gemm(TileArgs g, const TileMaps& maps, const Epi& epi, cudaStream_t st) {
-    using S = TileShape<KIND>;
+    using S = TileShape<KIND, Epi::NT>;
     static std::atomic<int> cached[64];  // resident pairs per device; 0 = not asked yet
     auto* kernel = tile_gemm_kernel<KIND, A_MN, B_MN, GATED, Epi>;
     int dev = 0;
@@ -333,9 +348,13 @@ cudaError_t launch_tile_gemm(TileArgs g, const TileMaps& maps, const Epi& epi, c
             cached[dev].store(pairs, std::memory_order_relaxed);
         }
     }
-    const int64_t tiles = (int64_t)g.mt * g.nt;
-    if (tiles <= 0) return cudaSuccess;
-    g.pairs = (int)std::min<int64_t>(pairs, tiles);
+    g.tiles = 0;
+    for (int p = 0; p < g.products; ++p) {
+        g.first[p] = g.tiles;
+        g.tiles += (int64_t)g.mt[p] * g.nt[p];
+    }
+    if (g.tiles <= 0) return cudaSuccess;
+    g.pairs = (int)std::min<int64_t>(pairs, g.tiles);
     cfg.numAttrs = 2;
     cfg.gridDim = dim3((unsigned)(2 * g.pairs));
     return cudaLaunchKernelEx(&cfg, kernel, g, maps, epi);
@@ -348,6 +367,15 @@ cudaError_t reset_tile_timeouts(unsigned int* count) {
     if (err != cudaSuccess) return err;
     const unsigned int zero = 0;
     return cudaMemcpyToSymbol(g_tile_timeouts, &zero, sizeof(unsigned int));
+}
+
+// Tiles of 128 columns instead of `wide` (256 or 192) where the pairs' rounds
+// over the narrow ones are shorter: a narrow tile takes about NARROWCOST of a wide
+// one's time, more than its share (its rows of A are read for fewer columns).
+inline bool narrow_tiles(int64_t wide_tiles, int64_t narrow_count, double narrow_cost) {
+    const int64_t pairs = std::max(1, tile_sms() / 2);
+    const int64_t wide_rounds = (wide_tiles + pairs - 1) / pairs, rounds = (narrow_count + pairs - 1) / pairs;
+    return (double)rounds * narrow_cost < (double)wide_rounds;
 }
 
 // ---- pieces of epilogues ----
