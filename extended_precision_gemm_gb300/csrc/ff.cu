@@ -16,14 +16,13 @@ namespace ddg {
 namespace {
 
 // C = accumulators, rounded once; of one product, or of each of three.
-template <typename T, int NT_, int P>
+template <typename T, int NT_, int P, bool ALIGNED>
 struct EpiStore {
     static constexpr int NT = NT_, GROUPS = 2;
     T* C[P];
     int64_t ldc[P], M[P], N[P];
-    bool vec[P];
     template <class Release>
-    __device__ __forceinline__ void run(uint32_t acc, int p, int64_t row, int nt, int group, int, Release release) const {
+    __device__ __forceinline__ void run(uint32_t acc, int p, int64_t row, int nt, int group, int lane, Release release) const {
         if (P == 1) p = 0;
         constexpr int STEPS = NT / GROUPS / 32;
 #pragma unroll 1
@@ -35,7 +34,7 @@ struct EpiStore {
             float f[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-            if (row < M[p]) store32(C[p] + row * ldc[p], (int64_t)nt * NT + c, N[p], vec[p], f);
+            store_block<ALIGNED>(C[p], ldc[p], row - lane, M[p], (int64_t)nt * NT + c, N[p], f, lane);
         }
     }
 };
@@ -72,10 +71,10 @@ struct EpiGate {
                     bv[i] = __uint_as_float(u[i]) * da;
                 }
             });
-            store32(h + row * ld, col, N, true, hv);
+            store_row(h + row * ld + col, hv);
             if (SAVE) {
-                store32(a + row * ld, col, N, true, av);
-                store32(b + row * ld, col, N, true, bv);
+                store_row(a + row * ld + col, av);
+                store_row(b + row * ld + col, bv);
             }
         }
     }
@@ -154,15 +153,27 @@ struct EpiSplitGate {
     }
 };
 
-// Rows of `cols` 16-bit elements to a 16-byte aligned leading dimension.
+// Rows of `cols` 16-bit elements to 128-byte aligned rows: a warp takes 256
+// elements of a row, 8 loads of one element a lane in flight (the source may be
+// aligned to its elements only), and stores 4 bytes a lane.
 __global__ void __launch_bounds__(256) realign_kernel(const uint16_t* src, int64_t ld, int64_t rows, int64_t cols,
                                                       uint16_t* dst, int64_t ldd) {
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t n = rows * cols;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / cols, c = i - r * cols;
-        dst[r * ldd + c] = src[r * ld + c];
+    const int lane = threadIdx.x & 31;
+    const int64_t parts = (cols + 255) / 256;
+    for (int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); item < rows * parts; item += (int64_t)gridDim.x * 8) {
+        const int64_t r = item / parts, c0 = item % parts * 256 + lane * 2;
+        const uint16_t* p = src + r * ld;
+        uint16_t v[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) v[i][j] = c0 + i * 64 + j < cols ? p[c0 + i * 64 + j] : (uint16_t)0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // ldd is cols rounded up to 64: a pair begun inside a row lies in it
+            if (c0 + i * 64 < cols)
+                *reinterpret_cast<uint32_t*>(dst + r * ldd + c0 + i * 64) = (uint32_t)v[i][0] | (uint32_t)v[i][1] << 16;
     }
 }
 
@@ -226,27 +237,29 @@ cudaError_t split16(const Matrix16& x, const Matrix16& W0, const Matrix16& W1, b
     return launch_split_gemm<KIND, PAIRED>(g, maps, epi, st);
 }
 
-template <typename T, int NT, int P>
-void set_store(EpiStore<T, NT, P>& epi, int p, void* C, int64_t ldc, int64_t M, int64_t N) {
-    epi.C[p] = static_cast<T*>(C);
+template <class Epi>
+void set_store(Epi& epi, int p, void* C, int64_t ldc, int64_t M, int64_t N) {
+    epi.C[p] = static_cast<decltype(epi.C[p] + 0)>(C);
     epi.ldc[p] = ldc;
     epi.M[p] = M;
     epi.N[p] = N;
-    epi.vec[p] = (uintptr_t)C % 32 == 0 && (ldc * sizeof(T)) % 32 == 0;
 }
 
 // C = sum over segments, with wide or narrow tiles.
+template <int KIND, typename T, bool B_MN, int NT, bool ALIGNED>
+cudaError_t store16_sized(int64_t M, int64_t N, int64_t K, int segs, const Matrix16& A0, const Matrix16& A1,
+                          const Matrix16& B0, const Matrix16& B1, void* C, int64_t ldc, cudaStream_t st) {
+    EpiStore<T, NT, 1, ALIGNED> epi;
+    set_store(epi, 0, C, ldc, M, N);
+    return product16<KIND, false, B_MN, false>(M, N, K, segs, A0, A1, B0, B1, epi, st);
+}
 template <int KIND, typename T, bool B_MN>
 cudaError_t store16(int64_t M, int64_t N, int64_t K, int segs, const Matrix16& A0, const Matrix16& A1,
                     const Matrix16& B0, const Matrix16& B1, void* C, int64_t ldc, cudaStream_t st) {
-    if (narrow16(M, N, 256)) {
-        EpiStore<T, 128, 1> epi;
-        set_store(epi, 0, C, ldc, M, N);
-        return product16<KIND, false, B_MN, false>(M, N, K, segs, A0, A1, B0, B1, epi, st);
-    }
-    EpiStore<T, 256, 1> epi;
-    set_store(epi, 0, C, ldc, M, N);
-    return product16<KIND, false, B_MN, false>(M, N, K, segs, A0, A1, B0, B1, epi, st);
+    const bool narrow = narrow16(M, N, 256), aligned = aligned_rows<T>(C, ldc);
+    auto f = narrow ? (aligned ? store16_sized<KIND, T, B_MN, 128, true> : store16_sized<KIND, T, B_MN, 128, false>)
+                    : (aligned ? store16_sized<KIND, T, B_MN, 256, true> : store16_sized<KIND, T, B_MN, 256, false>);
+    return f(M, N, K, segs, A0, A1, B0, B1, C, ldc, st);
 }
 
 template <int KIND, typename T, int NT, bool SAVE>
@@ -260,7 +273,7 @@ template <int KIND, typename T>
 cudaError_t forward_typed(const FfForward& f, cudaStream_t st) {
     const Matrix16 h{f.h, f.T, f.F, f.ld};
     cudaError_t err;
-    if (split_takes(f.T, pair_tiles(f.T, f.F, 128))) {
+    if (f.T <= kSplitTokens16) {
         err = split16<KIND, true>(f.x, f.wg, f.wu, false,
                                   EpiSplitGate<T>{static_cast<T*>(f.h), f.a, f.b, f.ld, f.F, f.act}, st);
     } else {
@@ -270,7 +283,7 @@ cudaError_t forward_typed(const FfForward& f, cudaStream_t st) {
     }
     if (err != cudaSuccess) return err;
     // Wd was complete before the launch above could end its own wait
-    if (split_takes(f.T, pair_tiles(f.T, f.D, 256)))
+    if (f.T <= kSplitTokens16)
         return split16<KIND, false>(h, f.wd, f.wd, true, EpiSplitStore<T>{static_cast<T*>(f.y), f.ldy, f.D}, st);
     return store16<KIND, T, false>(f.T, f.D, f.F, 1, h, h, f.wd, f.wd, f.y, f.ldy, st);
 }
@@ -284,11 +297,11 @@ cudaError_t gate_backward16(const FfBackward& f, cudaStream_t st) {
 
 // The weights' gradients that are wanted, in one launch: sums over the T rows
 // of both operands.
-template <int KIND, typename T, int NT>
+template <int KIND, typename T, int NT, bool ALIGNED>
 cudaError_t weights16(const FfBackward& f, const Matrix16& h, const Matrix16& dg, const Matrix16& du, cudaStream_t st) {
     TileMaps maps;
     memset(&maps, 0, sizeof(maps));
-    EpiStore<T, NT, kMaxProducts> epi = {};
+    EpiStore<T, NT, kMaxProducts, ALIGNED> epi = {};
     TileArgs g = tile_args(f.F, f.D, NT, f.T, 1);
     g.products = 0;
     cudaError_t err = cudaSuccess;
@@ -321,16 +334,20 @@ cudaError_t backward_typed(const FfBackward& f, cudaStream_t st) {
     if (err != cudaSuccess) return err;
     const int64_t wide = 2 * pair_tiles(f.F, f.D, 256) + pair_tiles(f.D, f.F, 256);
     const int64_t narrow = 2 * pair_tiles(f.F, f.D, 128) + pair_tiles(f.D, f.F, 128);
-    return narrow_tiles(wide, narrow, kNarrow16) ? weights16<KIND, T, 128>(f, h, dg, du, st)
-                                                 : weights16<KIND, T, 256>(f, h, dg, du, st);
+    const bool aligned = (f.dwg == nullptr || aligned_rows<T>(f.dwg, f.lddwg)) &&
+                         (f.dwu == nullptr || aligned_rows<T>(f.dwu, f.lddwu)) &&
+                         (f.dwd == nullptr || aligned_rows<T>(f.dwd, f.lddwd));
+    return narrow_tiles(wide, narrow, kNarrow16)
+               ? (aligned ? weights16<KIND, T, 128, true>(f, h, dg, du, st) : weights16<KIND, T, 128, false>(f, h, dg, du, st))
+               : (aligned ? weights16<KIND, T, 256, true>(f, h, dg, du, st) : weights16<KIND, T, 256, false>(f, h, dg, du, st));
 }
 
 }  // namespace
 
 cudaError_t launch_realign(const Matrix16& src, const Matrix16& dst, cudaStream_t st) {
-    const int64_t n = src.rows * src.cols;
-    if (n == 0) return cudaSuccess;
-    const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 152 * 8);
+    const int64_t items = src.rows * ((src.cols + 255) / 256);
+    if (items == 0) return cudaSuccess;
+    const unsigned blocks = (unsigned)std::min<int64_t>((items + 7) / 8, 1 << 20);
     return launch_pdl(realign_kernel, dim3(blocks), dim3(256), 0, st, static_cast<const uint16_t*>(src.p), src.ld,
                       src.rows, src.cols, static_cast<uint16_t*>(dst.p), dst.ld);
 }

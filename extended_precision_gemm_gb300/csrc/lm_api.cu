@@ -94,18 +94,23 @@ private:
 };
 
 // A 16-bit operand as the tensor copies need it (16-byte aligned rows): itself,
-// or a copy in the workspace.
+// or a copy in the workspace with whole 128-byte rows.  Rows that are not a
+// multiple of 128 bytes apart also make every copied row touch a line more
+// (1009 tokens, 2056 -> 5400 -> 2056: 82 us, with 2048 53 us); with many tokens
+// a copy costs less than that.
+constexpr int64_t kRealignTokens = 2048;
 struct Aligned16 {
     Matrix16 m;
     bool copy;
     int64_t offset;
-    Aligned16(const void* p, int64_t rows, int64_t cols, int64_t ld, Workspace& ws)
+    Aligned16(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t tokens, Workspace& ws)
         : m{const_cast<void*>(p), rows, cols, ld},
-          copy(rows > 0 && cols > 0 && !(aligned16(p) && (rows == 1 || ld % 8 == 0))),
-          offset(copy ? ws.reserve(rows * round_up(cols, 8) * 2) : 0) {}
+          copy(rows > 0 && cols > 0 && 
+               (!aligned16(p) || (rows > 1 && (ld % 8 != 0 || (tokens > kRealignTokens && ld % 64 != 0))))),
+          offset(copy ? ws.reserve(rows * round_up(cols, 64) * 2) : 0) {}
     cudaError_t resolve(const Workspace& ws, cudaStream_t st) {
         if (!copy) return cudaSuccess;
-        const Matrix16 to{ws.at<void>(offset), m.rows, m.cols, round_up(m.cols, 8)};
+        const Matrix16 to{ws.at<void>(offset), m.rows, m.cols, round_up(m.cols, 64)};
         cudaError_t err = launch_realign(m, to, st);
         m = to;
         return err;
@@ -246,7 +251,7 @@ ddgemm_status dd_ff_gated(int type, int activation, int64_t T, int64_t D, int64_
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (F == 0) return status_of(zero16(y, T, D, ldy, 2, st));
     Workspace ws(st);
-    Aligned16 ax(x, T, D, ldx, ws), ag(Wg, F, D, ldwg, ws), au(Wu, F, D, ldwu, ws), ad(Wd, D, F, ldwd, ws);
+    Aligned16 ax(x, T, D, ldx, T, ws), ag(Wg, F, D, ldwg, T, ws), au(Wu, F, D, ldwu, T, ws), ad(Wd, D, F, ldwd, T, ws);
     const int64_t h = saved ? 0 : ws.reserve(T * L.ld * 2);
     if (!ws.allocate()) return DDGEMM_ERR_ALLOC;
     cudaError_t err = ax.resolve(ws, st);
@@ -295,8 +300,8 @@ ddgemm_status dd_ff_gated_backward(int type, int64_t T, int64_t D, int64_t F, co
         return status_of(err);
     }
     Workspace ws(st);
-    Aligned16 ay(dy, T, D, lddy, ws), ax(x, T, D, ldx, ws), ag(Wg, F, D, ldwg, ws), au(Wu, F, D, ldwu, ws),
-        ad(Wd, D, F, ldwd, ws);
+    Aligned16 ay(dy, T, D, lddy, T, ws), ax(x, T, D, ldx, T, ws), ag(Wg, F, D, ldwg, T, ws), au(Wu, F, D, ldwu, T, ws),
+        ad(Wd, D, F, ldwd, T, ws);
     const int64_t og = ws.reserve(T * L.ld * 2), ou = ws.reserve(T * L.ld * 2);
     if (!ws.allocate()) return DDGEMM_ERR_ALLOC;
     cudaError_t err = ay.resolve(ws, st);
@@ -338,7 +343,7 @@ ddgemm_status dd_mx4_ff_gated(int format, int type, int activation, int64_t T, i
     if (F == 0) return status_of(zero16(y, T, D, ldy, es, st));
     const bool nv = format == DDGEMM_NVFP4;
     Workspace ws(st);
-    const int64_t xl = mx4_code_bytes(D), hl = mx4_code_bytes(F), ldh = round_up(F, 64);
+    const int64_t xl = round_up(mx4_code_bytes(D), 128), hl = round_up(mx4_code_bytes(F), 128), ldh = round_up(F, 64);
     const int64_t xc = ws.reserve(T * xl), xs = ws.reserve(mx4_scale_bytes(format, T, D)), xe = ws.reserve(T * 4);
     const int64_t hc = ws.reserve(T * hl), hs = ws.reserve(mx4_scale_bytes(format, T, F)), he = ws.reserve(T * 4);
     const int64_t hf = nv ? ws.reserve(T * ldh * 4) : 0;

@@ -14,15 +14,28 @@ __device__ __forceinline__ int column_exponent(const int32_t* f, int64_t c, int6
     return f != nullptr && c + lane < N ? f[c + lane] : 0;
 }
 
+// 32 values of a row times 2^(er + f_j), lane j holding f_j.  Exponents of
+// ordinary size take two multiplications by powers of two; the rest go by their
+// sum, lest a partial product leave the range (or its normal part) alone.
+__device__ __forceinline__ void scale_columns(float (&v)[32], int er, int fc) {
+    if (__all_sync(~0u, abs(er) <= 40 && abs(fc) <= 40)) {
+        const float row = exp2_int(er), column = exp2_int(fc);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= row * __shfl_sync(~0u, column, i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = scale_by_exp2(v[i], er + __shfl_sync(~0u, fc, i));
+    }
+}
+
 // C = alpha * accumulators * 2^(e_i + f_j), rounded once.
-template <int KIND, typename T, int NT_>
+template <int KIND, typename T, int NT_, bool ALIGNED>
 struct EpiScale {
     static constexpr int NT = NT_, GROUPS = NT / 64;
     T* C;
     int64_t ldc, M, N;
     const int32_t *e, *f;
     float alpha;
-    bool vec;
     template <class Release>
     __device__ __forceinline__ void run(uint32_t acc, int, int64_t row, int nt, int group, int lane, Release release) const {
         const int er = KIND == kKindNv && row < M ? e[row] : 0;
@@ -38,11 +51,9 @@ struct EpiScale {
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(v[i]) * alpha;
             if (KIND == kKindNv) {
-                const int fc = column_exponent(f, col, N, lane);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = scale_by_exp2(o[i], er + __shfl_sync(~0u, fc, i));
+                scale_columns(o, er, column_exponent(f, col, N, lane));
             }
-            if (row < M) store32(C + row * ldc, col, N, vec, o);
+            store_block<ALIGNED>(C, ldc, row - lane, M, col, N, o, lane);
         }
     }
 };
@@ -63,21 +74,22 @@ struct EpiGate4 {
     int act;
     template <class Release>
     __device__ __forceinline__ void run(uint32_t acc, int, int64_t row, int n, int group, int lane, Release release) const {
-        uint32_t g[32], u[32];
-        tc5::ld32(acc + group * 64, g);
-        tc5::ld32(acc + group * 64 + 32, u);
+        uint32_t raw[32];
+        float g[32], u[32];
+        tc5::ld32(acc + group * 64, raw);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) g[i] = __uint_as_float(raw[i]);
+        tc5::ld32(acc + group * 64 + 32, raw);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) u[i] = __uint_as_float(raw[i]);
         release();
         const int64_t c = (int64_t)n * (NT / 2) + group * 32;
         float hv[32];
         if (KIND == kKindNv) {
             const int64_t wc = (int64_t)n * NT + group * 64, W = round_up(F, 32) * 2;
             const int er = row < M ? e[row] : 0;
-            const int fg = column_exponent(f, wc, W, lane), fu = column_exponent(f, wc + 32, W, lane);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                g[i] = __float_as_uint(scale_by_exp2(__uint_as_float(g[i]), er + __shfl_sync(~0u, fg, i)));
-                u[i] = __float_as_uint(scale_by_exp2(__uint_as_float(u[i]), er + __shfl_sync(~0u, fu, i)));
-            }
+            scale_columns(g, er, column_exponent(f, wc, W, lane));
+            scale_columns(u, er, column_exponent(f, wc + 32, W, lane));
         }
         if (row >= M) return;
         if (c < F) {
@@ -85,13 +97,13 @@ struct EpiGate4 {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     float a, da;
-                    activation<decltype(tag)::value, false>(__uint_as_float(g[i]), a, da);
-                    hv[i] = a * __uint_as_float(u[i]);
+                    activation<decltype(tag)::value, false>(g[i], a, da);
+                    hv[i] = a * u[i];
                 }
             });
         }
         if (KIND == kKindNv) {
-            if (c < F) store32(h + row * ld, c, F, true, hv);
+            if (c < F) store_row(h + row * ld + c, hv);  // ld: F rounded up to 64
             return;
         }
         const int64_t tiles = mx4_scale_tiles(kMxfp4, F);
@@ -231,18 +243,24 @@ bool narrow4(const Mx4Matrix& A, const Mx4Matrix& B) {
     return narrow_tiles(pair_tiles(A, B, 192), pair_tiles(A, B, 128), kNarrow4);
 }
 
+template <int KIND, typename T, int NT, bool ALIGNED>
+cudaError_t gemm_sized(const Mx4Gemm& g, cudaStream_t st) {
+    return product4<KIND>(g.A, g.B,
+                          EpiScale<KIND, T, NT, ALIGNED>{static_cast<T*>(g.C), g.ldc, g.A.rows, g.B.rows, g.A.exponents,
+                                                         g.B.exponents, g.alpha},
+                          st);
+}
+
 template <int KIND, typename T>
 cudaError_t gemm_typed(const Mx4Gemm& g, cudaStream_t st) {
     T* C = static_cast<T*>(g.C);
-    if (split_takes(g.A.rows, pair_tiles(g.A, g.B, 192)))
+    if (g.A.rows <= kSplitTokens4)
         return split4<KIND>(g.A, g.B, g.early,
                             EpiSplitScale<KIND, T>{C, g.ldc, g.B.rows, g.A.exponents, g.B.exponents, g.alpha}, st);
-    const bool vec = (uintptr_t)C % 32 == 0 && (g.ldc * sizeof(T)) % 32 == 0;
-    if (narrow4(g.A, g.B))
-        return product4<KIND>(
-            g.A, g.B, EpiScale<KIND, T, 128>{C, g.ldc, g.A.rows, g.B.rows, g.A.exponents, g.B.exponents, g.alpha, vec}, st);
-    return product4<KIND>(
-        g.A, g.B, EpiScale<KIND, T, 192>{C, g.ldc, g.A.rows, g.B.rows, g.A.exponents, g.B.exponents, g.alpha, vec}, st);
+    const bool narrow = narrow4(g.A, g.B), aligned = aligned_rows<T>(C, g.ldc);
+    auto f = narrow ? (aligned ? gemm_sized<KIND, T, 128, true> : gemm_sized<KIND, T, 128, false>)
+                    : (aligned ? gemm_sized<KIND, T, 192, true> : gemm_sized<KIND, T, 192, false>);
+    return f(g, st);
 }
 
 template <int KIND>
@@ -266,7 +284,7 @@ template <int KIND>
 cudaError_t gate_kind(const Mx4Gate& g, cudaStream_t st) {
     uint8_t *codes = const_cast<uint8_t*>(g.hq.codes), *scales = const_cast<uint8_t*>(g.hq.scales);
     const int64_t ld = KIND == kKindMx ? g.hq.ldq : g.ldh;
-    if (split_takes(g.x.rows, pair_tiles(g.x, g.W, 192)))
+    if (g.x.rows <= kSplitTokens4)
         return split4<KIND>(g.x, g.W, true,  // x was quantised by the launch before, which waited for all before it
                             EpiSplitGate4<KIND>{codes, scales, g.h, ld, g.F, g.x.exponents, g.W.exponents, g.act}, st);
     const auto nt = [&](int n) { return (int)((g.W.rows + n - 1) / n); };

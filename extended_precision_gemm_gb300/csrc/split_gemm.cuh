@@ -5,14 +5,16 @@
 // One CTA multiplies 128 rows of the weights (the M side of the MMA, so that
 // no tensor-core row is idle however few tokens there are) with NQ tokens over
 // its share of k; a cluster of CTAs shares one such tile, each with its own
-// part of k.  The partial sums meet in shared memory: every CTA leaves its
-// tile there, and after a cluster barrier each adds its part of the outputs
-// over the CTAs in order (no atomics: results do not depend on timing).
-// Warps: 0 copies, 1 issues MMAs, 2-5 read the accumulators; all take part in
-// the final sums.  Two CTAs fit an SM.
+// part of k.  The partial sums meet in shared memory: every output has an
+// owner among the CTAs, all CTAs write their sums of it into the owner's memory
+// (remote stores, nobody waits for a remote load), and after a cluster barrier
+// the owner adds them in the CTAs' order (no atomics: results do not depend on
+// timing).  Warps: 0 copies, 1 issues MMAs, 2-9 read the accumulators (four for
+// every other 16 tokens); all take part in the final sums.  Two CTAs fit an SM.
 //
-// With EARLY weights (nothing that the launch before this one writes), the
-// ring is filled with them before the wait for that launch.
+// The wait for the launch before this one: the next stages of a CTA's weights
+// are fetched into L2 ahead of it (kAhead of them: all would not stay there), and if the weights are EARLY (nothing that the
+// launch before this one writes), the ring is filled with them ahead of it.
 #pragma once
 
 #include "mx4.cuh"
@@ -21,9 +23,10 @@
 namespace ddg {
 namespace {
 
-constexpr int kSplitThreads = 192;
+constexpr int kSplitThreads = 320;
 constexpr int kSplitSmem = 108 * 1024;  // of the ring: two CTAs on an SM
 constexpr int kMaxCluster = 8;
+constexpr int kAhead = 6;
 
 template <int KIND, int NQ>
 struct SplitShape {
@@ -37,7 +40,7 @@ struct SplitShape {
     static constexpr uint32_t ACC_COLS = NQ < 32 ? 32 : NQ;
     static constexpr uint32_t TMEM_COLS = !F4 ? ACC_COLS : NQ <= 64 ? 128 : 256;
     static_assert(STAGE_BYTES % 1024 == 0 && STAGES >= 2, "ring");
-    static_assert(128 * NQ * 4 <= STAGES * STAGE_BYTES, "partial sums fit the ring");
+    static_assert(128 * NQ * 4 + kMaxCluster * kMaxCluster * 256 <= STAGES * STAGE_BYTES, "partial sums fit the ring");
 };
 
 struct SplitMaps {
@@ -54,9 +57,12 @@ struct SplitArgs {
     int64_t M;         // tokens
 };
 
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ float ld_shared(uint32_t addr) {
     float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
 }
 
@@ -102,6 +108,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
             }
             mbar_init(done_bar, 1);
             fence_barrier_init();
+            for (int i = ahead; i < min(count, ahead + kAhead); ++i) {
+                const int kb = k0 + i;
+                tma_prefetch_2d(&maps.p[0], kb * ROW, nt * (PAIRED16 ? 64 : 128));
+                if (PAIRED16) tma_prefetch_2d(&maps.p[1], kb * ROW, nt * 64);
+            }
             for (int i = 0; i < ahead; ++i) {
                 mbar_expect_tx(full0 + 8 * i, S::STAGE_BYTES);
                 load_weights(i, ring + i * S::STAGE_BYTES, full0 + 8 * i);
@@ -204,17 +215,23 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
     }
     __syncwarp();
 
-    // partial sums to shared memory (the ring is no longer read or written
-    // once every MMA has finished): token m at m * 128, weight rows contiguous
+    // Units of outputs: 32 weight rows of one token, or (UNITS = 2) 32 rows of g
+    // and the 32 of u that go with them.  Unit w belongs to CTA w % splits, at
+    // slot w / splits of its memory; a slot holds a row of 32 for each CTA.
+    // Once every MMA of the cluster has finished, the rings hold nothing more.
+    constexpr int PARTS = Epi::UNITS, PER_TOKEN = 4 / PARTS;
     const int tokens = (int)min((int64_t)NQ, g.M - (int64_t)mt * NQ);
+    const int units = tokens * PER_TOKEN, splits = g.splits;
     if (!warp_wait(done_bar, 0, 2 * kTileWaitNs) && lane == 0) tile_timeout();
     tc5::fence_after_sync();
+    cluster_sync();
     if (warp >= 2) {
-        const int q = warp & 3;
-        const uint32_t base = ring + (uint32_t)(q * 32 + lane) * 4;
-#pragma unroll
-        for (int c = 0; c < NQ; c += 16) {
-            if (c >= tokens) break;
+        const int q = warp & 3;  // 32 rows of the tile: of which unit, and which of its parts
+        const int unit = PARTS == 1 ? q : PAIRED16 ? q % 2 : q / 2, part = PARTS == 1 ? 0 : PAIRED16 ? q / 2 : q % 2;
+        const uint32_t mine = ring + (uint32_t)(z * PARTS + part) * 128 + lane * 4, pitch = (uint32_t)(splits * PARTS) * 128;
+        const uint32_t inverse = 65536u / (uint32_t)splits + 1u;  // w / splits = w * inverse >> 16 for w < 4096
+#pragma unroll 1
+        for (int c = (warp - 2) / 4 * 16; c < tokens; c += 32) {
             uint32_t v[16];
             asm volatile(
                 "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -225,9 +242,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
                 : "r"(tmem + ((uint32_t)(q * 32) << 16) + c)
                 : "memory");
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (c + i < tokens)
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + (uint32_t)(c + i) * 512), "r"(v[i]) : "memory");
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t w = (uint32_t)((c + i) * PER_TOKEN + unit), slot = w * inverse >> 16;
+                if (c + i < tokens) st_cluster(cluster_addr(mine + slot * pitch, w - slot * splits), v[i]);
+            }
         }
     }
     tc5::fence_before_sync();
@@ -235,36 +253,25 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
     tc5::fence_after_sync();
     if (warp == 1) tc5::tmem_dealloc(tmem, S::TMEM_COLS);
 
-    // this CTA's share of the outputs, added over the CTAs in their order
     pdl_wait();  // the other warps' first access to global memory
-    constexpr int PER_TOKEN = Epi::UNITS == 2 ? 2 : 4;
-    // (in batches of units, so that the loads of several are in flight)
-    constexpr int BATCH = 4;
-    const int units = tokens * PER_TOKEN, stride = g.splits * (kSplitThreads / 32);
-    for (int w0 = z + warp * g.splits; w0 < units; w0 += stride * BATCH) {
-        float v0[BATCH], v1[BATCH];
+    for (int slot = warp; slot * splits + z < units; slot += kSplitThreads / 32) {
+        const int w = slot * splits + z;
+        const uint32_t at = ring + (uint32_t)(slot * splits * PARTS) * 128 + lane * 4;
+        float p0[kMaxCluster], p1[kMaxCluster];
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i) v0[i] = v1[i] = 0.0f;
-        for (int c = 0; c < g.splits; ++c) {
-            const uint32_t at = cluster_addr(ring + (uint32_t)lane * 4, (uint32_t)c);
-#pragma unroll
-            for (int i = 0; i < BATCH; ++i) {
-                const int w = w0 + i * stride, m = w / PER_TOKEN, unit = w % PER_TOKEN;
-                if (w >= units) break;
-                // rows of the tile: 32 unit, or g and u: 64-row halves (16 bits), 32-row groups in turn (4 bits)
-                const int r0 = Epi::UNITS == 1 || PAIRED16 ? unit * 32 : unit * 64;
-                const int r1 = PAIRED16 ? 64 + unit * 32 : unit * 64 + 32;
-                v0[i] += ld_cluster(at + (uint32_t)(m * 128 + r0) * 4);
-                if (Epi::UNITS == 2) v1[i] += ld_cluster(at + (uint32_t)(m * 128 + r1) * 4);
-            }
+        for (int c = 0; c < kMaxCluster; ++c) {
+            p0[c] = c < splits ? ld_shared(at + c * PARTS * 128) : 0.0f;
+            if (PARTS == 2) p1[c] = c < splits ? ld_shared(at + c * PARTS * 128 + 128) : 0.0f;
         }
+        float v0 = p0[0], v1 = PARTS == 2 ? p1[0] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-            const int w = w0 + i * stride;
-            if (w < units) epi.emit(v0[i], v1[i], (int64_t)mt * NQ + w / PER_TOKEN, w % PER_TOKEN, lane, nt);
+        for (int c = 1; c < kMaxCluster; ++c) {
+            if (c >= splits) break;
+            v0 += p0[c];
+            if (PARTS == 2) v1 += p1[c];
         }
+        epi.emit(v0, v1, (int64_t)mt * NQ + w / PER_TOKEN, w % PER_TOKEN, lane, nt);
     }
-    cluster_sync();  // no CTA leaves while another reads its sums
 }
 
 template <int KIND, int NQ, bool PAIRED16, class Epi>
@@ -311,8 +318,15 @@ inline int split_count(int64_t tiles, int nk) {
     return (nk + per - 1) / per;
 }
 
-// Whether the split kernel takes a product of M tokens: see the callers.
-inline bool split_takes(int64_t M, int64_t pair_tiles) { return M <= 128 || pair_tiles * 4 <= tile_sms(); }
+// Up to how many tokens the split kernel takes a product; beyond, the pairs'
+// tiles are faster although they leave SMs idle.  Weights from HBM, us:
+//                          64 tokens            128 tokens
+//                        split    pairs       split    pairs
+//   8192 x 8192 nvfp4     12.2     13.3        15.5     13.3
+//   12288 x 4096 mxfp4    10.1      9.1        13.6      9.8
+//   4096 x 12288 mxfp4     9.7     13.0        12.6     13.4
+//   16-bit block 4096 x 12288    59.9  79.0    68.9     80.4
+constexpr int kSplitTokens4 = 64, kSplitTokens16 = 128;
 
 template <int KIND, bool PAIRED16, class Epi>
 cudaError_t launch_split_gemm(SplitArgs g, const SplitMaps& maps, const Epi& epi, cudaStream_t st) {

@@ -148,6 +148,12 @@ __device__ __forceinline__ void tma_load_2d_group(uint32_t dst, const void* tmap
         : "memory");
 }
 
+// The box at (x, y) into L2 only.  Safe before the wait for earlier work on the
+// stream: whoever writes the box later writes it in L2 as well.
+__device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(tmap), "r"(x), "r"(y) : "memory");
+}
+
 namespace {
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
