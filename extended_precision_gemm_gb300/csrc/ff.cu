@@ -7,6 +7,11 @@
 // epilogues.  The training form keeps h (16 bits), a = act(g) and
 // b = u * act'(g): the backward pass is then dg = dh b, du = dh a and needs
 // neither g and u nor the activation again.
+//
+// a and b enter dg and du as factors, so their rounding adds to that of dg and
+// du themselves.  For bfloat16 (8 significant bits) they are kept as float16 (11)
+// with a power of two for every 32 of a row, which takes 2 bytes and leaves the
+// gradients' error as 32 bits would; for float16 in 32 bits.
 #include "activation.cuh"
 #include "mx4.cuh"
 #include "split_gemm.cuh"
@@ -14,6 +19,71 @@
 
 namespace ddg {
 namespace {
+
+// The planes a and b of the training form: T rows of ld values, and for
+// bfloat16 an exponent byte for every 32 of them.
+template <typename T> struct Keep;
+template <> struct Keep<__half> { using value = float; };
+template <> struct Keep<__nv_bfloat16> { using value = __half; };
+
+struct KeepPlanes {
+    void *a, *b;
+    uint8_t *ea, *eb;
+};
+
+// The exponent byte for values whose largest finite magnitude has these bits,
+// and the power of two that brings it to [2^14, 2^15).
+__device__ __forceinline__ uint32_t keep_byte(uint32_t max_bits) { return max(max_bits >> 23, 15u); }
+__device__ __forceinline__ float keep_scale(uint32_t byte) { return exp2_int(14 + 127 - (int)byte); }
+__device__ __forceinline__ float keep_inverse(uint32_t byte) { return exp2_int((int)byte - 127 - 14); }
+__device__ __forceinline__ uint32_t finite_bits(float v) {
+    const uint32_t b = __float_as_uint(v) & 0x7fffffffu;
+    return b < kInfBits ? b : 0u;
+}
+
+// A thread's 32 consecutive values of a row, at `at`.
+__device__ __forceinline__ void keep_row(__half* plane, uint8_t* bytes, int64_t at, float (&v)[32]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) m = max(m, finite_bits(v[i]));
+    const uint32_t byte = keep_byte(m);
+    const float s = keep_scale(byte);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= s;
+    store_row(plane + at, v);
+    bytes[at / 32] = (uint8_t)byte;
+}
+__device__ __forceinline__ void keep_row(float* plane, uint8_t*, int64_t at, float (&v)[32]) { store_row(plane + at, v); }
+
+// One value of 32 in a warp.
+__device__ __forceinline__ void keep_lane(__half* plane, uint8_t* bytes, int64_t at, float v, int lane) {
+    const uint32_t byte = keep_byte(__reduce_max_sync(~0u, finite_bits(v)));
+    plane[at] = __float2half_rn(v * keep_scale(byte));
+    if (lane == 0) bytes[at / 32] = (uint8_t)byte;
+}
+__device__ __forceinline__ void keep_lane(float* plane, uint8_t*, int64_t at, float v, int) { plane[at] = v; }
+
+// 16 kept values of a row; `at / 32` is their block.
+__device__ __forceinline__ void kept16(const __half* plane, const uint8_t* bytes, int64_t at, float (&v)[16]) {
+    uint32_t w[8];
+    load_v8(plane + at, w);
+    const float s = keep_inverse(bytes[at / 32]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        v[2 * i] = f.x * s;
+        v[2 * i + 1] = f.y * s;
+    }
+}
+__device__ __forceinline__ void kept16(const float* plane, const uint8_t*, int64_t at, float (&v)[16]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        uint32_t w[8];
+        load_v8(plane + at + 8 * k, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * k + i] = __uint_as_float(w[i]);
+    }
+}
 
 // C = accumulators, rounded once; of one product, or of each of three.
 template <typename T, int NT_, int P, bool ALIGNED>
@@ -46,8 +116,8 @@ template <typename T, int NT_, bool SAVE>
 struct EpiGate {
     static constexpr int NT = NT_, GROUPS = 2;
     T* h;
-    float *a, *b;
-    int64_t ld, M, N;  // N: F rounded up to 64 (the planes' rows, ld)
+    KeepPlanes keep;
+    int64_t M, N;  // N: F rounded up to 64, a row of every plane
     int act;
     template <class Release>
     __device__ __forceinline__ void run(uint32_t acc, int, int64_t row, int nt, int group, int, Release release) const {
@@ -71,10 +141,12 @@ struct EpiGate {
                     bv[i] = __uint_as_float(u[i]) * da;
                 }
             });
-            store_row(h + row * ld + col, hv);
+            const int64_t at = row * N + col;
+            store_row(h + at, hv);
             if (SAVE) {
-                store_row(a + row * ld + col, av);
-                store_row(b + row * ld + col, bv);
+                using V = typename Keep<T>::value;
+                keep_row(static_cast<V*>(keep.a), keep.ea, at, av);
+                keep_row(static_cast<V*>(keep.b), keep.eb, at, bv);
             }
         }
     }
@@ -84,9 +156,9 @@ struct EpiGate {
 template <typename T, int NT_>
 struct EpiGateBackward {
     static constexpr int NT = NT_, GROUPS = 2;
-    const float *a, *b;
+    KeepPlanes keep;
     T *dg, *du;
-    int64_t ld, M, N;
+    int64_t M, N;  // N: F rounded up to 64, a row of every plane
     template <class Release>
     __device__ __forceinline__ void run(uint32_t acc, int, int64_t row, int nt, int group, int, Release release) const {
         constexpr int STEPS = NT / GROUPS / 32;
@@ -98,24 +170,22 @@ struct EpiGateBackward {
             if (j == STEPS - 1) release();
             const int64_t col = (int64_t)nt * NT + c;
             if (row >= M || col >= N) continue;
+            using V = typename Keep<T>::value;
 #pragma unroll
             for (int i = 0; i < 32; i += 16) {
-                uint32_t wa[2][8], wb[2][8], pg[8], pu[8];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    load_v8(a + row * ld + col + i + 8 * k, wa[k]);
-                    load_v8(b + row * ld + col + i + 8 * k, wb[k]);
-                }
+                const int64_t at = row * N + col + i;
+                float a[16], b[16];
+                kept16(static_cast<const V*>(keep.a), keep.ea, at, a);
+                kept16(static_cast<const V*>(keep.b), keep.eb, at, b);
+                uint32_t pg[8], pu[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const float d0 = __uint_as_float(v[i + 2 * k]), d1 = __uint_as_float(v[i + 2 * k + 1]);
-                    const uint32_t* qa = &wa[k / 4][2 * k % 8];
-                    const uint32_t* qb = &wb[k / 4][2 * k % 8];
-                    pg[k] = pack2<T>(d0 * __uint_as_float(qb[0]), d1 * __uint_as_float(qb[1]));
-                    pu[k] = pack2<T>(d0 * __uint_as_float(qa[0]), d1 * __uint_as_float(qa[1]));
+                    pg[k] = pack2<T>(d0 * b[2 * k], d1 * b[2 * k + 1]);
+                    pu[k] = pack2<T>(d0 * a[2 * k], d1 * a[2 * k + 1]);
                 }
-                store_v8(dg + row * ld + col + i, pg);
-                store_v8(du + row * ld + col + i, pu);
+                store_v8(dg + at, pg);
+                store_v8(du + at, pu);
             }
         }
     }
@@ -137,18 +207,19 @@ template <typename T>
 struct EpiSplitGate {
     static constexpr int UNITS = 2;
     T* h;
-    float *a, *b;  // null: no backward pass follows
-    int64_t ld, N;
+    KeepPlanes keep;  // null: no backward pass follows
+    int64_t N;        // F rounded up to 64, a row of every plane
     int act;
     __device__ __forceinline__ void emit(float g, float u, int64_t m, int unit, int lane, int tile) const {
         const int64_t n = (int64_t)tile * 64 + unit * 32 + lane;
-        if (n >= N) return;
+        if (n >= N) return;  // whole warps
         float av = 0.0f, da = 0.0f;
         with_activation(act, [&](auto tag) { activation<decltype(tag)::value, true>(g, av, da); });
-        h[m * ld + n] = from_float<T>(av * u);
-        if (a != nullptr) {
-            a[m * ld + n] = av;
-            b[m * ld + n] = u * da;
+        h[m * N + n] = from_float<T>(av * u);
+        if (keep.a != nullptr) {
+            using V = typename Keep<T>::value;
+            keep_lane(static_cast<V*>(keep.a), keep.ea, m * N + n, av, lane);
+            keep_lane(static_cast<V*>(keep.b), keep.eb, m * N + n, u * da, lane);
         }
     }
 };
@@ -266,7 +337,7 @@ template <int KIND, typename T, int NT, bool SAVE>
 cudaError_t gate16(const FfForward& f, cudaStream_t st) {
     return product16<KIND, false, false, true>(
         f.T, f.F, f.D, 1, f.x, f.x, f.wg, f.wu,
-        EpiGate<T, NT, SAVE>{static_cast<T*>(f.h), f.a, f.b, f.ld, f.T, round_up(f.F, 64), f.act}, st);
+        EpiGate<T, NT, SAVE>{static_cast<T*>(f.h), KeepPlanes{f.a, f.b, f.ea, f.eb}, f.T, f.ld, f.act}, st);
 }
 
 template <int KIND, typename T>
@@ -275,7 +346,7 @@ cudaError_t forward_typed(const FfForward& f, cudaStream_t st) {
     cudaError_t err;
     if (f.T <= kSplitTokens16) {
         err = split16<KIND, true>(f.x, f.wg, f.wu, false,
-                                  EpiSplitGate<T>{static_cast<T*>(f.h), f.a, f.b, f.ld, f.F, f.act}, st);
+                                  EpiSplitGate<T>{static_cast<T*>(f.h), KeepPlanes{f.a, f.b, f.ea, f.eb}, f.ld, f.act}, st);
     } else {
         const bool narrow = narrow16(f.T, f.F, 128), save = f.a != nullptr;
         err = narrow ? (save ? gate16<KIND, T, 128, true>(f, st) : gate16<KIND, T, 128, false>(f, st))
@@ -292,7 +363,9 @@ template <int KIND, typename T, int NT>
 cudaError_t gate_backward16(const FfBackward& f, cudaStream_t st) {
     return product16<KIND, false, true, false>(
         f.T, f.F, f.D, 1, f.dy, f.dy, f.wd, f.wd,
-        EpiGateBackward<T, NT>{f.a, f.b, static_cast<T*>(f.dg), static_cast<T*>(f.du), f.ld, f.T, round_up(f.F, 64)}, st);
+        EpiGateBackward<T, NT>{KeepPlanes{const_cast<void*>(f.a), const_cast<void*>(f.b), const_cast<uint8_t*>(f.ea),
+                                           const_cast<uint8_t*>(f.eb)},
+                                static_cast<T*>(f.dg), static_cast<T*>(f.du), f.T, f.ld}, st);
 }
 
 // The weights' gradients that are wanted, in one launch: sums over the T rows

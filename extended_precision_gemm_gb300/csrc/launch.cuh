@@ -217,13 +217,15 @@ struct Matrix16 {
 };
 cudaError_t launch_realign(const Matrix16& src, const Matrix16& dst, cudaStream_t st);
 // The gated block; operands 16-byte aligned with 16-byte rows.  h, a, b (and
-// dg, du): planes of T rows, ld elements apart (a multiple of 64, >= F).
+// dg, du): planes of T rows of ld elements (F rounded up to 64); a and b as
+// float16 with a byte for every 32 in ea and eb (bfloat16), or in 32 bits.
 struct FfForward {
     int type, act;
     int64_t T, D, F;
     Matrix16 x, wg, wu, wd;
     void* h;
-    float *a, *b;  // null: no backward pass follows
+    void *a, *b;  // null: no backward pass follows
+    uint8_t *ea, *eb;
     int64_t ld;
     void* y;
     int64_t ldy;
@@ -234,7 +236,8 @@ struct FfBackward {
     int64_t T, D, F;
     Matrix16 dy, x, wg, wu, wd;
     const void* h;
-    const float *a, *b;
+    const void *a, *b;
+    const uint8_t *ea, *eb;
     void *dg, *du;
     int64_t ld;
     void* dx;  // any of the gradients may be null

@@ -137,14 +137,17 @@ cudaError_t zero16(void* p, int64_t rows, int64_t cols, int64_t ld, int64_t elem
     return cudaMemset2DAsync(p, (size_t)(ld * elem), 0, (size_t)(cols * elem), (size_t)rows, st);
 }
 
-// Planes of the training form: h (16 bits), a and b.
+// Planes of the training form: h, a and b, exponent bytes of a and b.
 struct SavedLayout {
-    int64_t ld, off_a, off_b, total;
-    SavedLayout(int64_t T, int64_t F) {
+    int64_t ld, off_a, off_b, off_ea, off_eb, total;
+    SavedLayout(int type, int64_t T, int64_t F) {
+        const int64_t elem = type == DDGEMM_BF16 ? 2 : 4, bytes = type == DDGEMM_BF16 ? 1 : 0;
         ld = round_up(F, 64);
         off_a = round_up(T * ld * 2, kAlign);
-        off_b = off_a + round_up(T * ld * 4, kAlign);
-        total = off_b + round_up(T * ld * 4, kAlign);
+        off_b = off_a + round_up(T * ld * elem, kAlign);
+        off_ea = off_b + round_up(T * ld * elem, kAlign);
+        off_eb = off_ea + round_up(T * ld / 32 * bytes, kAlign);
+        total = off_eb + round_up(T * ld / 32 * bytes, kAlign);
     }
 };
 
@@ -224,7 +227,7 @@ ddgemm_status dd_ff_gated_saved_size(int type, int64_t T, int64_t F, size_t* byt
     if (bytes == nullptr || !known_type16(type)) return DDGEMM_ERR_INVALID_ARG;
     const ddgemm_status s = check_ff_size(T, 0, F);
     if (s != DDGEMM_OK) return s;
-    *bytes = (size_t)SavedLayout(T, F).total;
+    *bytes = (size_t)SavedLayout(type, T, F).total;
     return DDGEMM_OK;
 }
 
@@ -239,7 +242,7 @@ ddgemm_status dd_ff_gated(int type, int activation, int64_t T, int64_t D, int64_
     if (ldy < std::max<int64_t>(1, D)) return DDGEMM_ERR_INVALID_ARG;
     if (T == 0 || D == 0) return DDGEMM_OK;
     if (bad_operand(out)) return DDGEMM_ERR_INVALID_ARG;
-    const SavedLayout L(T, F);
+    const SavedLayout L(type, T, F);
     if (saved != nullptr && ((uintptr_t)saved % kAlign != 0 || saved_bytes < (size_t)L.total))
         return DDGEMM_ERR_INVALID_ARG;
     for (const Span16& m : in) {
@@ -261,8 +264,9 @@ ddgemm_status dd_ff_gated(int type, int activation, int64_t T, int64_t D, int64_
     if (err != cudaSuccess) return status_of(err);
     char* sv = static_cast<char*>(saved);
     FfForward f{type, activation, T, D, F, ax.m, ag.m, au.m, ad.m, saved ? saved : ws.at<void>(h),
-                saved ? reinterpret_cast<float*>(sv + L.off_a) : nullptr,
-                saved ? reinterpret_cast<float*>(sv + L.off_b) : nullptr, L.ld, y, ldy};
+                saved ? sv + L.off_a : nullptr, saved ? sv + L.off_b : nullptr,
+                saved ? reinterpret_cast<uint8_t*>(sv + L.off_ea) : nullptr,
+                saved ? reinterpret_cast<uint8_t*>(sv + L.off_eb) : nullptr, L.ld, y, ldy};
     return status_of(launch_ff_forward(f, st));
 }
 
@@ -276,7 +280,7 @@ ddgemm_status dd_ff_gated_backward(int type, int64_t T, int64_t D, int64_t F, co
     if (s != DDGEMM_OK) return s;
     const Span16 in[5] = {{dy, T, D, lddy}, {x, T, D, ldx}, {Wg, F, D, ldwg}, {Wu, F, D, ldwu}, {Wd, D, F, ldwd}};
     const Span16 out[4] = {{dx, T, D, lddx}, {dWg, F, D, lddwg}, {dWu, F, D, lddwu}, {dWd, D, F, lddwd}};
-    const SavedLayout L(T, F);
+    const SavedLayout L(type, T, F);
     for (const Span16& m : in)
         if (bad_operand(m)) return DDGEMM_ERR_INVALID_ARG;
     if (T > 0 && F > 0 && D > 0 &&
@@ -312,8 +316,8 @@ ddgemm_status dd_ff_gated_backward(int type, int64_t T, int64_t D, int64_t F, co
     if (err != cudaSuccess) return status_of(err);
     const char* sv = static_cast<const char*>(saved);
     FfBackward f{type, T, D, F, ay.m, ax.m, ag.m, au.m, ad.m, saved,
-                 reinterpret_cast<const float*>(sv + L.off_a), reinterpret_cast<const float*>(sv + L.off_b),
-                 ws.at<void>(og), ws.at<void>(ou), L.ld, dx, lddx, dWg, lddwg, dWu, lddwu, dWd, lddwd};
+                 sv + L.off_a, sv + L.off_b, reinterpret_cast<const uint8_t*>(sv + L.off_ea),
+                 reinterpret_cast<const uint8_t*>(sv + L.off_eb), ws.at<void>(og), ws.at<void>(ou), L.ld, dx, lddx, dWg, lddwg, dWu, lddwu, dWd, lddwd};
     return status_of(launch_ff_backward(f, st));
 }
 

@@ -98,7 +98,7 @@ struct EpiGate4 {
                 for (int i = 0; i < 32; ++i) {
                     float a, da;
                     activation<decltype(tag)::value, false>(g[i], a, da);
-                    hv[i] = a * u[i];
+                    hv[i] = c + i < F ? a * u[i] : 0.0f;  // rows that fill up W take no part
                 }
             });
         }
@@ -165,7 +165,7 @@ struct EpiSplitGate4 {
         }
         float a = 0.0f, da;
         with_activation(act, [&](auto tag) { activation<decltype(tag)::value, false>(g, a, da); });
-        const float hv = a * u;
+        const float hv = n < F ? a * u : 0.0f;  // rows that fill up W take no part
         if (KIND == kKindNv) {
             if (n < F) h[m * ld + n] = hv;
             return;

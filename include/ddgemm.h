@@ -787,8 +787,8 @@ ddgemm_status dd_ff_gated_backward(int type, int64_t T, int64_t D, int64_t F, co
  * The block on 4-bit operands, for serving: x (T x D, of `type`) is quantised
  * along D, h along F (from its 32-bit values), both products run as
  * dd_mx4_gemm, y is of `type`.  W_in holds Wg and Wu in turn, 32 rows of Wg
- * then the same 32 of Wu, the last groups filled up with zero rows: 2 *
- * (F rounded up to 32) rows of length D.  W_out is Wd: D rows of length F.
+ * then the same 32 of Wu, the last groups filled up with rows that take no
+ * part: 2 * (F rounded up to 32) rows of length D.  W_out is Wd: D rows of length F.
  */
 ddgemm_status dd_mx4_ff_gated(int format, int type, int activation, int64_t T, int64_t D, int64_t F, const void* x,
                               int64_t ldx, const uint8_t* in_codes, int64_t ld_in, const uint8_t* in_scales,

@@ -119,3 +119,20 @@ def test_repeated_calls_and_other_streams_agree():
             second = ddg.mx4_ff_gated(x, *w, stream=side)
             side.synchronize()
             assert torch.equal(first, second) and torch.equal(first, ddg.mx4_ff_gated(x, *w))
+
+
+@pytest.mark.parametrize("fmt", ("mxfp4", "nvfp4"))
+@pytest.mark.parametrize("T", (3, 150))
+def test_rows_that_fill_up_the_last_group_take_no_part(T, fmt):
+    """Whatever the rows beyond F hold, NaN among it, the outputs are the same."""
+    torch = _torch()
+    D, F = 96, 72
+    w_in, w_out = ddg.mx4_ff_weights(*(torch.randn(s, device="cuda") for s in ((F, D), (F, D), (D, F))), fmt)
+    x = torch.randn(T, D, device="cuda").bfloat16()
+    want = ddg.mx4_ff_gated(x, w_in, w_out)
+    blocks = -(-D // ms.BLOCK[fmt])
+    rows = [g * 64 + h * 32 + i for g in (2,) for h in (0, 1) for i in range(F - 64, 32)]
+    at = [ms.scale_offset(r, b, fmt, D) for r in rows for b in range(blocks)]
+    w_in.scales[torch.tensor(at, device="cuda")] = 255 if fmt == "mxfp4" else 127
+    w_in.codes[torch.tensor(rows, device="cuda")] = 0x55
+    assert torch.equal(ddg.mx4_ff_gated(x, w_in, w_out), want)
