@@ -92,7 +92,7 @@ struct EpiStore {
     T* C[P];
     int64_t ldc[P], M[P], N[P];
     template <class Release>
-    __device__ __forceinline__ void run(uint32_t acc, int p, int64_t row, int nt, int group, int lane, Release release) const {
+    __device__ __forceinline__ void run(uint32_t acc, int p, int, int64_t row, int nt, int group, int lane, Release release) const {
         if (P == 1) p = 0;
         constexpr int STEPS = NT / GROUPS / 32;
 #pragma unroll 1
@@ -109,6 +109,61 @@ struct EpiStore {
     }
 };
 
+// The same where a tile is shared by several units: partial sums in 32 bits,
+// planes of M rows of ld (N rounded up to 32) for each split.
+template <int NT_, int P>
+struct EpiPartial {
+    static constexpr int NT = NT_, GROUPS = 2;
+    float* planes[P];
+    int64_t ld[P], M[P];
+    template <class Release>
+    __device__ __forceinline__ void run(uint32_t acc, int p, int z, int64_t row, int nt, int group, int, Release release) const {
+        if (P == 1) p = 0;
+        constexpr int STEPS = NT / GROUPS / 32;
+#pragma unroll 1
+        for (int j = 0; j < STEPS; ++j) {
+            const int c = (group * STEPS + j) * 32;
+            uint32_t v[32];
+            tc5::ld32(acc + c, v);
+            if (j == STEPS - 1) release();
+            const int64_t col = (int64_t)nt * NT + c;
+            if (row >= M[p] || col >= ld[p]) continue;
+            float f[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+            store_row(planes[p] + ((int64_t)z * M[p] + row) * ld[p] + col, f);
+        }
+    }
+};
+
+// C = the sum of the splits' planes, in their order, rounded once.
+template <typename T, int P>
+struct PartialSums {
+    const float* planes[P];
+    T* C[P];
+    int64_t ld[P], ldc[P], M[P], N[P];
+    int splits;
+};
+template <typename T, int P>
+__global__ void __launch_bounds__(256) add_partials_kernel(const __grid_constant__ PartialSums<T, P> s) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int p = P == 1 ? 0 : blockIdx.z;
+    const int64_t n = s.M[p] * s.ld[p];
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / s.ld[p], c = i - row * s.ld[p];
+        if (c >= s.N[p]) continue;
+        float v[16];
+#pragma unroll
+        for (int z = 0; z < 16; ++z) v[z] = z < s.splits ? s.planes[p][z * n + i] : 0.0f;
+        float sum = v[0];
+#pragma unroll
+        for (int z = 1; z < 16; ++z)
+            if (z < s.splits) sum += v[z];
+        s.C[p][row * s.ldc[p] + c] = from_float<T>(sum);
+    }
+}
+
 // h = act(g) * u from accumulators of NT / 2 columns of g and as many of u,
 // rounded to 16 bits (the operand of the next product); SAVE: a = act(g),
 // b = u act'(g).
@@ -120,7 +175,7 @@ struct EpiGate {
     int64_t M, N;  // N: F rounded up to 64, a row of every plane
     int act;
     template <class Release>
-    __device__ __forceinline__ void run(uint32_t acc, int, int64_t row, int nt, int group, int, Release release) const {
+    __device__ __forceinline__ void run(uint32_t acc, int, int, int64_t row, int nt, int group, int, Release release) const {
         constexpr int STEPS = NT / 2 / GROUPS / 32;
 #pragma unroll 1
         for (int j = 0; j < STEPS; ++j) {
@@ -160,7 +215,7 @@ struct EpiGateBackward {
     T *dg, *du;
     int64_t M, N;  // N: F rounded up to 64, a row of every plane
     template <class Release>
-    __device__ __forceinline__ void run(uint32_t acc, int, int64_t row, int nt, int group, int, Release release) const {
+    __device__ __forceinline__ void run(uint32_t acc, int, int, int64_t row, int nt, int group, int, Release release) const {
         constexpr int STEPS = NT / GROUPS / 32;
 #pragma unroll 1
         for (int j = 0; j < STEPS; ++j) {
@@ -224,27 +279,36 @@ struct EpiSplitGate {
     }
 };
 
-// Rows of `cols` 16-bit elements to 128-byte aligned rows: a warp takes 256
-// elements of a row, 8 loads of one element a lane in flight (the source may be
-// aligned to its elements only), and stores 4 bytes a lane.
-__global__ void __launch_bounds__(256) realign_kernel(const uint16_t* src, int64_t ld, int64_t rows, int64_t cols,
-                                                      uint16_t* dst, int64_t ldd) {
+// Rows of 16-bit elements to 128-byte aligned rows, up to five matrices in one
+// launch: a warp takes 256 elements of a row, 8 loads of one element a lane in
+// flight (the source may be aligned to its elements only), and stores 4 bytes a
+// lane.
+struct RealignAll {
+    Matrix16 src[kRealignMax], dst[kRealignMax];
+    int64_t end[kRealignMax];  // items up to and with each matrix
+    int count;
+};
+__global__ void __launch_bounds__(256) realign_kernel(const __grid_constant__ RealignAll a) {
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t parts = (cols + 255) / 256;
-    for (int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); item < rows * parts; item += (int64_t)gridDim.x * 8) {
+    for (int64_t i0 = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i0 < a.end[a.count - 1]; i0 += (int64_t)gridDim.x * 8) {
+        int k = 0;
+        while (i0 >= a.end[k]) ++k;
+        const int64_t item = i0 - (k > 0 ? a.end[k - 1] : 0);
+        const int64_t cols = a.src[k].cols, parts = (cols + 255) / 256;
         const int64_t r = item / parts, c0 = item % parts * 256 + lane * 2;
-        const uint16_t* p = src + r * ld;
+        const uint16_t* p = static_cast<const uint16_t*>(a.src[k].p) + r * a.src[k].ld;
+        uint16_t* d = static_cast<uint16_t*>(a.dst[k].p) + r * a.dst[k].ld;
         uint16_t v[4][2];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) v[i][j] = c0 + i * 64 + j < cols ? p[c0 + i * 64 + j] : (uint16_t)0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)  // ldd is cols rounded up to 64: a pair begun inside a row lies in it
+        for (int i = 0; i < 4; ++i)  // rows of cols rounded up to 64: a pair begun inside one lies in it
             if (c0 + i * 64 < cols)
-                *reinterpret_cast<uint32_t*>(dst + r * ldd + c0 + i * 64) = (uint32_t)v[i][0] | (uint32_t)v[i][1] << 16;
+                *reinterpret_cast<uint32_t*>(d + c0 + i * 64) = (uint32_t)v[i][0] | (uint32_t)v[i][1] << 16;
     }
 }
 
@@ -316,7 +380,52 @@ void set_store(Epi& epi, int p, void* C, int64_t ldc, int64_t M, int64_t N) {
     epi.N[p] = N;
 }
 
-// C = sum over segments, with wide or narrow tiles.
+// Products whose few tiles are shared by several units: the partial sums in the
+// library's pool, and the launch that adds them up.
+template <typename T, int P>
+class Partials {
+public:
+    void add(void* C, int64_t ldc, int64_t M, int64_t N) {
+        const int p = count_++;
+        sums_.C[p] = static_cast<T*>(C);
+        sums_.ldc[p] = ldc;
+        sums_.M[p] = M;
+        sums_.N[p] = N;
+        sums_.ld[p] = round_up(N, 32);
+        total_ += M * sums_.ld[p];
+        most_ = std::max(most_, M * sums_.ld[p]);
+    }
+    template <int KIND, bool A_MN, bool B_MN>
+    cudaError_t run(TileArgs g, int splits, const TileMaps& maps, cudaStream_t st) {
+        void* ws = nullptr;
+        cudaError_t err = pool_alloc(&ws, (size_t)(total_ * splits * 4), st);
+        if (err != cudaSuccess) return err;
+        EpiPartial<128, P> epi = {};
+        float* at = static_cast<float*>(ws);
+        for (int p = 0; p < count_; ++p) {
+            epi.planes[p] = at;
+            sums_.planes[p] = at;
+            epi.ld[p] = sums_.ld[p];
+            epi.M[p] = sums_.M[p];
+            at += sums_.M[p] * sums_.ld[p] * splits;
+        }
+        g.splits = splits;
+        sums_.splits = splits;
+        err = launch_tile_gemm<KIND, A_MN, B_MN, false>(g, maps, epi, st);
+        if (err == cudaSuccess)
+            err = launch_pdl(add_partials_kernel<T, P>, dim3((unsigned)std::min<int64_t>((most_ + 255) / 256, 1 << 20), 1, (unsigned)count_),
+                             dim3(256), 0, st, sums_);
+        const cudaError_t freed = cudaFreeAsync(ws, st);
+        return err == cudaSuccess ? freed : err;
+    }
+
+private:
+    PartialSums<T, P> sums_ = {};
+    int count_ = 0;
+    int64_t total_ = 0, most_ = 0;
+};
+
+// C = sum over segments, with wide or narrow tiles, or narrow ones shared.
 template <int KIND, typename T, bool B_MN, int NT, bool ALIGNED>
 cudaError_t store16_sized(int64_t M, int64_t N, int64_t K, int segs, const Matrix16& A0, const Matrix16& A1,
                           const Matrix16& B0, const Matrix16& B1, void* C, int64_t ldc, cudaStream_t st) {
@@ -327,6 +436,19 @@ cudaError_t store16_sized(int64_t M, int64_t N, int64_t K, int segs, const Matri
 template <int KIND, typename T, bool B_MN>
 cudaError_t store16(int64_t M, int64_t N, int64_t K, int segs, const Matrix16& A0, const Matrix16& A1,
                     const Matrix16& B0, const Matrix16& B1, void* C, int64_t ldc, cudaStream_t st) {
+    const int splits = tile_splits(pair_tiles(M, N, 128), (K + 63) / 64 * segs);
+    if (splits > 1) {
+        Partials<T, 1> parts;
+        parts.add(C, ldc, M, N);
+        TileMaps maps;
+        memset(&maps, 0, sizeof(maps));
+        cudaError_t err = map16(&maps.a[0], A0, 128);
+        if (err == cudaSuccess) err = map16(&maps.b[0], B0, 64);
+        if (err == cudaSuccess && segs == 2) err = map16(&maps.a[1], A1, 128);
+        if (err == cudaSuccess && segs == 2) err = map16(&maps.b[1], B1, 64);
+        if (err != cudaSuccess) return err;
+        return parts.template run<KIND, false, B_MN>(tile_args(M, N, 128, K, segs), splits, maps, st);
+    }
     const bool narrow = narrow16(M, N, 256), aligned = aligned_rows<T>(C, ldc);
     auto f = narrow ? (aligned ? store16_sized<KIND, T, B_MN, 128, true> : store16_sized<KIND, T, B_MN, 128, false>)
                     : (aligned ? store16_sized<KIND, T, B_MN, 256, true> : store16_sized<KIND, T, B_MN, 256, false>);
@@ -370,28 +492,63 @@ cudaError_t gate_backward16(const FfBackward& f, cudaStream_t st) {
 
 // The weights' gradients that are wanted, in one launch: sums over the T rows
 // of both operands.
-template <int KIND, typename T, int NT, bool ALIGNED>
-cudaError_t weights16(const FfBackward& f, const Matrix16& h, const Matrix16& dg, const Matrix16& du, cudaStream_t st) {
-    TileMaps maps;
+struct WeightProduct {
+    Matrix16 A, B;
+    void* C;
+    int64_t ldc;
+};
+template <int NT>
+cudaError_t weight_args(const WeightProduct* w, int count, int64_t T, TileArgs& g, TileMaps& maps) {
     memset(&maps, 0, sizeof(maps));
-    EpiStore<T, NT, kMaxProducts, ALIGNED> epi = {};
-    TileArgs g = tile_args(f.F, f.D, NT, f.T, 1);
-    g.products = 0;
+    g = tile_args(0, 0, NT, T, 1);
+    g.products = count;
     cudaError_t err = cudaSuccess;
-    auto add = [&](const Matrix16& A, const Matrix16& B, void* C, int64_t ldc) {
-        if (C == nullptr || err != cudaSuccess) return;
-        const int p = g.products++;
-        err = map16(&maps.a[p], A, 64);
-        if (err == cudaSuccess) err = map16(&maps.b[p], B, 64);
-        g.mt[p] = (int)((A.cols + 255) / 256);
-        g.nt[p] = (int)((B.cols + NT - 1) / NT);
-        set_store(epi, p, C, ldc, A.cols, B.cols);
-    };
-    add(dg, f.x, f.dwg, f.lddwg);
-    add(du, f.x, f.dwu, f.lddwu);
-    add(f.dy, h, f.dwd, f.lddwd);
-    if (err != cudaSuccess || g.products == 0) return err;
+    for (int p = 0; p < count && err == cudaSuccess; ++p) {
+        err = map16(&maps.a[p], w[p].A, 64);
+        if (err == cudaSuccess) err = map16(&maps.b[p], w[p].B, 64);
+        g.mt[p] = (int)((w[p].A.cols + 255) / 256);
+        g.nt[p] = (int)((w[p].B.cols + NT - 1) / NT);
+    }
+    return err;
+}
+template <int KIND, typename T, int NT, bool ALIGNED>
+cudaError_t weights16_sized(const WeightProduct* w, int count, int64_t tokens, cudaStream_t st) {
+    TileArgs g;
+    TileMaps maps;
+    const cudaError_t err = weight_args<NT>(w, count, tokens, g, maps);
+    if (err != cudaSuccess) return err;
+    EpiStore<T, NT, kMaxProducts, ALIGNED> epi = {};
+    for (int p = 0; p < count; ++p) set_store(epi, p, w[p].C, w[p].ldc, w[p].A.cols, w[p].B.cols);
     return launch_tile_gemm<KIND, true, true, false>(g, maps, epi, st);
+}
+template <int KIND, typename T>
+cudaError_t weights16(const FfBackward& f, const Matrix16& h, const Matrix16& dg, const Matrix16& du, cudaStream_t st) {
+    WeightProduct w[kMaxProducts];
+    int count = 0;
+    if (f.dwg != nullptr) w[count++] = WeightProduct{dg, f.x, f.dwg, f.lddwg};
+    if (f.dwu != nullptr) w[count++] = WeightProduct{du, f.x, f.dwu, f.lddwu};
+    if (f.dwd != nullptr) w[count++] = WeightProduct{f.dy, h, f.dwd, f.lddwd};
+    if (count == 0) return cudaSuccess;
+    int64_t wide = 0, narrow = 0;
+    bool aligned = true;
+    for (int p = 0; p < count; ++p) {
+        wide += pair_tiles(w[p].A.cols, w[p].B.cols, 256);
+        narrow += pair_tiles(w[p].A.cols, w[p].B.cols, 128);
+        aligned = aligned && aligned_rows<T>(w[p].C, w[p].ldc);
+    }
+    const int splits = tile_splits(narrow, (f.T + 63) / 64);
+    if (splits > 1) {
+        Partials<T, kMaxProducts> parts;
+        for (int p = 0; p < count; ++p) parts.add(w[p].C, w[p].ldc, w[p].A.cols, w[p].B.cols);
+        TileArgs g;
+        TileMaps maps;
+        const cudaError_t err = weight_args<128>(w, count, f.T, g, maps);
+        return err != cudaSuccess ? err : parts.template run<KIND, true, true>(g, splits, maps, st);
+    }
+    auto run = narrow_tiles(wide, narrow, kNarrow16)
+                   ? (aligned ? weights16_sized<KIND, T, 128, true> : weights16_sized<KIND, T, 128, false>)
+                   : (aligned ? weights16_sized<KIND, T, 256, true> : weights16_sized<KIND, T, 256, false>);
+    return run(w, count, f.T, st);
 }
 
 template <int KIND, typename T>
@@ -405,24 +562,24 @@ cudaError_t backward_typed(const FfBackward& f, cudaStream_t st) {
     if (err == cudaSuccess && f.dx != nullptr)
         err = store16<KIND, T, true>(f.T, f.D, f.F, 2, dg, du, f.wg, f.wu, f.dx, f.lddx, st);
     if (err != cudaSuccess) return err;
-    const int64_t wide = 2 * pair_tiles(f.F, f.D, 256) + pair_tiles(f.D, f.F, 256);
-    const int64_t narrow = 2 * pair_tiles(f.F, f.D, 128) + pair_tiles(f.D, f.F, 128);
-    const bool aligned = (f.dwg == nullptr || aligned_rows<T>(f.dwg, f.lddwg)) &&
-                         (f.dwu == nullptr || aligned_rows<T>(f.dwu, f.lddwu)) &&
-                         (f.dwd == nullptr || aligned_rows<T>(f.dwd, f.lddwd));
-    return narrow_tiles(wide, narrow, kNarrow16)
-               ? (aligned ? weights16<KIND, T, 128, true>(f, h, dg, du, st) : weights16<KIND, T, 128, false>(f, h, dg, du, st))
-               : (aligned ? weights16<KIND, T, 256, true>(f, h, dg, du, st) : weights16<KIND, T, 256, false>(f, h, dg, du, st));
+    return weights16<KIND, T>(f, h, dg, du, st);
 }
 
 }  // namespace
 
-cudaError_t launch_realign(const Matrix16& src, const Matrix16& dst, cudaStream_t st) {
-    const int64_t items = src.rows * ((src.cols + 255) / 256);
+cudaError_t launch_realign(const Matrix16* src, const Matrix16* dst, int count, cudaStream_t st) {
+    RealignAll a = {};
+    int64_t items = 0;
+    for (int i = 0; i < count; ++i) {
+        a.src[i] = src[i];
+        a.dst[i] = dst[i];
+        items += src[i].rows * ((src[i].cols + 255) / 256);
+        a.end[i] = items;
+    }
+    a.count = count;
     if (items == 0) return cudaSuccess;
     const unsigned blocks = (unsigned)std::min<int64_t>((items + 7) / 8, 1 << 20);
-    return launch_pdl(realign_kernel, dim3(blocks), dim3(256), 0, st, static_cast<const uint16_t*>(src.p), src.ld,
-                      src.rows, src.cols, static_cast<uint16_t*>(dst.p), dst.ld);
+    return launch_pdl(realign_kernel, dim3(blocks), dim3(256), 0, st, a);
 }
 
 cudaError_t launch_ff_forward(const FfForward& f, cudaStream_t st) {

@@ -215,7 +215,9 @@ struct Matrix16 {
     void* p;
     int64_t rows, cols, ld;
 };
-cudaError_t launch_realign(const Matrix16& src, const Matrix16& dst, cudaStream_t st);
+// Copies to rows of cols rounded up to 64 elements.
+constexpr int kRealignMax = 5;
+cudaError_t launch_realign(const Matrix16* src, const Matrix16* dst, int count, cudaStream_t st);
 // The gated block; operands 16-byte aligned with 16-byte rows.  h, a, b (and
 // dg, du): planes of T rows of ld elements (F rounded up to 64); a and b as
 // float16 with a byte for every 32 in ea and eb (bfloat16), or in 32 bits.

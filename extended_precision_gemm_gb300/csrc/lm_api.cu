@@ -32,7 +32,7 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
 ddgemm_status status_of(cudaError_t e) {
     if (e == cudaSuccess) return DDGEMM_OK;
     (void)cudaGetLastError();
-    return DDGEMM_ERR_CUDA;
+    return e == cudaErrorMemoryAllocation ? DDGEMM_ERR_ALLOC : DDGEMM_ERR_CUDA;
 }
 
 // Sizes of a 4-bit matrix: within the limits, and its scale tiles and row
@@ -108,14 +108,21 @@ struct Aligned16 {
           copy(rows > 0 && cols > 0 && 
                (!aligned16(p) || (rows > 1 && (ld % 8 != 0 || (tokens > kRealignTokens && ld % 64 != 0))))),
           offset(copy ? ws.reserve(rows * round_up(cols, 64) * 2) : 0) {}
-    cudaError_t resolve(const Workspace& ws, cudaStream_t st) {
-        if (!copy) return cudaSuccess;
-        const Matrix16 to{ws.at<void>(offset), m.rows, m.cols, round_up(m.cols, 64)};
-        cudaError_t err = launch_realign(m, to, st);
-        m = to;
-        return err;
-    }
 };
+
+// Makes the copies that are needed, in one launch, and points to them.
+cudaError_t resolve(Aligned16* const* operands, int count, const Workspace& ws, cudaStream_t st) {
+    Matrix16 src[kRealignMax], dst[kRealignMax];
+    int n = 0;
+    for (int i = 0; i < count; ++i) {
+        Aligned16& a = *operands[i];
+        if (!a.copy) continue;
+        src[n] = a.m;
+        a.m = Matrix16{ws.at<void>(a.offset), a.m.rows, a.m.cols, round_up(a.m.cols, 64)};
+        dst[n++] = a.m;
+    }
+    return n > 0 ? launch_realign(src, dst, n, st) : cudaSuccess;
+}
 
 ddgemm_status check_ff_size(int64_t T, int64_t D, int64_t F) {
     if (T < 0 || D < 0 || F < 0) return DDGEMM_ERR_INVALID_ARG;
@@ -257,10 +264,8 @@ ddgemm_status dd_ff_gated(int type, int activation, int64_t T, int64_t D, int64_
     Aligned16 ax(x, T, D, ldx, T, ws), ag(Wg, F, D, ldwg, T, ws), au(Wu, F, D, ldwu, T, ws), ad(Wd, D, F, ldwd, T, ws);
     const int64_t h = saved ? 0 : ws.reserve(T * L.ld * 2);
     if (!ws.allocate()) return DDGEMM_ERR_ALLOC;
-    cudaError_t err = ax.resolve(ws, st);
-    if (err == cudaSuccess) err = ag.resolve(ws, st);
-    if (err == cudaSuccess) err = au.resolve(ws, st);
-    if (err == cudaSuccess) err = ad.resolve(ws, st);
+    Aligned16* const operands[] = {&ax, &ag, &au, &ad};
+    cudaError_t err = resolve(operands, 4, ws, st);
     if (err != cudaSuccess) return status_of(err);
     char* sv = static_cast<char*>(saved);
     FfForward f{type, activation, T, D, F, ax.m, ag.m, au.m, ad.m, saved ? saved : ws.at<void>(h),
@@ -308,11 +313,8 @@ ddgemm_status dd_ff_gated_backward(int type, int64_t T, int64_t D, int64_t F, co
         ad(Wd, D, F, ldwd, T, ws);
     const int64_t og = ws.reserve(T * L.ld * 2), ou = ws.reserve(T * L.ld * 2);
     if (!ws.allocate()) return DDGEMM_ERR_ALLOC;
-    cudaError_t err = ay.resolve(ws, st);
-    if (err == cudaSuccess) err = ax.resolve(ws, st);
-    if (err == cudaSuccess) err = ag.resolve(ws, st);
-    if (err == cudaSuccess) err = au.resolve(ws, st);
-    if (err == cudaSuccess) err = ad.resolve(ws, st);
+    Aligned16* const operands[] = {&ay, &ax, &ag, &au, &ad};
+    cudaError_t err = resolve(operands, 5, ws, st);
     if (err != cudaSuccess) return status_of(err);
     const char* sv = static_cast<const char*>(saved);
     FfBackward f{type, T, D, F, ay.m, ax.m, ag.m, au.m, ad.m, saved,

@@ -104,13 +104,14 @@ __global__ void __launch_bounds__(QWARPS * 32) mxfp4_rows_kernel(const T* X, int
 
 // nvfp4 rows: one block for a row.  The row's values stay in registers
 // between the maximum and the conversion as far as KEEP tiles per warp reach
-// (8 warps: 16384 values of 16 bits, 8192 of 32); longer rows are read again.
+// (16 warps: 16384 values); longer rows are read again.
+constexpr int ROW_WARPS = 16;
 template <typename T>
-__global__ void __launch_bounds__(QWARPS * 32) nvfp4_rows_kernel(const T* X, int64_t ldx, int64_t K, bool vec,
+__global__ void __launch_bounds__(ROW_WARPS * 32) nvfp4_rows_kernel(const T* X, int64_t ldx, int64_t K, bool vec,
                                                                  uint8_t* codes, int64_t ldq, uint8_t* scales,
                                                                  int32_t* exponents) {
-    constexpr int KEEP = sizeof(T) == 2 ? 8 : 4;
-    __shared__ uint32_t part[QWARPS];
+    constexpr int KEEP = 4;
+    __shared__ uint32_t part[ROW_WARPS];
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -398,7 +399,7 @@ cudaError_t quantize_typed(const Mx4Quantize& q, const T* X, cudaStream_t st) {
                               dim3((unsigned)((items + QWARPS - 1) / QWARPS)), dim3(QWARPS * 32), 0, st, X, q.ldx,
                               q.rows, q.K, vec, q.codes, q.ldq, q.scales);
         }
-        const unsigned warps = (unsigned)(kts < QWARPS ? kts : QWARPS);
+        const unsigned warps = (unsigned)(kts < ROW_WARPS ? kts : ROW_WARPS);
         return launch_pdl(nvfp4_rows_kernel<T>, dim3((unsigned)q.rows), dim3(warps * 32), 0, st, X, q.ldx, q.K, vec,
                           q.codes, q.ldq, q.scales, q.exponents);
     }

@@ -37,7 +37,7 @@ struct EpiScale {
     const int32_t *e, *f;
     float alpha;
     template <class Release>
-    __device__ __forceinline__ void run(uint32_t acc, int, int64_t row, int nt, int group, int lane, Release release) const {
+    __device__ __forceinline__ void run(uint32_t acc, int, int, int64_t row, int nt, int group, int lane, Release release) const {
         const int er = KIND == kKindNv && row < M ? e[row] : 0;
 #pragma unroll 1
         for (int j = 0; j < 2; ++j) {
@@ -73,7 +73,7 @@ struct EpiGate4 {
     const int32_t *e, *f;
     int act;
     template <class Release>
-    __device__ __forceinline__ void run(uint32_t acc, int, int64_t row, int n, int group, int lane, Release release) const {
+    __device__ __forceinline__ void run(uint32_t acc, int, int, int64_t row, int n, int group, int lane, Release release) const {
         uint32_t raw[32];
         float g[32], u[32];
         tc5::ld32(acc + group * 64, raw);

@@ -13,6 +13,10 @@
 // only), the others run the epilogue, four warps (128 rows) for each group of
 // columns.
 //
+// Where the tiles are few and deep, the stages of a tile are shared out among
+// several units of work (splits), whose partial sums an epilogue leaves in
+// planes of their own to be added afterwards.
+//
 // 16-bit operands: NT = 256 (128 where that fills the SMs better), 64 k to a stage, either operand with k contiguous
 // or with its row index contiguous (64 x 64 blocks, the same swizzle); the
 // sum may run over two segments (A0 B0^T + A1 B1^T).
@@ -48,8 +52,9 @@ struct TileMaps {
 struct TileArgs {
     int mt[kMaxProducts], nt[kMaxProducts];  // tiles along m and n
     int64_t first[kMaxProducts];             // first tile of each product
-    int64_t tiles;
+    int64_t tiles;                           // of all products
     int products;
+    int splits, per;  // units that share a tile, stages of one (the last may have fewer)
     int pairs;       // CTA pairs in the grid
     int nk, segs;    // stages of a segment, segments (more than one: a single product)
     int last_steps;  // MMAs in a segment's last stage
@@ -72,7 +77,10 @@ struct TileShape {
     static_assert(!F4 || SCALE_COL + 2 * SCALE_COLS <= 512, "tensor memory");
 };
 
-__device__ __forceinline__ void tile_of(const TileArgs& g, int64_t t, int& p, int& m, int& n) {
+// Unit t: split z of tile (m, n) of product p.
+__device__ __forceinline__ void tile_of(const TileArgs& g, int64_t t, int& z, int& p, int& m, int& n) {
+    z = g.splits > 1 ? (int)(t / g.tiles) : 0;
+    t -= z * g.tiles;
     p = g.products > 2 && t >= g.first[2] ? 2 : g.products > 1 && t >= g.first[1] ? 1 : 0;
     t -= g.first[p];
     const int64_t per_group = (int64_t)kTileGroup * g.nt[p];
@@ -82,7 +90,7 @@ __device__ __forceinline__ void tile_of(const TileArgs& g, int64_t t, int& p, in
     n = (int)((t % per_group) / size);
 }
 
-// Epi: NT, GROUPS, and run(acc, product, m row, n tile, group, lane, release): takes this
+// Epi: NT, GROUPS, and run(acc, product, split, m row, n tile, group, lane, release): takes this
 // warp's 32 rows of the accumulators from column `acc` on (all lanes, also for
 // rows beyond the matrix) and calls release() after its last read of them.
 template <int KIND, bool A_MN, bool B_MN, bool GATED, class Epi>
@@ -101,8 +109,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int64_t pair = blockIdx.x >> 1;
-    const int64_t tiles = g.tiles;
-    const int per_tile = g.nk * g.segs;
+    const int64_t tiles = g.tiles * g.splits;  // units
+    const int all_stages = g.nk * g.segs;
 
     const uint32_t full0 = smem_addr(&bars[0]), empty0 = smem_addr(&bars[STAGES]);
     const uint32_t accf0 = smem_addr(&bars[2 * STAGES]), acce0 = smem_addr(&bars[2 * STAGES + 2]);
@@ -138,11 +146,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
         int64_t issued = 0;
         bool ok = true;
         for (int64_t t = pair; t < tiles && ok; t += g.pairs) {
-            int p, mt, nt;
-            tile_of(g, t, p, mt, nt);
+            int z, p, mt, nt;
+            tile_of(g, t, z, p, mt, nt);
+            const int it0 = z * g.per, per_tile = min(g.per, all_stages - it0);
             const int a_row = (mt * 2 + (int)rank) * 128;
             const int b_row = GATED ? nt * (NT / 2) : nt * NT + (int)rank * (NT / 2);
-            int seg = 0, kb = 0;
+            int seg = it0 / g.nk, kb = it0 % g.nk;
             for (int it = 0; it < per_tile; ++it) {
                 ok = warp_wait(empty0 + 8 * stage, phase ^ 1, kTileWaitNs);
                 if (!ok) break;
@@ -206,14 +215,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
             const uint64_t sd0 = tc5::desc_scale_tile(ring + S::A_BYTES + S::B_BYTES);
             uint32_t stage = 0, phase = 0, count = 0;
             for (int64_t t = pair; t < tiles && ok; t += g.pairs, ++count) {
-                int p, mt, nt;
-                tile_of(g, t, p, mt, nt);
+                int z, p, mt, nt;
+                tile_of(g, t, z, p, mt, nt);
+                const int it0 = z * g.per, per_tile = min(g.per, all_stages - it0);
                 const uint32_t buf = count & 1;
                 const uint32_t d = tmem + buf * NT;
                 ok = warp_wait(acce0 + 8 * buf, ((count >> 1) & 1) ^ 1, kTileWaitNs);
                 if (!ok) break;
                 tc5::fence_after_sync();
-                int kb = 0;
+                int kb = it0 % g.nk;
                 for (int it = 0; it < per_tile; ++it) {
                     ok = warp_wait(full0 + 8 * stage, phase, kTileWaitNs);
                     if (!ok) break;
@@ -275,8 +285,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
         const int q = warp & 3, group = (warp - 2) >> 2;
         uint32_t count = 0;
         for (int64_t t = pair; t < tiles; t += g.pairs, ++count) {
-            int p, mt, nt;
-            tile_of(g, t, p, mt, nt);
+            int z, p, mt, nt;
+            tile_of(g, t, z, p, mt, nt);
             const uint32_t buf = count & 1;
             if (!warp_wait(accf0 + 8 * buf, (count >> 1) & 1, kTileWaitNs)) {
                 if (lane == 0) tile_timeout();
@@ -284,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
             }
             tc5::fence_after_sync();
             const int64_t row = ((int64_t)mt * 2 + rank) * 128 + q * 32 + lane;
-            epi.run(tmem + buf * NT + ((uint32_t)(q * 32) << 16), p, row, nt, group, lane, [&]() {
+            epi.run(tmem + buf * NT + ((uint32_t)(q * 32) << 16), p, z, row, nt, group, lane, [&]() {
                 tc5::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
@@ -354,7 +364,9 @@ cudaError_t launch_tile_gemm(TileArgs g, const TileMaps& maps, const Epi& epi, c
         g.tiles += (int64_t)g.mt[p] * g.nt[p];
     }
     if (g.tiles <= 0) return cudaSuccess;
-    g.pairs = (int)std::min<int64_t>(pairs, g.tiles);
+    if (g.splits < 1) g.splits = 1;
+    g.per = (g.nk * g.segs + g.splits - 1) / g.splits;
+    g.pairs = (int)std::min<int64_t>(pairs, g.tiles * g.splits);
     cfg.numAttrs = 2;
     cfg.gridDim = dim3((unsigned)(2 * g.pairs));
     return cudaLaunchKernelEx(&cfg, kernel, g, maps, epi);
@@ -376,6 +388,18 @@ inline bool narrow_tiles(int64_t wide_tiles, int64_t narrow_count, double narrow
     const int64_t pairs = std::max(1, tile_sms() / 2);
     const int64_t wide_rounds = (wide_tiles + pairs - 1) / pairs, rounds = (narrow_count + pairs - 1) / pairs;
     return (double)rounds * narrow_cost < (double)wide_rounds;
+}
+
+// Splits of `tiles` tiles of `stages` stages: enough that the units fill the
+// pairs once, with at least 12 stages each (one costs about 0.2 us; adding the
+// partial sums up takes a launch of 3 us), at most 16; 1 where that gains
+// nothing.
+inline int tile_splits(int64_t tiles, int64_t stages) {
+    const int64_t pairs = std::max(1, tile_sms() / 2);
+    const int64_t s = std::min<int64_t>(std::min<int64_t>(pairs / std::max<int64_t>(1, tiles), stages / 12), 16);
+    if (s < 2 || stages < 32) return 1;
+    const int64_t per = (stages + s - 1) / s;
+    return (int)((stages + per - 1) / per);  // none empty
 }
 
 // ---- pieces of epilogues ----

@@ -207,3 +207,17 @@ def test_infinities_reach_what_depends_on_them_only():
     assert bad[7].any()
     bad[7] = False
     assert not bad.any()
+
+
+@pytest.mark.parametrize("dtype", ("bfloat16", "float16"))
+@pytest.mark.parametrize("T,D,F", [(3000, 136, 70), (9, 72, 3000), (2100, 200, 2200), (2500, 77, 131), (130, 40, 4000)])
+def test_few_tiles_and_deep_sums(T, D, F, dtype):
+    """Gradients whose sums are shared by several blocks and added up afterwards."""
+    x, wg, wu, wd, dy = inputs(T, D, F, dtype, T + F)
+    want = expected(x, wg, wu, wd, dy, "silu", dtype)
+    y, saved = ddg.ff_gated(x, wg, wu, wd, save=True)
+    dx, dwg, dwu, dwd = ddg.ff_gated_backward(dy, x, wg, wu, wd, saved)
+    got = {"y": y, "dx": dx, "dwg": dwg, "dwu": dwu, "dwd": dwd}
+    check(got, want, want)
+    again = ddg.ff_gated_backward(dy, x, wg, wu, wd, saved)
+    assert all(_torch().equal(a, got[n]) for a, n in zip(again, ("dx", "dwg", "dwu", "dwd")))
