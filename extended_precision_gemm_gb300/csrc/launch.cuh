@@ -189,6 +189,10 @@ cudaError_t launch_mx4_quantize(const Mx4Quantize& q, cudaStream_t st);
 cudaError_t launch_mx4_dequantize(int fmt, int type, int64_t rows, int64_t K, const uint8_t* codes, int64_t ldq,
                                   const uint8_t* scales, const int32_t* exponents, void* X, int64_t ldx,
                                   cudaStream_t st);
+// Exponents and scales of nvfp4 rows from the largest magnitudes of their blocks
+// (what launch_mx4_gate leaves; see mx4.cu).
+cudaError_t launch_nvfp4_finish(const float* most, int64_t rows, int64_t K, uint8_t* codes, int64_t ldq, uint8_t* scales,
+                                int32_t* exponents, cudaStream_t st);
 // C (A.rows x B.rows) = alpha A B^T.
 struct Mx4Gemm {
     int fmt, type;
@@ -199,13 +203,14 @@ struct Mx4Gemm {
     bool early;  // B was complete before the launch before this one began
 };
 cudaError_t launch_mx4_gemm(const Mx4Gemm& g, cudaStream_t st);
-// act(x Wg^T) * (x Wu^T) with Wg and Wu in turn, 32 rows each, in W; into hq
-// (mxfp4) or h in 32 bits (nvfp4).
+// act(x Wg^T) * (x Wu^T) with Wg and Wu in turn, 32 rows each, in W, into hq:
+// codes and scales (mxfp4), or codes and the largest magnitude of every block
+// for launch_nvfp4_finish (nvfp4).
 struct Mx4Gate {
     int fmt, act;
     Mx4Matrix x, W, hq;
-    float* h;
-    int64_t ldh, F;
+    float* most;
+    int64_t F;
 };
 cudaError_t launch_mx4_gate(const Mx4Gate& g, cudaStream_t st);
 cudaError_t read_and_reset_wait_timeouts_mx4(unsigned int* count);

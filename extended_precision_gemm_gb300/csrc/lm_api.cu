@@ -349,22 +349,20 @@ ddgemm_status dd_mx4_ff_gated(int format, int type, int activation, int64_t T, i
     if (F == 0) return status_of(zero16(y, T, D, ldy, es, st));
     const bool nv = format == DDGEMM_NVFP4;
     Workspace ws(st);
-    const int64_t xl = round_up(mx4_code_bytes(D), 128), hl = round_up(mx4_code_bytes(F), 128), ldh = round_up(F, 64);
+    const int64_t xl = round_up(mx4_code_bytes(D), 128), hl = round_up(mx4_code_bytes(F), 128);
     const int64_t xc = ws.reserve(T * xl), xs = ws.reserve(mx4_scale_bytes(format, T, D)), xe = ws.reserve(T * 4);
     const int64_t hc = ws.reserve(T * hl), hs = ws.reserve(mx4_scale_bytes(format, T, F)), he = ws.reserve(T * 4);
-    const int64_t hf = nv ? ws.reserve(T * ldh * 4) : 0;
+    const int64_t hm = nv ? ws.reserve(T * mx4_scale_tiles(format, F) * 4 * 4) : 0;
     if (!ws.allocate()) return DDGEMM_ERR_ALLOC;
     const Mx4Matrix xq{ws.at<uint8_t>(xc), xl, ws.at<uint8_t>(xs), ws.at<int32_t>(xe), T, D};
     const Mx4Matrix hq{ws.at<uint8_t>(hc), hl, ws.at<uint8_t>(hs), ws.at<int32_t>(he), T, F};
-    float* h = nv ? ws.at<float>(hf) : nullptr;
+    float* most = nv ? ws.at<float>(hm) : nullptr;
     cudaError_t err = launch_mx4_quantize(Mx4Quantize{format, type, false, T, D, x, ldx, ws.at<uint8_t>(xc), xl,
                                                       ws.at<uint8_t>(xs), ws.at<int32_t>(xe), nullptr},
                                           st);
-    if (err == cudaSuccess) err = launch_mx4_gate(Mx4Gate{format, activation, xq, W1, hq, h, ldh, F}, st);
+    if (err == cudaSuccess) err = launch_mx4_gate(Mx4Gate{format, activation, xq, W1, hq, most, F}, st);
     if (err == cudaSuccess && nv)
-        err = launch_mx4_quantize(Mx4Quantize{format, DDGEMM_F32, false, T, F, h, ldh, ws.at<uint8_t>(hc), hl,
-                                              ws.at<uint8_t>(hs), ws.at<int32_t>(he), nullptr},
-                                  st);
+        err = launch_nvfp4_finish(most, T, F, ws.at<uint8_t>(hc), hl, ws.at<uint8_t>(hs), ws.at<int32_t>(he), st);
     if (err == cudaSuccess) err = launch_mx4_gemm(Mx4Gemm{format, type, hq, W2, 1.0f, y, ldy, true}, st);
     return status_of(err);
 }

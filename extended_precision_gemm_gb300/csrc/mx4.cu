@@ -154,6 +154,59 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) nvfp4_rows_kernel(const T* X, 
     }
 }
 
+// nvfp4 rows whose codes were made block by block with nvfp4_wide_step: from
+// the blocks' largest finite magnitudes (the sign bit marks a block that also
+// holds an infinity or a NaN; tiles * 4 values a row, 0 beyond K) the row's
+// exponent and the scales, one block of threads for a row.  Where a scale is
+// subnormal (the block's largest is below 2^-14.8 of the row's) the step has
+// fewer bits than the codes were made with: they are rounded again.
+__global__ void __launch_bounds__(256) nvfp4_finish_kernel(const float* most, int64_t K, uint8_t* codes, int64_t ldq,
+                                                           uint8_t* scales, int32_t* exponents) {
+    __shared__ uint32_t part[8];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int64_t row = blockIdx.x, tiles = mx4_scale_tiles(kNvfp4, K);
+    const uint4* src = reinterpret_cast<const uint4*>(most + row * tiles * 4);
+    uint32_t m = 0;
+    for (int64_t t = threadIdx.x; t < tiles; t += blockDim.x) {
+        const uint4 b = src[t];
+        m = max(max(m, b.x & 0x7fffffffu), max(max(b.y & 0x7fffffffu, b.z & 0x7fffffffu), b.w & 0x7fffffffu));
+    }
+    m = __reduce_max_sync(~0u, m);
+    if (lane == 0) part[warp] = m;
+    __syncthreads();
+    m = part[0];
+    for (int w = 1; w < warps; ++w) m = max(m, part[w]);
+    const int e = nvfp4_row_exponent(m);
+    if (threadIdx.x == 0) exponents[row] = e;
+    for (int64_t t = threadIdx.x; t < tiles; t += blockDim.x) {
+        const uint4 b = src[t];
+        const uint32_t bits[4] = {b.x, b.y, b.z, b.w};
+        uint32_t word = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t top = bits[i] & 0x7fffffffu;
+            const uint32_t byte = bits[i] >> 31 ? 127u : nvfp4_scale_byte(top, exp2_int(-e));
+            word |= byte << (8 * i);
+            const float was = nvfp4_wide_step(top), is = nvfp4_step(byte, e);
+            if (byte != 0u && byte != 127u && was != is) {
+                const float r = nvfp4_inverse(byte, is);
+                uint32_t* c = reinterpret_cast<uint32_t*>(codes + row * ldq + (t * 4 + i) * 8);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float y[8];
+                    e2m1_unpack8(c[q], y);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] = quotient(y[j] * was, is, r);
+                    c[q] = e2m1_pack8(y);
+                }
+            }
+        }
+        *reinterpret_cast<uint32_t*>(scales + mx4_scale_word(row, t, tiles)) = word;
+    }
+}
+
 // Two consecutive elements, as they lie in memory.
 template <typename T> struct Two;
 template <> struct Two<float> {
@@ -438,6 +491,14 @@ cudaError_t launch_mx4_quantize(const Mx4Quantize& q, cudaStream_t st) {
         case DDGEMM_BF16: return quantize_typed(q, static_cast<const __nv_bfloat16*>(q.X), st);
         default: return quantize_typed(q, static_cast<const __half*>(q.X), st);
     }
+}
+
+cudaError_t launch_nvfp4_finish(const float* most, int64_t rows, int64_t K, uint8_t* codes, int64_t ldq, uint8_t* scales,
+                                int32_t* exponents, cudaStream_t st) {
+    if (rows == 0 || K == 0) return cudaSuccess;
+    const int64_t tiles = mx4_scale_tiles(kNvfp4, K);
+    const unsigned threads = (unsigned)(tiles >= 256 ? 256 : (tiles + 31) / 32 * 32);
+    return launch_pdl(nvfp4_finish_kernel, dim3((unsigned)rows), dim3(threads), 0, st, most, K, codes, ldq, scales, exponents);
 }
 
 cudaError_t launch_mx4_dequantize(int fmt, int type, int64_t rows, int64_t K, const uint8_t* codes, int64_t ldq,

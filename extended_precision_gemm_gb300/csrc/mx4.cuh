@@ -114,6 +114,17 @@ __device__ __forceinline__ float nvfp4_inverse(uint32_t byte, float step) {
     return byte == 0u || byte == 127u ? 0.0f : __frcp_rn(step);
 }
 
+// The same step before the row's exponent is known.  A power of two commutes
+// with rounding to E4M3's four significant bits, so max / 6 rounded to four
+// bits is the step of every block whose scale is not subnormal, whatever e
+// (max a finite magnitude's bits; at least the least step there is, 2^-109).
+__device__ __forceinline__ float nvfp4_wide_step(uint32_t max_bits) {
+    if (max_bits == 0u) return 0.0f;
+    uint32_t b = __float_as_uint(__fdiv_rn(__uint_as_float(max_bits), 6.0f));
+    b = (b + 0x7ffffu + (b >> 20 & 1u)) & ~0xfffffu;
+    return fmaxf(__uint_as_float(b), exp2_int(-109));
+}
+
 // y / s with r = 1 / s correctly rounded: one residual correction of y * r
 // gives the correctly rounded quotient (Markstein's theorem), and rounding
 // that to E2M1 is the same as rounding the exact quotient: |y - t s| is at

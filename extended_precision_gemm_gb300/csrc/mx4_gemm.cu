@@ -58,18 +58,40 @@ struct EpiScale {
     }
 };
 
-// h = act(g) * u, both in 32 bits, from 32 columns of g and 32 of u in turn.
-// mxfp4: a thread holds a whole block of 32 of its row and writes its codes
-// and scale; the last tile also clears the scales of the padding of k.
-// nvfp4: h in 32 bits, for the row's exponent is not known yet.
+// A block of hidden values: 16 of a thread's 32 (nvfp4), codes made before the
+// row's exponent is known; the largest finite magnitude, marked by the sign bit
+// if the block holds an infinity or a NaN.
+__device__ __forceinline__ uint32_t nonfinite_mark(uint32_t bits) { return bits >= kInfBits ? 0x80000000u : 0u; }
+__device__ __forceinline__ float nvfp4_hidden_block(const float* h, uint32_t (&w)[2]) {
+    uint32_t m = 0, mark = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t b = __float_as_uint(h[i]) & 0x7fffffffu;
+        mark |= nonfinite_mark(b);
+        m = max(m, b < kInfBits ? b : 0u);
+    }
+    const float s = nvfp4_wide_step(m), r = s > 0.0f ? __frcp_rn(s) : 0.0f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = quotient(h[k * 8 + i], s, r);
+        w[k] = e2m1_pack8(y);
+    }
+    return __uint_as_float(m | mark);
+}
+
+// h = act(g) * u, both in 32 bits, from 32 columns of g and 32 of u in turn:
+// a thread holds 32 hidden values of its row, whole blocks of either format.
+// The last tile also clears the padding of k.
 template <int KIND, int NT_>
 struct EpiGate4 {
     static constexpr int NT = NT_, GROUPS = NT / 64;
     uint8_t *codes, *scales;
-    float* h;
-    int64_t ld;      // bytes of a row of codes (mxfp4), elements of a row of h (nvfp4)
+    float* most;  // nvfp4: instead of the scales
+    int64_t ld;   // bytes of a row of codes
     int64_t M, F;
-    int nt;          // n tiles
+    int nt;       // n tiles
     const int32_t *e, *f;
     int act;
     template <class Release>
@@ -84,7 +106,6 @@ struct EpiGate4 {
         for (int i = 0; i < 32; ++i) u[i] = __uint_as_float(raw[i]);
         release();
         const int64_t c = (int64_t)n * (NT / 2) + group * 32;
-        float hv[32];
         if (KIND == kKindNv) {
             const int64_t wc = (int64_t)n * NT + group * 64, W = round_up(F, 32) * 2;
             const int er = row < M ? e[row] : 0;
@@ -92,7 +113,10 @@ struct EpiGate4 {
             scale_columns(u, er, column_exponent(f, wc + 32, W, lane));
         }
         if (row >= M) return;
+        constexpr int FMT = KIND == kKindMx ? kMxfp4 : kNvfp4;
+        const int64_t tiles = mx4_scale_tiles(FMT, F);
         if (c < F) {
+            float hv[32];
             with_activation(act, [&](auto tag) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
@@ -101,32 +125,38 @@ struct EpiGate4 {
                     hv[i] = c + i < F ? a * u[i] : 0.0f;  // rows that fill up W take no part
                 }
             });
-        }
-        if (KIND == kKindNv) {
-            if (c < F) store_row(h + row * ld + c, hv);  // ld: F rounded up to 64
-            return;
-        }
-        const int64_t tiles = mx4_scale_tiles(kMxfp4, F);
-        if (c < F) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(hv[i]) & 0x7fffffffu);
-            const uint32_t byte = mxfp4_scale_byte(m);
-            const float inv = mxfp4_inverse(byte);
             uint32_t w[4];
+            if (KIND == kKindMx) {
+                uint32_t m = 0;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float y[8];
+                for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(hv[i]) & 0x7fffffffu);
+                const uint32_t byte = mxfp4_scale_byte(m);
+                const float inv = mxfp4_inverse(byte);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = hv[k * 8 + i] * inv;
-                w[k] = e2m1_pack8(y);
+                for (int k = 0; k < 4; ++k) {
+                    float y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = hv[k * 8 + i] * inv;
+                    w[k] = e2m1_pack8(y);
+                }
+                const int64_t b = c / 32;
+                scales[mx4_scale_word(row, b / 4, tiles) + b % 4] = (uint8_t)byte;
+            } else {
+                float2 m;
+                uint32_t lo[2], hi[2];
+                m.x = nvfp4_hidden_block(hv, lo);
+                m.y = nvfp4_hidden_block(hv + 16, hi);
+                w[0] = lo[0], w[1] = lo[1], w[2] = hi[0], w[3] = hi[1];
+                *reinterpret_cast<float2*>(most + row * tiles * 4 + c / 16) = m;
             }
             *reinterpret_cast<uint4*>(codes + row * ld + c / 2) = make_uint4(w[0], w[1], w[2], w[3]);
-            const int64_t b = c / 32;
-            scales[mx4_scale_word(row, b / 4, tiles) + b % 4] = (uint8_t)byte;
         }
-        if (n == nt - 1 && group == GROUPS - 1)
-            for (int64_t b = (F + 31) / 32; b < tiles * 4; ++b) scales[mx4_scale_word(row, b / 4, tiles) + b % 4] = 0;
+        if (n == nt - 1 && group == GROUPS - 1) {
+            if (KIND == kKindMx)
+                for (int64_t b = (F + 31) / 32; b < tiles * 4; ++b) scales[mx4_scale_word(row, b / 4, tiles) + b % 4] = 0;
+            else
+                for (int64_t b = (F + 31) / 32 * 2; b < tiles * 4; ++b) most[row * tiles * 4 + b] = 0.0f;
+        }
     }
 };
 
@@ -151,12 +181,12 @@ template <int KIND>
 struct EpiSplitGate4 {
     static constexpr int UNITS = 2;
     uint8_t *codes, *scales;
-    float* h;
+    float* most;
     int64_t ld, F;
     const int32_t *e, *f;
     int act;
     __device__ __forceinline__ void emit(float g, float u, int64_t m, int unit, int lane, int tile) const {
-        const int64_t b = (int64_t)tile * 2 + unit, n = b * 32 + lane;  // block of 32 hidden values
+        const int64_t b = (int64_t)tile * 2 + unit, n = b * 32 + lane;  // 32 hidden values
         if (b * 32 >= F) return;
         if (KIND == kKindNv) {
             const int er = e[m];
@@ -166,22 +196,37 @@ struct EpiSplitGate4 {
         float a = 0.0f, da;
         with_activation(act, [&](auto tag) { activation<decltype(tag)::value, false>(g, a, da); });
         const float hv = n < F ? a * u : 0.0f;  // rows that fill up W take no part
-        if (KIND == kKindNv) {
-            if (n < F) h[m * ld + n] = hv;
-            return;
+        const uint32_t bits = __float_as_uint(hv) & 0x7fffffffu;
+        constexpr int FMT = KIND == kKindMx ? kMxfp4 : kNvfp4;
+        const int64_t tiles = mx4_scale_tiles(FMT, F);
+        const bool last = b * 32 + 32 >= F;
+        float q;
+        if (KIND == kKindMx) {
+            const uint32_t byte = mxfp4_scale_byte(__reduce_max_sync(~0u, bits));
+            q = hv * mxfp4_inverse(byte);
+            if (lane == 0) {
+                scales[mx4_scale_word(m, b / 4, tiles) + b % 4] = (uint8_t)byte;
+                if (last)  // the padding of k
+                    for (int64_t p = b + 1; p < tiles * 4; ++p) scales[mx4_scale_word(m, p / 4, tiles) + p % 4] = 0;
+            }
+        } else {
+            uint32_t top = bits < kInfBits ? bits : 0u, mark = nonfinite_mark(bits);
+#pragma unroll
+            for (int d = 1; d < 16; d *= 2) {  // of 16 lanes
+                top = max(top, __shfl_xor_sync(~0u, top, d));
+                mark |= __shfl_xor_sync(~0u, mark, d);
+            }
+            const float s = nvfp4_wide_step(top), r = s > 0.0f ? __frcp_rn(s) : 0.0f;
+            q = quotient(hv, s, r);
+            float* row = most + m * tiles * 4;
+            if (lane % 16 == 0) row[b * 2 + lane / 16] = __uint_as_float(top | mark);
+            if (last)
+                for (int64_t p = b * 2 + 2 + lane; p < tiles * 4; p += 32) row[p] = 0.0f;
         }
-        const uint32_t byte = mxfp4_scale_byte(__reduce_max_sync(~0u, __float_as_uint(hv) & 0x7fffffffu));
-        const float q = hv * mxfp4_inverse(byte);
         float y[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(~0u, q, (lane & 3) * 8 + i);
         if (lane < 4) *reinterpret_cast<uint32_t*>(codes + m * ld + b * 16 + lane * 4) = e2m1_pack8(y);
-        const int64_t tiles = mx4_scale_tiles(kMxfp4, F);
-        if (lane == 0) {
-            scales[mx4_scale_word(m, b / 4, tiles) + b % 4] = (uint8_t)byte;
-            if (n + 32 >= F)  // the last block: the padding of k
-                for (int64_t p = b + 1; p < tiles * 4; ++p) scales[mx4_scale_word(m, p / 4, tiles) + p % 4] = 0;
-        }
     }
 };
 
@@ -283,15 +328,15 @@ namespace {
 template <int KIND>
 cudaError_t gate_kind(const Mx4Gate& g, cudaStream_t st) {
     uint8_t *codes = const_cast<uint8_t*>(g.hq.codes), *scales = const_cast<uint8_t*>(g.hq.scales);
-    const int64_t ld = KIND == kKindMx ? g.hq.ldq : g.ldh;
+    const int64_t ld = g.hq.ldq;
     if (g.x.rows <= kSplitTokens4)
         return split4<KIND>(g.x, g.W, true,  // x was quantised by the launch before, which waited for all before it
-                            EpiSplitGate4<KIND>{codes, scales, g.h, ld, g.F, g.x.exponents, g.W.exponents, g.act}, st);
+                            EpiSplitGate4<KIND>{codes, scales, g.most, ld, g.F, g.x.exponents, g.W.exponents, g.act}, st);
     const auto nt = [&](int n) { return (int)((g.W.rows + n - 1) / n); };
     if (narrow4(g.x, g.W))
-        return product4<KIND>(g.x, g.W, EpiGate4<KIND, 128>{codes, scales, g.h, ld, g.x.rows, g.F, nt(128), g.x.exponents,
+        return product4<KIND>(g.x, g.W, EpiGate4<KIND, 128>{codes, scales, g.most, ld, g.x.rows, g.F, nt(128), g.x.exponents,
                                                             g.W.exponents, g.act}, st);
-    return product4<KIND>(g.x, g.W, EpiGate4<KIND, 192>{codes, scales, g.h, ld, g.x.rows, g.F, nt(192), g.x.exponents,
+    return product4<KIND>(g.x, g.W, EpiGate4<KIND, 192>{codes, scales, g.most, ld, g.x.rows, g.F, nt(192), g.x.exponents,
                                                         g.W.exponents, g.act}, st);
 }
 

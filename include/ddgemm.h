@@ -785,8 +785,10 @@ ddgemm_status dd_ff_gated_backward(int type, int64_t T, int64_t D, int64_t F, co
 
 /*
  * The block on 4-bit operands, for serving: x (T x D, of `type`) is quantised
- * along D, h along F (from its 32-bit values), both products run as
- * dd_mx4_gemm, y is of `type`.  W_in holds Wg and Wu in turn, 32 rows of Wg
+ * along D, h along F from its 32-bit values (nvfp4: in blocks whose scale is
+ * subnormal, the largest value below 2^-14.8 of the row's, it is rounded to
+ * E2M1 with a step of four bits first, then with the scale), both products run
+ * as dd_mx4_gemm, y is of `type`.  W_in holds Wg and Wu in turn, 32 rows of Wg
  * then the same 32 of Wu, the last groups filled up with rows that take no
  * part: 2 * (F rounded up to 32) rows of length D.  W_out is Wd: D rows of length F.
  */

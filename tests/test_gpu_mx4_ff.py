@@ -136,3 +136,35 @@ def test_rows_that_fill_up_the_last_group_take_no_part(T, fmt):
     w_in.scales[torch.tensor(at, device="cuda")] = 255 if fmt == "mxfp4" else 127
     w_in.codes[torch.tensor(rows, device="cuda")] = 0x55
     assert torch.equal(ddg.mx4_ff_gated(x, w_in, w_out), want)
+
+
+@pytest.mark.parametrize("T", (2, 140))
+def test_hidden_blocks_far_below_the_row(T):
+    """nvfp4 blocks of hidden values 2^-4 to 2^-40 of the row's largest: scales
+    that are normal, subnormal and the least one.  Below 2^-14.8 a value may be
+    off by a further step of its block, at most 2^-18 of the row's largest (the
+    scale's least bit is 2^-9 2^e, max > 1344 2^e, and codes are at most 2
+    apart); relu and powers of two keep everything else exact."""
+    torch = _torch()
+    D, F = 64, 320
+    rng = np.random.default_rng(7)
+    pick = lambda *s: rng.choice([-1.0, 1.0, 2.0, 0.5], s)  # noqa: E731
+    small = np.repeat(2.0 ** -np.array([0, 4, 9, 13, 14, 15, 17, 19, 24, 40] * 2)[: F // 16], 16)
+    wg, wu, wd = pick(F, D) / 8, pick(F, D) / 8 * small[:, None], pick(D, F)
+    x = pick(T, D)
+    t = [torch.from_numpy(v).float().cuda() for v in (x, wg, wu, wd)]
+    w_in, w_out = ddg.mx4_ff_weights(*t[1:], "nvfp4")
+    y = ddg.mx4_ff_gated(t[0], w_in, w_out, act="relu").double().cpu().numpy()
+    both = ddg.mx4_dequantize(w_in, torch.float32).double().cpu().numpy().reshape(-1, 2, 32, D)
+    vg, vu = both[:, 0].reshape(-1, D)[:F], both[:, 1].reshape(-1, D)[:F]
+    vd = ddg.mx4_dequantize(w_out, torch.float32).double().cpu().numpy()
+    xv = ddg.mx4_dequantize(ddg.mx4_quantize(t[0], "nvfp4"), torch.float32).double().cpu().numpy()
+    h = np.maximum(xv @ vg.T, 0) * (xv @ vu.T)
+    e = 2.0**-20 * (np.abs(xv) @ np.abs(vg).T) * (np.abs(xv) @ np.abs(vu).T)
+    q, worst = hidden_span(h, e, "nvfp4")
+    top = np.abs(h).max(axis=1, keepdims=True)
+    assert ((np.abs(h) < 2.0**-15 * top) & (h != 0)).any()
+    worst = worst + np.where(np.abs(h) < 2.0**-14 * top, 2.0**-18 * top, 0.0)
+    want = q @ vd.T
+    room = worst @ np.abs(vd).T + 2.0**-18 * (np.abs(q) @ np.abs(vd).T)
+    assert (np.abs(y - want) <= room).all(), (np.abs(y - want) / room).max()
