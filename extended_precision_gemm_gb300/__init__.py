@@ -139,6 +139,7 @@ _SIGNATURES = {
                      ctypes.c_size_t, _ptr], _int),
     "dd_ff_gated_backward": ([_int, _i64, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64,
                               _ptr, ctypes.c_size_t, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr], _int),
+    "dd_call_packed": ([_int, ctypes.c_char_p], _int),
 }
 
 

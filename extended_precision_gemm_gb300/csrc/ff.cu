@@ -332,7 +332,7 @@ TileArgs tile_args(int64_t M, int64_t N, int64_t per_tile, int64_t K, int segs) 
 
 int64_t pair_tiles(int64_t M, int64_t N, int64_t per_tile) { return (M + 255) / 256 * ((N + per_tile - 1) / per_tile); }
 
-constexpr double kNarrow16 = 0.6;  // see narrow_tiles
+constexpr double kNarrow16 = 0.6;  // 128 columns for 256: 783 us against 683 for the forward of 4096 x 4096 x 12288
 bool narrow16(int64_t M, int64_t N, int64_t wide) {
     return narrow_tiles(pair_tiles(M, N, wide), pair_tiles(M, N, wide / 2), kNarrow16);
 }

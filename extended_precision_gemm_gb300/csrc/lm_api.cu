@@ -3,6 +3,7 @@
 // workspaces, launch sequences.
 #include <algorithm>
 #include <cstdint>
+#include <cstring>
 
 #include "launch.cuh"
 #include "mx4.cuh"
@@ -157,6 +158,32 @@ struct SavedLayout {
         total = off_eb + round_up(T * ld / 32 * bytes, kAlign);
     }
 };
+
+// Arguments packed as 64-bit words (of any alignment).
+class Words {
+public:
+    explicit Words(const void* p) : p_(static_cast<const char*>(p)) {}
+    template <typename T> T number(int i) const { return (T)word(i); }
+    template <typename T> T* pointer(int i) const { return reinterpret_cast<T*>((uintptr_t)word(i)); }
+    double real(int i) const {
+        double v;
+        memcpy(&v, p_ + 8 * i, 8);
+        return v;
+    }
+
+private:
+    int64_t word(int i) const {
+        int64_t v;
+        memcpy(&v, p_ + 8 * i, 8);
+        return v;
+    }
+    const char* p_;
+};
+// formats, types and flags are small: anything else is no valid one
+template <> int Words::number<int>(int i) const {
+    const int64_t v = word(i);
+    return v >= 0 && v < (1 << 30) ? (int)v : -1;
+}
 
 }  // namespace
 
@@ -365,6 +392,55 @@ ddgemm_status dd_mx4_ff_gated(int format, int type, int activation, int64_t T, i
         err = launch_nvfp4_finish(most, T, F, ws.at<uint8_t>(hc), hl, ws.at<uint8_t>(hs), ws.at<int32_t>(he), st);
     if (err == cudaSuccess) err = launch_mx4_gemm(Mx4Gemm{format, type, hq, W2, 1.0f, y, ldy, true}, st);
     return status_of(err);
+}
+
+ddgemm_status dd_call_packed(int call, const void* words) {
+    if (words == nullptr) return DDGEMM_ERR_INVALID_ARG;
+    const Words w(words);
+    switch (call) {
+        case DDGEMM_CALL_MX4_QUANTIZE:
+            return dd_mx4_quantize(w.number<int>(0), w.number<int>(1), w.number<int>(2), w.number<int64_t>(3),
+                                   w.number<int64_t>(4), w.pointer<const void>(5), w.number<int64_t>(6),
+                                   w.pointer<uint8_t>(7), w.number<int64_t>(8), w.pointer<uint8_t>(9),
+                                   w.pointer<int32_t>(10), w.pointer<void>(11));
+        case DDGEMM_CALL_MX4_DEQUANTIZE:
+            return dd_mx4_dequantize(w.number<int>(0), w.number<int>(1), w.number<int64_t>(2),
+                                     w.number<int64_t>(3), w.pointer<const uint8_t>(4), w.number<int64_t>(5),
+                                     w.pointer<const uint8_t>(6), w.pointer<const int32_t>(7), w.pointer<void>(8),
+                                     w.number<int64_t>(9), w.pointer<void>(10));
+        case DDGEMM_CALL_MX4_GEMM:
+            return dd_mx4_gemm(w.number<int>(0), w.number<int64_t>(1), w.number<int64_t>(2), w.number<int64_t>(3),
+                               w.pointer<const uint8_t>(4), w.number<int64_t>(5), w.pointer<const uint8_t>(6),
+                               w.pointer<const int32_t>(7), w.pointer<const uint8_t>(8), w.number<int64_t>(9),
+                               w.pointer<const uint8_t>(10), w.pointer<const int32_t>(11), (float)w.real(12),
+                               w.number<int>(13), w.pointer<void>(14), w.number<int64_t>(15), w.pointer<void>(16));
+        case DDGEMM_CALL_MX4_FF_GATED:
+            return dd_mx4_ff_gated(w.number<int>(0), w.number<int>(1), w.number<int>(2), w.number<int64_t>(3),
+                                   w.number<int64_t>(4), w.number<int64_t>(5), w.pointer<const void>(6),
+                                   w.number<int64_t>(7), w.pointer<const uint8_t>(8), w.number<int64_t>(9),
+                                   w.pointer<const uint8_t>(10), w.pointer<const int32_t>(11),
+                                   w.pointer<const uint8_t>(12), w.number<int64_t>(13),
+                                   w.pointer<const uint8_t>(14), w.pointer<const int32_t>(15), w.pointer<void>(16),
+                                   w.number<int64_t>(17), w.pointer<void>(18));
+        case DDGEMM_CALL_FF_GATED:
+            return dd_ff_gated(w.number<int>(0), w.number<int>(1), w.number<int64_t>(2), w.number<int64_t>(3),
+                               w.number<int64_t>(4), w.pointer<const void>(5), w.number<int64_t>(6),
+                               w.pointer<const void>(7), w.number<int64_t>(8), w.pointer<const void>(9),
+                               w.number<int64_t>(10), w.pointer<const void>(11), w.number<int64_t>(12),
+                               w.pointer<void>(13), w.number<int64_t>(14), w.pointer<void>(15),
+                               w.number<size_t>(16), w.pointer<void>(17));
+        case DDGEMM_CALL_FF_GATED_BACKWARD:
+            return dd_ff_gated_backward(w.number<int>(0), w.number<int64_t>(1), w.number<int64_t>(2),
+                                        w.number<int64_t>(3), w.pointer<const void>(4), w.number<int64_t>(5),
+                                        w.pointer<const void>(6), w.number<int64_t>(7), w.pointer<const void>(8),
+                                        w.number<int64_t>(9), w.pointer<const void>(10), w.number<int64_t>(11),
+                                        w.pointer<const void>(12), w.number<int64_t>(13),
+                                        w.pointer<const void>(14), w.number<size_t>(15), w.pointer<void>(16),
+                                        w.number<int64_t>(17), w.pointer<void>(18), w.number<int64_t>(19),
+                                        w.pointer<void>(20), w.number<int64_t>(21), w.pointer<void>(22),
+                                        w.number<int64_t>(23), w.pointer<void>(24));
+        default: return DDGEMM_ERR_INVALID_ARG;
+    }
 }
 
 }  // extern "C"

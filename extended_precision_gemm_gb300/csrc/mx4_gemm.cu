@@ -268,10 +268,10 @@ cudaError_t split4(const Mx4Matrix& x, const Mx4Matrix& W, bool early, const Epi
     memset(&maps, 0, sizeof(maps));
     cudaError_t err = map_codes(&maps.p[0], W, 128);
     if (err == cudaSuccess) err = map_codes(&maps.q, x, split_nq(x.rows));
-    if (err == cudaSuccess) err = map_scales(&maps.sp, FMT, W);
-    if (err == cudaSuccess) err = map_scales(&maps.sq, FMT, x);
     if (err != cudaSuccess) return err;
     SplitArgs g = {};
+    g.sp = W.scales;
+    g.sq = x.scales;
     g.nt = (int)((W.rows + 127) / 128);
     g.nk = (int)((x.K + MX4_TILE_K - 1) / MX4_TILE_K);
     g.last_steps = (int)((x.K - (int64_t)(g.nk - 1) * MX4_TILE_K + 63) / 64);
@@ -283,7 +283,7 @@ cudaError_t split4(const Mx4Matrix& x, const Mx4Matrix& W, bool early, const Epi
 
 int64_t pair_tiles(const Mx4Matrix& A, const Mx4Matrix& B, int nt) { return (A.rows + 255) / 256 * ((B.rows + nt - 1) / nt); }
 
-constexpr double kNarrow4 = 0.75;  // see narrow_tiles
+constexpr double kNarrow4 = 0.78;  // 128 columns for 192: 195 us against 166 for 8192^3 nvfp4
 bool narrow4(const Mx4Matrix& A, const Mx4Matrix& B) {
     return narrow_tiles(pair_tiles(A, B, 192), pair_tiles(A, B, 128), kNarrow4);
 }

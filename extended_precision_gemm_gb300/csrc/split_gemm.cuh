@@ -44,7 +44,7 @@ struct SplitShape {
 };
 
 struct SplitMaps {
-    CUtensorMap p[2], q, sp, sq;  // weights (gated 16-bit: Wg and Wu, 64 rows each), tokens, scales
+    CUtensorMap p[2], q;  // weights (gated 16-bit: Wg and Wu, 64 rows each), tokens
 };
 
 struct SplitArgs {
@@ -52,6 +52,7 @@ struct SplitArgs {
     int nk, per;       // stages along k, and of one CTA
     int last_steps;    // MMAs in the last stage
     int tiles_k;       // 4-bit kinds: scale tiles in a row of 128
+    const uint8_t *sp, *sq;  // scales of the weights and of the tokens
     int splits;        // CTAs of a cluster
     int early;         // the weights may be read before the wait
     int64_t M;         // tokens
@@ -97,7 +98,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
         } else {
             tma_load_2d(dst, &maps.p[0], kb * ROW, nt * 128, bar);
         }
-        if (F4) tma_load_2d(dst + S::P_BYTES + S::Q_BYTES, &maps.sp, 0, nt * g.tiles_k + kb * S::SCALE_TILES, bar);
+        if (F4)  // tiles of scales lie one after the other along k
+            bulk_load_at(dst + S::P_BYTES + S::Q_BYTES, g.sp + ((int64_t)nt * g.tiles_k + kb * S::SCALE_TILES) * 512,
+                         S::SCALE_BYTES, bar);
     };
     const int ahead = g.early ? min(count, STAGES) : 0;
     if (warp == 0) {
@@ -146,8 +149,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
                 const int kb = k0 + i;
                 tma_load_2d(dst + S::P_BYTES, &maps.q, kb * ROW, mt * NQ, bar);
                 if (F4)
-                    tma_load_2d(dst + S::P_BYTES + S::Q_BYTES + S::SCALE_BYTES, &maps.sq, 0,
-                                mt * g.tiles_k + kb * S::SCALE_TILES, bar);  // mt > 0 only with 128 tokens
+                    bulk_load_at(dst + S::P_BYTES + S::Q_BYTES + S::SCALE_BYTES,  // mt > 0 only with 128 tokens
+                                 g.sq + ((int64_t)mt * g.tiles_k + kb * S::SCALE_TILES) * 512, S::SCALE_BYTES, bar);
             }
             __syncwarp();
             issued = max(issued, i + 1);

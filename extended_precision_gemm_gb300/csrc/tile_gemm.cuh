@@ -382,7 +382,7 @@ cudaError_t reset_tile_timeouts(unsigned int* count) {
 }
 
 // Tiles of 128 columns instead of `wide` (256 or 192) where the pairs' rounds
-// over the narrow ones are shorter: a narrow tile takes about NARROWCOST of a wide
+// over the narrow ones are shorter: a narrow tile takes `narrow_cost` of a wide
 // one's time, more than its share (its rows of A are read for fewer columns).
 inline bool narrow_tiles(int64_t wide_tiles, int64_t narrow_count, double narrow_cost) {
     const int64_t pairs = std::max(1, tile_sms() / 2);

@@ -148,6 +148,14 @@ __device__ __forceinline__ void tma_load_2d_group(uint32_t dst, const void* tmap
         : "memory");
 }
 
+// Plain copy of `bytes` (a multiple of 16, both sides 16-byte aligned) into this
+// CTA's shared memory.
+__device__ __forceinline__ void bulk_load_at(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 // The box at (x, y) into L2 only.  Safe before the wait for earlier work on the
 // stream: whoever writes the box later writes it in L2 as well.
 __device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int x, int y) {

@@ -13,6 +13,8 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
+import struct
 
 import extended_precision_gemm_gb300 as _ddg
 
@@ -44,8 +46,20 @@ def _stream(stream, t):
     return _torch().cuda.current_stream(t.device).cuda_stream
 
 
+# dd_call_packed's number of an entry point, and how its arguments are packed
+_PACKED = {
+    "dd_mx4_quantize": (0, struct.Struct("=12q").pack),
+    "dd_mx4_dequantize": (1, struct.Struct("=11q").pack),
+    "dd_mx4_gemm": (2, struct.Struct("=12qd4q").pack),
+    "dd_mx4_ff_gated": (3, struct.Struct("=19q").pack),
+    "dd_ff_gated": (4, struct.Struct("=18q").pack),
+    "dd_ff_gated_backward": (5, struct.Struct("=25q").pack),
+}
+
+
 def _call(name, *args):
-    status = getattr(_ddg._lib or _ddg.load(), name)(*args)
+    call, pack = _PACKED[name]
+    status = (_ddg._lib or _ddg.load()).dd_call_packed(call, pack(*args))
     if status != 0:
         raise _ddg.DDGemmError(name, status)
 
@@ -131,45 +145,61 @@ class MX4:
         return (self.rows, self.k)
 
     def _args(self, name):
-        """Format, pointers and leading dimension, checked."""
+        """(device, format, codes, leading dimension, scales, exponents), checked;
+        the one test that a sound matrix passes comes first, the reasons after."""
         if _types is None:
             _torch()
+        c, s, e, rows, k = self.codes, self.scales, self.exponents, self.rows, self.k
+        fmt = MX4_FORMATS.get(self.fmt)
+        if fmt is not None and isinstance(c, _Tensor) and isinstance(s, _Tensor):
+            shape, stride, device = c.shape, c.stride(), c.get_device()
+            width = -(-k // 32) * 16
+            if (len(shape) == 2 and c.dtype is _uint8 and s.dtype is _uint8 and device >= 0 and s.get_device() == device
+                    and shape[0] == rows and shape[1] >= width and (stride[1] == 1 or rows == 0 or shape[1] <= 1)
+                    and s.numel() >= _scale_bytes(fmt, rows, k) and s.is_contiguous()):
+                ld = stride[0] if rows > 1 else -(-shape[1] // 16) * 16
+                if fmt == 0:
+                    return device, 0, c.data_ptr(), ld, s.data_ptr(), 0
+                if (isinstance(e, _Tensor) and e.dtype is _int32 and e.get_device() == device and e.numel() >= rows
+                        and e.is_contiguous()):
+                    return device, 1, c.data_ptr(), ld, s.data_ptr(), e.data_ptr()
+        self._refuse(name)
+
+    def _refuse(self, name):
+        """Raises for what _args found wrong."""
         fmt = _lookup(MX4_FORMATS, self.fmt, "fmt")
         c, s, e, rows = self.codes, self.scales, self.exponents, self.rows
         width, scale_bytes = _sizes(fmt, rows, self.k)
         if not isinstance(c, _Tensor) or c.dtype != _uint8 or c.dim() != 2 or not c.is_cuda:
             raise TypeError(f"{name}.codes must be a 2-D uint8 CUDA tensor")
-        have, bytes_ = c.shape
-        ld, unit = c.stride()
-        if have != rows or bytes_ < width or (bytes_ > 1 and rows > 0 and unit != 1):
+        if c.shape[0] != rows or c.shape[1] < width or c.stride(1) != 1:
             raise ValueError(f"{name}.codes must be {rows} rows of at least {width} bytes")
         if not isinstance(s, _Tensor) or s.dtype != _uint8 or not s.is_cuda:
             raise TypeError(f"{name}.scales must be a uint8 CUDA tensor")
         if s.numel() < scale_bytes or not s.is_contiguous():
             raise ValueError(f"{name}.scales must hold {scale_bytes} contiguous bytes")
-        pointer = None
         if fmt == 1:
             if not isinstance(e, _Tensor) or e.dtype != _int32 or not e.is_cuda:
                 raise TypeError(f"{name}.exponents must be an int32 CUDA tensor")
             if e.numel() < rows or not e.is_contiguous():
                 raise ValueError(f"{name}.exponents must hold {rows} contiguous values")
-            _same_device(c, s, e)
-            pointer = e.data_ptr()
-        else:
-            _same_device(c, s)
-        return fmt, c.data_ptr(), ld if rows > 1 else -(-bytes_ // 16) * 16, s.data_ptr(), pointer
+        raise ValueError(f"the tensors of {name} must be on the same device")
+
+
+def _scale_bytes(fmt, rows, k):
+    return -(-rows // 128) * -(-k // 256) * (1024 if fmt == 0 else 2048)
 
 
 def _sizes(fmt, rows, k):
     """dd_mx4_layout for sizes that a tensor can have."""
-    per_k = 8 if fmt == 0 else 16
-    return -(-k // 32) * 16, -(-rows // 128) * -(-k // 256) * per_k * 128
+    return -(-k // 32) * 16, _scale_bytes(fmt, rows, k)
 
 
 def mx4_layout(rows: int, k: int, fmt: str = "mxfp4"):
     """(bytes of a row of codes, bytes of all scales) of a rows x k matrix."""
     width, scales = ctypes.c_int64(), ctypes.c_int64()
-    _call("dd_mx4_layout", _lookup(MX4_FORMATS, fmt, "fmt"), rows, k, ctypes.byref(width), ctypes.byref(scales))
+    _ddg._check("dd_mx4_layout", _ddg.load().dd_mx4_layout(_lookup(MX4_FORMATS, fmt, "fmt"), rows, k,
+                                                          ctypes.byref(width), ctypes.byref(scales)))
     return width.value, scales.value
 
 
@@ -189,11 +219,11 @@ def mx4_quantize(x, fmt: str = "mxfp4", cols: bool = False, out: MX4 | None = No
         if stream is not None:
             for part in (codes, scales) + ((exponents,) if f else ()):
                 part.record_stream(stream)
-        args = codes.data_ptr(), width, scales.data_ptr(), exponents.data_ptr() if f else None
+        args = codes.data_ptr(), width, scales.data_ptr(), exponents.data_ptr() if f else 0
     else:
         if out.shape != (rows, k) or out.fmt != fmt:
             raise ValueError(f"out must be a {rows} x {k} {fmt} matrix")
-        args = out._args("out")[1:]
+        args = out._args("out")[2:]
         _same_device(x, out.codes)
     _call("dd_mx4_quantize", f, t, int(cols), rows, k, x.data_ptr(), ld, *args, _stream(stream, x))
     return out
@@ -205,7 +235,7 @@ def mx4_dequantize(q: MX4, dtype=None, out=None, stream=None):
     t = _type(dtype, "dtype")
     args = q._args("q")
     out, ld = _like(out, (q.rows, q.k), dtype, q.codes, "out", stream)
-    _call("dd_mx4_dequantize", args[0], t, q.rows, q.k, *args[1:], out.data_ptr(), ld, _stream(stream, out))
+    _call("dd_mx4_dequantize", args[1], t, q.rows, q.k, *args[2:], out.data_ptr(), ld, _stream(stream, out))
     return out
 
 
@@ -226,11 +256,12 @@ def mx4_gemm(a: MX4, b: MX4, dtype=None, out=None, alpha: float = 1.0, stream=No
         raise ValueError("a and b must share format and k")
     dtype = dtype or (out.dtype if out is not None else _torch().bfloat16)
     t = _type(dtype, "dtype")
-    left, right = a._args("a"), b._args("b")
-    _same_device(a.codes, b.codes)
+    device, fmt, *left = a._args("a")
+    other, _, *right = b._args("b")
+    if device != other:
+        raise ValueError("a and b must be on the same device")
     out, ld = _like(out, (a.rows, b.rows), dtype, a.codes, "out", stream)
-    _call("dd_mx4_gemm", left[0], a.rows, b.rows, a.k, *left[1:], *right[1:], alpha, t, out.data_ptr(), ld,
-          _stream(stream, out))
+    _call("dd_mx4_gemm", fmt, a.rows, b.rows, a.k, *left, *right, alpha, t, out.data_ptr(), ld, _stream(stream, out))
     return out
 
 
@@ -252,8 +283,13 @@ def _ff_shapes(x, Wg, Wu, Wd):
 
 def ff_gated_saved_size(T: int, F: int, dtype) -> int:
     """Bytes that ff_gated(save=True) keeps for the backward pass."""
+    return _saved_size(T, F, _type(dtype, "dtype", sixteen=True))
+
+
+@functools.lru_cache(maxsize=64)
+def _saved_size(T, F, code):
     n = ctypes.c_size_t()
-    _call("dd_ff_gated_saved_size", _type(dtype, "dtype", sixteen=True), T, F, ctypes.byref(n))
+    _ddg._check("dd_ff_gated_saved_size", _ddg.load().dd_ff_gated_saved_size(code, T, F, ctypes.byref(n)))
     return n.value
 
 
@@ -265,11 +301,11 @@ def ff_gated(x, Wg, Wu, Wd, act: str = "silu", save: bool = False, out=None, str
     y, ldy = _like(out, (T, D), x.dtype, x, "out", stream)
     saved, n = None, 0
     if save:
-        n = ff_gated_saved_size(T, F, x.dtype)
+        n = _saved_size(T, F, code)
         saved = _empty(n, dtype=_uint8, device=x.device)
         if stream is not None:
             saved.record_stream(stream)
-    _call("dd_ff_gated", code, a, T, D, F, *operands, y.data_ptr(), ldy, saved.data_ptr() if n else None, n,
+    _call("dd_ff_gated", code, a, T, D, F, *operands, y.data_ptr(), ldy, saved.data_ptr() if n else 0, n,
           _stream(stream, x))
     return (y, saved) if save else y
 
@@ -285,15 +321,15 @@ def ff_gated_backward(dy, x, Wg, Wu, Wd, saved, dx=None, dWg=None, dWu=None, dWd
     if not isinstance(saved, _Tensor) or saved.dtype != _uint8 or not saved.is_cuda or not saved.is_contiguous():
         raise TypeError("saved must be the uint8 CUDA tensor that ff_gated returned")
     n = saved.numel()
-    if n != ff_gated_saved_size(T, F, x.dtype):
+    if n != _saved_size(T, F, code):
         raise ValueError("saved is of another T, F or type")
     _same_device(x, dy, saved)
     outs, args = [], []
     for name, o, shape, want in zip(("dx", "dWg", "dWu", "dWd"), (dx, dWg, dWu, dWd), ((T, D), (F, D), (F, D), (D, F)), need):
         o, ld = _like(o, shape, x.dtype, x, name, stream) if want else (None, shape[1] or 1)
         outs.append(o)
-        args += (o.data_ptr() if want else None, ld)
-    _call("dd_ff_gated_backward", code, T, D, F, dy.data_ptr(), lddy, *operands, saved.data_ptr() if n else None, n, *args,
+        args += (o.data_ptr() if want else 0, ld)
+    _call("dd_ff_gated_backward", code, T, D, F, dy.data_ptr(), lddy, *operands, saved.data_ptr() if n else 0, n, *args,
           _stream(stream, x))
     return tuple(outs)
 
@@ -325,9 +361,11 @@ def mx4_ff_gated(x, w_in: MX4, w_out: MX4, act: str = "silu", out=None, stream=N
     F = w_out.k
     if w_in.fmt != w_out.fmt or w_in.k != D or w_out.rows != D or w_in.rows != 2 * (-(-F // 32) * 32):
         raise ValueError("w_in must be 2 * (F rounded up to 32) x D and w_out D x F, of one format")
-    first, second = w_in._args("w_in"), w_out._args("w_out")
-    _same_device(x, w_in.codes, w_out.codes)
+    device, fmt, *first = w_in._args("w_in")
+    other, _, *second = w_out._args("w_out")
+    if not device == other == x.get_device():
+        raise ValueError("x and the weights must be on the same device")
     y, ldy = _like(out, (T, D), x.dtype, x, "out", stream)
-    _call("dd_mx4_ff_gated", first[0], t, a, T, D, F, x.data_ptr(), ldx, *first[1:], *second[1:], y.data_ptr(), ldy,
+    _call("dd_mx4_ff_gated", fmt, t, a, T, D, F, x.data_ptr(), ldx, *first, *second, y.data_ptr(), ldy,
           _stream(stream, x))
     return y

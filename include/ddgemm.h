@@ -798,6 +798,21 @@ ddgemm_status dd_mx4_ff_gated(int format, int type, int activation, int64_t T, i
                               const uint8_t* out_scales, const int32_t* out_exponents, void* y, int64_t ldy,
                               void* stream);
 
+/*
+ * One of the six entry points above with its arguments, in their order, as an
+ * array of 64-bit words (integers and pointers as they are, alpha as the bits
+ * of a double): for bindings to which every argument of a foreign call costs
+ * (19 of them take 2.0 us through Python's ctypes on the host of a GB300, a
+ * packed array 0.4 us).  An unknown `call` returns DDGEMM_ERR_INVALID_ARG.
+ */
+#define DDGEMM_CALL_MX4_QUANTIZE 0
+#define DDGEMM_CALL_MX4_DEQUANTIZE 1
+#define DDGEMM_CALL_MX4_GEMM 2
+#define DDGEMM_CALL_MX4_FF_GATED 3
+#define DDGEMM_CALL_FF_GATED 4
+#define DDGEMM_CALL_FF_GATED_BACKWARD 5
+ddgemm_status dd_call_packed(int call, const void* words);
+
 #ifdef __cplusplus
 }
 #endif

@@ -188,3 +188,23 @@ def test_binding_refusals():
     with pytest.raises(ddg.DDGemmError) as e:
         ddg.mx4_layout(-1, 4)
     assert e.value.status == 1
+
+
+def test_packed_calls_are_the_same_entry_points(lib):
+    """dd_call_packed refuses what the entry points refuse (each by an argument near its end), and unknown calls."""
+    import struct
+    assert lib.dd_call_packed(6, struct.pack("=12q", *[0] * 12)) == 1
+    assert lib.dd_call_packed(-1, struct.pack("=12q", *[0] * 12)) == 1
+    assert lib.dd_call_packed(0, None) == 1
+    a = [i << 40 for i in range(1, 9)]
+    quant = lambda e: struct.pack("=12q", 1, 1, 0, 8, 64, a[0], 64, a[1], 32, a[2], e, 0)  # noqa: E731
+    assert lib.dd_call_packed(0, quant(0)) == 1                                   # nvfp4 without exponents
+    assert lib.dd_call_packed(0, struct.pack("=12q", 1 << 40, 1, 0, 8, 64, a[0], 64, a[1], 32, a[2], a[3], 0)) == 1
+    assert lib.dd_call_packed(1, struct.pack("=11q", 0, 1, 8, 64, a[0], 32, a[1], 0, a[2], 63, 0)) == 1
+    gemm = lambda ldc: struct.pack("=12qd4q", 0, 8, 8, 64, a[0], 32, a[1], 0, a[2], 32, a[3], 0, 1.0, 1, a[4], ldc, 0)  # noqa: E731
+    assert lib.dd_call_packed(2, gemm(7)) == 1
+    assert lib.dd_call_packed(2, struct.pack("=12qd4q", 0, 0, 8, 64, 0, 32, 0, 0, 0, 32, 0, 0, 1.0, 1, 0, 8, 0)) == 0
+    assert lib.dd_call_packed(3, struct.pack("=19q", 0, 1, 0, 3, 64, 40, a[0], 64, a[1], 32, a[2], 0, a[3], 32, a[4], 0, a[5], 63, 0)) == 1
+    assert lib.dd_call_packed(4, struct.pack("=18q", 1, 0, 5, 8, 100, a[0], 8, a[1], 8, a[2], 8, a[3], 100, a[4], 8, a[5], 16, 0)) == 1
+    back = [1, 5, 8, 100, a[0], 8, a[1], 8, a[2], 8, a[3], 8, a[4], 100, a[5], 1 << 20, 0, 8, 0, 8, 0, 8, a[0], 100, 0]
+    assert lib.dd_call_packed(5, struct.pack("=25q", *back)) == 1                 # dWd over dy
