@@ -171,8 +171,8 @@ struct Mx4Matrix {
     int64_t rows, K;
 };
 // X (rows x K, or K x rows if cols) of type DDGEMM_F32 / _BF16 / _F16 into
-// codes, scales and (nvfp4) row exponents; column_max: `rows` words of
-// workspace, nvfp4 columns only.
+// codes, scales and (nvfp4) row exponents; most: a workspace of the largest
+// magnitude of every block, rows x 4 scale tiles, nvfp4 columns only.
 struct Mx4Quantize {
     int fmt, type;
     bool cols;
@@ -183,7 +183,7 @@ struct Mx4Quantize {
     int64_t ldq;
     uint8_t* scales;
     int32_t* exponents;
-    uint32_t* column_max;
+    float* most;
 };
 cudaError_t launch_mx4_quantize(const Mx4Quantize& q, cudaStream_t st);
 cudaError_t launch_mx4_dequantize(int fmt, int type, int64_t rows, int64_t K, const uint8_t* codes, int64_t ldq,

@@ -154,59 +154,6 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) nvfp4_rows_kernel(const T* X, 
     }
 }
 
-// nvfp4 rows whose codes were made block by block with nvfp4_wide_step: from
-// the blocks' largest finite magnitudes (the sign bit marks a block that also
-// holds an infinity or a NaN; tiles * 4 values a row, 0 beyond K) the row's
-// exponent and the scales, one block of threads for a row.  Where a scale is
-// subnormal (the block's largest is below 2^-14.8 of the row's) the step has
-// fewer bits than the codes were made with: they are rounded again.
-__global__ void __launch_bounds__(256) nvfp4_finish_kernel(const float* most, int64_t K, uint8_t* codes, int64_t ldq,
-                                                           uint8_t* scales, int32_t* exponents) {
-    __shared__ uint32_t part[8];
-    pdl_wait();
-    pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int64_t row = blockIdx.x, tiles = mx4_scale_tiles(kNvfp4, K);
-    const uint4* src = reinterpret_cast<const uint4*>(most + row * tiles * 4);
-    uint32_t m = 0;
-    for (int64_t t = threadIdx.x; t < tiles; t += blockDim.x) {
-        const uint4 b = src[t];
-        m = max(max(m, b.x & 0x7fffffffu), max(max(b.y & 0x7fffffffu, b.z & 0x7fffffffu), b.w & 0x7fffffffu));
-    }
-    m = __reduce_max_sync(~0u, m);
-    if (lane == 0) part[warp] = m;
-    __syncthreads();
-    m = part[0];
-    for (int w = 1; w < warps; ++w) m = max(m, part[w]);
-    const int e = nvfp4_row_exponent(m);
-    if (threadIdx.x == 0) exponents[row] = e;
-    for (int64_t t = threadIdx.x; t < tiles; t += blockDim.x) {
-        const uint4 b = src[t];
-        const uint32_t bits[4] = {b.x, b.y, b.z, b.w};
-        uint32_t word = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t top = bits[i] & 0x7fffffffu;
-            const uint32_t byte = bits[i] >> 31 ? 127u : nvfp4_scale_byte(top, exp2_int(-e));
-            word |= byte << (8 * i);
-            const float was = nvfp4_wide_step(top), is = nvfp4_step(byte, e);
-            if (byte != 0u && byte != 127u && was != is) {
-                const float r = nvfp4_inverse(byte, is);
-                uint32_t* c = reinterpret_cast<uint32_t*>(codes + row * ldq + (t * 4 + i) * 8);
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float y[8];
-                    e2m1_unpack8(c[q], y);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] = quotient(y[j] * was, is, r);
-                    c[q] = e2m1_pack8(y);
-                }
-            }
-        }
-        *reinterpret_cast<uint32_t*>(scales + mx4_scale_word(row, t, tiles)) = word;
-    }
-}
-
 // Two consecutive elements, as they lie in memory.
 template <typename T> struct Two;
 template <> struct Two<float> {
@@ -283,77 +230,49 @@ __device__ __forceinline__ void load_columns(const T* X, int64_t ldx, int64_t k,
     }
 }
 
-// Largest finite magnitude of each column of X (K x R), as bits, over 256
-// rows per block: 64 columns, 8 warps of 32 rows.
-template <typename T>
-__global__ void __launch_bounds__(256) column_max_kernel(const T* X, int64_t ldx, int64_t R, int64_t K, bool vec,
-                                                         uint32_t* most) {
-    __shared__ uint32_t part[8][64];
-    pdl_wait();
-    pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 64 + lane * 2, k0 = (int64_t)blockIdx.y * 256 + warp * 32;
-    uint32_t m0, m1;
-    typename Two<T>::raw raw[32];
-    load_columns<T, 32>(X, ldx, k0, c, K, R, vec, raw);
-    max_pair<T, 32, true>(raw, m0, m1);
-    part[warp][lane * 2] = m0;
-    part[warp][lane * 2 + 1] = m1;
-    __syncthreads();
-    if (threadIdx.x < 64 && (int64_t)blockIdx.x * 64 + threadIdx.x < R) {
-        uint32_t m = part[0][threadIdx.x];
-#pragma unroll
-        for (int w = 1; w < 8; ++w) m = max(m, part[w][threadIdx.x]);
-        if (m > 0) atomicMax(most + (int64_t)blockIdx.x * 64 + threadIdx.x, m);
-    }
-}
-
 // Columns of X (K x R) as rows of the result: a block takes 64 columns and 256
 // k.  Warp w reads rows 32 w .. + 31, a lane two columns of them, so a lane
 // holds whole blocks of k and needs no exchange for their maxima; codes and
 // scales go through shared memory (rows of 33 and 5 words: no bank conflicts)
-// and leave as whole 128-byte rows.  The blocks take k in descending order:
-// the maxima before read X upwards and leave its end in L2.
+// and leave as whole 128-byte rows.  X is read once in either format: nvfp4 codes
+// are made with nvfp4_wide_step, and the blocks' largest magnitudes go to `most`
+// for nvfp4_finish_kernel, which a pass over X for the columns' maxima ahead of
+// this one would replace at 0.25 bytes a value less written but 2 more read
+// (8192 x 16384 values: 102 us with that pass, 83 without).
 template <typename T, int FMT>
 __global__ void __launch_bounds__(256) mx4_columns_kernel(const T* X, int64_t ldx, int64_t R, int64_t K, bool vec,
-                                                          const uint32_t* most, uint8_t* codes, int64_t ldq,
-                                                          uint8_t* scales, int32_t* exponents) {
+                                                          uint8_t* codes, int64_t ldq, uint8_t* scales, float* most) {
     constexpr int BLOCK = mx4_block(FMT), WORDS = mx4_tiles_per_k(FMT);
     __shared__ uint32_t code[64][33];   // row p: column (p % 32) * 2 + p / 32 of the tile
-    __shared__ uint32_t scale[64][5];
+    __shared__ uint32_t scale[64][FMT == kMxfp4 ? 5 : 17];  // scale bytes, or largest magnitudes
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t r0 = (int64_t)blockIdx.x * 64, kt = gridDim.y - 1 - blockIdx.y;
+    const int64_t r0 = (int64_t)blockIdx.x * 64, kt = blockIdx.y;
     const int64_t c = r0 + lane * 2, k0 = kt * MX4_TILE_K + warp * 32;
     typename Two<T>::raw raw[32];
     load_columns<T, 32>(X, ldx, k0, c, K, R, vec, raw);
-    int e[2] = {0, 0};
-    if (FMT == kNvfp4) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            if (c + j < R) {
-                e[j] = nvfp4_row_exponent(most[c + j]);
-                if (kt == 0 && warp == 0) exponents[c + j] = e[j];
-            }
-    }
 #pragma unroll
     for (int b = 0; b < 32 / BLOCK; ++b) {
-        uint32_t m[2];
+        uint32_t m[2], mark[2] = {0, 0};
         max_pair<T, BLOCK, false>(raw + b * BLOCK, m[0], m[1]);
+        if (FMT == kNvfp4 && (m[0] >= kInfBits || m[1] >= kInfBits)) {  // rare: the finite ones alone
+            mark[0] = m[0] >= kInfBits ? 0x80000000u : 0u;
+            mark[1] = m[1] >= kInfBits ? 0x80000000u : 0u;
+            max_pair<T, BLOCK, true>(raw + b * BLOCK, m[0], m[1]);
+        }
         float s[2] = {0.0f, 0.0f}, r[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            uint32_t byte;
             if (FMT == kMxfp4) {
-                byte = mxfp4_scale_byte(m[j]);
+                const uint32_t byte = mxfp4_scale_byte(m[j]);
                 r[j] = mxfp4_inverse(byte);
+                reinterpret_cast<uint8_t*>(&scale[j * 32 + lane][0])[warp] = (uint8_t)byte;
             } else {
-                byte = nvfp4_scale_byte(m[j], exp2_int(-e[j]));
-                s[j] = nvfp4_step(byte, e[j]);
-                r[j] = nvfp4_inverse(byte, s[j]);
+                s[j] = nvfp4_wide_step(m[j]);
+                r[j] = s[j] > 0.0f ? __frcp_rn(s[j]) : 0.0f;
+                scale[j * 32 + lane][warp * 2 + b] = m[j] | mark[j];
             }
-            reinterpret_cast<uint8_t*>(&scale[j * 32 + lane][0])[warp * (32 / BLOCK) + b] = (uint8_t)byte;
         }
         const uint64_t rr = pack_pair(r[0], r[1]), ss = pack_pair(-s[0], -s[1]);
 #pragma unroll
@@ -382,10 +301,90 @@ __global__ void __launch_bounds__(256) mx4_columns_kernel(const T* X, int64_t ld
                 make_uint4(code[p][at * 4], code[p][at * 4 + 1], code[p][at * 4 + 2], code[p][at * 4 + 3]);
     }
     const int64_t tiles = mx4_scale_tiles(FMT, K);
-    if (threadIdx.x < 64 * WORDS) {
-        const int p = threadIdx.x % 64, w = threadIdx.x / 64;
+    if (FMT == kMxfp4) {
+        if (threadIdx.x < 64 * WORDS) {
+            const int p = threadIdx.x % 64, w = threadIdx.x / 64;
+            const int64_t row = r0 + p % 32 * 2 + p / 32;
+            if (row < R) *reinterpret_cast<uint32_t*>(scales + mx4_scale_word(row, kt * WORDS + w, tiles)) = scale[p][w];
+        }
+    } else {  // 16 magnitudes a row: 64 bytes, 4 threads a row
+        const int p = threadIdx.x / 4, at = threadIdx.x % 4 * 4;
         const int64_t row = r0 + p % 32 * 2 + p / 32;
-        if (row < R) *reinterpret_cast<uint32_t*>(scales + mx4_scale_word(row, kt * WORDS + w, tiles)) = scale[p][w];
+        if (row < R)
+            *reinterpret_cast<uint4*>(most + row * tiles * 4 + kt * 16 + at) =
+                make_uint4(scale[p][at], scale[p][at + 1], scale[p][at + 2], scale[p][at + 3]);
+    }
+}
+
+// nvfp4 rows whose codes were made block by block with nvfp4_wide_step: from
+// the blocks' largest finite magnitudes (the sign bit marks a block that also
+// holds an infinity or a NaN; tiles * 4 values a row, 0 beyond K) the row's
+// exponent and the scales, one block of threads for a row.  Where a scale is
+// subnormal (the block's largest is below 2^-14.8 of the row's) the step has
+// fewer bits than the codes were made with: they are made again, from the
+// values themselves (row i being column i of X) or, without X, from the codes.
+template <typename T>
+__device__ __forceinline__ void remake_codes(uint32_t word, uint4 b, int e, int64_t t, int64_t row, int64_t K, uint8_t* codes,
+                                          const T* X, int64_t ldx) {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t byte = word >> (8 * i) & 0xffu;
+        const uint32_t top = (i == 0 ? b.x : i == 1 ? b.y : i == 2 ? b.z : b.w) & 0x7fffffffu;
+        const float was = nvfp4_wide_step(top), is = nvfp4_step(byte, e);
+        if (byte == 0u || byte > 8u || was == is) continue;
+        const float r = nvfp4_inverse(byte, is);
+        uint32_t* c = reinterpret_cast<uint32_t*>(codes + (t * 4 + i) * 8);
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+            float y[8];
+            const int64_t k = (t * 4 + i) * 16 + q * 8;
+            e2m1_unpack8(c[q], y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float v = y[j] * was;
+                if (X != nullptr) v = k + j < K ? to_float<T>(X[(k + j) * ldx + row]) : 0.0f;
+                y[j] = quotient(v, is, r);
+            }
+            c[q] = e2m1_pack8(y);
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) nvfp4_finish_kernel(const float* most, int64_t K, uint8_t* codes, int64_t ldq,
+                                                           uint8_t* scales, int32_t* exponents, const T* X, int64_t ldx) {
+    __shared__ uint32_t part[8];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int64_t row = blockIdx.x, tiles = mx4_scale_tiles(kNvfp4, K);
+    const uint4* src = reinterpret_cast<const uint4*>(most) + row * tiles;
+    uint32_t m = 0;
+    for (int64_t t = threadIdx.x; t < tiles; t += blockDim.x) {
+        const uint4 b = src[t];
+        m = max(max(m, b.x & 0x7fffffffu), max(max(b.y & 0x7fffffffu, b.z & 0x7fffffffu), b.w & 0x7fffffffu));
+    }
+    m = __reduce_max_sync(~0u, m);
+    if (lane == 0) part[warp] = m;
+    __syncthreads();
+    m = part[0];
+    for (int w = 1; w < warps; ++w) m = max(m, part[w]);
+    const int e = nvfp4_row_exponent(m);
+    const float unit = exp2_int(-e);
+    if (threadIdx.x == 0) exponents[row] = e;
+    for (int64_t t = threadIdx.x; t < tiles; t += blockDim.x) {
+        const uint4 b = src[t];
+        const uint32_t bits[4] = {b.x, b.y, b.z, b.w};
+        uint32_t word = 0;
+        bool low = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t byte = bits[i] >> 31 ? 127u : nvfp4_scale_byte(bits[i], unit);
+            word |= byte << (8 * i);
+            low |= byte > 0u && byte <= 8u;  // 8: the least normal one, perhaps rounded up to
+        }
+        if (low) remake_codes(word, b, e, t, row, K, codes + row * ldq, X, ldx);
+        *reinterpret_cast<uint32_t*>(scales + mx4_scale_word(row, t, tiles)) = word;
     }
 }
 
@@ -440,6 +439,15 @@ __global__ void __launch_bounds__(QWARPS * 32) mx4_dequantize_kernel(const uint8
 }
 
 template <typename T>
+cudaError_t finish(const float* most, int64_t rows, int64_t K, uint8_t* codes, int64_t ldq, uint8_t* scales,
+                   int32_t* exponents, const T* X, int64_t ldx, cudaStream_t st) {
+    const int64_t tiles = mx4_scale_tiles(kNvfp4, K);
+    const unsigned threads = (unsigned)(tiles >= 256 ? 256 : (tiles + 31) / 32 * 32);
+    return launch_pdl(nvfp4_finish_kernel<T>, dim3((unsigned)rows), dim3(threads), 0, st, most, K, codes, ldq, scales,
+                      exponents, X, ldx);
+}
+
+template <typename T>
 cudaError_t quantize_typed(const Mx4Quantize& q, const T* X, cudaStream_t st) {
     const int64_t kts = (q.K + MX4_TILE_K - 1) / MX4_TILE_K;
     if (!q.cols) {
@@ -458,16 +466,13 @@ cudaError_t quantize_typed(const Mx4Quantize& q, const T* X, cudaStream_t st) {
     }
     const bool vec = (uintptr_t)X % (2 * sizeof(T)) == 0 && q.ldx % 2 == 0;
     const dim3 grid((unsigned)((q.rows + 63) / 64), (unsigned)kts);
-    if (q.fmt == kMxfp4)
-        return launch_pdl(mx4_columns_kernel<T, kMxfp4>, grid, dim3(256), 0, st, X, q.ldx, q.rows, q.K, vec,
-                          (const uint32_t*)nullptr, q.codes, q.ldq, q.scales, (int32_t*)nullptr);
-    cudaError_t err = cudaMemsetAsync(q.column_max, 0, (size_t)q.rows * 4, st);
-    if (err == cudaSuccess)
-        err = launch_pdl(column_max_kernel<T>, grid, dim3(256), 0, st, X, q.ldx, q.rows, q.K, vec, q.column_max);
-    if (err == cudaSuccess)
-        err = launch_pdl(mx4_columns_kernel<T, kNvfp4>, grid, dim3(256), 0, st, X, q.ldx, q.rows, q.K, vec,
-                         (const uint32_t*)q.column_max, q.codes, q.ldq, q.scales, q.exponents);
-    return err;
+    const cudaError_t err =
+        q.fmt == kMxfp4 ? launch_pdl(mx4_columns_kernel<T, kMxfp4>, grid, dim3(256), 0, st, X, q.ldx, q.rows, q.K, vec,
+                                     q.codes, q.ldq, q.scales, (float*)nullptr)
+                        : launch_pdl(mx4_columns_kernel<T, kNvfp4>, grid, dim3(256), 0, st, X, q.ldx, q.rows, q.K, vec,
+                                     q.codes, q.ldq, (uint8_t*)nullptr, q.most);
+    if (err != cudaSuccess || q.fmt == kMxfp4) return err;
+    return finish(q.most, q.rows, q.K, q.codes, q.ldq, q.scales, q.exponents, X, q.ldx, st);
 }
 
 template <typename T>
@@ -496,9 +501,7 @@ cudaError_t launch_mx4_quantize(const Mx4Quantize& q, cudaStream_t st) {
 cudaError_t launch_nvfp4_finish(const float* most, int64_t rows, int64_t K, uint8_t* codes, int64_t ldq, uint8_t* scales,
                                 int32_t* exponents, cudaStream_t st) {
     if (rows == 0 || K == 0) return cudaSuccess;
-    const int64_t tiles = mx4_scale_tiles(kNvfp4, K);
-    const unsigned threads = (unsigned)(tiles >= 256 ? 256 : (tiles + 31) / 32 * 32);
-    return launch_pdl(nvfp4_finish_kernel, dim3((unsigned)rows), dim3(threads), 0, st, most, K, codes, ldq, scales, exponents);
+    return finish<float>(most, rows, K, codes, ldq, scales, exponents, nullptr, 0, st);
 }
 
 cudaError_t launch_mx4_dequantize(int fmt, int type, int64_t rows, int64_t K, const uint8_t* codes, int64_t ldq,

@@ -88,16 +88,28 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
     return __half2float(__ushort_as_half((unsigned short)(h2 & 0xffffu)));
 }
 
+// y / s with r = 1 / s correctly rounded: one residual correction of y * r
+// gives the correctly rounded quotient (Markstein's theorem), and rounding
+// that to E2M1 is the same as rounding the exact quotient: |y - t s| is at
+// least one last place of y for every tie point t (3 bits) but a true tie.
+__device__ __forceinline__ float quotient(float y, float s, float r) {
+    const float q = y * r;
+    return fmaf(fmaf(-q, s, y), r, q);
+}
+
+__device__ __forceinline__ float sixth(float x) { return quotient(x, 6.0f, 1.0f / 6.0f); }
+
 // The E4M3 byte of an nvfp4 block: max / (6 * 2^e) rounded to nearest, at
 // least the smallest scale for a block that is not zero; 127 (NaN) where a
-// value is infinite or NaN.  `unit` is 2^-e.  The quotient of floats is
-// correctly rounded, and no quotient but a true tie of the E4M3 grid lands on
-// one (6 t has at most 8 significant bits, so max differs from it by at least
-// one of its own last places, more than half a last place of the quotient).
+// value is infinite or NaN.  `unit` is 2^-e.  The sixth is correctly rounded
+// (but for values so small that the scale is the least one anyway), and none
+// but a true tie of the E4M3 grid lands on one (6 t has at most 8 significant
+// bits, so max differs from it by at least one of its own last places, more
+// than half a last place of the quotient).
 __device__ __forceinline__ uint32_t nvfp4_scale_byte(uint32_t max_bits, float unit) {
     if (max_bits >= kInfBits) return 127u;
     if (max_bits == 0u) return 0u;
-    const float want = __fdiv_rn(__uint_as_float(max_bits) * unit, 6.0f);
+    const float want = sixth(__uint_as_float(max_bits)) * unit;
     unsigned short two;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.0f), "f"(want));
     const uint32_t byte = two & 0xffu;
@@ -120,18 +132,9 @@ __device__ __forceinline__ float nvfp4_inverse(uint32_t byte, float step) {
 // (max a finite magnitude's bits; at least the least step there is, 2^-109).
 __device__ __forceinline__ float nvfp4_wide_step(uint32_t max_bits) {
     if (max_bits == 0u) return 0.0f;
-    uint32_t b = __float_as_uint(__fdiv_rn(__uint_as_float(max_bits), 6.0f));
+    uint32_t b = __float_as_uint(sixth(__uint_as_float(max_bits)));
     b = (b + 0x7ffffu + (b >> 20 & 1u)) & ~0xfffffu;
     return fmaxf(__uint_as_float(b), exp2_int(-109));
-}
-
-// y / s with r = 1 / s correctly rounded: one residual correction of y * r
-// gives the correctly rounded quotient (Markstein's theorem), and rounding
-// that to E2M1 is the same as rounding the exact quotient: |y - t s| is at
-// least one last place of y for every tie point t (3 bits) but a true tie.
-__device__ __forceinline__ float quotient(float y, float s, float r) {
-    const float q = y * r;
-    return fmaf(fmaf(-q, s, y), r, q);
 }
 
 // The same for two values with scales of their own, on packed 32-bit pairs.
