@@ -85,7 +85,7 @@ __device__ __forceinline__ void kept16(const float* plane, const uint8_t*, int64
     }
 }
 
-// C = accumulators, rounded once; of one product, or of each of three.
+// C = accumulators, rounded once; of each product of a launch.
 template <typename T, int NT_, int P, bool ALIGNED>
 struct EpiStore {
     static constexpr int NT = NT_, GROUPS = 2;
@@ -93,7 +93,6 @@ struct EpiStore {
     int64_t ldc[P], M[P], N[P];
     template <class Release>
     __device__ __forceinline__ void run(uint32_t acc, int p, int, int64_t row, int nt, int group, int lane, Release release) const {
-        if (P == 1) p = 0;
         constexpr int STEPS = NT / GROUPS / 32;
 #pragma unroll 1
         for (int j = 0; j < STEPS; ++j) {
@@ -110,15 +109,16 @@ struct EpiStore {
 };
 
 // The same where a tile is shared by several units: partial sums in 32 bits,
-// planes of M rows of ld (N rounded up to 32) for each split.
-template <int NT_, int P>
+// planes of M rows of ld (N rounded up to 32) for each split.  Products of the
+// launch that are not shared (no planes) go straight to their C.
+template <typename T, int NT_, int P>
 struct EpiPartial {
     static constexpr int NT = NT_, GROUPS = 2;
     float* planes[P];
-    int64_t ld[P], M[P];
+    T* C[P];
+    int64_t ld[P], ldc[P], M[P], N[P];
     template <class Release>
-    __device__ __forceinline__ void run(uint32_t acc, int p, int z, int64_t row, int nt, int group, int, Release release) const {
-        if (P == 1) p = 0;
+    __device__ __forceinline__ void run(uint32_t acc, int p, int z, int64_t row, int nt, int group, int lane, Release release) const {
         constexpr int STEPS = NT / GROUPS / 32;
 #pragma unroll 1
         for (int j = 0; j < STEPS; ++j) {
@@ -127,42 +127,52 @@ struct EpiPartial {
             tc5::ld32(acc + c, v);
             if (j == STEPS - 1) release();
             const int64_t col = (int64_t)nt * NT + c;
-            if (row >= M[p] || col >= ld[p]) continue;
             float f[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-            store_row(planes[p] + ((int64_t)z * M[p] + row) * ld[p] + col, f);
+            if (planes[p] == nullptr) store_block<false>(C[p], ldc[p], row - lane, M[p], col, N[p], f, lane);
+            else if (row < M[p] && col < ld[p]) store_row(planes[p] + ((int64_t)z * M[p] + row) * ld[p] + col, f);
         }
     }
 };
 
-// C = the sum of the splits' planes, in their order, rounded once.
-template <typename T, int P>
+// C = the sum of the splits' planes, in their order, rounded once: a thread for
+// four columns of a row (the planes hold few tiles: 32-bit indices do).
+template <typename T>
 struct PartialSums {
-    const float* planes[P];
-    T* C[P];
-    int64_t ld[P], ldc[P], M[P], N[P];
-    int splits;
+    const float* planes;
+    T* C;
+    int64_t ldc;
+    int M, N, ld, splits;
 };
 template <typename T, int P>
-__global__ void __launch_bounds__(256) add_partials_kernel(const __grid_constant__ PartialSums<T, P> s) {
+struct AllPartialSums {
+    PartialSums<T> s[P];
+};
+template <typename T, int P>
+__global__ void __launch_bounds__(256) add_partials_kernel(const __grid_constant__ AllPartialSums<T, P> all) {
     pdl_wait();
     pdl_launch_dependents();
-    const int p = P == 1 ? 0 : blockIdx.z;
-    const int64_t n = s.M[p] * s.ld[p];
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t row = i / s.ld[p], c = i - row * s.ld[p];
-        if (c >= s.N[p]) continue;
-        float v[16];
-#pragma unroll
-        for (int z = 0; z < 16; ++z) v[z] = z < s.splits ? s.planes[p][z * n + i] : 0.0f;
-        float sum = v[0];
-#pragma unroll
-        for (int z = 1; z < 16; ++z)
-            if (z < s.splits) sum += v[z];
-        s.C[p][row * s.ldc[p] + c] = from_float<T>(sum);
+    const PartialSums<T>& s = all.s[blockIdx.y];
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x, quads = (uint32_t)s.ld / 4, n = (uint32_t)s.M * quads;
+    if (i >= n) return;
+    const uint32_t row = i / quads, c = (i - row * quads) * 4;
+    if (c >= (uint32_t)s.N) return;
+    const float4* p = reinterpret_cast<const float4*>(s.planes) + i;
+    const int splits = s.splits;
+    float4 sum = p[0];
+#pragma unroll 4
+    for (int z = 1; z < splits; ++z) {
+        const float4 v = p[(size_t)z * n];
+        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
     }
+    T* dst = s.C + row * s.ldc + c;
+    const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (c + j < (uint32_t)s.N) dst[j] = from_float<T>(v[j]);
 }
+constexpr int kMaxSplits = 16;
 
 // h = act(g) * u from accumulators of NT / 2 columns of g and as many of u,
 // rounded to 16 bits (the operand of the next product); SAVE: a = act(g),
@@ -317,19 +327,6 @@ cudaError_t map16(CUtensorMap* m, const Matrix16& x, int box_rows) {
     return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, x.p, x.cols, x.rows, ld * 2, 64, box_rows, true);
 }
 
-// A product's depth and tiles; PER: columns of B under a tile (64 or 128 of
-// each matrix if gated).
-TileArgs tile_args(int64_t M, int64_t N, int64_t per_tile, int64_t K, int segs) {
-    TileArgs g = {};
-    g.products = 1;
-    g.mt[0] = (int)((M + 255) / 256);
-    g.nt[0] = (int)((N + per_tile - 1) / per_tile);
-    g.nk = (int)((K + 63) / 64);
-    g.segs = segs;
-    g.last_steps = (int)((K - (int64_t)(g.nk - 1) * 64 + 15) / 16);
-    return g;
-}
-
 int64_t pair_tiles(int64_t M, int64_t N, int64_t per_tile) { return (M + 255) / 256 * ((N + per_tile - 1) / per_tile); }
 
 constexpr double kNarrow16 = 0.6;  // 128 columns for 256: 783 us against 683 for the forward of 4096 x 4096 x 12288
@@ -337,19 +334,50 @@ bool narrow16(int64_t M, int64_t N, int64_t wide) {
     return narrow_tiles(pair_tiles(M, N, wide), pair_tiles(M, N, wide / 2), kNarrow16);
 }
 
-// sum over segments of A_s B_s^T; A_MN: A is K x M, B_MN: B is K x N.
-template <int KIND, bool A_MN, bool B_MN, bool GATED, class Epi>
-cudaError_t product16(int64_t M, int64_t N, int64_t K, int segs, const Matrix16& A0, const Matrix16& A1,
-                      const Matrix16& B0, const Matrix16& B1, const Epi& epi, cudaStream_t st) {
-    TileMaps maps;
+// One product of a launch: C (M x N) = sum over segments of A_s B_s^T, depth K
+// each; a_mn: A is stored K x M.
+struct Product16 {
+    Matrix16 A[2], B[2];
+    int segs;
+    bool a_mn;
+    int64_t M, N, K;
+    void* C;
+    int64_t ldc;
+    int64_t stages() const { return (K + 63) / 64 * segs; }
+};
+
+// Tiles of `per_tile` columns (64 or 128 of each matrix if gated) and maps of
+// products; b_box: rows of a box of B.
+cudaError_t tile_args(const Product16* w, int count, int64_t per_tile, int b_maps, int b_box, TileArgs& g, TileMaps& maps) {
     memset(&maps, 0, sizeof(maps));
-    constexpr int A_BOX = A_MN ? 64 : 128, B_BOX = B_MN ? 64 : Epi::NT / 2;
-    cudaError_t err = map16(&maps.a[0], A0, A_BOX);
-    if (err == cudaSuccess) err = map16(&maps.b[0], B0, B_BOX);
-    if (err == cudaSuccess && segs == 2) err = map16(&maps.a[1], A1, A_BOX);
-    if (err == cudaSuccess && (segs == 2 || GATED)) err = map16(&maps.b[1], B1, B_BOX);
-    if (err != cudaSuccess) return err;
-    return launch_tile_gemm<KIND, A_MN, B_MN, GATED>(tile_args(M, N, GATED ? Epi::NT / 2 : Epi::NT, K, segs), maps, epi, st);
+    g = TileArgs{};
+    g.products = count;
+    int map = 0;
+    cudaError_t err = cudaSuccess;
+    for (int p = 0; p < count; ++p) {
+        TileProduct& q = g.p[p];
+        q.mt = (int)((w[p].M + 255) / 256);
+        q.nt = (int)((w[p].N + per_tile - 1) / per_tile);
+        q.nk = (int)((w[p].K + 63) / 64);
+        q.segs = w[p].segs;
+        q.last_steps = (int)((w[p].K - (int64_t)(q.nk - 1) * 64 + 15) / 16);
+        q.a_mn = w[p].a_mn;
+        q.map = map;
+        for (int s = 0; s < w[p].segs && err == cudaSuccess; ++s) err = map16(&maps.a[map + s], w[p].A[s], w[p].a_mn ? 64 : 128);
+        for (int s = 0; s < std::max(w[p].segs, b_maps) && err == cudaSuccess; ++s) err = map16(&maps.b[map + s], w[p].B[s], b_box);
+        map += w[p].segs;
+    }
+    return err;
+}
+
+// One product with an epilogue of its own; A with k contiguous.
+template <int KIND, bool B_MN, bool GATED, class Epi>
+cudaError_t product16(const Product16& w, const Epi& epi, cudaStream_t st) {
+    TileArgs g;
+    TileMaps maps;
+    const cudaError_t err =
+        tile_args(&w, 1, GATED ? Epi::NT / 2 : Epi::NT, GATED ? 2 : 1, B_MN ? 64 : Epi::NT / 2, g, maps);
+    return err != cudaSuccess ? err : launch_tile_gemm<KIND, kMajorK, B_MN, GATED>(g, maps, epi, st);
 }
 
 // x (tokens x K) times the rows of W0 (and W1, 64 rows of each to a tile).
@@ -372,93 +400,124 @@ cudaError_t split16(const Matrix16& x, const Matrix16& W0, const Matrix16& W1, b
     return launch_split_gemm<KIND, PAIRED>(g, maps, epi, st);
 }
 
-template <class Epi>
-void set_store(Epi& epi, int p, void* C, int64_t ldc, int64_t M, int64_t N) {
-    epi.C[p] = static_cast<decltype(epi.C[p] + 0)>(C);
-    epi.ldc[p] = ldc;
-    epi.M[p] = M;
-    epi.N[p] = N;
+// Products into their C, with wide or narrow tiles.
+template <int KIND, typename T, int A_MAJOR, bool B_MN, int NT, bool ALIGNED>
+cudaError_t store16_sized(const Product16* w, int count, cudaStream_t st) {
+    TileArgs g;
+    TileMaps maps;
+    const cudaError_t err = tile_args(w, count, NT, 1, B_MN ? 64 : NT / 2, g, maps);
+    if (err != cudaSuccess) return err;
+    EpiStore<T, NT, kMaxProducts, ALIGNED> epi = {};
+    for (int p = 0; p < count; ++p) {
+        epi.C[p] = static_cast<T*>(w[p].C);
+        epi.ldc[p] = w[p].ldc;
+        epi.M[p] = w[p].M;
+        epi.N[p] = w[p].N;
+    }
+    return launch_tile_gemm<KIND, A_MAJOR, B_MN, false>(g, maps, epi, st);
 }
 
-// Products whose few tiles are shared by several units: the partial sums in the
-// library's pool, and the launch that adds them up.
-template <typename T, int P>
-class Partials {
-public:
-    void add(void* C, int64_t ldc, int64_t M, int64_t N) {
-        const int p = count_++;
-        sums_.C[p] = static_cast<T*>(C);
-        sums_.ldc[p] = ldc;
-        sums_.M[p] = M;
-        sums_.N[p] = N;
-        sums_.ld[p] = round_up(N, 32);
-        total_ += M * sums_.ld[p];
-        most_ = std::max(most_, M * sums_.ld[p]);
+// Products whose few narrow tiles are shared by several units of `depth` stages:
+// partial sums in the library's pool, and a launch that adds them up.
+template <int KIND, typename T, int A_MAJOR, bool B_MN>
+cudaError_t store16_shared(const Product16* w, int count, int64_t depth, cudaStream_t st) {
+    TileArgs g;
+    TileMaps maps;
+    cudaError_t err = tile_args(w, count, 128, 1, 64, g, maps);
+    if (err != cudaSuccess) return err;
+    AllPartialSums<T, kMaxProducts> sums = {};
+    EpiPartial<T, 128, kMaxProducts> epi = {};
+    int64_t total = 0, most = 0;
+    int shared = 0, of[kMaxProducts];
+    for (int p = 0; p < count; ++p) {
+        const int64_t ld = round_up(w[p].N, 32), s = (w[p].stages() + depth - 1) / depth;
+        const int64_t per = (w[p].stages() + s - 1) / s;
+        g.p[p].splits = (int)((w[p].stages() + per - 1) / per);  // none empty
+        epi.C[p] = static_cast<T*>(w[p].C);
+        epi.ldc[p] = w[p].ldc;
+        epi.M[p] = w[p].M;
+        epi.N[p] = w[p].N;
+        epi.ld[p] = ld;
+        if (g.p[p].splits == 1) continue;
+        of[shared] = p;
+        sums.s[shared++] = PartialSums<T>{nullptr, epi.C[p], w[p].ldc, (int)w[p].M, (int)w[p].N, (int)ld, g.p[p].splits};
+        total += w[p].M * ld * g.p[p].splits;
+        most = std::max(most, w[p].M * ld / 4);
     }
-    template <int KIND, bool A_MN, bool B_MN>
-    cudaError_t run(TileArgs g, int splits, const TileMaps& maps, cudaStream_t st) {
-        void* ws = nullptr;
-        cudaError_t err = pool_alloc(&ws, (size_t)(total_ * splits * 4), st);
-        if (err != cudaSuccess) return err;
-        EpiPartial<128, P> epi = {};
-        float* at = static_cast<float*>(ws);
-        for (int p = 0; p < count_; ++p) {
-            epi.planes[p] = at;
-            sums_.planes[p] = at;
-            epi.ld[p] = sums_.ld[p];
-            epi.M[p] = sums_.M[p];
-            at += sums_.M[p] * sums_.ld[p] * splits;
+    void* ws = nullptr;
+    err = pool_alloc(&ws, (size_t)total * 4, st);
+    if (err != cudaSuccess) return err;
+    float* at = static_cast<float*>(ws);
+    for (int i = 0; i < shared; ++i) {
+        sums.s[i].planes = epi.planes[of[i]] = at;
+        at += (int64_t)sums.s[i].M * sums.s[i].ld * sums.s[i].splits;
+    }
+    err = launch_tile_gemm<KIND, A_MAJOR, B_MN, false>(g, maps, epi, st);
+    if (err == cudaSuccess)
+        err = launch_pdl(add_partials_kernel<T, kMaxProducts>, dim3((unsigned)((most + 255) / 256), (unsigned)shared), dim3(256),
+                         0, st, sums);
+    const cudaError_t freed = cudaFreeAsync(ws, st);
+    return err == cudaSuccess ? freed : err;
+}
+
+// How deep the units of a launch with few narrow tiles had best be, from dealing
+// them out as the kernel does: in stages (0.2 us each), a unit costs its stages
+// and 8 more, adding partial sums up 20.  0: too many tiles for that to matter.
+int64_t shared_depth(const Product16* w, int count) {
+    constexpr int kMaxPairs = 256;
+    const int64_t pairs = std::min(kMaxPairs, std::max(1, tile_sms() / 2));
+    int64_t deepest = 0, tiles = 0;
+    for (int p = 0; p < count; ++p) {
+        deepest = std::max(deepest, w[p].stages());
+        tiles += pair_tiles(w[p].M, w[p].N, 128);
+    }
+    if (count == 0 || tiles > 2 * pairs) return 0;
+    int64_t best = deepest, best_cost = INT64_MAX;
+    for (int64_t depth = deepest; depth >= 12; depth = depth * 4 / 5) {
+        int64_t load[kMaxPairs] = {0}, t = 0, units = 0;
+        bool fits = true;
+        for (int p = 0; p < count && fits; ++p) {
+            const int64_t s = (w[p].stages() + depth - 1) / depth, each = (w[p].stages() + s - 1) / s + 8;
+            const int64_t n = pair_tiles(w[p].M, w[p].N, 128) * s;
+            units += n;
+            fits = s <= kMaxSplits && units <= 4 * pairs;
+            for (int64_t i = 0; i < n && fits; ++i, t = t + 1 == pairs ? 0 : t + 1) load[t] += each;
         }
-        g.splits = splits;
-        sums_.splits = splits;
-        err = launch_tile_gemm<KIND, A_MN, B_MN, false>(g, maps, epi, st);
-        if (err == cudaSuccess)
-            err = launch_pdl(add_partials_kernel<T, P>, dim3((unsigned)std::min<int64_t>((most_ + 255) / 256, 1 << 20), 1, (unsigned)count_),
-                             dim3(256), 0, st, sums_);
-        const cudaError_t freed = cudaFreeAsync(ws, st);
-        return err == cudaSuccess ? freed : err;
+        if (!fits) break;
+        const int64_t cost = *std::max_element(load, load + pairs) + (depth < deepest ? 20 : 0);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = depth;
+        }
     }
-
-private:
-    PartialSums<T, P> sums_ = {};
-    int count_ = 0;
-    int64_t total_ = 0, most_ = 0;
-};
-
-// C = sum over segments, with wide or narrow tiles, or narrow ones shared.
-template <int KIND, typename T, bool B_MN, int NT, bool ALIGNED>
-cudaError_t store16_sized(int64_t M, int64_t N, int64_t K, int segs, const Matrix16& A0, const Matrix16& A1,
-                          const Matrix16& B0, const Matrix16& B1, void* C, int64_t ldc, cudaStream_t st) {
-    EpiStore<T, NT, 1, ALIGNED> epi;
-    set_store(epi, 0, C, ldc, M, N);
-    return product16<KIND, false, B_MN, false>(M, N, K, segs, A0, A1, B0, B1, epi, st);
+    return best;
 }
-template <int KIND, typename T, bool B_MN>
-cudaError_t store16(int64_t M, int64_t N, int64_t K, int segs, const Matrix16& A0, const Matrix16& A1,
-                    const Matrix16& B0, const Matrix16& B1, void* C, int64_t ldc, cudaStream_t st) {
-    const int splits = tile_splits(pair_tiles(M, N, 128), (K + 63) / 64 * segs);
-    if (splits > 1) {
-        Partials<T, 1> parts;
-        parts.add(C, ldc, M, N);
-        TileMaps maps;
-        memset(&maps, 0, sizeof(maps));
-        cudaError_t err = map16(&maps.a[0], A0, 128);
-        if (err == cudaSuccess) err = map16(&maps.b[0], B0, 64);
-        if (err == cudaSuccess && segs == 2) err = map16(&maps.a[1], A1, 128);
-        if (err == cudaSuccess && segs == 2) err = map16(&maps.b[1], B1, 64);
-        if (err != cudaSuccess) return err;
-        return parts.template run<KIND, false, B_MN>(tile_args(M, N, 128, K, segs), splits, maps, st);
+
+// Products of one launch: shared if they are few and deep, else with the tiles
+// whose rounds are the shorter.
+template <int KIND, typename T, int A_MAJOR, bool B_MN>
+cudaError_t store16(const Product16* w, int count, cudaStream_t st) {
+    if (count == 0) return cudaSuccess;
+    int64_t wide = 0, narrow = 0, deepest = 0;
+    bool aligned = true;
+    for (int p = 0; p < count; ++p) {
+        wide += pair_tiles(w[p].M, w[p].N, 256);
+        narrow += pair_tiles(w[p].M, w[p].N, 128);
+        deepest = std::max(deepest, w[p].stages());
+        aligned = aligned && aligned_rows<T>(w[p].C, w[p].ldc);
     }
-    const bool narrow = narrow16(M, N, 256), aligned = aligned_rows<T>(C, ldc);
-    auto f = narrow ? (aligned ? store16_sized<KIND, T, B_MN, 128, true> : store16_sized<KIND, T, B_MN, 128, false>)
-                    : (aligned ? store16_sized<KIND, T, B_MN, 256, true> : store16_sized<KIND, T, B_MN, 256, false>);
-    return f(M, N, K, segs, A0, A1, B0, B1, C, ldc, st);
+    const int64_t depth = shared_depth(w, count);
+    if (depth > 0 && depth < deepest) return store16_shared<KIND, T, A_MAJOR, B_MN>(w, count, depth, st);
+    auto f = narrow_tiles(wide, narrow, kNarrow16)
+                 ? (aligned ? store16_sized<KIND, T, A_MAJOR, B_MN, 128, true> : store16_sized<KIND, T, A_MAJOR, B_MN, 128, false>)
+                 : (aligned ? store16_sized<KIND, T, A_MAJOR, B_MN, 256, true> : store16_sized<KIND, T, A_MAJOR, B_MN, 256, false>);
+    return f(w, count, st);
 }
 
 template <int KIND, typename T, int NT, bool SAVE>
 cudaError_t gate16(const FfForward& f, cudaStream_t st) {
-    return product16<KIND, false, false, true>(
-        f.T, f.F, f.D, 1, f.x, f.x, f.wg, f.wu,
+    return product16<KIND, false, true>(
+        Product16{{f.x}, {f.wg, f.wu}, 1, false, f.T, f.F, f.D, nullptr, 0},
         EpiGate<T, NT, SAVE>{static_cast<T*>(f.h), KeepPlanes{f.a, f.b, f.ea, f.eb}, f.T, f.ld, f.act}, st);
 }
 
@@ -478,77 +537,17 @@ cudaError_t forward_typed(const FfForward& f, cudaStream_t st) {
     // Wd was complete before the launch above could end its own wait
     if (f.T <= kSplitTokens16)
         return split16<KIND, false>(h, f.wd, f.wd, true, EpiSplitStore<T>{static_cast<T*>(f.y), f.ldy, f.D}, st);
-    return store16<KIND, T, false>(f.T, f.D, f.F, 1, h, h, f.wd, f.wd, f.y, f.ldy, st);
+    const Product16 y{{h}, {f.wd}, 1, false, f.T, f.D, f.F, f.y, f.ldy};
+    return store16<KIND, T, kMajorK, false>(&y, 1, st);
 }
 
 template <int KIND, typename T, int NT>
 cudaError_t gate_backward16(const FfBackward& f, cudaStream_t st) {
-    return product16<KIND, false, true, false>(
-        f.T, f.F, f.D, 1, f.dy, f.dy, f.wd, f.wd,
+    return product16<KIND, true, false>(
+        Product16{{f.dy}, {f.wd}, 1, false, f.T, f.F, f.D, nullptr, 0},
         EpiGateBackward<T, NT>{KeepPlanes{const_cast<void*>(f.a), const_cast<void*>(f.b), const_cast<uint8_t*>(f.ea),
                                            const_cast<uint8_t*>(f.eb)},
                                 static_cast<T*>(f.dg), static_cast<T*>(f.du), f.T, f.ld}, st);
-}
-
-// The weights' gradients that are wanted, in one launch: sums over the T rows
-// of both operands.
-struct WeightProduct {
-    Matrix16 A, B;
-    void* C;
-    int64_t ldc;
-};
-template <int NT>
-cudaError_t weight_args(const WeightProduct* w, int count, int64_t T, TileArgs& g, TileMaps& maps) {
-    memset(&maps, 0, sizeof(maps));
-    g = tile_args(0, 0, NT, T, 1);
-    g.products = count;
-    cudaError_t err = cudaSuccess;
-    for (int p = 0; p < count && err == cudaSuccess; ++p) {
-        err = map16(&maps.a[p], w[p].A, 64);
-        if (err == cudaSuccess) err = map16(&maps.b[p], w[p].B, 64);
-        g.mt[p] = (int)((w[p].A.cols + 255) / 256);
-        g.nt[p] = (int)((w[p].B.cols + NT - 1) / NT);
-    }
-    return err;
-}
-template <int KIND, typename T, int NT, bool ALIGNED>
-cudaError_t weights16_sized(const WeightProduct* w, int count, int64_t tokens, cudaStream_t st) {
-    TileArgs g;
-    TileMaps maps;
-    const cudaError_t err = weight_args<NT>(w, count, tokens, g, maps);
-    if (err != cudaSuccess) return err;
-    EpiStore<T, NT, kMaxProducts, ALIGNED> epi = {};
-    for (int p = 0; p < count; ++p) set_store(epi, p, w[p].C, w[p].ldc, w[p].A.cols, w[p].B.cols);
-    return launch_tile_gemm<KIND, true, true, false>(g, maps, epi, st);
-}
-template <int KIND, typename T>
-cudaError_t weights16(const FfBackward& f, const Matrix16& h, const Matrix16& dg, const Matrix16& du, cudaStream_t st) {
-    WeightProduct w[kMaxProducts];
-    int count = 0;
-    if (f.dwg != nullptr) w[count++] = WeightProduct{dg, f.x, f.dwg, f.lddwg};
-    if (f.dwu != nullptr) w[count++] = WeightProduct{du, f.x, f.dwu, f.lddwu};
-    if (f.dwd != nullptr) w[count++] = WeightProduct{f.dy, h, f.dwd, f.lddwd};
-    if (count == 0) return cudaSuccess;
-    int64_t wide = 0, narrow = 0;
-    bool aligned = true;
-    for (int p = 0; p < count; ++p) {
-        wide += pair_tiles(w[p].A.cols, w[p].B.cols, 256);
-        narrow += pair_tiles(w[p].A.cols, w[p].B.cols, 128);
-        aligned = aligned && aligned_rows<T>(w[p].C, w[p].ldc);
-    }
-    const int splits = tile_splits(narrow, (f.T + 63) / 64);
-    if (splits > 1) {
-        Partials<T, kMaxProducts> parts;
-        for (int p = 0; p < count; ++p) parts.add(w[p].C, w[p].ldc, w[p].A.cols, w[p].B.cols);
-        TileArgs g;
-        TileMaps maps;
-        const cudaError_t err = weight_args<128>(w, count, f.T, g, maps);
-        return err != cudaSuccess ? err : parts.template run<KIND, true, true>(g, splits, maps, st);
-    }
-    auto run = narrow_tiles(wide, narrow, kNarrow16)
-                   ? (aligned ? weights16_sized<KIND, T, 128, true> : weights16_sized<KIND, T, 128, false>)
-                   : (aligned ? weights16_sized<KIND, T, 256, true> : weights16_sized<KIND, T, 256, false>);
-    return run(w, count, f.T, st);
 }
 
 template <int KIND, typename T>
@@ -558,11 +557,21 @@ cudaError_t backward_typed(const FfBackward& f, cudaStream_t st) {
     // dh = dy Wd (B is Wd, D x F: K x N), unless only dWd is wanted
     if (f.dx != nullptr || f.dwg != nullptr || f.dwu != nullptr)
         err = narrow16(f.T, f.F, 256) ? gate_backward16<KIND, T, 128>(f, st) : gate_backward16<KIND, T, 256>(f, st);
-    // dx = dg Wg + du Wu
-    if (err == cudaSuccess && f.dx != nullptr)
-        err = store16<KIND, T, true>(f.T, f.D, f.F, 2, dg, du, f.wg, f.wu, f.dx, f.lddx, st);
     if (err != cudaSuccess) return err;
-    return weights16<KIND, T>(f, h, dg, du, st);
+    // dx = dg Wg + du Wu; the weights' gradients are sums over the T rows of both
+    // operands.  All in one launch where the tiles are few (shared_depth); else dx
+    // by itself (its tiles are of another depth: dealt out with the others, some
+    // pairs would have one more of the deep ones).
+    Product16 w[kMaxProducts];
+    int count = 0;
+    if (f.dx != nullptr) w[count++] = Product16{{dg, du}, {f.wg, f.wu}, 2, false, f.T, f.D, f.F, f.dx, f.lddx};
+    const int others = count;
+    if (f.dwg != nullptr) w[count++] = Product16{{dg}, {f.x}, 1, true, f.F, f.D, f.T, f.dwg, f.lddwg};
+    if (f.dwu != nullptr) w[count++] = Product16{{du}, {f.x}, 1, true, f.F, f.D, f.T, f.dwu, f.lddwu};
+    if (f.dwd != nullptr) w[count++] = Product16{{f.dy}, {h}, 1, true, f.D, f.F, f.T, f.dwd, f.lddwd};
+    if (shared_depth(w, count) > 0) return store16<KIND, T, kMajorAny, true>(w, count, st);
+    err = store16<KIND, T, kMajorAny, true>(w, others, st);
+    return err != cudaSuccess ? err : store16<KIND, T, kMajorAny, true>(w + others, count - others, st);
 }
 
 }  // namespace

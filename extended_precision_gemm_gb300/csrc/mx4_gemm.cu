@@ -251,13 +251,14 @@ cudaError_t product4(const Mx4Matrix& A, const Mx4Matrix& B, const Epi& epi, cud
     if (err != cudaSuccess) return err;
     TileArgs g = {};
     g.products = 1;
-    g.mt[0] = (int)((A.rows + 255) / 256);
-    g.nt[0] = (int)((B.rows + Epi::NT - 1) / Epi::NT);
-    g.nk = (int)((A.K + MX4_TILE_K - 1) / MX4_TILE_K);
-    g.segs = 1;
-    g.last_steps = (int)((A.K - (int64_t)(g.nk - 1) * MX4_TILE_K + 63) / 64);
+    TileProduct& q = g.p[0];
+    q.mt = (int)((A.rows + 255) / 256);
+    q.nt = (int)((B.rows + Epi::NT - 1) / Epi::NT);
+    q.nk = (int)((A.K + MX4_TILE_K - 1) / MX4_TILE_K);
+    q.segs = 1;
+    q.last_steps = (int)((A.K - (int64_t)(q.nk - 1) * MX4_TILE_K + 63) / 64);
     g.tiles_k = (int)mx4_scale_tiles(FMT, A.K);
-    return launch_tile_gemm<KIND, false, false, false>(g, maps, epi, st);
+    return launch_tile_gemm<KIND, kMajorK, false, false>(g, maps, epi, st);
 }
 
 // x (tokens x K) times the rows of W.

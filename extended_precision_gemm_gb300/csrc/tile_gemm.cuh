@@ -4,8 +4,7 @@
 // accumulators.  Everything is in an unnamed namespace, so each including file
 // has its own count of bounded waits that gave up.
 //
-// D = sum over k of A[m, k] B[n, k], for up to three products of the same kind
-// and depth in one launch.  A pair of CTAs on two SMs owns a tile of 256 m by
+// D = sum over k of A[m, k] B[n, k], for up to four products in one launch.  A pair of CTAs on two SMs owns a tile of 256 m by
 // NT n: each CTA holds 128 rows of A, one half of the rows of B, and
 // 128 rows of the accumulators (f32, in tensor memory, twice: the MMAs of a
 // tile overlap the epilogue of the one before).  A stage of the shared-memory
@@ -42,23 +41,29 @@ __device__ unsigned int g_tile_timeouts = 0;
 
 __device__ __forceinline__ void tile_timeout() { atomicAdd(&g_tile_timeouts, 1u); }
 
-constexpr int kMaxProducts = 3;
+constexpr int kMaxProducts = 4, kMaxMaps = kMaxProducts + 1;
 
 struct TileMaps {
-    CUtensorMap a[kMaxProducts], b[kMaxProducts];  // by product, by segment, or (gated) b by CTA
-    CUtensorMap sa, sb;                            // scales (4-bit kinds): tiles of 128 words
+    CUtensorMap a[kMaxMaps], b[kMaxMaps];  // by product and segment, or (gated) b by CTA
+    CUtensorMap sa, sb;                    // scales (4-bit kinds): tiles of 128 words
+};
+
+struct TileProduct {
+    int mt, nt;       // tiles along m and n
+    int nk, segs;     // stages of a segment, segments
+    int last_steps;   // MMAs in a segment's last stage
+    int map;          // its first maps
+    int a_mn;         // A stored with m contiguous (kernels that take either)
+    int splits, per;  // units that share a tile, stages of one (the last may have fewer)
+    int64_t first;    // first unit
 };
 
 struct TileArgs {
-    int mt[kMaxProducts], nt[kMaxProducts];  // tiles along m and n
-    int64_t first[kMaxProducts];             // first tile of each product
-    int64_t tiles;                           // of all products
+    TileProduct p[kMaxProducts];
+    int64_t units;  // of all products
     int products;
-    int splits, per;  // units that share a tile, stages of one (the last may have fewer)
-    int pairs;       // CTA pairs in the grid
-    int nk, segs;    // stages of a segment, segments (more than one: a single product)
-    int last_steps;  // MMAs in a segment's last stage
-    int tiles_k;     // 4-bit kinds: scale tiles in a row of 128
+    int pairs;      // CTA pairs in the grid
+    int tiles_k;    // 4-bit kinds: scale tiles in a row of 128
 };
 
 template <int KIND, int NT_>
@@ -79,21 +84,29 @@ struct TileShape {
 
 // Unit t: split z of tile (m, n) of product p.
 __device__ __forceinline__ void tile_of(const TileArgs& g, int64_t t, int& z, int& p, int& m, int& n) {
-    z = g.splits > 1 ? (int)(t / g.tiles) : 0;
-    t -= z * g.tiles;
-    p = g.products > 2 && t >= g.first[2] ? 2 : g.products > 1 && t >= g.first[1] ? 1 : 0;
-    t -= g.first[p];
-    const int64_t per_group = (int64_t)kTileGroup * g.nt[p];
+    p = 0;
+#pragma unroll
+    for (int i = 1; i < kMaxProducts; ++i)
+        if (i < g.products && t >= g.p[i].first) p = i;
+    const TileProduct& q = g.p[p];
+    t -= q.first;
+    const int64_t tiles = (int64_t)q.mt * q.nt;
+    z = q.splits > 1 ? (int)(t / tiles) : 0;
+    t -= z * tiles;
+    const int64_t per_group = (int64_t)kTileGroup * q.nt;
     const int64_t group = t / per_group;
-    const int first = (int)group * kTileGroup, size = min(kTileGroup, g.mt[p] - first);
+    const int first = (int)group * kTileGroup, size = min(kTileGroup, q.mt - first);
     m = first + (int)((t % per_group) % size);
     n = (int)((t % per_group) / size);
 }
 
+// How A is stored: k contiguous, m contiguous, or as each product says.
+enum Major { kMajorK = 0, kMajorMN = 1, kMajorAny = 2 };
+
 // Epi: NT, GROUPS, and run(acc, product, split, m row, n tile, group, lane, release): takes this
 // warp's 32 rows of the accumulators from column `acc` on (all lanes, also for
 // rows beyond the matrix) and calls release() after its last read of them.
-template <int KIND, bool A_MN, bool B_MN, bool GATED, class Epi>
+template <int KIND, int A_MAJOR, bool B_MN, bool GATED, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROUPS, 1)
     tile_gemm_kernel(const __grid_constant__ TileArgs g, const __grid_constant__ TileMaps maps,
                      const __grid_constant__ Epi epi) {
@@ -109,8 +122,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int64_t pair = blockIdx.x >> 1;
-    const int64_t tiles = g.tiles * g.splits;  // units
-    const int all_stages = g.nk * g.segs;
+    const int64_t units = g.units;
 
     const uint32_t full0 = smem_addr(&bars[0]), empty0 = smem_addr(&bars[STAGES]);
     const uint32_t accf0 = smem_addr(&bars[2 * STAGES]), acce0 = smem_addr(&bars[2 * STAGES + 2]);
@@ -145,23 +157,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
         uint32_t stage = 0, phase = 0;
         int64_t issued = 0;
         bool ok = true;
-        for (int64_t t = pair; t < tiles && ok; t += g.pairs) {
+        for (int64_t t = pair; t < units && ok; t += g.pairs) {
             int z, p, mt, nt;
             tile_of(g, t, z, p, mt, nt);
-            const int it0 = z * g.per, per_tile = min(g.per, all_stages - it0);
+            const TileProduct& q = g.p[p];
+            const int it0 = z * q.per, per_tile = min(q.per, q.nk * q.segs - it0);
+            const bool a_mn = A_MAJOR == kMajorAny ? q.a_mn != 0 : A_MAJOR == kMajorMN;
             const int a_row = (mt * 2 + (int)rank) * 128;
             const int b_row = GATED ? nt * (NT / 2) : nt * NT + (int)rank * (NT / 2);
-            int seg = it0 / g.nk, kb = it0 % g.nk;
+            int seg = it0 / q.nk, kb = it0 % q.nk;
             for (int it = 0; it < per_tile; ++it) {
                 ok = warp_wait(empty0 + 8 * stage, phase ^ 1, kTileWaitNs);
                 if (!ok) break;
                 if (elect_one()) {
                     const uint32_t dst = ring + stage * S::STAGE_BYTES, bar = full_lead0 + 8 * stage;
-                    const CUtensorMap* ma = &maps.a[p + seg];
-                    const CUtensorMap* mb = &maps.b[GATED ? rank : p + seg];
+                    const CUtensorMap* ma = &maps.a[q.map + seg];
+                    const CUtensorMap* mb = &maps.b[GATED ? rank : q.map + seg];
                     if (leader) mbar_expect_tx(full0 + 8 * stage, 2u * S::STAGE_BYTES);
                     constexpr int ROW = F4 ? 128 : 64;  // elements (bytes of codes) of a 128-byte row
-                    if (!A_MN) {
+                    if (!a_mn) {
                         tma_load_2d_group(dst, ma, kb * ROW, a_row, bar);
                     } else {
                         tma_load_2d_group(dst, ma, a_row, kb * 64, bar);
@@ -186,7 +200,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
                     }
                 }
                 __syncwarp();
-                if (++kb == g.nk) { kb = 0; ++seg; }
+                if (++kb == q.nk) { kb = 0; ++seg; }
                 ++issued;
                 if (++stage == STAGES) { stage = 0; phase ^= 1; }
             }
@@ -207,23 +221,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
         if (leader) {
             // ---- MMAs ----
             constexpr uint32_t IDESC = F4 ? tc5::idesc_e2m1(KIND == kKindMx, 256, NT)
-                                          : tc5::idesc_f16(KIND == kKindBF16, A_MN, B_MN, 256, NT);
-            constexpr uint64_t A_STEP = A_MN ? 2048 / 16 : 2, B_STEP = B_MN ? 2048 / 16 : 2;
-            const uint64_t ad0 = A_MN ? tc5::desc_mnmajor_sw128(ring, 8192) : tc5::desc_kmajor_sw128(ring);
+                                          : tc5::idesc_f16(KIND == kKindBF16, false, B_MN, 256, NT);
+            constexpr uint64_t B_STEP = B_MN ? 2048 / 16 : 2;
             const uint64_t bd0 = B_MN ? tc5::desc_mnmajor_sw128(ring + S::A_BYTES, 8192)
                                       : tc5::desc_kmajor_sw128(ring + S::A_BYTES);
             const uint64_t sd0 = tc5::desc_scale_tile(ring + S::A_BYTES + S::B_BYTES);
             uint32_t stage = 0, phase = 0, count = 0;
-            for (int64_t t = pair; t < tiles && ok; t += g.pairs, ++count) {
+            for (int64_t t = pair; t < units && ok; t += g.pairs, ++count) {
                 int z, p, mt, nt;
                 tile_of(g, t, z, p, mt, nt);
-                const int it0 = z * g.per, per_tile = min(g.per, all_stages - it0);
+                const TileProduct& q = g.p[p];
+                const int it0 = z * q.per, per_tile = min(q.per, q.nk * q.segs - it0), nk = q.nk, last_steps = q.last_steps;
+                const bool a_mn = A_MAJOR == kMajorAny ? q.a_mn != 0 : A_MAJOR == kMajorMN;
+                const uint64_t ad0 = a_mn ? tc5::desc_mnmajor_sw128(ring, 8192) : tc5::desc_kmajor_sw128(ring);
+                const uint64_t a_step = a_mn ? 2048 / 16 : 2;
+                const uint32_t idesc = IDESC | (a_mn ? 1u << 15 : 0u);
                 const uint32_t buf = count & 1;
                 const uint32_t d = tmem + buf * NT;
                 ok = warp_wait(acce0 + 8 * buf, ((count >> 1) & 1) ^ 1, kTileWaitNs);
                 if (!ok) break;
                 tc5::fence_after_sync();
-                int kb = it0 % g.nk;
+                int kb = it0 % nk;
                 for (int it = 0; it < per_tile; ++it) {
                     ok = warp_wait(full0 + 8 * stage, phase, kTileWaitNs);
                     if (!ok) break;
@@ -231,7 +249,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
                     if (elect_one()) {
                         const uint64_t off = (uint64_t)((stage * S::STAGE_BYTES) >> 4);
                         const uint64_t ad = ad0 + off, bd = bd0 + off;
-                        const int steps = kb == g.nk - 1 ? g.last_steps : 4;
+                        const int steps = kb == nk - 1 ? last_steps : 4;
                         if constexpr (F4) {
                             const uint32_t sc = tmem + S::SCALE_COL + (it & 1) * S::SCALE_COLS;
                             const uint64_t sd = sd0 + off;
@@ -249,42 +267,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
                                 if (j >= steps) break;
                                 const uint32_t acc = (it | j) != 0 ? 1u : 0u;
                                 if (KIND == kKindMx)
-                                    tc5::mma_mx_pair(d, ad + A_STEP * j, bd + B_STEP * j,
+                                    tc5::mma_mx_pair(d, ad + 2 * j, bd + B_STEP * j,
                                                      tc5::idesc_scale_byte(IDESC, (j & 1) * 2), sc + (j / 2) * 4,
                                                      sc + 16 + (j / 2) * SB + sbo, acc);
                                 else
-                                    tc5::mma_nv_pair(d, ad + A_STEP * j, bd + B_STEP * j, IDESC, sc + j * 4,
+                                    tc5::mma_nv_pair(d, ad + 2 * j, bd + B_STEP * j, IDESC, sc + j * 4,
                                                      sc + 16 + j * SB + sbo, acc);
                             }
                         } else {
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 if (j >= steps) break;
-                                tc5::mma_f16_pair(d, ad + A_STEP * j, bd + B_STEP * j, IDESC, (it | j) != 0 ? 1u : 0u);
+                                tc5::mma_f16_pair(d, ad + a_step * j, bd + B_STEP * j, idesc, (it | j) != 0 ? 1u : 0u);
                             }
                         }
                         tc5::commit_pair(empty0 + 8 * stage, 0x3);
                         if (it == per_tile - 1) tc5::commit_pair(accf0 + 8 * buf, 0x3);
                     }
                     __syncwarp();
-                    if (++kb == g.nk) kb = 0;
+                    if (++kb == nk) kb = 0;
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
             }
-            if (pair < tiles) {
+            if (pair < units) {
                 if (elect_one()) tc5::commit_pair(done_bar, 0x3);
                 __syncwarp();
             }
         }
         // every MMA has finished before either CTA gives up its shared or
         // tensor memory
-        if (pair < tiles) ok = warp_wait(done_bar, 0, leader ? kTileWaitNs : kTileWaitNs * 4) && ok;
+        if (pair < units) ok = warp_wait(done_bar, 0, leader ? kTileWaitNs : kTileWaitNs * 4) && ok;
         if (!ok && lane == 0) tile_timeout();
     } else {
         // ---- epilogue ----
         const int q = warp & 3, group = (warp - 2) >> 2;
         uint32_t count = 0;
-        for (int64_t t = pair; t < tiles; t += g.pairs, ++count) {
+        for (int64_t t = pair; t < units; t += g.pairs, ++count) {
             int z, p, mt, nt;
             tile_of(g, t, z, p, mt, nt);
             const uint32_t buf = count & 1;
@@ -324,11 +342,11 @@ int tile_sms() {
 }
 
 // Launch on as many CTA pairs as can be resident (never more than tiles).
-template <int KIND, bool A_MN, bool B_MN, bool GATED, class Epi>
+template <int KIND, int A_MAJOR, bool B_MN, bool GATED, class Epi>
 cudaError_t launch_tile_gemm(TileArgs g, const TileMaps& maps, const Epi& epi, cudaStream_t st) {
     using S = TileShape<KIND, Epi::NT>;
     static std::atomic<int> cached[64];  // resident pairs per device; 0 = not asked yet
-    auto* kernel = tile_gemm_kernel<KIND, A_MN, B_MN, GATED, Epi>;
+    auto* kernel = tile_gemm_kernel<KIND, A_MAJOR, B_MN, GATED, Epi>;
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
@@ -358,15 +376,16 @@ cudaError_t launch_tile_gemm(TileArgs g, const TileMaps& maps, const Epi& epi, c
             cached[dev].store(pairs, std::memory_order_relaxed);
         }
     }
-    g.tiles = 0;
+    g.units = 0;
     for (int p = 0; p < g.products; ++p) {
-        g.first[p] = g.tiles;
-        g.tiles += (int64_t)g.mt[p] * g.nt[p];
+        TileProduct& q = g.p[p];
+        if (q.splits < 1) q.splits = 1;
+        q.per = (q.nk * q.segs + q.splits - 1) / q.splits;
+        q.first = g.units;
+        g.units += (int64_t)q.mt * q.nt * q.splits;
     }
-    if (g.tiles <= 0) return cudaSuccess;
-    if (g.splits < 1) g.splits = 1;
-    g.per = (g.nk * g.segs + g.splits - 1) / g.splits;
-    g.pairs = (int)std::min<int64_t>(pairs, g.tiles * g.splits);
+    if (g.units <= 0) return cudaSuccess;
+    g.pairs = (int)std::min<int64_t>(pairs, g.units);
     cfg.numAttrs = 2;
     cfg.gridDim = dim3((unsigned)(2 * g.pairs));
     return cudaLaunchKernelEx(&cfg, kernel, g, maps, epi);
@@ -388,18 +407,6 @@ inline bool narrow_tiles(int64_t wide_tiles, int64_t narrow_count, double narrow
     const int64_t pairs = std::max(1, tile_sms() / 2);
     const int64_t wide_rounds = (wide_tiles + pairs - 1) / pairs, rounds = (narrow_count + pairs - 1) / pairs;
     return (double)rounds * narrow_cost < (double)wide_rounds;
-}
-
-// Splits of `tiles` tiles of `stages` stages: enough that the units fill the
-// pairs once, with at least 12 stages each (one costs about 0.2 us; adding the
-// partial sums up takes a launch of 3 us), at most 16; 1 where that gains
-// nothing.
-inline int tile_splits(int64_t tiles, int64_t stages) {
-    const int64_t pairs = std::max(1, tile_sms() / 2);
-    const int64_t s = std::min<int64_t>(std::min<int64_t>(pairs / std::max<int64_t>(1, tiles), stages / 12), 16);
-    if (s < 2 || stages < 32) return 1;
-    const int64_t per = (stages + s - 1) / s;
-    return (int)((stages + per - 1) / per);  // none empty
 }
 
 // ---- pieces of epilogues ----
