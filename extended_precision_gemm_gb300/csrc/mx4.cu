@@ -363,11 +363,13 @@ __global__ void __launch_bounds__(256) nvfp4_finish_kernel(const float* most, in
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int64_t row = blockIdx.x, tiles = mx4_scale_tiles(kNvfp4, K);
     const uint4* src = reinterpret_cast<const uint4*>(most) + row * tiles;
-    uint32_t m = 0;
-    for (int64_t t = threadIdx.x; t < tiles; t += blockDim.x) {
-        const uint4 b = src[t];
-        m = max(max(m, b.x & 0x7fffffffu), max(max(b.y & 0x7fffffffu, b.z & 0x7fffffffu), b.w & 0x7fffffffu));
-    }
+    auto most4 = [](const uint4& b) {
+        return max(max(b.x & 0x7fffffffu, b.y & 0x7fffffffu), max(b.z & 0x7fffffffu, b.w & 0x7fffffffu));
+    };
+    // a thread's first tile stays in registers; rows beyond 16384 are read again
+    const uint4 kept = threadIdx.x < tiles ? src[threadIdx.x] : make_uint4(0, 0, 0, 0);
+    uint32_t m = most4(kept);
+    for (int64_t t = threadIdx.x + blockDim.x; t < tiles; t += blockDim.x) m = max(m, most4(src[t]));
     m = __reduce_max_sync(~0u, m);
     if (lane == 0) part[warp] = m;
     __syncthreads();
@@ -377,7 +379,7 @@ __global__ void __launch_bounds__(256) nvfp4_finish_kernel(const float* most, in
     const float unit = exp2_int(-e);
     if (threadIdx.x == 0) exponents[row] = e;
     for (int64_t t = threadIdx.x; t < tiles; t += blockDim.x) {
-        const uint4 b = src[t];
+        const uint4 b = t == threadIdx.x ? kept : src[t];
         const uint32_t bits[4] = {b.x, b.y, b.z, b.w};
         uint32_t word = 0;
         bool low = false;
