@@ -417,16 +417,16 @@ cudaError_t store16_sized(const Product16* w, int count, cudaStream_t st) {
     return launch_tile_gemm<KIND, A_MAJOR, B_MN, false>(g, maps, epi, st);
 }
 
-// Products whose few narrow tiles are shared by several units of `depth` stages:
+// Products whose few tiles are shared by several units of `depth` stages:
 // partial sums in the library's pool, and a launch that adds them up.
-template <int KIND, typename T, int A_MAJOR, bool B_MN>
+template <int KIND, typename T, int A_MAJOR, bool B_MN, int NT>
 cudaError_t store16_shared(const Product16* w, int count, int64_t depth, cudaStream_t st) {
     TileArgs g;
     TileMaps maps;
-    cudaError_t err = tile_args(w, count, 128, 1, 64, g, maps);
+    cudaError_t err = tile_args(w, count, NT, 1, B_MN ? 64 : NT / 2, g, maps);
     if (err != cudaSuccess) return err;
     AllPartialSums<T, kMaxProducts> sums = {};
-    EpiPartial<T, 128, kMaxProducts> epi = {};
+    EpiPartial<T, NT, kMaxProducts> epi = {};
     int64_t total = 0, most = 0;
     int shared = 0, of[kMaxProducts];
     for (int p = 0; p < count; ++p) {
@@ -460,10 +460,17 @@ cudaError_t store16_shared(const Product16* w, int count, int64_t depth, cudaStr
     return err == cudaSuccess ? freed : err;
 }
 
-// How deep the units of a launch with few narrow tiles had best be, from dealing
-// them out as the kernel does: in stages (0.2 us each), a unit costs its stages
-// and 8 more, adding partial sums up 20.  0: too many tiles for that to matter.
-int64_t shared_depth(const Product16* w, int count) {
+// How wide the tiles of a launch with few of them had best be and how deep its
+// units, from dealing them out as the kernel does: a unit costs its stages (0.2
+// us each, narrow ones kNarrow16 of that) and 8 more, adding partial sums up 20.
+// Sharing wide tiles moves a third less through L2 than narrow ones of the same
+// count (192 x 12288 -> 4096: 32 us narrow, 28 wide).
+struct Share {
+    int nt;         // 0: too many tiles for that to matter
+    int64_t depth;  // of a unit, at most
+    bool split;     // some tile is shared
+};
+Share best_share(const Product16* w, int count) {
     constexpr int kMaxPairs = 256;
     const int64_t pairs = std::min(kMaxPairs, std::max(1, tile_sms() / 2));
     int64_t deepest = 0, tiles = 0;
@@ -471,46 +478,53 @@ int64_t shared_depth(const Product16* w, int count) {
         deepest = std::max(deepest, w[p].stages());
         tiles += pair_tiles(w[p].M, w[p].N, 128);
     }
-    if (count == 0 || tiles > 2 * pairs) return 0;
-    int64_t best = deepest, best_cost = INT64_MAX;
-    for (int64_t depth = deepest; depth >= 12; depth = depth * 4 / 5) {
-        int64_t load[kMaxPairs] = {0}, t = 0, units = 0;
-        bool fits = true;
-        for (int p = 0; p < count && fits; ++p) {
-            const int64_t s = (w[p].stages() + depth - 1) / depth, each = (w[p].stages() + s - 1) / s + 8;
-            const int64_t n = pair_tiles(w[p].M, w[p].N, 128) * s;
-            units += n;
-            fits = s <= kMaxSplits && units <= 4 * pairs;
-            for (int64_t i = 0; i < n && fits; ++i, t = t + 1 == pairs ? 0 : t + 1) load[t] += each;
-        }
-        if (!fits) break;
-        const int64_t cost = *std::max_element(load, load + pairs) + (depth < deepest ? 20 : 0);
-        if (cost < best_cost) {
-            best_cost = cost;
-            best = depth;
+    Share best{0, deepest, false};
+    if (count == 0 || tiles > 2 * pairs) return best;
+    double best_cost = 1e30;
+    for (const int nt : {128, 256}) {
+        for (int64_t depth = deepest; depth >= 12; depth = depth * 3 / 4) {
+            double load[kMaxPairs] = {0};
+            int64_t t = 0, units = 0;
+            bool fits = true;
+            for (int p = 0; p < count && fits; ++p) {
+                const int64_t s = (w[p].stages() + depth - 1) / depth;
+                const int64_t n = pair_tiles(w[p].M, w[p].N, nt) * s;
+                const double each = (double)((w[p].stages() + s - 1) / s) * (nt == 128 ? kNarrow16 : 1.0) + 8;
+                units += n;
+                fits = s <= kMaxSplits && units <= 4 * pairs;
+                for (int64_t i = 0; i < n && fits; ++i, t = t + 1 == pairs ? 0 : t + 1) load[t] += each;
+            }
+            if (!fits) break;
+            const double cost = *std::max_element(load, load + pairs) + (depth < deepest ? 20 : 0);
+            if (cost < best_cost) {
+                best_cost = cost;
+                best = Share{nt, depth, depth < deepest};
+            }
+            if (deepest < 12) break;
         }
     }
+    if (best.nt == 0) best = Share{128, deepest, false};  // all shallower than 12
     return best;
 }
 
 // Products of one launch: shared if they are few and deep, else with the tiles
 // whose rounds are the shorter.
 template <int KIND, typename T, int A_MAJOR, bool B_MN>
-cudaError_t store16(const Product16* w, int count, cudaStream_t st) {
+cudaError_t store16(const Product16* w, int count, const Share& share, cudaStream_t st) {
     if (count == 0) return cudaSuccess;
-    int64_t wide = 0, narrow = 0, deepest = 0;
+    int64_t wide = 0, few = 0;
     bool aligned = true;
     for (int p = 0; p < count; ++p) {
         wide += pair_tiles(w[p].M, w[p].N, 256);
-        narrow += pair_tiles(w[p].M, w[p].N, 128);
-        deepest = std::max(deepest, w[p].stages());
+        few += pair_tiles(w[p].M, w[p].N, 128);
         aligned = aligned && aligned_rows<T>(w[p].C, w[p].ldc);
     }
-    const int64_t depth = shared_depth(w, count);
-    if (depth > 0 && depth < deepest) return store16_shared<KIND, T, A_MAJOR, B_MN>(w, count, depth, st);
-    auto f = narrow_tiles(wide, narrow, kNarrow16)
-                 ? (aligned ? store16_sized<KIND, T, A_MAJOR, B_MN, 128, true> : store16_sized<KIND, T, A_MAJOR, B_MN, 128, false>)
-                 : (aligned ? store16_sized<KIND, T, A_MAJOR, B_MN, 256, true> : store16_sized<KIND, T, A_MAJOR, B_MN, 256, false>);
+    if (share.split)
+        return share.nt == 128 ? store16_shared<KIND, T, A_MAJOR, B_MN, 128>(w, count, share.depth, st)
+                               : store16_shared<KIND, T, A_MAJOR, B_MN, 256>(w, count, share.depth, st);
+    const bool narrow = share.nt != 0 ? share.nt == 128 : narrow_tiles(wide, few, kNarrow16);
+    auto f = narrow ? (aligned ? store16_sized<KIND, T, A_MAJOR, B_MN, 128, true> : store16_sized<KIND, T, A_MAJOR, B_MN, 128, false>)
+                    : (aligned ? store16_sized<KIND, T, A_MAJOR, B_MN, 256, true> : store16_sized<KIND, T, A_MAJOR, B_MN, 256, false>);
     return f(w, count, st);
 }
 
@@ -538,7 +552,7 @@ cudaError_t forward_typed(const FfForward& f, cudaStream_t st) {
     if (f.T <= kSplitTokens16)
         return split16<KIND, false>(h, f.wd, f.wd, true, EpiSplitStore<T>{static_cast<T*>(f.y), f.ldy, f.D}, st);
     const Product16 y{{h}, {f.wd}, 1, false, f.T, f.D, f.F, f.y, f.ldy};
-    return store16<KIND, T, kMajorK, false>(&y, 1, st);
+    return store16<KIND, T, kMajorK, false>(&y, 1, best_share(&y, 1), st);
 }
 
 template <int KIND, typename T, int NT>
@@ -559,7 +573,7 @@ cudaError_t backward_typed(const FfBackward& f, cudaStream_t st) {
         err = narrow16(f.T, f.F, 256) ? gate_backward16<KIND, T, 128>(f, st) : gate_backward16<KIND, T, 256>(f, st);
     if (err != cudaSuccess) return err;
     // dx = dg Wg + du Wu; the weights' gradients are sums over the T rows of both
-    // operands.  All in one launch where the tiles are few (shared_depth); else dx
+    // operands.  All in one launch where the tiles are few (best_share); else dx
     // by itself (its tiles are of another depth: dealt out with the others, some
     // pairs would have one more of the deep ones).
     Product16 w[kMaxProducts];
@@ -569,9 +583,11 @@ cudaError_t backward_typed(const FfBackward& f, cudaStream_t st) {
     if (f.dwg != nullptr) w[count++] = Product16{{dg}, {f.x}, 1, true, f.F, f.D, f.T, f.dwg, f.lddwg};
     if (f.dwu != nullptr) w[count++] = Product16{{du}, {f.x}, 1, true, f.F, f.D, f.T, f.dwu, f.lddwu};
     if (f.dwd != nullptr) w[count++] = Product16{{f.dy}, {h}, 1, true, f.D, f.F, f.T, f.dwd, f.lddwd};
-    if (shared_depth(w, count) > 0) return store16<KIND, T, kMajorAny, true>(w, count, st);
-    err = store16<KIND, T, kMajorAny, true>(w, others, st);
-    return err != cudaSuccess ? err : store16<KIND, T, kMajorAny, true>(w + others, count - others, st);
+    const Share all = best_share(w, count);
+    if (all.nt != 0) return store16<KIND, T, kMajorAny, true>(w, count, all, st);
+    err = store16<KIND, T, kMajorAny, true>(w, others, best_share(w, others), st);
+    if (err != cudaSuccess) return err;
+    return store16<KIND, T, kMajorAny, true>(w + others, count - others, best_share(w + others, count - others), st);
 }
 
 }  // namespace
