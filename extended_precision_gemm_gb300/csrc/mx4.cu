@@ -3,7 +3,7 @@
 // Quantisation reads each value once and writes 4 bits and its share of a
 // scale byte: bound by HBM (2.56 bytes per 16-bit value for nvfp4, 2.53 for
 // mxfp4) with about 10 instructions to hide for every 32 values of a warp.
-// Columns of 8192 x 16384 16-bit values to nvfp4: 59 us and 24 us to finish the
+// Columns of 8192 x 16384 16-bit values to nvfp4: 59 us and 22 us to finish the
 // scales (0.86 of the copy rate in the first, 63% of the issue slots); back to
 // 16 bits 51 us (343 MB, 0.98 of the copy rate).  4096 x 4096 rows to mxfp4:
 // 12.5 us (43 MB); one row of 8192: 3 us, the latency of a launch.

@@ -1,5 +1,9 @@
 // mx4_gemm.cu -- products of matrices in 4-bit microscaled form
-// (C = alpha A B^T) and the two products of the 4-bit gated block.
+// (C = alpha A B^T) and the two products of the 4-bit gated block: operands,
+// epilogues and launches for the two kernels that multiply.  Up to 64 rows of A
+// the weights are what has to be moved and split_gemm.cuh streams them over all
+// SMs (HBM; 1 x 8192 x 8192 nvfp4 8.5 us); more rows are the tensor pipe's work
+// and go by CTA pairs in tile_gemm.cuh (8192^3 nvfp4 163 us).
 #include "activation.cuh"
 #include "mx4.cuh"
 #include "split_gemm.cuh"

@@ -13,8 +13,9 @@
 // every other 16 tokens); all take part in the final sums.  Two CTAs fit an SM.
 //
 // The wait for the launch before this one: the next stages of a CTA's weights
-// are fetched into L2 ahead of it (kAhead of them: all would not stay there), and if the weights are EARLY (nothing that the
-// launch before this one writes), the ring is filled with them ahead of it.
+// are fetched into L2 ahead of it (kAhead of them: all would not stay there),
+// and if the weights are EARLY (nothing that the launch before this one
+// writes), the ring is filled with them ahead of it.
 //
 // Weights of 37.7 MB from HBM (8192 x 8192 nvfp4) with one token: 9.2 us, 4.1
 // TB/s; the 16-bit block of 302 MB: 51 us, 5.9 TB/s, 0.87 of the copy rate.  A

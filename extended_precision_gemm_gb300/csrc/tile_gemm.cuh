@@ -4,21 +4,22 @@
 // accumulators.  Everything is in an unnamed namespace, so each including file
 // has its own count of bounded waits that gave up.
 //
-// D = sum over k of A[m, k] B[n, k], for up to four products in one launch.  A pair of CTAs on two SMs owns a tile of 256 m by
-// NT n: each CTA holds 128 rows of A, one half of the rows of B, and
-// 128 rows of the accumulators (f32, in tensor memory, twice: the MMAs of a
-// tile overlap the epilogue of the one before).  A stage of the shared-memory
-// ring is 128 bytes of k.  Warps: 0 copies (TMA), 1 issues the MMAs (even CTA
-// only), the others run the epilogue, four warps (128 rows) for each group of
-// columns.
+// D = sum over k of A[m, k] B[n, k], for up to four products in one launch.  A
+// pair of CTAs on two SMs owns a tile of 256 m by NT n: each CTA holds 128 rows
+// of A, one half of the rows of B, and 128 rows of the accumulators (f32, in
+// tensor memory, twice: the MMAs of a tile overlap the epilogue of the one
+// before).  A stage of the shared-memory ring is 128 bytes of k.  Warps: 0 copies
+// (TMA), 1 issues the MMAs (even CTA only), the others run the epilogue, four
+// warps (128 rows) for each group of columns.
 //
 // Where the tiles are few and deep, the stages of a tile are shared out among
 // several units of work (splits), whose partial sums an epilogue leaves in
 // planes of their own to be added afterwards.
 //
-// 16-bit operands: NT = 256 (128 where that fills the SMs better), 64 k to a stage, either operand with k contiguous
-// or with its row index contiguous (64 x 64 blocks, the same swizzle); the
-// sum may run over two segments (A0 B0^T + A1 B1^T).
+// 16-bit operands: NT = 256 (128 where that fills the SMs better), 64 k to a
+// stage, either operand with k contiguous or with its row index contiguous
+// (64 x 64 blocks, the same swizzle); the sum may run over two segments
+// (A0 B0^T + A1 B1^T).
 // 4-bit operands: NT = 192 (or 128), 256 k to a stage; two accumulators of 192
 // columns leave 128 columns of tensor memory to the scales (16 for A's 128
 // rows, 32 for two tiles of 128 rows of B, twice).  192 rows of B start at a
@@ -443,21 +444,23 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) 
     return w;
 }
 
-// Whether the rows of a matrix are 16-byte aligned.
+// Whether the rows of a matrix begin at whole 32-byte sectors.
 template <typename T>
 inline bool aligned_rows(const void* C, int64_t ldc) {
-    return ((uintptr_t)C | (uintptr_t)(ldc * (int64_t)sizeof(T))) % 16 == 0;
+    return ((uintptr_t)C | (uintptr_t)(ldc * (int64_t)sizeof(T))) % 32 == 0;
 }
 
-// A warp's 32 x 32 block: lane l holds row l of it on entry, column l on return.
-__device__ __forceinline__ void transpose32(float (&v)[32], int lane) {
+// Blocks of N x N words, one in each N lanes of a warp: lane l holds row l of
+// its block on entry, column l on return.
+template <int N, typename W>
+__device__ __forceinline__ void turn(W (&v)[N], int lane) {
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) {
+    for (int s = N / 2; s > 0; s >>= 1) {
         const bool up = (lane & s) != 0;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < N; ++i) {
             if (i & s) continue;
-            const float got = __shfl_xor_sync(~0u, up ? v[i] : v[i | s], s);
+            const W got = __shfl_xor_sync(~0u, up ? v[i] : v[i | s], s);
             v[i] = up ? got : v[i];
             v[i | s] = up ? v[i | s] : got;
         }
@@ -466,13 +469,15 @@ __device__ __forceinline__ void transpose32(float (&v)[32], int lane) {
 
 // A warp's 32 rows by 32 columns of C from (row0, c) on; lane l holds row
 // row0 + l.  Rows and columns beyond M and N are left out.  ALIGNED rows leave
-// in whole 32-byte sectors, or in 16-byte pieces where they are aligned to no
-// more (half sectors: 144 us instead of 122 for 4096 x 24576 x 4096 mxfp4, whose
-// output is 201 MB).  Others are turned first, so that a warp's stores are
-// contiguous (row by row, an element a lane): a thread storing its own row
+// in whole 32-byte sectors.  Others are turned first, so that a warp's stores
+// are contiguous: 32 elements of a row, or, of 16-bit elements whose rows are
+// 4-byte aligned, 16 words of each of two.  (A thread storing its own row
 // element by element made a product of 333 x 2050 x 4100 take 27 us instead of
-// 14.  (A variant of the kernel for each: both paths in one cost the aligned
-// one registers, 12% of a 4096^3 nvfp4 product.)
+// 14.  8192 x N x 1024 mxfp4, in bf16: 39 us for N = 8192, 51 for 8190, 87 for
+// 8191, 84 for 8190 without the words; in f32 84 for 8188, 175 with each row
+// stored by its thread in 16-byte pieces, 107 for 8191.  A variant of the kernel
+// for each: both paths in one cost the aligned one registers, 12% of a 4096^3
+// nvfp4 product.)
 template <bool ALIGNED, typename T>
 __device__ __forceinline__ void store_block(T* C, int64_t ldc, int64_t row0, int64_t M, int64_t c, int64_t N,
                                             float (&v)[32], int lane) {
@@ -481,7 +486,6 @@ __device__ __forceinline__ void store_block(T* C, int64_t ldc, int64_t row0, int
         T* p = C + (row0 + lane) * ldc + c;
         constexpr int PER = 32 / sizeof(T);
         if (c + 32 <= N) {
-            const bool sectors = (uintptr_t)p % 32 == 0 && ldc * sizeof(T) % 32 == 0;  // the same in all lanes
 #pragma unroll
             for (int i = 0; i < 32; i += PER) {
                 uint32_t w[8];
@@ -490,12 +494,7 @@ __device__ __forceinline__ void store_block(T* C, int64_t ldc, int64_t row0, int
                     if constexpr (sizeof(T) == 4) w[j] = __float_as_uint(v[i + j]);
                     else w[j] = pack2<T>(v[i + 2 * j], v[i + 2 * j + 1]);
                 }
-                if (sectors) {
-                    store_v8(p + i, w);
-                } else {
-                    reinterpret_cast<uint4*>(p + i)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                    reinterpret_cast<uint4*>(p + i)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                }
+                store_v8(p + i, w);
             }
         } else {
 #pragma unroll
@@ -504,7 +503,28 @@ __device__ __forceinline__ void store_block(T* C, int64_t ldc, int64_t row0, int
         }
     } else {
         if (c >= N || row0 >= M) return;
-        transpose32(v, lane);
+        if constexpr (sizeof(T) == 2) {
+            if (((uintptr_t)C | (uintptr_t)(ldc * 2)) % 4 == 0) {
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+                turn<16>(w, lane);  // word i: row (lane & 16) + i, columns 2 (lane & 15) and the next
+                const int64_t row = row0 + (lane & 16), col = c + 2 * (lane & 15);
+                const int rows = (int)min((int64_t)16, max((int64_t)0, M - row));
+                T* p = C + row * ldc + col;
+                if (col + 1 < N) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (i < rows) *reinterpret_cast<uint32_t*>(p + i * ldc) = w[i];
+                } else if (col < N) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (i < rows) reinterpret_cast<uint16_t*>(p)[i * ldc] = (uint16_t)w[i];
+                }
+                return;
+            }
+        }
+        turn<32>(v, lane);
         const int rows = (int)min((int64_t)32, M - row0);
         T* p = C + row0 * ldc + c + lane;
         if (c + lane < N) {

@@ -238,6 +238,21 @@ def test_product_into_strided_output_and_empty_sums():
         assert ddg.mx4_gemm(z, ddg.mx4_quantize(torch.randn(9, 64, device="cuda"), fmt)).shape == (0, 9)
 
 
+@pytest.mark.parametrize("dtype", ("bfloat16", "float16", "float32"))
+@pytest.mark.parametrize("m,n", [(300, 601), (261, 514), (129, 96), (300, 33)])
+def test_product_into_rows_of_every_alignment(m, n, dtype):
+    torch = _torch()
+    t = getattr(torch, dtype)
+    qa, qb = (ddg.mx4_quantize(torch.randn(r, 320, device="cuda"), "nvfp4") for r in (m, n))
+    want = ddg.mx4_gemm(qa, qb, dtype=t)
+    for ld in (640, 648, 642, 641):  # rows of whole sectors, of 16 bytes, of words, of elements
+        for first in (0, 1, 2, 8, 16):
+            out = torch.full((m, ld), 5.0, dtype=t, device="cuda")
+            ddg.mx4_gemm(qa, qb, out=out[:, first:first + n])
+            assert torch.equal(out[:, first:first + n], want), (ld, first)
+            assert (out[:, :first] == 5).all() and (out[:, first + n:] == 5).all(), (ld, first)
+
+
 def test_operands_with_wide_rows_and_scales_quantised_elsewhere():
     torch = _torch()
     x = torch.randn(40, 512, device="cuda")
