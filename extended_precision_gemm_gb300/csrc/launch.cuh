@@ -171,8 +171,9 @@ struct Mx4Matrix {
     int64_t rows, K;
 };
 // X (rows x K, or K x rows if cols) of type DDGEMM_F32 / _BF16 / _F16 into
-// codes, scales and (nvfp4) row exponents; most: a workspace of the largest
-// magnitude of every block, rows x 4 scale tiles, nvfp4 columns only.
+// codes, scales and (nvfp4) row exponents; most: a workspace of 17 values for
+// every 256 k of a row, the largest magnitudes of its 16 blocks and of all of
+// them, nvfp4 columns only.
 struct Mx4Quantize {
     int fmt, type;
     bool cols;

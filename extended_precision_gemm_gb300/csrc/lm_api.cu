@@ -214,7 +214,7 @@ ddgemm_status dd_mx4_quantize(int format, int type, int columns, int64_t rows, i
     if (overlaps_mx4(format, q, X, span(xr, xc, ldx, type_bytes(type)))) return DDGEMM_ERR_INVALID_ARG;
     Workspace ws(st);
     const bool maxima = columns && format == DDGEMM_NVFP4;
-    if (maxima) ws.reserve(rows * mx4_scale_tiles(format, K) * 4 * 4);
+    if (maxima) ws.reserve(rows * mx4_scale_tiles(format, K) / 4 * 17 * 4);
     if (!ws.allocate()) return DDGEMM_ERR_ALLOC;
     return status_of(launch_mx4_quantize(Mx4Quantize{format, type, columns == 1, rows, K, X, ldx, codes, ldq, scales,
                                                      exponents, maxima ? ws.at<float>(0) : nullptr},

@@ -3,8 +3,8 @@
 // Quantisation reads each value once and writes 4 bits and its share of a
 // scale byte: bound by HBM (2.56 bytes per 16-bit value for nvfp4, 2.53 for
 // mxfp4) with about 10 instructions to hide for every 32 values of a warp.
-// Columns of 8192 x 16384 16-bit values to nvfp4: 59 us and 22 us to finish the
-// scales (0.86 of the copy rate in the first, 63% of the issue slots); back to
+// Columns of 8192 x 16384 16-bit values to nvfp4: 56 us and 15 us to finish the
+// scales (0.90 of the copy rate in the first, 63% of the issue slots); back to
 // 16 bits 51 us (343 MB, 0.98 of the copy rate).  4096 x 4096 rows to mxfp4:
 // 12.5 us (43 MB); one row of 8192: 3 us, the latency of a launch.
 #include "launch.cuh"
@@ -234,6 +234,11 @@ __device__ __forceinline__ void load_columns(const T* X, int64_t ldx, int64_t k,
     }
 }
 
+// The largest of four blocks' finite magnitudes (the sign bit is a mark).
+__device__ __forceinline__ uint32_t largest(const uint4& b) {
+    return max(max(b.x & 0x7fffffffu, b.y & 0x7fffffffu), max(b.z & 0x7fffffffu, b.w & 0x7fffffffu));
+}
+
 // Columns of X (K x R) as rows of the result: a block takes 64 columns and 256
 // k.  Warp w reads rows 32 w .. + 31, a lane two columns of them, so a lane
 // holds whole blocks of k and needs no exchange for their maxima; codes and
@@ -242,7 +247,7 @@ __device__ __forceinline__ void load_columns(const T* X, int64_t ldx, int64_t k,
 // are made with nvfp4_wide_step, and the blocks' largest magnitudes go to `most`
 // for nvfp4_finish_kernel, which a pass over X for the columns' maxima ahead of
 // this one would replace at 0.25 bytes a value less written but 2 more read
-// (8192 x 16384 values: 102 us with that pass, 83 without).
+// (8192 x 16384 values: 102 us with that pass, 71 without).
 template <typename T, int FMT>
 __global__ void __launch_bounds__(256) mx4_columns_kernel(const T* X, int64_t ldx, int64_t R, int64_t K, bool vec,
                                                           uint8_t* codes, int64_t ldq, uint8_t* scales, float* most) {
@@ -311,20 +316,24 @@ __global__ void __launch_bounds__(256) mx4_columns_kernel(const T* X, int64_t ld
             const int64_t row = r0 + p % 32 * 2 + p / 32;
             if (row < R) *reinterpret_cast<uint32_t*>(scales + mx4_scale_word(row, kt * WORDS + w, tiles)) = scale[p][w];
         }
-    } else {  // 16 magnitudes a row: 64 bytes, 4 threads a row
-        const int p = threadIdx.x / 4, at = threadIdx.x % 4 * 4;
-        const int64_t row = r0 + p % 32 * 2 + p / 32;
-        if (row < R)
-            *reinterpret_cast<uint4*>(most + row * tiles * 4 + kt * 16 + at) =
-                make_uint4(scale[p][at], scale[p][at + 1], scale[p][at + 2], scale[p][at + 3]);
+    } else {  // 16 magnitudes a row: 64 bytes, 4 threads a row; after all of them, the largest finite one of the 16
+        const int i = threadIdx.x / 4, p = i % 2 * 32 + i / 2, at = threadIdx.x % 4 * 4;
+        const int64_t row = r0 + i;
+        const uint4 b = make_uint4(scale[p][at], scale[p][at + 1], scale[p][at + 2], scale[p][at + 3]);
+        uint32_t m = largest(b);
+        m = max(m, __shfl_xor_sync(~0u, m, 1));
+        m = max(m, __shfl_xor_sync(~0u, m, 2));
+        if (row < R) {
+            reinterpret_cast<uint4*>(most)[(kt * R + row) * 4 + at / 4] = b;
+            if (at == 0) reinterpret_cast<uint32_t*>(most)[gridDim.y * R * 16 + kt * R + row] = m;
+        }
     }
 }
 
 // nvfp4 rows whose codes were made block by block with nvfp4_wide_step: from
 // the blocks' largest finite magnitudes (the sign bit marks a block that also
 // holds an infinity or a NaN; tiles * 4 values a row, 0 beyond K) the row's
-// exponent and the scales, one block of threads for a row.  Where a scale is
-// subnormal (the block's largest is below 2^-14.8 of the row's) the step has
+// exponent and the scales.  Where a scale is subnormal (the block's largest is below 2^-14.8 of the row's) the step has
 // fewer bits than the codes were made with: they are made again, from the
 // values themselves (row i being column i of X) or, without X, from the codes.
 template <typename T>
@@ -354,43 +363,124 @@ __device__ __forceinline__ void remake_codes(uint32_t word, uint4 b, int e, int6
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) nvfp4_finish_kernel(const float* most, int64_t K, uint8_t* codes, int64_t ldq,
-                                                           uint8_t* scales, int32_t* exponents, const T* X, int64_t ldx) {
+// A block of threads takes a row, or (WARP) a warp, which needs no barrier: many
+// rows of at most 128 tiles, which a warp holds in registers (the block of 8192 x
+// 1024 x 2048 78 us, 84 otherwise; no gain from 256 tiles on, 363 us for 361).
+template <bool WARP>
+__global__ void __launch_bounds__(256, 4) nvfp4_finish_kernel(const float* most, int64_t rows, int64_t K, uint8_t* codes,
+                                                              int64_t ldq, uint8_t* scales, int32_t* exponents) {
+    constexpr int KEPT = WARP ? 4 : 1;  // a thread's first tiles stay in registers, others are read again
     __shared__ uint32_t part[8];
     pdl_wait();
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int64_t row = blockIdx.x, tiles = mx4_scale_tiles(kNvfp4, K);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = WARP ? (int64_t)blockIdx.x * 8 + warp : blockIdx.x, tiles = mx4_scale_tiles(kNvfp4, K);
+    const int first = WARP ? lane : threadIdx.x, step = WARP ? 32 : blockDim.x;
+    if (WARP && row >= rows) return;
     const uint4* src = reinterpret_cast<const uint4*>(most) + row * tiles;
-    auto most4 = [](const uint4& b) {
-        return max(max(b.x & 0x7fffffffu, b.y & 0x7fffffffu), max(b.z & 0x7fffffffu, b.w & 0x7fffffffu));
-    };
-    // a thread's first tile stays in registers; rows beyond 16384 are read again
-    const uint4 kept = threadIdx.x < tiles ? src[threadIdx.x] : make_uint4(0, 0, 0, 0);
-    uint32_t m = most4(kept);
-    for (int64_t t = threadIdx.x + blockDim.x; t < tiles; t += blockDim.x) m = max(m, most4(src[t]));
+    uint4 kept[KEPT];
+#pragma unroll
+    for (int j = 0; j < KEPT; ++j) kept[j] = first + j * step < tiles ? src[first + j * step] : make_uint4(0, 0, 0, 0);
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < KEPT; ++j) m = max(m, largest(kept[j]));
+    for (int64_t t = first + KEPT * step; t < tiles; t += step) m = max(m, largest(src[t]));
     m = __reduce_max_sync(~0u, m);
-    if (lane == 0) part[warp] = m;
-    __syncthreads();
-    m = part[0];
-    for (int w = 1; w < warps; ++w) m = max(m, part[w]);
+    if constexpr (!WARP) {
+        if (lane == 0) part[warp] = m;
+        __syncthreads();
+        m = part[0];
+        for (int w = 1; w < blockDim.x >> 5; ++w) m = max(m, part[w]);
+    }
     const int e = nvfp4_row_exponent(m);
     const float unit = exp2_int(-e);
-    if (threadIdx.x == 0) exponents[row] = e;
-    for (int64_t t = threadIdx.x; t < tiles; t += blockDim.x) {
-        const uint4 b = t == threadIdx.x ? kept : src[t];
-        const uint32_t bits[4] = {b.x, b.y, b.z, b.w};
-        uint32_t word = 0;
-        bool low = false;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t byte = bits[i] >> 31 ? 127u : nvfp4_scale_byte(bits[i], unit);
-            word |= byte << (8 * i);
-            low |= byte > 0u && byte <= 8u;  // 8: the least normal one, perhaps rounded up to
-        }
-        if (low) remake_codes(word, b, e, t, row, K, codes + row * ldq, X, ldx);
+    if (first == 0) exponents[row] = e;
+    bool low = false;
+    auto tile = [&](const uint4& b, int64_t t) {
+        const uint32_t word = nvfp4_scale_bytes(b, unit);
+        low |= nvfp4_low_scales(word);
         *reinterpret_cast<uint32_t*>(scales + mx4_scale_word(row, t, tiles)) = word;
+    };
+#pragma unroll
+    for (int j = 0; j < KEPT; ++j)
+        if (first + j * step < tiles) tile(kept[j], first + j * step);
+    for (int64_t t = first + KEPT * step; t < tiles; t += step) tile(src[t], t);
+    if (!low) return;
+#pragma unroll 1
+    for (int64_t t = first; t < tiles; t += step) {
+        const uint32_t word = nvfp4_scale_bytes(src[t], unit);
+        if (nvfp4_low_scales(word)) remake_codes<float>(word, src[t], e, t, row, K, codes + row * ldq, nullptr, 0);
+    }
+}
+
+// The same for what mx4_columns_kernel leaves: for every 256 k the blocks'
+// magnitudes, 16 a row, and after all of them the rows' largest.  A block of
+// threads takes the 128 rows of a scale tile and 1024 k: all it reads and the
+// scales it writes are contiguous.  (8192 x 16384: 15 us; 22 with a row for a
+// block of threads, whose scales left 4 bytes at a time.)
+template <typename T>
+__global__ void __launch_bounds__(256) nvfp4_finish_columns_kernel(const uint32_t* most, int64_t R, int64_t K, uint8_t* codes,
+                                                                   int64_t ldq, uint8_t* scales, int32_t* exponents,
+                                                                   const T* X, int64_t ldx) {
+    constexpr int KTS = 4, N = 128 * 4 * KTS / 256;
+    __shared__ uint32_t part[2][128];
+    __shared__ uint32_t words[KTS * 4][128];  // a scale tile each
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t r0 = (int64_t)blockIdx.x * 128, kt0 = (int64_t)blockIdx.y * KTS, kts = (K + MX4_TILE_K - 1) / MX4_TILE_K;
+    const int64_t tiles = kts * 4;
+    const int at = threadIdx.x % 4, i0 = threadIdx.x / 4;  // tile of its 256 k, row (and the 64th after it)
+    uint4 b[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int64_t kt = kt0 + j / 2, row = r0 + i0 + j % 2 * 64;
+        b[j] = kt < kts && row < R ? reinterpret_cast<const uint4*>(most)[(kt * R + row) * 4 + at] : make_uint4(0, 0, 0, 0);
+    }
+    {
+        const int i = threadIdx.x % 128, half = threadIdx.x / 128;
+        const uint32_t* rows = most + kts * R * 16 + r0 + i;
+        uint32_t m = 0;
+        if (r0 + i < R) {
+#pragma unroll 8
+            for (int64_t kt = half; kt < kts; kt += 2) m = max(m, rows[kt * R]);
+        }
+        part[half][i] = m;
+    }
+    __syncthreads();
+    int e[2];
+    float unit[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        e[j] = nvfp4_row_exponent(max(part[0][i0 + j * 64], part[1][i0 + j * 64]));
+        unit[j] = exp2_int(-e[j]);
+        if (blockIdx.y == 0 && at == 0 && r0 + i0 + j * 64 < R) exponents[r0 + i0 + j * 64] = e[j];
+    }
+    uint32_t low = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const uint32_t word = nvfp4_scale_bytes(b[j], unit[j % 2]);
+        const int i = i0 + j % 2 * 64;
+        words[j / 2 * 4 + at][i % 32 * 4 + i / 32] = word;
+        low |= (uint32_t)nvfp4_low_scales(word) << j;
+    }
+    __syncthreads();
+    const int64_t left = min((int64_t)KTS * 4, tiles - kt0 * 4);
+    uint8_t* to = scales + mx4_scale_word(r0, kt0 * 4, tiles);
+    if (r0 + 128 <= R) {
+#pragma unroll
+        for (int i = threadIdx.x; i < KTS * 4 * 32; i += 256)
+            if (i / 32 < left)
+                reinterpret_cast<uint4*>(to)[i] = *reinterpret_cast<const uint4*>(&words[i / 32][i % 32 * 4]);
+    } else {
+        for (int i = threadIdx.x; i < KTS * 4 * 128; i += 256)
+            if (i / 128 < left && r0 + i % 128 / 4 + i % 4 * 32 < R) reinterpret_cast<uint32_t*>(to)[i] = words[i / 128][i % 128];
+    }
+    while (low != 0u) {
+        const int j = __ffs(low) - 1;
+        low &= low - 1;
+        const int64_t kt = kt0 + j / 2, row = r0 + i0 + j % 2 * 64;
+        const uint4 again = reinterpret_cast<const uint4*>(most)[(kt * R + row) * 4 + at];
+        remake_codes(nvfp4_scale_bytes(again, unit[j % 2]), again, e[j % 2], kt * 4 + at, row, K, codes + row * ldq, X, ldx);
     }
 }
 
@@ -445,15 +535,6 @@ __global__ void __launch_bounds__(QWARPS * 32) mx4_dequantize_kernel(const uint8
 }
 
 template <typename T>
-cudaError_t finish(const float* most, int64_t rows, int64_t K, uint8_t* codes, int64_t ldq, uint8_t* scales,
-                   int32_t* exponents, const T* X, int64_t ldx, cudaStream_t st) {
-    const int64_t tiles = mx4_scale_tiles(kNvfp4, K);
-    const unsigned threads = (unsigned)(tiles >= 256 ? 256 : (tiles + 31) / 32 * 32);
-    return launch_pdl(nvfp4_finish_kernel<T>, dim3((unsigned)rows), dim3(threads), 0, st, most, K, codes, ldq, scales,
-                      exponents, X, ldx);
-}
-
-template <typename T>
 cudaError_t quantize_typed(const Mx4Quantize& q, const T* X, cudaStream_t st) {
     const int64_t kts = (q.K + MX4_TILE_K - 1) / MX4_TILE_K;
     if (!q.cols) {
@@ -478,7 +559,9 @@ cudaError_t quantize_typed(const Mx4Quantize& q, const T* X, cudaStream_t st) {
                         : launch_pdl(mx4_columns_kernel<T, kNvfp4>, grid, dim3(256), 0, st, X, q.ldx, q.rows, q.K, vec,
                                      q.codes, q.ldq, (uint8_t*)nullptr, q.most);
     if (err != cudaSuccess || q.fmt == kMxfp4) return err;
-    return finish(q.most, q.rows, q.K, q.codes, q.ldq, q.scales, q.exponents, X, q.ldx, st);
+    return launch_pdl(nvfp4_finish_columns_kernel<T>, dim3((unsigned)((q.rows + 127) / 128), (unsigned)((kts + 3) / 4)),
+                      dim3(256), 0, st, reinterpret_cast<const uint32_t*>(q.most), q.rows, q.K, q.codes, q.ldq, q.scales,
+                      q.exponents, X, q.ldx);
 }
 
 template <typename T>
@@ -507,7 +590,13 @@ cudaError_t launch_mx4_quantize(const Mx4Quantize& q, cudaStream_t st) {
 cudaError_t launch_nvfp4_finish(const float* most, int64_t rows, int64_t K, uint8_t* codes, int64_t ldq, uint8_t* scales,
                                 int32_t* exponents, cudaStream_t st) {
     if (rows == 0 || K == 0) return cudaSuccess;
-    return finish<float>(most, rows, K, codes, ldq, scales, exponents, nullptr, 0, st);
+    const int64_t tiles = mx4_scale_tiles(kNvfp4, K);
+    if (rows >= 152 * 16 && tiles <= 128)
+        return launch_pdl(nvfp4_finish_kernel<true>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, most, rows, K,
+                          codes, ldq, scales, exponents);
+    const unsigned threads = (unsigned)(tiles >= 256 ? 256 : (tiles + 31) / 32 * 32);
+    return launch_pdl(nvfp4_finish_kernel<false>, dim3((unsigned)rows), dim3(threads), 0, st, most, rows, K, codes, ldq,
+                      scales, exponents);
 }
 
 cudaError_t launch_mx4_dequantize(int fmt, int type, int64_t rows, int64_t K, const uint8_t* codes, int64_t ldq,

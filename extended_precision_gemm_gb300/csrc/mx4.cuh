@@ -162,6 +162,42 @@ __device__ __forceinline__ uint64_t quotient_pair(uint64_t y, uint64_t minus_s, 
     return fma_pair(fma_pair(q, minus_s, y), r, q);
 }
 
+// The bytes of four blocks, the first lowest, where the sign bit marks a block
+// that is to be NaN: the same operations, two blocks at a time.
+__device__ __forceinline__ uint32_t nvfp4_scale_bytes(const uint4& marked, float unit) {
+    const uint32_t bits[4] = {marked.x & 0x7fffffffu, marked.y & 0x7fffffffu, marked.z & 0x7fffffffu,
+                              marked.w & 0x7fffffffu};
+    const uint64_t minus_six = pack_pair(-6.0f, -6.0f), part = pack_pair(1.0f / 6.0f, 1.0f / 6.0f), units = pack_pair(unit, unit);
+    float want[4];
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        const uint64_t most = pack_pair(__uint_as_float(bits[i]), __uint_as_float(bits[i + 1]));
+        unpack_pair(mul_pair(quotient_pair(most, minus_six, part), units), want[i], want[i + 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) want[i] = bits[i] != 0u ? fmaxf(want[i], 0x1p-9f) : 0.0f;
+    uint32_t word;
+    asm("{\n"
+        " .reg .b16 t0, t1;\n"
+        " cvt.rn.satfinite.e4m3x2.f32 t0, %2, %1;\n"
+        " cvt.rn.satfinite.e4m3x2.f32 t1, %4, %3;\n"
+        " mov.b32 %0, {t0, t1};\n"
+        "}\n"
+        : "=r"(word)
+        : "f"(want[0]), "f"(want[1]), "f"(want[2]), "f"(want[3]));
+    if ((marked.x | marked.y | marked.z | marked.w) >> 31) {
+        word |= (marked.x >> 31) * 0x7fu | (marked.y >> 31) * 0x7f00u | (marked.z >> 31) * 0x7f0000u |
+                (marked.w >> 31) * 0x7f000000u;
+    }
+    return word;
+}
+
+// Whether one of four bytes (none above 127) is 1 to 8: a subnormal scale, or
+// the least normal one, perhaps rounded up to.
+__device__ __forceinline__ bool nvfp4_low_scales(uint32_t word) {
+    return ((word + 0x7f7f7f7fu) & ~(word + 0x77777777u) & 0x80808080u) != 0u;
+}
+
 // Eight values (already divided by their scales) as eight E2M1 codes, the
 // first in the lowest nibble; to nearest, ties to even, saturating at 6.
 __device__ __forceinline__ uint32_t e2m1_pack8(const float (&y)[8]) {

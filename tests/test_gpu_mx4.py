@@ -128,6 +128,22 @@ def test_infinities_and_nans_stay_in_their_blocks(fmt, cols):
     assert np.array_equal(np.isnan(d), np.isnan(v)) and np.array_equal(np.nan_to_num(d), np.nan_to_num(v).astype(np.float32))
 
 
+@pytest.mark.parametrize("dtype", ("bfloat16", "float16", "float32"))
+@pytest.mark.parametrize("rows,k", [(128, 1024), (300, 2600), (257, 4099), (1030, 1300)])
+def test_columns_with_blocks_far_apart(rows, k, dtype):
+    torch = _torch()
+    rng = np.random.default_rng(rows)
+    x = sample(rows, k, rows) * np.repeat(2.0 ** -rng.integers(0, 24, (rows, -(-k // 16))), 16, axis=1)[:, :k]
+    x[rng.integers(0, rows, 40), rng.integers(0, k, 40)] = np.tile([np.inf, -np.inf, np.nan, 0.0], 10)
+    x = torch.from_numpy(x).to(_dtype(dtype))
+    for fmt in FORMATS:
+        q = ddg.mx4_quantize(x.t().contiguous().cuda(), fmt, cols=True)
+        check_quantised(q, x.double().numpy())
+        r = ddg.mx4_quantize(x.cuda(), fmt)
+        v, w = (ddg.mx4_dequantize(t, torch.float32).nan_to_num(7e30) for t in (q, r))
+        assert torch.equal(v, w)
+
+
 def test_quantise_strided_and_misaligned_inputs():
     torch = _torch()
     base = torch.randn(70, 700, device="cuda").to(torch.bfloat16)

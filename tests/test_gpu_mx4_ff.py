@@ -168,3 +168,13 @@ def test_hidden_blocks_far_below_the_row(T):
     want = q @ vd.T
     room = worst @ np.abs(vd).T + 2.0**-18 * (np.abs(q) @ np.abs(vd).T)
     assert (np.abs(y - want) <= room).all(), (np.abs(y - want) / room).max()
+
+
+@pytest.mark.parametrize("fmt", ("mxfp4", "nvfp4"))
+@pytest.mark.parametrize("T,D,F", [(2433, 64, 160), (3001, 96, 8200)])
+def test_many_tokens(T, D, F, fmt):
+    check_block(T, D, F, fmt, "bfloat16", "silu", T)
+
+
+def test_hidden_blocks_far_below_the_row_for_many_tokens():
+    test_hidden_blocks_far_below_the_row(2600)
