@@ -12,6 +12,15 @@
 // du themselves.  For bfloat16 (8 significant bits) they are kept as float16 (11)
 // with a power of two for every 32 of a row, which takes 2 bytes and leaves the
 // gradients' error as 32 bits would; for float16 in 32 bits.
+//
+// h, dg and du are rounded to the type before the next product.  Of many tokens
+// these roundings average out: an output's error is 1.41 times that of its own
+// rounding.  Of up to kFullTokens the few largest values decide, and it was up
+// to 1.55 times: there what the rounding leaves is kept in as many rows more and
+// enters the products too (16 significant bits for bfloat16, 22 for float16),
+// which costs little, as the weights bind and tiles are mostly idle (4096 x
+// 12288, one token: 50.2 us for 50.0, forward and backward 218 for 214; 16 tokens
+// 53.4 for 52.7 and 201 for 195).
 #include "activation.cuh"
 #include "mx4.cuh"
 #include "split_gemm.cuh"
@@ -83,6 +92,13 @@ __device__ __forceinline__ void kept16(const float* plane, const uint8_t*, int64
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[8 * k + i] = __uint_as_float(w[i]);
     }
+}
+
+// The part of v that hi, v rounded, leaves (0 where that is infinite or NaN).
+template <typename T>
+__device__ __forceinline__ float remainder_of(float v, T hi) {
+    const float h = to_float<T>(hi);
+    return finite_bits(h) == (__float_as_uint(h) & 0x7fffffffu) ? v - h : 0.0f;
 }
 
 // C = accumulators, rounded once; of each product of a launch.
@@ -217,13 +233,15 @@ struct EpiGate {
     }
 };
 
-// dg = dh b, du = dh a, rounded to 16 bits (operands of the next products).
-template <typename T, int NT_>
+// dg = dh b, du = dh a, rounded to 16 bits (operands of the next products);
+// REST: and what that leaves, M rows further on.
+template <typename T, int NT_, bool REST>
 struct EpiGateBackward {
     static constexpr int NT = NT_, GROUPS = 2;
     KeepPlanes keep;
     T *dg, *du;
     int64_t M, N;  // N: F rounded up to 64, a row of every plane
+    static __device__ __forceinline__ float rest(float v) { return remainder_of(v, from_float<T>(v)); }
     template <class Release>
     __device__ __forceinline__ void run(uint32_t acc, int, int, int64_t row, int nt, int group, int, Release release) const {
         constexpr int STEPS = NT / GROUPS / 32;
@@ -251,27 +269,38 @@ struct EpiGateBackward {
                 }
                 store_v8(dg + at, pg);
                 store_v8(du + at, pu);
+                if constexpr (REST) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float d0 = __uint_as_float(v[i + 2 * k]), d1 = __uint_as_float(v[i + 2 * k + 1]);
+                        pg[k] = pack2<T>(rest(d0 * b[2 * k]), rest(d1 * b[2 * k + 1]));
+                        pu[k] = pack2<T>(rest(d0 * a[2 * k]), rest(d1 * a[2 * k + 1]));
+                    }
+                    store_v8(dg + at + M * N, pg);
+                    store_v8(du + at + M * N, pu);
+                }
             }
         }
     }
 };
 
 // The same two epilogues for the split kernel: one value per lane.
-template <typename T>
+template <typename T, int HALVES_>
 struct EpiSplitStore {
-    static constexpr int UNITS = 1;
+    static constexpr int UNITS = 1, HALVES = HALVES_;
     T* C;
     int64_t ldc, N;
-    __device__ __forceinline__ void emit(float v, float, int64_t m, int unit, int lane, int tile) const {
+    __device__ __forceinline__ void emit(float v, float rest, int64_t m, int unit, int lane, int tile) const {
         const int64_t n = (int64_t)tile * 128 + unit * 32 + lane;
-        if (n < N) C[m * ldc + n] = from_float<T>(v);
+        if (n < N) C[m * ldc + n] = from_float<T>(HALVES == 2 ? v + rest : v);
     }
 };
 
 template <typename T>
 struct EpiSplitGate {
-    static constexpr int UNITS = 2;
+    static constexpr int UNITS = 2, HALVES = 1;
     T* h;
+    int64_t rest;     // rows from a value to what its rounding leaves; 0: not kept
     KeepPlanes keep;  // null: no backward pass follows
     int64_t N;        // F rounded up to 64, a row of every plane
     int act;
@@ -280,7 +309,9 @@ struct EpiSplitGate {
         if (n >= N) return;  // whole warps
         float av = 0.0f, da = 0.0f;
         with_activation(act, [&](auto tag) { activation<decltype(tag)::value, true>(g, av, da); });
-        h[m * N + n] = from_float<T>(av * u);
+        const T hi = from_float<T>(av * u);
+        h[m * N + n] = hi;
+        if (rest != 0) h[(m + rest) * N + n] = from_float<T>(remainder_of(av * u, hi));
         if (keep.a != nullptr) {
             using V = typename Keep<T>::value;
             keep_lane(static_cast<V*>(keep.a), keep.ea, m * N + n, av, lane);
@@ -343,6 +374,7 @@ struct Product16 {
     int64_t M, N, K;
     void* C;
     int64_t ldc;
+    bool doubled;  // rows M / 2 and on of the product are added to the first ones
     int64_t stages() const { return (K + 63) / 64 * segs; }
 };
 
@@ -396,7 +428,7 @@ cudaError_t split16(const Matrix16& x, const Matrix16& W0, const Matrix16& W1, b
     g.nk = (int)((x.cols + 63) / 64);
     g.last_steps = (int)((x.cols - (int64_t)(g.nk - 1) * 64 + 15) / 16);
     g.early = early;
-    g.M = x.rows;
+    g.M = x.rows / Epi::HALVES;
     return launch_split_gemm<KIND, PAIRED>(g, maps, epi, st);
 }
 
@@ -438,9 +470,10 @@ cudaError_t store16_shared(const Product16* w, int count, int64_t depth, cudaStr
         epi.M[p] = w[p].M;
         epi.N[p] = w[p].N;
         epi.ld[p] = ld;
-        if (g.p[p].splits == 1) continue;
+        if (g.p[p].splits == 1 && !w[p].doubled) continue;
         of[shared] = p;
         sums.s[shared++] = PartialSums<T>{nullptr, epi.C[p], w[p].ldc, (int)w[p].M, (int)w[p].N, (int)ld, g.p[p].splits};
+        if (w[p].doubled) sums.s[shared - 1].M /= 2, sums.s[shared - 1].splits *= 2;  // a plane of M rows is two of M / 2
         total += w[p].M * ld * g.p[p].splits;
         most = std::max(most, w[p].M * ld / 4);
     }
@@ -519,7 +552,7 @@ cudaError_t store16(const Product16* w, int count, const Share& share, cudaStrea
         few += pair_tiles(w[p].M, w[p].N, 128);
         aligned = aligned && aligned_rows<T>(w[p].C, w[p].ldc);
     }
-    if (share.split)
+    if (share.split || w[0].doubled)
         return share.nt == 128 ? store16_shared<KIND, T, A_MAJOR, B_MN, 128>(w, count, share.depth, st)
                                : store16_shared<KIND, T, A_MAJOR, B_MN, 256>(w, count, share.depth, st);
     const bool narrow = share.nt != 0 ? share.nt == 128 : narrow_tiles(wide, few, kNarrow16);
@@ -531,17 +564,18 @@ cudaError_t store16(const Product16* w, int count, const Share& share, cudaStrea
 template <int KIND, typename T, int NT, bool SAVE>
 cudaError_t gate16(const FfForward& f, cudaStream_t st) {
     return product16<KIND, false, true>(
-        Product16{{f.x}, {f.wg, f.wu}, 1, false, f.T, f.F, f.D, nullptr, 0},
+        Product16{{f.x}, {f.wg, f.wu}, 1, false, f.T, f.F, f.D, nullptr, 0, false},
         EpiGate<T, NT, SAVE>{static_cast<T*>(f.h), KeepPlanes{f.a, f.b, f.ea, f.eb}, f.T, f.ld, f.act}, st);
 }
 
 template <int KIND, typename T>
 cudaError_t forward_typed(const FfForward& f, cudaStream_t st) {
-    const Matrix16 h{f.h, f.T, f.F, f.ld};
+    const int64_t rest = f.T <= kFullTokens ? f.T : 0;
+    const Matrix16 h{f.h, f.T + rest, f.F, f.ld};
     cudaError_t err;
     if (f.T <= kSplitTokens16) {
         err = split16<KIND, true>(f.x, f.wg, f.wu, false,
-                                  EpiSplitGate<T>{static_cast<T*>(f.h), KeepPlanes{f.a, f.b, f.ea, f.eb}, f.ld, f.act}, st);
+                                  EpiSplitGate<T>{static_cast<T*>(f.h), rest, KeepPlanes{f.a, f.b, f.ea, f.eb}, f.ld, f.act}, st);
     } else {
         const bool narrow = narrow16(f.T, f.F, 128), save = f.a != nullptr;
         err = narrow ? (save ? gate16<KIND, T, 128, true>(f, st) : gate16<KIND, T, 128, false>(f, st))
@@ -549,28 +583,40 @@ cudaError_t forward_typed(const FfForward& f, cudaStream_t st) {
     }
     if (err != cudaSuccess) return err;
     // Wd was complete before the launch above could end its own wait
+    if (rest != 0)
+        return split16<KIND, false>(h, f.wd, f.wd, true, EpiSplitStore<T, 2>{static_cast<T*>(f.y), f.ldy, f.D}, st);
     if (f.T <= kSplitTokens16)
-        return split16<KIND, false>(h, f.wd, f.wd, true, EpiSplitStore<T>{static_cast<T*>(f.y), f.ldy, f.D}, st);
-    const Product16 y{{h}, {f.wd}, 1, false, f.T, f.D, f.F, f.y, f.ldy};
+        return split16<KIND, false>(h, f.wd, f.wd, true, EpiSplitStore<T, 1>{static_cast<T*>(f.y), f.ldy, f.D}, st);
+    const Product16 y{{h}, {f.wd}, 1, false, f.T, f.D, f.F, f.y, f.ldy, false};
     return store16<KIND, T, kMajorK, false>(&y, 1, best_share(&y, 1), st);
 }
 
-template <int KIND, typename T, int NT>
+template <int KIND, typename T, int NT, bool REST>
 cudaError_t gate_backward16(const FfBackward& f, cudaStream_t st) {
     return product16<KIND, true, false>(
-        Product16{{f.dy}, {f.wd}, 1, false, f.T, f.F, f.D, nullptr, 0},
-        EpiGateBackward<T, NT>{KeepPlanes{const_cast<void*>(f.a), const_cast<void*>(f.b), const_cast<uint8_t*>(f.ea),
+        Product16{{f.dy}, {f.wd}, 1, false, f.T, f.F, f.D, nullptr, 0, false},
+        EpiGateBackward<T, NT, REST>{KeepPlanes{const_cast<void*>(f.a), const_cast<void*>(f.b), const_cast<uint8_t*>(f.ea),
                                            const_cast<uint8_t*>(f.eb)},
                                 static_cast<T*>(f.dg), static_cast<T*>(f.du), f.T, f.ld}, st);
 }
 
 template <int KIND, typename T>
 cudaError_t backward_typed(const FfBackward& f, cudaStream_t st) {
-    const Matrix16 h{const_cast<void*>(f.h), f.T, f.F, f.ld}, dg{f.dg, f.T, f.F, f.ld}, du{f.du, f.T, f.F, f.ld};
+    const bool full = f.T <= kFullTokens;
+    const int segs = full ? 2 : 1;
+    Matrix16 h[2], dg[2], du[2];  // and what their roundings leave
+    for (int i = 0; i < 2; ++i) {
+        const int64_t from = i * f.T * f.ld;
+        h[i] = Matrix16{static_cast<T*>(const_cast<void*>(f.h)) + from, f.T, f.F, f.ld};
+        dg[i] = Matrix16{static_cast<T*>(f.dg) + from, f.T, f.F, f.ld};
+        du[i] = Matrix16{static_cast<T*>(f.du) + from, f.T, f.F, f.ld};
+    }
     cudaError_t err = cudaSuccess;
     // dh = dy Wd (B is Wd, D x F: K x N), unless only dWd is wanted
     if (f.dx != nullptr || f.dwg != nullptr || f.dwu != nullptr)
-        err = narrow16(f.T, f.F, 256) ? gate_backward16<KIND, T, 128>(f, st) : gate_backward16<KIND, T, 256>(f, st);
+        err = narrow16(f.T, f.F, 256)
+                  ? (full ? gate_backward16<KIND, T, 128, true>(f, st) : gate_backward16<KIND, T, 128, false>(f, st))
+                  : (full ? gate_backward16<KIND, T, 256, true>(f, st) : gate_backward16<KIND, T, 256, false>(f, st));
     if (err != cudaSuccess) return err;
     // dx = dg Wg + du Wu; the weights' gradients are sums over the T rows of both
     // operands.  All in one launch where the tiles are few (best_share); else dx
@@ -578,11 +624,15 @@ cudaError_t backward_typed(const FfBackward& f, cudaStream_t st) {
     // pairs would have one more of the deep ones).
     Product16 w[kMaxProducts];
     int count = 0;
-    if (f.dx != nullptr) w[count++] = Product16{{dg, du}, {f.wg, f.wu}, 2, false, f.T, f.D, f.F, f.dx, f.lddx};
+    if (f.dx != nullptr) {
+        const int64_t rows = f.T * segs;
+        const Matrix16 g{f.dg, rows, f.F, f.ld}, u{f.du, rows, f.F, f.ld};
+        w[count++] = Product16{{g, u}, {f.wg, f.wu}, 2, false, rows, f.D, f.F, f.dx, f.lddx, full};
+    }
     const int others = count;
-    if (f.dwg != nullptr) w[count++] = Product16{{dg}, {f.x}, 1, true, f.F, f.D, f.T, f.dwg, f.lddwg};
-    if (f.dwu != nullptr) w[count++] = Product16{{du}, {f.x}, 1, true, f.F, f.D, f.T, f.dwu, f.lddwu};
-    if (f.dwd != nullptr) w[count++] = Product16{{f.dy}, {h}, 1, true, f.D, f.F, f.T, f.dwd, f.lddwd};
+    if (f.dwg != nullptr) w[count++] = Product16{{dg[0], dg[1]}, {f.x, f.x}, segs, true, f.F, f.D, f.T, f.dwg, f.lddwg, false};
+    if (f.dwu != nullptr) w[count++] = Product16{{du[0], du[1]}, {f.x, f.x}, segs, true, f.F, f.D, f.T, f.dwu, f.lddwu, false};
+    if (f.dwd != nullptr) w[count++] = Product16{{f.dy, f.dy}, {h[0], h[1]}, segs, true, f.D, f.F, f.T, f.dwd, f.lddwd, false};
     const Share all = best_share(w, count);
     if (all.nt != 0) return store16<KIND, T, kMajorAny, true>(w, count, all, st);
     err = store16<KIND, T, kMajorAny, true>(w, others, best_share(w, others), st);

@@ -151,7 +151,7 @@ struct SavedLayout {
     SavedLayout(int type, int64_t T, int64_t F) {
         const int64_t elem = type == DDGEMM_BF16 ? 2 : 4, bytes = type == DDGEMM_BF16 ? 1 : 0;
         ld = round_up(F, 64);
-        off_a = round_up(T * ld * 2, kAlign);
+        off_a = round_up(ff_rows(T) * ld * 2, kAlign);
         off_b = off_a + round_up(T * ld * elem, kAlign);
         off_ea = off_b + round_up(T * ld * elem, kAlign);
         off_eb = off_ea + round_up(T * ld / 32 * bytes, kAlign);
@@ -289,7 +289,7 @@ ddgemm_status dd_ff_gated(int type, int activation, int64_t T, int64_t D, int64_
     if (F == 0) return status_of(zero16(y, T, D, ldy, 2, st));
     Workspace ws(st);
     Aligned16 ax(x, T, D, ldx, T, ws), ag(Wg, F, D, ldwg, T, ws), au(Wu, F, D, ldwu, T, ws), ad(Wd, D, F, ldwd, T, ws);
-    const int64_t h = saved ? 0 : ws.reserve(T * L.ld * 2);
+    const int64_t h = saved ? 0 : ws.reserve(ff_rows(T) * L.ld * 2);
     if (!ws.allocate()) return DDGEMM_ERR_ALLOC;
     Aligned16* const operands[] = {&ax, &ag, &au, &ad};
     cudaError_t err = resolve(operands, 4, ws, st);
@@ -338,7 +338,7 @@ ddgemm_status dd_ff_gated_backward(int type, int64_t T, int64_t D, int64_t F, co
     Workspace ws(st);
     Aligned16 ay(dy, T, D, lddy, T, ws), ax(x, T, D, ldx, T, ws), ag(Wg, F, D, ldwg, T, ws), au(Wu, F, D, ldwu, T, ws),
         ad(Wd, D, F, ldwd, T, ws);
-    const int64_t og = ws.reserve(T * L.ld * 2), ou = ws.reserve(T * L.ld * 2);
+    const int64_t og = ws.reserve(ff_rows(T) * L.ld * 2), ou = ws.reserve(ff_rows(T) * L.ld * 2);
     if (!ws.allocate()) return DDGEMM_ERR_ALLOC;
     Aligned16* const operands[] = {&ay, &ax, &ag, &au, &ad};
     cudaError_t err = resolve(operands, 5, ws, st);

@@ -167,7 +167,7 @@ struct EpiGate4 {
 // The same two epilogues for the split kernel: one value per lane.
 template <int KIND, typename T>
 struct EpiSplitScale {
-    static constexpr int UNITS = 1;
+    static constexpr int UNITS = 1, HALVES = 1;
     T* C;
     int64_t ldc, N;
     const int32_t *e, *f;
@@ -183,7 +183,7 @@ struct EpiSplitScale {
 
 template <int KIND>
 struct EpiSplitGate4 {
-    static constexpr int UNITS = 2;
+    static constexpr int UNITS = 2, HALVES = 1;
     uint8_t *codes, *scales;
     float* most;
     int64_t ld, F;

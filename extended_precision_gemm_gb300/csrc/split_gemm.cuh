@@ -76,6 +76,8 @@ __device__ __forceinline__ float ld_shared(uint32_t addr) {
 // Epi: UNITS (1: a unit of work is 32 weight rows of one token, 4 units to a
 // tile and token; 2: it is 32 rows of g and 32 of u, 2 units) and
 // emit(v0, v1, token, unit, lane, tile): the whole warp, one row per lane.
+// HALVES = 2: the tokens' matrix holds two rows for each of M tokens, all first
+// ones, then all second ones; v0 and v1 are the sums of each (one tile of NQ).
 template <int KIND, int NQ, bool PAIRED16, class Epi>
 __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __grid_constant__ SplitArgs g,
                                                                    const __grid_constant__ SplitMaps maps,
@@ -228,19 +230,21 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
     // and the 32 of u that go with them.  Unit w belongs to CTA w % splits, at
     // slot w / splits of its memory; a slot holds a row of 32 for each CTA.
     // Once every MMA of the cluster has finished, the rings hold nothing more.
-    constexpr int PARTS = Epi::UNITS, PER_TOKEN = 4 / PARTS;
+    constexpr int HALVES = Epi::HALVES, PARTS = Epi::UNITS * HALVES, PER_TOKEN = 4 / Epi::UNITS;
+    static_assert(PARTS <= 2, "two sums of a unit at most");
     const int tokens = (int)min((int64_t)NQ, g.M - (int64_t)mt * NQ);
-    const int units = tokens * PER_TOKEN, splits = g.splits;
+    const int units = tokens * PER_TOKEN, splits = g.splits, columns = tokens * HALVES;
     if (!warp_wait(done_bar, 0, 2 * kTileWaitNs) && lane == 0) tile_timeout();
     tc5::fence_after_sync();
     cluster_sync();
     if (warp >= 2) {
         const int q = warp & 3;  // 32 rows of the tile: of which unit, and which of its parts
-        const int unit = PARTS == 1 ? q : PAIRED16 ? q % 2 : q / 2, part = PARTS == 1 ? 0 : PAIRED16 ? q / 2 : q % 2;
+        const int unit = Epi::UNITS == 1 ? q : PAIRED16 ? q % 2 : q / 2;
+        const int part = Epi::UNITS == 1 ? 0 : PAIRED16 ? q / 2 : q % 2;
         const uint32_t mine = ring + (uint32_t)(z * PARTS + part) * 128 + lane * 4, pitch = (uint32_t)(splits * PARTS) * 128;
         const uint32_t inverse = 65536u / (uint32_t)splits + 1u;  // w / splits = w * inverse >> 16 for w < 4096
 #pragma unroll 1
-        for (int c = (warp - 2) / 4 * 16; c < tokens; c += 32) {
+        for (int c = (warp - 2) / 4 * 16; c < columns; c += 32) {
             uint32_t v[16];
             asm volatile(
                 "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -252,8 +256,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
                 : "memory");
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const uint32_t w = (uint32_t)((c + i) * PER_TOKEN + unit), slot = w * inverse >> 16;
-                if (c + i < tokens) st_cluster(cluster_addr(mine + slot * pitch, w - slot * splits), v[i]);
+                const bool second = HALVES == 2 && c + i >= tokens;
+                const uint32_t w = (uint32_t)((c + i - (second ? tokens : 0)) * PER_TOKEN + unit), slot = w * inverse >> 16;
+                if (c + i < columns)
+                    st_cluster(cluster_addr(mine + slot * pitch + (second ? 128 : 0), w - slot * splits), v[i]);
             }
         }
     }
@@ -339,8 +345,9 @@ constexpr int kSplitTokens4 = 64, kSplitTokens16 = 128;
 
 template <int KIND, bool PAIRED16, class Epi>
 cudaError_t launch_split_gemm(SplitArgs g, const SplitMaps& maps, const Epi& epi, cudaStream_t st) {
-    const int nq = split_nq(g.M);
-    g.mt = (int)((g.M + nq - 1) / nq);
+    const int64_t rows = g.M * Epi::HALVES;
+    const int nq = split_nq(rows);
+    g.mt = (int)((rows + nq - 1) / nq);
     g.splits = split_count((int64_t)g.nt * g.mt, g.nk);
     g.per = (g.nk + g.splits - 1) / g.splits;
     switch (nq) {

@@ -50,7 +50,7 @@ __device__ unsigned int g_tile_timeouts = 0;
 
 __device__ __forceinline__ void tile_timeout() { atomicAdd(&g_tile_timeouts, 1u); }
 
-constexpr int kMaxProducts = 4, kMaxMaps = kMaxProducts + 1;
+constexpr int kMaxProducts = 4, kMaxMaps = 2 * kMaxProducts;
 
 struct TileMaps {
     CUtensorMap a[kMaxMaps], b[kMaxMaps];  // by product and segment, or (gated) b by CTA

@@ -221,3 +221,30 @@ def test_few_tiles_and_deep_sums(T, D, F, dtype):
     check(got, want, want)
     again = ddg.ff_gated_backward(dy, x, wg, wu, wd, saved)
     assert all(_torch().equal(a, got[n]) for a, n in zip(again, ("dx", "dwg", "dwu", "dwd")))
+
+
+@pytest.mark.parametrize("dtype", ("bfloat16", "float16"))
+@pytest.mark.parametrize("T,D,F", [(1, 128, 640), (2, 64, 128), (4, 130, 192), (8, 120, 979), (16, 400, 222), (5, 2100, 4200)])
+def test_few_tokens_are_rounded_once(T, D, F, dtype):
+    """Of up to 16 tokens an intermediate value's rounding leaves 2^-8 of itself
+    at most, kept in turn: errors are those of the outputs' own rounding, with
+    room of a tenth for the backward pass's factors (kept to 2^-11) and for sums
+    in 32 bits."""
+    torch = _torch()
+    g = torch.Generator().manual_seed(T * 1000 + F)
+    make = lambda r, c, s=1.0: (torch.randn(r, c, generator=g) * s).to(getattr(torch, dtype)).cuda()  # noqa: E731
+    x, dy, wg, wu, wd = make(T, D), make(T, D), make(F, D, D**-0.5), make(F, D, D**-0.5), make(D, F, F**-0.5)
+    y, saved = ddg.ff_gated(x, wg, wu, wd, act="silu", save=True)
+    assert torch.equal(y, ddg.ff_gated(x, wg, wu, wd, act="silu"))
+    got = (y,) + ddg.ff_gated_backward(dy, x, wg, wu, wd, saved)
+    X, DY, G, U, W = (t.double() for t in (x, dy, wg, wu, wd))
+    gg, uu = X @ G.t(), X @ U.t()
+    p = torch.sigmoid(gg)
+    a, da = gg * p, p + gg * p * (1 - p)
+    dh = DY @ W
+    dg, du = dh * uu * da, dh * a
+    want = ((a * uu) @ W.t(), dg @ G + du @ U, dg.t() @ X, du.t() @ X, DY.t() @ (a * uu))
+    for o, w in zip(got, want):
+        least = (w.to(o.dtype).double() - w).norm()
+        assert (o.double() - w).norm() <= 1.1 * least, ((o.double() - w).norm() / least).item()
+    assert ddg.wait_timeouts() == 0
