@@ -761,7 +761,8 @@ ddgemm_status dd_mx4_gemm(int format, int64_t M, int64_t N, int64_t K, const uin
  * y = h Wd^T with h = act(x Wg^T) * (x Wu^T): x T x D, Wg and Wu F x D, Wd
  * D x F, y T x D, all of `type` (DDGEMM_BF16 or DDGEMM_F16), any leading
  * dimensions.  Sums, the activation and the product are in 32 bits; h is
- * rounded to `type` between the two products.  `saved`, if not NULL, receives
+ * rounded to `type` between the two products (of up to 16 tokens, to twice its
+ * bits).  `saved`, if not NULL, receives
  * what the backward pass needs (dd_ff_gated_saved_size bytes, 256-byte
  * aligned; opaque, of the library's version that wrote it).
  */
