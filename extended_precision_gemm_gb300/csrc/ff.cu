@@ -21,6 +21,9 @@
 // which costs little, as the weights bind and tiles are mostly idle (4096 x
 // 12288, one token: 50.2 us for 50.0, forward and backward 218 for 214; 16 tokens
 // 53.4 for 52.7 and 201 for 195).
+// Where a sum with remainders is not finite it is the sum without them: an
+// infinity stays one, as of more tokens (156 us for 155, the backward pass of one
+// token, 150 for 149 of 16).
 #include "activation.cuh"
 #include "mx4.cuh"
 #include "split_gemm.cuh"
@@ -101,12 +104,64 @@ __device__ __forceinline__ float remainder_of(float v, T hi) {
     return finite_bits(h) == (__float_as_uint(h) & 0x7fffffffu) ? v - h : 0.0f;
 }
 
-// C = accumulators, rounded once; of each product of a launch.
-template <typename T, int NT_, int P, bool ALIGNED>
+// v, a sum over rounded values and what the roundings leave, unless that is not
+// finite: a remainder times an infinity of the other operand is a NaN of its own
+// (0 inf) or has the other sign.  Then the sum over the rounded values alone.
+__device__ __forceinline__ bool is_finite(float v) { return (__float_as_uint(v) & 0x7fffffffu) < kInfBits; }
+__device__ __forceinline__ float with_rest(float v, float rest) {
+    const float sum = v + rest;
+    return is_finite(sum) ? sum : v;
+}
+
+// A weight gradient of few tokens, C[m, n] = sum over t of a[t, m] b[t, n] and as
+// many terms with what the roundings of a (or b) leave, all in one accumulator:
+// the terms of the rounded values again, for elements that are not finite.
+template <typename T>
+struct RoundedTerms {
+    const T *a, *b;
+    int64_t lda, ldb;
+    int tokens;
+};
+// A bit for each of a thread's values that is not finite; whether a warp has any
+// takes one operation a value (0 v is 0 or NaN).
+__device__ __forceinline__ uint32_t not_finite(const float (&f)[32]) {
+    float nan[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) nan[i % 4] = fmaf(f[i], 0.0f, nan[i % 4]);
+    const float any = (nan[0] + nan[1]) + (nan[2] + nan[3]);
+    uint32_t bad = 0;
+    if (__any_sync(~0u, any != any)) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) bad |= is_finite(f[i]) ? 0u : 1u << i;
+    }
+    return bad;
+}
+// `bad`: those of a thread's 32 columns from c on of its row, which the warp has
+// just stored.
+template <typename T>
+__device__ __forceinline__ void store_rounded_terms(const RoundedTerms<T>& t, uint32_t bad, T* C, int64_t ldc, int64_t row,
+                                                    int64_t M, int64_t c, int64_t N) {
+    __syncwarp();
+    if (row >= M) return;
+#pragma unroll 1
+    for (; bad != 0u; bad &= bad - 1) {
+        const int64_t col = c + __ffs(bad) - 1;
+        if (col >= N) return;
+        float sum = 0.0f;
+#pragma unroll 1
+        for (int i = 0; i < t.tokens; ++i) sum = fmaf(to_float<T>(t.a[i * t.lda + row]), to_float<T>(t.b[i * t.ldb + col]), sum);
+        C[row * ldc + col] = from_float<T>(sum);
+    }
+}
+
+// C = accumulators, rounded once; of each product of a launch.  REST: all of
+// them weight gradients with remainders.
+template <typename T, int NT_, int P, bool ALIGNED, bool REST>
 struct EpiStore {
     static constexpr int NT = NT_, GROUPS = 2;
     T* C[P];
     int64_t ldc[P], M[P], N[P];
+    RoundedTerms<T> terms[REST ? P : 1];
     template <class Release>
     __device__ __forceinline__ void run(uint32_t acc, int p, int, int64_t row, int nt, int group, int lane, Release release) const {
         constexpr int STEPS = NT / GROUPS / 32;
@@ -119,20 +174,25 @@ struct EpiStore {
             float f[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-            store_block<ALIGNED>(C[p], ldc[p], row - lane, M[p], (int64_t)nt * NT + c, N[p], f, lane);
+            const int64_t col = (int64_t)nt * NT + c;
+            const uint32_t bad = REST ? not_finite(f) : 0u;
+            store_block<ALIGNED>(C[p], ldc[p], row - lane, M[p], col, N[p], f, lane);
+            if (REST && __any_sync(~0u, bad != 0u)) store_rounded_terms(terms[p], bad, C[p], ldc[p], row, M[p], col, N[p]);
         }
     }
 };
 
 // The same where a tile is shared by several units: partial sums in 32 bits,
 // planes of M rows of ld (N rounded up to 32) for each split.  Products of the
-// launch that are not shared (no planes) go straight to their C.
-template <typename T, int NT_, int P>
+// launch that are not shared (no planes) go straight to their C.  REST: those are
+// weight gradients with remainders.
+template <typename T, int NT_, int P, bool REST>
 struct EpiPartial {
     static constexpr int NT = NT_, GROUPS = 2;
     float* planes[P];
     T* C[P];
     int64_t ld[P], ldc[P], M[P], N[P];
+    RoundedTerms<T> terms[REST ? P : 1];
     template <class Release>
     __device__ __forceinline__ void run(uint32_t acc, int p, int z, int64_t row, int nt, int group, int lane, Release release) const {
         constexpr int STEPS = NT / GROUPS / 32;
@@ -146,20 +206,27 @@ struct EpiPartial {
             float f[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-            if (planes[p] == nullptr) store_block<false>(C[p], ldc[p], row - lane, M[p], col, N[p], f, lane);
-            else if (row < M[p] && col < ld[p]) store_row(planes[p] + ((int64_t)z * M[p] + row) * ld[p] + col, f);
+            if (planes[p] == nullptr) {
+                const uint32_t bad = REST ? not_finite(f) : 0u;
+                store_block<false>(C[p], ldc[p], row - lane, M[p], col, N[p], f, lane);
+                if (REST && __any_sync(~0u, bad != 0u)) store_rounded_terms(terms[p], bad, C[p], ldc[p], row, M[p], col, N[p]);
+            } else if (row < M[p] && col < ld[p]) {
+                store_row(planes[p] + ((int64_t)z * M[p] + row) * ld[p] + col, f);
+            }
         }
     }
 };
 
 // C = the sum of the splits' planes, in their order, rounded once: a thread for
-// four columns of a row (the planes hold few tiles: 32-bit indices do).
+// four columns of a row (the planes hold few tiles: 32-bit indices do).  halves: a
+// split has two planes of M rows, of rounded values and of what that leaves.
 template <typename T>
 struct PartialSums {
     const float* planes;
     T* C;
     int64_t ldc;
     int M, N, ld, splits;
+    bool halves;
 };
 template <typename T, int P>
 struct AllPartialSums {
@@ -176,11 +243,20 @@ __global__ void __launch_bounds__(256) add_partials_kernel(const __grid_constant
     if (c >= (uint32_t)s.N) return;
     const float4* p = reinterpret_cast<const float4*>(s.planes) + i;
     const int splits = s.splits;
-    float4 sum = p[0];
+    const size_t step = s.halves ? 2 * (size_t)n : n;
+    float4 sum = p[0], rest = s.halves ? p[n] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
     for (int z = 1; z < splits; ++z) {
-        const float4 v = p[(size_t)z * n];
+        const float4 v = p[z * step];
         sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        if (s.halves) {
+            const float4 w = p[z * step + n];
+            rest.x += w.x, rest.y += w.y, rest.z += w.z, rest.w += w.w;
+        }
+    }
+    if (s.halves) {
+        sum.x = with_rest(sum.x, rest.x), sum.y = with_rest(sum.y, rest.y);
+        sum.z = with_rest(sum.z, rest.z), sum.w = with_rest(sum.w, rest.w);
     }
     T* dst = s.C + row * s.ldc + c;
     const float v[4] = {sum.x, sum.y, sum.z, sum.w};
@@ -292,7 +368,7 @@ struct EpiSplitStore {
     int64_t ldc, N;
     __device__ __forceinline__ void emit(float v, float rest, int64_t m, int unit, int lane, int tile) const {
         const int64_t n = (int64_t)tile * 128 + unit * 32 + lane;
-        if (n < N) C[m * ldc + n] = from_float<T>(HALVES == 2 ? v + rest : v);
+        if (n < N) C[m * ldc + n] = from_float<T>(HALVES == 2 ? with_rest(v, rest) : v);
     }
 };
 
@@ -376,6 +452,10 @@ struct Product16 {
     int64_t ldc;
     bool doubled;  // rows M / 2 and on of the product are added to the first ones
     int64_t stages() const { return (K + 63) / 64 * segs; }
+    // of a sum over tokens with remainders: its first segment
+    template <typename T> RoundedTerms<T> rounded() const {
+        return {static_cast<const T*>(A[0].p), static_cast<const T*>(B[0].p), A[0].ld, B[0].ld, (int)K};
+    }
 };
 
 // Tiles of `per_tile` columns (64 or 128 of each matrix if gated) and maps of
@@ -433,32 +513,33 @@ cudaError_t split16(const Matrix16& x, const Matrix16& W0, const Matrix16& W1, b
 }
 
 // Products into their C, with wide or narrow tiles.
-template <int KIND, typename T, int A_MAJOR, bool B_MN, int NT, bool ALIGNED>
+template <int KIND, typename T, int A_MAJOR, bool B_MN, bool REST, int NT, bool ALIGNED>
 cudaError_t store16_sized(const Product16* w, int count, cudaStream_t st) {
     TileArgs g;
     TileMaps maps;
     const cudaError_t err = tile_args(w, count, NT, 1, B_MN ? 64 : NT / 2, g, maps);
     if (err != cudaSuccess) return err;
-    EpiStore<T, NT, kMaxProducts, ALIGNED> epi = {};
+    EpiStore<T, NT, kMaxProducts, ALIGNED, REST> epi = {};
     for (int p = 0; p < count; ++p) {
         epi.C[p] = static_cast<T*>(w[p].C);
         epi.ldc[p] = w[p].ldc;
         epi.M[p] = w[p].M;
         epi.N[p] = w[p].N;
+        if (REST) epi.terms[p] = w[p].rounded<T>();
     }
     return launch_tile_gemm<KIND, A_MAJOR, B_MN, false>(g, maps, epi, st);
 }
 
 // Products whose few tiles are shared by several units of `depth` stages:
 // partial sums in the library's pool, and a launch that adds them up.
-template <int KIND, typename T, int A_MAJOR, bool B_MN, int NT>
+template <int KIND, typename T, int A_MAJOR, bool B_MN, bool REST, int NT>
 cudaError_t store16_shared(const Product16* w, int count, int64_t depth, cudaStream_t st) {
     TileArgs g;
     TileMaps maps;
     cudaError_t err = tile_args(w, count, NT, 1, B_MN ? 64 : NT / 2, g, maps);
     if (err != cudaSuccess) return err;
     AllPartialSums<T, kMaxProducts> sums = {};
-    EpiPartial<T, NT, kMaxProducts> epi = {};
+    EpiPartial<T, NT, kMaxProducts, REST> epi = {};
     int64_t total = 0, most = 0;
     int shared = 0, of[kMaxProducts];
     for (int p = 0; p < count; ++p) {
@@ -470,10 +551,11 @@ cudaError_t store16_shared(const Product16* w, int count, int64_t depth, cudaStr
         epi.M[p] = w[p].M;
         epi.N[p] = w[p].N;
         epi.ld[p] = ld;
+        if (REST) epi.terms[p] = w[p].rounded<T>();
         if (g.p[p].splits == 1 && !w[p].doubled) continue;
         of[shared] = p;
-        sums.s[shared++] = PartialSums<T>{nullptr, epi.C[p], w[p].ldc, (int)w[p].M, (int)w[p].N, (int)ld, g.p[p].splits};
-        if (w[p].doubled) sums.s[shared - 1].M /= 2, sums.s[shared - 1].splits *= 2;  // a plane of M rows is two of M / 2
+        sums.s[shared++] = PartialSums<T>{nullptr, epi.C[p], w[p].ldc, (int)(w[p].doubled ? w[p].M / 2 : w[p].M), (int)w[p].N, (int)ld,
+                                         g.p[p].splits, w[p].doubled};
         total += w[p].M * ld * g.p[p].splits;
         most = std::max(most, w[p].M * ld / 4);
     }
@@ -483,7 +565,7 @@ cudaError_t store16_shared(const Product16* w, int count, int64_t depth, cudaStr
     float* at = static_cast<float*>(ws);
     for (int i = 0; i < shared; ++i) {
         sums.s[i].planes = epi.planes[of[i]] = at;
-        at += (int64_t)sums.s[i].M * sums.s[i].ld * sums.s[i].splits;
+        at += w[of[i]].M * epi.ld[of[i]] * sums.s[i].splits;
     }
     err = launch_tile_gemm<KIND, A_MAJOR, B_MN, false>(g, maps, epi, st);
     if (err == cudaSuccess)
@@ -541,8 +623,9 @@ Share best_share(const Product16* w, int count) {
 }
 
 // Products of one launch: shared if they are few and deep, else with the tiles
-// whose rounds are the shorter.
-template <int KIND, typename T, int A_MAJOR, bool B_MN>
+// whose rounds are the shorter.  REST: dx doubled, if it is among them, and weight
+// gradients of a few tokens (two stages each: never shared).
+template <int KIND, typename T, int A_MAJOR, bool B_MN, bool REST>
 cudaError_t store16(const Product16* w, int count, const Share& share, cudaStream_t st) {
     if (count == 0) return cudaSuccess;
     int64_t wide = 0, few = 0;
@@ -553,11 +636,13 @@ cudaError_t store16(const Product16* w, int count, const Share& share, cudaStrea
         aligned = aligned && aligned_rows<T>(w[p].C, w[p].ldc);
     }
     if (share.split || w[0].doubled)
-        return share.nt == 128 ? store16_shared<KIND, T, A_MAJOR, B_MN, 128>(w, count, share.depth, st)
-                               : store16_shared<KIND, T, A_MAJOR, B_MN, 256>(w, count, share.depth, st);
+        return share.nt == 128 ? store16_shared<KIND, T, A_MAJOR, B_MN, REST, 128>(w, count, share.depth, st)
+                               : store16_shared<KIND, T, A_MAJOR, B_MN, REST, 256>(w, count, share.depth, st);
     const bool narrow = share.nt != 0 ? share.nt == 128 : narrow_tiles(wide, few, kNarrow16);
-    auto f = narrow ? (aligned ? store16_sized<KIND, T, A_MAJOR, B_MN, 128, true> : store16_sized<KIND, T, A_MAJOR, B_MN, 128, false>)
-                    : (aligned ? store16_sized<KIND, T, A_MAJOR, B_MN, 256, true> : store16_sized<KIND, T, A_MAJOR, B_MN, 256, false>);
+    auto f = narrow ? (aligned ? store16_sized<KIND, T, A_MAJOR, B_MN, REST, 128, true>
+                               : store16_sized<KIND, T, A_MAJOR, B_MN, REST, 128, false>)
+                    : (aligned ? store16_sized<KIND, T, A_MAJOR, B_MN, REST, 256, true>
+                               : store16_sized<KIND, T, A_MAJOR, B_MN, REST, 256, false>);
     return f(w, count, st);
 }
 
@@ -588,7 +673,7 @@ cudaError_t forward_typed(const FfForward& f, cudaStream_t st) {
     if (f.T <= kSplitTokens16)
         return split16<KIND, false>(h, f.wd, f.wd, true, EpiSplitStore<T, 1>{static_cast<T*>(f.y), f.ldy, f.D}, st);
     const Product16 y{{h}, {f.wd}, 1, false, f.T, f.D, f.F, f.y, f.ldy, false};
-    return store16<KIND, T, kMajorK, false>(&y, 1, best_share(&y, 1), st);
+    return store16<KIND, T, kMajorK, false, false>(&y, 1, best_share(&y, 1), st);
 }
 
 template <int KIND, typename T, int NT, bool REST>
@@ -633,11 +718,12 @@ cudaError_t backward_typed(const FfBackward& f, cudaStream_t st) {
     if (f.dwg != nullptr) w[count++] = Product16{{dg[0], dg[1]}, {f.x, f.x}, segs, true, f.F, f.D, f.T, f.dwg, f.lddwg, false};
     if (f.dwu != nullptr) w[count++] = Product16{{du[0], du[1]}, {f.x, f.x}, segs, true, f.F, f.D, f.T, f.dwu, f.lddwu, false};
     if (f.dwd != nullptr) w[count++] = Product16{{f.dy, f.dy}, {h[0], h[1]}, segs, true, f.D, f.F, f.T, f.dwd, f.lddwd, false};
+    const auto store = full ? store16<KIND, T, kMajorAny, true, true> : store16<KIND, T, kMajorAny, true, false>;
     const Share all = best_share(w, count);
-    if (all.nt != 0) return store16<KIND, T, kMajorAny, true>(w, count, all, st);
-    err = store16<KIND, T, kMajorAny, true>(w, others, best_share(w, others), st);
+    if (all.nt != 0) return store(w, count, all, st);
+    err = store(w, others, best_share(w, others), st);
     if (err != cudaSuccess) return err;
-    return store16<KIND, T, kMajorAny, true>(w + others, count - others, best_share(w + others, count - others), st);
+    return store(w + others, count - others, best_share(w + others, count - others), st);
 }
 
 }  // namespace
