@@ -22,23 +22,28 @@ MX4_FORMATS = {"mxfp4": 0, "nvfp4": 1}
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 
 
-_types = _types16 = _uint8 = _int32 = _Tensor = _empty = _raw_stream = None
+_types = _types16 = _uint8 = _int32 = _Tensor = _empty = _raw_stream = _current_device = None
 
 
 def _torch():
     """torch, imported on the first call (with the lookups that every call makes)."""
-    global _types, _types16, _uint8, _int32, _Tensor, _empty, _raw_stream
+    global _types, _types16, _uint8, _int32, _Tensor, _empty, _raw_stream, _current_device
     import torch
     if _types is None:
         _uint8, _int32, _Tensor, _empty = torch.uint8, torch.int32, torch.Tensor, torch.empty
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _types16 = {torch.bfloat16: 1, torch.float16: 2}
         _types = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
     return torch
 
 
 def _stream(stream, t):
-    """The handle of `stream`, or of the current stream of t's device."""
+    """The handle of `stream`, or of the current stream of t's device, which has
+    to be the current one: launches and workspaces are on that, and so is the
+    default stream, whose handle is the same on every device."""
+    if t.get_device() != _current_device():
+        raise ValueError("tensors must be on the current CUDA device (torch.cuda.device)")
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:

@@ -1,0 +1,87 @@
+"""Calls of the 4-bit and feed-forward entry points that must not reach the GPU
+(no GPU needed)."""
+import pytest
+
+import extended_precision_gemm_gb300 as ddg
+from extended_precision_gemm_gb300 import low_precision as lp
+
+
+# ---- tensors of a device that is not the current one ----
+
+class Stand:
+    """What the binding asks of a contiguous CUDA tensor."""
+
+    is_cuda = True
+
+    def __init__(self, shape, dtype, device=0):
+        self.shape = (shape,) if isinstance(shape, int) else tuple(shape)
+        self.dtype, self.device = dtype, device
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i=None):
+        s = (self.shape[1], 1) if len(self.shape) == 2 else (1,)
+        return s if i is None else s[i]
+
+    def numel(self):
+        n = 1
+        for v in self.shape:
+            n *= v
+        return n
+
+    def get_device(self):
+        return self.device
+
+    def data_ptr(self):
+        return 1 << 40
+
+    def is_contiguous(self):
+        return True
+
+
+@pytest.fixture
+def binding(monkeypatch):
+    """The binding with stand-ins for tensors, the stream and the library; the calls that reach the library."""
+    pytest.importorskip("torch")
+    lp._torch()
+    calls = []
+    monkeypatch.setattr(lp, "_Tensor", Stand)
+    monkeypatch.setattr(lp, "_empty", lambda shape, dtype, device: Stand(shape, dtype, device))
+    monkeypatch.setattr(lp, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(lp, "_call", lambda name, *args: calls.append(name))
+    return calls
+
+
+def every_call():
+    import torch
+    half = lambda r, c: Stand((r, c), torch.bfloat16)  # noqa: E731
+    q = lambda rows, k: ddg.MX4(Stand((rows, -(-k // 32) * 16), torch.uint8), Stand(lp._scale_bytes(1, rows, k), torch.uint8),  # noqa: E731
+                                Stand(rows, torch.int32), rows, k, "nvfp4")
+    T, D, F = 5, 64, 96
+    x, wg, wu, wd = half(T, D), half(F, D), half(F, D), half(D, F)
+    saved = Stand(ddg.ff_gated_saved_size(T, F, torch.bfloat16), torch.uint8)
+    return {
+        "dd_mx4_quantize": lambda: ddg.mx4_quantize(x, "nvfp4"),
+        "dd_mx4_dequantize": lambda: ddg.mx4_dequantize(q(T, D)),
+        "dd_mx4_gemm": lambda: ddg.mx4_gemm(q(T, D), q(F, D)),
+        "dd_mx4_ff_gated": lambda: ddg.mx4_ff_gated(x, q(2 * F, D), q(D, F)),
+        "dd_ff_gated": lambda: ddg.ff_gated(x, wg, wu, wd, save=True),
+        "dd_ff_gated_backward": lambda: ddg.ff_gated_backward(x, x, wg, wu, wd, saved),
+    }
+
+
+def test_tensors_of_another_device_than_the_current_one_are_refused(binding, monkeypatch):
+    """Launches, workspaces and the default stream are the current device's."""
+    monkeypatch.setattr(lp, "_current_device", lambda: 1, raising=False)
+    for name, call in every_call().items():
+        with pytest.raises(ValueError, match="current"):
+            call()
+        assert not binding, name
+
+
+def test_tensors_of_the_current_device_are_taken(binding, monkeypatch):
+    monkeypatch.setattr(lp, "_current_device", lambda: 0, raising=False)
+    for name, call in every_call().items():
+        call()
+        assert binding.pop() == name and not binding
