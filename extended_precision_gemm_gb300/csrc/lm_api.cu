@@ -54,7 +54,7 @@ ddgemm_status check_mx4(int format, const Mx4Matrix& m) {
     if (m.codes == nullptr || m.scales == nullptr || !aligned16(m.codes) || !aligned16(m.scales))
         return DDGEMM_ERR_INVALID_ARG;
     if (m.ldq % 16 != 0 || m.ldq < mx4_code_bytes(m.K)) return DDGEMM_ERR_INVALID_ARG;
-    if (format == DDGEMM_NVFP4 && m.exponents == nullptr) return DDGEMM_ERR_INVALID_ARG;
+    if (format == DDGEMM_NVFP4 && (m.exponents == nullptr || (uintptr_t)m.exponents % 4 != 0)) return DDGEMM_ERR_INVALID_ARG;
     return DDGEMM_OK;
 }
 

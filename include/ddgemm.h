@@ -708,7 +708,7 @@ ddgemm_status dd_wait_timeouts(unsigned int* count);
  * their tile.  A row's scales cover K rounded up to 256; those beyond K are 0.
  * Scales of rows beyond the last are not read into any result and need not be
  * set.  exponents: int32 per row (nvfp4; ignored, may be NULL, for mxfp4).
- * codes and scales start on 16-byte boundaries.
+ * codes and scales start on 16-byte boundaries, exponents on 4-byte ones.
  */
 #define DDGEMM_MXFP4 0
 #define DDGEMM_NVFP4 1

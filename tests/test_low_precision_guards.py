@@ -1,9 +1,16 @@
 """Calls of the 4-bit and feed-forward entry points that must not reach the GPU
 (no GPU needed)."""
+import ctypes
+
 import pytest
 
 import extended_precision_gemm_gb300 as ddg
 from extended_precision_gemm_gb300 import low_precision as lp
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return ddg.load()
 
 
 # ---- tensors of a device that is not the current one ----
@@ -85,3 +92,20 @@ def test_tensors_of_the_current_device_are_taken(binding, monkeypatch):
     for name, call in every_call().items():
         call()
         assert binding.pop() == name and not binding
+
+
+# ---- row exponents that are not aligned ----
+
+def test_misaligned_row_exponents_are_refused(lib):
+    a, b, c, d, e, f, y = (ctypes.c_void_p(i << 40) for i in range(1, 8))
+    for off in (1, 2, 3):
+        odd = ctypes.c_void_p((9 << 40) + off)
+        assert lib.dd_mx4_quantize(1, 1, 0, 8, 64, a, 64, b, 32, c, odd, None) == 1
+        assert lib.dd_mx4_quantize(1, 1, 1, 8, 64, a, 8, b, 32, c, odd, None) == 1
+        assert lib.dd_mx4_dequantize(1, 1, 8, 64, a, 32, b, odd, c, 64, None) == 1
+        assert lib.dd_mx4_gemm(1, 8, 8, 64, a, 32, b, odd, c, 32, d, e, 1.0, 1, y, 8, None) == 1
+        assert lib.dd_mx4_gemm(1, 8, 8, 64, a, 32, b, e, c, 32, d, odd, 1.0, 1, y, 8, None) == 1
+        for first, second in ((odd, y), (y, odd)):
+            assert lib.dd_mx4_ff_gated(1, 1, 0, 3, 64, 40, a, 64, b, 32, c, first, d, 32, e, second, f, 64, None) == 1
+        # without anything to read or write they are not looked at
+        assert lib.dd_mx4_quantize(1, 1, 0, 0, 64, a, 64, b, 32, c, odd, None) == 0
