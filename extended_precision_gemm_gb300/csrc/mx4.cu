@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(256) nvfp4_finish_columns_kernel(const uint32_
                                                                    const T* X, int64_t ldx) {
     constexpr int KTS = 4, N = 128 * 4 * KTS / 256;
     __shared__ uint32_t part[2][128];
-    __shared__ uint32_t words[KTS * 4][128];  // a scale tile each
+    __shared__ __align__(16) uint32_t words[KTS * 4][128];  // a scale tile each, stored 16 bytes at a time
     pdl_wait();
     pdl_launch_dependents();
     const int64_t r0 = (int64_t)blockIdx.x * 128, kt0 = (int64_t)blockIdx.y * KTS, kts = (K + MX4_TILE_K - 1) / MX4_TILE_K;

@@ -1,6 +1,8 @@
 """Calls of the 4-bit and feed-forward entry points that must not reach the GPU
 (no GPU needed)."""
 import ctypes
+import pathlib
+import re
 
 import pytest
 
@@ -109,3 +111,26 @@ def test_misaligned_row_exponents_are_refused(lib):
             assert lib.dd_mx4_ff_gated(1, 1, 0, 3, 64, 40, a, 64, b, 32, c, first, d, 32, e, second, f, 64, None) == 1
         # without anything to read or write they are not looked at
         assert lib.dd_mx4_quantize(1, 1, 0, 0, 64, a, 64, b, 32, c, odd, None) == 0
+
+
+# ---- shared memory read in words wider than its elements ----
+
+WIDE = {"uint4": 16, "int4": 16, "float4": 16, "uint2": 8, "int2": 8, "float2": 8, "double2": 16, "ulonglong2": 16}
+BYTES = {"uint8_t": 1, "uint16_t": 2, "uint32_t": 4, "int": 4, "float": 4, "uint64_t": 8, "double": 8, **WIDE}
+
+
+def test_shared_arrays_are_aligned_to_what_is_read_from_them():
+    """A __shared__ array that is cast to a wider type says so where it is declared: the compiler places it by its
+    elements otherwise, and an unaligned wide access faults."""
+    seen = 0
+    for path in sorted((pathlib.Path(lp.__file__).parent / "csrc").glob("*.cu*")):
+        text = path.read_text()
+        for m in re.finditer(r"__shared__\s+(__align__\((\d+)\)\s+)?(\w+)\s+(\w+)((?:\[[^;]*?\])+);", text):
+            align, elem, name = int(m.group(2) or 0), m.group(3), m.group(4)
+            end = re.search(r"\n}", text[m.end():])
+            body = text[m.end(): m.end() + (end.start() if end else 0)]
+            for cast in re.finditer(r"reinterpret_cast<(?:const )?(?:volatile )?(\w+)\s*\*>\(&?" + name + r"\b", body):
+                need = BYTES.get(cast.group(1), 1)
+                seen += 1
+                assert max(align, BYTES.get(elem, 1)) >= need, f"{path.name}: {name} is read as {cast.group(1)}"
+    assert seen > 0
