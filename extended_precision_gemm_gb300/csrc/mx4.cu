@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(QWARPS * 32) mx4_dequantize_kernel(const uint8
     const int64_t row = item / steps, kt0 = item % steps * DSTEPS;
     const uint8_t* src = codes + row * ldq;
     const uint8_t* sc = scales + mx4_scale_word(row, 0, mx4_scale_tiles(FMT, K)) + block % 4;
-    const float unit = FMT == kMxfp4 ? 1.0f : exp2_int(exponents[row]);
+    const float2 unit = FMT == kMxfp4 ? make_float2(1.0f, 1.0f) : exp2_factors(exponents[row]);
     uint32_t w[DSTEPS], byte[DSTEPS];
 #pragma unroll
     for (int j = 0; j < DSTEPS; ++j) {
@@ -520,9 +520,9 @@ __global__ void __launch_bounds__(QWARPS * 32) mx4_dequantize_kernel(const uint8
         if (k0 >= K) return;
         float y[8];
         e2m1_unpack8(w[j], y);
-        const float s = FMT == kMxfp4 ? mxfp4_scale(byte[j]) : e4m3_value(byte[j]);
+        const float s = FMT == kMxfp4 ? mxfp4_scale(byte[j]) : e4m3_value(byte[j]) * unit.x;  // exact
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = y[i] * s * unit;
+        for (int i = 0; i < 8; ++i) y[i] = FMT == kMxfp4 ? y[i] * s : y[i] * s * unit.y;
         T* dst = X + row * ldx + k0;
         if (vec && k0 + 8 <= K) {
             store8(dst, y);

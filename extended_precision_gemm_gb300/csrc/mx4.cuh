@@ -49,11 +49,24 @@ constexpr uint32_t kInfBits = 0x7f800000u;
 // 2^e as a float, -126 <= e <= 127.
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// x * 2^s for any |s| <= 252 in two steps of the same direction, so that no
-// partial result leaves the range before the whole does.
+// 2^s as two factors of the same direction, so that no partial result leaves the
+// range before the whole does.  s is bounded to +-200: beyond, what is scaled
+// here (codes times scales, 2^-10 to 2^12, and sums of their products, 2^-20 to
+// 2^45) is 0 or infinite in 32 bits anyway.
+__device__ __forceinline__ float2 exp2_factors(int s) {
+    s = min(max(s, -200), 200);
+    const int h = s >> 1;
+    return make_float2(exp2_int(h), exp2_int(s - h));
+}
+// The sum of two exponents that may be any 32-bit numbers, bounded to 32 bits.
+__device__ __forceinline__ int add_exponents(int a, int b) {
+    int s;
+    asm("add.sat.s32 %0, %1, %2;" : "=r"(s) : "r"(a), "r"(b));
+    return s;
+}
 __device__ __forceinline__ float scale_by_exp2(float x, int s) {
-    const int h = s / 2;
-    return x * exp2_int(h) * exp2_int(s - h);
+    const float2 f = exp2_factors(s);
+    return x * f.x * f.y;
 }
 
 // The E8M0 byte of a block whose largest magnitude has these bits:

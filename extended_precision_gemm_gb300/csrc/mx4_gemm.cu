@@ -22,13 +22,13 @@ __device__ __forceinline__ int column_exponent(const int32_t* f, int64_t c, int6
 // ordinary size take two multiplications by powers of two; the rest go by their
 // sum, lest a partial product leave the range (or its normal part) alone.
 __device__ __forceinline__ void scale_columns(float (&v)[32], int er, int fc) {
-    if (__all_sync(~0u, abs(er) <= 40 && abs(fc) <= 40)) {
+    if (__all_sync(~0u, (uint32_t)er + 40u <= 80u && (uint32_t)fc + 40u <= 80u)) {
         const float row = exp2_int(er), column = exp2_int(fc);
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] *= row * __shfl_sync(~0u, column, i);
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = scale_by_exp2(v[i], er + __shfl_sync(~0u, fc, i));
+        for (int i = 0; i < 32; ++i) v[i] = scale_by_exp2(v[i], add_exponents(er, __shfl_sync(~0u, fc, i)));
     }
 }
 
@@ -176,7 +176,7 @@ struct EpiSplitScale {
         const int64_t n = (int64_t)tile * 128 + unit * 32 + lane;
         if (n >= N) return;
         v *= alpha;
-        if (KIND == kKindNv) v = scale_by_exp2(v, e[m] + f[n]);
+        if (KIND == kKindNv) v = scale_by_exp2(v, add_exponents(e[m], f[n]));
         C[m * ldc + n] = from_float<T>(v);
     }
 };
@@ -194,8 +194,8 @@ struct EpiSplitGate4 {
         if (b * 32 >= F) return;
         if (KIND == kKindNv) {
             const int er = e[m];
-            g = scale_by_exp2(g, er + f[b * 64 + lane]);
-            u = scale_by_exp2(u, er + f[b * 64 + 32 + lane]);
+            g = scale_by_exp2(g, add_exponents(er, f[b * 64 + lane]));
+            u = scale_by_exp2(u, add_exponents(er, f[b * 64 + 32 + lane]));
         }
         float a = 0.0f, da;
         with_activation(act, [&](auto tag) { activation<decltype(tag)::value, false>(g, a, da); });

@@ -707,7 +707,8 @@ ddgemm_status dd_wait_timeouts(unsigned int* count);
  * other; row r and block b at (r % 32) * 16 + (r % 128 / 32) * 4 + b % 4 of
  * their tile.  A row's scales cover K rounded up to 256; those beyond K are 0.
  * Scales of rows beyond the last are not read into any result and need not be
- * set.  exponents: int32 per row (nvfp4; ignored, may be NULL, for mxfp4).
+ * set.  exponents: int32 per row, of any value (nvfp4; ignored, may be NULL, for
+ * mxfp4): what is beyond a type's range becomes 0 or an infinity.
  * codes and scales start on 16-byte boundaries, exponents on 4-byte ones.
  */
 #define DDGEMM_MXFP4 0
