@@ -4,6 +4,8 @@
 // the weights are what has to be moved and split_gemm.cuh streams them over all
 // SMs (HBM; 1 x 8192 x 8192 nvfp4 8.5 us); more rows are the tensor pipe's work
 // and go by CTA pairs in tile_gemm.cuh (8192^3 nvfp4 163 us).
+#include <cmath>
+
 #include "activation.cuh"
 #include "mx4.cuh"
 #include "split_gemm.cuh"
@@ -18,18 +20,32 @@ __device__ __forceinline__ int column_exponent(const int32_t* f, int64_t c, int6
     return f != nullptr && c + lane < N ? f[c + lane] : 0;
 }
 
-// 32 values of a row times 2^(er + f_j), lane j holding f_j.  Exponents of
+// 32 values of a row times 2^(er + f_j + ea), lane j holding f_j.  Exponents of
 // ordinary size take two multiplications by powers of two; the rest go by their
 // sum, lest a partial product leave the range (or its normal part) alone.
-__device__ __forceinline__ void scale_columns(float (&v)[32], int er, int fc) {
-    if (__all_sync(~0u, (uint32_t)er + 40u <= 80u && (uint32_t)fc + 40u <= 80u)) {
-        const float row = exp2_int(er), column = exp2_int(fc);
+__device__ __forceinline__ bool ordinary_exponent(int e) { return (uint32_t)e + 40u <= 80u; }
+__device__ __forceinline__ void scale_columns(float (&v)[32], int er, int fc, int ea) {
+    if (__all_sync(~0u, ordinary_exponent(er) && ordinary_exponent(fc) && ordinary_exponent(ea))) {
+        const float row = exp2_int(er + ea), column = exp2_int(fc);
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] *= row * __shfl_sync(~0u, column, i);
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = scale_by_exp2(v[i], add_exponents(er, __shfl_sync(~0u, fc, i)));
+        for (int i = 0; i < 32; ++i) v[i] = scale_by_exp2(v[i], add_exponents(add_exponents(er, __shfl_sync(~0u, fc, i)), ea));
     }
+}
+
+// alpha as it enters the epilogues: of nvfp4, whose accumulators get a power of two
+// besides, a factor in [1/2, 1) and an exponent that joins the rows', so that no
+// partial product leaves the range where the result does not.
+struct Factor {
+    float value;
+    int exponent;
+};
+Factor split_factor(int kind, float alpha) {
+    Factor f{alpha, 0};
+    if (kind == kKindNv && std::isfinite(alpha)) f.value = std::frexp(alpha, &f.exponent);
+    return f;
 }
 
 // C = alpha * accumulators * 2^(e_i + f_j), rounded once.
@@ -39,7 +55,7 @@ struct EpiScale {
     T* C;
     int64_t ldc, M, N;
     const int32_t *e, *f;
-    float alpha;
+    Factor alpha;
     template <class Release>
     __device__ __forceinline__ void run(uint32_t acc, int, int, int64_t row, int nt, int group, int lane, Release release) const {
         const int er = KIND == kKindNv && row < M ? e[row] : 0;
@@ -53,9 +69,9 @@ struct EpiScale {
             if (col >= N) continue;
             float o[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(v[i]) * alpha;
+            for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(v[i]) * alpha.value;
             if (KIND == kKindNv) {
-                scale_columns(o, er, column_exponent(f, col, N, lane));
+                scale_columns(o, er, column_exponent(f, col, N, lane), alpha.exponent);
             }
             store_block<ALIGNED>(C, ldc, row - lane, M, col, N, o, lane);
         }
@@ -113,8 +129,8 @@ struct EpiGate4 {
         if (KIND == kKindNv) {
             const int64_t wc = (int64_t)n * NT + group * 64, W = round_up(F, 32) * 2;
             const int er = row < M ? e[row] : 0;
-            scale_columns(g, er, column_exponent(f, wc, W, lane));
-            scale_columns(u, er, column_exponent(f, wc + 32, W, lane));
+            scale_columns(g, er, column_exponent(f, wc, W, lane), 0);
+            scale_columns(u, er, column_exponent(f, wc + 32, W, lane), 0);
         }
         if (row >= M) return;
         constexpr int FMT = KIND == kKindMx ? kMxfp4 : kNvfp4;
@@ -171,12 +187,12 @@ struct EpiSplitScale {
     T* C;
     int64_t ldc, N;
     const int32_t *e, *f;
-    float alpha;
+    Factor alpha;
     __device__ __forceinline__ void emit(float v, float, int64_t m, int unit, int lane, int tile) const {
         const int64_t n = (int64_t)tile * 128 + unit * 32 + lane;
         if (n >= N) return;
-        v *= alpha;
-        if (KIND == kKindNv) v = scale_by_exp2(v, add_exponents(e[m], f[n]));
+        v *= alpha.value;
+        if (KIND == kKindNv) v = scale_by_exp2(v, add_exponents(add_exponents(e[m], f[n]), alpha.exponent));
         C[m * ldc + n] = from_float<T>(v);
     }
 };
@@ -297,7 +313,7 @@ template <int KIND, typename T, int NT, bool ALIGNED>
 cudaError_t gemm_sized(const Mx4Gemm& g, cudaStream_t st) {
     return product4<KIND>(g.A, g.B,
                           EpiScale<KIND, T, NT, ALIGNED>{static_cast<T*>(g.C), g.ldc, g.A.rows, g.B.rows, g.A.exponents,
-                                                         g.B.exponents, g.alpha},
+                                                         g.B.exponents, split_factor(KIND, g.alpha)},
                           st);
 }
 
@@ -306,7 +322,7 @@ cudaError_t gemm_typed(const Mx4Gemm& g, cudaStream_t st) {
     T* C = static_cast<T*>(g.C);
     if (g.A.rows <= kSplitTokens4)
         return split4<KIND>(g.A, g.B, g.early,
-                            EpiSplitScale<KIND, T>{C, g.ldc, g.B.rows, g.A.exponents, g.B.exponents, g.alpha}, st);
+                            EpiSplitScale<KIND, T>{C, g.ldc, g.B.rows, g.A.exponents, g.B.exponents, split_factor(KIND, g.alpha)}, st);
     const bool narrow = narrow4(g.A, g.B), aligned = aligned_rows<T>(C, g.ldc);
     auto f = narrow ? (aligned ? gemm_sized<KIND, T, 128, true> : gemm_sized<KIND, T, 128, false>)
                     : (aligned ? gemm_sized<KIND, T, 192, true> : gemm_sized<KIND, T, 192, false>);
