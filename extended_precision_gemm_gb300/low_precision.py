@@ -348,9 +348,13 @@ def mx4_ff_weights(Wg, Wu, Wd, fmt: str = "mxfp4", stream=None):
     F, D = Wg.shape
     if tuple(Wu.shape) != (F, D) or tuple(Wd.shape) != (D, F):
         raise ValueError("Wg and Wu must be F x D and Wd D x F")
-    if stream is not None:
+    if stream is not None:  # made in the stream's share of memory, kept while the current one uses them
+        current = torch.cuda.current_stream(Wg.device)
         with torch.cuda.stream(stream):
-            return mx4_ff_weights(Wg, Wu, Wd, fmt)
+            made = mx4_ff_weights(Wg, Wu, Wd, fmt)
+        for part in (t for q in made for t in (q.codes, q.scales, q.exponents) if t is not None):
+            part.record_stream(current)
+        return made
     pair = [torch.nn.functional.pad(w, (0, 0, 0, -F % 32)).reshape(-1, 32, D) for w in (Wg, Wu)]
     both = torch.stack(pair, 1).view(-1, D)
     return mx4_quantize(both, fmt), mx4_quantize(Wd, fmt)
