@@ -508,7 +508,7 @@ cudaError_t split16(const Matrix16& x, const Matrix16& W0, const Matrix16& W1, b
     g.nk = (int)((x.cols + 63) / 64);
     g.last_steps = (int)((x.cols - (int64_t)(g.nk - 1) * 64 + 15) / 16);
     g.early = early;
-    g.M = x.rows / Epi::HALVES;
+    g.M = (int)x.rows / Epi::HALVES;
     return launch_split_gemm<KIND, PAIRED>(g, maps, epi, st);
 }
 
@@ -587,7 +587,7 @@ struct Share {
 };
 Share best_share(const Product16* w, int count) {
     constexpr int kMaxPairs = 256;
-    const int64_t pairs = std::min(kMaxPairs, std::max(1, tile_sms() / 2));
+    const int64_t pairs = std::min(kMaxPairs, std::max(1, device_sms() / 2));
     int64_t deepest = 0, tiles = 0;
     for (int p = 0; p < count; ++p) {
         deepest = std::max(deepest, w[p].stages());
@@ -615,7 +615,6 @@ Share best_share(const Product16* w, int count) {
                 best_cost = cost;
                 best = Share{nt, depth, depth < deepest};
             }
-            if (deepest < 12) break;
         }
     }
     if (best.nt == 0) best = Share{128, deepest, false};  // all shallower than 12

@@ -27,6 +27,14 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// SMs of the current device.
+inline int device_sms() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 152;
+    return sms;
+}
+
 // Step 1: exponents and part planes.  An operand is A (its rows) or B (its
 // columns); `rows` counts rows of A or columns of B; element (r, k) is
 // hi[r * ld + k] for A and hi[k * ld + r] for B.  Exponent arrays are

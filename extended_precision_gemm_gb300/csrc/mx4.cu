@@ -541,7 +541,7 @@ cudaError_t quantize_typed(const Mx4Quantize& q, const T* X, cudaStream_t st) {
         const bool vec = (uintptr_t)X % 16 == 0 && q.ldx * sizeof(T) % 16 == 0 && q.K % 8 == 0;
         if (q.fmt == kMxfp4) {
             // four tiles a warp once that leaves every SM its 64 warps
-            const bool many = q.rows * kts >= 4 * 64 * 152;
+            const bool many = q.rows * kts >= 4 * 64 * device_sms();
             const int64_t items = many ? q.rows * ((kts + 3) / 4) : q.rows * kts;
             return launch_pdl(many ? mxfp4_rows_kernel<T, 4> : mxfp4_rows_kernel<T, 1>,
                               dim3((unsigned)((items + QWARPS - 1) / QWARPS)), dim3(QWARPS * 32), 0, st, X, q.ldx,
@@ -591,7 +591,7 @@ cudaError_t launch_nvfp4_finish(const float* most, int64_t rows, int64_t K, uint
                                 int32_t* exponents, cudaStream_t st) {
     if (rows == 0 || K == 0) return cudaSuccess;
     const int64_t tiles = mx4_scale_tiles(kNvfp4, K);
-    if (rows >= 152 * 16 && tiles <= 128)
+    if (rows >= 16 * device_sms() && tiles <= 128)
         return launch_pdl(nvfp4_finish_kernel<true>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, most, rows, K,
                           codes, ldq, scales, exponents);
     const unsigned threads = (unsigned)(tiles >= 256 ? 256 : (tiles + 31) / 32 * 32);

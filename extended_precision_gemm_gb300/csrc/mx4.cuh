@@ -258,17 +258,7 @@ template <> __device__ __forceinline__ float from_float<float>(float v) { return
 template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_float<__half>(float v) { return __float2half_rn(v); }
 
-// Eight consecutive elements as floats; `vec`: the address is 16-byte aligned.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&y)[8]) {
-    constexpr int W = sizeof(T) * 8 / 16;
-    uint4 raw[W];
-#pragma unroll
-    for (int i = 0; i < W; ++i) raw[i] = reinterpret_cast<const uint4*>(p)[i];
-    const T* t = reinterpret_cast<const T*>(raw);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = to_float<T>(t[i]);
-}
+// Eight floats as consecutive elements from a 16-byte aligned address on.
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&y)[8]) {
     constexpr int W = sizeof(T) * 8 / 16;

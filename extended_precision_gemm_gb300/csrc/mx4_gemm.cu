@@ -298,7 +298,7 @@ cudaError_t split4(const Mx4Matrix& x, const Mx4Matrix& W, bool early, const Epi
     g.last_steps = (int)((x.K - (int64_t)(g.nk - 1) * MX4_TILE_K + 63) / 64);
     g.tiles_k = (int)mx4_scale_tiles(FMT, x.K);
     g.early = early;
-    g.M = x.rows;
+    g.M = (int)x.rows;
     return launch_split_gemm<KIND, false>(g, maps, epi, st);
 }
 

@@ -44,7 +44,8 @@ struct SplitShape {
     static constexpr int STAGES = kSplitSmem / STAGE_BYTES;
     static constexpr int SMEM = STAGES * STAGE_BYTES + 1024;
     static constexpr uint32_t ACC_COLS = NQ < 32 ? 32 : NQ;
-    static constexpr uint32_t TMEM_COLS = !F4 ? ACC_COLS : NQ <= 64 ? 128 : 256;
+    static constexpr uint32_t TMEM_COLS = !F4 ? ACC_COLS : 128;  // with two sets of 32 columns of scales
+    static_assert(!F4 || NQ <= 64, "tensor memory");
     static_assert(STAGE_BYTES % 1024 == 0 && STAGES >= 2, "ring");
     static_assert(128 * NQ * 4 + kMaxCluster * kMaxCluster * 256 <= STAGES * STAGE_BYTES, "partial sums fit the ring");
 };
@@ -54,14 +55,14 @@ struct SplitMaps {
 };
 
 struct SplitArgs {
-    int nt, mt;        // tiles of 128 weight rows, of NQ tokens
+    int nt;            // tiles of 128 weight rows
     int nk, per;       // stages along k, and of one CTA
     int last_steps;    // MMAs in the last stage
     int tiles_k;       // 4-bit kinds: scale tiles in a row of 128
     const uint8_t *sp, *sq;  // scales of the weights and of the tokens
     int splits;        // CTAs of a cluster
     int early;         // the weights may be read before the wait
-    int64_t M;         // tokens
+    int M;             // tokens
 };
 
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
@@ -77,7 +78,7 @@ __device__ __forceinline__ float ld_shared(uint32_t addr) {
 // tile and token; 2: it is 32 rows of g and 32 of u, 2 units) and
 // emit(v0, v1, token, unit, lane, tile): the whole warp, one row per lane.
 // HALVES = 2: the tokens' matrix holds two rows for each of M tokens, all first
-// ones, then all second ones; v0 and v1 are the sums of each (one tile of NQ).
+// ones, then all second ones; v0 and v1 are the sums of each.
 template <int KIND, int NQ, bool PAIRED16, class Epi>
 __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __grid_constant__ SplitArgs g,
                                                                    const __grid_constant__ SplitMaps maps,
@@ -92,8 +93,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
     const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int z = (int)cluster_ctarank();
-    const int tile = blockIdx.x / g.splits;
-    const int nt = tile % g.nt, mt = tile / g.nt;
+    const int nt = blockIdx.x / g.splits;
     const int k0 = z * g.per, count = min(g.per, g.nk - k0);
     const uint32_t full0 = smem_addr(&bars[0]), empty0 = smem_addr(&bars[STAGES]), done_bar = smem_addr(&bars[2 * STAGES]);
 
@@ -155,10 +155,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
                     load_weights(i, dst, bar);
                 }
                 const int kb = k0 + i;
-                tma_load_2d(dst + S::P_BYTES, &maps.q, kb * ROW, mt * NQ, bar);
+                tma_load_2d(dst + S::P_BYTES, &maps.q, kb * ROW, 0, bar);
                 if (F4)
-                    bulk_load_at(dst + S::P_BYTES + S::Q_BYTES + S::SCALE_BYTES,  // mt > 0 only with 128 tokens
-                                 g.sq + ((int64_t)mt * g.tiles_k + kb * S::SCALE_TILES) * 512, S::SCALE_BYTES, bar);
+                    bulk_load_at(dst + S::P_BYTES + S::Q_BYTES + S::SCALE_BYTES, g.sq + (int64_t)kb * S::SCALE_TILES * 512,
+                                 S::SCALE_BYTES, bar);
             }
             __syncwarp();
             issued = max(issued, i + 1);
@@ -232,8 +232,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
     // Once every MMA of the cluster has finished, the rings hold nothing more.
     constexpr int HALVES = Epi::HALVES, PARTS = Epi::UNITS * HALVES, PER_TOKEN = 4 / Epi::UNITS;
     static_assert(PARTS <= 2, "two sums of a unit at most");
-    const int tokens = (int)min((int64_t)NQ, g.M - (int64_t)mt * NQ);
-    const int units = tokens * PER_TOKEN, splits = g.splits, columns = tokens * HALVES;
+    const int tokens = g.M, units = tokens * PER_TOKEN, splits = g.splits, columns = tokens * HALVES;
     if (!warp_wait(done_bar, 0, 2 * kTileWaitNs) && lane == 0) tile_timeout();
     tc5::fence_after_sync();
     cluster_sync();
@@ -285,7 +284,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) split_gemm_kernel(const __gr
             v0 += p0[c];
             if (PARTS == 2) v1 += p1[c];
         }
-        epi.emit(v0, v1, (int64_t)mt * NQ + w / PER_TOKEN, w % PER_TOKEN, lane, nt);
+        epi.emit(v0, v1, w / PER_TOKEN, w % PER_TOKEN, lane, nt);
     }
 }
 
@@ -304,7 +303,7 @@ cudaError_t launch_split_sized(SplitArgs g, const SplitMaps& maps, const Epi& ep
         ready.fetch_or(1ULL << dev, std::memory_order_relaxed);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((int64_t)g.nt * g.mt * g.splits));
+    cfg.gridDim = dim3((unsigned)((int64_t)g.nt * g.splits));
     cfg.blockDim = dim3(kSplitThreads);
     cfg.dynamicSmemBytes = S::SMEM;
     cfg.stream = st;
@@ -320,13 +319,13 @@ cudaError_t launch_split_sized(SplitArgs g, const SplitMaps& maps, const Epi& ep
     return cudaLaunchKernelEx(&cfg, kernel, g, maps, epi);
 }
 
-// Tokens of a tile: the least of 16, 32, 64 and 128 that holds them all.
+// Tokens that a CTA multiplies: the least of 16, 32, 64 and 128 that holds them all.
 inline int split_nq(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
 // CTAs along k: as many as two to an SM give each tile, at most a cluster,
 // with at least two stages each.
 inline int split_count(int64_t tiles, int nk) {
-    const int64_t slots = 2 * (int64_t)tile_sms();
+    const int64_t slots = 2 * (int64_t)device_sms();
     int64_t s = std::min<int64_t>(kMaxCluster, std::max<int64_t>(1, slots / std::max<int64_t>(1, tiles)));
     s = std::min<int64_t>(s, std::max(1, nk / 2));
     const int per = (int)((nk + s - 1) / s);
@@ -345,17 +344,21 @@ constexpr int kSplitTokens4 = 64, kSplitTokens16 = 128;
 
 template <int KIND, bool PAIRED16, class Epi>
 cudaError_t launch_split_gemm(SplitArgs g, const SplitMaps& maps, const Epi& epi, cudaStream_t st) {
-    const int64_t rows = g.M * Epi::HALVES;
-    const int nq = split_nq(rows);
-    g.mt = (int)((rows + nq - 1) / nq);
-    g.splits = split_count((int64_t)g.nt * g.mt, g.nk);
+    // rows of the tokens' matrix: what the callers send here at most
+    constexpr int MOST = Epi::HALVES == 2 ? 2 * (int)kFullTokens : kind_is_4bit(KIND) ? kSplitTokens4 : kSplitTokens16;
+    const int rows = g.M * Epi::HALVES;
+    if (rows > MOST) return cudaErrorInvalidValue;
+    g.splits = split_count(g.nt, g.nk);
     g.per = (g.nk + g.splits - 1) / g.splits;
-    switch (nq) {
-        case 16: return launch_split_sized<KIND, 16, PAIRED16>(g, maps, epi, st);
-        case 32: return launch_split_sized<KIND, 32, PAIRED16>(g, maps, epi, st);
-        case 64: return launch_split_sized<KIND, 64, PAIRED16>(g, maps, epi, st);
-        default: return launch_split_sized<KIND, 128, PAIRED16>(g, maps, epi, st);
+    const int nq = split_nq(rows);
+    if (nq == 16) return launch_split_sized<KIND, 16, PAIRED16>(g, maps, epi, st);
+    if constexpr (MOST >= 64) {
+        if (nq == 64) return launch_split_sized<KIND, 64, PAIRED16>(g, maps, epi, st);
     }
+    if constexpr (MOST >= 128) {
+        if (nq == 128) return launch_split_sized<KIND, 128, PAIRED16>(g, maps, epi, st);
+    }
+    return launch_split_sized<KIND, 32, PAIRED16>(g, maps, epi, st);
 }
 
 }  // namespace

@@ -109,8 +109,8 @@ __device__ __forceinline__ void tile_of(const TileArgs& g, int64_t t, int& z, in
     n = (int)((t % per_group) / size);
 }
 
-// How A is stored: k contiguous, m contiguous, or as each product says.
-enum Major { kMajorK = 0, kMajorMN = 1, kMajorAny = 2 };
+// How A is stored: k contiguous, or k or m as each product says.
+enum Major { kMajorK = 0, kMajorAny = 1 };
 
 // Epi: NT, GROUPS, and run(acc, product, split, m row, n tile, group, lane, release): takes this
 // warp's 32 rows of the accumulators from column `acc` on (all lanes, also for
@@ -171,7 +171,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
             tile_of(g, t, z, p, mt, nt);
             const TileProduct& q = g.p[p];
             const int it0 = z * q.per, per_tile = min(q.per, q.nk * q.segs - it0);
-            const bool a_mn = A_MAJOR == kMajorAny ? q.a_mn != 0 : A_MAJOR == kMajorMN;
+            const bool a_mn = A_MAJOR == kMajorAny && q.a_mn != 0;
             const int a_row = (mt * 2 + (int)rank) * 128;
             const int b_row = GATED ? nt * (NT / 2) : nt * NT + (int)rank * (NT / 2);
             int seg = it0 / q.nk, kb = it0 % q.nk;
@@ -241,7 +241,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
                 tile_of(g, t, z, p, mt, nt);
                 const TileProduct& q = g.p[p];
                 const int it0 = z * q.per, per_tile = min(q.per, q.nk * q.segs - it0), nk = q.nk, last_steps = q.last_steps;
-                const bool a_mn = A_MAJOR == kMajorAny ? q.a_mn != 0 : A_MAJOR == kMajorMN;
+                const bool a_mn = A_MAJOR == kMajorAny && q.a_mn != 0;
                 const uint64_t ad0 = a_mn ? tc5::desc_mnmajor_sw128(ring, 8192) : tc5::desc_kmajor_sw128(ring);
                 const uint64_t a_step = a_mn ? 2048 / 16 : 2;
                 const uint32_t idesc = IDESC | (a_mn ? 1u << 15 : 0u);
@@ -343,13 +343,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 128 * Epi::GROU
     }
 }
 
-int tile_sms() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 152;
-    return sms;
-}
-
 // Launch on as many CTA pairs as can be resident (never more than tiles).
 template <int KIND, int A_MAJOR, bool B_MN, bool GATED, class Epi>
 cudaError_t launch_tile_gemm(TileArgs g, const TileMaps& maps, const Epi& epi, cudaStream_t st) {
@@ -377,10 +370,10 @@ cudaError_t launch_tile_gemm(TileArgs g, const TileMaps& maps, const Epi& epi, c
         err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
         if (err != cudaSuccess) return err;
         cfg.numAttrs = 1;
-        cfg.gridDim = dim3((unsigned)(2 * std::max(1, tile_sms() / 2)));
+        cfg.gridDim = dim3((unsigned)(2 * std::max(1, device_sms() / 2)));
         if (cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg) != cudaSuccess || pairs <= 0) {
             (void)cudaGetLastError();
-            pairs = std::max(1, tile_sms() / 2);
+            pairs = std::max(1, device_sms() / 2);
         } else {
             cached[dev].store(pairs, std::memory_order_relaxed);
         }
@@ -413,7 +406,7 @@ cudaError_t reset_tile_timeouts(unsigned int* count) {
 // over the narrow ones are shorter: a narrow tile takes `narrow_cost` of a wide
 // one's time, more than its share (its rows of A are read for fewer columns).
 inline bool narrow_tiles(int64_t wide_tiles, int64_t narrow_count, double narrow_cost) {
-    const int64_t pairs = std::max(1, tile_sms() / 2);
+    const int64_t pairs = std::max(1, device_sms() / 2);
     const int64_t wide_rounds = (wide_tiles + pairs - 1) / pairs, rounds = (narrow_count + pairs - 1) / pairs;
     return (double)rounds * narrow_cost < (double)wide_rounds;
 }

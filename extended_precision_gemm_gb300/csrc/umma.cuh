@@ -46,9 +46,6 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigne
 // scales (mx4.cuh).
 enum Kind { kKindF16 = 0, kKindBF16 = 1, kKindMx = 2, kKindNv = 3 };
 __host__ __device__ constexpr bool kind_is_4bit(int kind) { return kind >= kKindMx; }
-// k of a 128-byte shared-memory row, and of one MMA (32 bytes).
-__host__ __device__ constexpr int kind_row_k(int kind) { return kind_is_4bit(kind) ? 256 : 64; }
-__host__ __device__ constexpr int kind_mma_k(int kind) { return kind_is_4bit(kind) ? 64 : 16; }
 
 namespace tc5 {
 
