@@ -96,17 +96,20 @@ private:
 
 // A 16-bit operand as the tensor copies need it (16-byte aligned rows): itself,
 // or a copy in the workspace with whole 128-byte rows.  Rows that are not a
-// multiple of 128 bytes apart also make every copied row touch a line more
-// (1009 tokens, 2056 -> 5400 -> 2056: 82 us, with 2048 53 us); with many tokens
-// a copy costs less than that.
-constexpr int64_t kRealignTokens = 2048;
+// multiple of 128 bytes apart also make every copied row touch a line more (1009
+// tokens, 2056 -> 5400 -> 2056: 65 us, with 2048 for 2056 54 us), which grows with
+// the tokens; a copy costs the weights' bytes.  Forward, us, as they lie and
+// copied: 2049 tokens 129 and 146, 4096 191 and 202, 6144 279 and 278, 8192 368
+// and 361; 4104 -> 12296 -> 4104: 475 and 533, 806 and 829, 1208 and 1199, 1632 and
+// 1559.
+constexpr int64_t kRealignTokens = 6000;
 struct Aligned16 {
     Matrix16 m;
     bool copy;
     int64_t offset;
     Aligned16(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t tokens, Workspace& ws)
         : m{const_cast<void*>(p), rows, cols, ld},
-          copy(rows > 0 && cols > 0 && 
+          copy(rows > 0 && cols > 0 &&
                (!aligned16(p) || (rows > 1 && (ld % 8 != 0 || (tokens > kRealignTokens && ld % 64 != 0))))),
           offset(copy ? ws.reserve(rows * round_up(cols, 64) * 2) : 0) {}
 };
