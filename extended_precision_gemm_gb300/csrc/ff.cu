@@ -17,13 +17,13 @@
 // these roundings average out: an output's error is 1.41 times that of its own
 // rounding.  Of up to kFullTokens the few largest values decide, and it was up
 // to 1.55 times: there what the rounding leaves is kept in as many rows more and
-// enters the products too (16 significant bits for bfloat16, 22 for float16),
-// which costs little, as the weights bind and tiles are mostly idle (4096 x
-// 12288, one token: 50.2 us for 50.0, forward and backward 218 for 214; 16 tokens
-// 53.4 for 52.7 and 201 for 195).
-// Where a sum with remainders is not finite it is the sum without them: an
-// infinity stays one, as of more tokens (156 us for 155, the backward pass of one
-// token, 150 for 149 of 16).
+// enters the products too (16 significant bits for bfloat16, 22 for float16).
+// Where such a sum is not finite it is the one without the remainders: an infinity
+// stays one, as of more tokens.  What this costs, us with and without: 4096 x
+// 12288, where the weights bind, forward 49.9 and 49.8, backward 155 and 149 (one
+// token), 53.4 and 52.5, 151 and 145 (16); small blocks pay for the launch that
+// adds dx's two sums up, 512 x 2048, 16 tokens, 8.6 and 8.3, 18.5 and 16.5, 128 x
+// 640, one token, 6.9 and 6.7, 15.8 and 11.3.
 #include "activation.cuh"
 #include "mx4.cuh"
 #include "split_gemm.cuh"
@@ -436,7 +436,7 @@ cudaError_t map16(CUtensorMap* m, const Matrix16& x, int box_rows) {
 
 int64_t pair_tiles(int64_t M, int64_t N, int64_t per_tile) { return (M + 255) / 256 * ((N + per_tile - 1) / per_tile); }
 
-constexpr double kNarrow16 = 0.6;  // 128 columns for 256: 783 us against 683 for the forward of 4096 x 4096 x 12288
+constexpr double kNarrow16 = 0.6;  // 128 columns for 256: 722 us against 642 for the forward of 4096 x 4096 x 12288
 bool narrow16(int64_t M, int64_t N, int64_t wide) {
     return narrow_tiles(pair_tiles(M, N, wide), pair_tiles(M, N, wide / 2), kNarrow16);
 }

@@ -232,11 +232,11 @@ struct Matrix16 {
 // Copies to rows of cols rounded up to 64 elements.
 constexpr int kRealignMax = 5;
 cudaError_t launch_realign(const Matrix16* src, const Matrix16* dst, int count, cudaStream_t st);
-// The gated block; operands 16-byte aligned with 16-byte rows.  h, a, b (and
-// dg, du): planes of T rows of ld elements (F rounded up to 64); a and b as
-// float16 with a byte for every 32 in ea and eb (bfloat16), or in 32 bits.
-// Up to how many tokens h, dg and du keep what their rounding leaves, in as many
-// rows more (see ff.cu).
+// The gated block; operands 16-byte aligned with 16-byte rows.  h (and dg, du):
+// planes of ff_rows(T) rows of ld elements (F rounded up to 64), a and b of T rows,
+// as float16 with a byte for every 32 in ea and eb (bfloat16), or in 32 bits.
+// kFullTokens: up to how many tokens h, dg and du keep what their rounding leaves,
+// in as many rows more (see ff.cu).
 constexpr int64_t kFullTokens = 16;
 inline int64_t ff_rows(int64_t T) { return T <= kFullTokens ? 2 * T : T; }
 struct FfForward {

@@ -4,9 +4,11 @@
 // scale byte: bound by HBM (2.56 bytes per 16-bit value for nvfp4, 2.53 for
 // mxfp4) with about 10 instructions to hide for every 32 values of a warp.
 // Columns of 8192 x 16384 16-bit values to nvfp4: 56 us and 15 us to finish the
-// scales (0.90 of the copy rate in the first, 63% of the issue slots); back to
-// 16 bits 51 us (343 MB, 0.98 of the copy rate).  4096 x 4096 rows to mxfp4:
-// 12.5 us (43 MB); one row of 8192: 3 us, the latency of a launch.
+// scales (0.90 of the copy rate in the first, 63% of the issue slots), to mxfp4 51
+// us; back to 16 bits 51 us (343 MB, 0.98 of the copy rate).  Rows, which a warp
+// converts a value at a time, take the issue slots: 74 us to mxfp4 (75% of them, 54%
+// of HBM), 121 us to nvfp4 (quotients instead of products: 76%, 33%); 4096 x 4096
+// rows 10.2 and 37.5 us; one row of 8192 1.7 us behind another launch.
 #include "launch.cuh"
 #include "mx4.cuh"
 

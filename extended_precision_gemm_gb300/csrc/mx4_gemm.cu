@@ -2,8 +2,8 @@
 // (C = alpha A B^T) and the two products of the 4-bit gated block: operands,
 // epilogues and launches for the two kernels that multiply.  Up to 64 rows of A
 // the weights are what has to be moved and split_gemm.cuh streams them over all
-// SMs (HBM; 1 x 8192 x 8192 nvfp4 8.5 us); more rows are the tensor pipe's work
-// and go by CTA pairs in tile_gemm.cuh (8192^3 nvfp4 163 us).
+// SMs (1 x 8192 x 8192 nvfp4 9.1 us from HBM, 6.8 from L2); more rows are the tensor
+// pipe's work and go by CTA pairs in tile_gemm.cuh (8192^3 nvfp4 161 us).
 #include <cmath>
 
 #include "activation.cuh"
@@ -304,7 +304,7 @@ cudaError_t split4(const Mx4Matrix& x, const Mx4Matrix& W, bool early, const Epi
 
 int64_t pair_tiles(const Mx4Matrix& A, const Mx4Matrix& B, int nt) { return (A.rows + 255) / 256 * ((B.rows + nt - 1) / nt); }
 
-constexpr double kNarrow4 = 0.78;  // 128 columns for 192: 195 us against 166 for 8192^3 nvfp4
+constexpr double kNarrow4 = 0.78;  // 128 columns for 192: 191 us against 162 for 8192^3 nvfp4
 bool narrow4(const Mx4Matrix& A, const Mx4Matrix& B) {
     return narrow_tiles(pair_tiles(A, B, 192), pair_tiles(A, B, 128), kNarrow4);
 }

@@ -17,10 +17,10 @@
 // and if the weights are EARLY (nothing that the launch before this one
 // writes), the ring is filled with them ahead of it.
 //
-// Weights of 37.7 MB from HBM (8192 x 8192 nvfp4) with one token: 9.2 us, 4.1
-// TB/s; the 16-bit block of 302 MB: 51 us, 5.9 TB/s, 0.87 of the copy rate.  A
+// Weights of 37.7 MB from HBM (8192 x 8192 nvfp4) with one token: 9.1 us, 4.1
+// TB/s; the 16-bit block of 302 MB: 51 us, 5.9 TB/s, 0.88 of the copy rate.  A
 // launch by itself has 6 us in which HBM is idle (launch, first copies, barriers,
-// store); each further token costs about 0.1 us, in the epilogue.
+// store); each further token costs about 0.05 us, in the epilogue.
 #pragma once
 
 #include "mx4.cuh"
@@ -334,12 +334,18 @@ inline int split_count(int64_t tiles, int nk) {
 
 // Up to how many tokens the split kernel takes a product; beyond, the pairs'
 // tiles are faster although they leave SMs idle.  Weights from HBM, us:
-//                          64 tokens            128 tokens
-//                        split    pairs       split    pairs
-//   8192 x 8192 nvfp4     12.2     13.3        15.5     13.3
-//   12288 x 4096 mxfp4    10.1      9.1        13.6      9.8
-//   4096 x 12288 mxfp4     9.7     13.0        12.6     13.4
-//   16-bit block 4096 x 12288    59.9  79.0    68.9     80.4
+//                          33 tokens         64 tokens        128 tokens
+//                        split    pairs    split    pairs    split    pairs
+//   8192 x 8192 nvfp4     10.7     12.9     12.0     13.0     15.5     13.3
+//   8192 x 8192 mxfp4      9.7     10.9     10.8     11.1
+//   4096 x 12288 mxfp4     8.4     12.9      9.6     13.0     12.6     13.4
+//   2048 x 16384 mxfp4     8.2     15.4      9.5     15.6
+//   512 x 16384 nvfp4      6.3     16.2      7.3     16.3
+//   12288 x 4096 mxfp4     9.1     10.4     10.0      9.4     13.6      9.8
+//   8192 x 1024 mxfp4      5.2      4.8      6.3      5.1
+//   2048 x 1024 nvfp4      5.4      5.3      6.9      5.5
+//   16-bit block 4096 x 12288               59.9     79.0     68.9     80.4
+// Short sums are the exception from 33 tokens on, by up to 1.4 us.
 constexpr int kSplitTokens4 = 64, kSplitTokens16 = 128;
 
 template <int KIND, bool PAIRED16, class Epi>

@@ -27,8 +27,9 @@
 // for every other tile.
 //
 // Bound by the tensor pipe (16 bits: 94 to 98% busy, 1.69 to 1.93 PF/s at 4096 x
-// 4096 x 8192, and the power cap in a loop; 4 bits: 83% busy, 6.2 P/s at 4096 x
-// 4096 x 16384, 163 us for 8192^3 nvfp4 and 150 us mxfp4).  A pair's tile of 256
+// 4096 x 8192, and the power cap in a loop; 4 bits: 83% busy, 6.5 P/s at 4096 x
+// 4096 x 16384; 8192^3 nvfp4 161 us and mxfp4 151, in a loop, at the power cap, 187
+// and 168).  A pair's tile of 256
 // by NT is the largest whose accumulators fit tensor memory twice: an epilogue
 // costs up to 3 us, which one accumulator would add to every tile.  Short sums
 // are bound by their epilogue all the same (depth 1280, gelu: 3 us a tile against

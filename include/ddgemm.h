@@ -733,7 +733,7 @@ ddgemm_status dd_mx4_quantize(int format, int type, int columns, int64_t rows, i
                               uint8_t* codes, int64_t ldq, uint8_t* scales, int32_t* exponents, void* stream);
 
 /* The values a 4-bit matrix stands for, rounded to `type` (exact in F32 and
- * BF16 but for underflow): X is rows x K, ldx >= K. */
+ * BF16 within their ranges): X is rows x K, ldx >= K. */
 ddgemm_status dd_mx4_dequantize(int format, int type, int64_t rows, int64_t K, const uint8_t* codes, int64_t ldq,
                                 const uint8_t* scales, const int32_t* exponents, void* X, int64_t ldx, void* stream);
 
@@ -763,9 +763,9 @@ ddgemm_status dd_mx4_gemm(int format, int64_t M, int64_t N, int64_t K, const uin
  * D x F, y T x D, all of `type` (DDGEMM_BF16 or DDGEMM_F16), any leading
  * dimensions.  Sums, the activation and the product are in 32 bits; h is
  * rounded to `type` between the two products (of up to 16 tokens, to twice its
- * bits).  `saved`, if not NULL, receives
- * what the backward pass needs (dd_ff_gated_saved_size bytes, 256-byte
- * aligned; opaque, of the library's version that wrote it).
+ * bits, unless a sum then is not finite).  `saved`, if not NULL, receives what the
+ * backward pass needs (dd_ff_gated_saved_size bytes, 256-byte aligned; opaque, of
+ * the library's version that wrote it).
  */
 ddgemm_status dd_ff_gated_saved_size(int type, int64_t T, int64_t F, size_t* bytes);
 ddgemm_status dd_ff_gated(int type, int activation, int64_t T, int64_t D, int64_t F, const void* x, int64_t ldx,
@@ -776,8 +776,8 @@ ddgemm_status dd_ff_gated(int type, int activation, int64_t T, int64_t D, int64_
  * The gradients of the block from dy (T x D): dx (T x D), dWg and dWu (F x D)
  * and dWd (D x F), each written (not added to); one that is NULL is not
  * computed.  dh = dy Wd; dg = dh u act'(g) and du = dh act(g) are rounded to
- * `type` before the products they enter.  `saved` is that of dd_ff_gated on
- * the same T, F and type.
+ * `type` before the products they enter (of up to 16 tokens, to twice its bits).
+ * `saved` is that of dd_ff_gated on the same T, F and type.
  */
 ddgemm_status dd_ff_gated_backward(int type, int64_t T, int64_t D, int64_t F, const void* dy, int64_t lddy,
                                    const void* x, int64_t ldx, const void* Wg, int64_t ldwg, const void* Wu,
