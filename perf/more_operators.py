@@ -12,7 +12,8 @@ The cache.  A token has one row of k and one of v for each key/value head, in a
 4-bit format:
 
   mxfp4   E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and negatives), blocks of 32
-          with scale 2^(byte - 127), byte = floor(log2 max|x|) - 2 + 127
+          with scale 2^(byte - 127), byte = floor(log2 max|x|) - 2 + 127; the
+          row's exponent is its largest byte - 127
   nvfp4   the same codes, blocks of 16 with scale E4M3 = max|x| / (6 2^e) to
           nearest, e for each row: the least with max|row| <= 2688 2^e
 
@@ -20,7 +21,7 @@ Values round to the nearest code, ties to the even one, and saturate at 6.  Rows
 are stored with the head dimension filled up to 64, 128 or 256, in pages of
 page_size tokens: codes (pages, 2, heads, page_size, width / 2) with the even
 element in the low nibble, scales (pages, 2, heads, page_size, width / block),
-exponents (nvfp4, int8) (pages, 2, heads, page_size); 0 is k and 1 is v.
+exponents (int8) (pages, 2, heads, page_size); 0 is k and 1 is v.
 
 A batch.  Sequence b has lengths[b] tokens in the cache, the pages page_table[b],
 and the new tokens starts[b] .. starts[b + 1] of the call, which are its last.
@@ -149,7 +150,7 @@ def work(case):
     if kind == "rotary":
         n = case["tokens"] * case["heads"] * case["dim"] * (2 if case["train"] else 1)
         return {"bytes": 2 * n * size, "flops": 3.0 * n * case["part"] / case["dim"]}
-    stored = case["dim"] * (0.5 + 1 / FORMATS[case["fmt"]]) + (case["fmt"] == "nvfp4")  # bytes of a row
+    stored = case["dim"] * (0.5 + 1 / FORMATS[case["fmt"]]) + 1  # bytes of a row
     batch = batch_of(case)
     if kind == "cache":
         rows = 2 * case["heads"] * sum(n for _, n in batch)
@@ -270,9 +271,10 @@ def stored(x, fmt, dim):
     m, ex = torch.frexp(scale)
     if fmt == "mxfp4":
         byte = torch.where(scale > 0, ex + 126, 0)
+        e = byte.amax(-1) - 127
     else:  # E4M3: subnormals count in steps of 2^-9
         byte = torch.where(scale < 2.0 ** -6, scale * 512, (ex + 6) * 8 + (m * 16 - 8))
-    return {"codes": (code[..., 0::2] | code[..., 1::2] << 4).contiguous(), "scales": byte.to(torch.uint8), "exponents": e.to(torch.int8) if fmt == "nvfp4" else None,
+    return {"codes": (code[..., 0::2] | code[..., 1::2] << 4).contiguous(), "scales": byte.to(torch.uint8), "exponents": e.to(torch.int8),
             "head_dim": dim, "fmt": fmt}
 
 
@@ -349,9 +351,9 @@ def run_plain(s):
         values = torch.nn.functional.pad(torch.stack((k.float(), s["v"].float()), 1), (0, width_of(dim) - dim))
         new = stored(values, fmt, dim)
         at, off = s["table"][b, position // page].long(), position % page
-        for name in ("codes", "scales") + (("exponents",) if fmt == "nvfp4" else ()):
+        for name in ("codes", "scales", "exponents"):
             cache[name][at, :, :, off] = new[name]
-        rows = [None if cache[name] is None else cache[name][at, :, :, off] for name in ("codes", "scales", "exponents")]
+        rows = [cache[name][at, :, :, off] for name in ("codes", "scales", "exponents")]
         values = stood_for(*rows, fmt)[..., :dim].to(torch.bfloat16)
         return values[:, 0].contiguous(), values[:, 1].contiguous()
 
@@ -359,7 +361,7 @@ def run_plain(s):
     most = s["most_seen"]
     j = torch.arange(most, device="cuda")
     at, off = s["table"][:, j // page].clamp(min=0).long(), j % page
-    rows = [None if cache[name] is None else cache[name][at, :, :, off] for name in ("codes", "scales", "exponents")]
+    rows = [cache[name][at, :, :, off] for name in ("codes", "scales", "exponents")]
     k, v = stood_for(*rows, fmt)[..., :dim].permute(2, 0, 3, 1, 4)
     heads, group = s["heads"], s["group"]
     q = torch.zeros(s["batch"], s["most_new"], heads, group, dim, device="cuda")
@@ -444,7 +446,7 @@ def exact(case, seed):
     out, at = [], 0
     for b, (length, n) in enumerate(batch):
         used = s["table"][b, : -(-length // case["page"])].long()
-        rows = [None if s["cache"][name] is None else s["cache"][name][used].movedim(3, 1).flatten(0, 1)[:length] for name in ("codes", "scales", "exponents")]
+        rows = [s["cache"][name][used].movedim(3, 1).flatten(0, 1)[:length] for name in ("codes", "scales", "exponents")]
         kv = stood_for(*rows, case["fmt"], torch.float64)[..., : case["dim"]]  # (length, 2, heads, dim)
         q = s["q"][at : at + n].double().unflatten(1, (case["heads"], case["group"]))
         at += n
