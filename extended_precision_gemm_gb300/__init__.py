@@ -40,6 +40,8 @@ __all__ = [
     "md_recombine_tc",
     "MX4", "MX4_FORMATS", "mx4_layout", "mx4_quantize", "mx4_dequantize", "mx4_tile_scales", "mx4_gemm",
     "mx4_ff_weights", "mx4_ff_gated", "ACTIVATIONS", "ff_gated", "ff_gated_backward", "ff_gated_saved_size",
+    "Rotary", "ROTARY_SCALINGS", "rotary_table", "rotary", "rotary_backward",
+    "MX4Cache", "mx4_cache_layout", "mx4_cache", "mx4_cache_append", "mx4_cache_read", "mx4_attention",
 ]
 
 SLICES = 8
@@ -139,6 +141,12 @@ _SIGNATURES = {
                      ctypes.c_size_t, _ptr], _int),
     "dd_ff_gated_backward": ([_int, _i64, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64,
                               _ptr, ctypes.c_size_t, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr], _int),
+    "dd_rotary": ([_int, _i64, _i64, _i64, _ptr, _i64, _i64, _ptr, _int, _ptr, _int, _ptr, _i64, _i64, _ptr], _int),
+    "dd_mx4_cache_layout": ([_int, _i64, _ptr, _ptr], _int),
+    "dd_mx4_cache_append": ([_ptr, _ptr, _int, _ptr, _i64, _i64, _ptr, _i64, _i64, _ptr, _ptr], _int),
+    "dd_mx4_cache_read": ([_ptr, _ptr, _int, _ptr, _i64, _i64, _ptr, _i64, _i64, _ptr], _int),
+    "dd_mx4_attention": ([_ptr, _ptr, _int, _i64, _ptr, _i64, _i64, _i64, _i64, ctypes.c_float, _ptr, _i64, _i64,
+                          _ptr], _int),
     "dd_call_packed": ([_int, ctypes.c_char_p], _int),
 }
 
@@ -1028,3 +1036,10 @@ def md_recombine_tc(nparts: int, M: int, N: int, P, e, f, splits=None, C=None, s
 from .low_precision import (  # noqa: E402
     ACTIVATIONS, MX4, MX4_FORMATS, ff_gated, ff_gated_backward, ff_gated_saved_size, mx4_dequantize, mx4_ff_gated,
     mx4_ff_weights, mx4_gemm, mx4_layout, mx4_quantize, mx4_tile_scales)
+
+
+# ---- rotary positions, the 4-bit key/value cache and attention over it ----
+
+from .attention import (  # noqa: E402
+    ROTARY_SCALINGS, MX4Cache, Rotary, mx4_attention, mx4_cache, mx4_cache_append, mx4_cache_layout, mx4_cache_read, rotary,
+    rotary_backward, rotary_table)

@@ -1,0 +1,149 @@
+// attend.cuh -- what the kernels of attention over the 4-bit cache share: which
+// tokens a query sees, and the partial results of work split over a long cache.
+//
+// o = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m) over the tokens j that a query sees,
+// with s_j = scale log2(e) q.k_j.  A cache row's value is its codes and block scales
+// (exact in 16-bit floating point) times 2^r, r the row's exponent: it joins s_j as
+// a factor for keys, and for values the weight is 2^(s_j + r_j - M) with a reference
+// M of its own, so rows of any size meet in range.  A part of the sum is (m, M, l, o):
+// l = sum 2^(s - m), o = sum 2^(s + r - M) (codes times scales).
+#pragma once
+
+#include <cstdint>
+#include <cstring>
+#include <type_traits>
+
+#include "kv_cache.cuh"
+
+namespace ddg {
+
+// A launch of the kernels below.
+struct AttendArgs {
+    CacheView c;
+    BatchView b;
+    const void* q;
+    void* out;
+    int64_t qt, qh, ot, oh;  // strides of tokens and heads
+    int heads, group;        // of queries; queries a key/value head
+    int window, sinks;       // window 0: none
+    float scale;             // log2(e) times the scale of scores
+    bool vec_q, vec_out;
+    int splits;
+    float4* part;  // (m, M, l, 1 if any token is seen) by split and row (token, query head)
+    float* sums;   // o by split and row, `width` each
+};
+
+#ifdef __CUDACC__
+
+namespace {
+
+__device__ __forceinline__ float minus_infinity() { return __uint_as_float(0xff800000u); }
+__device__ __forceinline__ float not_a_number() { return __uint_as_float(0x7fc00000u); }
+
+// 2^x by one instruction (2^-22; 0 below 2^-126).
+__device__ __forceinline__ float power2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A reference that may be minus infinity (nothing seen yet) as a number to subtract.
+__device__ __forceinline__ float reference(float m) { return m == minus_infinity() ? 0.0f : m; }
+
+// Query tokens [first, last] of a sequence, at positions p0 .. p1: the groups of 16
+// tokens that any of them sees, those of the sinks and then those from `low` on.
+struct Groups {
+    int sink, low, count;
+};
+// The last one is at most the first that the page table does not reach.
+__device__ __forceinline__ Groups groups_of(const CacheView& c, const BatchView& b, int p0, int p1, int window, int sinks) {
+    Groups g{0, 0, 0};
+    if (p1 < 0) return g;
+    const int end = (int)min((int64_t)p1 / 16 + 1, (int64_t)b.table_pages * c.page_size / 16 + 1);
+    if (window > 0 && p0 >= window) {
+        g.low = min((p0 - window + 1) / 16, end - 1);
+        g.sink = min((min(sinks, p1 + 1) + 15) / 16, g.low);
+    }
+    g.count = g.sink + end - g.low;
+    return g;
+}
+__device__ __forceinline__ int group_token(const Groups& g, int i) { return (i < g.sink ? i : i - g.sink + g.low) * 16; }
+
+__device__ __forceinline__ bool sees(int p, int j, int window, int sinks) {
+    return j <= p && (window == 0 || j > p - window || j < sinks);
+}
+
+// Work items are tiles of `columns` (query token, head of the group) pairs of one
+// sequence and key/value head.  Sequence b's tiles are numbered from
+// floor(starts[b] group / columns) + b on, which leaves room for all of them
+// whatever the sequences' sizes; numbers between are of no tile.
+struct Item {
+    int sequence, column, columns, first_token, tokens, length;
+};
+// The last sequence b with starts[b] group / columns + step b <= t, found by a whole
+// warp; -1 if there is none.
+__device__ __forceinline__ int search(const BatchView& b, int64_t t, int group, int columns, int step) {
+    const int lane = threadIdx.x & 31;
+    int low = 0, high = b.batch;  // the answer is in [low, high)
+    bool none = b.batch <= 0;
+    while (!none && (high - low > 1 || low == 0)) {
+        const int stride = (high - low + 31) / 32;
+        const int i = low + lane * stride;
+        const bool at = i < high && (int64_t)b.starts[i] * group / columns + (int64_t)step * i <= t;
+        const int n = __popc(__ballot_sync(~0u, at));
+        none = n == 0;
+        low += none ? 0 : (n - 1) * stride;
+        high = min(high, low + stride);
+        if (stride == 1) break;
+    }
+    return none ? -1 : low;
+}
+// Tile t's part of the batch.
+__device__ __forceinline__ Item item_of(const BatchView& b, int64_t t, int group, int columns) {
+    const Item nothing{-1, 0, 0, 0, 0, 0};
+    const int s = search(b, t, group, columns, 1);
+    if (s < 0) return nothing;
+    const int64_t s0 = b.starts[s], s1 = b.starts[s + 1];
+    const int64_t column = (t - (s0 * group / columns + s)) * columns;
+    if (s0 < 0 || s1 > b.tokens || column < 0 || column >= (s1 - s0) * group) return nothing;
+    return Item{s, (int)column, (int)min((int64_t)columns, (s1 - s0) * group - column), (int)s0, (int)(s1 - s0), b.lengths[s]};
+}
+
+// How a row's sums become its output: times x twice (half of the exponent each),
+// over l; 0 where no token is seen.
+struct Finish {
+    float x, inverse;
+};
+__device__ __forceinline__ Finish finish_of(float m, float M, float l, float lift, bool any) {
+    if (!any) return Finish{0.0f, 0.0f};
+    return Finish{power2(0.5f * (reference(M) - reference(m) - lift)), 1.0f / l};
+}
+// Elements d .. d + 3 of an output row.
+template <typename T>
+__device__ __forceinline__ void store4(T* out, int d, int dim, bool vec, const Finish& z, const float (&y)[4]) {
+    T t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = from_float<T>(z.inverse == 0.0f && z.x == 0.0f ? 0.0f : y[i] * z.x * z.x * z.inverse);
+    if (vec && d + 4 <= dim) {
+        uint2 w;
+        memcpy(&w, t, 8);
+        *reinterpret_cast<uint2*>(out + d) = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (d + i < dim) out[d + i] = t[i];
+    }
+}
+
+}  // namespace
+
+#endif  // __CUDACC__
+
+// Tiles of `columns` that sequences of `tokens` tokens in all may have.
+inline int64_t attend_tiles(const BatchView& b, int group, int columns) { return b.tokens * group / columns + b.batch; }
+
+cudaError_t launch_attend_columns(const AttendArgs& a, int type, cudaStream_t st);
+// Into how many parts it cuts a row's tokens.
+int attend_columns_parts(const AttendArgs& a);
+
+}  // namespace ddg

@@ -1,0 +1,226 @@
+// attend_api.cu -- the C entry points of rotary positions, the paged 4-bit cache and
+// attention over it (declarations in ddgemm.h): argument checks, workspaces,
+// launch sequences.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "attend.cuh"
+#include "entry.cuh"
+
+using namespace ddg;
+
+namespace {
+
+// A tokens x heads x dim array with its strides of tokens and heads.
+struct Heads {
+    const void* p;
+    int64_t tokens, heads, dim, per_token, per_head, elem;
+
+    // Heads and tokens that do not overlap, whichever of the two is the inner one,
+    // within 2^62 bytes.
+    bool sound() const {
+        if (tokens == 0 || heads == 0 || dim == 0) return true;
+        if (p == nullptr || (uintptr_t)p % elem != 0) return false;
+        const long double t = tokens > 1 ? per_token : 0, h = heads > 1 ? per_head : 0;
+        const long double all_tokens = (tokens - 1) * t, all_heads = (heads - 1) * h;
+        if (t < 0 || h < 0 || (all_tokens + all_heads + dim) * elem > 4.6e18L) return false;
+        if (heads > 1 && tokens > 1) return (h >= dim && t >= all_heads + dim) || (t >= dim && h >= all_tokens + dim);
+        return (heads <= 1 || h >= dim) && (tokens <= 1 || t >= dim);
+    }
+    int64_t bytes() const {
+        if (tokens == 0 || heads == 0 || dim == 0) return 0;
+        return ((tokens - 1) * (tokens > 1 ? per_token : 0) + (heads - 1) * (heads > 1 ? per_head : 0) + dim) * elem;
+    }
+};
+bool meet(const Heads& a, const Heads& b) { return overlap(a.p, a.bytes(), b.p, b.bytes()); }
+
+ddgemm_status check_cache(const ddgemm_mx4_cache* c, CacheView& v) {
+    if (c == nullptr || !known_format(c->format) || c->pages < 0 || c->heads < 1 || c->head_dim < 1) return DDGEMM_ERR_INVALID_ARG;
+    if (c->head_dim > 256 || c->heads > DDGEMM_MAX_HEADS || c->pages >= (1LL << 31)) return DDGEMM_ERR_UNSUPPORTED;
+    if (c->page_size < 16 || c->page_size > 65536 || (c->page_size & (c->page_size - 1)) != 0) return DDGEMM_ERR_INVALID_ARG;
+    if (c->pages > (1LL << 50) / (c->page_size * c->heads * 256)) return DDGEMM_ERR_UNSUPPORTED;
+    if (c->pages > 0 && (c->codes == nullptr || c->scales == nullptr || c->exponents == nullptr || !aligned16(c->codes) ||
+                         !aligned16(c->scales) || !aligned16(c->exponents)))
+        return DDGEMM_ERR_INVALID_ARG;
+    int shift = 0;
+    while ((1 << shift) < c->page_size) ++shift;
+    v = CacheView{c->format, cache_width(c->head_dim), (int)c->head_dim, (int)c->heads, c->pages, (int)c->page_size, shift,
+                  c->codes, c->scales, c->exponents};
+    return DDGEMM_OK;
+}
+
+ddgemm_status check_batch(const ddgemm_batch* b, BatchView& v) {
+    if (b == nullptr || b->tokens < 0 || b->batch < 0 || b->table_pages < 0) return DDGEMM_ERR_INVALID_ARG;
+    if (b->tokens > DDGEMM_MAX_TOKENS || b->batch > DDGEMM_MAX_TOKENS || b->table_pages > DDGEMM_MAX_TOKENS)
+        return DDGEMM_ERR_UNSUPPORTED;
+    if (b->batch > 0 && b->tokens > 0) {
+        if (b->starts == nullptr || b->lengths == nullptr || (b->page_table == nullptr && b->table_pages > 0)) return DDGEMM_ERR_INVALID_ARG;
+        if (((uintptr_t)b->starts | (uintptr_t)b->lengths | (uintptr_t)b->page_table) % 4 != 0) return DDGEMM_ERR_INVALID_ARG;
+        if (b->batch > 1 && b->table_stride < b->table_pages) return DDGEMM_ERR_INVALID_ARG;
+    }
+    v = BatchView{b->tokens, (int)b->batch, b->starts, b->lengths, b->page_table, (int)b->table_pages, b->table_stride};
+    return DDGEMM_OK;
+}
+
+bool overlaps_cache(const CacheView& c, const void* p, int64_t bytes) {
+    const int64_t rows = c.pages * 2 * c.heads * c.page_size;
+    return overlap(c.codes, rows * (c.width / 2), p, bytes) || overlap(c.scales, rows * (c.width / mx4_block(c.fmt)), p, bytes) ||
+           overlap(c.exponents, rows, p, bytes);
+}
+bool overlaps_batch(const BatchView& b, const void* p, int64_t bytes) {
+    return overlap(b.starts, (b.batch + 1LL) * 4, p, bytes) || overlap(b.lengths, b.batch * 4LL, p, bytes) ||
+           overlap(b.table, b.batch > 0 ? ((b.batch - 1) * b.ld_table + b.table_pages) * 4 : 0, p, bytes);
+}
+// Nothing of the cache or of the batch is written through another argument.
+bool batch_in_cache(const CacheView& c, const BatchView& b) {
+    return overlaps_cache(c, b.starts, (b.batch + 1LL) * 4) || overlaps_cache(c, b.lengths, b.batch * 4LL) ||
+           overlaps_cache(c, b.table, b.batch > 0 ? ((b.batch - 1) * b.ld_table + b.table_pages) * 4 : 0);
+}
+
+// The factor of a rotation as a float and what it leaves.
+void two_floats(double x, float& hi, float& lo) {
+    hi = (float)x;
+    lo = std::isfinite(hi) ? (float)(x - (double)hi) : 0.0f;
+}
+
+ddgemm_status check_rotary(const ddgemm_rotary* r, int64_t dim) {
+    if (r == nullptr || r->pairs < 0 || (r->interleaved != 0 && r->interleaved != 1)) return DDGEMM_ERR_INVALID_ARG;
+    if (r->pairs > dim / 2) return DDGEMM_ERR_INVALID_ARG;
+    if (r->pairs > 0 && (r->turns == nullptr || (uintptr_t)r->turns % 8 != 0)) return DDGEMM_ERR_INVALID_ARG;
+    return DDGEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ddgemm_status dd_rotary(int type, int64_t tokens, int64_t heads, int64_t dim, const void* x, int64_t x_token,
+                        int64_t x_head, const void* positions, int wide, const ddgemm_rotary* rotary, int inverse,
+                        void* y, int64_t y_token, int64_t y_head, void* stream) {
+    if (!known_type(type) || tokens < 0 || heads < 0 || dim < 0 || (wide != 0 && wide != 1) || (inverse != 0 && inverse != 1))
+        return DDGEMM_ERR_INVALID_ARG;
+    if (tokens > DDGEMM_MAX_TOKENS || heads > DDGEMM_MAX_HEADS || dim > DDGEMM_MAX_ROTARY_DIM) return DDGEMM_ERR_UNSUPPORTED;
+    const ddgemm_status s = check_rotary(rotary, dim);
+    if (s != DDGEMM_OK) return s;
+    const Heads in{x, tokens, heads, dim, x_token, x_head, type_bytes(type)}, out{y, tokens, heads, dim, y_token, y_head, type_bytes(type)};
+    if (!in.sound() || !out.sound()) return DDGEMM_ERR_INVALID_ARG;
+    if (tokens == 0 || heads == 0 || dim == 0) return DDGEMM_OK;
+    const int64_t pos = wide ? 8 : 4;
+    if (positions == nullptr || (uintptr_t)positions % pos != 0) return DDGEMM_ERR_INVALID_ARG;
+    const bool in_place = x == y && (tokens <= 1 || x_token == y_token) && (heads <= 1 || x_head == y_head);
+    if (!in_place && meet(in, out)) return DDGEMM_ERR_INVALID_ARG;
+    if (overlap(positions, tokens * pos, y, out.bytes()) || overlap(rotary->turns, rotary->pairs * 8, y, out.bytes()))
+        return DDGEMM_ERR_INVALID_ARG;
+    Rotary r{type, tokens, (int)heads, (int)dim, x, x_token, x_head, y, y_token, y_head, positions, wide == 1, rotary->turns,
+             (int)rotary->pairs, 0.0f, 0.0f, rotary->interleaved == 1, inverse == 1, 0};
+    two_floats(rotary->scale, r.m, r.ml);
+    return status_of(launch_rotary(r, static_cast<cudaStream_t>(stream)));
+}
+
+ddgemm_status dd_mx4_cache_layout(int format, int64_t head_dim, int64_t* width, int64_t* scale_bytes) {
+    if (!known_format(format) || head_dim < 1) return DDGEMM_ERR_INVALID_ARG;
+    if (head_dim > 256) return DDGEMM_ERR_UNSUPPORTED;
+    const int w = cache_width(head_dim);
+    if (width) *width = w;
+    if (scale_bytes) *scale_bytes = w / mx4_block(format);
+    return DDGEMM_OK;
+}
+
+ddgemm_status dd_mx4_cache_append(const ddgemm_mx4_cache* cache, const ddgemm_batch* batch, int type, const void* k,
+                                  int64_t k_token, int64_t k_head, const void* v, int64_t v_token, int64_t v_head,
+                                  const ddgemm_rotary* rotary, void* stream) {
+    CacheAppend g{};
+    if (!known_type(type)) return DDGEMM_ERR_INVALID_ARG;
+    ddgemm_status s = check_cache(cache, g.cache);
+    if (s == DDGEMM_OK) s = check_batch(batch, g.batch);
+    if (s == DDGEMM_OK && rotary != nullptr) s = check_rotary(rotary, cache->head_dim);
+    if (s != DDGEMM_OK) return s;
+    const int64_t T = batch->tokens, H = cache->heads, D = cache->head_dim;
+    const Heads hk{k, T, H, D, k_token, k_head, type_bytes(type)}, hv{v, T, H, D, v_token, v_head, type_bytes(type)};
+    if (!hk.sound() || !hv.sound()) return DDGEMM_ERR_INVALID_ARG;
+    if (T == 0 || batch->batch == 0) return DDGEMM_OK;
+    if (overlaps_cache(g.cache, k, hk.bytes()) || overlaps_cache(g.cache, v, hv.bytes()) || batch_in_cache(g.cache, g.batch) ||
+        (rotary != nullptr && overlaps_cache(g.cache, rotary->turns, rotary->pairs * 8)))
+        return DDGEMM_ERR_INVALID_ARG;
+    g.type = type;
+    g.k = k, g.kt = k_token, g.kh = k_head;
+    g.v = v, g.vt = v_token, g.vh = v_head;
+    if (rotary != nullptr && rotary->pairs > 0) {
+        g.turns = rotary->turns;
+        g.half = (int)rotary->pairs;
+        two_floats(rotary->scale, g.m, g.ml);
+        g.interleaved = rotary->interleaved == 1;
+    }
+    return status_of(launch_cache_append(g, static_cast<cudaStream_t>(stream)));
+}
+
+ddgemm_status dd_mx4_cache_read(const ddgemm_mx4_cache* cache, const ddgemm_batch* batch, int type, void* k,
+                                int64_t k_token, int64_t k_head, void* v, int64_t v_token, int64_t v_head, void* stream) {
+    CacheRead g{};
+    if (!known_type(type)) return DDGEMM_ERR_INVALID_ARG;
+    ddgemm_status s = check_cache(cache, g.cache);
+    if (s == DDGEMM_OK) s = check_batch(batch, g.batch);
+    if (s != DDGEMM_OK) return s;
+    const int64_t T = batch->tokens, H = cache->heads, D = cache->head_dim;
+    const Heads hk{k, T, H, D, k_token, k_head, type_bytes(type)}, hv{v, T, H, D, v_token, v_head, type_bytes(type)};
+    if (!hk.sound() || !hv.sound()) return DDGEMM_ERR_INVALID_ARG;
+    if (T == 0 || batch->batch == 0) return DDGEMM_OK;
+    if (meet(hk, hv)) {  // the two may be parts of one array: heads side by side
+        const bool same = k_token == v_token && k_head == v_head && T > 1;
+        const int64_t apart = std::abs((intptr_t)k - (intptr_t)v) / type_bytes(type), own = (H - 1) * (H > 1 ? k_head : 0) + D;
+        if (!same || apart < own || apart + own > k_token) return DDGEMM_ERR_INVALID_ARG;
+    }
+    for (const Heads* h : {&hk, &hv})
+        if (overlaps_cache(g.cache, h->p, h->bytes()) || overlaps_batch(g.batch, h->p, h->bytes())) return DDGEMM_ERR_INVALID_ARG;
+    g.type = type;
+    g.k = k, g.kt = k_token, g.kh = k_head;
+    g.v = v, g.vt = v_token, g.vh = v_head;
+    return status_of(launch_cache_read(g, static_cast<cudaStream_t>(stream)));
+}
+
+ddgemm_status dd_mx4_attention(const ddgemm_mx4_cache* cache, const ddgemm_batch* batch, int type, int64_t q_heads,
+                               const void* q, int64_t q_token, int64_t q_head, int64_t window, int64_t sinks,
+                               float scale, void* out, int64_t out_token, int64_t out_head, void* stream) {
+    AttendArgs a{};
+    if (!known_type16(type) || window < 0 || sinks < 0) return DDGEMM_ERR_INVALID_ARG;
+    ddgemm_status s = check_cache(cache, a.c);
+    if (s == DDGEMM_OK) s = check_batch(batch, a.b);
+    if (s != DDGEMM_OK) return s;
+    if (q_heads < 1 || q_heads % cache->heads != 0) return DDGEMM_ERR_INVALID_ARG;
+    if (q_heads > DDGEMM_MAX_HEADS) return DDGEMM_ERR_UNSUPPORTED;
+    const int64_t T = batch->tokens, D = cache->head_dim;
+    const Heads hq{q, T, q_heads, D, q_token, q_head, 2}, ho{out, T, q_heads, D, out_token, out_head, 2};
+    if (!hq.sound() || !ho.sound()) return DDGEMM_ERR_INVALID_ARG;
+    if (T == 0 || batch->batch == 0) return DDGEMM_OK;
+    if (meet(hq, ho) || overlaps_cache(a.c, out, ho.bytes()) || overlaps_batch(a.b, out, ho.bytes())) return DDGEMM_ERR_INVALID_ARG;
+    a.q = q, a.qt = q_token, a.qh = q_head;
+    a.out = out, a.ot = out_token, a.oh = out_head;
+    a.heads = (int)q_heads;
+    a.group = (int)(q_heads / cache->heads);
+    const int64_t far = 1LL << 30;  // beyond every position
+    a.window = (int)std::min(window, far);
+    a.sinks = (int)std::min(sinks, far);
+    a.scale = scale * 1.4426950408889634f;
+    const auto whole = [&](const void* p, int64_t t, int64_t h) { return aligned16(p) && (T <= 1 || t % 8 == 0) && (q_heads <= 1 || h % 8 == 0); };
+    a.vec_q = whole(q, q_token, q_head);
+    a.vec_out = whole(out, out_token, out_head);
+    if (attend_tiles(a.b, a.group, 8) >= (1LL << 31)) return DDGEMM_ERR_UNSUPPORTED;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    a.splits = attend_columns_parts(a);
+    Workspace ws(st);
+    const int64_t rows = T * q_heads;
+    int64_t parts = 0, sums = 0;
+    if (a.splits > 1) {
+        parts = ws.reserve(a.splits * rows * (int64_t)sizeof(float4));
+        sums = ws.reserve(a.splits * rows * a.c.width * 4);
+    }
+    if (!ws.allocate()) return DDGEMM_ERR_ALLOC;
+    if (a.splits > 1) {
+        a.part = ws.at<float4>(parts);
+        a.sums = ws.at<float>(sums);
+    }
+    return status_of(launch_attend_columns(a, type, st));
+}
+
+}  // extern "C"

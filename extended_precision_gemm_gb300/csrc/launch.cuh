@@ -272,6 +272,69 @@ struct FfBackward {
 cudaError_t launch_ff_backward(const FfBackward& f, cudaStream_t st);
 cudaError_t read_and_reset_wait_timeouts_ff(unsigned int* count);
 
+// ---- rotary positions, the paged 4-bit cache (kv_cache.cuh) ----
+
+// y = x with the first 2 half elements of each head turned, T tokens by H heads of D.
+struct Rotary {
+    int type;
+    int64_t T;
+    int H, D;
+    const void* x;
+    int64_t xt, xh;  // strides of tokens and heads
+    void* y;
+    int64_t yt, yh;
+    const void* positions;  // int64 (wide) or int32
+    bool wide;
+    const uint64_t* turns;
+    int half;
+    float m, ml;  // the factor
+    bool interleaved, inverse;
+    int units;  // set by the launch
+};
+cudaError_t launch_rotary(const Rotary& r, cudaStream_t st);
+
+struct CacheView {
+    int fmt, width, dim, heads;
+    int64_t pages;
+    int page_size, page_shift;
+    uint8_t* codes;
+    uint8_t* scales;
+    int8_t* exponents;
+};
+struct BatchView {
+    int64_t tokens;
+    int batch;
+    const int32_t* starts;
+    const int32_t* lengths;
+    const int32_t* table;
+    int table_pages;
+    int64_t ld_table;
+};
+struct CacheAppend {
+    int type;
+    CacheView cache;
+    BatchView batch;
+    const void* k;
+    int64_t kt, kh;
+    const void* v;
+    int64_t vt, vh;
+    const uint64_t* turns;  // null: keys as they are
+    int half;
+    float m, ml;
+    bool interleaved;
+};
+cudaError_t launch_cache_append(const CacheAppend& g, cudaStream_t st);
+struct CacheRead {
+    int type;
+    CacheView cache;
+    BatchView batch;
+    void* k;
+    int64_t kt, kh;
+    void* v;
+    int64_t vt, vh;
+};
+cudaError_t launch_cache_read(const CacheRead& g, cudaStream_t st);
+
 // Stream-ordered allocation from the library's pool (cudaFreeAsync returns it).
 cudaError_t pool_alloc(void** ptr, size_t bytes, cudaStream_t st);
 

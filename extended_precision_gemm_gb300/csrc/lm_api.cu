@@ -3,38 +3,13 @@
 // workspaces, launch sequences.
 #include <algorithm>
 #include <cstdint>
-#include <cstring>
 
-#include "launch.cuh"
+#include "entry.cuh"
 #include "mx4.cuh"
 
 using namespace ddg;
 
 namespace {
-
-constexpr int64_t kAlign = 256;
-
-bool known_format(int f) { return f == DDGEMM_MXFP4 || f == DDGEMM_NVFP4; }
-bool known_type(int t) { return t == DDGEMM_F32 || t == DDGEMM_BF16 || t == DDGEMM_F16; }
-bool known_type16(int t) { return t == DDGEMM_BF16 || t == DDGEMM_F16; }
-bool known_activation(int a) { return a >= DDGEMM_ACT_SILU && a <= DDGEMM_ACT_RELU; }
-int64_t type_bytes(int t) { return t == DDGEMM_F32 ? 4 : 2; }
-bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
-
-// Bytes from the first to the last element of a matrix.
-int64_t span(int64_t rows, int64_t cols, int64_t ld, int64_t elem) {
-    return rows == 0 || cols == 0 ? 0 : ((rows - 1) * ld + cols) * elem;
-}
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-    if (a == nullptr || b == nullptr || na <= 0 || nb <= 0) return false;
-    return (uintptr_t)a < (uintptr_t)b + (uintptr_t)nb && (uintptr_t)b < (uintptr_t)a + (uintptr_t)na;
-}
-
-ddgemm_status status_of(cudaError_t e) {
-    if (e == cudaSuccess) return DDGEMM_OK;
-    (void)cudaGetLastError();
-    return e == cudaErrorMemoryAllocation ? DDGEMM_ERR_ALLOC : DDGEMM_ERR_CUDA;
-}
 
 // Sizes of a 4-bit matrix: within the limits, and its scale tiles and row
 // tiles within the coordinates of tensor copies and grids.
@@ -63,36 +38,6 @@ bool overlaps_mx4(int format, const Mx4Matrix& m, const void* p, int64_t bytes) 
            overlap(m.scales, mx4_scale_bytes(format, m.rows, m.K), p, bytes) ||
            (format == DDGEMM_NVFP4 && overlap(m.exponents, m.rows * 4, p, bytes));
 }
-
-// One block of the library's pool, handed out in 256-byte aligned pieces and
-// returned, in stream order, when the call ends.
-class Workspace {
-public:
-    explicit Workspace(cudaStream_t st) : st_(st) {}
-    ~Workspace() {
-        if (base_ != nullptr) (void)cudaFreeAsync(base_, st_);
-    }
-    Workspace(const Workspace&) = delete;
-    Workspace& operator=(const Workspace&) = delete;
-    int64_t reserve(int64_t bytes) {
-        const int64_t at = total_;
-        total_ = round_up(total_ + bytes, kAlign);
-        return at;
-    }
-    bool allocate() {
-        if (total_ == 0) return true;
-        if (pool_alloc(&base_, (size_t)total_, st_) == cudaSuccess) return true;
-        (void)cudaGetLastError();
-        base_ = nullptr;
-        return false;
-    }
-    template <typename T> T* at(int64_t offset) const { return reinterpret_cast<T*>(static_cast<char*>(base_) + offset); }
-
-private:
-    cudaStream_t st_;
-    void* base_ = nullptr;
-    int64_t total_ = 0;
-};
 
 // A 16-bit operand as the tensor copies need it (16-byte aligned rows): itself,
 // or a copy in the workspace with whole 128-byte rows.  Rows that are not a
@@ -162,30 +107,14 @@ struct SavedLayout {
     }
 };
 
-// Arguments packed as 64-bit words (of any alignment).
-class Words {
-public:
-    explicit Words(const void* p) : p_(static_cast<const char*>(p)) {}
-    template <typename T> T number(int i) const { return (T)word(i); }
-    template <typename T> T* pointer(int i) const { return reinterpret_cast<T*>((uintptr_t)word(i)); }
-    double real(int i) const {
-        double v;
-        memcpy(&v, p_ + 8 * i, 8);
-        return v;
-    }
-
-private:
-    int64_t word(int i) const {
-        int64_t v;
-        memcpy(&v, p_ + 8 * i, 8);
-        return v;
-    }
-    const char* p_;
-};
-// formats, types and flags are small: anything else is no valid one
-template <> int Words::number<int>(int i) const {
-    const int64_t v = word(i);
-    return v >= 0 && v < (1 << 30) ? (int)v : -1;
+// The members of the structures, in turn, from word i on.
+ddgemm_mx4_cache cache_words(const Words& w, int i) {
+    return ddgemm_mx4_cache{w.number<int>(i), w.number<int64_t>(i + 1), w.number<int64_t>(i + 2), w.number<int64_t>(i + 3),
+                            w.number<int64_t>(i + 4), w.pointer<uint8_t>(i + 5), w.pointer<uint8_t>(i + 6), w.pointer<int8_t>(i + 7)};
+}
+ddgemm_batch batch_words(const Words& w, int i) {
+    return ddgemm_batch{w.number<int64_t>(i), w.number<int64_t>(i + 1), w.pointer<const int32_t>(i + 2), w.pointer<const int32_t>(i + 3),
+                        w.pointer<const int32_t>(i + 4), w.number<int64_t>(i + 5), w.number<int64_t>(i + 6)};
 }
 
 }  // namespace
@@ -442,6 +371,36 @@ ddgemm_status dd_call_packed(int call, const void* words) {
                                         w.number<int64_t>(17), w.pointer<void>(18), w.number<int64_t>(19),
                                         w.pointer<void>(20), w.number<int64_t>(21), w.pointer<void>(22),
                                         w.number<int64_t>(23), w.pointer<void>(24));
+        case DDGEMM_CALL_ROTARY: {
+            const ddgemm_rotary r{w.pointer<const uint64_t>(9), w.number<int64_t>(10), w.real(11), w.number<int>(12)};
+            return dd_rotary(w.number<int>(0), w.number<int64_t>(1), w.number<int64_t>(2), w.number<int64_t>(3),
+                             w.pointer<const void>(4), w.number<int64_t>(5), w.number<int64_t>(6),
+                             w.pointer<const void>(7), w.number<int>(8), &r, w.number<int>(13), w.pointer<void>(14),
+                             w.number<int64_t>(15), w.number<int64_t>(16), w.pointer<void>(17));
+        }
+        case DDGEMM_CALL_MX4_CACHE_APPEND: {
+            const ddgemm_mx4_cache c = cache_words(w, 0);
+            const ddgemm_batch b = batch_words(w, 8);
+            const ddgemm_rotary r{w.pointer<const uint64_t>(22), w.number<int64_t>(23), w.real(24), w.number<int>(25)};
+            return dd_mx4_cache_append(&c, &b, w.number<int>(15), w.pointer<const void>(16), w.number<int64_t>(17),
+                                       w.number<int64_t>(18), w.pointer<const void>(19), w.number<int64_t>(20),
+                                       w.number<int64_t>(21), r.turns ? &r : nullptr, w.pointer<void>(26));
+        }
+        case DDGEMM_CALL_MX4_CACHE_READ: {
+            const ddgemm_mx4_cache c = cache_words(w, 0);
+            const ddgemm_batch b = batch_words(w, 8);
+            return dd_mx4_cache_read(&c, &b, w.number<int>(15), w.pointer<void>(16), w.number<int64_t>(17),
+                                     w.number<int64_t>(18), w.pointer<void>(19), w.number<int64_t>(20),
+                                     w.number<int64_t>(21), w.pointer<void>(22));
+        }
+        case DDGEMM_CALL_MX4_ATTENTION: {
+            const ddgemm_mx4_cache c = cache_words(w, 0);
+            const ddgemm_batch b = batch_words(w, 8);
+            return dd_mx4_attention(&c, &b, w.number<int>(15), w.number<int64_t>(16), w.pointer<const void>(17),
+                                    w.number<int64_t>(18), w.number<int64_t>(19), w.number<int64_t>(20),
+                                    w.number<int64_t>(21), (float)w.real(22), w.pointer<void>(23),
+                                    w.number<int64_t>(24), w.number<int64_t>(25), w.pointer<void>(26));
+        }
         default: return DDGEMM_ERR_INVALID_ARG;
     }
 }

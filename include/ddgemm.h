@@ -800,11 +800,119 @@ ddgemm_status dd_mx4_ff_gated(int format, int type, int activation, int64_t T, i
                               const uint8_t* out_scales, const int32_t* out_exponents, void* y, int64_t ldy,
                               void* stream);
 
+/* ------------------------------------------------------------------ */
+/* Rotary positions, a paged 4-bit key/value cache, attention over it   */
+/* ------------------------------------------------------------------ */
+
 /*
- * One of the six entry points above with its arguments, in their order, as an
- * array of 64-bit words (integers and pointers as they are, alpha as the bits
- * of a double): for bindings to which every argument of a foreign call costs
- * (19 of them take 2.0 us through Python's ctypes on the host of a GB300, a
+ * A rotation by positions.  Pair i of a head (pairs of them, 2 * pairs the number
+ * of elements that are turned) turns by p * turns[i] / 2^64 turns at position p:
+ *   y1 = scale (x1 cos - x2 sin),  y2 = scale (x1 sin + x2 cos).
+ * `turns` is on the device, in 64-bit fixed point (round(f / (2 pi) 2^64) for f
+ * radians per position, modulo 2^64), so that angles are exact modulo a turn for
+ * every position, negative ones included.  Pairs are the elements i and pairs + i,
+ * or with interleaved = 1 the elements 2 i and 2 i + 1.
+ */
+typedef struct {
+    const uint64_t* turns;
+    int64_t pairs;
+    double scale;
+    int interleaved;
+} ddgemm_rotary;
+
+/*
+ * y = the rotation of x, heads of `dim` elements of which the first 2 pairs are
+ * turned and the rest are copied; x is tokens x heads x dim with any strides of
+ * tokens and heads (elements; the head dimension is contiguous, heads and tokens
+ * do not overlap), y likewise.  positions: one per token, int64 (wide = 1) or int32.
+ * inverse = 1: the transposed rotation, dx from dy.  y may be x itself (the same
+ * pointer and strides); otherwise they do not overlap.  Sums in 32 bits, cos and
+ * sin correctly rounded but for a few in 10^3, one rounding to `type`.
+ */
+#define DDGEMM_MAX_HEADS 4096
+#define DDGEMM_MAX_TOKENS (1 << 28)
+#define DDGEMM_MAX_ROTARY_DIM 4096
+ddgemm_status dd_rotary(int type, int64_t tokens, int64_t heads, int64_t dim, const void* x, int64_t x_token,
+                        int64_t x_head, const void* positions, int wide, const ddgemm_rotary* rotary, int inverse,
+                        void* y, int64_t y_token, int64_t y_head, void* stream);
+
+/*
+ * A key/value cache in 4-bit microscaled form, in pages of page_size tokens (a
+ * power of two, 16 to 65536).  A row is what one token has of one head, keys or
+ * values: head_dim values (1 to 256) filled up with zeros to a width of 64, 128 or
+ * 256, as codes (width / 2 bytes, the even element in the low nibble), scale bytes
+ * (width / 32 for mxfp4, width / 16 for nvfp4) and one exponent byte (int8): rows,
+ * blocks and roundings are those of dd_mx4_quantize on the row; the exponent is
+ * nvfp4's row exponent, and for mxfp4 the row's largest scale byte (NaN aside)
+ * minus 127, which spares its readers the search.  Rows of the three arrays lie in
+ * the order [pages][2: keys, values][heads][page_size].  16-byte aligned.
+ */
+typedef struct {
+    int format;
+    int64_t pages, page_size, heads, head_dim;
+    uint8_t* codes;
+    uint8_t* scales;
+    int8_t* exponents;
+} ddgemm_mx4_cache;
+
+/*
+ * A batch of sequences, all on the device.  The call's tokens starts[b] up to
+ * starts[b + 1] (int32, batch + 1 of them, not falling) are the last ones of
+ * sequence b, which has lengths[b] tokens in all: token t is at position lengths[b]
+ * - starts[b + 1] + t.  Its tokens lie in the pages page_table[b * table_stride + i]
+ * (i < table_pages), page_size to each.  Tokens of no sequence (before starts[0],
+ * from starts[batch] on) are not touched.  A page number outside the cache, a
+ * position beyond the page table or a negative one stands for tokens that are not
+ * there: they are not written, read as NaN, and make the queries that see them NaN; a
+ * query at a negative position sees none and gets zeros.  starts outside [0, tokens]
+ * or falling give unspecified results (no fault), and pages that two sequences write
+ * hold rows of either or a mix of both.
+ */
+typedef struct {
+    int64_t tokens, batch;
+    const int32_t* starts;
+    const int32_t* lengths;
+    const int32_t* page_table;
+    int64_t table_pages, table_stride;
+} ddgemm_batch;
+
+/* Width of a row, and bytes of its scales. */
+ddgemm_status dd_mx4_cache_layout(int format, int64_t head_dim, int64_t* width, int64_t* scale_bytes);
+
+/*
+ * Quantise the batch's tokens into the cache: k and v are tokens x heads x head_dim
+ * of `type` (any strides of tokens and heads).  rotary, if not NULL, turns the keys
+ * at their tokens' positions on the way, in 32 bits and what these leave, so that
+ * only the code is a rounding.
+ */
+ddgemm_status dd_mx4_cache_append(const ddgemm_mx4_cache* cache, const ddgemm_batch* batch, int type, const void* k,
+                                  int64_t k_token, int64_t k_head, const void* v, int64_t v_token, int64_t v_head,
+                                  const ddgemm_rotary* rotary, void* stream);
+
+/* The values that the batch's tokens have in the cache, rounded to `type` (exact in F32 and BF16 within their ranges). */
+ddgemm_status dd_mx4_cache_read(const ddgemm_mx4_cache* cache, const ddgemm_batch* batch, int type, void* k,
+                                int64_t k_token, int64_t k_head, void* v, int64_t v_token, int64_t v_head, void* stream);
+
+/*
+ * Attention of the batch's tokens over the cache: out = softmax(scale q k^T) v, a
+ * query at position p over the tokens j <= p of its sequence, with a window w > 0
+ * those with j > p - w or j < sinks.  q and out: tokens x q_heads x head_dim of
+ * `type` (DDGEMM_BF16 or DDGEMM_F16), any strides of tokens and heads; q_heads is a
+ * multiple of the cache's heads, and query head h uses head h / (q_heads / heads).
+ * The cache's values enter exactly; scores, softmax and sums are in 32 bits, weights
+ * have 11 significant bits (bfloat16) or 22 (float16).  An infinity or NaN in a token
+ * that a query does not see does not reach it.
+ */
+ddgemm_status dd_mx4_attention(const ddgemm_mx4_cache* cache, const ddgemm_batch* batch, int type, int64_t q_heads,
+                               const void* q, int64_t q_token, int64_t q_head, int64_t window, int64_t sinks,
+                               float scale, void* out, int64_t out_token, int64_t out_head, void* stream);
+
+/*
+ * One of the ten entry points above with its arguments, in their order, as an
+ * array of 64-bit words (integers and pointers as they are, floating-point numbers
+ * as the bits of a double, structures as their members in turn, a NULL rotary as
+ * turns = 0 and the rest): for bindings to which every argument of a foreign call
+ * costs (19 of them take 2.0 us through Python's ctypes on the host of a GB300, a
  * packed array 0.4 us).  An unknown `call` returns DDGEMM_ERR_INVALID_ARG.
  */
 #define DDGEMM_CALL_MX4_QUANTIZE 0
@@ -813,6 +921,10 @@ ddgemm_status dd_mx4_ff_gated(int format, int type, int activation, int64_t T, i
 #define DDGEMM_CALL_MX4_FF_GATED 3
 #define DDGEMM_CALL_FF_GATED 4
 #define DDGEMM_CALL_FF_GATED_BACKWARD 5
+#define DDGEMM_CALL_ROTARY 6
+#define DDGEMM_CALL_MX4_CACHE_APPEND 7
+#define DDGEMM_CALL_MX4_CACHE_READ 8
+#define DDGEMM_CALL_MX4_ATTENTION 9
 ddgemm_status dd_call_packed(int call, const void* words);
 
 #ifdef __cplusplus
