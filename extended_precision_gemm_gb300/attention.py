@@ -28,10 +28,10 @@ from . import low_precision as _lp
 from .low_precision import MX4_FORMATS, _lookup, _type
 
 _lp._PACKED.update({
-    "dd_rotary": (6, struct.Struct("=11qd6q").pack),
-    "dd_mx4_cache_append": (7, struct.Struct("=24qd2q").pack),
-    "dd_mx4_cache_read": (8, struct.Struct("=23q").pack),
-    "dd_mx4_attention": (9, struct.Struct("=22qd4q").pack),
+    "dd_rotary": (16, struct.Struct("=11qd6q").pack),
+    "dd_mx4_cache_append": (17, struct.Struct("=24qd2q").pack),
+    "dd_mx4_cache_read": (18, struct.Struct("=23q").pack),
+    "dd_mx4_attention": (19, struct.Struct("=22qd4q").pack),
 })
 
 

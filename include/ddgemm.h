@@ -921,10 +921,10 @@ ddgemm_status dd_mx4_attention(const ddgemm_mx4_cache* cache, const ddgemm_batch
 #define DDGEMM_CALL_MX4_FF_GATED 3
 #define DDGEMM_CALL_FF_GATED 4
 #define DDGEMM_CALL_FF_GATED_BACKWARD 5
-#define DDGEMM_CALL_ROTARY 6
-#define DDGEMM_CALL_MX4_CACHE_APPEND 7
-#define DDGEMM_CALL_MX4_CACHE_READ 8
-#define DDGEMM_CALL_MX4_ATTENTION 9
+#define DDGEMM_CALL_ROTARY 16
+#define DDGEMM_CALL_MX4_CACHE_APPEND 17
+#define DDGEMM_CALL_MX4_CACHE_READ 18
+#define DDGEMM_CALL_MX4_ATTENTION 19
 ddgemm_status dd_call_packed(int call, const void* words);
 
 #ifdef __cplusplus
