@@ -25,7 +25,7 @@ LIB = BUILD / "libddgemm.so"
 BUILD_CHECKED = PKG / "_build_checked"
 LIB_CHECKED = BUILD_CHECKED / "libddgemm_checked.so"
 SOURCES = ["split.cu", "slice_gemm.cu", "slice_gemm_fused.cu", "slice_gemm_i64.cu", "recombine.cu", "simt.cu", "md.cu", "tc.cu", "tc_md.cu", "mx4.cu", "mx4_gemm.cu", "ff.cu",
-           "lm_api.cu", "rotary.cu", "kv_cache.cu", "attend.cu", "attend_api.cu", "api.cu"]
+           "lm_api.cu", "rotary.cu", "kv_cache.cu", "attend.cu", "attend_tile.cu", "attend_api.cu", "api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + [
     "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-fmad=false",

@@ -523,11 +523,12 @@ ddgemm_status dd_wait_timeouts(unsigned int* count) {
     if (s == DDGEMM_OK) s = from_cuda(read_and_reset_wait_timeouts_qd(&c));
     unsigned int m = 0;
     if (s == DDGEMM_OK) s = from_cuda(read_and_reset_wait_timeouts_tc(&d));
-    unsigned int f = 0, x = 0;
+    unsigned int f = 0, x = 0, t = 0;
     if (s == DDGEMM_OK) s = from_cuda(read_and_reset_wait_timeouts_tc_md(&m));
     if (s == DDGEMM_OK) s = from_cuda(read_and_reset_wait_timeouts_ff(&f));
     if (s == DDGEMM_OK) s = from_cuda(read_and_reset_wait_timeouts_mx4(&x));
-    *count = a + b + c + d + m + f + x;
+    if (s == DDGEMM_OK) s = from_cuda(read_and_reset_wait_timeouts_attend(&t));
+    *count = a + b + c + d + m + f + x + t;
     return s;
 }
 

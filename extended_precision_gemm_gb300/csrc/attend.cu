@@ -550,7 +550,10 @@ cudaError_t launch_attend_columns(const AttendArgs& a, int type, cudaStream_t st
     else
         err = a.c.width == 64 ? columns<__half, 64>(a, st) : a.c.width == 128 ? columns<__half, 128>(a, st) : columns<__half, 256>(a, st);
     if (err != cudaSuccess || a.splits == 1) return err;
-    const float lift = kLift + (a.c.fmt == kMxfp4 ? kMxLift : 0);
+    return launch_attend_join(a, type, kLift + (a.c.fmt == kMxfp4 ? kMxLift : 0), st);
+}
+
+cudaError_t launch_attend_join(const AttendArgs& a, int type, float lift, cudaStream_t st) {
     if (type == DDGEMM_BF16)
         return a.c.width == 64 ? join<__nv_bfloat16, 64>(a, lift, st) : a.c.width == 128 ? join<__nv_bfloat16, 128>(a, lift, st) : join<__nv_bfloat16, 256>(a, lift, st);
     return a.c.width == 64 ? join<__half, 64>(a, lift, st) : a.c.width == 128 ? join<__half, 128>(a, lift, st) : join<__half, 256>(a, lift, st);

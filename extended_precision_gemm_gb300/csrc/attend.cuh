@@ -145,5 +145,11 @@ inline int64_t attend_tiles(const BatchView& b, int group, int columns) { return
 cudaError_t launch_attend_columns(const AttendArgs& a, int type, cudaStream_t st);
 // Into how many parts it cuts a row's tokens.
 int attend_columns_parts(const AttendArgs& a);
+// The same for many queries, by tiles of 128 rows on the tensor cores.
+cudaError_t launch_attend_tile(const AttendArgs& a, int type, cudaStream_t st);
+int attend_tile_parts(const AttendArgs& a);
+// The outputs from the parts of each row; lift: the exponent by which the sums are too
+// large.
+cudaError_t launch_attend_join(const AttendArgs& a, int type, float lift, cudaStream_t st);
 
 }  // namespace ddg

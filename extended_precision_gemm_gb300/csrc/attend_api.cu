@@ -91,6 +91,10 @@ ddgemm_status check_rotary(const ddgemm_rotary* r, int64_t dim) {
     return DDGEMM_OK;
 }
 
+// Rows (query tokens times heads of a group) of a sequence on average up to which
+// the kernel for few queries runs.
+constexpr int64_t kColumnsMost = 16;
+
 }  // namespace
 
 extern "C" {
@@ -205,9 +209,10 @@ ddgemm_status dd_mx4_attention(const ddgemm_mx4_cache* cache, const ddgemm_batch
     const auto whole = [&](const void* p, int64_t t, int64_t h) { return aligned16(p) && (T <= 1 || t % 8 == 0) && (q_heads <= 1 || h % 8 == 0); };
     a.vec_q = whole(q, q_token, q_head);
     a.vec_out = whole(out, out_token, out_head);
-    if (attend_tiles(a.b, a.group, 8) >= (1LL << 31)) return DDGEMM_ERR_UNSUPPORTED;
+    if (attend_tiles(a.b, a.group, 8) * cache->heads >= (1LL << 31)) return DDGEMM_ERR_UNSUPPORTED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    a.splits = attend_columns_parts(a);
+    const bool many = T * a.group > kColumnsMost * batch->batch;
+    a.splits = many ? attend_tile_parts(a) : attend_columns_parts(a);
     Workspace ws(st);
     const int64_t rows = T * q_heads;
     int64_t parts = 0, sums = 0;
@@ -220,7 +225,7 @@ ddgemm_status dd_mx4_attention(const ddgemm_mx4_cache* cache, const ddgemm_batch
         a.part = ws.at<float4>(parts);
         a.sums = ws.at<float>(sums);
     }
-    return status_of(launch_attend_columns(a, type, st));
+    return status_of(many ? launch_attend_tile(a, type, st) : launch_attend_columns(a, type, st));
 }
 
 }  // extern "C"

@@ -1,0 +1,694 @@
+// attend_tile.cu -- attention over the 4-bit cache for many queries, on the tensor
+// cores (tcgen05).
+//
+// A CTA takes tiles of 128 (query token, head of the group) rows of one sequence and
+// key/value head, two at a time (one of width 256), over the cache in tiles of 128
+// tokens, eight groups of 16 wherever their pages lie.  Warps: 0-3 and 4-7 the
+// softmax of a tile of rows each, 8-11 turn codes into 16-bit keys and values, 12
+// issues the MMAs:
+//   S = Q K^T       operands in shared memory, 128-byte swizzle, f32 in tensor memory;
+//   P = 2^(S f - m) a thread for a row, from tensor memory and back into it in 16
+//                   bits, over S;
+//   O += P V        P from tensor memory, V as it lies (tokens by head elements).
+// One tile's softmax overlaps the other's MMAs; O stays in tensor memory and is
+// multiplied only when a row's reference m has to follow (by more than 2^kLag).
+//
+// The conversion is shared by the 256 rows: 256 codes a thread and tile.  Exponents of
+// rows become relative to the tile's largest, for keys a factor of all its scores
+// and for values one of all its weights: codes times scales are exact in 16 bits down
+// to 2^-18 of the tile's largest row, and rounded to 2^-40 of it.
+//
+// Bound: 4 * width operations a score on the tensor pipe, one 2^x a score, and about 5
+// instructions a score and 2 a code of issue.
+#include <algorithm>
+
+#include "attend.cuh"
+#include "umma.cuh"
+
+namespace ddg {
+namespace {
+
+constexpr unsigned long long kWaitNs = 2000000000ULL;  // bounded waits: 2 s
+constexpr float kLag = 5.0f;   // references follow when they are exceeded by more than 2^5
+constexpr int kShift = 3;      // ... and the values' exponent by more than 2^3 either way
+constexpr float kLift = 7.0f;  // weights up to 2^(5 + 3 + 7), below the largest float16
+constexpr int kFar = 64;       // values' exponents are at most so far below the largest seen
+constexpr int kThreads = 13 * 32;
+constexpr int kNoToken = -128;  // in the place of an exponent
+
+__device__ unsigned int g_attend_timeouts = 0;
+
+// By how much codes times scales are lifted: the largest becomes 2^15.4 (E4M3) or 2^15.6.
+template <int FMT> __host__ __device__ constexpr int lift_of() { return FMT == kMxfp4 ? 13 : 4; }
+
+template <int WIDTH>
+struct Shape {
+    static constexpr int NQ = WIDTH == 256 ? 1 : 2;       // tiles of rows
+    static constexpr int STAGES = WIDTH == 256 ? 1 : 2;   // of keys, and of values
+    static constexpr int BLOCK_BYTES = 128 * 128;         // 128 rows of 64 elements
+    static constexpr int TILE_BYTES = WIDTH / 64 * BLOCK_BYTES;
+    static constexpr int K0 = NQ * TILE_BYTES, V0 = K0 + STAGES * TILE_BYTES;
+    static constexpr int SMEM = V0 + STAGES * TILE_BYTES + 1024;
+    static constexpr int CHUNKS = WIDTH / 32;             // pieces of 32 codes of a token, and a thread's pieces of a tile
+    static constexpr uint32_t S_COL = 0, O_COL = 256;
+};
+
+// What the softmax has to know of a tile.
+struct TileInfo {
+    float key_factor;
+    int value_exponent;
+    uint32_t bad;  // groups whose page is not there
+    uint32_t any_nan;
+    uint32_t nan[128];  // blocks of a token's values that are NaN
+};
+
+// Keys or values of a tile as a thread reads them.
+template <int CHUNKS>
+struct Raw {
+    uint4 codes[CHUNKS];
+    uint16_t scales[CHUNKS];
+    int exponent;  // of token `thread`
+};
+
+__device__ __forceinline__ uint32_t half2_of(float a, float b) {  // a in the low half
+    uint32_t w;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+    return w;
+}
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// Eight codes as four pairs of halves.
+__device__ __forceinline__ uint4 halves_of(uint32_t w) {
+    uint4 h;
+    asm("{\n"
+        " .reg .b8 t0, t1, t2, t3;\n"
+        " mov.b32 {t0, t1, t2, t3}, %4;\n"
+        " cvt.rn.f16x2.e2m1x2 %0, t0;\n"
+        " cvt.rn.f16x2.e2m1x2 %1, t1;\n"
+        " cvt.rn.f16x2.e2m1x2 %2, t2;\n"
+        " cvt.rn.f16x2.e2m1x2 %3, t3;\n"
+        "}\n"
+        : "=r"(h.x), "=r"(h.y), "=r"(h.z), "=r"(h.w)
+        : "r"(w));
+    return h;
+}
+__device__ __forceinline__ void store_shared(uint32_t at, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// D = A B^T (+ D) with A in tensor memory.
+__device__ __forceinline__ void mma_from_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void store_tmem16(uint32_t at, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void wait_tmem_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+struct Barriers {
+    uint64_t q, k_full[2], k_empty[2], v_full[2], v_empty[2], s[2], p[2], o[2], done;
+};
+
+template <typename T, int WIDTH, int FMT>
+__global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendArgs a) {
+    using S = Shape<WIDTH>;
+    constexpr bool REST = std::is_same_v<T, __half>;  // what the rounding of weights leaves enters the sum too
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    __shared__ __align__(8) Barriers bars;
+    __shared__ uint32_t tmem_slot;
+    __shared__ TileInfo info[S::STAGES];
+    __shared__ __align__(16) int page_ring[4][8];
+    __shared__ int8_t exponents[2][128];
+    __shared__ int largest[2][4];
+
+    pdl_wait();
+    pdl_launch_dependents();
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
+    const int head = (int)(blockIdx.x % a.c.heads);
+    // the last rows of a sequence see the most tokens: they go first
+    const Item item = item_of(a.b, (int64_t)((gridDim.x - 1 - blockIdx.x) / a.c.heads), a.group, 128 * S::NQ);
+    if (item.sequence < 0) return;
+    const int before = item.length - item.tokens;
+    const auto position = [&](int column) { return before + (item.column + column) / a.group; };
+    const int p0 = position(0), p1 = position(item.columns - 1);
+    const Groups groups = groups_of(a.c, a.b, p0, p1, a.window, a.sinks);
+    const int tiles = (groups.count + 7) / 8;
+    const int t0 = (int)((int64_t)tiles * blockIdx.z / a.splits), t1 = (int)((int64_t)tiles * (blockIdx.z + 1) / a.splits);
+    // tiles that the rows of tile x see, counted from t0
+    int need[2] = {0, 0};
+#pragma unroll
+    for (int x = 0; x < S::NQ; ++x) {
+        if (item.columns > x * 128) {
+            const int last = position(min(item.columns, (x + 1) * 128) - 1);
+            const int count = last < 0 ? 0 : min(groups.count, groups.sink + max(0, last / 16 + 1 - groups.low));
+            need[x] = max(0, min((count + 7) / 8, t1) - t0);
+        }
+    }
+    const int n = max(need[0], need[1]);
+
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const uint32_t q_full = smem_addr(&bars.q), done = smem_addr(&bars.done);
+    const auto bar = [&](uint64_t* b, int i) { return smem_addr(b) + 8u * (uint32_t)i; };
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 4 * S::NQ);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(bars.k_full, i), 4);
+            mbar_init(bar(bars.v_full, i), 4);
+            mbar_init(bar(bars.k_empty, i), 1);
+            mbar_init(bar(bars.v_empty, i), 1);
+            mbar_init(bar(bars.s, i), 1);
+            mbar_init(bar(bars.p, i), 4);
+            mbar_init(bar(bars.o, i), 1);
+        }
+        mbar_init(done, 1);
+        fence_barrier_init();
+    }
+    if (warp == 12) {
+        tc5::tmem_alloc(smem_addr(&tmem_slot), 512);
+        tc5::tmem_relinquish();
+    }
+    tc5::fence_before_sync();
+    __syncthreads();
+    tc5::fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp < 4 * S::NQ) {
+        // ---- softmax: a thread for a row ----
+        const int x = warp / 4, quarter = warp % 4, row = quarter * 32 + lane;
+        const int column = x * 128 + row;
+        const bool have = column < item.columns;
+        const int p = have ? position(column) : -1;
+        const int first = position(x * 128), last = position(min(item.columns, (x + 1) * 128) - 1);
+        const int query = item.column + column;
+        const int64_t token = item.first_token + query / a.group, h = head * a.group + query % a.group;
+        float factor = fabsf(a.scale);
+        {   // the row into shared memory, 64 elements (128 bytes, swizzled) at a time
+            const T* src = static_cast<const T*>(a.q) + (have ? token * a.qt + h * a.qh : 0);
+            const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
+            float2 up = make_float2(sign, 1.0f);
+            if (!REST) {  // bfloat16: the row's largest to [2^11, 2^12)
+                uint32_t most = 0;
+                if (have) {
+                    if (a.vec_q) {
+                        for (int d = 0; d + 8 <= a.c.dim; d += 8) {
+                            const uint4 raw = *reinterpret_cast<const uint4*>(src + d);
+                            const T* t = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const uint32_t bits = __float_as_uint(to_float<T>(t[j])) & 0x7fffffffu;
+                                most = max(most, bits < kInfBits ? bits : 0u);
+                            }
+                        }
+                    }
+                    for (int d = a.vec_q ? a.c.dim / 8 * 8 : 0; d < a.c.dim; ++d) {
+                        const uint32_t bits = __float_as_uint(to_float<T>(src[d])) & 0x7fffffffu;
+                        most = max(most, bits < kInfBits ? bits : 0u);
+                    }
+                }
+                const int e = max((int)(most >> 23) - 127 - 11, -126);
+                const float2 down = exp2_factors(e);
+                up = exp2_factors(-e);
+                up.x *= sign;
+                factor = factor * down.x * down.y;
+            }
+            const uint32_t q = base + x * S::TILE_BYTES + row * 128;
+#pragma unroll 4
+            for (int d = 0; d < WIDTH; d += 8) {
+                float v[8];
+                if (have && a.vec_q && d + 8 <= a.c.dim) {
+                    const uint4 raw = *reinterpret_cast<const uint4*>(src + d);
+                    const T* t = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = to_float<T>(t[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = have && d + j < a.c.dim ? to_float<T>(src[d + j]) : 0.0f;
+                }
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = half2_of(v[2 * j] * up.x * up.y, v[2 * j + 1] * up.x * up.y);
+                store_shared(q + d / 64 * S::BLOCK_BYTES + (uint32_t)((d / 8 % 8 ^ row % 8) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+        }
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const uint32_t o_at = tmem + S::O_COL + x * WIDTH + lanes;
+        float m = minus_infinity(), l = 0.0f;
+        int reference_exponent = 0;
+        uint32_t poison = 0;
+        bool ok = true;
+        const int mine = need[x];
+        for (int j = 0; j < mine; ++j) {
+            const int stage = j % S::STAGES;
+            const int buffer = S::NQ == 2 ? x : j & 1;
+            const uint32_t s_at = tmem + S::S_COL + buffer * 128 + lanes;
+            ok = warp_wait(bar(bars.v_full, stage), (j / S::STAGES) & 1, kWaitNs) &&
+                 warp_wait(bar(bars.s, buffer), (S::NQ == 2 ? j : j >> 1) & 1, kWaitNs);
+            if (!ok) break;
+            tc5::fence_after_sync();
+            const TileInfo& tile = info[stage];
+            const float f = factor * tile.key_factor;
+            const int g0 = (t0 + j) * 8;
+            const int begin = group_token(groups, g0), end = group_token(groups, g0 + 7) + 15;
+            const bool whole = tile.bad == 0 && g0 + 8 <= groups.count && end <= first && (a.window == 0 || begin > last - a.window);
+            const auto visible = [&](int t) {
+                const int g = g0 + t / 16;
+                return g < groups.count && sees(p, group_token(groups, g) + t % 16, a.window, a.sinks);
+            };
+            // the tile's largest score
+            float top = minus_infinity();
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) {
+                uint32_t s[32];
+                tc5::ld32(s_at + c, s);
+                if (whole) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(s[i]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (visible(c + i)) top = fmaxf(top, __uint_as_float(s[i]));
+                    __syncwarp();
+                }
+            }
+            top = top == minus_infinity() ? top : top * f;
+            int shift = tile.value_exponent - reference_exponent;
+            float turn = 1.0f;
+            if (j == 0) {
+                reference_exponent = tile.value_exponent;
+                shift = 0;
+            } else if (shift > kShift || shift < -kShift) {
+                const float2 t = exp2_factors(-shift);
+                turn = t.x * t.y;
+                reference_exponent = tile.value_exponent;
+                shift = 0;
+            }
+            if (top > m + kLag || (m == minus_infinity() && top > m)) {
+                const float by = power2(m - top);
+                m = top;
+                l *= by;
+                turn *= by;
+            }
+            if (j > 0 && __any_sync(~0u, turn != 1.0f)) {
+                ok = warp_wait(bar(bars.o, S::NQ == 2 ? x : 0), (j - 1) & 1, kWaitNs);
+                if (!ok) break;
+                tc5::fence_after_sync();
+#pragma unroll 1
+                for (int c = 0; c < WIDTH; c += 32) {
+                    uint32_t v[32], half[16];
+                    tc5::ld32(o_at + c, v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) half[i] = __float_as_uint(__uint_as_float(v[i]) * turn);
+                    store_tmem16(o_at + c, half);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) half[i] = __float_as_uint(__uint_as_float(v[16 + i]) * turn);
+                    store_tmem16(o_at + c + 16, half);
+                }
+                wait_tmem_stores();
+            }
+            const float offset = (float)shift + kLift - reference(m);
+            float sum = 0.0f;
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) {
+                uint32_t s[32], w[16], rest[16];
+                tc5::ld32(s_at + c, s);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    float u[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        u[k] = power2(fmaf(__uint_as_float(s[i + k]), f, offset));
+                        if (!whole) {
+                            if (tile.bad >> ((c + i + k) / 16) & 1) u[k] = not_a_number();
+                            if (!visible(c + i + k)) u[k] = 0.0f;
+                        }
+                        sum += u[k];
+                    }
+                    w[i / 2] = half2_of(u[0], u[1]);
+                    if (REST) {
+                        const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&w[i / 2]));
+                        rest[i / 2] = half2_of(u[0] - back.x, u[1] - back.y);
+                    }
+                }
+                __syncwarp();
+                store_tmem16(s_at + c, w);
+                if (REST) store_tmem16(s_at + c + 16, rest);
+            }
+            l = fmaf(sum, exp2_int(-shift - (int)kLift), l);
+            if (tile.any_nan != 0) {
+                for (int t = 0; t < 128; ++t)
+                    if (tile.nan[t] != 0 && visible(t)) poison |= tile.nan[t];
+                __syncwarp();
+            }
+            wait_tmem_stores();
+            tc5::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(bars.p, buffer));
+        }
+        if (ok && mine > 0) {
+            ok = warp_wait(bar(bars.o, S::NQ == 2 ? x : 0), (mine - 1) & 1, kWaitNs);
+            tc5::fence_after_sync();
+        }
+        if (!ok && lane == 0) atomicAdd(&g_attend_timeouts, 1u);
+        const float M = m + (float)reference_exponent;
+        const int64_t out_row = token * a.heads + h;
+        const int64_t part = (int64_t)blockIdx.z * (a.b.tokens * a.heads) + out_row;
+        const Finish z = finish_of(m, M, l, kLift + lift_of<FMT>(), p >= 0);
+        if (a.splits > 1 && have) a.part[part] = make_float4(m, M, l, p >= 0 ? 1.0f : 0.0f);
+#pragma unroll 1
+        for (int c = 0; c < WIDTH; c += 32) {
+            uint32_t v[32];
+            if (mine > 0 && ok) {
+                tc5::ld32(o_at + c, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0;
+            }
+            if (have) {
+                if (poison != 0) {
+                    constexpr int BLOCK = mx4_block(FMT);
+    #pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (poison >> ((c + i) / BLOCK) & 1) v[i] = 0x7fc00000u;
+                }
+                if (a.splits > 1) {
+                    float4* to = reinterpret_cast<float4*>(a.sums + part * WIDTH + c);
+    #pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        to[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+                } else {
+                    T* out = static_cast<T*>(a.out) + token * a.ot + h * a.oh;
+    #pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        float y[8];
+    #pragma unroll
+                        for (int k = 0; k < 8; ++k) y[k] = p < 0 ? 0.0f : __uint_as_float(v[i + k]) * z.x * z.x * z.inverse;
+                        if (a.vec_out && c + i + 8 <= a.c.dim) {
+                            store8(out + c + i, y);
+                        } else {
+    #pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                if (c + i + k < a.c.dim) out[c + i + k] = from_float<T>(y[k]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        tc5::fence_before_sync();
+    } else if (warp >= 8 && warp < 12) {
+        // ---- codes to 16 bits ----
+        constexpr int CHUNKS = S::CHUNKS, BLOCK = mx4_block(FMT), BLOCKS = WIDTH / BLOCK;
+        const int thread = threadIdx.x - 8 * 32, w = warp - 8;
+        const int units = 2 * n;  // K0, K1, V0, K2, V1, ..., V(n - 1)
+        const auto is_value = [&](int u) { return u == units - 1 || (u > 0 && u % 2 == 0); };
+        const auto tile_of = [&](int u) { return u == units - 1 ? n - 1 : u == 0 ? 0 : u % 2 ? (u + 1) / 2 : u / 2 - 1; };
+        const auto page_for = [&](int j) {  // of group thread % 8 of tile j
+            const int g = (t0 + j) * 8 + thread;
+            return j < n && g < groups.count ? page_of(a.c, a.b, item.sequence, group_token(groups, g)) : -1;
+        };
+        int held = -1;
+        if (thread < 8) {
+            page_ring[0][thread] = page_for(0);
+            page_ring[1][thread] = page_for(1);
+            held = page_for(2);
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        Raw<CHUNKS> even, odd;  // units u and u + 1 in turn: one is loaded while the other is converted
+        const auto load = [&](int u, Raw<CHUNKS>& raw) {
+            const int j = tile_of(u), kv = is_value(u) ? 1 : 0, g0 = (t0 + j) * 8;
+            const int* pages = page_ring[j & 3];
+#pragma unroll
+            for (int i = 0; i < CHUNKS; ++i) {
+                const int at = i * 128 + thread, t = at / CHUNKS, part = at % CHUNKS;
+                const int page = pages[t / 16];
+                raw.codes[i] = make_uint4(0, 0, 0, 0);
+                raw.scales[i] = 0;
+                if (page >= 0) {
+                    const int64_t r = cache_row(a.c, page, kv, head, group_token(groups, g0 + t / 16) & (a.c.page_size - 1)) + t % 16;
+                    raw.codes[i] = __ldg(reinterpret_cast<const uint4*>(a.c.codes + r * (WIDTH / 2)) + part);
+                    raw.scales[i] = FMT == kMxfp4 ? (uint16_t)__ldg(a.c.scales + r * BLOCKS + part)
+                                                  : __ldg(reinterpret_cast<const uint16_t*>(a.c.scales + r * BLOCKS) + part);
+                }
+            }
+            const int page = pages[thread / 16], token = group_token(groups, g0 + thread / 16) + thread % 16;
+            raw.exponent = kNoToken;
+            if (page >= 0 && token < item.length)
+                raw.exponent = __ldg(a.c.exponents + cache_row(a.c, page, kv, head, token & (a.c.page_size - 1)));
+        };
+        bool ok = true;
+        int most_seen = kNoToken, key_exponent[2] = {0, 0};
+        const auto convert = [&](int u, Raw<CHUNKS>& raw, Raw<CHUNKS>& following) {
+            const int j = tile_of(u), stage = j % S::STAGES, parity = u & 1;
+            const bool value = is_value(u);
+            // a warp that gave up once goes on without waiting: the others meet it at the barrier below
+            ok = ok && warp_wait(bar(value ? bars.v_empty : bars.k_empty, stage), ((j / S::STAGES) & 1) ^ 1, kWaitNs);
+            // pages of two tiles on, for the loads behind the next barrier
+            if (!value && thread < 8) {
+                page_ring[(j + 2) & 3][thread] = held;
+                held = page_for(j + 3);
+            }
+            exponents[parity][thread] = (int8_t)raw.exponent;
+            const int top = __reduce_max_sync(~0u, raw.exponent);
+            if (lane == 0) largest[parity][w] = top;
+            if (value) {
+                info[stage].nan[thread] = 0;
+                if (thread == 0) info[stage].any_nan = 0;
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (u + 1 < units) load(u + 1, following);
+            int e = max(max(largest[parity][0], largest[parity][1]), max(largest[parity][2], largest[parity][3]));
+            if (value) {
+                most_seen = max(most_seen, e);
+                e = max(e, most_seen - kFar);
+            }
+            e = max(e, -127);
+            if (value && thread == 0) {
+                info[stage].key_factor = mxfp4_scale((uint32_t)(key_exponent[j & 1] + 127)) * exp2_int(-lift_of<FMT>());
+                info[stage].value_exponent = e;
+                uint32_t bad = 0;
+                for (int g = 0; g < 8; ++g)
+                    if ((t0 + j) * 8 + g < groups.count && page_ring[j & 3][g] < 0) bad |= 1u << g;
+                info[stage].bad = bad;
+            }
+            if (!value) key_exponent[j & 1] = e;
+            const uint32_t to = base + (value ? S::V0 : S::K0) + stage * S::TILE_BYTES;
+#pragma unroll
+            for (int i = 0; i < CHUNKS; ++i) {
+                const int at = i * 128 + thread, t = at / CHUNKS, part = at % CHUNKS;
+                const int et = exponents[parity][t];
+                uint32_t s[2];
+                if (FMT == kMxfp4) {
+                    const float power = exp2_int(min(max((int)raw.scales[i] - 127 - e + lift_of<kMxfp4>(), -126), 15));
+                    s[0] = s[1] = raw.scales[i] == 255u ? 0x7fff7fffu : half2_of(power, power);
+                } else {
+                    const float lifted = exp2_int(min(max(et - e + lift_of<kNvfp4>(), -126), 15));
+                    const uint32_t power = half2_of(lifted, lifted);
+                    uint32_t h2;
+                    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(raw.scales[i]));
+                    h2 = mul_half2(h2, power);
+                    s[0] = __byte_perm(h2, h2, 0x1010);
+                    s[1] = __byte_perm(h2, h2, 0x3232);
+                }
+                if (et == kNoToken) s[0] = s[1] = 0;
+                if (value) {
+                    constexpr int PER = 32 / BLOCK;
+#pragma unroll
+                    for (int b = 0; b < PER; ++b) {
+                        if ((s[b] & 0x7fffu) > 0x7c00u) {
+                            s[b] = 0;
+                            if (PER == 1) s[1] = 0;
+                            atomicOr(&info[stage].nan[t], 1u << (part * PER + b));
+                            info[stage].any_nan = 1;
+                        }
+                    }
+                }
+                const uint32_t row = to + part / 2 * S::BLOCK_BYTES + t * 128;
+                const uint32_t words[4] = {raw.codes[i].x, raw.codes[i].y, raw.codes[i].z, raw.codes[i].w};
+#pragma unroll
+                for (int k0 = 0; k0 < 4; ++k0) {
+                    uint4 v = halves_of(words[k0]);
+                    const uint32_t sc = s[k0 / 2];
+                    v.x = mul_half2(v.x, sc);
+                    v.y = mul_half2(v.y, sc);
+                    v.z = mul_half2(v.z, sc);
+                    v.w = mul_half2(v.w, sc);
+                    store_shared(row + (uint32_t)((part % 2 * 4 + k0 ^ t % 8) << 4), v);
+                }
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(value ? bars.v_full : bars.k_full, stage));
+        };
+        if (n > 0) load(0, even);
+        for (int u = 0; u < units; u += 2) {  // an even number of them
+            convert(u, even, odd);
+            convert(u + 1, odd, even);
+        }
+        if (!ok && lane == 0) atomicAdd(&g_attend_timeouts, 1u);
+    } else if (warp == 12 && n > 0) {
+        // ---- MMAs ----
+        constexpr uint32_t S_DESC = tc5::idesc_f16(false, false, false, 128, 128);
+        constexpr uint32_t O_DESC = tc5::idesc_f16(false, false, true, 128, WIDTH);
+        const auto score = [&](int x, int j, int buffer) {
+            if (elect_one()) {
+                const uint64_t qd = tc5::desc_kmajor_sw128(base + x * S::TILE_BYTES);
+                const uint64_t kd = tc5::desc_kmajor_sw128(base + S::K0 + j % S::STAGES * S::TILE_BYTES);
+#pragma unroll
+                for (int k = 0; k < WIDTH / 16; ++k) {
+                    const uint64_t at = (uint64_t)(k / 4 * (S::BLOCK_BYTES / 16) + k % 4 * 2);
+                    tc5::mma_f16_single(tmem + S::S_COL + buffer * 128, qd + at, kd + at, S_DESC, k > 0 ? 1u : 0u);
+                }
+                tc5::commit(bar(bars.s, buffer));
+            }
+            __syncwarp();
+        };
+        const auto weigh = [&](int x, int j, int buffer) {
+            if (elect_one()) {
+                const uint64_t vd = tc5::desc_mnmajor_sw128(base + S::V0 + j % S::STAGES * S::TILE_BYTES, S::BLOCK_BYTES);
+                const uint32_t p_at = tmem + S::S_COL + buffer * 128, o_at = tmem + S::O_COL + x * WIDTH;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t from = p_at + k / 2 * 32 + k % 2 * 8;
+                    mma_from_tmem(o_at, from, vd + k * (2048 / 16), O_DESC, (j | k) != 0 ? 1u : 0u);
+                    if (REST) mma_from_tmem(o_at, from + 16, vd + k * (2048 / 16), O_DESC, 1u);
+                }
+                tc5::commit(bar(bars.o, x));
+            }
+            __syncwarp();
+        };
+        const auto free_stage = [&](uint64_t* b, int j) {
+            if (elect_one()) tc5::commit(bar(b, j % S::STAGES));
+            __syncwarp();
+        };
+        const auto keys = [&](int j) { return warp_wait(bar(bars.k_full, j % S::STAGES), (j / S::STAGES) & 1, kWaitNs); };
+        bool ok = warp_wait(q_full, 0, kWaitNs);
+        if (S::NQ == 2) {
+            if (ok && (ok = keys(0))) {
+                tc5::fence_after_sync();
+                for (int x = 0; x < 2; ++x)
+                    if (need[x] > 0) score(x, 0, x);
+                free_stage(bars.k_empty, 0);
+            }
+            for (int j = 0; j < n && ok; ++j) {
+                ok = warp_wait(bar(bars.v_full, j % S::STAGES), (j / S::STAGES) & 1, kWaitNs);
+                for (int x = 0; x < 2 && ok; ++x) {
+                    if (j < need[x]) {
+                        ok = warp_wait(bar(bars.p, x), j & 1, kWaitNs);
+                        if (!ok) break;
+                        tc5::fence_after_sync();
+                        weigh(x, j, x);
+                    }
+                    if (x == 1) free_stage(bars.v_empty, j);
+                    if (j + 1 < n) {
+                        ok = keys(j + 1);
+                        if (!ok) break;
+                        tc5::fence_after_sync();
+                        if (j + 1 < need[x]) score(x, j + 1, x);
+                        if (x == 1) free_stage(bars.k_empty, j + 1);
+                    }
+                }
+            }
+        } else {
+            for (int j = 0; j < 2 && j < n && ok; ++j) {
+                ok = keys(j);
+                if (!ok) break;
+                tc5::fence_after_sync();
+                score(0, j, j);
+                free_stage(bars.k_empty, j);
+            }
+            for (int j = 0; j < n && ok; ++j) {
+                ok = warp_wait(bar(bars.v_full, j % S::STAGES), (j / S::STAGES) & 1, kWaitNs) && warp_wait(bar(bars.p, j & 1), (j >> 1) & 1, kWaitNs);
+                if (!ok) break;
+                tc5::fence_after_sync();
+                weigh(0, j, j & 1);
+                free_stage(bars.v_empty, j);
+                if (j + 2 < n) {
+                    ok = keys(j + 2);
+                    if (!ok) break;
+                    tc5::fence_after_sync();
+                    score(0, j + 2, j & 1);
+                    free_stage(bars.k_empty, j + 2);
+                }
+            }
+        }
+        // every MMA has finished before shared or tensor memory is given up
+        if (elect_one()) tc5::commit(done);
+        __syncwarp();
+        ok = warp_wait(done, 0, kWaitNs) && ok;
+        if (!ok && lane == 0) atomicAdd(&g_attend_timeouts, 1u);
+    }
+    tc5::fence_before_sync();
+    __syncthreads();
+    tc5::fence_after_sync();
+    if (warp == 12) {
+        __syncwarp();
+        tc5::tmem_dealloc(tmem, 512);
+    }
+}
+
+template <typename T, int WIDTH, int FMT>
+cudaError_t launch(const AttendArgs& a, cudaStream_t st) {
+    using S = Shape<WIDTH>;
+    auto* kernel = attend_tile_kernel<T, WIDTH, FMT>;
+    static std::atomic<bool> asked[64];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!asked[dev].load(std::memory_order_relaxed)) {
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        if (err != cudaSuccess) return err;
+        asked[dev].store(true, std::memory_order_relaxed);
+    }
+    const dim3 grid((unsigned)(a.c.heads * attend_tiles(a.b, a.group, 128 * S::NQ)), 1, (unsigned)a.splits);
+    err = launch_pdl(kernel, grid, dim3(kThreads), S::SMEM, st, a);
+    if (err != cudaSuccess || a.splits == 1) return err;
+    return launch_attend_join(a, std::is_same_v<T, __half> ? DDGEMM_F16 : DDGEMM_BF16, kLift + lift_of<FMT>(), st);
+}
+template <typename T>
+cudaError_t by_width(const AttendArgs& a, cudaStream_t st) {
+    if (a.c.fmt == kMxfp4) return a.c.width == 64 ? launch<T, 64, kMxfp4>(a, st) : a.c.width == 128 ? launch<T, 128, kMxfp4>(a, st) : launch<T, 256, kMxfp4>(a, st);
+    return a.c.width == 64 ? launch<T, 64, kNvfp4>(a, st) : a.c.width == 128 ? launch<T, 128, kNvfp4>(a, st) : launch<T, 256, kNvfp4>(a, st);
+}
+
+}  // namespace
+
+int attend_tile_parts(const AttendArgs& a) {
+    const int rows = a.c.width == 256 ? 128 : 256;
+    const int64_t tiles = std::max(a.b.tokens * a.group / rows, (int64_t)a.b.batch) * a.c.heads;
+    const int64_t longest = a.window > 0 ? (int64_t)a.window + a.sinks : (int64_t)a.b.table_pages * a.c.page_size;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({device_sms() / std::max<int64_t>(1, tiles), (longest + 1023) / 1024, 64}));
+}
+
+cudaError_t launch_attend_tile(const AttendArgs& a, int type, cudaStream_t st) {
+    return type == DDGEMM_BF16 ? by_width<__nv_bfloat16>(a, st) : by_width<__half>(a, st);
+}
+
+cudaError_t read_and_reset_wait_timeouts_attend(unsigned int* count) {
+    cudaError_t err = cudaDeviceSynchronize();
+    if (err != cudaSuccess) return err;
+    err = cudaMemcpyFromSymbol(count, g_attend_timeouts, sizeof(unsigned int));
+    if (err != cudaSuccess) return err;
+    const unsigned int zero = 0;
+    return cudaMemcpyToSymbol(g_attend_timeouts, &zero, sizeof(unsigned int));
+}
+
+}  // namespace ddg

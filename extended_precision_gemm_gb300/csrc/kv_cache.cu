@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Append<T> a, int
             const int64_t at = cache_row(a.c, page, kv, head, p.position & (a.c.page_size - 1));
             *reinterpret_cast<uint32_t*>(a.c.codes + at * (WIDTH / 2) + lane * 4) = e2m1_pack8(y);
             if (lane % SHARE == 0) a.c.scales[at * BLOCKS + lane / SHARE] = (uint8_t)byte;
-            if (lane == 0) a.c.exponents[at] = (int8_t)e;
+            if (lane == 0) a.c.exponents[at] = (int8_t)(FMT == kNvfp4 && finite == 0u ? -127 : e);
         }
     }
 }

@@ -334,6 +334,7 @@ struct CacheRead {
     int64_t vt, vh;
 };
 cudaError_t launch_cache_read(const CacheRead& g, cudaStream_t st);
+cudaError_t read_and_reset_wait_timeouts_attend(unsigned int* count);
 
 // Stream-ordered allocation from the library's pool (cudaFreeAsync returns it).
 cudaError_t pool_alloc(void** ptr, size_t bytes, cudaStream_t st);

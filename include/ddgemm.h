@@ -843,8 +843,9 @@ ddgemm_status dd_rotary(int type, int64_t tokens, int64_t heads, int64_t dim, co
  * 256, as codes (width / 2 bytes, the even element in the low nibble), scale bytes
  * (width / 32 for mxfp4, width / 16 for nvfp4) and one exponent byte (int8): rows,
  * blocks and roundings are those of dd_mx4_quantize on the row; the exponent is
- * nvfp4's row exponent, and for mxfp4 the row's largest scale byte (NaN aside)
- * minus 127, which spares its readers the search.  Rows of the three arrays lie in
+ * nvfp4's row exponent (-127 for a row without a finite value other than 0), and for
+ * mxfp4 the row's largest scale byte (NaN aside) minus 127, which spares its readers
+ * the search.  Rows of the three arrays lie in
  * the order [pages][2: keys, values][heads][page_size].  16-byte aligned.
  */
 typedef struct {

@@ -39,6 +39,8 @@ def rows(x, fmt):
     code = code.reshape(n, -1)
     if fmt == "mxfp4":
         exps = np.where(byte == 255, 0, byte).max(axis=1).astype(np.int32) - 127
+    else:
+        exps = np.where(np.where(np.isfinite(x), x, 0).any(axis=1), exps, -127)
     return (code[:, 0::2] | code[:, 1::2] << 4).astype(np.uint8), byte, exps.astype(np.int8)
 
 

@@ -277,3 +277,8 @@ def test_a_prompt_and_then_token_by_token(fmt, dim, group):
     most = np.abs(k64).reshape(*k64.shape[:2], -1, 16 if fmt == "nvfp4" else 32).max(-1).repeat(16 if fmt == "nvfp4" else 32, -1)
     assert (np.abs(kk.cpu().numpy() - k64) <= most * (0.26 if fmt == "mxfp4" else 0.2)).all()
     assert np.array_equal(vv.cpu().numpy(), ddg.mx4_dequantize(ddg.mx4_quantize(torch.cat([torch.cat(x) for x in vals]).reshape(-1, dim), fmt), torch.float32).cpu().numpy().reshape(vv.shape))
+
+
+def test_no_wait_gave_up():
+    """After the calls above (the count is of the process)."""
+    assert ddg.wait_timeouts() == 0
