@@ -95,8 +95,18 @@ __device__ __forceinline__ uint4 halves_of(uint32_t w) {
         : "r"(w));
     return h;
 }
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 __device__ __forceinline__ void store_shared(uint32_t at, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void swap(uint32_t& a, uint32_t& b) {
+    const uint32_t t = a;
+    a = b;
+    b = t;
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -264,13 +274,29 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             if (!ok) break;
             tc5::fence_after_sync();
             const TileInfo& tile = info[stage];
-            const float f = factor * tile.key_factor;
+            const float f = fmaxf(factor * tile.key_factor, 0x1p-120f);  // no 0: minus infinity stays what it is
             const int g0 = (t0 + j) * 8;
             const int begin = group_token(groups, g0), end = group_token(groups, g0 + 7) + 15;
             const bool whole = tile.bad == 0 && g0 + 8 <= groups.count && end <= first && (a.window == 0 || begin > last - a.window);
-            const auto visible = [&](int t) {
-                const int g = g0 + t / 16;
-                return g < groups.count && sees(p, group_token(groups, g) + t % 16, a.window, a.sinks);
+            // bits of 32 tokens from c on: those that the row sees
+            const auto seen = [&](int c) {
+                uint32_t bits = 0;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int g = g0 + c / 16 + k, j0 = group_token(groups, g);
+                    const uint32_t upto = (1u << min(max(p - j0 + 1, 0), 16)) - 1u;
+                    uint32_t from = 0xffffu;
+                    if (a.window > 0) from = ~((1u << min(max(p - a.window - j0 + 1, 0), 16)) - 1u) | ((1u << min(max(a.sinks - j0, 0), 16)) - 1u);
+                    if (g < groups.count) bits |= (upto & from & 0xffffu) << (16 * k);
+                }
+                return bits;
+            };
+            // scores of what is not seen become minus infinity, of tokens without a page NaN
+            const auto mask = [&](int c, uint32_t (&s)[32]) {
+                const uint32_t bits = seen(c), lost = tile.bad >> (c / 16);
+                const uint32_t nan = (lost & 1u ? 0xffffu : 0u) | (lost & 2u ? 0xffff0000u : 0u);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) s[i] = bits >> i & 1u ? (nan >> i & 1u ? 0x7fc00000u : s[i]) : 0xff800000u;
             };
             // the tile's largest score
             float top = minus_infinity();
@@ -278,15 +304,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             for (int c = 0; c < 128; c += 32) {
                 uint32_t s[32];
                 tc5::ld32(s_at + c, s);
-                if (whole) {
+                if (!whole) mask(c, s);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(s[i]));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (visible(c + i)) top = fmaxf(top, __uint_as_float(s[i]));
-                    __syncwarp();
-                }
+                for (int i = 0; i < 32; i += 2) top = fmaxf(top, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
             }
             top = top == minus_infinity() ? top : top * f;
             int shift = tile.value_exponent - reference_exponent;
@@ -324,37 +344,41 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
                 wait_tmem_stores();
             }
             const float offset = (float)shift + kLift - reference(m);
-            float sum = 0.0f;
+            const uint64_t ff = pack_pair(f, f), oo = pack_pair(offset, offset);
+            uint64_t sums2[2] = {pack_pair(0.0f, 0.0f), pack_pair(0.0f, 0.0f)};
 #pragma unroll
             for (int c = 0; c < 128; c += 32) {
                 uint32_t s[32], w[16], rest[16];
                 tc5::ld32(s_at + c, s);
+                if (!whole) mask(c, s);
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
-                    float u[2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        u[k] = power2(fmaf(__uint_as_float(s[i + k]), f, offset));
-                        if (!whole) {
-                            if (tile.bad >> ((c + i + k) / 16) & 1) u[k] = not_a_number();
-                            if (!visible(c + i + k)) u[k] = 0.0f;
-                        }
-                        sum += u[k];
-                    }
-                    w[i / 2] = half2_of(u[0], u[1]);
+                    float u, v;
+                    unpack_pair(fma_pair(pack_pair(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), ff, oo), u, v);
+                    u = power2(u);
+                    v = power2(v);
+                    sums2[i / 2 & 1] = add_pair(sums2[i / 2 & 1], pack_pair(u, v));
+                    w[i / 2] = half2_of(u, v);
                     if (REST) {
                         const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&w[i / 2]));
-                        rest[i / 2] = half2_of(u[0] - back.x, u[1] - back.y);
+                        rest[i / 2] = half2_of(u - back.x, v - back.y);
                     }
                 }
-                __syncwarp();
                 store_tmem16(s_at + c, w);
                 if (REST) store_tmem16(s_at + c + 16, rest);
             }
+            float sum, other;
+            unpack_pair(add_pair(sums2[0], sums2[1]), sum, other);
+            sum += other;
             l = fmaf(sum, exp2_int(-shift - (int)kLift), l);
             if (tile.any_nan != 0) {
-                for (int t = 0; t < 128; ++t)
-                    if (tile.nan[t] != 0 && visible(t)) poison |= tile.nan[t];
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 32) {
+                    const uint32_t bits = whole ? ~0u : seen(c);
+#pragma unroll 1
+                    for (int t = 0; t < 32; ++t)
+                        if (bits >> t & 1u) poison |= tile.nan[c + t];
+                }
                 __syncwarp();
             }
             wait_tmem_stores();
@@ -520,8 +544,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
                         }
                     }
                 }
+                // 16-byte pieces in an order that keeps the 8 lanes of a store on different banks
                 const uint32_t row = to + part / 2 * S::BLOCK_BYTES + t * 128;
-                const uint32_t words[4] = {raw.codes[i].x, raw.codes[i].y, raw.codes[i].z, raw.codes[i].w};
+                const int turn = CHUNKS == 2 ? 0 : CHUNKS == 4 ? part & 2 : part / 2;
+                uint32_t words[4] = {raw.codes[i].x, raw.codes[i].y, raw.codes[i].z, raw.codes[i].w};
+                if (CHUNKS > 2 && (turn & 2)) {
+                    swap(words[0], words[2]);
+                    swap(words[1], words[3]);
+                    swap(s[0], s[1]);
+                }
+                if (CHUNKS > 4 && (turn & 1)) {
+                    swap(words[0], words[1]);
+                    swap(words[2], words[3]);
+                }
 #pragma unroll
                 for (int k0 = 0; k0 < 4; ++k0) {
                     uint4 v = halves_of(words[k0]);
@@ -530,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
                     v.y = mul_half2(v.y, sc);
                     v.z = mul_half2(v.z, sc);
                     v.w = mul_half2(v.w, sc);
-                    store_shared(row + (uint32_t)((part % 2 * 4 + k0 ^ t % 8) << 4), v);
+                    store_shared(row + (uint32_t)(((part % 2 * 4 + (k0 ^ turn)) ^ t % 8) << 4), v);
                 }
             }
             fence_async();
