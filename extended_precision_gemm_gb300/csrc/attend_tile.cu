@@ -33,7 +33,7 @@ constexpr float kLag = 5.0f;   // references follow when they are exceeded by mo
 constexpr int kShift = 3;      // ... and the values' exponent by more than 2^3 either way
 constexpr float kLift = 7.0f;  // weights up to 2^(5 + 3 + 7), below the largest float16
 constexpr int kFar = 64;       // values' exponents are at most so far below the largest seen
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 16 * 32;  // the last three warps only give up their registers
 constexpr int kNoToken = -128;  // in the place of an exponent
 
 __device__ unsigned int g_attend_timeouts = 0;
@@ -51,6 +51,10 @@ struct Shape {
     static constexpr int SMEM = V0 + STAGES * TILE_BYTES + 1024;
     static constexpr int CHUNKS = WIDTH / 32;             // pieces of 32 codes of a token, and a thread's pieces of a tile
     static constexpr uint32_t S_COL = 0, O_COL = 256;
+    // registers of a thread by role: of the 128 that each is launched with, four warps (one of each
+    // role, or two of the softmax) share 512 on a part of the SM
+    static constexpr int SOFTMAX_REGS = NQ == 2 ? 176 : 184, CONVERT_REGS = NQ == 2 ? 112 : 208, MMA_REGS = NQ == 2 ? 48 : 56;
+    static_assert((NQ == 2 ? 2 * SOFTMAX_REGS + CONVERT_REGS + MMA_REGS : SOFTMAX_REGS + CONVERT_REGS + 2 * MMA_REGS) <= 512, "registers of the launch");
 };
 
 // What the softmax has to know of a tile.
@@ -66,7 +70,7 @@ struct TileInfo {
 template <int CHUNKS>
 struct Raw {
     uint4 codes[CHUNKS];
-    uint16_t scales[CHUNKS];
+    uint16_t scales[CHUNKS];  // not set for a token without a page, whose scale is 0
     int exponent;  // of token `thread`
 };
 
@@ -128,7 +132,35 @@ __device__ __forceinline__ void store_tmem16(uint32_t at, const uint32_t (&v)[16
         "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
+// The same columns as tc5::ld32, without the wait: the values are there after
+// wait_tmem_loads, which names them so that no use moves ahead of it.
+__device__ __forceinline__ void start_load32(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]),
+          "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]),
+          "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void wait_tmem_loads(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                   "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]),
+                   "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                   "+r"(v[30]), "+r"(v[31])
+                 :
+                 : "memory");
+}
 __device__ __forceinline__ void wait_tmem_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+template <int N> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 struct Barriers {
     uint64_t q, k_full[2], k_empty[2], v_full[2], v_empty[2], s[2], p[2], o[2], done;
@@ -142,9 +174,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
     __shared__ __align__(8) Barriers bars;
     __shared__ uint32_t tmem_slot;
     __shared__ TileInfo info[S::STAGES];
-    __shared__ __align__(16) int page_ring[4][8];
+    __shared__ int64_t rows[4][8];  // of the groups of four tiles, -1 where there is no page
     __shared__ int8_t exponents[2][128];
-    __shared__ int largest[2][4];
+    __shared__ __align__(16) int largest[2][4];
 
     pdl_wait();
     pdl_launch_dependents();
@@ -199,6 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
 
     if (warp < 4 * S::NQ) {
         // ---- softmax: a thread for a row ----
+        more_registers<S::SOFTMAX_REGS>();
         const int x = warp / 4, quarter = warp % 4, row = quarter * 32 + lane;
         const int column = x * 128 + row;
         const bool have = column < item.columns;
@@ -300,10 +333,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             };
             // the tile's largest score
             float top = minus_infinity();
+            uint32_t ring[2][32];  // one half is loaded while the other is worked on
+            start_load32(s_at, ring[0]);
 #pragma unroll
             for (int c = 0; c < 128; c += 32) {
-                uint32_t s[32];
-                tc5::ld32(s_at + c, s);
+                uint32_t(&s)[32] = ring[c / 32 & 1];
+                wait_tmem_loads(s);
+                start_load32(s_at + (c + 32) % 128, ring[c / 32 & 1 ^ 1]);  // at the end the first again, for the weights
                 if (!whole) mask(c, s);
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) top = fmaxf(top, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
@@ -348,8 +384,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             uint64_t sums2[2] = {pack_pair(0.0f, 0.0f), pack_pair(0.0f, 0.0f)};
 #pragma unroll
             for (int c = 0; c < 128; c += 32) {
-                uint32_t s[32], w[16], rest[16];
-                tc5::ld32(s_at + c, s);
+                uint32_t w[16], rest[16];
+                uint32_t(&s)[32] = ring[c / 32 & 1];
+                wait_tmem_loads(s);
+                if (c < 96) start_load32(s_at + c + 32, ring[c / 32 & 1 ^ 1]);
                 if (!whole) mask(c, s);
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
@@ -439,55 +477,64 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
         tc5::fence_before_sync();
     } else if (warp >= 8 && warp < 12) {
         // ---- codes to 16 bits ----
+        if constexpr (S::CONVERT_REGS < 128) fewer_registers<S::CONVERT_REGS>();
+        else more_registers<S::CONVERT_REGS>();
         constexpr int CHUNKS = S::CHUNKS, BLOCK = mx4_block(FMT), BLOCKS = WIDTH / BLOCK;
         const int thread = threadIdx.x - 8 * 32, w = warp - 8;
+        // piece i of the thread: 32 codes of token i * 128 / CHUNKS + t, the part-th of it
+        const int t = thread / CHUNKS, part = thread % CHUNKS;
         const int units = 2 * n;  // K0, K1, V0, K2, V1, ..., V(n - 1)
         const auto is_value = [&](int u) { return u == units - 1 || (u > 0 && u % 2 == 0); };
         const auto tile_of = [&](int u) { return u == units - 1 ? n - 1 : u == 0 ? 0 : u % 2 ? (u + 1) / 2 : u / 2 - 1; };
-        const auto page_for = [&](int j) {  // of group thread % 8 of tile j
+        // the row of the keys of the first token of group thread % 8 of tile j, -1 where it has no page
+        const auto row_for = [&](int j) -> int64_t {
             const int g = (t0 + j) * 8 + thread;
-            return j < n && g < groups.count ? page_of(a.c, a.b, item.sequence, group_token(groups, g)) : -1;
+            if (j >= n || g >= groups.count) return -1;
+            const int token = group_token(groups, g), page = page_of(a.c, a.b, item.sequence, token);
+            return page < 0 ? -1 : cache_row(a.c, page, 0, head, token & (a.c.page_size - 1));
         };
-        int held = -1;
+        const int64_t to_values = (int64_t)a.c.heads * a.c.page_size;  // rows from a key to its value
+        int64_t held = -1;
         if (thread < 8) {
-            page_ring[0][thread] = page_for(0);
-            page_ring[1][thread] = page_for(1);
-            held = page_for(2);
+            rows[0][thread] = row_for(0);
+            rows[1][thread] = row_for(1);
+            held = row_for(2);
         }
         asm volatile("bar.sync 1, 128;" ::: "memory");
+        const uint8_t* const code_base = a.c.codes + (t % 16) * (WIDTH / 2) + part * 16;
+        const uint8_t* const scale_base = a.c.scales + (t % 16) * BLOCKS + part * (32 / BLOCK);
+        const int8_t* const exponent_base = a.c.exponents + thread % 16;
         Raw<CHUNKS> even, odd;  // units u and u + 1 in turn: one is loaded while the other is converted
         const auto load = [&](int u, Raw<CHUNKS>& raw) {
-            const int j = tile_of(u), kv = is_value(u) ? 1 : 0, g0 = (t0 + j) * 8;
-            const int* pages = page_ring[j & 3];
+            const int j = tile_of(u);
+            const int64_t add = is_value(u) ? to_values : 0;
 #pragma unroll
             for (int i = 0; i < CHUNKS; ++i) {
-                const int at = i * 128 + thread, t = at / CHUNKS, part = at % CHUNKS;
-                const int page = pages[t / 16];
-                raw.codes[i] = make_uint4(0, 0, 0, 0);
-                raw.scales[i] = 0;
-                if (page >= 0) {
-                    const int64_t r = cache_row(a.c, page, kv, head, group_token(groups, g0 + t / 16) & (a.c.page_size - 1)) + t % 16;
-                    raw.codes[i] = __ldg(reinterpret_cast<const uint4*>(a.c.codes + r * (WIDTH / 2)) + part);
-                    raw.scales[i] = FMT == kMxfp4 ? (uint16_t)__ldg(a.c.scales + r * BLOCKS + part)
-                                                  : __ldg(reinterpret_cast<const uint16_t*>(a.c.scales + r * BLOCKS) + part);
+                const int64_t r = rows[j & 3][i * (8 / CHUNKS) + t / 16];
+                if (r >= 0) {
+                    raw.codes[i] = __ldg(reinterpret_cast<const uint4*>(code_base + (r + add) * (WIDTH / 2)));
+                    raw.scales[i] = FMT == kMxfp4 ? (uint16_t)__ldg(scale_base + (r + add) * BLOCKS)
+                                                  : __ldg(reinterpret_cast<const uint16_t*>(scale_base + (r + add) * BLOCKS));
                 }
             }
-            const int page = pages[thread / 16], token = group_token(groups, g0 + thread / 16) + thread % 16;
+            const int64_t r = rows[j & 3][thread / 16];
             raw.exponent = kNoToken;
-            if (page >= 0 && token < item.length)
-                raw.exponent = __ldg(a.c.exponents + cache_row(a.c, page, kv, head, token & (a.c.page_size - 1)));
+            if (r >= 0 && group_token(groups, (t0 + j) * 8 + thread / 16) + thread % 16 < item.length) raw.exponent = __ldg(exponent_base + r + add);
         };
+        // where a piece goes: 16-byte pieces in an order that keeps the 8 lanes of a store on different banks
+        const int turn = CHUNKS == 2 ? 0 : CHUNKS == 4 ? part & 2 : part / 2;
+        const uint32_t place = base + part / 2 * S::BLOCK_BYTES + t * 128 + (uint32_t)(((part % 2 * 4) ^ turn ^ (t % 8)) << 4);
         bool ok = true;
-        int most_seen = kNoToken, key_exponent[2] = {0, 0};
+        int most_seen = kNoToken, key_exponent = 0, next_key_exponent = 0;
         const auto convert = [&](int u, Raw<CHUNKS>& raw, Raw<CHUNKS>& following) {
             const int j = tile_of(u), stage = j % S::STAGES, parity = u & 1;
             const bool value = is_value(u);
             // a warp that gave up once goes on without waiting: the others meet it at the barrier below
             ok = ok && warp_wait(bar(value ? bars.v_empty : bars.k_empty, stage), ((j / S::STAGES) & 1) ^ 1, kWaitNs);
-            // pages of two tiles on, for the loads behind the next barrier
+            // rows of two tiles on, for the loads behind the next barrier
             if (!value && thread < 8) {
-                page_ring[(j + 2) & 3][thread] = held;
-                held = page_for(j + 3);
+                rows[(j + 2) & 3][thread] = held;
+                held = row_for(j + 3);
             }
             exponents[parity][thread] = (int8_t)raw.exponent;
             const int top = __reduce_max_sync(~0u, raw.exponent);
@@ -498,26 +545,32 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             }
             asm volatile("bar.sync 1, 128;" ::: "memory");
             if (u + 1 < units) load(u + 1, following);
-            int e = max(max(largest[parity][0], largest[parity][1]), max(largest[parity][2], largest[parity][3]));
+            const int4 tops = *reinterpret_cast<const int4*>(largest[parity]);
+            int e = max(max(tops.x, tops.y), max(tops.z, tops.w));
             if (value) {
                 most_seen = max(most_seen, e);
                 e = max(e, most_seen - kFar);
             }
             e = max(e, -127);
-            if (value && thread == 0) {
-                info[stage].key_factor = mxfp4_scale((uint32_t)(key_exponent[j & 1] + 127)) * exp2_int(-lift_of<FMT>());
-                info[stage].value_exponent = e;
-                uint32_t bad = 0;
-                for (int g = 0; g < 8; ++g)
-                    if ((t0 + j) * 8 + g < groups.count && page_ring[j & 3][g] < 0) bad |= 1u << g;
-                info[stage].bad = bad;
+            if (value) {
+                if (thread == 0) {
+                    info[stage].key_factor = mxfp4_scale((uint32_t)(key_exponent + 127)) * exp2_int(-lift_of<FMT>());
+                    info[stage].value_exponent = e;
+                    uint32_t bad = 0;
+#pragma unroll 1
+                    for (int g = 0; g < 8; ++g)
+                        if ((t0 + j) * 8 + g < groups.count && rows[j & 3][g] < 0) bad |= 1u << g;
+                    info[stage].bad = bad;
+                }
+                key_exponent = next_key_exponent;
+            } else {
+                (u == 0 ? key_exponent : next_key_exponent) = e;
             }
-            if (!value) key_exponent[j & 1] = e;
-            const uint32_t to = base + (value ? S::V0 : S::K0) + stage * S::TILE_BYTES;
+            const uint32_t to = place + (value ? S::V0 : S::K0) + stage * S::TILE_BYTES;
 #pragma unroll
             for (int i = 0; i < CHUNKS; ++i) {
-                const int at = i * 128 + thread, t = at / CHUNKS, part = at % CHUNKS;
-                const int et = exponents[parity][t];
+                const int at = i * (128 / CHUNKS) + t;
+                const int et = exponents[parity][at];
                 uint32_t s[2];
                 if (FMT == kMxfp4) {
                     const float power = exp2_int(min(max((int)raw.scales[i] - 127 - e + lift_of<kMxfp4>(), -126), 15));
@@ -532,21 +585,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
                     s[1] = __byte_perm(h2, h2, 0x3232);
                 }
                 if (et == kNoToken) s[0] = s[1] = 0;
-                if (value) {
+                if (value && ((s[0] & 0x7fffu) > 0x7c00u || (s[1] & 0x7fffu) > 0x7c00u)) {  // NaN: 0 here, and a mark
                     constexpr int PER = 32 / BLOCK;
+                    uint32_t marks = 0;
 #pragma unroll
-                    for (int b = 0; b < PER; ++b) {
-                        if ((s[b] & 0x7fffu) > 0x7c00u) {
-                            s[b] = 0;
-                            if (PER == 1) s[1] = 0;
-                            atomicOr(&info[stage].nan[t], 1u << (part * PER + b));
-                            info[stage].any_nan = 1;
-                        }
-                    }
+                    for (int b = 0; b < PER; ++b)
+                        if ((s[b] & 0x7fffu) > 0x7c00u) marks |= 1u << (part * PER + b);
+                    if ((s[0] & 0x7fffu) > 0x7c00u) s[0] = 0;
+                    if ((s[1] & 0x7fffu) > 0x7c00u) s[1] = 0;
+                    atomicOr(&info[stage].nan[at], marks);
+                    info[stage].any_nan = 1;
                 }
-                // 16-byte pieces in an order that keeps the 8 lanes of a store on different banks
-                const uint32_t row = to + part / 2 * S::BLOCK_BYTES + t * 128;
-                const int turn = CHUNKS == 2 ? 0 : CHUNKS == 4 ? part & 2 : part / 2;
                 uint32_t words[4] = {raw.codes[i].x, raw.codes[i].y, raw.codes[i].z, raw.codes[i].w};
                 if (CHUNKS > 2 && (turn & 2)) {
                     swap(words[0], words[2]);
@@ -565,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
                     v.y = mul_half2(v.y, sc);
                     v.z = mul_half2(v.z, sc);
                     v.w = mul_half2(v.w, sc);
-                    store_shared(row + (uint32_t)(((part % 2 * 4 + (k0 ^ turn)) ^ t % 8) << 4), v);
+                    store_shared((to + i * (128 / CHUNKS) * 128) ^ (uint32_t)(k0 << 4), v);
                 }
             }
             fence_async();
@@ -578,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             convert(u + 1, odd, even);
         }
         if (!ok && lane == 0) atomicAdd(&g_attend_timeouts, 1u);
-    } else if (warp == 12 && n > 0) {
+    } else if (fewer_registers<S::MMA_REGS>(); warp == 12 && n > 0) {
         // ---- MMAs ----
         constexpr uint32_t S_DESC = tc5::idesc_f16(false, false, false, 128, 128);
         constexpr uint32_t O_DESC = tc5::idesc_f16(false, false, true, 128, WIDTH);
