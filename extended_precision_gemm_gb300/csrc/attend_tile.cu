@@ -33,7 +33,9 @@ constexpr float kLag = 5.0f;   // references follow when they are exceeded by mo
 constexpr int kShift = 3;      // ... and the values' exponent by more than 2^3 either way
 constexpr float kLift = 7.0f;  // weights up to 2^(5 + 3 + 7), below the largest float16
 constexpr int kFar = 64;       // values' exponents are at most so far below the largest seen
-constexpr int kThreads = 16 * 32;  // the last three warps only give up their registers
+constexpr int kThreads = 20 * 32;  // the last three warps only give up their registers
+constexpr int kConverters = 256;
+constexpr int kRing = 4;  // tiles whose rows, exponents and marks are kept
 constexpr int kNoToken = -128;  // in the place of an exponent
 
 __device__ unsigned int g_attend_timeouts = 0;
@@ -49,12 +51,14 @@ struct Shape {
     static constexpr int TILE_BYTES = WIDTH / 64 * BLOCK_BYTES;
     static constexpr int K0 = NQ * TILE_BYTES, V0 = K0 + STAGES * TILE_BYTES;
     static constexpr int SMEM = V0 + STAGES * TILE_BYTES + 1024;
-    static constexpr int CHUNKS = WIDTH / 32;             // pieces of 32 codes of a token, and a thread's pieces of a tile
+    static constexpr int PIECES = WIDTH / 32;                     // of 32 codes, of a token
+    static constexpr int PER_PASS = kConverters / PIECES;         // tokens that the threads convert at once
+    static constexpr int PASSES = 128 / PER_PASS;
     static constexpr uint32_t S_COL = 0, O_COL = 256;
-    // registers of a thread by role: of the 128 that each is launched with, four warps (one of each
-    // role, or two of the softmax) share 512 on a part of the SM
-    static constexpr int SOFTMAX_REGS = NQ == 2 ? 176 : 184, CONVERT_REGS = NQ == 2 ? 112 : 208, MMA_REGS = NQ == 2 ? 48 : 56;
-    static_assert((NQ == 2 ? 2 * SOFTMAX_REGS + CONVERT_REGS + MMA_REGS : SOFTMAX_REGS + CONVERT_REGS + 2 * MMA_REGS) <= 512, "registers of the launch");
+    // registers of a thread by role: of the 96 that each is launched with, five warps (two of the softmax,
+    // two that convert, one of the last four) share 480 on a part of the SM
+    static constexpr int SOFTMAX_REGS = NQ == 2 ? 136 : 168, IDLE_REGS = 24, CONVERT_REGS = NQ == 2 ? 80 : 120, MMA_REGS = 48;
+    static_assert(SOFTMAX_REGS + (NQ == 2 ? SOFTMAX_REGS : IDLE_REGS) + 2 * CONVERT_REGS + MMA_REGS <= 480, "registers of the launch");
 };
 
 // What the softmax has to know of a tile.
@@ -66,12 +70,11 @@ struct TileInfo {
     uint32_t nan[128];  // blocks of a token's values that are NaN
 };
 
-// Keys or values of a tile as a thread reads them.
-template <int CHUNKS>
+// A thread's pieces of a tile's keys or values.
+template <int PASSES>
 struct Raw {
-    uint4 codes[CHUNKS];
-    uint16_t scales[CHUNKS];  // not set for a token without a page, whose scale is 0
-    int exponent;  // of token `thread`
+    uint4 codes[PASSES];
+    uint16_t scales[PASSES];  // not set for a token without a page, whose scale is 0
 };
 
 __device__ __forceinline__ uint32_t half2_of(float a, float b) {  // a in the low half
@@ -164,6 +167,7 @@ template <int N> __device__ __forceinline__ void fewer_registers() { asm volatil
 
 struct Barriers {
     uint64_t q, k_full[2], k_empty[2], v_full[2], v_empty[2], s[2], p[2], o[2], done;
+    uint64_t info[kRing], marks[kRing];  // of tiles in turn: what the softmax has to know, and the NaN of its values
 };
 
 template <typename T, int WIDTH, int FMT>
@@ -173,10 +177,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
     extern __shared__ __align__(16) uint8_t smem_raw[];
     __shared__ __align__(8) Barriers bars;
     __shared__ uint32_t tmem_slot;
-    __shared__ TileInfo info[S::STAGES];
-    __shared__ int64_t rows[4][8];  // of the groups of four tiles, -1 where there is no page
-    __shared__ int8_t exponents[2][128];
-    __shared__ __align__(16) int largest[2][4];
+    __shared__ TileInfo info[kRing];
+    __shared__ int64_t rows[kRing][8];  // of groups of keys, -1 where there is no page
+    __shared__ int8_t exponents[kRing][2][128];  // of keys and values
+    __shared__ __align__(16) int largest[2][2][4];  // of the tiles in turn
 
     pdl_wait();
     pdl_launch_dependents();
@@ -209,18 +213,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
     if (threadIdx.x == 0) {
         mbar_init(q_full, 4 * S::NQ);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(bars.k_full, i), 4);
-            mbar_init(bar(bars.v_full, i), 4);
+            mbar_init(bar(bars.k_full, i), kConverters / 32);
+            mbar_init(bar(bars.v_full, i), kConverters / 32);
             mbar_init(bar(bars.k_empty, i), 1);
             mbar_init(bar(bars.v_empty, i), 1);
             mbar_init(bar(bars.s, i), 1);
             mbar_init(bar(bars.p, i), 4);
             mbar_init(bar(bars.o, i), 1);
         }
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(bar(bars.info, i), 1);
+            mbar_init(bar(bars.marks, i), kConverters / 32);
+        }
         mbar_init(done, 1);
         fence_barrier_init();
     }
-    if (warp == 12) {
+    if (warp == 16) {
         tc5::tmem_alloc(smem_addr(&tmem_slot), 512);
         tc5::tmem_relinquish();
     }
@@ -298,41 +306,56 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
         uint32_t poison = 0;
         bool ok = true;
         const int mine = need[x];
+        // bits of 32 tokens from the c-th of a tile of groups from g0 on: those that the row sees
+        const auto seen = [&](int g0, int c) {
+            uint32_t bits = 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int g = g0 + c / 16 + k, j0 = group_token(groups, g);
+                const uint32_t upto = (1u << min(max(p - j0 + 1, 0), 16)) - 1u;
+                uint32_t from = 0xffffu;
+                if (a.window > 0) from = ~((1u << min(max(p - a.window - j0 + 1, 0), 16)) - 1u) | ((1u << min(max(a.sinks - j0, 0), 16)) - 1u);
+                if (g < groups.count) bits |= (upto & from & 0xffffu) << (16 * k);
+            }
+            return bits;
+        };
+        // the blocks of values that are NaN in tokens of tile j that the row sees
+        const auto take_marks = [&](int j) {
+            if (!warp_wait(bar(bars.marks, j % kRing), (j / kRing) & 1, kWaitNs)) return false;
+            const TileInfo& tile = info[j % kRing];
+            if (tile.any_nan != 0) {
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 32) {
+                    const uint32_t bits = seen((t0 + j) * 8, c);
+#pragma unroll 1
+                    for (int t = 0; t < 32; ++t)
+                        if (bits >> t & 1u) poison |= tile.nan[c + t];
+                }
+                __syncwarp();
+            }
+            return true;
+        };
         for (int j = 0; j < mine; ++j) {
-            const int stage = j % S::STAGES;
             const int buffer = S::NQ == 2 ? x : j & 1;
             const uint32_t s_at = tmem + S::S_COL + buffer * 128 + lanes;
-            ok = warp_wait(bar(bars.v_full, stage), (j / S::STAGES) & 1, kWaitNs) &&
+            ok = warp_wait(bar(bars.info, j % kRing), (j / kRing) & 1, kWaitNs) &&
                  warp_wait(bar(bars.s, buffer), (S::NQ == 2 ? j : j >> 1) & 1, kWaitNs);
             if (!ok) break;
             tc5::fence_after_sync();
-            const TileInfo& tile = info[stage];
+            const TileInfo& tile = info[j % kRing];
             const float f = fmaxf(factor * tile.key_factor, 0x1p-120f);  // no 0: minus infinity stays what it is
             const int g0 = (t0 + j) * 8;
             const int begin = group_token(groups, g0), end = group_token(groups, g0 + 7) + 15;
             const bool whole = tile.bad == 0 && g0 + 8 <= groups.count && end <= first && (a.window == 0 || begin > last - a.window);
-            // bits of 32 tokens from c on: those that the row sees
-            const auto seen = [&](int c) {
-                uint32_t bits = 0;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int g = g0 + c / 16 + k, j0 = group_token(groups, g);
-                    const uint32_t upto = (1u << min(max(p - j0 + 1, 0), 16)) - 1u;
-                    uint32_t from = 0xffffu;
-                    if (a.window > 0) from = ~((1u << min(max(p - a.window - j0 + 1, 0), 16)) - 1u) | ((1u << min(max(a.sinks - j0, 0), 16)) - 1u);
-                    if (g < groups.count) bits |= (upto & from & 0xffffu) << (16 * k);
-                }
-                return bits;
-            };
             // scores of what is not seen become minus infinity, of tokens without a page NaN
             const auto mask = [&](int c, uint32_t (&s)[32]) {
-                const uint32_t bits = seen(c), lost = tile.bad >> (c / 16);
+                const uint32_t bits = seen(g0, c), lost = tile.bad >> (c / 16);
                 const uint32_t nan = (lost & 1u ? 0xffffu : 0u) | (lost & 2u ? 0xffff0000u : 0u);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) s[i] = bits >> i & 1u ? (nan >> i & 1u ? 0x7fc00000u : s[i]) : 0xff800000u;
             };
             // the tile's largest score
-            float top = minus_infinity();
+            float tops[4] = {minus_infinity(), minus_infinity(), minus_infinity(), minus_infinity()};
             uint32_t ring[2][32];  // one half is loaded while the other is worked on
             start_load32(s_at, ring[0]);
 #pragma unroll
@@ -342,8 +365,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
                 start_load32(s_at + (c + 32) % 128, ring[c / 32 & 1 ^ 1]);  // at the end the first again, for the weights
                 if (!whole) mask(c, s);
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) top = fmaxf(top, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
+                for (int i = 0; i < 32; i += 2)
+                    tops[i / 2 & 3] = fmaxf(tops[i / 2 & 3], fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
             }
+            float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             top = top == minus_infinity() ? top : top * f;
             int shift = tile.value_exponent - reference_exponent;
             float turn = 1.0f;
@@ -409,16 +434,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             unpack_pair(add_pair(sums2[0], sums2[1]), sum, other);
             sum += other;
             l = fmaf(sum, exp2_int(-shift - (int)kLift), l);
-            if (tile.any_nan != 0) {
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 32) {
-                    const uint32_t bits = whole ? ~0u : seen(c);
-#pragma unroll 1
-                    for (int t = 0; t < 32; ++t)
-                        if (bits >> t & 1u) poison |= tile.nan[c + t];
-                }
-                __syncwarp();
-            }
+            // marks are read before the weights are announced, which keeps their slot: of the tile before this
+            // one, whose values were converted long since, and of the last one too
+            if (j > 0) ok = take_marks(j - 1);
+            if (ok && j == mine - 1) ok = take_marks(j);
+            if (!ok) break;
             wait_tmem_stores();
             tc5::fence_before_sync();
             __syncwarp();
@@ -475,14 +495,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             __syncwarp();
         }
         tc5::fence_before_sync();
-    } else if (warp >= 8 && warp < 12) {
+    } else if (warp < 8) {
+        fewer_registers<S::IDLE_REGS>();
+    } else if (warp < 16) {
         // ---- codes to 16 bits ----
-        if constexpr (S::CONVERT_REGS < 128) fewer_registers<S::CONVERT_REGS>();
+        if constexpr (S::CONVERT_REGS < 96) fewer_registers<S::CONVERT_REGS>();
         else more_registers<S::CONVERT_REGS>();
-        constexpr int CHUNKS = S::CHUNKS, BLOCK = mx4_block(FMT), BLOCKS = WIDTH / BLOCK;
-        const int thread = threadIdx.x - 8 * 32, w = warp - 8;
-        // piece i of the thread: 32 codes of token i * 128 / CHUNKS + t, the part-th of it
-        const int t = thread / CHUNKS, part = thread % CHUNKS;
+        constexpr int PIECES = S::PIECES, PASSES = S::PASSES, BLOCK = mx4_block(FMT), BLOCKS = WIDTH / BLOCK;
+        const int thread = threadIdx.x - 8 * 32;
+        // in a pass the thread has 32 codes of token t, the part-th of it
+        const int t = thread / PIECES, part = thread % PIECES;
         const int units = 2 * n;  // K0, K1, V0, K2, V1, ..., V(n - 1)
         const auto is_value = [&](int u) { return u == units - 1 || (u > 0 && u % 2 == 0); };
         const auto tile_of = [&](int u) { return u == units - 1 ? n - 1 : u == 0 ? 0 : u % 2 ? (u + 1) / 2 : u / 2 - 1; };
@@ -500,83 +522,90 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             rows[1][thread] = row_for(1);
             held = row_for(2);
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(kConverters) : "memory");
         const uint8_t* const code_base = a.c.codes + (t % 16) * (WIDTH / 2) + part * 16;
         const uint8_t* const scale_base = a.c.scales + (t % 16) * BLOCKS + part * (32 / BLOCK);
-        const int8_t* const exponent_base = a.c.exponents + thread % 16;
-        Raw<CHUNKS> even, odd;  // units u and u + 1 in turn: one is loaded while the other is converted
-        const auto load = [&](int u, Raw<CHUNKS>& raw) {
+        // of exponents a thread has one: a key's (threads 0 to 127) or a value's
+        const int kv = thread / 128, et = thread % 128;
+        const int8_t* const exponent_base = a.c.exponents + (kv ? to_values : 0) + et % 16;
+        Raw<PASSES> even, odd;  // units u and u + 1 in turn: one is loaded while the other is converted
+        int exponent = kNoToken;  // of the next tile
+        const auto load = [&](int u, Raw<PASSES>& raw) {
             const int j = tile_of(u);
-            const int64_t add = is_value(u) ? to_values : 0;
+            const bool value = is_value(u);
+            const int64_t add = value ? to_values : 0;
 #pragma unroll
-            for (int i = 0; i < CHUNKS; ++i) {
-                const int64_t r = rows[j & 3][i * (8 / CHUNKS) + t / 16];
+            for (int i = 0; i < PASSES; ++i) {
+                const int64_t r = rows[j % kRing][i * (S::PER_PASS / 16) + t / 16];
                 if (r >= 0) {
                     raw.codes[i] = __ldg(reinterpret_cast<const uint4*>(code_base + (r + add) * (WIDTH / 2)));
                     raw.scales[i] = FMT == kMxfp4 ? (uint16_t)__ldg(scale_base + (r + add) * BLOCKS)
                                                   : __ldg(reinterpret_cast<const uint16_t*>(scale_base + (r + add) * BLOCKS));
                 }
             }
-            const int64_t r = rows[j & 3][thread / 16];
-            raw.exponent = kNoToken;
-            if (r >= 0 && group_token(groups, (t0 + j) * 8 + thread / 16) + thread % 16 < item.length) raw.exponent = __ldg(exponent_base + r + add);
+            if (!value) {
+                const int64_t r = rows[j % kRing][et / 16];
+                exponent = kNoToken;
+                if (r >= 0 && group_token(groups, (t0 + j) * 8 + et / 16) + et % 16 < item.length) exponent = __ldg(exponent_base + r);
+            }
         };
         // where a piece goes: 16-byte pieces in an order that keeps the 8 lanes of a store on different banks
-        const int turn = CHUNKS == 2 ? 0 : CHUNKS == 4 ? part & 2 : part / 2;
+        const int turn = PIECES == 2 ? 0 : PIECES == 4 ? part & 2 : part / 2;
         const uint32_t place = base + part / 2 * S::BLOCK_BYTES + t * 128 + (uint32_t)(((part % 2 * 4) ^ turn ^ (t % 8)) << 4);
         bool ok = true;
-        int most_seen = kNoToken, key_exponent = 0, next_key_exponent = 0;
-        const auto convert = [&](int u, Raw<CHUNKS>& raw, Raw<CHUNKS>& following) {
-            const int j = tile_of(u), stage = j % S::STAGES, parity = u & 1;
+        int most_seen = kNoToken, key_exponent = 0, value_exponent[2] = {0, 0};  // value_exponent: of the tile at hand and the next
+        const auto convert = [&](int u, Raw<PASSES>& raw, Raw<PASSES>& following) {
+            const int j = tile_of(u), stage = j % S::STAGES, slot = j % kRing;
             const bool value = is_value(u);
-            // a warp that gave up once goes on without waiting: the others meet it at the barrier below
+            int e;
+            // a warp that gave up once goes on without waiting: the others meet it at the barrier
             ok = ok && warp_wait(bar(value ? bars.v_empty : bars.k_empty, stage), ((j / S::STAGES) & 1) ^ 1, kWaitNs);
-            // rows of two tiles on, for the loads behind the next barrier
-            if (!value && thread < 8) {
-                rows[(j + 2) & 3][thread] = held;
-                held = row_for(j + 3);
-            }
-            exponents[parity][thread] = (int8_t)raw.exponent;
-            const int top = __reduce_max_sync(~0u, raw.exponent);
-            if (lane == 0) largest[parity][w] = top;
-            if (value) {
-                info[stage].nan[thread] = 0;
-                if (thread == 0) info[stage].any_nan = 0;
-            }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            if (u + 1 < units) load(u + 1, following);
-            const int4 tops = *reinterpret_cast<const int4*>(largest[parity]);
-            int e = max(max(tops.x, tops.y), max(tops.z, tops.w));
-            if (value) {
-                most_seen = max(most_seen, e);
-                e = max(e, most_seen - kFar);
-            }
-            e = max(e, -127);
-            if (value) {
+            if (!value) {
+                // the scores of tile j - 2 are there: the softmax has done with tile j - 4, whose slot this is
+                exponents[slot][kv][et] = (int8_t)exponent;
+                const int top = __reduce_max_sync(~0u, exponent);
+                if (lane == 0) largest[j & 1][kv][et / 32] = top;
+                if (thread < 128) info[slot].nan[thread] = 0;
+                if (thread == 0) info[slot].any_nan = 0;
+                asm volatile("bar.sync 1, %0;" ::"n"(kConverters) : "memory");
+                if (u + 1 < units) load(u + 1, following);
+                if (thread < 8) {  // rows of two tiles on, for loads behind the next barrier
+                    rows[(j + 2) % kRing][thread] = held;
+                    held = row_for(j + 3);
+                }
+                const int4 a0 = *reinterpret_cast<const int4*>(largest[j & 1][0]), a1 = *reinterpret_cast<const int4*>(largest[j & 1][1]);
+                e = key_exponent = max(max(max(a0.x, a0.y), max(a0.z, a0.w)), -127);
+                const int v = max(max(a1.x, a1.y), max(a1.z, a1.w));
+                most_seen = max(most_seen, v);
+                value_exponent[0] = u == 0 ? 0 : value_exponent[1];
+                value_exponent[1] = max(max(v, most_seen - kFar), -127);
+                if (u == 0) value_exponent[0] = value_exponent[1];
                 if (thread == 0) {
-                    info[stage].key_factor = mxfp4_scale((uint32_t)(key_exponent + 127)) * exp2_int(-lift_of<FMT>());
-                    info[stage].value_exponent = e;
+                    info[slot].key_factor = mxfp4_scale((uint32_t)(key_exponent + 127)) * exp2_int(-lift_of<FMT>());
+                    info[slot].value_exponent = value_exponent[1];
                     uint32_t bad = 0;
 #pragma unroll 1
                     for (int g = 0; g < 8; ++g)
-                        if ((t0 + j) * 8 + g < groups.count && rows[j & 3][g] < 0) bad |= 1u << g;
-                    info[stage].bad = bad;
+                        if ((t0 + j) * 8 + g < groups.count && rows[slot][g] < 0) bad |= 1u << g;
+                    info[slot].bad = bad;
+                    mbar_arrive(bar(bars.info, slot));
                 }
-                key_exponent = next_key_exponent;
             } else {
-                (u == 0 ? key_exponent : next_key_exponent) = e;
+                if (u + 1 < units) load(u + 1, following);
+                // K(j + 1) went before V(j), but for the last
+                e = u == units - 1 ? value_exponent[1] : value_exponent[0];
             }
             const uint32_t to = place + (value ? S::V0 : S::K0) + stage * S::TILE_BYTES;
 #pragma unroll
-            for (int i = 0; i < CHUNKS; ++i) {
-                const int at = i * (128 / CHUNKS) + t;
-                const int et = exponents[parity][at];
+            for (int i = 0; i < PASSES; ++i) {
+                const int at = i * S::PER_PASS + t;
+                const int own = exponents[slot][value ? 1 : 0][at];
                 uint32_t s[2];
                 if (FMT == kMxfp4) {
                     const float power = exp2_int(min(max((int)raw.scales[i] - 127 - e + lift_of<kMxfp4>(), -126), 15));
                     s[0] = s[1] = raw.scales[i] == 255u ? 0x7fff7fffu : half2_of(power, power);
                 } else {
-                    const float lifted = exp2_int(min(max(et - e + lift_of<kNvfp4>(), -126), 15));
+                    const float lifted = exp2_int(min(max(own - e + lift_of<kNvfp4>(), -126), 15));
                     const uint32_t power = half2_of(lifted, lifted);
                     uint32_t h2;
                     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(raw.scales[i]));
@@ -584,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
                     s[0] = __byte_perm(h2, h2, 0x1010);
                     s[1] = __byte_perm(h2, h2, 0x3232);
                 }
-                if (et == kNoToken) s[0] = s[1] = 0;
+                if (own == kNoToken) s[0] = s[1] = 0;
                 if (value && ((s[0] & 0x7fffu) > 0x7c00u || (s[1] & 0x7fffu) > 0x7c00u)) {  // NaN: 0 here, and a mark
                     constexpr int PER = 32 / BLOCK;
                     uint32_t marks = 0;
@@ -593,16 +622,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
                         if ((s[b] & 0x7fffu) > 0x7c00u) marks |= 1u << (part * PER + b);
                     if ((s[0] & 0x7fffu) > 0x7c00u) s[0] = 0;
                     if ((s[1] & 0x7fffu) > 0x7c00u) s[1] = 0;
-                    atomicOr(&info[stage].nan[at], marks);
-                    info[stage].any_nan = 1;
+                    atomicOr(&info[slot].nan[at], marks);
+                    info[slot].any_nan = 1;
                 }
                 uint32_t words[4] = {raw.codes[i].x, raw.codes[i].y, raw.codes[i].z, raw.codes[i].w};
-                if (CHUNKS > 2 && (turn & 2)) {
+                if (PIECES > 2 && (turn & 2)) {
                     swap(words[0], words[2]);
                     swap(words[1], words[3]);
                     swap(s[0], s[1]);
                 }
-                if (CHUNKS > 4 && (turn & 1)) {
+                if (PIECES > 4 && (turn & 1)) {
                     swap(words[0], words[1]);
                     swap(words[2], words[3]);
                 }
@@ -614,12 +643,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
                     v.y = mul_half2(v.y, sc);
                     v.z = mul_half2(v.z, sc);
                     v.w = mul_half2(v.w, sc);
-                    store_shared((to + i * (128 / CHUNKS) * 128) ^ (uint32_t)(k0 << 4), v);
+                    store_shared((to + i * S::PER_PASS * 128) ^ (uint32_t)(k0 << 4), v);
                 }
             }
             fence_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(value ? bars.v_full : bars.k_full, stage));
+            if (lane == 0) {
+                mbar_arrive(bar(value ? bars.v_full : bars.k_full, stage));
+                if (value) mbar_arrive(bar(bars.marks, slot));
+            }
         };
         if (n > 0) load(0, even);
         for (int u = 0; u < units; u += 2) {  // an even number of them
@@ -627,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             convert(u + 1, odd, even);
         }
         if (!ok && lane == 0) atomicAdd(&g_attend_timeouts, 1u);
-    } else if (fewer_registers<S::MMA_REGS>(); warp == 12 && n > 0) {
+    } else if (fewer_registers<S::MMA_REGS>(); warp == 16 && n > 0) {
         // ---- MMAs ----
         constexpr uint32_t S_DESC = tc5::idesc_f16(false, false, false, 128, 128);
         constexpr uint32_t O_DESC = tc5::idesc_f16(false, false, true, 128, WIDTH);
@@ -722,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
     tc5::fence_before_sync();
     __syncthreads();
     tc5::fence_after_sync();
-    if (warp == 12) {
+    if (warp == 16) {
         __syncwarp();
         tc5::tmem_dealloc(tmem, 512);
     }
