@@ -110,6 +110,32 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
 __device__ __forceinline__ void store_shared(uint32_t at, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
+// Loads that stay where they are written, ahead of the conversions of the tile before.
+__device__ __forceinline__ uint4 fetch16(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint16_t fetch2(const void* p) {
+    uint16_t v;
+    asm volatile("ld.global.nc.b16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint16_t fetch1(const void* p) {
+    uint16_t v;
+    asm volatile("ld.global.nc.u8 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ int fetch_signed1(const void* p) {
+    int v;
+    asm volatile("ld.global.nc.s8 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ int fetch4(const void* p) {
+    int v;
+    asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
 __device__ __forceinline__ void swap(uint32_t& a, uint32_t& b) {
     const uint32_t t = a;
     a = b;
@@ -164,6 +190,30 @@ __device__ __forceinline__ void wait_tmem_stores() { asm volatile("tcgen05.wait:
 
 template <int N> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// 16 columns of 32 bits, with the wait for them.
+__device__ __forceinline__ void load_tmem16(uint32_t at, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+          "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(at)
+        : "memory");
+}
+// 32 weights (and what their rounding left) times a power of two.
+template <bool REST>
+__device__ __noinline__ void follow_weights(uint32_t at, uint32_t by) {
+    wait_tmem_stores();
+#pragma unroll
+    for (int k = 0; k < (REST ? 2 : 1); ++k) {
+        uint32_t v[16];
+        load_tmem16(at + 16 * k, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = mul_half2(v[i], by);
+        store_tmem16(at + 16 * k, v);
+    }
+}
 
 struct Barriers {
     uint64_t q, k_full[2], k_empty[2], v_full[2], v_empty[2], s[2], p[2], o[2], done;
@@ -354,24 +404,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
 #pragma unroll
                 for (int i = 0; i < 32; ++i) s[i] = bits >> i & 1u ? (nan >> i & 1u ? 0x7fc00000u : s[i]) : 0xff800000u;
             };
-            // the tile's largest score
-            float tops[4] = {minus_infinity(), minus_infinity(), minus_infinity(), minus_infinity()};
-            uint32_t ring[2][32];  // one half is loaded while the other is worked on
-            start_load32(s_at, ring[0]);
-#pragma unroll
-            for (int c = 0; c < 128; c += 32) {
-                uint32_t(&s)[32] = ring[c / 32 & 1];
-                wait_tmem_loads(s);
-                start_load32(s_at + (c + 32) % 128, ring[c / 32 & 1 ^ 1]);  // at the end the first again, for the weights
-                if (!whole) mask(c, s);
-#pragma unroll
-                for (int i = 0; i < 32; i += 2)
-                    tops[i / 2 & 3] = fmaxf(tops[i / 2 & 3], fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
-            }
-            float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-            top = top == minus_infinity() ? top : top * f;
+            // The values' exponent first: it is the same for all rows.
             int shift = tile.value_exponent - reference_exponent;
-            float turn = 1.0f;
+            float turn = 1.0f;  // what O has to be multiplied by
             if (j == 0) {
                 reference_exponent = tile.value_exponent;
                 shift = 0;
@@ -381,32 +416,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
                 reference_exponent = tile.value_exponent;
                 shift = 0;
             }
-            if (top > m + kLag || (m == minus_infinity() && top > m)) {
-                const float by = power2(m - top);
-                m = top;
-                l *= by;
-                turn *= by;
-            }
-            if (j > 0 && __any_sync(~0u, turn != 1.0f)) {
-                ok = warp_wait(bar(bars.o, S::NQ == 2 ? x : 0), (j - 1) & 1, kWaitNs);
-                if (!ok) break;
-                tc5::fence_after_sync();
-#pragma unroll 1
-                for (int c = 0; c < WIDTH; c += 32) {
-                    uint32_t v[32], half[16];
-                    tc5::ld32(o_at + c, v);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) half[i] = __float_as_uint(__uint_as_float(v[i]) * turn);
-                    store_tmem16(o_at + c, half);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) half[i] = __float_as_uint(__uint_as_float(v[16 + i]) * turn);
-                    store_tmem16(o_at + c + 16, half);
-                }
-                wait_tmem_stores();
-            }
-            const float offset = (float)shift + kLift - reference(m);
-            const uint64_t ff = pack_pair(f, f), oo = pack_pair(offset, offset);
+            // 32 scores at a time, in one pass: weights by the reference m so far.  Where one exceeds it by more than
+            // 2^kLag, m follows, to a whole number: the weights that are there already change by a power of two.
+            float offset = (float)shift + kLift - reference(m);
+            const uint64_t ff = pack_pair(f, f);
+            uint64_t oo = pack_pair(offset, offset);
             uint64_t sums2[2] = {pack_pair(0.0f, 0.0f), pack_pair(0.0f, 0.0f)};
+            uint32_t ring[2][32];  // one half is loaded while the other is worked on
+            start_load32(s_at, ring[0]);
 #pragma unroll
             for (int c = 0; c < 128; c += 32) {
                 uint32_t w[16], rest[16];
@@ -414,6 +431,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
                 wait_tmem_loads(s);
                 if (c < 96) start_load32(s_at + c + 32, ring[c / 32 & 1 ^ 1]);
                 if (!whole) mask(c, s);
+                float tops[4] = {minus_infinity(), minus_infinity(), minus_infinity(), minus_infinity()};
+#pragma unroll
+                for (int i = 0; i < 32; i += 2)
+                    tops[i / 2 & 3] = fmaxf(tops[i / 2 & 3], fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
+                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * f;
+                const bool follow = top > m + kLag || (m == minus_infinity() && top > m);
+                if (__any_sync(~0u, follow)) {
+                    const float to = follow ? ceilf(top) : m, by = m == to ? 1.0f : power2(m - to);
+                    m = to;
+                    l *= by;
+                    turn *= by;
+                    offset = (float)shift + kLift - reference(m);
+                    oo = pack_pair(offset, offset);
+                    const uint64_t scale2 = pack_pair(by, by);
+                    sums2[0] = mul_pair(sums2[0], scale2);
+                    sums2[1] = mul_pair(sums2[1], scale2);
+                    const uint32_t half = half2_of(by, by);
+                    if (c < 96) wait_tmem_loads(ring[c / 32 & 1 ^ 1]);  // no load is in flight over a call
+#pragma unroll 1
+                    for (int d = 0; d < c; d += 32) follow_weights<REST>(s_at + d, half);
+                }
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
                     float u, v;
@@ -433,6 +471,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             float sum, other;
             unpack_pair(add_pair(sums2[0], sums2[1]), sum, other);
             sum += other;
+            if (j > 0 && __any_sync(~0u, turn != 1.0f)) {
+                ok = warp_wait(bar(bars.o, S::NQ == 2 ? x : 0), (j - 1) & 1, kWaitNs);
+                if (!ok) break;
+                tc5::fence_after_sync();
+#pragma unroll 1
+                for (int c = 0; c < WIDTH; c += 16) {
+                    uint32_t v[16];
+                    load_tmem16(o_at + c, v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * turn);
+                    store_tmem16(o_at + c, v);
+                }
+            }
             l = fmaf(sum, exp2_int(-shift - (int)kLift), l);
             // marks are read before the weights are announced, which keeps their slot: of the tile before this
             // one, whose values were converted long since, and of the last one too
@@ -508,19 +559,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
         const int units = 2 * n;  // K0, K1, V0, K2, V1, ..., V(n - 1)
         const auto is_value = [&](int u) { return u == units - 1 || (u > 0 && u % 2 == 0); };
         const auto tile_of = [&](int u) { return u == units - 1 ? n - 1 : u == 0 ? 0 : u % 2 ? (u + 1) / 2 : u / 2 - 1; };
-        // the row of the keys of the first token of group thread % 8 of tile j, -1 where it has no page
-        const auto row_for = [&](int j) -> int64_t {
+        // the page table's entry for group thread % 8 of tile j, -1 where it has none, and the row of the keys
+        // of the group's first token; an entry is read a tile before it is looked at
+        const auto page_for = [&](int j) {
             const int g = (t0 + j) * 8 + thread;
             if (j >= n || g >= groups.count) return -1;
-            const int token = group_token(groups, g), page = page_of(a.c, a.b, item.sequence, token);
-            return page < 0 ? -1 : cache_row(a.c, page, 0, head, token & (a.c.page_size - 1));
+            const int at = group_token(groups, g) >> a.c.page_shift;
+            return at < a.b.table_pages ? fetch4(a.b.table + item.sequence * a.b.ld_table + at) : -1;
+        };
+        const auto row_for = [&](int j, int page) -> int64_t {
+            return page < 0 || page >= a.c.pages
+                       ? -1
+                       : cache_row(a.c, page, 0, head, group_token(groups, (t0 + j) * 8 + thread) & (a.c.page_size - 1));
         };
         const int64_t to_values = (int64_t)a.c.heads * a.c.page_size;  // rows from a key to its value
-        int64_t held = -1;
+        int held = -1;
         if (thread < 8) {
-            rows[0][thread] = row_for(0);
-            rows[1][thread] = row_for(1);
-            held = row_for(2);
+            const int first_page = page_for(0), second_page = page_for(1);
+            held = page_for(2);
+            rows[0][thread] = row_for(0, first_page);
+            rows[1][thread] = row_for(1, second_page);
         }
         asm volatile("bar.sync 1, %0;" ::"n"(kConverters) : "memory");
         const uint8_t* const code_base = a.c.codes + (t % 16) * (WIDTH / 2) + part * 16;
@@ -538,15 +596,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             for (int i = 0; i < PASSES; ++i) {
                 const int64_t r = rows[j % kRing][i * (S::PER_PASS / 16) + t / 16];
                 if (r >= 0) {
-                    raw.codes[i] = __ldg(reinterpret_cast<const uint4*>(code_base + (r + add) * (WIDTH / 2)));
-                    raw.scales[i] = FMT == kMxfp4 ? (uint16_t)__ldg(scale_base + (r + add) * BLOCKS)
-                                                  : __ldg(reinterpret_cast<const uint16_t*>(scale_base + (r + add) * BLOCKS));
+                    raw.codes[i] = fetch16(code_base + (r + add) * (WIDTH / 2));
+                    raw.scales[i] = FMT == kMxfp4 ? fetch1(scale_base + (r + add) * BLOCKS) : fetch2(scale_base + (r + add) * BLOCKS);
                 }
             }
             if (!value) {
                 const int64_t r = rows[j % kRing][et / 16];
                 exponent = kNoToken;
-                if (r >= 0 && group_token(groups, (t0 + j) * 8 + et / 16) + et % 16 < item.length) exponent = __ldg(exponent_base + r);
+                if (r >= 0 && group_token(groups, (t0 + j) * 8 + et / 16) + et % 16 < item.length) exponent = fetch_signed1(exponent_base + r);
             }
         };
         // where a piece goes: 16-byte pieces in an order that keeps the 8 lanes of a store on different banks
@@ -570,8 +627,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
                 asm volatile("bar.sync 1, %0;" ::"n"(kConverters) : "memory");
                 if (u + 1 < units) load(u + 1, following);
                 if (thread < 8) {  // rows of two tiles on, for loads behind the next barrier
-                    rows[(j + 2) % kRing][thread] = held;
-                    held = row_for(j + 3);
+                    rows[(j + 2) % kRing][thread] = row_for(j + 2, held);
+                    held = page_for(j + 3);
                 }
                 const int4 a0 = *reinterpret_cast<const int4*>(largest[j & 1][0]), a1 = *reinterpret_cast<const int4*>(largest[j & 1][1]);
                 e = key_exponent = max(max(max(a0.x, a0.y), max(a0.z, a0.w)), -127);
@@ -580,15 +637,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
                 value_exponent[0] = u == 0 ? 0 : value_exponent[1];
                 value_exponent[1] = max(max(v, most_seen - kFar), -127);
                 if (u == 0) value_exponent[0] = value_exponent[1];
-                if (thread == 0) {
-                    info[slot].key_factor = mxfp4_scale((uint32_t)(key_exponent + 127)) * exp2_int(-lift_of<FMT>());
-                    info[slot].value_exponent = value_exponent[1];
-                    uint32_t bad = 0;
-#pragma unroll 1
-                    for (int g = 0; g < 8; ++g)
-                        if ((t0 + j) * 8 + g < groups.count && rows[slot][g] < 0) bad |= 1u << g;
-                    info[slot].bad = bad;
-                    mbar_arrive(bar(bars.info, slot));
+                if (thread / 32 == 1) {
+                    const uint32_t bad = __ballot_sync(~0u, lane < 8 && (t0 + j) * 8 + lane < groups.count && rows[slot][lane % 8] < 0);
+                    if (lane == 0) {
+                        info[slot].key_factor = mxfp4_scale((uint32_t)(key_exponent + 127)) * exp2_int(-lift_of<FMT>());
+                        info[slot].value_exponent = value_exponent[1];
+                        info[slot].bad = bad;
+                        mbar_arrive(bar(bars.info, slot));
+                    }
                 }
             } else {
                 if (u + 1 < units) load(u + 1, following);
