@@ -39,7 +39,7 @@ ddgemm_status check_cache(const ddgemm_mx4_cache* c, CacheView& v) {
     if (c == nullptr || !known_format(c->format) || c->pages < 0 || c->heads < 1 || c->head_dim < 1) return DDGEMM_ERR_INVALID_ARG;
     if (c->head_dim > 256 || c->heads > DDGEMM_MAX_HEADS || c->pages >= (1LL << 31)) return DDGEMM_ERR_UNSUPPORTED;
     if (c->page_size < 16 || c->page_size > 65536 || (c->page_size & (c->page_size - 1)) != 0) return DDGEMM_ERR_INVALID_ARG;
-    if (c->pages > (1LL << 50) / (c->page_size * c->heads * 256)) return DDGEMM_ERR_UNSUPPORTED;
+    if (c->pages > ((1LL << 34) - 1) / (c->page_size * c->heads)) return DDGEMM_ERR_UNSUPPORTED;  // 2^35 rows
     if (c->pages > 0 && (c->codes == nullptr || c->scales == nullptr || c->exponents == nullptr || !aligned16(c->codes) ||
                          !aligned16(c->scales) || !aligned16(c->exponents)))
         return DDGEMM_ERR_INVALID_ARG;
@@ -211,7 +211,7 @@ ddgemm_status dd_mx4_attention(const ddgemm_mx4_cache* cache, const ddgemm_batch
     a.vec_out = whole(out, out_token, out_head);
     if (attend_tiles(a.b, a.group, 8) * cache->heads >= (1LL << 31)) return DDGEMM_ERR_UNSUPPORTED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool many = T * a.group > kColumnsMost * batch->batch;
+    const bool many = T * a.group > kColumnsMost * batch->batch && cache->pages > 0;
     a.splits = many ? attend_tile_parts(a) : attend_columns_parts(a);
     Workspace ws(st);
     const int64_t rows = T * q_heads;

@@ -29,14 +29,14 @@ namespace ddg {
 namespace {
 
 constexpr unsigned long long kWaitNs = 2000000000ULL;  // bounded waits: 2 s
-constexpr float kLag = 5.0f;   // references follow when they are exceeded by more than 2^5
+constexpr float kMost = 32768.0f;  // a row's reference follows where 32 weights are more than this in all
 constexpr int kShift = 3;      // ... and the values' exponent by more than 2^3 either way
-constexpr float kLift = 7.0f;  // weights up to 2^(5 + 3 + 7), below the largest float16
+constexpr float kLift = 7.0f;  // the weight of a score equal to the reference is 2^(7 + up to 3 either way)
 constexpr int kFar = 64;       // values' exponents are at most so far below the largest seen
 constexpr int kThreads = 20 * 32;  // the last three warps only give up their registers
 constexpr int kConverters = 256;
 constexpr int kRing = 4;  // tiles whose rows, exponents and marks are kept
-constexpr int kNoToken = -128;  // in the place of an exponent
+constexpr int kNoToken = -4096;  // in the place of an exponent
 
 __device__ unsigned int g_attend_timeouts = 0;
 
@@ -66,15 +66,13 @@ struct TileInfo {
     float key_factor;
     int value_exponent;
     uint32_t bad;  // groups whose page is not there
-    uint32_t any_nan;
-    uint32_t nan[128];  // blocks of a token's values that are NaN
 };
 
 // A thread's pieces of a tile's keys or values.
 template <int PASSES>
 struct Raw {
     uint4 codes[PASSES];
-    uint16_t scales[PASSES];  // not set for a token without a page, whose scale is 0
+    uint16_t scales[PASSES];
 };
 
 __device__ __forceinline__ uint32_t half2_of(float a, float b) {  // a in the low half
@@ -135,11 +133,6 @@ __device__ __forceinline__ int fetch4(const void* p) {
     int v;
     asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
     return v;
-}
-__device__ __forceinline__ void swap(uint32_t& a, uint32_t& b) {
-    const uint32_t t = a;
-    a = b;
-    b = t;
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -217,8 +210,36 @@ __device__ __noinline__ void follow_weights(uint32_t at, uint32_t by) {
 
 struct Barriers {
     uint64_t q, k_full[2], k_empty[2], v_full[2], v_empty[2], s[2], p[2], o[2], done;
-    uint64_t info[kRing], marks[kRing];  // of tiles in turn: what the softmax has to know, and the NaN of its values
+    uint64_t info[kRing];  // of tiles in turn
 };
+
+// NaN in an output row (or its part) for the blocks of values that are NaN in a token
+// of groups g0 .. g1 - 1 that the row sees.
+template <typename T, int WIDTH, int FMT>
+__device__ __noinline__ void mark_nan(const AttendArgs& a, const Item& item, const Groups& groups, int head, int p, int g0, int g1,
+                                      int64_t token, int64_t h) {
+    constexpr int BLOCK = mx4_block(FMT), BLOCKS = WIDTH / BLOCK;
+    uint32_t blocks = 0;
+    for (int g = g0; g < g1; ++g) {
+        const int first = group_token(groups, g), page = page_of(a.c, a.b, item.sequence, first);
+        if (page < 0) continue;
+        const uint8_t* row = a.c.scales + cache_row(a.c, page, 1, head, first & (a.c.page_size - 1)) * BLOCKS;
+        for (int t = 0; t < 16; ++t) {
+            if (!sees(p, first + t, a.window, a.sinks)) continue;
+            for (int b = 0; b < BLOCKS; ++b) {
+                const uint32_t byte = row[t * BLOCKS + b];
+                if (FMT == kMxfp4 ? byte == 255u : (byte & 0x7fu) == 0x7fu) blocks |= 1u << b;
+            }
+        }
+    }
+    const int64_t part = ((int64_t)blockIdx.z * (a.b.tokens * a.heads) + token * a.heads + h) * WIDTH;
+    T* out = static_cast<T*>(a.out) + token * a.ot + h * a.oh;
+    for (int d = 0; d < a.c.dim; ++d) {
+        if (!(blocks >> (d / BLOCK) & 1)) continue;
+        if (a.splits > 1) a.sums[part + d] = not_a_number();
+        else out[d] = from_float<T>(not_a_number());
+    }
+}
 
 template <typename T, int WIDTH, int FMT>
 __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendArgs a) {
@@ -228,8 +249,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
     __shared__ __align__(8) Barriers bars;
     __shared__ uint32_t tmem_slot;
     __shared__ TileInfo info[kRing];
-    __shared__ int64_t rows[kRing][8];  // of groups of keys, -1 where there is no page
-    __shared__ int8_t exponents[kRing][2][128];  // of keys and values
+    __shared__ int rows[kRing][8];  // of groups of keys, in 16s, -1 where there is no page
+    __shared__ int16_t exponents[kRing][2][128];  // of keys and values
+    __shared__ int any_nan;                       // in values
     __shared__ __align__(16) int largest[2][2][4];  // of the tiles in turn
 
     pdl_wait();
@@ -273,9 +295,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(bar(bars.info, i), 1);
-            mbar_init(bar(bars.marks, i), kConverters / 32);
         }
         mbar_init(done, 1);
+        any_nan = 0;
         fence_barrier_init();
     }
     if (warp == 16) {
@@ -351,9 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
         }
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t o_at = tmem + S::O_COL + x * WIDTH + lanes;
-        float m = minus_infinity(), l = 0.0f;
+        float m = p >= 0 ? minus_infinity() : 0.0f, l = 0.0f;
         int reference_exponent = 0;
-        uint32_t poison = 0;
         bool ok = true;
         const int mine = need[x];
         // bits of 32 tokens from the c-th of a tile of groups from g0 on: those that the row sees
@@ -368,22 +389,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
                 if (g < groups.count) bits |= (upto & from & 0xffffu) << (16 * k);
             }
             return bits;
-        };
-        // the blocks of values that are NaN in tokens of tile j that the row sees
-        const auto take_marks = [&](int j) {
-            if (!warp_wait(bar(bars.marks, j % kRing), (j / kRing) & 1, kWaitNs)) return false;
-            const TileInfo& tile = info[j % kRing];
-            if (tile.any_nan != 0) {
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 32) {
-                    const uint32_t bits = seen((t0 + j) * 8, c);
-#pragma unroll 1
-                    for (int t = 0; t < 32; ++t)
-                        if (bits >> t & 1u) poison |= tile.nan[c + t];
-                }
-                __syncwarp();
-            }
-            return true;
         };
         for (int j = 0; j < mine; ++j) {
             const int buffer = S::NQ == 2 ? x : j & 1;
@@ -416,12 +421,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
                 reference_exponent = tile.value_exponent;
                 shift = 0;
             }
-            // 32 scores at a time, in one pass: weights by the reference m so far.  Where one exceeds it by more than
-            // 2^kLag, m follows, to a whole number: the weights that are there already change by a power of two.
-            float offset = (float)shift + kLift - reference(m);
+            // 32 scores at a time, in one pass: weights by the reference m so far.  Where they come out above kMost
+            // (or there is no reference yet), m becomes the largest score, up to a whole number: the weights that are
+            // there already change by a power of two.
+            float offset = (float)shift + kLift - reference(m), sum = 0.0f;
             const uint64_t ff = pack_pair(f, f);
-            uint64_t oo = pack_pair(offset, offset);
-            uint64_t sums2[2] = {pack_pair(0.0f, 0.0f), pack_pair(0.0f, 0.0f)};
             uint32_t ring[2][32];  // one half is loaded while the other is worked on
             start_load32(s_at, ring[0]);
 #pragma unroll
@@ -431,46 +435,49 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
                 wait_tmem_loads(s);
                 if (c < 96) start_load32(s_at + c + 32, ring[c / 32 & 1 ^ 1]);
                 if (!whole) mask(c, s);
-                float tops[4] = {minus_infinity(), minus_infinity(), minus_infinity(), minus_infinity()};
+                float part;
+                const auto weights = [&]() {
+                    const uint64_t oo = pack_pair(offset, offset);
+                    uint64_t sums2[2] = {pack_pair(0.0f, 0.0f), pack_pair(0.0f, 0.0f)};
 #pragma unroll
-                for (int i = 0; i < 32; i += 2)
-                    tops[i / 2 & 3] = fmaxf(tops[i / 2 & 3], fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
-                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * f;
-                const bool follow = top > m + kLag || (m == minus_infinity() && top > m);
-                if (__any_sync(~0u, follow)) {
-                    const float to = follow ? ceilf(top) : m, by = m == to ? 1.0f : power2(m - to);
-                    m = to;
+                    for (int i = 0; i < 32; i += 2) {
+                        float u, v;
+                        unpack_pair(fma_pair(pack_pair(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), ff, oo), u, v);
+                        u = power2(u);
+                        v = power2(v);
+                        sums2[i / 2 & 1] = add_pair(sums2[i / 2 & 1], pack_pair(u, v));
+                        w[i / 2] = half2_of(u, v);
+                        if (REST) {
+                            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&w[i / 2]));
+                            rest[i / 2] = half2_of(u - back.x, v - back.y);
+                        }
+                    }
+                    float other;
+                    unpack_pair(add_pair(sums2[0], sums2[1]), part, other);
+                    part += other;
+                };
+                weights();
+                if (__any_sync(~0u, part > kMost || m == minus_infinity())) {
+                    float tops[4] = {minus_infinity(), minus_infinity(), minus_infinity(), minus_infinity()};
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) tops[i & 3] = fmaxf(tops[i & 3], __uint_as_float(s[i]));
+                    const float top = ceilf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * f);
+                    const float by = top > m ? power2(m - top) : 1.0f;
+                    m = top > m ? top : m;
                     l *= by;
+                    sum *= by;
                     turn *= by;
                     offset = (float)shift + kLift - reference(m);
-                    oo = pack_pair(offset, offset);
-                    const uint64_t scale2 = pack_pair(by, by);
-                    sums2[0] = mul_pair(sums2[0], scale2);
-                    sums2[1] = mul_pair(sums2[1], scale2);
-                    const uint32_t half = half2_of(by, by);
                     if (c < 96) wait_tmem_loads(ring[c / 32 & 1 ^ 1]);  // no load is in flight over a call
+                    const uint32_t half = half2_of(by, by);
 #pragma unroll 1
                     for (int d = 0; d < c; d += 32) follow_weights<REST>(s_at + d, half);
+                    weights();
                 }
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    float u, v;
-                    unpack_pair(fma_pair(pack_pair(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), ff, oo), u, v);
-                    u = power2(u);
-                    v = power2(v);
-                    sums2[i / 2 & 1] = add_pair(sums2[i / 2 & 1], pack_pair(u, v));
-                    w[i / 2] = half2_of(u, v);
-                    if (REST) {
-                        const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&w[i / 2]));
-                        rest[i / 2] = half2_of(u - back.x, v - back.y);
-                    }
-                }
+                sum += part;
                 store_tmem16(s_at + c, w);
                 if (REST) store_tmem16(s_at + c + 16, rest);
             }
-            float sum, other;
-            unpack_pair(add_pair(sums2[0], sums2[1]), sum, other);
-            sum += other;
             if (j > 0 && __any_sync(~0u, turn != 1.0f)) {
                 ok = warp_wait(bar(bars.o, S::NQ == 2 ? x : 0), (j - 1) & 1, kWaitNs);
                 if (!ok) break;
@@ -485,18 +492,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
                 }
             }
             l = fmaf(sum, exp2_int(-shift - (int)kLift), l);
-            // marks are read before the weights are announced, which keeps their slot: of the tile before this
-            // one, whose values were converted long since, and of the last one too
-            if (j > 0) ok = take_marks(j - 1);
-            if (ok && j == mine - 1) ok = take_marks(j);
-            if (!ok) break;
             wait_tmem_stores();
             tc5::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(bars.p, buffer));
         }
         if (ok && mine > 0) {
-            ok = warp_wait(bar(bars.o, S::NQ == 2 ? x : 0), (mine - 1) & 1, kWaitNs);
+            // one phase at a time: with one tile of rows the sum before the last may be under way too
+            if (S::NQ == 1 && mine > 1) ok = warp_wait(bar(bars.o, 0), (mine - 2) & 1, kWaitNs);
+            ok = ok && warp_wait(bar(bars.o, S::NQ == 2 ? x : 0), (mine - 1) & 1, kWaitNs);
             tc5::fence_after_sync();
         }
         if (!ok && lane == 0) atomicAdd(&g_attend_timeouts, 1u);
@@ -515,12 +519,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
                 for (int i = 0; i < 32; ++i) v[i] = 0;
             }
             if (have) {
-                if (poison != 0) {
-                    constexpr int BLOCK = mx4_block(FMT);
-    #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (poison >> ((c + i) / BLOCK) & 1) v[i] = 0x7fc00000u;
-                }
                 if (a.splits > 1) {
                     float4* to = reinterpret_cast<float4*>(a.sums + part * WIDTH + c);
     #pragma unroll
@@ -554,11 +552,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
         else more_registers<S::CONVERT_REGS>();
         constexpr int PIECES = S::PIECES, PASSES = S::PASSES, BLOCK = mx4_block(FMT), BLOCKS = WIDTH / BLOCK;
         const int thread = threadIdx.x - 8 * 32;
-        // in a pass the thread has 32 codes of token t, the part-th of it
-        const int t = thread / PIECES, part = thread % PIECES;
-        const int units = 2 * n;  // K0, K1, V0, K2, V1, ..., V(n - 1)
-        const auto is_value = [&](int u) { return u == units - 1 || (u > 0 && u % 2 == 0); };
-        const auto tile_of = [&](int u) { return u == units - 1 ? n - 1 : u == 0 ? 0 : u % 2 ? (u + 1) / 2 : u / 2 - 1; };
+        // In a pass the thread has 32 codes of token t, the part-th of it.  8 lanes in a row have 4 tokens and
+        // 2 parts: their 16-byte pieces lie on different banks, and a warp's codes are contiguous all the same.
+        constexpr int LOG = PIECES == 2 ? 1 : PIECES == 4 ? 2 : 3;
+        const int part = (lane & 1) | (lane >> 3 & (PIECES / 2 - 1)) << 1;
+        const int t = (thread >> 5) * (32 >> LOG) + ((lane >> 1 & 3) | lane >> (2 + LOG) << 2);
         // the page table's entry for group thread % 8 of tile j, -1 where it has none, and the row of the keys
         // of the group's first token; an entry is read a tile before it is looked at
         const auto page_for = [&](int j) {
@@ -567,12 +565,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             const int at = group_token(groups, g) >> a.c.page_shift;
             return at < a.b.table_pages ? fetch4(a.b.table + item.sequence * a.b.ld_table + at) : -1;
         };
-        const auto row_for = [&](int j, int page) -> int64_t {
+        const auto row_for = [&](int j, int page) {
             return page < 0 || page >= a.c.pages
                        ? -1
-                       : cache_row(a.c, page, 0, head, group_token(groups, (t0 + j) * 8 + thread) & (a.c.page_size - 1));
+                       : (int)(cache_row(a.c, page, 0, head, group_token(groups, (t0 + j) * 8 + thread) & (a.c.page_size - 1)) / 16);
         };
-        const int64_t to_values = (int64_t)a.c.heads * a.c.page_size;  // rows from a key to its value
+        const int to_values = a.c.heads * (a.c.page_size / 16);  // rows from a key to its value, in 16s
         int held = -1;
         if (thread < 8) {
             const int first_page = page_for(0), second_page = page_for(1);
@@ -585,112 +583,57 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
         const uint8_t* const scale_base = a.c.scales + (t % 16) * BLOCKS + part * (32 / BLOCK);
         // of exponents a thread has one: a key's (threads 0 to 127) or a value's
         const int kv = thread / 128, et = thread % 128;
-        const int8_t* const exponent_base = a.c.exponents + (kv ? to_values : 0) + et % 16;
-        Raw<PASSES> even, odd;  // units u and u + 1 in turn: one is loaded while the other is converted
-        int exponent = kNoToken;  // of the next tile
-        const auto load = [&](int u, Raw<PASSES>& raw) {
-            const int j = tile_of(u);
-            const bool value = is_value(u);
-            const int64_t add = value ? to_values : 0;
+        const int8_t* const exponent_base = a.c.exponents + (kv ? (int64_t)to_values * 16 : 0) + et % 16;
+        // tokens of the tiles from t0 on, up to the end of the sequence (only the last group reaches beyond it)
+        const int tokens = groups.count > 0 ? (groups.count - 1) * 16 + min(16, item.length - group_token(groups, groups.count - 1)) - t0 * 128 : 0;
+        Raw<PASSES> keys, values;  // the ones are loaded while the others are converted
+        int exponent = kNoToken;   // of the next tile
+        const auto load = [&](int j, int add, Raw<PASSES>& raw) {
 #pragma unroll
-            for (int i = 0; i < PASSES; ++i) {
-                const int64_t r = rows[j % kRing][i * (S::PER_PASS / 16) + t / 16];
-                if (r >= 0) {
-                    raw.codes[i] = fetch16(code_base + (r + add) * (WIDTH / 2));
-                    raw.scales[i] = FMT == kMxfp4 ? fetch1(scale_base + (r + add) * BLOCKS) : fetch2(scale_base + (r + add) * BLOCKS);
-                }
-            }
-            if (!value) {
-                const int64_t r = rows[j % kRing][et / 16];
-                exponent = kNoToken;
-                if (r >= 0 && group_token(groups, (t0 + j) * 8 + et / 16) + et % 16 < item.length) exponent = fetch_signed1(exponent_base + r);
+            for (int i = 0; i < PASSES; ++i) {  // what is not there is read from the first page: its scale becomes 0
+                const uint32_t r = (uint32_t)(max(rows[j & (kRing - 1)][i * (S::PER_PASS / 16) + t / 16], 0) + add);
+                raw.codes[i] = fetch16(code_base + (uint64_t)r * (16 * WIDTH / 2));
+                raw.scales[i] = FMT == kMxfp4 ? fetch1(scale_base + (uint64_t)r * (16 * BLOCKS)) : fetch2(scale_base + (uint64_t)r * (16 * BLOCKS));
             }
         };
-        // where a piece goes: 16-byte pieces in an order that keeps the 8 lanes of a store on different banks
-        const int turn = PIECES == 2 ? 0 : PIECES == 4 ? part & 2 : part / 2;
-        const uint32_t place = base + part / 2 * S::BLOCK_BYTES + t * 128 + (uint32_t)(((part % 2 * 4) ^ turn ^ (t % 8)) << 4);
+        const auto load_exponent = [&](int j) {
+            const int r = rows[j & (kRing - 1)][et / 16];
+            exponent = kNoToken;
+            if (r >= 0 && j * 128 + et < tokens) exponent = fetch_signed1(exponent_base + (uint64_t)(uint32_t)r * 16);
+        };
+        const uint32_t place = base + part / 2 * S::BLOCK_BYTES + t * 128 + (uint32_t)(((part % 2 * 4) ^ (t % 8)) << 4);
         bool ok = true;
-        int most_seen = kNoToken, key_exponent = 0, value_exponent[2] = {0, 0};  // value_exponent: of the tile at hand and the next
-        const auto convert = [&](int u, Raw<PASSES>& raw, Raw<PASSES>& following) {
-            const int j = tile_of(u), stage = j % S::STAGES, slot = j % kRing;
-            const bool value = is_value(u);
-            int e;
-            // a warp that gave up once goes on without waiting: the others meet it at the barrier
-            ok = ok && warp_wait(bar(value ? bars.v_empty : bars.k_empty, stage), ((j / S::STAGES) & 1) ^ 1, kWaitNs);
-            if (!value) {
-                // the scores of tile j - 2 are there: the softmax has done with tile j - 4, whose slot this is
-                exponents[slot][kv][et] = (int8_t)exponent;
-                const int top = __reduce_max_sync(~0u, exponent);
-                if (lane == 0) largest[j & 1][kv][et / 32] = top;
-                if (thread < 128) info[slot].nan[thread] = 0;
-                if (thread == 0) info[slot].any_nan = 0;
-                asm volatile("bar.sync 1, %0;" ::"n"(kConverters) : "memory");
-                if (u + 1 < units) load(u + 1, following);
-                if (thread < 8) {  // rows of two tiles on, for loads behind the next barrier
-                    rows[(j + 2) % kRing][thread] = row_for(j + 2, held);
-                    held = page_for(j + 3);
-                }
-                const int4 a0 = *reinterpret_cast<const int4*>(largest[j & 1][0]), a1 = *reinterpret_cast<const int4*>(largest[j & 1][1]);
-                e = key_exponent = max(max(max(a0.x, a0.y), max(a0.z, a0.w)), -127);
-                const int v = max(max(a1.x, a1.y), max(a1.z, a1.w));
-                most_seen = max(most_seen, v);
-                value_exponent[0] = u == 0 ? 0 : value_exponent[1];
-                value_exponent[1] = max(max(v, most_seen - kFar), -127);
-                if (u == 0) value_exponent[0] = value_exponent[1];
-                if (thread / 32 == 1) {
-                    const uint32_t bad = __ballot_sync(~0u, lane < 8 && (t0 + j) * 8 + lane < groups.count && rows[slot][lane % 8] < 0);
-                    if (lane == 0) {
-                        info[slot].key_factor = mxfp4_scale((uint32_t)(key_exponent + 127)) * exp2_int(-lift_of<FMT>());
-                        info[slot].value_exponent = value_exponent[1];
-                        info[slot].bad = bad;
-                        mbar_arrive(bar(bars.info, slot));
-                    }
-                }
-            } else {
-                if (u + 1 < units) load(u + 1, following);
-                // K(j + 1) went before V(j), but for the last
-                e = u == units - 1 ? value_exponent[1] : value_exponent[0];
-            }
+        int most_seen = kNoToken, key_exponent = 0, value_exponent = 0, next_value_exponent = 0;
+        const auto convert = [&](int j, bool value, int e, const Raw<PASSES>& raw) {
+            const int stage = j % S::STAGES;
+            const int16_t* const own = exponents[j & (kRing - 1)][value ? 1 : 0];
             const uint32_t to = place + (value ? S::V0 : S::K0) + stage * S::TILE_BYTES;
+            const int add = lift_of<FMT>() - e - (FMT == kMxfp4 ? 127 : 0);
 #pragma unroll
             for (int i = 0; i < PASSES; ++i) {
-                const int at = i * S::PER_PASS + t;
-                const int own = exponents[slot][value ? 1 : 0][at];
+                const int o = own[i * S::PER_PASS + t];
                 uint32_t s[2];
                 if (FMT == kMxfp4) {
-                    const float power = exp2_int(min(max((int)raw.scales[i] - 127 - e + lift_of<kMxfp4>(), -126), 15));
-                    s[0] = s[1] = raw.scales[i] == 255u ? 0x7fff7fffu : half2_of(power, power);
+                    const float power = exp2_int(min(max((int)raw.scales[i] + add, -126), 15));
+                    s[0] = raw.scales[i] == 255u ? 0x7fff7fffu : half2_of(power, power);
+                    if (o == kNoToken) s[0] = 0;
                 } else {
-                    const float lifted = exp2_int(min(max(own - e + lift_of<kNvfp4>(), -126), 15));
-                    const uint32_t power = half2_of(lifted, lifted);
-                    uint32_t h2;
-                    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(raw.scales[i]));
-                    h2 = mul_half2(h2, power);
-                    s[0] = __byte_perm(h2, h2, 0x1010);
-                    s[1] = __byte_perm(h2, h2, 0x3232);
+                    const float power = exp2_int(min(max(o + add, -126), 15));  // 0 as a half where there is no token
+                    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s[0]) : "h"(raw.scales[i]));
+                    if (o == kNoToken) s[0] = 0;
+                    s[0] = mul_half2(s[0], half2_of(power, power));
                 }
-                if (own == kNoToken) s[0] = s[1] = 0;
-                if (value && ((s[0] & 0x7fffu) > 0x7c00u || (s[1] & 0x7fffu) > 0x7c00u)) {  // NaN: 0 here, and a mark
-                    constexpr int PER = 32 / BLOCK;
-                    uint32_t marks = 0;
-#pragma unroll
-                    for (int b = 0; b < PER; ++b)
-                        if ((s[b] & 0x7fffu) > 0x7c00u) marks |= 1u << (part * PER + b);
-                    if ((s[0] & 0x7fffu) > 0x7c00u) s[0] = 0;
-                    if ((s[1] & 0x7fffu) > 0x7c00u) s[1] = 0;
-                    atomicOr(&info[slot].nan[at], marks);
-                    info[slot].any_nan = 1;
+                if (value) {  // NaN: 0 here, and looked for at the end
+                    const __half2 is = __hisnan2(*reinterpret_cast<const __half2*>(&s[0]));
+                    const uint32_t nan = *reinterpret_cast<const uint32_t*>(&is);
+                    if (nan != 0) {
+                        any_nan = 1;
+                        s[0] &= (nan & 0xffffu ? 0u : 0xffffu) | (nan >> 16 ? 0u : 0xffff0000u);
+                    }
                 }
-                uint32_t words[4] = {raw.codes[i].x, raw.codes[i].y, raw.codes[i].z, raw.codes[i].w};
-                if (PIECES > 2 && (turn & 2)) {
-                    swap(words[0], words[2]);
-                    swap(words[1], words[3]);
-                    swap(s[0], s[1]);
-                }
-                if (PIECES > 4 && (turn & 1)) {
-                    swap(words[0], words[1]);
-                    swap(words[2], words[3]);
-                }
+                s[1] = FMT == kMxfp4 ? s[0] : __byte_perm(s[0], s[0], 0x3232);
+                if (FMT == kNvfp4) s[0] = __byte_perm(s[0], s[0], 0x1010);
+                const uint32_t words[4] = {raw.codes[i].x, raw.codes[i].y, raw.codes[i].z, raw.codes[i].w};
 #pragma unroll
                 for (int k0 = 0; k0 < 4; ++k0) {
                     uint4 v = halves_of(words[k0]);
@@ -704,15 +647,61 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             }
             fence_async();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar(value ? bars.v_full : bars.k_full, stage));
-                if (value) mbar_arrive(bar(bars.marks, slot));
-            }
+            if (lane == 0) mbar_arrive(bar(value ? bars.v_full : bars.k_full, stage));
         };
-        if (n > 0) load(0, even);
-        for (int u = 0; u < units; u += 2) {  // an even number of them
-            convert(u, even, odd);
-            convert(u + 1, odd, even);
+        // A warp that gave up a wait once goes on without waiting: the others meet it at the barrier.
+        const auto convert_keys = [&](int j, bool with_values) {
+            const int slot = j & (kRing - 1);
+            ok = ok && warp_wait(bar(bars.k_empty, j % S::STAGES), ((j / S::STAGES) & 1) ^ 1, kWaitNs);
+            // the scores of tile j - 2 are there: the softmax has done with tile j - 4, whose slot this is
+            exponents[slot][kv][et] = (int16_t)exponent;
+            const int top = __reduce_max_sync(~0u, exponent);
+            if (lane == 0) largest[j & 1][kv][et / 32] = top;
+            asm volatile("bar.sync 1, %0;" ::"n"(kConverters) : "memory");
+            if (with_values) load(j - 1, to_values, values);
+            const int4 a0 = *reinterpret_cast<const int4*>(largest[j & 1][0]), a1 = *reinterpret_cast<const int4*>(largest[j & 1][1]);
+            key_exponent = max(max(max(a0.x, a0.y), max(a0.z, a0.w)), -127);
+            const int v = max(max(a1.x, a1.y), max(a1.z, a1.w));
+            most_seen = max(most_seen, v);
+            value_exponent = next_value_exponent;
+            next_value_exponent = max(max(v, most_seen - kFar), -127);
+            if (thread / 32 == 1) {
+                const uint32_t bad = __ballot_sync(~0u, lane < 8 && (t0 + j) * 8 + lane < groups.count && rows[slot][lane % 8] < 0);
+                if (lane == 0) {
+                    info[slot].key_factor = mxfp4_scale((uint32_t)(key_exponent + 127)) * exp2_int(-lift_of<FMT>());
+                    info[slot].value_exponent = next_value_exponent;
+                    info[slot].bad = bad;
+                    mbar_arrive(bar(bars.info, slot));
+                }
+            }
+            if (thread < 8) {  // rows of two tiles on, for loads behind the next barrier
+                rows[(j + 2) & (kRing - 1)][thread] = row_for(j + 2, held);
+                held = page_for(j + 3);
+            }
+            convert(j, false, key_exponent, keys);
+        };
+        if (n > 0) {
+            load(0, 0, keys);
+            load_exponent(0);
+            convert_keys(0, false);
+            if (n > 1) {
+                load(1, 0, keys);
+                load_exponent(1);
+            }
+            for (int j = 0; j < n; ++j) {  // K(j + 1), then V(j)
+                if (j + 1 < n) {
+                    convert_keys(j + 1, true);
+                } else {
+                    load(j, to_values, values);
+                    value_exponent = next_value_exponent;
+                }
+                if (j + 2 < n) {
+                    load(j + 2, 0, keys);
+                    load_exponent(j + 2);
+                }
+                ok = ok && warp_wait(bar(bars.v_empty, j % S::STAGES), ((j / S::STAGES) & 1) ^ 1, kWaitNs);
+                convert(j, true, value_exponent, values);
+            }
         }
         if (!ok && lane == 0) atomicAdd(&g_attend_timeouts, 1u);
     } else if (fewer_registers<S::MMA_REGS>(); warp == 16 && n > 0) {
@@ -813,6 +802,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
     if (warp == 16) {
         __syncwarp();
         tc5::tmem_dealloc(tmem, 512);
+    }
+    // Values that are NaN entered the sums as 0: where there were any, each row looks for those that it sees
+    if (any_nan != 0 && threadIdx.x < 128 * S::NQ && (int)threadIdx.x < item.columns) {
+        const int p = position(threadIdx.x), query = item.column + threadIdx.x;
+        const int64_t token = item.first_token + query / a.group, h = head * a.group + query % a.group;
+        const int x = threadIdx.x / 128;
+        mark_nan<T, WIDTH, FMT>(a, item, groups, head, p, t0 * 8, min(groups.count, (t0 + need[x]) * 8), token, h);
     }
 }
 

@@ -846,7 +846,8 @@ ddgemm_status dd_rotary(int type, int64_t tokens, int64_t heads, int64_t dim, co
  * nvfp4's row exponent (-127 for a row without a finite value other than 0), and for
  * mxfp4 the row's largest scale byte (NaN aside) minus 127, which spares its readers
  * the search.  Rows of the three arrays lie in
- * the order [pages][2: keys, values][heads][page_size].  16-byte aligned.
+ * the order [pages][2: keys, values][heads][page_size].  16-byte aligned; fewer than
+ * 2^34 tokens times heads.
  */
 typedef struct {
     int format;

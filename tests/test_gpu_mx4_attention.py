@@ -282,3 +282,17 @@ def test_a_prompt_and_then_token_by_token(fmt, dim, group):
 def test_no_wait_gave_up():
     """After the calls above (the count is of the process)."""
     assert ddg.wait_timeouts() == 0
+
+
+def test_the_first_call_on_a_cold_cache():
+    """Loads from memory, not from L2: the last tile's values arrive long after its weights."""
+    import torch
+    batch = Batch([(129, 129), (700, 260)], 16)
+    cache, values = filled(batch, 2, 256, "nvfp4")
+    q = queries(batch, 6, 256, "float16")
+    other = torch.empty(300 << 20, dtype=torch.uint8, device="cuda")
+    want = ddg.mx4_attention(q, cache, *batch.dev)
+    check(want, q, batch, values, "float16")
+    for i in range(5):
+        other.fill_(i)
+        assert torch.equal(ddg.mx4_attention(q, cache, *batch.dev), want)
