@@ -51,6 +51,7 @@ struct Shape {
     static constexpr int TILE_BYTES = WIDTH / 64 * BLOCK_BYTES;
     static constexpr int K0 = NQ * TILE_BYTES, V0 = K0 + STAGES * TILE_BYTES;
     static constexpr int SMEM = V0 + STAGES * TILE_BYTES + 1024;
+    static constexpr int BUFFERS = 2 / NQ;                // of scores, of a tile of rows
     static constexpr int PIECES = WIDTH / 32;                     // of 32 codes, of a token
     static constexpr int PER_PASS = kConverters / PIECES;         // tokens that the threads convert at once
     static constexpr int PASSES = 128 / PER_PASS;
@@ -209,7 +210,8 @@ __device__ __noinline__ void follow_weights(uint32_t at, uint32_t by) {
 }
 
 struct Barriers {
-    uint64_t q, k_full[2], k_empty[2], v_full[2], v_empty[2], s[2], p[2], o[2], done;
+    uint64_t q, k_full[2], k_empty[2], v_full[2], v_empty[2], done;
+    uint64_t s[2], p[2], o[2];
     uint64_t info[kRing];  // of tiles in turn
 };
 
@@ -391,10 +393,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             return bits;
         };
         for (int j = 0; j < mine; ++j) {
-            const int buffer = S::NQ == 2 ? x : j & 1;
+            const int buffer = x * S::BUFFERS + j % S::BUFFERS;
             const uint32_t s_at = tmem + S::S_COL + buffer * 128 + lanes;
-            ok = warp_wait(bar(bars.info, j % kRing), (j / kRing) & 1, kWaitNs) &&
-                 warp_wait(bar(bars.s, buffer), (S::NQ == 2 ? j : j >> 1) & 1, kWaitNs);
+            ok = warp_wait(bar(bars.info, j % kRing), (j / kRing) & 1, kWaitNs);
+            ok = ok && warp_wait(bar(bars.s, buffer), (j / S::BUFFERS) & 1, kWaitNs);
             if (!ok) break;
             tc5::fence_after_sync();
             const TileInfo& tile = info[j % kRing];
@@ -478,10 +480,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
                 store_tmem16(s_at + c, w);
                 if (REST) store_tmem16(s_at + c + 16, rest);
             }
-            if (j > 0 && __any_sync(~0u, turn != 1.0f)) {
-                ok = warp_wait(bar(bars.o, S::NQ == 2 ? x : 0), (j - 1) & 1, kWaitNs);
+            // The scores were there after the sum of BUFFERS tiles before.  That of the tile before has to be there too
+            // where O is to change, and of the last tile, so that one phase at most is open behind the loop.
+            const bool change = j > 0 && __any_sync(~0u, turn != 1.0f);
+            if (change || (j > 0 && j == mine - 1)) {
+                ok = warp_wait(bar(bars.o, x), (j - 1) & 1, kWaitNs);
                 if (!ok) break;
                 tc5::fence_after_sync();
+            }
+            if (change) {
 #pragma unroll 1
                 for (int c = 0; c < WIDTH; c += 16) {
                     uint32_t v[16];
@@ -498,9 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             if (lane == 0) mbar_arrive(bar(bars.p, buffer));
         }
         if (ok && mine > 0) {
-            // one phase at a time: with one tile of rows the sum before the last may be under way too
-            if (S::NQ == 1 && mine > 1) ok = warp_wait(bar(bars.o, 0), (mine - 2) & 1, kWaitNs);
-            ok = ok && warp_wait(bar(bars.o, S::NQ == 2 ? x : 0), (mine - 1) & 1, kWaitNs);
+            ok = warp_wait(bar(bars.o, x), (mine - 1) & 1, kWaitNs);
             tc5::fence_after_sync();
         }
         if (!ok && lane == 0) atomicAdd(&g_attend_timeouts, 1u);
@@ -708,8 +713,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
         // ---- MMAs ----
         constexpr uint32_t S_DESC = tc5::idesc_f16(false, false, false, 128, 128);
         constexpr uint32_t O_DESC = tc5::idesc_f16(false, false, true, 128, WIDTH);
-        const auto score = [&](int x, int j, int buffer) {
+        const auto score = [&](int x, int j) {
             if (elect_one()) {
+                const int buffer = x * S::BUFFERS + j % S::BUFFERS;
                 const uint64_t qd = tc5::desc_kmajor_sw128(base + x * S::TILE_BYTES);
                 const uint64_t kd = tc5::desc_kmajor_sw128(base + S::K0 + j % S::STAGES * S::TILE_BYTES);
 #pragma unroll
@@ -721,8 +727,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             }
             __syncwarp();
         };
-        const auto weigh = [&](int x, int j, int buffer) {
+        const auto weigh = [&](int x, int j) {
             if (elect_one()) {
+                const int buffer = x * S::BUFFERS + j % S::BUFFERS;
                 const uint64_t vd = tc5::desc_mnmajor_sw128(base + S::V0 + j % S::STAGES * S::TILE_BYTES, S::BLOCK_BYTES);
                 const uint32_t p_at = tmem + S::S_COL + buffer * 128, o_at = tmem + S::O_COL + x * WIDTH;
 #pragma unroll
@@ -740,53 +747,33 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             __syncwarp();
         };
         const auto keys = [&](int j) { return warp_wait(bar(bars.k_full, j % S::STAGES), (j / S::STAGES) & 1, kWaitNs); };
+        // scores go BUFFERS tiles ahead of the sums
         bool ok = warp_wait(q_full, 0, kWaitNs);
-        if (S::NQ == 2) {
-            if (ok && (ok = keys(0))) {
-                tc5::fence_after_sync();
-                for (int x = 0; x < 2; ++x)
-                    if (need[x] > 0) score(x, 0, x);
-                free_stage(bars.k_empty, 0);
-            }
-            for (int j = 0; j < n && ok; ++j) {
-                ok = warp_wait(bar(bars.v_full, j % S::STAGES), (j / S::STAGES) & 1, kWaitNs);
-                for (int x = 0; x < 2 && ok; ++x) {
-                    if (j < need[x]) {
-                        ok = warp_wait(bar(bars.p, x), j & 1, kWaitNs);
-                        if (!ok) break;
-                        tc5::fence_after_sync();
-                        weigh(x, j, x);
-                    }
-                    if (x == 1) free_stage(bars.v_empty, j);
-                    if (j + 1 < n) {
-                        ok = keys(j + 1);
-                        if (!ok) break;
-                        tc5::fence_after_sync();
-                        if (j + 1 < need[x]) score(x, j + 1, x);
-                        if (x == 1) free_stage(bars.k_empty, j + 1);
-                    }
-                }
-            }
-        } else {
-            for (int j = 0; j < 2 && j < n && ok; ++j) {
-                ok = keys(j);
-                if (!ok) break;
-                tc5::fence_after_sync();
-                score(0, j, j);
-                free_stage(bars.k_empty, j);
-            }
-            for (int j = 0; j < n && ok; ++j) {
-                ok = warp_wait(bar(bars.v_full, j % S::STAGES), (j / S::STAGES) & 1, kWaitNs) && warp_wait(bar(bars.p, j & 1), (j >> 1) & 1, kWaitNs);
-                if (!ok) break;
-                tc5::fence_after_sync();
-                weigh(0, j, j & 1);
-                free_stage(bars.v_empty, j);
-                if (j + 2 < n) {
-                    ok = keys(j + 2);
+        for (int j = 0; j < S::BUFFERS && j < n && ok; ++j) {
+            ok = keys(j);
+            if (!ok) break;
+            tc5::fence_after_sync();
+            for (int x = 0; x < S::NQ; ++x)
+                if (j < need[x]) score(x, j);
+            free_stage(bars.k_empty, j);
+        }
+        for (int j = 0; j < n && ok; ++j) {
+            const int ahead = j + S::BUFFERS;
+            ok = warp_wait(bar(bars.v_full, j % S::STAGES), (j / S::STAGES) & 1, kWaitNs);
+            for (int x = 0; x < S::NQ && ok; ++x) {
+                if (j < need[x]) {
+                    ok = warp_wait(bar(bars.p, x * S::BUFFERS + j % S::BUFFERS), (j / S::BUFFERS) & 1, kWaitNs);
                     if (!ok) break;
                     tc5::fence_after_sync();
-                    score(0, j + 2, j & 1);
-                    free_stage(bars.k_empty, j + 2);
+                    weigh(x, j);
+                }
+                if (x == S::NQ - 1) free_stage(bars.v_empty, j);
+                if (ahead < n) {
+                    ok = keys(ahead);
+                    if (!ok) break;
+                    tc5::fence_after_sync();
+                    if (ahead < need[x]) score(x, ahead);
+                    if (x == S::NQ - 1) free_stage(bars.k_empty, ahead);
                 }
             }
         }
