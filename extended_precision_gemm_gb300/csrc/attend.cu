@@ -17,7 +17,9 @@
 // Weights are rounded to 16 bits (11 significant) for bfloat16 outputs, and what that
 // leaves enters the sum too for float16 ones, whose own rounding is as small.
 #include <algorithm>
+#include <atomic>
 
+#include "async_copy.cuh"
 #include "attend.cuh"
 
 namespace ddg {
@@ -83,385 +85,537 @@ __device__ __forceinline__ void static_for(F f) {
     }
 }
 
-template <int N>  // N words, aligned to their size up to 16 bytes
+template <int N>  // N words of shared memory, aligned to their size up to 16 bytes
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
     if constexpr (N == 1) {
-        asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
     } else if constexpr (N == 2) {
-        asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x, w[1] = v.y;
     } else {
 #pragma unroll
-        for (int i = 0; i < N; i += 4)
-            asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                         : "l"(p + 4 * i));
+        for (int i = 0; i < N; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
+            w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+        }
     }
 }
+__device__ __forceinline__ void copy16(uint32_t to, const uint8_t* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void close_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// What a lane (r, c) = (lane / 4, lane % 4) reads of a group of 16 tokens: of keys,
-// a quarter c of tokens 2 r and 2 r + 1; of values, the eighth r of tokens 4 c .. 4 c + 3.
-// Row i of the score fragment is token 2 (i % 8) + i / 8, so that both halves agree
-// on the four tokens of a lane.
+// A group of 16 tokens on its way: a warp copies it to shared memory kAhead groups
+// ahead, and a lane (r, c) = (lane / 4, lane % 4) reads of keys a quarter c of tokens r
+// and r + 8, of values the eighth r of tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9.  Two
+// tokens' values are followed by 32 bytes of nothing: their readers are on different
+// banks then.
+constexpr int kStages = 4, kAhead = kStages - 1;
 template <int WIDTH, int FMT>
-struct Group16 {
+struct Stage {
     static constexpr int KW = WIDTH / 32, VW = WIDTH / 64;                 // words of codes of a token
     static constexpr int BLOCK = mx4_block(FMT), BLOCKS = WIDTH / BLOCK;
     static constexpr int KB = WIDTH / 4 / BLOCK > 0 ? WIDTH / 4 / BLOCK : 1;  // blocks a lane's codes touch
     static constexpr int VB = WIDTH / 8 / BLOCK > 0 ? WIDTH / 8 / BLOCK : 1;
-    uint32_t k[2][KW], v[4][VW];
-    uint8_t ks[2][KB], vs[4][VB];
-    uint16_t ke;   // the two keys' exponents
-    uint16_t vr;   // the two values' exponents of tokens 2 r, 2 r + 1
-    uint32_t ve;   // the four values' (mxfp4)
-    bool bad;      // no such page
+    static constexpr int ROW = WIDTH / 2;                                  // bytes of codes
+    static constexpr int V0 = 16 * ROW, S0 = V0 + 16 * ROW + 8 * 32;       // values' codes, scales of keys and values
+    static constexpr int E0 = S0 + 32 * BLOCKS, BYTES = E0 + 32;           // exponents of keys and values
+    static constexpr int PIECES = 2 * BLOCKS + 2;                          // of scales and exponents, 16 bytes each
 
-    __device__ __forceinline__ void load(const CacheView& c, int page, int head, int offset, int lane) {
-        bad = page < 0;
-        if (bad) {
+    // The lane's places in the first group of 16 rows of the cache.
+    struct Base {
+        const uint8_t *k, *v, *small[(PIECES + 31) / 32];
+        uint32_t small_stride[(PIECES + 31) / 32];  // of a group of rows
+    };
+    static __device__ __forceinline__ Base base_of(const CacheView& c, int lane) {
+        Base b;
+        const int64_t values = (int64_t)c.heads * (c.page_size / 16);  // from a key to its value, in groups of 16 rows
+        b.k = c.codes + lane * 16;
+        b.v = b.k + values * (16 * ROW);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                for (int i = 0; i < KW; ++i) k[t][i] = 0;
-#pragma unroll
-                for (int i = 0; i < KB; ++i) ks[t][i] = 0;
-            }
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-#pragma unroll
-                for (int i = 0; i < VW; ++i) v[t][i] = 0;
-#pragma unroll
-                for (int i = 0; i < VB; ++i) vs[t][i] = 0;
-            }
-            ke = vr = 0;
-            ve = 0;
-            return;
+        for (int i = 0; i < (PIECES + 31) / 32; ++i) {
+            const int piece = lane + 32 * i;
+            const bool exponent = piece >= 2 * BLOCKS;
+            const int kv = exponent ? piece - 2 * BLOCKS : piece / BLOCKS;
+            b.small_stride[i] = exponent ? 16 : 16 * BLOCKS;
+            b.small[i] = (exponent ? reinterpret_cast<const uint8_t*>(c.exponents) : c.scales + piece % BLOCKS * 16) + (kv ? values * b.small_stride[i] : 0);
         }
-        const int r = lane / 4, q = lane % 4;
-        const int64_t krow = cache_row(c, page, 0, head, offset), vrow = cache_row(c, page, 1, head, offset);
-        const uint8_t* kc = c.codes + (krow + 2 * r) * (WIDTH / 2) + q * (WIDTH / 8);
-        const uint8_t* vc = c.codes + (vrow + 4 * q) * (WIDTH / 2) + r * (WIDTH / 16);
+        return b;
+    }
+    // row: of the group's keys, in 16s; negative: no page, nothing is copied.
+    static __device__ __forceinline__ void copy(const Base& b, int row, uint32_t to, int lane) {
+        if (row >= 0) {
+            const uint8_t *k = b.k + (uint64_t)(uint32_t)row * (16 * ROW), *v = b.v + (uint64_t)(uint32_t)row * (16 * ROW);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) load_words<KW>(kc + t * (WIDTH / 2), k[t]);
+            for (int i = 0; i < 16 * ROW / 512; ++i) {
+                const int at = i * 512 + lane * 16;
+                copy16(to + at, k + i * 512);
+                copy16(to + V0 + at + at / (2 * ROW) * 32, v + i * 512);
+            }
 #pragma unroll
-        for (int t = 0; t < 4; ++t) load_words<VW>(vc + t * (WIDTH / 2), v[t]);
-        const uint8_t* ksp = c.scales + (krow + 2 * r) * BLOCKS + q * (WIDTH / 4) / BLOCK;
-        const uint8_t* vsp = c.scales + (vrow + 4 * q) * BLOCKS + r * (WIDTH / 8) / BLOCK;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int i = 0; i < KB; ++i) ks[t][i] = __ldg(ksp + t * BLOCKS + i);
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int i = 0; i < VB; ++i) vs[t][i] = __ldg(vsp + t * BLOCKS + i);
-        ke = __ldg(reinterpret_cast<const uint16_t*>(c.exponents + krow) + r);
-        vr = __ldg(reinterpret_cast<const uint16_t*>(c.exponents + vrow) + r);
-        if (FMT == kMxfp4) ve = __ldg(reinterpret_cast<const uint32_t*>(c.exponents + vrow) + q);
+            for (int i = 0; i < (PIECES + 31) / 32; ++i)
+                if (lane + 32 * i < PIECES) copy16(to + S0 + (lane + 32 * i) * 16, b.small[i] + (uint64_t)(uint32_t)row * b.small_stride[i]);
+        }
+        close_copies();
     }
 };
 
-__device__ __forceinline__ int signed_byte(uint32_t w, int i) { return (int)(int8_t)(uint8_t)(w >> (8 * i)); }
+// N scale bytes of a row with exponent e as halves.
+template <int FMT, int N>
+__device__ __forceinline__ void half_scales(const uint8_t* bytes, int e, uint32_t (&h)[N]) {
+#pragma unroll
+    for (int b = 0; b < N; b += 2) {
+        const uint16_t two = N == 1 ? (uint16_t)bytes[0] : *reinterpret_cast<const uint16_t*>(bytes + b);
+        if (FMT == kNvfp4) {
+            uint32_t h2;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(two));
+            h[b] = h2;  // the low half counts
+            if (b + 1 < N) h[b + 1] = h2 >> 16;
+        } else {
+            h[b] = half_scale<kMxfp4>(two & 0xffu, e);
+            if (b + 1 < N) h[b + 1] = half_scale<kMxfp4>(two >> 8, e);
+        }
+    }
+}
+__device__ __forceinline__ uint32_t both_low(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
 
-// One block: a tile of 8 columns and a share of its groups, dealt out to the warps
-// in turn.
+// ---- how the work is dealt out ----
+//
+// An item is a tile of 8 columns of a sequence with one key/value head; its cost is
+// the number of its groups of 16 tokens (at least one).  The items of all sequences in
+// turn, their groups one after the other, are cut into equal runs, one for each CTA,
+// so that lengths do not matter.  An item that one CTA does as a whole is written by
+// it; of a cut one each CTA leaves a part: the one that begins it in its second slot,
+// the others in their first.
+struct Cut {
+    int64_t total;   // groups of all items
+    int64_t ctas;    // that work: at least kLeast groups each
+    __device__ __forceinline__ int64_t first(int64_t cta) const { return total * cta / ctas; }
+    // the CTA that has group g
+    __device__ __forceinline__ int64_t owner(int64_t g) const { return ((g + 1) * ctas - 1) / total; }
+};
+constexpr int kLeast = 8;
+__device__ __forceinline__ Cut cut_of(int64_t total, int ctas) {
+    return Cut{total, max((int64_t)1, min((int64_t)ctas, total / kLeast))};
+}
+
+struct Sequence {
+    int first_token, tokens, length;
+};
+__device__ __forceinline__ Sequence sequence_at(const BatchView& b, int i) {
+    const int s0 = b.starts[i], s1 = b.starts[i + 1];
+    if (s0 < 0 || s1 > b.tokens || s1 <= s0) return Sequence{0, 0, 0};
+    return Sequence{s0, s1 - s0, b.lengths[i]};
+}
+// The groups of tile `ct` of 8 columns, and (with count at least 1) its cost.
+__device__ __forceinline__ Groups tile_groups(const AttendArgs& a, const Sequence& s, int ct) {
+    const int before = s.length - s.tokens;
+    const int64_t last = min((int64_t)s.tokens * a.group, (int64_t)(ct + 1) * 8) - 1;
+    Groups g = groups_of(a.c, a.b, before + (int)((int64_t)ct * 8 / a.group), before + (int)(last / a.group), a.window, a.sinks);
+    g.count = max(g.count, 1);
+    return g;
+}
+__device__ __forceinline__ int tiles_of(const AttendArgs& a, const Sequence& s) { return (int)(((int64_t)s.tokens * a.group + 7) / 8); }
+__device__ __forceinline__ int64_t cost_of(const AttendArgs& a, const Sequence& s) {
+    int64_t n = 0;
+    for (int ct = 0; ct < tiles_of(a, s); ++ct) n += tile_groups(a, s, ct).count;
+    return n;
+}
+
+// One CTA: its run of groups, item by item; of an item's groups the warps take one after
+// the other in turn.
 template <typename T, int WIDTH, int FMT>
-__global__ void __launch_bounds__(kWarps * 32) attend_columns_kernel(const AttendArgs a) {
-    using G = Group16<WIDTH, FMT>;
+__global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : 4) attend_columns_kernel(const AttendArgs a) {
+    using G = Stage<WIDTH, FMT>;
     constexpr int KS = WIDTH / 16;  // MMAs along the head
-    constexpr bool REST = sizeof(T) == 2 && std::is_same_v<T, __half>;
+    constexpr bool REST = std::is_same_v<T, __half>;
     constexpr int ROW = WIDTH + 4;  // a column's sums in shared memory
-    extern __shared__ __align__(16) float sums[];  // [warp][8][ROW]
+    extern __shared__ __align__(16) uint8_t shared[];  // [warp][stage], and [warp][8][ROW] floats behind an item's last group
+    float* const sums = reinterpret_cast<float*>(shared);
     __shared__ float s_m[kWarps][8], s_M[kWarps][8], s_l[kWarps][8];
+    __shared__ int64_t scan[kWarps];
+    __shared__ int64_t found_before;
+    __shared__ int found;
+    __shared__ Sequence found_sequence;
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane / 4, c = lane % 4;
-    const int head = blockIdx.y;
-    const Item item = item_of(a.b, blockIdx.x, a.group, 8);
-    if (item.sequence < 0) return;
-    const int before = item.length - item.tokens;  // the position of the first query token
-    const int p0 = before + item.column / a.group, p1 = before + (item.column + item.columns - 1) / a.group;
-    const Groups groups = groups_of(a.c, a.b, p0, p1, a.window, a.sinks);
-    const int g0 = (int)((int64_t)groups.count * blockIdx.z / a.splits);
-    const int g1 = (int)((int64_t)groups.count * (blockIdx.z + 1) / a.splits);
 
-    // the queries: column r, elements c WIDTH / 4 .. of it
-    uint32_t q[KS][2];
-    float qf = a.scale;  // what a score is to be multiplied by
+    // the whole cost, and the sequence in which this CTA's run begins
+    int64_t run, run_end, start;  // run: groups from the item's first on; start: of the sequence's
+    int b;
     {
-        const bool have = r < item.columns;
-        const int col = item.column + r;
-        const T* src = static_cast<const T*>(a.q) + (int64_t)(item.first_token + (have ? col / a.group : 0)) * a.qt +
-                       (int64_t)(head * a.group + (have ? col % a.group : 0)) * a.qh;
-        const int d0 = c * (WIDTH / 4);
-        float x[WIDTH / 4];
-        if (have && a.vec_q && d0 + WIDTH / 4 <= a.c.dim) {
-#pragma unroll
-            for (int i = 0; i < WIDTH / 4; i += 8) {
-                const uint4 raw = *reinterpret_cast<const uint4*>(src + d0 + i);
-                const T* t = reinterpret_cast<const T*>(&raw);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[i + j] = to_float<T>(t[j]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < WIDTH / 4; ++i) x[i] = have && d0 + i < a.c.dim ? to_float<T>(src[d0 + i]) : 0.0f;
+        const int per = (a.b.batch + kWarps * 32 - 1) / (kWarps * 32), b0 = min((int)threadIdx.x * per, a.b.batch), b1 = min(b0 + per, a.b.batch);
+        int64_t mine = 0;
+        Sequence own{0, 0, 0};
+        for (int i = b0; i < b1; ++i) {
+            own = sequence_at(a.b, i);
+            mine += cost_of(a, own);
         }
-        if (!REST) {  // bfloat16: the row's largest to [2^11, 2^12)
-            uint32_t most = 0;
+        int64_t upto = mine;
 #pragma unroll
-            for (int i = 0; i < WIDTH / 4; ++i) {
-                const uint32_t bits = __float_as_uint(x[i]) & 0x7fffffffu;
-                most = max(most, bits < kInfBits ? bits : 0u);
-            }
-            most = max(most, __shfl_xor_sync(~0u, most, 1));
-            most = max(most, __shfl_xor_sync(~0u, most, 2));
-            const int e = max((int)(most >> 23) - 127 - 11, -126);
-            const float2 up = exp2_factors(-e), down = exp2_factors(e);
-#pragma unroll
-            for (int i = 0; i < WIDTH / 4; ++i) x[i] = x[i] * up.x * up.y;
-            qf = qf * down.x * down.y;
+        for (int d = 1; d < 32; d *= 2) {
+            const int64_t v = __shfl_up_sync(~0u, upto, d);
+            if (lane >= d) upto += v;
         }
-#pragma unroll
-        for (int j = 0; j < KS; ++j) {
-            q[j][0] = half2_of(x[4 * j], x[4 * j + 1]);
-            q[j][1] = half2_of(x[4 * j + 2], x[4 * j + 3]);
-        }
-        if (FMT == kMxfp4) qf *= exp2_int(-kMxLift);
-    }
-    // this lane's columns in the fragments are 2 c and 2 c + 1
-    const float qf0 = __shfl_sync(~0u, qf, 8 * c), qf1 = __shfl_sync(~0u, qf, 8 * c + 4);
-    const int pa = 2 * c < item.columns ? before + (item.column + 2 * c) / a.group : -1;
-    const int pb = 2 * c + 1 < item.columns ? before + (item.column + 2 * c + 1) / a.group : -1;
-
-    float o[KS][4];
-#pragma unroll
-    for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    float ma = minus_infinity(), mb = ma, Ma = ma, Mb = ma, la = 0.0f, lb = 0.0f;
-
-    const int mine = g1 - g0 > warp ? (g1 - g0 - warp + kWarps - 1) / kWarps : 0;
-    int pages = -1, base = 0;  // pages of 32 rounds, a lane each
-    auto page_at = [&](int i) {
-        if (i % 32 == 0) {
-            base = i;
-            pages = i + lane < mine ? page_of(a.c, a.b, item.sequence, group_token(groups, g0 + warp + (i + lane) * kWarps)) : -1;
-        }
-        return __shfl_sync(~0u, pages, i - base);
-    };
-    G now, next;
-    if (mine > 0) now.load(a.c, page_at(0), head, group_token(groups, g0 + warp) & (a.c.page_size - 1), lane);
-    for (int i = 0; i < mine; ++i) {
-        const int token = group_token(groups, g0 + warp + i * kWarps);
-        if (i + 1 < mine)
-            next.load(a.c, page_at(i + 1), head, group_token(groups, g0 + warp + (i + 1) * kWarps) & (a.c.page_size - 1), lane);
-
-        // scores
-        uint32_t ks[2][G::KB];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int b = 0; b < G::KB; ++b) ks[t][b] = half_scale<FMT>(now.ks[t][b], signed_byte(now.ke, t)) * 0x10001u;
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        constexpr int PER = KS / G::KB;  // MMAs of a block of a lane's codes
-        auto score_step = [&](auto J) {
-            constexpr int j = decltype(J)::value;
-            const uint32_t x = ks[0][j / PER], y = ks[1][j / PER];
-            constexpr int w = j / 2, lo = j % 2 * 2;
-            mma16816(s, mul_half2(codes2<lo>(now.k[0][w]), x), mul_half2(codes2<lo>(now.k[1][w]), y),
-                     mul_half2(codes2<lo + 1>(now.k[0][w]), x), mul_half2(codes2<lo + 1>(now.k[1][w]), y), q[j][0], q[j][1]);
-        };
-        static_for<KS>(score_step);
-        const float k0 = now.bad ? not_a_number() : mxfp4_scale(signed_byte(now.ke, 0) + 127),
-                    k1 = now.bad ? not_a_number() : mxfp4_scale(signed_byte(now.ke, 1) + 127);
-        s[0] = s[0] * qf0 * k0;
-        s[1] = s[1] * qf1 * k0;
-        s[2] = s[2] * qf0 * k1;
-        s[3] = s[3] * qf1 * k1;
-        const bool whole = token + 15 <= p0 && (a.window == 0 || token > p1 - a.window);
-        const int t0 = token + 2 * r;
-        if (!whole) {
-            if (!sees(pa, t0, a.window, a.sinks)) s[0] = minus_infinity();
-            if (!sees(pb, t0, a.window, a.sinks)) s[1] = minus_infinity();
-            if (!sees(pa, t0 + 1, a.window, a.sinks)) s[2] = minus_infinity();
-            if (!sees(pb, t0 + 1, a.window, a.sinks)) s[3] = minus_infinity();
-        }
-        const float e0 = (float)signed_byte(now.vr, 0), e1 = (float)signed_byte(now.vr, 1);
-        float u[4] = {s[0] + e0, s[1] + e0, s[2] + e1, s[3] + e1};
-        const float sa = fmaxf(s[0], s[2]), sb = fmaxf(s[1], s[3]), ua = fmaxf(u[0], u[2]), ub = fmaxf(u[1], u[3]);
-        if (__any_sync(~0u, sa > ma + kLag || sb > mb + kLag || ua > Ma + kLag || ub > Mb + kLag)) {
-            float na = sa, nb = sb, Na = ua, Nb = ub;
-#pragma unroll
-            for (int d = 4; d < 32; d *= 2) {
-                na = fmaxf(na, __shfl_xor_sync(~0u, na, d));
-                nb = fmaxf(nb, __shfl_xor_sync(~0u, nb, d));
-                Na = fmaxf(Na, __shfl_xor_sync(~0u, Na, d));
-                Nb = fmaxf(Nb, __shfl_xor_sync(~0u, Nb, d));
-            }
-            na = fmaxf(ma, na);
-            nb = fmaxf(mb, nb);
-            Na = fmaxf(Ma, Na);
-            Nb = fmaxf(Mb, Nb);
-            la *= power2(ma - reference(na));
-            lb *= power2(mb - reference(nb));
-            const float fa = power2(Ma - reference(Na)), fb = power2(Mb - reference(Nb));
-#pragma unroll
-            for (int d = 0; d < KS; ++d) {
-                o[d][0] *= fa;
-                o[d][1] *= fb;
-                o[d][2] *= fa;
-                o[d][3] *= fb;
-            }
-            ma = na, mb = nb, Ma = Na, Mb = Nb;
-        }
-        const float ra = reference(ma), rb = reference(mb), Ra = reference(Ma) - kLift, Rb = reference(Mb) - kLift;
-        la += power2(s[0] - ra) + power2(s[2] - ra);
-        lb += power2(s[1] - rb) + power2(s[3] - rb);
-#pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-            u[i] = power2(u[i] - Ra);
-            u[i + 1] = power2(u[i + 1] - Rb);
-        }
-        const uint32_t h0 = half2_of(u[0], u[1]), h1 = half2_of(u[2], u[3]);
-        const uint32_t w0 = transpose8x8(h0), w1 = transpose8x8(h1);
-        uint32_t x0 = 0, x1 = 0;
-        if (REST) {
-            x0 = transpose8x8(half2_of(u[0] - low_half(h0), u[1] - high_half(h0)));
-            x1 = transpose8x8(half2_of(u[2] - low_half(h1), u[3] - high_half(h1)));
-        }
-
-        // values: tokens 4 c, 4 c + 2 (rows 2 c, 2 c + 1) and 4 c + 1, 4 c + 3 (rows 2 c + 8, 2 c + 9)
-        uint32_t vs[2][G::VB];
-#pragma unroll
-        for (int b = 0; b < G::VB; ++b) {
-            uint32_t h[4];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) h[t] = half_scale<FMT>(now.vs[t][b], signed_byte(now.ve, t));
-            if (!whole) {
-                // a NaN reaches only the columns that see its token
-                uint32_t nan = 0;
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    if (half_is_nan(h[t])) {
-                        nan |= 1u << t;
-                        h[t] = 0;
-                    }
-                }
-                if (__any_sync(~0u, nan != 0)) {
-#pragma unroll 1
-                    for (int cc = 0; cc < 4; ++cc) {
-                        const uint32_t theirs = __shfl_sync(~0u, nan, (lane & ~3) | cc);
-#pragma unroll 1
-                        for (int t = 0; t < 4; ++t) {
-                            if (!(theirs >> t & 1)) continue;
-                            const bool hit_a = sees(pa, token + 4 * cc + t, a.window, a.sinks);
-                            const bool hit_b = sees(pb, token + 4 * cc + t, a.window, a.sinks);
-                            constexpr int SPAN = KS / G::VB;
-#pragma unroll
-                            for (int d = b * SPAN; d < (b + 1) * SPAN; ++d) {
-                                if (hit_a) o[d][0] = o[d][2] = not_a_number();
-                                if (hit_b) o[d][1] = o[d][3] = not_a_number();
-                            }
-                        }
-                    }
-                }
-            }
-            vs[0][b] = h[0] | h[2] << 16;
-            vs[1][b] = h[1] | h[3] << 16;
-        }
-        auto value_word = [&](auto W) {
-            constexpr int w = decltype(W)::value;
-            // bytes of (token, token + 2): even elements in xe, odd ones in xo
-            const uint32_t m = 0x0f0f0f0fu;
-            const uint32_t xe = (now.v[0][w] & m) | (now.v[2][w] << 4 & ~m), xo = (now.v[0][w] >> 4 & m) | (now.v[2][w] & ~m);
-            const uint32_t ye = (now.v[1][w] & m) | (now.v[3][w] << 4 & ~m), yo = (now.v[1][w] >> 4 & m) | (now.v[3][w] & ~m);
-            auto tile = [&](auto I) {
-                constexpr int i = decltype(I)::value, d = w * 4 + i;
-                constexpr int b = d / (KS / G::VB);
-                const uint32_t a0 = mul_half2(codes2<i>(xe), vs[0][b]), a1 = mul_half2(codes2<i>(xo), vs[0][b]);
-                const uint32_t a2 = mul_half2(codes2<i>(ye), vs[1][b]), a3 = mul_half2(codes2<i>(yo), vs[1][b]);
-                mma16816(o[d], a0, a1, a2, a3, w0, w1);
-                if (REST) mma16816(o[d], a0, a1, a2, a3, x0, x1);
-            };
-            static_for<4>(tile);
-        };
-        static_for<G::VW>(value_word);
-        now = next;
-    }
-
-    // the warps' parts
-#pragma unroll
-    for (int d = 4; d < 32; d *= 2) {
-        la += __shfl_xor_sync(~0u, la, d);
-        lb += __shfl_xor_sync(~0u, lb, d);
-    }
-    if (r == 0) {
-        s_m[warp][2 * c] = ma;
-        s_m[warp][2 * c + 1] = mb;
-        s_M[warp][2 * c] = Ma;
-        s_M[warp][2 * c + 1] = Mb;
-        s_l[warp][2 * c] = la;
-        s_l[warp][2 * c + 1] = lb;
-    }
-    {
-        float* mine_a = sums + (warp * 8 + 2 * c) * ROW + r * (WIDTH / 8);
-        float* mine_b = mine_a + ROW;
-#pragma unroll
-        for (int d = 0; d < KS; ++d) {
-            *reinterpret_cast<float2*>(mine_a + 2 * d) = make_float2(o[d][0], o[d][2]);
-            *reinterpret_cast<float2*>(mine_b + 2 * d) = make_float2(o[d][1], o[d][3]);
-        }
-    }
-    __syncthreads();
-    constexpr int LANES = kWarps * 32 / 8;  // threads of a column
-    const int col = threadIdx.x / LANES, at = threadIdx.x % LANES;
-    if (col >= item.columns) return;
-    float m = s_m[0][col], M = s_M[0][col];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
-        m = fmaxf(m, s_m[w][col]);
-        M = fmaxf(M, s_M[w][col]);
-    }
-    float l = 0.0f, f[kWarps];
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        l += s_l[w][col] * power2(s_m[w][col] - reference(m));
-        f[w] = power2(s_M[w][col] - reference(M));
-    }
-    const int64_t token = item.first_token + (item.column + col) / a.group, h = head * a.group + (item.column + col) % a.group;
-    const int64_t row = token * a.heads + h;
-    const bool any = before + (item.column + col) / a.group >= 0;
-    if (a.splits > 1) {
-        const int64_t part = blockIdx.z * (a.b.tokens * a.heads) + row;
-        if (at == 0) a.part[part] = make_float4(m, M, l, any ? 1.0f : 0.0f);
-#pragma unroll
-        for (int d = at * 4; d < WIDTH; d += LANES * 4) {
-            float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float4 x = *reinterpret_cast<const float4*>(sums + (w * 8 + col) * ROW + d);
-                y.x = fmaf(x.x, f[w], y.x);
-                y.y = fmaf(x.y, f[w], y.y);
-                y.z = fmaf(x.z, f[w], y.z);
-                y.w = fmaf(x.w, f[w], y.w);
-            }
-            *reinterpret_cast<float4*>(a.sums + part * WIDTH + d) = y;
-        }
-        return;
-    }
-    const Finish z = finish_of(m, M, l, kLift + (FMT == kMxfp4 ? kMxLift : 0), any);
-    T* out = static_cast<T*>(a.out) + token * a.ot + h * a.oh;
-#pragma unroll
-    for (int d = at * 4; d < WIDTH; d += LANES * 4) {
-        float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (lane == 31) scan[warp] = upto;
+        __syncthreads();
+        int64_t before = upto - mine, total = 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float4 x = *reinterpret_cast<const float4*>(sums + (w * 8 + col) * ROW + d);
-            y[0] = fmaf(x.x, f[w], y[0]);
-            y[1] = fmaf(x.y, f[w], y[1]);
-            y[2] = fmaf(x.z, f[w], y[2]);
-            y[3] = fmaf(x.w, f[w], y[3]);
+            if (w < warp) before += scan[w];
+            total += scan[w];
         }
-        store4(out, d, a.c.dim, a.vec_out, z, y);
+        total *= a.c.heads;
+        const Cut cut = cut_of(total, a.splits);
+        if (total == 0 || blockIdx.x >= cut.ctas) return;
+        run = cut.first(blockIdx.x);
+        run_end = cut.first(blockIdx.x + 1);
+        int64_t at = before * a.c.heads;
+        for (int i = b0; i < b1; ++i) {
+            if (per > 1) own = sequence_at(a.b, i);
+            const int64_t cost = (per > 1 ? cost_of(a, own) : mine) * a.c.heads;
+            if (run >= at && run < at + cost) {
+                found = i;
+                found_before = at;
+                found_sequence = own;
+            }
+            at += cost;
+        }
+        __syncthreads();
+        b = found;
+        start = found_before;
+    }
+    Sequence seq = found_sequence;
+    int ct = 0, head;
+    Groups groups = tile_groups(a, seq, 0);
+    while (run >= start + (int64_t)groups.count * a.c.heads) {
+        start += (int64_t)groups.count * a.c.heads;
+        groups = tile_groups(a, seq, ++ct);
+    }
+    head = (int)((run - start) / groups.count);
+    int g0 = (int)((run - start) % groups.count);
+    const typename G::Base base = G::base_of(a.c, lane);
+    constexpr float kSumLift = kLift + (FMT == kMxfp4 ? kMxLift : 0);
+
+    while (true) {
+        const int g1 = (int)min((int64_t)groups.count, g0 + (run_end - run));
+        const int column0 = ct * 8, columns = (int)min((int64_t)8, (int64_t)seq.tokens * a.group - column0);
+        const int before = seq.length - seq.tokens;  // the position of the first query token
+        const int p0 = before + column0 / a.group, p1 = before + (column0 + columns - 1) / a.group;
+
+        // rows of the keys of the groups of 32 rounds, a lane each
+        const int mine = g1 - g0 > warp ? (g1 - g0 - warp + kWarps - 1) / kWarps : 0;
+        int rows = -1;
+        const auto rows_from = [&](int i) {
+            const int g = g0 + warp + (i + lane) * kWarps;
+            rows = -1;
+            if (g < g1) {
+                const int token = group_token(groups, g), page = page_of(a.c, a.b, b, token);
+                if (page >= 0) rows = (int)(cache_row(a.c, page, 0, head, token & (a.c.page_size - 1)) / 16);
+            }
+        };
+        const uint32_t ring = smem_addr(shared) + warp * kStages * G::BYTES;
+        uint32_t bad_groups = 0;  // stages whose group has no page
+        const auto copy = [&](int i) {  // of round i, if there is one; a group of copies either way
+            if (i % 32 == 0 && i < mine) rows_from(i);
+            const int row = i < mine ? __shfl_sync(~0u, rows, i % 32) : -1;
+            const uint32_t bit = 1u << i % kStages;
+            bad_groups = row < 0 ? bad_groups | bit : bad_groups & ~bit;
+            G::copy(base, row, ring + i % kStages * G::BYTES, lane);
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) copy(i);
+
+        // the queries: column r, elements c WIDTH / 4 .. of it
+        uint32_t q[KS][2];
+        float qf = a.scale;  // what a score is to be multiplied by
+        {
+            const bool have = r < columns;
+            const int col = column0 + r;
+            const T* src = static_cast<const T*>(a.q) + (int64_t)(seq.first_token + (have ? col / a.group : 0)) * a.qt +
+                           (int64_t)(head * a.group + (have ? col % a.group : 0)) * a.qh;
+            const int d0 = c * (WIDTH / 4);
+            float x[WIDTH / 4];
+            if (have && a.vec_q && d0 + WIDTH / 4 <= a.c.dim) {
+#pragma unroll
+                for (int i = 0; i < WIDTH / 4; i += 8) {
+                    const uint4 raw = *reinterpret_cast<const uint4*>(src + d0 + i);
+                    const T* t = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[i + j] = to_float<T>(t[j]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < WIDTH / 4; ++i) x[i] = have && d0 + i < a.c.dim ? to_float<T>(src[d0 + i]) : 0.0f;
+            }
+            if (!REST) {  // bfloat16: the row's largest to [2^11, 2^12)
+                uint32_t most = 0;
+#pragma unroll
+                for (int i = 0; i < WIDTH / 4; ++i) {
+                    const uint32_t bits = __float_as_uint(x[i]) & 0x7fffffffu;
+                    most = max(most, bits < kInfBits ? bits : 0u);
+                }
+                most = max(most, __shfl_xor_sync(~0u, most, 1));
+                most = max(most, __shfl_xor_sync(~0u, most, 2));
+                const int e = max((int)(most >> 23) - 127 - 11, -126);
+                const float2 up = exp2_factors(-e), down = exp2_factors(e);
+#pragma unroll
+                for (int i = 0; i < WIDTH / 4; ++i) x[i] = x[i] * up.x * up.y;
+                qf = qf * down.x * down.y;
+            }
+#pragma unroll
+            for (int j = 0; j < KS; ++j) {
+                q[j][0] = half2_of(x[4 * j], x[4 * j + 1]);
+                q[j][1] = half2_of(x[4 * j + 2], x[4 * j + 3]);
+            }
+            if (FMT == kMxfp4) qf *= exp2_int(-kMxLift);
+        }
+        // this lane's columns in the fragments are 2 c and 2 c + 1
+        const float qf0 = __shfl_sync(~0u, qf, 8 * c), qf1 = __shfl_sync(~0u, qf, 8 * c + 4);
+        const int pa = 2 * c < columns ? before + (column0 + 2 * c) / a.group : -1;
+        const int pb = 2 * c + 1 < columns ? before + (column0 + 2 * c + 1) / a.group : -1;
+
+        float o[KS][4];
+#pragma unroll
+        for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+        float ma = minus_infinity(), mb = ma, Ma = ma, Mb = ma, la = 0.0f, lb = 0.0f;
+
+#pragma unroll 1
+        for (int i = 0; i < mine; ++i) {
+            const int token = group_token(groups, g0 + warp + i * kWarps);
+            const bool bad = bad_groups >> i % kStages & 1;
+            wait_copies<kAhead - 1>();
+            __syncwarp();
+            const uint8_t* const at = shared + (warp * kStages + i % kStages) * G::BYTES;
+            // the stage of the round before is free: every lane has read it
+            copy(i + kAhead);
+
+            // scores: tokens r and r + 8 in rows r and r + 8
+            uint32_t k[2][G::KW], ks[2][G::KB];
+            int ke[2], ve[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                ke[t] = reinterpret_cast<const int8_t*>(at + G::E0)[r + 8 * t];
+                ve[t] = reinterpret_cast<const int8_t*>(at + G::E0 + 16)[r + 8 * t];
+                load_words<G::KW>(at + (r + 8 * t) * G::ROW + c * (G::ROW / 4), k[t]);
+                half_scales<FMT, G::KB>(at + G::S0 + (r + 8 * t) * G::BLOCKS + c * (WIDTH / 4) / G::BLOCK, ke[t], ks[t]);
+#pragma unroll
+                for (int d = 0; d < G::KB; ++d) ks[t][d] = both_low(ks[t][d], ks[t][d]);
+            }
+            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s2[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // two chains of MMAs
+            constexpr int PER = KS / G::KB;  // MMAs of a block of a lane's codes
+            auto score_step = [&](auto J) {
+                constexpr int j = decltype(J)::value;
+                const uint32_t x = ks[0][j / PER], y = ks[1][j / PER];
+                constexpr int w = j / 2, lo = j % 2 * 2;
+                mma16816(j % 2 ? s2 : s, mul_half2(codes2<lo>(k[0][w]), x), mul_half2(codes2<lo>(k[1][w]), y),
+                         mul_half2(codes2<lo + 1>(k[0][w]), x), mul_half2(codes2<lo + 1>(k[1][w]), y), q[j][0], q[j][1]);
+            };
+            static_for<KS>(score_step);
+            const float k0 = mxfp4_scale(ke[0] + 127), k1 = mxfp4_scale(ke[1] + 127);
+            s[0] = (s[0] + s2[0]) * qf0 * k0;
+            s[1] = (s[1] + s2[1]) * qf1 * k0;
+            s[2] = (s[2] + s2[2]) * qf0 * k1;
+            s[3] = (s[3] + s2[3]) * qf1 * k1;
+            const bool whole = token + 15 <= p0 && (a.window == 0 || token > p1 - a.window) && !bad;
+            if (!whole) {
+                const int t0 = token + r;
+                if (bad) s[0] = s[1] = s[2] = s[3] = not_a_number();
+                if (!sees(pa, t0, a.window, a.sinks)) s[0] = minus_infinity();
+                if (!sees(pb, t0, a.window, a.sinks)) s[1] = minus_infinity();
+                if (!sees(pa, t0 + 8, a.window, a.sinks)) s[2] = minus_infinity();
+                if (!sees(pb, t0 + 8, a.window, a.sinks)) s[3] = minus_infinity();
+            }
+            const float e0 = bad ? 0.0f : (float)ve[0], e1 = bad ? 0.0f : (float)ve[1];
+            float u[4] = {s[0] + e0, s[1] + e0, s[2] + e1, s[3] + e1};
+            const float sa = fmaxf(s[0], s[2]), sb = fmaxf(s[1], s[3]), ua = fmaxf(u[0], u[2]), ub = fmaxf(u[1], u[3]);
+            if (__any_sync(~0u, sa > ma + kLag || sb > mb + kLag || ua > Ma + kLag || ub > Mb + kLag)) {
+                float na = sa, nb = sb, Na = ua, Nb = ub;
+#pragma unroll
+                for (int d = 4; d < 32; d *= 2) {
+                    na = fmaxf(na, __shfl_xor_sync(~0u, na, d));
+                    nb = fmaxf(nb, __shfl_xor_sync(~0u, nb, d));
+                    Na = fmaxf(Na, __shfl_xor_sync(~0u, Na, d));
+                    Nb = fmaxf(Nb, __shfl_xor_sync(~0u, Nb, d));
+                }
+                na = fmaxf(ma, na);
+                nb = fmaxf(mb, nb);
+                Na = fmaxf(Ma, Na);
+                Nb = fmaxf(Mb, Nb);
+                la *= power2(ma - reference(na));
+                lb *= power2(mb - reference(nb));
+                const float fa = power2(Ma - reference(Na)), fb = power2(Mb - reference(Nb));
+#pragma unroll
+                for (int d = 0; d < KS; ++d) {
+                    o[d][0] *= fa;
+                    o[d][1] *= fb;
+                    o[d][2] *= fa;
+                    o[d][3] *= fb;
+                }
+                ma = na, mb = nb, Ma = Na, Mb = Nb;
+            }
+            const float ra = reference(ma), rb = reference(mb), Ra = reference(Ma) - kLift, Rb = reference(Mb) - kLift;
+            la += power2(s[0] - ra) + power2(s[2] - ra);
+            lb += power2(s[1] - rb) + power2(s[3] - rb);
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+                u[i] = power2(u[i] - Ra);
+                u[i + 1] = power2(u[i + 1] - Rb);
+            }
+            const uint32_t h0 = half2_of(u[0], u[1]), h1 = half2_of(u[2], u[3]);
+            const uint32_t w0 = transpose8x8(h0), w1 = transpose8x8(h1);
+            uint32_t x0 = 0, x1 = 0;
+            if (REST) {
+                x0 = transpose8x8(half2_of(u[0] - low_half(h0), u[1] - high_half(h0)));
+                x1 = transpose8x8(half2_of(u[2] - low_half(h1), u[3] - high_half(h1)));
+            }
+
+            // values: tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9 in rows of the same numbers
+            uint32_t v[4][G::VW], hv[4][G::VB], vs[2][G::VB];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int row = 2 * c + (t & 1) + (t >> 1) * 8;
+                load_words<G::VW>(at + G::V0 + row * G::ROW + row / 2 * 32 + r * (G::ROW / 8), v[t]);
+                half_scales<FMT, G::VB>(at + G::S0 + 16 * G::BLOCKS + row * G::BLOCKS + r * (WIDTH / 8) / G::BLOCK,
+                                        FMT == kMxfp4 ? reinterpret_cast<const int8_t*>(at + G::E0 + 16)[row] : 0, hv[t]);
+            }
+            if (!whole) {
+                // a NaN reaches only the columns that see its token
+#pragma unroll
+                for (int d = 0; d < G::VB; ++d) {
+                    uint32_t nan = 0;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        if (bad || half_is_nan(hv[t][d])) {
+                            nan |= 1u << t;
+                            hv[t][d] = 0;
+                        }
+                    }
+                    if (__any_sync(~0u, nan != 0)) {
+#pragma unroll 1
+                        for (int cc = 0; cc < 4; ++cc) {
+                            const uint32_t theirs = __shfl_sync(~0u, nan, (lane & ~3) | cc);
+#pragma unroll 1
+                            for (int t = 0; t < 4; ++t) {
+                                if (!(theirs >> t & 1)) continue;
+                                const int j = token + 2 * cc + (t & 1) + (t >> 1) * 8;
+                                const bool hit_a = sees(pa, j, a.window, a.sinks), hit_b = sees(pb, j, a.window, a.sinks);
+                                constexpr int SPAN = KS / G::VB;
+#pragma unroll
+                                for (int i = d * SPAN; i < (d + 1) * SPAN; ++i) {
+                                    if (hit_a) o[i][0] = o[i][2] = not_a_number();
+                                    if (hit_b) o[i][1] = o[i][3] = not_a_number();
+                                }
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < G::VB; ++d) {
+                vs[0][d] = both_low(hv[0][d], hv[1][d]);
+                vs[1][d] = both_low(hv[2][d], hv[3][d]);
+            }
+            auto value_word = [&](auto W) {
+                constexpr int w = decltype(W)::value;
+                // bytes of two tokens: even elements in xe, odd ones in xo
+                const uint32_t m = 0x0f0f0f0fu;
+                const uint32_t xe = (v[0][w] & m) | (v[1][w] << 4 & ~m), xo = (v[0][w] >> 4 & m) | (v[1][w] & ~m);
+                const uint32_t ye = (v[2][w] & m) | (v[3][w] << 4 & ~m), yo = (v[2][w] >> 4 & m) | (v[3][w] & ~m);
+                auto tile = [&](auto I) {
+                    constexpr int i = decltype(I)::value, d = w * 4 + i;
+                    constexpr int blk = d / (KS / G::VB);
+                    const uint32_t a0 = mul_half2(codes2<i>(xe), vs[0][blk]), a1 = mul_half2(codes2<i>(xo), vs[0][blk]);
+                    const uint32_t a2 = mul_half2(codes2<i>(ye), vs[1][blk]), a3 = mul_half2(codes2<i>(yo), vs[1][blk]);
+                    mma16816(o[d], a0, a1, a2, a3, w0, w1);
+                    if (REST) mma16816(o[d], a0, a1, a2, a3, x0, x1);
+                };
+                static_for<4>(tile);
+            };
+            static_for<G::VW>(value_word);
+        }
+        wait_copies<0>();
+        __syncthreads();  // the warps' stages become their sums
+
+        // the warps' parts
+#pragma unroll
+        for (int d = 4; d < 32; d *= 2) {
+            la += __shfl_xor_sync(~0u, la, d);
+            lb += __shfl_xor_sync(~0u, lb, d);
+        }
+        if (r == 0) {
+            s_m[warp][2 * c] = ma;
+            s_m[warp][2 * c + 1] = mb;
+            s_M[warp][2 * c] = Ma;
+            s_M[warp][2 * c + 1] = Mb;
+            s_l[warp][2 * c] = la;
+            s_l[warp][2 * c + 1] = lb;
+        }
+        {
+            float* mine_a = sums + (warp * 8 + 2 * c) * ROW + r * (WIDTH / 8);
+            float* mine_b = mine_a + ROW;
+#pragma unroll
+            for (int d = 0; d < KS; ++d) {
+                *reinterpret_cast<float2*>(mine_a + 2 * d) = make_float2(o[d][0], o[d][2]);
+                *reinterpret_cast<float2*>(mine_b + 2 * d) = make_float2(o[d][1], o[d][3]);
+            }
+        }
+        __syncthreads();
+        constexpr int LANES = kWarps * 32 / 8;  // threads of a column
+        const int col = threadIdx.x / LANES, at = threadIdx.x % LANES;
+        if (col < columns) {
+            float m = s_m[0][col], M = s_M[0][col];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) {
+                m = fmaxf(m, s_m[w][col]);
+                M = fmaxf(M, s_M[w][col]);
+            }
+            float l = 0.0f, f[kWarps];
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                l += s_l[w][col] * power2(s_m[w][col] - reference(m));
+                f[w] = power2(s_M[w][col] - reference(M));
+            }
+            const bool any = before + (column0 + col) / a.group >= 0;
+            const bool complete = g0 == 0 && g1 == groups.count;
+            const int64_t token = seq.first_token + (column0 + col) / a.group, h = head * a.group + (column0 + col) % a.group;
+            const int64_t part = (2LL * blockIdx.x + (g0 == 0 ? 1 : 0)) * 8 + col;
+            const Finish z = finish_of(m, M, l, kSumLift, any);
+            T* out = static_cast<T*>(a.out) + token * a.ot + h * a.oh;
+            if (!complete && at == 0) a.part[part] = make_float4(m, M, l, any ? 1.0f : 0.0f);
+#pragma unroll
+            for (int d = at * 4; d < WIDTH; d += LANES * 4) {
+                float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float4 x = *reinterpret_cast<const float4*>(sums + (w * 8 + col) * ROW + d);
+                    y[0] = fmaf(x.x, f[w], y[0]);
+                    y[1] = fmaf(x.y, f[w], y[1]);
+                    y[2] = fmaf(x.z, f[w], y[2]);
+                    y[3] = fmaf(x.w, f[w], y[3]);
+                }
+                if (complete) store4(out, d, a.c.dim, a.vec_out, z, y);
+                else *reinterpret_cast<float4*>(a.sums + part * WIDTH + d) = make_float4(y[0], y[1], y[2], y[3]);
+            }
+        }
+        // the next item
+        run += g1 - g0;
+        if (run >= run_end) break;
+        __syncthreads();
+        g0 = 0;
+        if (++head == a.c.heads) {
+            head = 0;
+            if (++ct == tiles_of(a, seq)) {
+                ct = 0;
+                do seq = sequence_at(a.b, ++b);
+                while (seq.tokens == 0);
+            }
+            groups = tile_groups(a, seq, ct);
+        }
     }
 }
 
@@ -516,12 +670,105 @@ __global__ void __launch_bounds__(128) join_kernel(const AttendArgs a, float lif
     if (at < WIDTH) store4(static_cast<T*>(a.out) + token * a.ot + h * a.oh, at, a.c.dim, a.vec_out, finish_of(m, M, l, lift, any), y);
 }
 
+// Row `row`'s place: its item's first and last CTA (which differ if it was cut).
+struct CutRow {
+    int64_t first, last;
+    int column;
+};
+__device__ __forceinline__ CutRow cut_row(const AttendArgs& a, int64_t row, int lane) {
+    const CutRow whole{0, 0, 0};
+    if (row >= a.b.tokens * a.heads) return whole;
+    const int64_t token = row / a.heads;
+    const int h = (int)(row % a.heads), b = search(a.b, token, 1, 1, 0);
+    if (b < 0) return whole;
+    const Sequence seq = sequence_at(a.b, b);
+    if (token < seq.first_token || token >= seq.first_token + seq.tokens) return whole;
+    int64_t before = 0, total = 0;
+    for (int i = lane; i < a.b.batch; i += 32) {
+        const int64_t cost = cost_of(a, sequence_at(a.b, i));
+        total += cost;
+        if (i < b) before += cost;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) {
+        before += __shfl_xor_sync(~0u, before, d);
+        total += __shfl_xor_sync(~0u, total, d);
+    }
+    const Cut cut = cut_of(total * a.c.heads, a.splits);
+    const int head = h / a.group, column = (int)(token - seq.first_token) * a.group + h % a.group, ct = column / 8;
+    for (int i = 0; i < ct; ++i) before += tile_groups(a, seq, i).count;
+    const int count = tile_groups(a, seq, ct).count;
+    const int64_t begin = before * a.c.heads + (int64_t)head * count;
+    return CutRow{cut.owner(begin), cut.owner(begin + count - 1), column};
+}
+
+// The outputs of the items that were cut: a warp for a row.  What came before the
+// kernel that leaves the parts is complete, since its blocks waited for it before they
+// let this one begin: so the batch may be read ahead of the wait, the parts may not.
+// Every block waits, so that what follows this kernel follows that one too.
 template <typename T, int WIDTH>
+__global__ void __launch_bounds__(128) join_cut_kernel(const AttendArgs a, float lift) {
+    constexpr int VALUES = WIDTH / 32;  // of a lane
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = (int64_t)blockIdx.x * 4 + warp;
+    const CutRow place = cut_row(a, row, lane);
+    pdl_wait();
+    const int64_t c0 = place.first, c1 = place.last;
+    if (c0 == c1) return;
+    const int column = place.column, h = (int)(row % a.heads);
+    const int64_t token = row / a.heads;
+    const auto slot = [&](int64_t c) { return (2 * c + (c == c0 ? 1 : 0)) * 8 + column % 8; };
+    float m = minus_infinity(), M = m;
+    float4 mine = make_float4(m, m, 0.0f, 0.0f);
+    for (int64_t c = c0 + lane; c <= c1; c += 32) {
+        const float4 p = a.part[slot(c)];
+        if (c < c0 + 32) mine = p;
+        m = fmaxf(m, p.x);
+        M = fmaxf(M, p.y);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) {
+        m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+        M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
+    }
+    const bool any = __shfl_sync(~0u, mine.w, 0) != 0.0f;
+    float y[VALUES], l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VALUES; ++i) y[i] = 0.0f;
+    for (int64_t i0 = c0; i0 <= c1; i0 += 32) {
+        if (i0 > c0) mine = i0 + lane <= c1 ? a.part[slot(i0 + lane)] : make_float4(minus_infinity(), minus_infinity(), 0.0f, 0.0f);
+        l += mine.z * power2(mine.x - reference(m));
+        const float f = power2(mine.y - reference(M));
+        const int n = (int)min((int64_t)32, c1 - i0 + 1);
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) {
+            const float w = __shfl_sync(~0u, f, i);
+            const float* x = a.sums + slot(i0 + i) * WIDTH + lane;
+#pragma unroll
+            for (int k = 0; k < VALUES; ++k) y[k] = fmaf(x[32 * k], w, y[k]);
+        }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) l += __shfl_xor_sync(~0u, l, d);
+    const Finish z = finish_of(m, M, l, lift, any);
+    T* out = static_cast<T*>(a.out) + token * a.ot + h * a.oh;
+#pragma unroll
+    for (int k = 0; k < VALUES; ++k)
+        if (lane + 32 * k < a.c.dim) out[lane + 32 * k] = from_float<T>(any ? y[k] * z.x * z.x * z.inverse : 0.0f);
+}
+
+template <int WIDTH, int FMT>
+constexpr size_t columns_smem() {
+    return std::max<size_t>(kWarps * 8 * (WIDTH + 4) * sizeof(float), (size_t)kWarps * kStages * Stage<WIDTH, FMT>::BYTES);
+}
+template <typename T, int WIDTH, int FMT>
 cudaError_t columns(const AttendArgs& a, cudaStream_t st) {
-    const dim3 grid((unsigned)attend_tiles(a.b, a.group, 8), (unsigned)a.c.heads, (unsigned)a.splits);
-    const size_t smem = (size_t)kWarps * 8 * (WIDTH + 4) * sizeof(float);
-    return a.c.fmt == kMxfp4 ? launch_pdl(attend_columns_kernel<T, WIDTH, kMxfp4>, grid, dim3(kWarps * 32), smem, st, a)
-                             : launch_pdl(attend_columns_kernel<T, WIDTH, kNvfp4>, grid, dim3(kWarps * 32), smem, st, a);
+    const size_t smem = columns_smem<WIDTH, FMT>();
+    cudaError_t err = launch_pdl(attend_columns_kernel<T, WIDTH, FMT>, dim3((unsigned)a.splits), dim3(kWarps * 32), smem, st, a);
+    if (err != cudaSuccess) return err;
+    const int64_t rows = a.b.tokens * a.heads;
+    return launch_pdl(join_cut_kernel<T, WIDTH>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, a, kLift + (FMT == kMxfp4 ? kMxLift : 0));
 }
 template <typename T, int WIDTH>
 cudaError_t join(const AttendArgs& a, float lift, cudaStream_t st) {
@@ -529,28 +776,52 @@ cudaError_t join(const AttendArgs& a, float lift, cudaStream_t st) {
     return launch_pdl(join_kernel<T, WIDTH>, dim3((unsigned)((rows + per - 1) / per)), dim3(128), 0, st, a, lift);
 }
 
-// How many parts a row's tokens are cut into: as many blocks as the SMs hold (4
-// each), at least 4 groups of 16 tokens for each of a block's warps.
-int parts_of(const AttendArgs& a) {
-    const int64_t tiles = std::max(a.b.tokens * a.group / 8, (int64_t)a.b.batch) * a.c.heads;
-    const int64_t longest = a.window > 0 ? a.window + a.sinks : (int64_t)a.b.table_pages * a.c.page_size;
-    const int64_t most = (longest + kWarps * 64 - 1) / (kWarps * 64);
-    const int64_t want = 4LL * device_sms() / std::max<int64_t>(1, tiles);
-    return (int)std::max<int64_t>(1, std::min<int64_t>({want, most, 128}));
+// CTAs that the SMs hold at once.
+template <typename T, int WIDTH, int FMT>
+int resident() {
+    static std::atomic<int> cached[64];
+    int dev = 0, per = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+    int n = cached[dev].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    const size_t smem = columns_smem<WIDTH, FMT>();
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(attend_columns_kernel<T, WIDTH, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return device_sms();
+    }
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, attend_columns_kernel<T, WIDTH, FMT>, kWarps * 32, smem) != cudaSuccess || per < 1) {
+        (void)cudaGetLastError();
+        return device_sms();
+    }
+    n = per * device_sms();
+    cached[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// f(type, width, format) for those of the call.
+template <class F>
+auto with_kernel(const AttendArgs& a, int type, F f) {
+    const auto width = [&](auto t, auto fmt) {
+        using W = std::integral_constant<int, 64>;
+        using X = std::integral_constant<int, 128>;
+        using Y = std::integral_constant<int, 256>;
+        return a.c.width == 64 ? f(t, W{}, fmt) : a.c.width == 128 ? f(t, X{}, fmt) : f(t, Y{}, fmt);
+    };
+    const auto format = [&](auto t) {
+        return a.c.fmt == kMxfp4 ? width(t, std::integral_constant<int, kMxfp4>{}) : width(t, std::integral_constant<int, kNvfp4>{});
+    };
+    return type == DDGEMM_BF16 ? format(__nv_bfloat16{}) : format(__half{});
 }
 
 }  // namespace
 
-int attend_columns_parts(const AttendArgs& a) { return parts_of(a); }
+int attend_columns_ctas(const AttendArgs& a, int type) {
+    return with_kernel(a, type, [](auto t, auto w, auto f) { return resident<decltype(t), decltype(w)::value, decltype(f)::value>(); });
+}
 
 cudaError_t launch_attend_columns(const AttendArgs& a, int type, cudaStream_t st) {
-    cudaError_t err;
-    if (type == DDGEMM_BF16)
-        err = a.c.width == 64 ? columns<__nv_bfloat16, 64>(a, st) : a.c.width == 128 ? columns<__nv_bfloat16, 128>(a, st) : columns<__nv_bfloat16, 256>(a, st);
-    else
-        err = a.c.width == 64 ? columns<__half, 64>(a, st) : a.c.width == 128 ? columns<__half, 128>(a, st) : columns<__half, 256>(a, st);
-    if (err != cudaSuccess || a.splits == 1) return err;
-    return launch_attend_join(a, type, kLift + (a.c.fmt == kMxfp4 ? kMxLift : 0), st);
+    return with_kernel(a, type, [&](auto t, auto w, auto f) { return columns<decltype(t), decltype(w)::value, decltype(f)::value>(a, st); });
 }
 
 cudaError_t launch_attend_join(const AttendArgs& a, int type, float lift, cudaStream_t st) {

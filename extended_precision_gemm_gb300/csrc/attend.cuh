@@ -28,9 +28,9 @@ struct AttendArgs {
     int window, sinks;       // window 0: none
     float scale;             // log2(e) times the scale of scores
     bool vec_q, vec_out;
-    int splits;
-    float4* part;  // (m, M, l, 1 if any token is seen) by split and row (token, query head)
-    float* sums;   // o by split and row, `width` each
+    int splits;    // attend_tile.cu: parts of every row; attend.cu: CTAs
+    float4* part;  // (m, M, l, 1 if any token is seen) of a part: by split and row (token, query head), or by CTA (attend.cu)
+    float* sums;   // its o, `width` elements
 };
 
 #ifdef __CUDACC__
@@ -143,8 +143,9 @@ __device__ __forceinline__ void store4(T* out, int d, int dim, bool vec, const F
 inline int64_t attend_tiles(const BatchView& b, int group, int columns) { return b.tokens * group / columns + b.batch; }
 
 cudaError_t launch_attend_columns(const AttendArgs& a, int type, cudaStream_t st);
-// Into how many parts it cuts a row's tokens.
-int attend_columns_parts(const AttendArgs& a);
+// CTAs of that launch, and rows of the workspace: (part, sums) of two cut items each.
+int attend_columns_ctas(const AttendArgs& a, int type);
+inline int64_t attend_columns_rows(int ctas) { return 2LL * 8 * ctas; }
 // The same for many queries, by tiles of 128 rows on the tensor cores.
 cudaError_t launch_attend_tile(const AttendArgs& a, int type, cudaStream_t st);
 int attend_tile_parts(const AttendArgs& a);

@@ -212,19 +212,13 @@ ddgemm_status dd_mx4_attention(const ddgemm_mx4_cache* cache, const ddgemm_batch
     if (attend_tiles(a.b, a.group, 8) * cache->heads >= (1LL << 31)) return DDGEMM_ERR_UNSUPPORTED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool many = T * a.group > kColumnsMost * batch->batch && cache->pages > 0;
-    a.splits = many ? attend_tile_parts(a) : attend_columns_parts(a);
+    a.splits = many ? attend_tile_parts(a) : attend_columns_ctas(a, type);
     Workspace ws(st);
-    const int64_t rows = T * q_heads;
-    int64_t parts = 0, sums = 0;
-    if (a.splits > 1) {
-        parts = ws.reserve(a.splits * rows * (int64_t)sizeof(float4));
-        sums = ws.reserve(a.splits * rows * a.c.width * 4);
-    }
+    const int64_t rows = many ? (a.splits > 1 ? a.splits * T * q_heads : 0) : attend_columns_rows(a.splits);
+    const int64_t parts = ws.reserve(rows * (int64_t)sizeof(float4)), sums = ws.reserve(rows * a.c.width * 4);
     if (!ws.allocate()) return DDGEMM_ERR_ALLOC;
-    if (a.splits > 1) {
-        a.part = ws.at<float4>(parts);
-        a.sums = ws.at<float>(sums);
-    }
+    a.part = rows ? ws.at<float4>(parts) : nullptr;
+    a.sums = rows ? ws.at<float>(sums) : nullptr;
     return status_of(many ? launch_attend_tile(a, type, st) : launch_attend_columns(a, type, st));
 }
 
