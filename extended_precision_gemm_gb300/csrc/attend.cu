@@ -53,17 +53,6 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w) {
     return h;
 }
 
-// A block's scale as the bits of a half: E4M3 is exact; E8M0 relative to 2^e.
-template <int FMT>
-__device__ __forceinline__ uint32_t half_scale(uint32_t byte, int e) {
-    if (FMT == kNvfp4) {
-        uint32_t h2;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((unsigned short)byte));
-        return h2 & 0xffffu;
-    }
-    const int t = (int)byte - e - 127 + kMxLift + 15;
-    return byte == 255u ? 0x7fffu : (uint32_t)min(max(t, 0), 30) << 10;
-}
 __device__ __forceinline__ bool half_is_nan(uint32_t h) { return (h & 0x7fffu) > 0x7c00u; }
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -161,20 +150,25 @@ struct Stage {
     }
 };
 
-// N scale bytes of a row with exponent e as halves.
+// The scale bytes of N blocks of a row with exponent e as halves, each in both halves
+// of a word.  (mxfp4: t 2^10 in both is one multiplication.)
 template <int FMT, int N>
 __device__ __forceinline__ void half_scales(const uint8_t* bytes, int e, uint32_t (&h)[N]) {
 #pragma unroll
     for (int b = 0; b < N; b += 2) {
-        const uint16_t two = N == 1 ? (uint16_t)bytes[0] : *reinterpret_cast<const uint16_t*>(bytes + b);
+        const uint32_t two = N == 1 ? bytes[0] : *reinterpret_cast<const uint16_t*>(bytes + b);
         if (FMT == kNvfp4) {
             uint32_t h2;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(two));
-            h[b] = h2;  // the low half counts
-            if (b + 1 < N) h[b + 1] = h2 >> 16;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)two));
+            h[b] = __byte_perm(h2, h2, 0x1010);
+            if (b + 1 < N) h[b + 1] = __byte_perm(h2, h2, 0x3232);
         } else {
-            h[b] = half_scale<kMxfp4>(two & 0xffu, e);
-            if (b + 1 < N) h[b + 1] = half_scale<kMxfp4>(two >> 8, e);
+            const auto half = [&](uint32_t byte) {
+                const int t = min(max((int)byte - e - 127 + kMxLift + 15, 0), 30);
+                return byte == 255u ? 0x7fff7fffu : (uint32_t)t * 0x04000400u;
+            };
+            h[b] = half(two & 0xffu);
+            if (b + 1 < N) h[b + 1] = half(two >> 8);
         }
     }
 }
@@ -195,7 +189,7 @@ struct Cut {
     // the CTA that has group g
     __device__ __forceinline__ int64_t owner(int64_t g) const { return ((g + 1) * ctas - 1) / total; }
 };
-constexpr int kLeast = 8;
+constexpr int kLeast = 4;
 __device__ __forceinline__ Cut cut_of(int64_t total, int ctas) {
     return Cut{total, max((int64_t)1, min((int64_t)ctas, total / kLeast))};
 }
@@ -244,7 +238,7 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : 4) attend_colu
     const int r = lane / 4, c = lane % 4;
 
     // the whole cost, and the sequence in which this CTA's run begins
-    int64_t run, run_end, start;  // run: groups from the item's first on; start: of the sequence's
+    int64_t total = 0, ctas, run, run_end, start;  // run: groups from the item's first on; start: of the sequence's
     int b;
     {
         const int per = (a.b.batch + kWarps * 32 - 1) / (kWarps * 32), b0 = min((int)threadIdx.x * per, a.b.batch), b1 = min(b0 + per, a.b.batch);
@@ -262,7 +256,7 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : 4) attend_colu
         }
         if (lane == 31) scan[warp] = upto;
         __syncthreads();
-        int64_t before = upto - mine, total = 0;
+        int64_t before = upto - mine;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             if (w < warp) before += scan[w];
@@ -270,7 +264,11 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : 4) attend_colu
         }
         total *= a.c.heads;
         const Cut cut = cut_of(total, a.splits);
-        if (total == 0 || blockIdx.x >= cut.ctas) return;
+        ctas = cut.ctas;
+        if (total == 0 || blockIdx.x >= ctas) {
+            if (threadIdx.x == 0) a.cuts[blockIdx.x] = CutItem{0, 0, 0, 0, 0, 0};
+            return;
+        }
         run = cut.first(blockIdx.x);
         run_end = cut.first(blockIdx.x + 1);
         int64_t at = before * a.c.heads;
@@ -318,16 +316,21 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : 4) attend_colu
             }
         };
         const uint32_t ring = smem_addr(shared) + warp * kStages * G::BYTES;
-        uint32_t bad_groups = 0;  // stages whose group has no page
-        const auto copy = [&](int i) {  // of round i, if there is one; a group of copies either way
+        uint32_t bad_groups = 0;  // bit 0: the group of the round at hand has no page; the next rounds above it
+        const auto copy = [&](int i, uint32_t stage) {  // of round i, if there is one; a group of copies either way
             if (i % 32 == 0 && i < mine) rows_from(i);
             const int row = i < mine ? __shfl_sync(~0u, rows, i % 32) : -1;
-            const uint32_t bit = 1u << i % kStages;
-            bad_groups = row < 0 ? bad_groups | bit : bad_groups & ~bit;
-            G::copy(base, row, ring + i % kStages * G::BYTES, lane);
+            bad_groups |= (uint32_t)(row < 0) << kAhead;
+            G::copy(base, row, ring + stage, lane);
         };
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) copy(i);
+        for (int i = 0; i < kAhead; ++i) {
+            copy(i, i * G::BYTES);
+            bad_groups >>= 1;
+        }
+        // groups that every column sees as a whole: list numbers from whole0 to whole1 - 1
+        const int whole0 = a.window > 0 && p1 >= a.window ? max(groups.sink, groups.sink + (p1 - a.window) / 16 + 1 - groups.low) : 0;
+        const int whole1 = p0 < 0 ? 0 : groups.sink + (p0 + 1) / 16 - groups.low;
 
         // the queries: column r, elements c WIDTH / 4 .. of it
         uint32_t q[KS][2];
@@ -382,16 +385,21 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : 4) attend_colu
 #pragma unroll
         for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
         float ma = minus_infinity(), mb = ma, Ma = ma, Mb = ma, la = 0.0f, lb = 0.0f;
+        float ra = 0.0f, rb = 0.0f, Ra = -kLift, Rb = -kLift;  // what is subtracted from exponents
 
+        uint32_t stage = 0;
 #pragma unroll 1
         for (int i = 0; i < mine; ++i) {
-            const int token = group_token(groups, g0 + warp + i * kWarps);
-            const bool bad = bad_groups >> i % kStages & 1;
             wait_copies<kAhead - 1>();
             __syncwarp();
-            const uint8_t* const at = shared + (warp * kStages + i % kStages) * G::BYTES;
+            const bool bad = bad_groups & 1;
+            const int group = g0 + warp + i * kWarps;
+            const bool whole = group >= whole0 && group < whole1 && !bad;
+            const uint8_t* const at = shared + warp * kStages * G::BYTES + stage;
             // the stage of the round before is free: every lane has read it
-            copy(i + kAhead);
+            copy(i + kAhead, stage == 0 ? kAhead * G::BYTES : stage - G::BYTES);
+            bad_groups >>= 1;
+            stage = stage == kAhead * G::BYTES ? 0 : stage + G::BYTES;
 
             // scores: tokens r and r + 8 in rows r and r + 8
             uint32_t k[2][G::KW], ks[2][G::KB];
@@ -402,8 +410,6 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : 4) attend_colu
                 ve[t] = reinterpret_cast<const int8_t*>(at + G::E0 + 16)[r + 8 * t];
                 load_words<G::KW>(at + (r + 8 * t) * G::ROW + c * (G::ROW / 4), k[t]);
                 half_scales<FMT, G::KB>(at + G::S0 + (r + 8 * t) * G::BLOCKS + c * (WIDTH / 4) / G::BLOCK, ke[t], ks[t]);
-#pragma unroll
-                for (int d = 0; d < G::KB; ++d) ks[t][d] = both_low(ks[t][d], ks[t][d]);
             }
             float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s2[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // two chains of MMAs
             constexpr int PER = KS / G::KB;  // MMAs of a block of a lane's codes
@@ -415,12 +421,13 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : 4) attend_colu
                          mul_half2(codes2<lo + 1>(k[0][w]), x), mul_half2(codes2<lo + 1>(k[1][w]), y), q[j][0], q[j][1]);
             };
             static_for<KS>(score_step);
-            const float k0 = mxfp4_scale(ke[0] + 127), k1 = mxfp4_scale(ke[1] + 127);
+            // 2^-127 counts as 0: rows of zeros have it, and those below 2^-125
+            const float k0 = __uint_as_float((uint32_t)(ke[0] + 127) << 23), k1 = __uint_as_float((uint32_t)(ke[1] + 127) << 23);
             s[0] = (s[0] + s2[0]) * qf0 * k0;
             s[1] = (s[1] + s2[1]) * qf1 * k0;
             s[2] = (s[2] + s2[2]) * qf0 * k1;
             s[3] = (s[3] + s2[3]) * qf1 * k1;
-            const bool whole = token + 15 <= p0 && (a.window == 0 || token > p1 - a.window) && !bad;
+            const int token = whole ? 0 : group_token(groups, group);
             if (!whole) {
                 const int t0 = token + r;
                 if (bad) s[0] = s[1] = s[2] = s[3] = not_a_number();
@@ -456,8 +463,8 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : 4) attend_colu
                     o[d][3] *= fb;
                 }
                 ma = na, mb = nb, Ma = Na, Mb = Nb;
+                ra = reference(ma), rb = reference(mb), Ra = reference(Ma) - kLift, Rb = reference(Mb) - kLift;
             }
-            const float ra = reference(ma), rb = reference(mb), Ra = reference(Ma) - kLift, Rb = reference(Mb) - kLift;
             la += power2(s[0] - ra) + power2(s[2] - ra);
             lb += power2(s[1] - rb) + power2(s[3] - rb);
 #pragma unroll
@@ -604,7 +611,15 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : 4) attend_colu
         }
         // the next item
         run += g1 - g0;
-        if (run >= run_end) break;
+        if (run >= run_end) {
+            if (threadIdx.x == 0) {
+                CutItem cut{0, 0, 0, 0, 0, 0};
+                if (g0 == 0 && g1 < groups.count)
+                    cut = CutItem{columns, (int)(Cut{total, ctas}.owner(run + groups.count - g1 - 1) - blockIdx.x), seq.first_token, column0, head, before};
+                a.cuts[blockIdx.x] = cut;
+            }
+            break;
+        }
         __syncthreads();
         g0 = 0;
         if (++head == a.c.heads) {
@@ -670,89 +685,72 @@ __global__ void __launch_bounds__(128) join_kernel(const AttendArgs a, float lif
     if (at < WIDTH) store4(static_cast<T*>(a.out) + token * a.ot + h * a.oh, at, a.c.dim, a.vec_out, finish_of(m, M, l, lift, any), y);
 }
 
-// Row `row`'s place: its item's first and last CTA (which differ if it was cut).
-struct CutRow {
-    int64_t first, last;
-    int column;
-};
-__device__ __forceinline__ CutRow cut_row(const AttendArgs& a, int64_t row, int lane) {
-    const CutRow whole{0, 0, 0};
-    if (row >= a.b.tokens * a.heads) return whole;
-    const int64_t token = row / a.heads;
-    const int h = (int)(row % a.heads), b = search(a.b, token, 1, 1, 0);
-    if (b < 0) return whole;
-    const Sequence seq = sequence_at(a.b, b);
-    if (token < seq.first_token || token >= seq.first_token + seq.tokens) return whole;
-    int64_t before = 0, total = 0;
-    for (int i = lane; i < a.b.batch; i += 32) {
-        const int64_t cost = cost_of(a, sequence_at(a.b, i));
-        total += cost;
-        if (i < b) before += cost;
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) {
-        before += __shfl_xor_sync(~0u, before, d);
-        total += __shfl_xor_sync(~0u, total, d);
-    }
-    const Cut cut = cut_of(total * a.c.heads, a.splits);
-    const int head = h / a.group, column = (int)(token - seq.first_token) * a.group + h % a.group, ct = column / 8;
-    for (int i = 0; i < ct; ++i) before += tile_groups(a, seq, i).count;
-    const int count = tile_groups(a, seq, ct).count;
-    const int64_t begin = before * a.c.heads + (int64_t)head * count;
-    return CutRow{cut.owner(begin), cut.owner(begin + count - 1), column};
-}
-
-// The outputs of the items that were cut: a warp for a row.  What came before the
-// kernel that leaves the parts is complete, since its blocks waited for it before they
-// let this one begin: so the batch may be read ahead of the wait, the parts may not.
-// Every block waits, so that what follows this kernel follows that one too.
-template <typename T, int WIDTH>
-__global__ void __launch_bounds__(128) join_cut_kernel(const AttendArgs a, float lift) {
+// The outputs of the items that were cut: block i that which CTA i began, PER warps for
+// a column, each with every PER-th part.
+template <typename T, int WIDTH, int PER>
+__global__ void __launch_bounds__(8 * PER * 32) join_cut_kernel(const AttendArgs a, float lift) {
     constexpr int VALUES = WIDTH / 32;  // of a lane
-    pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = (int64_t)blockIdx.x * 4 + warp;
-    const CutRow place = cut_row(a, row, lane);
+    constexpr int BATCH = 8;            // parts loaded at once
+    __shared__ float y_of[PER > 1 ? 8 * PER : 1][PER > 1 ? WIDTH : 1];
+    __shared__ float l_of[8 * PER];
     pdl_wait();
-    const int64_t c0 = place.first, c1 = place.last;
-    if (c0 == c1) return;
-    const int column = place.column, h = (int)(row % a.heads);
-    const int64_t token = row / a.heads;
-    const auto slot = [&](int64_t c) { return (2 * c + (c == c0 ? 1 : 0)) * 8 + column % 8; };
-    float m = minus_infinity(), M = m;
-    float4 mine = make_float4(m, m, 0.0f, 0.0f);
-    for (int64_t c = c0 + lane; c <= c1; c += 32) {
-        const float4 p = a.part[slot(c)];
-        if (c < c0 + 32) mine = p;
-        m = fmaxf(m, p.x);
-        M = fmaxf(M, p.y);
-    }
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, column = warp / PER, share = warp % PER;
+    const CutItem item = a.cuts[blockIdx.x];
+    if (item.columns == 0) return;
+    const int parts = item.others + 1;
+    const auto slot = [&](int i) { return (2LL * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * 8 + column; };
+    float m = minus_infinity(), M = m, l = 0.0f, y[VALUES];
 #pragma unroll
-    for (int d = 16; d > 0; d /= 2) {
-        m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-        M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
-    }
-    const bool any = __shfl_sync(~0u, mine.w, 0) != 0.0f;
-    float y[VALUES], l = 0.0f;
+    for (int k = 0; k < VALUES; ++k) y[k] = 0.0f;
+    if (column < item.columns) {
+        for (int i = lane; i < parts; i += 32) {
+            const float4 p = a.part[slot(i)];
+            m = fmaxf(m, p.x);
+            M = fmaxf(M, p.y);
+        }
 #pragma unroll
-    for (int i = 0; i < VALUES; ++i) y[i] = 0.0f;
-    for (int64_t i0 = c0; i0 <= c1; i0 += 32) {
-        if (i0 > c0) mine = i0 + lane <= c1 ? a.part[slot(i0 + lane)] : make_float4(minus_infinity(), minus_infinity(), 0.0f, 0.0f);
-        l += mine.z * power2(mine.x - reference(m));
-        const float f = power2(mine.y - reference(M));
-        const int n = (int)min((int64_t)32, c1 - i0 + 1);
-#pragma unroll 8
-        for (int i = 0; i < n; ++i) {
-            const float w = __shfl_sync(~0u, f, i);
-            const float* x = a.sums + slot(i0 + i) * WIDTH + lane;
+        for (int d = 16; d > 0; d /= 2) {
+            m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+            M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
+        }
+        for (int i0 = share; i0 < parts; i0 += BATCH * PER) {
+            float x[BATCH][VALUES];
+            float4 p[BATCH];
 #pragma unroll
-            for (int k = 0; k < VALUES; ++k) y[k] = fmaf(x[32 * k], w, y[k]);
+            for (int i = 0; i < BATCH; ++i) {
+                const int64_t at = slot(min(i0 + i * PER, parts - 1));
+                p[i] = a.part[at];
+#pragma unroll
+                for (int k = 0; k < VALUES; ++k) x[i][k] = a.sums[at * WIDTH + lane + 32 * k];
+            }
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                if (i0 + i * PER >= parts) continue;
+                l += p[i].z * power2(p[i].x - reference(m));
+                const float f = power2(p[i].y - reference(M));
+#pragma unroll
+                for (int k = 0; k < VALUES; ++k) y[k] = fmaf(x[i][k], f, y[k]);
+            }
+        }
+        if (PER > 1) {
+#pragma unroll
+            for (int k = 0; k < VALUES; ++k) y_of[warp][lane + 32 * k] = y[k];
+            if (lane == 0) l_of[warp] = l;
         }
     }
+    if (PER > 1) __syncthreads();
+    if (share != 0 || column >= item.columns) return;
 #pragma unroll
-    for (int d = 16; d > 0; d /= 2) l += __shfl_xor_sync(~0u, l, d);
+    for (int w = 1; w < PER; ++w) {
+        l += l_of[warp + w];
+#pragma unroll
+        for (int k = 0; k < VALUES; ++k) y[k] += y_of[warp + w][lane + 32 * k];
+    }
+    const int col = item.column + column;
+    const bool any = item.before + col / a.group >= 0;
     const Finish z = finish_of(m, M, l, lift, any);
-    T* out = static_cast<T*>(a.out) + token * a.ot + h * a.oh;
+    T* out = static_cast<T*>(a.out) + (int64_t)(item.first_token + col / a.group) * a.ot + (int64_t)(item.head * a.group + col % a.group) * a.oh;
 #pragma unroll
     for (int k = 0; k < VALUES; ++k)
         if (lane + 32 * k < a.c.dim) out[lane + 32 * k] = from_float<T>(any ? y[k] * z.x * z.x * z.inverse : 0.0f);
@@ -767,8 +765,11 @@ cudaError_t columns(const AttendArgs& a, cudaStream_t st) {
     const size_t smem = columns_smem<WIDTH, FMT>();
     cudaError_t err = launch_pdl(attend_columns_kernel<T, WIDTH, FMT>, dim3((unsigned)a.splits), dim3(kWarps * 32), smem, st, a);
     if (err != cudaSuccess) return err;
-    const int64_t rows = a.b.tokens * a.heads;
-    return launch_pdl(join_cut_kernel<T, WIDTH>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, a, kLift + (FMT == kMxfp4 ? kMxLift : 0));
+    // few items for many CTAs: many parts of each
+    const float lift = kLift + (FMT == kMxfp4 ? kMxLift : 0);
+    const bool long_items = attend_tiles(a.b, a.group, 8) * a.c.heads * 8 < a.splits;
+    return long_items ? launch_pdl(join_cut_kernel<T, WIDTH, WIDTH == 256 ? 2 : 4>, dim3((unsigned)a.splits), dim3(WIDTH == 256 ? 512 : 1024), 0, st, a, lift)
+                      : launch_pdl(join_cut_kernel<T, WIDTH, 1>, dim3((unsigned)a.splits), dim3(256), 0, st, a, lift);
 }
 template <typename T, int WIDTH>
 cudaError_t join(const AttendArgs& a, float lift, cudaStream_t st) {

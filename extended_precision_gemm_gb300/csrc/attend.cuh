@@ -17,6 +17,7 @@
 
 namespace ddg {
 
+struct CutItem;
 // A launch of the kernels below.
 struct AttendArgs {
     CacheView c;
@@ -31,6 +32,7 @@ struct AttendArgs {
     int splits;    // attend_tile.cu: parts of every row; attend.cu: CTAs
     float4* part;  // (m, M, l, 1 if any token is seen) of a part: by split and row (token, query head), or by CTA (attend.cu)
     float* sums;   // its o, `width` elements
+    CutItem* cuts;  // attend.cu: one for each CTA
 };
 
 #ifdef __CUDACC__
@@ -146,6 +148,11 @@ cudaError_t launch_attend_columns(const AttendArgs& a, int type, cudaStream_t st
 // CTAs of that launch, and rows of the workspace: (part, sums) of two cut items each.
 int attend_columns_ctas(const AttendArgs& a, int type);
 inline int64_t attend_columns_rows(int ctas) { return 2LL * 8 * ctas; }
+// What a CTA says of the item that it begins and others end (0 columns: none): further CTAs, place of its columns,
+// the position of its sequence's first query.
+struct CutItem {
+    int columns, others, first_token, column, head, before;
+};
 // The same for many queries, by tiles of 128 rows on the tensor cores.
 cudaError_t launch_attend_tile(const AttendArgs& a, int type, cudaStream_t st);
 int attend_tile_parts(const AttendArgs& a);

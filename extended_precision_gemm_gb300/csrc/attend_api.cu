@@ -215,10 +215,12 @@ ddgemm_status dd_mx4_attention(const ddgemm_mx4_cache* cache, const ddgemm_batch
     a.splits = many ? attend_tile_parts(a) : attend_columns_ctas(a, type);
     Workspace ws(st);
     const int64_t rows = many ? (a.splits > 1 ? a.splits * T * q_heads : 0) : attend_columns_rows(a.splits);
-    const int64_t parts = ws.reserve(rows * (int64_t)sizeof(float4)), sums = ws.reserve(rows * a.c.width * 4);
+    const int64_t parts = ws.reserve(rows * (int64_t)sizeof(float4)), sums = ws.reserve(rows * a.c.width * 4),
+                  cuts = ws.reserve(many ? 0 : a.splits * (int64_t)sizeof(CutItem));
     if (!ws.allocate()) return DDGEMM_ERR_ALLOC;
     a.part = rows ? ws.at<float4>(parts) : nullptr;
     a.sums = rows ? ws.at<float>(sums) : nullptr;
+    a.cuts = many ? nullptr : ws.at<CutItem>(cuts);
     return status_of(many ? launch_attend_tile(a, type, st) : launch_attend_columns(a, type, st));
 }
 
