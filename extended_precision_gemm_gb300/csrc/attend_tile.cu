@@ -826,11 +826,15 @@ cudaError_t by_width(const AttendArgs& a, cudaStream_t st) {
 
 }  // namespace
 
+// Enough items for two rounds of the SMs are left whole; fewer are cut so that there are
+// four rounds of parts, of 512 tokens at least: lengths differ, and a part's start costs
+// 3 us.
 int attend_tile_parts(const AttendArgs& a) {
     const int rows = a.c.width == 256 ? 128 : 256;
-    const int64_t tiles = std::max(a.b.tokens * a.group / rows, (int64_t)a.b.batch) * a.c.heads;
+    const int64_t items = std::max(a.b.tokens * a.group / rows, (int64_t)a.b.batch) * a.c.heads;
     const int64_t longest = a.window > 0 ? (int64_t)a.window + a.sinks : (int64_t)a.b.table_pages * a.c.page_size;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({device_sms() / std::max<int64_t>(1, tiles), (longest + 1023) / 1024, 64}));
+    if (items >= 2 * device_sms()) return 1;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({4 * device_sms() / std::max<int64_t>(1, items), (longest + 511) / 512, 64}));
 }
 
 cudaError_t launch_attend_tile(const AttendArgs& a, int type, cudaStream_t st) {

@@ -6,6 +6,7 @@
 // consecutive values of a row; a row is 8, 16 or 32 lanes.  Keys may be rotated on
 // the way in: in 32 bits and what they leave (rotary.cuh), so that a value is rounded
 // once, to its code.
+#include "eight.cuh"
 #include "kv_cache.cuh"
 #include "rotary.cuh"
 
@@ -13,23 +14,55 @@ namespace ddg {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMostTokens = 8;  // of a block
+constexpr int kMostTokens = 16;  // of a block
 
 // Eight values of a row from element d on, 0 beyond `dim`.
 template <typename T>
-__device__ __forceinline__ void load_values(const T* row, int d, int dim, bool vec, float (&x)[8]) {
+__device__ __forceinline__ void load_values(const T* row, int d, int dim, bool vec, Eight<T>& x) {
     if (vec && d + 8 <= dim) {
-        constexpr int W = sizeof(T) * 8 / 16;
-        uint4 raw[W];
-#pragma unroll
-        for (int i = 0; i < W; ++i) raw[i] = reinterpret_cast<const uint4*>(row + d)[i];
-        const T* t = reinterpret_cast<const T*>(raw);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = to_float<T>(t[i]);
+        load8(row + d, x);
     } else {
+        T* t = reinterpret_cast<T*>(x.w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = d + i < dim ? to_float<T>(row[d + i]) : 0.0f;
+        for (int i = 0; i < 8; ++i) t[i] = d + i < dim ? row[d + i] : from_float<T>(0.0f);
     }
+}
+
+// A thread's rows of a block's tokens, one after the other: token, keys or values (0 or
+// 1) and head, `step` rows apart.
+struct Rows {
+    int t, row, heads, dt, dr;
+    __device__ __forceinline__ Rows(int first, int step, int heads_) : heads(heads_) {
+        const int of_token = 2 * heads;
+        t = first / of_token;
+        row = first - t * of_token;
+        dt = step / of_token;
+        dr = step - dt * of_token;
+    }
+    __device__ __forceinline__ int kv() const { return row >= heads; }
+    __device__ __forceinline__ int head() const { return row >= heads ? row - heads : row; }
+    __device__ __forceinline__ void next() {
+        t += dt;
+        row += dr;
+        if (row >= 2 * heads) {
+            row -= 2 * heads;
+            ++t;
+        }
+    }
+};
+
+// The places of a block's tokens.  The starts go to shared memory where they fit: the
+// search's steps wait for one another.
+constexpr int kStarts = 512;
+__device__ __forceinline__ void find_places(const CacheView& c, const BatchView& b, int64_t t0, int here, Place* places) {
+    __shared__ int32_t starts[kStarts + 1];
+    const bool fit = b.batch <= kStarts;
+    if (fit) {
+        for (int i = threadIdx.x; i <= b.batch; i += kThreads) starts[i] = b.starts[i];
+        __syncthreads();
+    }
+    if ((int)threadIdx.x < here) places[threadIdx.x] = place_of(c, b, fit ? starts : b.starts, t0 + threadIdx.x);
+    __syncthreads();
 }
 
 template <typename T>
@@ -46,67 +79,89 @@ struct Append {
 };
 
 template <typename T, int FMT, int WIDTH>
-__global__ void __launch_bounds__(kThreads) append_kernel(const Append<T> a, int tokens) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 2 : 3) append_kernel(const Append<T> a, int tokens) {
     constexpr int LANES = WIDTH / 8, BLOCK = mx4_block(FMT), SHARE = BLOCK / 8, BLOCKS = WIDTH / BLOCK;
-    extern __shared__ float4 turns[];  // [tokens][half]
+    // [tokens][8 stride]: pair 8 i + k of a token at k stride + i, so that neighbouring lanes read neighbouring words
+    extern __shared__ float4 turns[];
+    const int stride = (a.half + 7) / 8;
     __shared__ Place places[kMostTokens];
     pdl_wait();
     pdl_launch_dependents();
     const int64_t t0 = (int64_t)blockIdx.x * tokens;
     const int here = (int)min((int64_t)tokens, a.b.tokens - t0);
-    for (int i = 0; i < here; ++i) {
-        const Place p = place_of(a.b, t0 + i);
-        if (threadIdx.x == 0) places[i] = p;
-    }
-    __syncthreads();
+    find_places(a.c, a.b, t0, here, places);
     if (a.turns != nullptr) {
         for (int i = threadIdx.x; i < here * a.half; i += kThreads) {
-            const Turn t = times(turn_of((uint64_t)(int64_t)places[i / a.half].position * a.turns[i % a.half]), a.m, a.ml);
-            turns[i] = make_float4(t.c, t.cl, t.s, t.sl);
+            const int k = i / a.half, pair = i - k * a.half;
+            const Turn t = times(turn_of((uint64_t)(int64_t)places[k].position * a.turns[pair]), a.m, a.ml);
+            turns[(k * 8 + pair % 8) * stride + pair / 8] = make_float4(t.c, t.cl, t.s, t.sl);
         }
         __syncthreads();
     }
     const int lane = threadIdx.x % LANES, d = lane * 8;
-    const int heads = a.c.heads, rows = here * 2 * heads;
-    for (int row = threadIdx.x / LANES; row < (int)round_up(rows, 32 / LANES); row += kThreads / LANES) {
-        // whole warps take part in the exchanges below
-        const int r = min(row, rows - 1);
-        const int t = r / (2 * heads), kv = r / heads % 2, head = r % heads;
+    // whole warps take part in the exchanges below; a thread has its next row's values on the way
+    const int rows = here * 2 * a.c.heads, whole = (int)round_up(rows, 32 / LANES);
+    Rows at(threadIdx.x / LANES, kThreads / LANES, a.c.heads);
+    const auto source = [&](const Rows& r) {
+        return r.kv() == 0 ? a.k + (t0 + r.t) * a.kt + r.head() * a.kh : a.v + (t0 + r.t) * a.vt + r.head() * a.vh;
+    };
+    Eight<T> now, following{};
+    if (at.t < here) load_values(source(at), d, a.c.dim, at.kv() == 0 ? a.vec_k : a.vec_v, following);
+    for (int row = threadIdx.x / LANES; row < whole; row += kThreads / LANES) {
+        now = following;
+        const Rows r = at;
+        at.next();
+        if (row + kThreads / LANES < rows) load_values(source(at), d, a.c.dim, at.kv() == 0 ? a.vec_k : a.vec_v, following);
+        const int t = min(r.t, here - 1), kv = r.kv(), head = r.head();
         const Place p = places[t];
-        const int page = p.sequence < 0 ? -1 : page_of(a.c, a.b, p.sequence, p.position);
+        const int page = p.page;
         const bool store = row < rows && page >= 0;
         float x[8];
+        unpack8(now, x);
+        // lanes whose values are turned: whole rows' first lanes
+        const uint32_t turning = __ballot_sync(~0u, kv == 0 && a.turns != nullptr && d < 2 * a.half);
         if (kv == 0) {
             const T* src = a.k + (t0 + t) * a.kt + head * a.kh;
-            load_values(src, d, a.c.dim, a.vec_k, x);
             if (a.turns != nullptr && d < 2 * a.half) {
-                const float4* turn = turns + t * a.half;
+                const auto turn = [&](int pair) { return turns[(t * 8 + pair % 8) * stride + pair / 8]; };
                 if (a.interleaved) {
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {
                         if (d + i < 2 * a.half) {
-                            const float4 w = turn[(d + i) / 2];
+                            const float4 w = turn((d + i) / 2);
                             const float u = x[i], v = x[i + 1];
                             x[i] = sum_of_products(u, w.x, w.y, -v, w.z, w.w);
                             x[i + 1] = sum_of_products(u, w.z, w.w, v, w.x, w.y);
                         }
                     }
-                } else {
+                } else if (a.half % 8 == 0) {
+                    // the partners are another lane's
+                    const bool second = d >= a.half;
+                    const int from = (threadIdx.x & 31) + (second ? -a.half : a.half) / 8;
+                    const float4* at_pair = turns + t * 8 * stride + (second ? d - a.half : d) / 8;
+                    Eight<T> partner;
+#pragma unroll
+                    for (int i = 0; i < (int)sizeof(T) * 2; ++i) partner.w[i] = __shfl_sync(turning, now.w[i], from);
+                    float other[8];
+                    unpack8(partner, other);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
+                        const float4 w = at_pair[i * stride];
+                        x[i] = sum_of_products(x[i], w.x, w.y, second ? other[i] : -other[i], w.z, w.w);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {  // (first, second) of a pair: first cos - second sin, second cos + first sin
                         const int e = d + i;
-                        if (e < a.half) {
-                            const float4 w = turn[e];
-                            x[i] = sum_of_products(x[i], w.x, w.y, -to_float<T>(src[e + a.half]), w.z, w.w);
-                        } else if (e < 2 * a.half) {
-                            const float4 w = turn[e - a.half];
-                            x[i] = sum_of_products(to_float<T>(src[e - a.half]), w.z, w.w, x[i], w.x, w.y);
-                        }
+                        if (e >= 2 * a.half) break;
+                        const bool second = e >= a.half;
+                        const int pair = second ? e - a.half : e;
+                        const float4 w = turn(pair);
+                        const float other = to_float<T>(src[second ? pair : e + a.half]);
+                        x[i] = sum_of_products(x[i], w.x, w.y, second ? other : -other, w.z, w.w);
                     }
                 }
             }
-        } else {
-            load_values(a.v + (t0 + t) * a.vt + head * a.vh, d, a.c.dim, a.vec_v, x);
         }
         uint32_t most = 0, finite = 0;
 #pragma unroll
@@ -139,10 +194,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Append<T> a, int
             for (int i = 0; i < 8; ++i) y[i] = quotient(x[i], step, inverse);
         }
         if (store) {
-            const int64_t at = cache_row(a.c, page, kv, head, p.position & (a.c.page_size - 1));
-            *reinterpret_cast<uint32_t*>(a.c.codes + at * (WIDTH / 2) + lane * 4) = e2m1_pack8(y);
-            if (lane % SHARE == 0) a.c.scales[at * BLOCKS + lane / SHARE] = (uint8_t)byte;
-            if (lane == 0) a.c.exponents[at] = (int8_t)(FMT == kNvfp4 && finite == 0u ? -127 : e);
+            const int64_t to = cache_row(a.c, page, kv, head, p.position & (a.c.page_size - 1));
+            *reinterpret_cast<uint32_t*>(a.c.codes + to * (WIDTH / 2) + lane * 4) = e2m1_pack8(y);
+            if (lane % SHARE == 0) a.c.scales[to * BLOCKS + lane / SHARE] = (uint8_t)byte;
+            if (lane == 0) a.c.exponents[to] = (int8_t)(FMT == kNvfp4 && finite == 0u ? -127 : e);
         }
     }
 }
@@ -164,18 +219,16 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Read<T> a, int tok
     pdl_launch_dependents();
     const int64_t t0 = (int64_t)blockIdx.x * tokens;
     const int here = (int)min((int64_t)tokens, a.b.tokens - t0);
-    for (int i = 0; i < here; ++i) {
-        const Place p = place_of(a.b, t0 + i);
-        if (threadIdx.x == 0) places[i] = p;
-    }
-    __syncthreads();
+    find_places(a.c, a.b, t0, here, places);
     const int lane = threadIdx.x % LANES, d = lane * 8;
-    const int heads = a.c.heads, rows = here * 2 * heads;
-    for (int row = threadIdx.x / LANES; row < rows; row += kThreads / LANES) {
-        const int t = row / (2 * heads), kv = row / heads % 2, head = row % heads;
+    const int rows = here * 2 * a.c.heads;
+    Rows r(threadIdx.x / LANES, kThreads / LANES, a.c.heads);
+#pragma unroll 2
+    for (int row = threadIdx.x / LANES; row < rows; row += kThreads / LANES, r.next()) {
+        const int t = r.t, kv = r.kv(), head = r.head();
         const Place p = places[t];
         if (p.sequence < 0 || d >= a.c.dim) continue;
-        const int page = page_of(a.c, a.b, p.sequence, p.position);
+        const int page = p.page;
         float y[8];
         if (page < 0) {
 #pragma unroll
@@ -198,7 +251,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Read<T> a, int tok
         }
         T* out = kv == 0 ? a.k + (t0 + t) * a.kt + head * a.kh : a.v + (t0 + t) * a.vt + head * a.vh;
         if ((kv == 0 ? a.vec_k : a.vec_v) && d + 8 <= a.c.dim) {
-            store8(out + d, y);
+            pack8(out + d, y);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -214,12 +267,11 @@ bool whole_rows(const void* p, int64_t tokens, int64_t per_token, int64_t heads,
     return (uintptr_t)p % 16 == 0 && (tokens <= 1 || per_token % per == 0) && (heads <= 1 || per_head % per == 0);
 }
 
-// A block's rows in one or two rounds of its threads, with enough blocks for the
-// machine first.
+// As many tokens to a block as leave each SM several blocks: a block's start (places,
+// angles) costs more than its rows.
 inline int tokens_of_block(const CacheView& c, int64_t tokens) {
-    const int rows = kThreads / (c.width / 8);  // at once
     int n = 1;
-    while (n < kMostTokens && n * 2 * c.heads < 2 * rows && tokens >= 8LL * n * device_sms()) n *= 2;
+    while (n < kMostTokens && tokens >= 12LL * n * device_sms()) n *= 2;
     return n;
 }
 
@@ -229,7 +281,7 @@ cudaError_t append(const CacheAppend& g, cudaStream_t st) {
                 whole_rows<T>(g.k, g.batch.tokens, g.kt, g.cache.heads, g.kh),
                 whole_rows<T>(g.v, g.batch.tokens, g.vt, g.cache.heads, g.vh), g.turns, g.half, g.m, g.ml, g.interleaved};
     const int tokens = tokens_of_block(g.cache, g.batch.tokens);
-    const size_t smem = g.turns ? (size_t)tokens * g.half * sizeof(float4) : 0;
+    const size_t smem = g.turns ? (size_t)tokens * round_up(g.half, 8) * sizeof(float4) : 0;
     return launch_pdl(append_kernel<T, FMT, WIDTH>, dim3((unsigned)((g.batch.tokens + tokens - 1) / tokens)), dim3(kThreads), smem, st, a, tokens);
 }
 

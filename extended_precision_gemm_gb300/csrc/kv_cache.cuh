@@ -19,12 +19,6 @@ inline int cache_width(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 :
 
 #ifdef __CUDACC__
 
-// What a call's token is: its sequence and position, -1 for a token of none.
-struct Place {
-    int sequence;
-    int position;
-};
-
 // Row number of token `offset` of a page.
 __device__ __forceinline__ int64_t cache_row(const CacheView& c, int64_t page, int kv, int head, int offset) {
     return ((page * 2 + kv) * c.heads + head) * (int64_t)c.page_size + offset;
@@ -38,16 +32,22 @@ __device__ __forceinline__ int page_of(const CacheView& c, const BatchView& b, i
     return p >= 0 && p < c.pages ? p : -1;
 }
 
-// The sequence of token t, found by a whole block: the number of sequences that
-// end at or before t.
-__device__ __forceinline__ Place place_of(const BatchView& b, int64_t t) {
-    int count = 0;
-    for (int i = 0; i < b.batch; i += blockDim.x) {
-        const int s = i + (int)threadIdx.x;
-        count += __syncthreads_count(s < b.batch && b.starts[s + 1] <= t);
+// What a call's token is: its sequence (-1 for a token of none), position, and page (-1
+// where it has none in the cache).
+struct Place {
+    int sequence, position, page;
+};
+// `starts`: those of the batch, here or in shared memory.
+__device__ __forceinline__ Place place_of(const CacheView& c, const BatchView& b, const int32_t* starts, int64_t t) {
+    int low = 0, high = b.batch;  // the number of sequences that end at or before t is in [low, high]
+    while (low < high) {
+        const int mid = (low + high) / 2;
+        if (starts[mid + 1] <= t) low = mid + 1;
+        else high = mid;
     }
-    if (count >= b.batch || b.starts[count] > t) return {-1, -1};
-    return {count, b.lengths[count] - (b.starts[count + 1] - (int)t)};
+    if (low >= b.batch || starts[low] > t) return {-1, -1, -1};
+    const int position = b.lengths[low] - (starts[low + 1] - (int)t);
+    return {low, position, page_of(c, b, low, position)};
 }
 
 #endif  // __CUDACC__

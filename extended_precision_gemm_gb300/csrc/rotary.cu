@@ -3,8 +3,8 @@
 //
 // Bound by HBM: each value is read once and written once.  The angles of a block's
 // tokens are computed once, a thread for a pair, and shared by all its heads.
+#include "eight.cuh"
 #include "launch.cuh"
-#include "mx4.cuh"
 #include "rotary.cuh"
 
 namespace ddg {
@@ -13,83 +13,112 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTokens = 4;  // tokens of a block where there are many
 
-// Eight elements from a 16-byte aligned address on.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
-    constexpr int W = sizeof(T) * 8 / 16;
-    uint4 raw[W];
-#pragma unroll
-    for (int i = 0; i < W; ++i) raw[i] = reinterpret_cast<const uint4*>(p)[i];
-    const T* t = reinterpret_cast<const T*>(raw);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = to_float<T>(t[i]);
-}
-
 __device__ __forceinline__ void turn_pair(float& a, float& b, float2 t) {
     const float x = a, y = b;
     a = fmaf(x, t.x, -(y * t.y));
     b = fmaf(x, t.y, y * t.x);
 }
 
-// A unit of work is 8 elements of a head and their partners (VEC: everything in
-// 16-byte pieces), or a pair, or what lies behind the turned part.  Threads:
-// x units of a head, y rows (token, head).
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const Rotary r, int tokens, int heads) {
-    extern __shared__ float2 turns[];  // [tokens][half]
+// A unit of work is 8 elements of a head and their partners (kHalf, kInterleaved: all in
+// 16-byte pieces), or a pair (kSingle), or what lies behind the turned part.  Threads: x
+// units of a head, y heads.
+enum Mode { kSingle, kHalf, kInterleaved };
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const Rotary r, int tokens, int heads) {
+    constexpr int PER = MODE == kSingle ? 1 : MODE == kHalf ? 8 : 4;  // pairs of a unit
+    constexpr int ROWS = MODE == kHalf ? 2 : 4;                       // heads whose loads a thread has in flight
+    // [tokens][half], pair u PER + i of a token at i half / PER + u: neighbouring threads read neighbouring words (as
+    // they lie a warp's reads would meet in a few banks, half of the time of 8192 x 40 x 128)
+    extern __shared__ float2 turns[];
     pdl_wait();
     pdl_launch_dependents();
     const int64_t t0 = (int64_t)blockIdx.x * tokens;
     const int here = (int)min((int64_t)tokens, r.T - t0);
-    const int h0 = blockIdx.y * heads, hs = min(heads, r.H - h0);
+    const int h0 = blockIdx.y * heads, hs = min(heads, r.H - h0), stride = r.half / PER;
     const int thread = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
     for (int i = thread; i < here * r.half; i += threads) {
-        const int64_t t = t0 + i / r.half;
+        const int k = i / r.half, pair = i - k * r.half;
+        const int64_t t = t0 + k;
         const int64_t p = r.wide ? static_cast<const int64_t*>(r.positions)[t] : static_cast<const int32_t*>(r.positions)[t];
-        const Turn a = times(turn_of((uint64_t)p * r.turns[i % r.half]), r.m, r.ml);
-        turns[i] = make_float2(a.c, r.inverse ? -a.s : a.s);
+        const Turn a = times(turn_of((uint64_t)p * r.turns[pair]), r.m, r.ml);
+        turns[k * r.half + pair % PER * stride + pair / PER] = make_float2(a.c, r.inverse ? -a.s : a.s);
     }
     __syncthreads();
-    const int rows = here * hs;
-    int t = 0, h = threadIdx.y;
-    const T* x0 = static_cast<const T*>(r.x) + t0 * r.xt + h0 * r.xh;
-    T* y0 = static_cast<T*>(r.y) + t0 * r.yt + h0 * r.yh;
-    for (int row = threadIdx.y; row < rows; row += blockDim.y, h += blockDim.y) {
-        while (h >= hs) {
-            h -= hs;
-            ++t;
-        }
-        const T* x = x0 + t * r.xt + h * r.xh;
-        T* y = y0 + t * r.yt + h * r.yh;
-        const float2* turn = turns + t * r.half;
+    const T* x0 = static_cast<const T*>(r.x) + t0 * r.xt + (int64_t)h0 * r.xh;
+    T* y0 = static_cast<T*>(r.y) + t0 * r.yt + (int64_t)h0 * r.yh;
+    if constexpr (MODE != kSingle) {
+        const int64_t xs = (int64_t)blockDim.y * r.xh, ys = (int64_t)blockDim.y * r.yh;
         for (int u = threadIdx.x; u < r.units; u += blockDim.x) {
-            if (VEC) {
-                float a[8], b[8];
-                if (u * 8 >= (r.interleaved ? 2 * r.half : r.half)) {
-                    const int d = u * 8 + (r.interleaved ? 0 : r.half);
-                    load8(x + d, a);
-                    store8(y + d, a);
-                } else if (r.interleaved) {
-                    load8(x + u * 8, a);
+            const bool copied = u * 8 >= (MODE == kHalf ? r.half : 2 * r.half);
+            const int d = u * 8 + (copied && MODE == kHalf ? r.half : 0);
+            const T* xt = x0 + threadIdx.y * r.xh + d;
+            T* yt = y0 + threadIdx.y * r.yh + d;
+            for (int t = 0; t < here; ++t, xt += r.xt, yt += r.yt) {
+                float2 turn[PER];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) turn_pair(a[2 * i], a[2 * i + 1], turn[u * 4 + i]);
-                    store8(y + u * 8, a);
-                } else {
-                    load8(x + u * 8, a);
-                    load8(x + r.half + u * 8, b);
+                for (int i = 0; i < PER; ++i) turn[i] = copied ? make_float2(1.0f, 0.0f) : turns[t * r.half + u + i * stride];
+                const T* x = xt;
+                T* y = yt;
+                for (int h = threadIdx.y; h < hs; h += ROWS * blockDim.y, x += ROWS * xs, y += ROWS * ys) {
+                    Eight<T> a[ROWS], b[MODE == kHalf ? ROWS : 1];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) turn_pair(a[i], b[i], turn[u * 8 + i]);
-                    store8(y + u * 8, a);
-                    store8(y + r.half + u * 8, b);
+                    for (int k = 0; k < ROWS; ++k) {
+                        if (h + k * (int)blockDim.y >= hs) break;
+                        load8(x + k * xs, a[k]);
+                        if (MODE == kHalf && !copied) load8(x + k * xs + r.half, b[k]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < ROWS; ++k) {
+                        if (h + k * (int)blockDim.y >= hs) break;
+                        if (copied) {
+                            float v[8];
+                            unpack8(a[k], v);
+                            pack8(y + k * ys, v);
+                            continue;
+                        }
+                        float v[8], w[8];
+                        unpack8(a[k], v);
+                        if (MODE == kHalf) {
+                            unpack8(b[k], w);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) turn_pair(v[i], w[i], turn[i % PER]);
+                            pack8(y + k * ys + r.half, w);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) turn_pair(v[2 * i], v[2 * i + 1], turn[i % PER]);
+                        }
+                        pack8(y + k * ys, v);
+                    }
                 }
-            } else if (u < r.half) {
-                const int i = r.interleaved ? 2 * u : u, j = r.interleaved ? 2 * u + 1 : u + r.half;
-                float a = to_float<T>(x[i]), b = to_float<T>(x[j]);
-                turn_pair(a, b, turn[u]);
-                y[i] = from_float<T>(a);
-                y[j] = from_float<T>(b);
+            }
+        }
+    } else {
+        // units of all heads of all tokens, one after the other
+        const int all = here * hs * r.units, step = threads / r.units, rest = threads - step * r.units;
+        int row = thread / r.units, u = thread - row * r.units, t = row / hs, h = row - t * hs;
+        const int dt = step / hs, dh = step - dt * hs;
+        for (int i = thread; i < all; i += threads) {
+            const T* x = x0 + t * r.xt + h * r.xh;
+            T* y = y0 + t * r.yt + h * r.yh;
+            if (u < r.half) {
+                const int j = r.interleaved ? 2 * u : u, k = r.interleaved ? 2 * u + 1 : u + r.half;
+                float a = to_float<T>(x[j]), b = to_float<T>(x[k]);
+                turn_pair(a, b, turns[t * r.half + u]);
+                y[j] = from_float<T>(a);
+                y[k] = from_float<T>(b);
             } else {
                 y[u + r.half] = x[u + r.half];
+            }
+            u += rest;
+            h += dh;
+            t += dt;
+            if (u >= r.units) {
+                u -= r.units;
+                ++h;
+            }
+            while (h >= hs) {
+                h -= hs;
+                ++t;
             }
         }
     }
@@ -105,14 +134,18 @@ cudaError_t launch(Rotary r, cudaStream_t st) {
     const int end = r.x == r.y ? 2 * r.half : r.D;
     r.units = vec ? (r.interleaved ? end : end - r.half) / 8 : end - r.half;
     const int ux = r.units < 64 ? r.units : 64, uy = kThreads / ux > 0 ? kThreads / ux : 1;
-    // few tokens: a block for as many heads as it has rows of threads
-    const int tokens = r.T >= 8 * device_sms() ? kTokens : 1;
+    // few tokens: a block for as many heads as it has rows of threads; many: several heads for a thread, which share
+    // the token's angles
+    const bool many = r.T >= 8 * device_sms();
+    const int tokens = many ? kTokens : 1;
     const int heads = r.T >= 2 * device_sms() || r.H <= uy ? r.H : uy;
+    const int most = many ? (uy + 1) / 2 : uy, rounds = (heads + most - 1) / most, rows = (heads + rounds - 1) / rounds;
     const int64_t blocks = (r.T + tokens - 1) / tokens;
-    const dim3 grid((unsigned)blocks, (unsigned)((r.H + heads - 1) / heads)), block((unsigned)ux, (unsigned)uy);
+    const dim3 grid((unsigned)blocks, (unsigned)((r.H + heads - 1) / heads)), block(vec ? (unsigned)ux : kThreads, vec ? (unsigned)rows : 1);
     const size_t smem = (size_t)tokens * r.half * sizeof(float2);
-    return vec ? launch_pdl(rotary_kernel<T, true>, grid, block, smem, st, r, tokens, heads)
-               : launch_pdl(rotary_kernel<T, false>, grid, block, smem, st, r, tokens, heads);
+    return !vec ? launch_pdl(rotary_kernel<T, kSingle>, grid, block, smem, st, r, tokens, heads)
+                : r.interleaved ? launch_pdl(rotary_kernel<T, kInterleaved>, grid, block, smem, st, r, tokens, heads)
+                                : launch_pdl(rotary_kernel<T, kHalf>, grid, block, smem, st, r, tokens, heads);
 }
 
 }  // namespace
