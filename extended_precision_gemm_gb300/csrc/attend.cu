@@ -95,12 +95,11 @@ __device__ __forceinline__ void copy16(uint32_t to, const uint8_t* from) {
 __device__ __forceinline__ void close_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// A group of 16 tokens on its way: a warp copies it to shared memory kAhead groups
+// A group of 16 tokens on its way: a warp copies it to shared memory one or two rounds
 // ahead, and a lane (r, c) = (lane / 4, lane % 4) reads of keys a quarter c of tokens r
 // and r + 8, of values the eighth r of tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9.  Two
 // tokens' values are followed by 32 bytes of nothing: their readers are on different
 // banks then.
-constexpr int kStages = 4, kAhead = kStages - 1;
 template <int WIDTH, int FMT>
 struct Stage {
     static constexpr int KW = WIDTH / 32, VW = WIDTH / 64;                 // words of codes of a token
@@ -111,6 +110,7 @@ struct Stage {
     static constexpr int V0 = 16 * ROW, S0 = V0 + 16 * ROW + 8 * 32;       // values' codes, scales of keys and values
     static constexpr int E0 = S0 + 32 * BLOCKS, BYTES = E0 + 32;           // exponents of keys and values
     static constexpr int PIECES = 2 * BLOCKS + 2;                          // of scales and exponents, 16 bytes each
+    static constexpr int STAGES = WIDTH == 256 ? 2 : 3;                    // of two groups, which a round takes together
 
     // The lane's places in the first group of 16 rows of the cache.
     struct Base {
@@ -146,7 +146,6 @@ struct Stage {
             for (int i = 0; i < (PIECES + 31) / 32; ++i)
                 if (lane + 32 * i < PIECES) copy16(to + S0 + (lane + 32 * i) * 16, b.small[i] + (uint64_t)(uint32_t)row * b.small_stride[i]);
         }
-        close_copies();
     }
 };
 
@@ -189,7 +188,7 @@ struct Cut {
     // the CTA that has group g
     __device__ __forceinline__ int64_t owner(int64_t g) const { return ((g + 1) * ctas - 1) / total; }
 };
-constexpr int kLeast = 4;
+constexpr int kLeast = 8;
 __device__ __forceinline__ Cut cut_of(int64_t total, int ctas) {
     return Cut{total, max((int64_t)1, min((int64_t)ctas, total / kLeast))};
 }
@@ -220,11 +219,12 @@ __device__ __forceinline__ int64_t cost_of(const AttendArgs& a, const Sequence& 
 // One CTA: its run of groups, item by item; of an item's groups the warps take one after
 // the other in turn.
 template <typename T, int WIDTH, int FMT>
-__global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : 4) attend_columns_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : WIDTH == 128 ? 3 : 4) attend_columns_kernel(const AttendArgs a) {
     using G = Stage<WIDTH, FMT>;
     constexpr int KS = WIDTH / 16;  // MMAs along the head
     constexpr bool REST = std::is_same_v<T, __half>;
     constexpr int ROW = WIDTH + 4;  // a column's sums in shared memory
+    constexpr int kStages = G::STAGES, kAhead = kStages - 1;
     extern __shared__ __align__(16) uint8_t shared[];  // [warp][stage], and [warp][8][ROW] floats behind an item's last group
     float* const sums = reinterpret_cast<float*>(shared);
     __shared__ float s_m[kWarps][8], s_M[kWarps][8], s_l[kWarps][8];
@@ -304,29 +304,33 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : 4) attend_colu
         const int before = seq.length - seq.tokens;  // the position of the first query token
         const int p0 = before + column0 / a.group, p1 = before + (column0 + columns - 1) / a.group;
 
-        // rows of the keys of the groups of 32 rounds, a lane each
-        const int mine = g1 - g0 > warp ? (g1 - g0 - warp + kWarps - 1) / kWarps : 0;
+        // the warp's groups are pair warp, warp + kWarps, ... of the run; rows of the keys of 16 pairs, a lane each
+        const int pairs = (g1 - g0 + 1) / 2, mine = pairs > warp ? (pairs - warp + kWarps - 1) / kWarps : 0;
         int rows = -1;
         const auto rows_from = [&](int i) {
-            const int g = g0 + warp + (i + lane) * kWarps;
+            const int g = g0 + 2 * (warp + (i + lane / 2) * kWarps) + lane % 2;
             rows = -1;
             if (g < g1) {
                 const int token = group_token(groups, g), page = page_of(a.c, a.b, b, token);
                 if (page >= 0) rows = (int)(cache_row(a.c, page, 0, head, token & (a.c.page_size - 1)) / 16);
             }
         };
-        const uint32_t ring = smem_addr(shared) + warp * kStages * G::BYTES;
-        uint32_t bad_groups = 0;  // bit 0: the group of the round at hand has no page; the next rounds above it
+        const uint32_t ring = smem_addr(shared) + warp * kStages * 2 * G::BYTES;
+        uint32_t bad_groups = 0;  // two bits a round: the groups of the round at hand that have no page; the next rounds above
         const auto copy = [&](int i, uint32_t stage) {  // of round i, if there is one; a group of copies either way
-            if (i % 32 == 0 && i < mine) rows_from(i);
-            const int row = i < mine ? __shfl_sync(~0u, rows, i % 32) : -1;
-            bad_groups |= (uint32_t)(row < 0) << kAhead;
-            G::copy(base, row, ring + stage, lane);
+            if (i % 16 == 0 && i < mine) rows_from(i);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int row = i < mine ? __shfl_sync(~0u, rows, i % 16 * 2 + k) : -1;
+                bad_groups |= (uint32_t)(row < 0) << (2 * kAhead + k);
+                G::copy(base, row, ring + stage + k * G::BYTES, lane);
+            }
+            close_copies();
         };
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            copy(i, i * G::BYTES);
-            bad_groups >>= 1;
+            copy(i, i * 2 * G::BYTES);
+            bad_groups >>= 2;
         }
         // groups that every column sees as a whole: list numbers from whole0 to whole1 - 1
         const int whole0 = a.window > 0 && p1 >= a.window ? max(groups.sink, groups.sink + (p1 - a.window) / 16 + 1 - groups.low) : 0;
@@ -392,53 +396,65 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : 4) attend_colu
         for (int i = 0; i < mine; ++i) {
             wait_copies<kAhead - 1>();
             __syncwarp();
-            const bool bad = bad_groups & 1;
-            const int group = g0 + warp + i * kWarps;
-            const bool whole = group >= whole0 && group < whole1 && !bad;
-            const uint8_t* const at = shared + warp * kStages * G::BYTES + stage;
+            const uint32_t bad = bad_groups & 3;
+            const int group = g0 + 2 * (warp + i * kWarps);
+            const bool whole = group >= whole0 && group + 1 < whole1 && group + 1 < g1 && bad == 0;
+            const uint8_t* const at = shared + warp * kStages * 2 * G::BYTES + stage;
             // the stage of the round before is free: every lane has read it
-            copy(i + kAhead, stage == 0 ? kAhead * G::BYTES : stage - G::BYTES);
-            bad_groups >>= 1;
-            stage = stage == kAhead * G::BYTES ? 0 : stage + G::BYTES;
+            copy(i + kAhead, stage == 0 ? kAhead * 2 * G::BYTES : stage - 2 * G::BYTES);
+            bad_groups >>= 2;
+            stage = stage == kAhead * 2 * G::BYTES ? 0 : stage + 2 * G::BYTES;
 
-            // scores: tokens r and r + 8 in rows r and r + 8
-            uint32_t k[2][G::KW], ks[2][G::KB];
-            int ke[2], ve[2];
+            // scores: of each group tokens r and r + 8 in rows r and r + 8
+            float s[2][4], u[2][4];
+            const auto score_group = [&](auto N) {
+                constexpr int n = decltype(N)::value;
+                const uint8_t* const from = at + n * G::BYTES;
+                uint32_t k[2][G::KW], ks[2][G::KB];
+                int ke[2];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                ke[t] = reinterpret_cast<const int8_t*>(at + G::E0)[r + 8 * t];
-                ve[t] = reinterpret_cast<const int8_t*>(at + G::E0 + 16)[r + 8 * t];
-                load_words<G::KW>(at + (r + 8 * t) * G::ROW + c * (G::ROW / 4), k[t]);
-                half_scales<FMT, G::KB>(at + G::S0 + (r + 8 * t) * G::BLOCKS + c * (WIDTH / 4) / G::BLOCK, ke[t], ks[t]);
-            }
-            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s2[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // two chains of MMAs
-            constexpr int PER = KS / G::KB;  // MMAs of a block of a lane's codes
-            auto score_step = [&](auto J) {
-                constexpr int j = decltype(J)::value;
-                const uint32_t x = ks[0][j / PER], y = ks[1][j / PER];
-                constexpr int w = j / 2, lo = j % 2 * 2;
-                mma16816(j % 2 ? s2 : s, mul_half2(codes2<lo>(k[0][w]), x), mul_half2(codes2<lo>(k[1][w]), y),
-                         mul_half2(codes2<lo + 1>(k[0][w]), x), mul_half2(codes2<lo + 1>(k[1][w]), y), q[j][0], q[j][1]);
+                for (int t = 0; t < 2; ++t) {
+                    ke[t] = reinterpret_cast<const int8_t*>(from + G::E0)[r + 8 * t];
+                    load_words<G::KW>(from + (r + 8 * t) * G::ROW + c * (G::ROW / 4), k[t]);
+                    half_scales<FMT, G::KB>(from + G::S0 + (r + 8 * t) * G::BLOCKS + c * (WIDTH / 4) / G::BLOCK, ke[t], ks[t]);
+                }
+                float x[4] = {0.0f, 0.0f, 0.0f, 0.0f}, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // two chains of MMAs
+                constexpr int PER = KS / G::KB;  // MMAs of a block of a lane's codes
+                auto score_step = [&](auto J) {
+                    constexpr int j = decltype(J)::value;
+                    const uint32_t s0 = ks[0][j / PER], s1 = ks[1][j / PER];
+                    constexpr int w = j / 2, lo = j % 2 * 2;
+                    mma16816(j % 2 ? y : x, mul_half2(codes2<lo>(k[0][w]), s0), mul_half2(codes2<lo>(k[1][w]), s1),
+                             mul_half2(codes2<lo + 1>(k[0][w]), s0), mul_half2(codes2<lo + 1>(k[1][w]), s1), q[j][0], q[j][1]);
+                };
+                static_for<KS>(score_step);
+                // 2^-127 counts as 0: rows of zeros have it, and those below 2^-125
+                const float k0 = __uint_as_float((uint32_t)(ke[0] + 127) << 23), k1 = __uint_as_float((uint32_t)(ke[1] + 127) << 23);
+                s[n][0] = (x[0] + y[0]) * qf0 * k0;
+                s[n][1] = (x[1] + y[1]) * qf1 * k0;
+                s[n][2] = (x[2] + y[2]) * qf0 * k1;
+                s[n][3] = (x[3] + y[3]) * qf1 * k1;
+                float e0 = (float)reinterpret_cast<const int8_t*>(from + G::E0 + 16)[r], e1 = (float)reinterpret_cast<const int8_t*>(from + G::E0 + 16)[r + 8];
+                if (!whole) {
+                    if (bad >> n & 1) {
+                        s[n][0] = s[n][1] = s[n][2] = s[n][3] = not_a_number();
+                        e0 = e1 = 0.0f;
+                    }
+                    const int t0 = group_token(groups, group + n) + r;
+                    const bool there = group + n < g1;
+                    if (!there || !sees(pa, t0, a.window, a.sinks)) s[n][0] = minus_infinity();
+                    if (!there || !sees(pb, t0, a.window, a.sinks)) s[n][1] = minus_infinity();
+                    if (!there || !sees(pa, t0 + 8, a.window, a.sinks)) s[n][2] = minus_infinity();
+                    if (!there || !sees(pb, t0 + 8, a.window, a.sinks)) s[n][3] = minus_infinity();
+                }
+                u[n][0] = s[n][0] + e0;
+                u[n][1] = s[n][1] + e0;
+                u[n][2] = s[n][2] + e1;
+                u[n][3] = s[n][3] + e1;
             };
-            static_for<KS>(score_step);
-            // 2^-127 counts as 0: rows of zeros have it, and those below 2^-125
-            const float k0 = __uint_as_float((uint32_t)(ke[0] + 127) << 23), k1 = __uint_as_float((uint32_t)(ke[1] + 127) << 23);
-            s[0] = (s[0] + s2[0]) * qf0 * k0;
-            s[1] = (s[1] + s2[1]) * qf1 * k0;
-            s[2] = (s[2] + s2[2]) * qf0 * k1;
-            s[3] = (s[3] + s2[3]) * qf1 * k1;
-            const int token = whole ? 0 : group_token(groups, group);
-            if (!whole) {
-                const int t0 = token + r;
-                if (bad) s[0] = s[1] = s[2] = s[3] = not_a_number();
-                if (!sees(pa, t0, a.window, a.sinks)) s[0] = minus_infinity();
-                if (!sees(pb, t0, a.window, a.sinks)) s[1] = minus_infinity();
-                if (!sees(pa, t0 + 8, a.window, a.sinks)) s[2] = minus_infinity();
-                if (!sees(pb, t0 + 8, a.window, a.sinks)) s[3] = minus_infinity();
-            }
-            const float e0 = bad ? 0.0f : (float)ve[0], e1 = bad ? 0.0f : (float)ve[1];
-            float u[4] = {s[0] + e0, s[1] + e0, s[2] + e1, s[3] + e1};
-            const float sa = fmaxf(s[0], s[2]), sb = fmaxf(s[1], s[3]), ua = fmaxf(u[0], u[2]), ub = fmaxf(u[1], u[3]);
+            static_for<2>(score_group);
+            const float sa = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2])), sb = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
+            const float ua = fmaxf(fmaxf(u[0][0], u[0][2]), fmaxf(u[1][0], u[1][2])), ub = fmaxf(fmaxf(u[0][1], u[0][3]), fmaxf(u[1][1], u[1][3]));
             if (__any_sync(~0u, sa > ma + kLag || sb > mb + kLag || ua > Ma + kLag || ub > Mb + kLag)) {
                 float na = sa, nb = sb, Na = ua, Nb = ub;
 #pragma unroll
@@ -465,85 +481,86 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : 4) attend_colu
                 ma = na, mb = nb, Ma = Na, Mb = Nb;
                 ra = reference(ma), rb = reference(mb), Ra = reference(Ma) - kLift, Rb = reference(Mb) - kLift;
             }
-            la += power2(s[0] - ra) + power2(s[2] - ra);
-            lb += power2(s[1] - rb) + power2(s[3] - rb);
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-                u[i] = power2(u[i] - Ra);
-                u[i + 1] = power2(u[i + 1] - Rb);
-            }
-            const uint32_t h0 = half2_of(u[0], u[1]), h1 = half2_of(u[2], u[3]);
-            const uint32_t w0 = transpose8x8(h0), w1 = transpose8x8(h1);
-            uint32_t x0 = 0, x1 = 0;
-            if (REST) {
-                x0 = transpose8x8(half2_of(u[0] - low_half(h0), u[1] - high_half(h0)));
-                x1 = transpose8x8(half2_of(u[2] - low_half(h1), u[3] - high_half(h1)));
-            }
+            la += (power2(s[0][0] - ra) + power2(s[0][2] - ra)) + (power2(s[1][0] - ra) + power2(s[1][2] - ra));
+            lb += (power2(s[0][1] - rb) + power2(s[0][3] - rb)) + (power2(s[1][1] - rb) + power2(s[1][3] - rb));
 
-            // values: tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9 in rows of the same numbers
-            uint32_t v[4][G::VW], hv[4][G::VB], vs[2][G::VB];
+            const auto weigh_group = [&](auto N) {
+                constexpr int n = decltype(N)::value;
+                const uint8_t* const from = at + n * G::BYTES;
+                const float w[4] = {power2(u[n][0] - Ra), power2(u[n][1] - Rb), power2(u[n][2] - Ra), power2(u[n][3] - Rb)};
+                const uint32_t h0 = half2_of(w[0], w[1]), h1 = half2_of(w[2], w[3]);
+                const uint32_t w0 = transpose8x8(h0), w1 = transpose8x8(h1);
+                uint32_t x0 = 0, x1 = 0;
+                if (REST) {
+                    x0 = transpose8x8(half2_of(w[0] - low_half(h0), w[1] - high_half(h0)));
+                    x1 = transpose8x8(half2_of(w[2] - low_half(h1), w[3] - high_half(h1)));
+                }
+                // values: tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9 in rows of the same numbers
+                uint32_t v[4][G::VW], hv[4][G::VB], vs[2][G::VB];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int row = 2 * c + (t & 1) + (t >> 1) * 8;
-                load_words<G::VW>(at + G::V0 + row * G::ROW + row / 2 * 32 + r * (G::ROW / 8), v[t]);
-                half_scales<FMT, G::VB>(at + G::S0 + 16 * G::BLOCKS + row * G::BLOCKS + r * (WIDTH / 8) / G::BLOCK,
-                                        FMT == kMxfp4 ? reinterpret_cast<const int8_t*>(at + G::E0 + 16)[row] : 0, hv[t]);
-            }
-            if (!whole) {
-                // a NaN reaches only the columns that see its token
+                for (int t = 0; t < 4; ++t) {
+                    const int row = 2 * c + (t & 1) + (t >> 1) * 8;
+                    load_words<G::VW>(from + G::V0 + row * G::ROW + row / 2 * 32 + r * (G::ROW / 8), v[t]);
+                    half_scales<FMT, G::VB>(from + G::S0 + 16 * G::BLOCKS + row * G::BLOCKS + r * (WIDTH / 8) / G::BLOCK,
+                                            FMT == kMxfp4 ? reinterpret_cast<const int8_t*>(from + G::E0 + 16)[row] : 0, hv[t]);
+                }
+                if (!whole) {
+                    // a NaN reaches only the columns that see its token
 #pragma unroll
-                for (int d = 0; d < G::VB; ++d) {
-                    uint32_t nan = 0;
+                    for (int d = 0; d < G::VB; ++d) {
+                        uint32_t nan = 0;
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        if (bad || half_is_nan(hv[t][d])) {
-                            nan |= 1u << t;
-                            hv[t][d] = 0;
-                        }
-                    }
-                    if (__any_sync(~0u, nan != 0)) {
-#pragma unroll 1
-                        for (int cc = 0; cc < 4; ++cc) {
-                            const uint32_t theirs = __shfl_sync(~0u, nan, (lane & ~3) | cc);
-#pragma unroll 1
-                            for (int t = 0; t < 4; ++t) {
-                                if (!(theirs >> t & 1)) continue;
-                                const int j = token + 2 * cc + (t & 1) + (t >> 1) * 8;
-                                const bool hit_a = sees(pa, j, a.window, a.sinks), hit_b = sees(pb, j, a.window, a.sinks);
-                                constexpr int SPAN = KS / G::VB;
-#pragma unroll
-                                for (int i = d * SPAN; i < (d + 1) * SPAN; ++i) {
-                                    if (hit_a) o[i][0] = o[i][2] = not_a_number();
-                                    if (hit_b) o[i][1] = o[i][3] = not_a_number();
-                                }
+                        for (int t = 0; t < 4; ++t) {
+                            if ((bad >> n & 1) || half_is_nan(hv[t][d])) {
+                                nan |= 1u << t;
+                                hv[t][d] = 0;
                             }
                         }
-                        __syncwarp();
+                        if (group + n < g1 && __any_sync(~0u, nan != 0)) {
+#pragma unroll 1
+                            for (int cc = 0; cc < 4; ++cc) {
+                                const uint32_t theirs = __shfl_sync(~0u, nan, (lane & ~3) | cc);
+#pragma unroll 1
+                                for (int t = 0; t < 4; ++t) {
+                                    if (!(theirs >> t & 1)) continue;
+                                    const int j = group_token(groups, group + n) + 2 * cc + (t & 1) + (t >> 1) * 8;
+                                    const bool hit_a = sees(pa, j, a.window, a.sinks), hit_b = sees(pb, j, a.window, a.sinks);
+                                    constexpr int SPAN = KS / G::VB;
+#pragma unroll
+                                    for (int e = d * SPAN; e < (d + 1) * SPAN; ++e) {
+                                        if (hit_a) o[e][0] = o[e][2] = not_a_number();
+                                        if (hit_b) o[e][1] = o[e][3] = not_a_number();
+                                    }
+                                }
+                            }
+                            __syncwarp();
+                        }
                     }
                 }
-            }
 #pragma unroll
-            for (int d = 0; d < G::VB; ++d) {
-                vs[0][d] = both_low(hv[0][d], hv[1][d]);
-                vs[1][d] = both_low(hv[2][d], hv[3][d]);
-            }
-            auto value_word = [&](auto W) {
-                constexpr int w = decltype(W)::value;
-                // bytes of two tokens: even elements in xe, odd ones in xo
-                const uint32_t m = 0x0f0f0f0fu;
-                const uint32_t xe = (v[0][w] & m) | (v[1][w] << 4 & ~m), xo = (v[0][w] >> 4 & m) | (v[1][w] & ~m);
-                const uint32_t ye = (v[2][w] & m) | (v[3][w] << 4 & ~m), yo = (v[2][w] >> 4 & m) | (v[3][w] & ~m);
-                auto tile = [&](auto I) {
-                    constexpr int i = decltype(I)::value, d = w * 4 + i;
-                    constexpr int blk = d / (KS / G::VB);
-                    const uint32_t a0 = mul_half2(codes2<i>(xe), vs[0][blk]), a1 = mul_half2(codes2<i>(xo), vs[0][blk]);
-                    const uint32_t a2 = mul_half2(codes2<i>(ye), vs[1][blk]), a3 = mul_half2(codes2<i>(yo), vs[1][blk]);
-                    mma16816(o[d], a0, a1, a2, a3, w0, w1);
-                    if (REST) mma16816(o[d], a0, a1, a2, a3, x0, x1);
+                for (int d = 0; d < G::VB; ++d) {
+                    vs[0][d] = both_low(hv[0][d], hv[1][d]);
+                    vs[1][d] = both_low(hv[2][d], hv[3][d]);
+                }
+                auto value_word = [&](auto W) {
+                    constexpr int w = decltype(W)::value;
+                    // bytes of two tokens: even elements in xe, odd ones in xo
+                    const uint32_t m = 0x0f0f0f0fu;
+                    const uint32_t xe = (v[0][w] & m) | (v[1][w] << 4 & ~m), xo = (v[0][w] >> 4 & m) | (v[1][w] & ~m);
+                    const uint32_t ye = (v[2][w] & m) | (v[3][w] << 4 & ~m), yo = (v[2][w] >> 4 & m) | (v[3][w] & ~m);
+                    auto tile = [&](auto I) {
+                        constexpr int i = decltype(I)::value, d = w * 4 + i;
+                        constexpr int blk = d / (KS / G::VB);
+                        const uint32_t a0 = mul_half2(codes2<i>(xe), vs[0][blk]), a1 = mul_half2(codes2<i>(xo), vs[0][blk]);
+                        const uint32_t a2 = mul_half2(codes2<i>(ye), vs[1][blk]), a3 = mul_half2(codes2<i>(yo), vs[1][blk]);
+                        mma16816(o[d], a0, a1, a2, a3, w0, w1);
+                        if (REST) mma16816(o[d], a0, a1, a2, a3, x0, x1);
+                    };
+                    static_for<4>(tile);
                 };
-                static_for<4>(tile);
+                static_for<G::VW>(value_word);
             };
-            static_for<G::VW>(value_word);
+            static_for<2>(weigh_group);
         }
         wait_copies<0>();
         __syncthreads();  // the warps' stages become their sums
@@ -758,7 +775,7 @@ __global__ void __launch_bounds__(8 * PER * 32) join_cut_kernel(const AttendArgs
 
 template <int WIDTH, int FMT>
 constexpr size_t columns_smem() {
-    return std::max<size_t>(kWarps * 8 * (WIDTH + 4) * sizeof(float), (size_t)kWarps * kStages * Stage<WIDTH, FMT>::BYTES);
+    return std::max<size_t>(kWarps * 8 * (WIDTH + 4) * sizeof(float), (size_t)kWarps * Stage<WIDTH, FMT>::STAGES * 2 * Stage<WIDTH, FMT>::BYTES);
 }
 template <typename T, int WIDTH, int FMT>
 cudaError_t columns(const AttendArgs& a, cudaStream_t st) {
