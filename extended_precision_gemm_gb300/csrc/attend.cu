@@ -216,9 +216,17 @@ __device__ __forceinline__ int64_t cost_of(const AttendArgs& a, const Sequence& 
     return n;
 }
 
-// One CTA: its run of groups, item by item; of an item's groups the warps take one after
-// the other in turn.
-template <typename T, int WIDTH, int FMT>
+__device__ __forceinline__ float read_cluster(uint32_t local, uint32_t rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr(local, rank)) : "memory");
+    return v;
+}
+
+// One CTA: its run of groups, item by item; of an item's groups the warps take pairs in
+// turn.  TOGETHER: instead a cluster of a.splits CTAs for each item, each with its share
+// of the groups, whose parts are summed through distributed shared memory; for short
+// sequences, where the second launch would take as long as the first.
+template <typename T, int WIDTH, int FMT, bool TOGETHER>
 __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : WIDTH == 128 ? 3 : 4) attend_columns_kernel(const AttendArgs a) {
     using G = Stage<WIDTH, FMT>;
     constexpr int KS = WIDTH / 16;  // MMAs along the head
@@ -237,64 +245,78 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : WIDTH == 128 ?
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane / 4, c = lane % 4;
 
-    // the whole cost, and the sequence in which this CTA's run begins
-    int64_t total = 0, ctas, run, run_end, start;  // run: groups from the item's first on; start: of the sequence's
-    int b;
-    {
-        const int per = (a.b.batch + kWarps * 32 - 1) / (kWarps * 32), b0 = min((int)threadIdx.x * per, a.b.batch), b1 = min(b0 + per, a.b.batch);
-        int64_t mine = 0;
-        Sequence own{0, 0, 0};
-        for (int i = b0; i < b1; ++i) {
-            own = sequence_at(a.b, i);
-            mine += cost_of(a, own);
-        }
-        int64_t upto = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const int64_t v = __shfl_up_sync(~0u, upto, d);
-            if (lane >= d) upto += v;
-        }
-        if (lane == 31) scan[warp] = upto;
-        __syncthreads();
-        int64_t before = upto - mine;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += scan[w];
-            total += scan[w];
-        }
-        total *= a.c.heads;
-        const Cut cut = cut_of(total, a.splits);
-        ctas = cut.ctas;
-        if (total == 0 || blockIdx.x >= ctas) {
-            if (threadIdx.x == 0) a.cuts[blockIdx.x] = CutItem{0, 0, 0, 0, 0, 0};
-            return;
-        }
-        run = cut.first(blockIdx.x);
-        run_end = cut.first(blockIdx.x + 1);
-        int64_t at = before * a.c.heads;
-        for (int i = b0; i < b1; ++i) {
-            if (per > 1) own = sequence_at(a.b, i);
-            const int64_t cost = (per > 1 ? cost_of(a, own) : mine) * a.c.heads;
-            if (run >= at && run < at + cost) {
-                found = i;
-                found_before = at;
-                found_sequence = own;
+    int64_t total = 0, ctas = 0, run = 0, run_end = 0, start = 0;  // run: groups from the item's first on; start: of the sequence's
+    int b, ct = 0, head, g0;
+    Sequence seq;
+    Groups groups;
+    const uint32_t rank = TOGETHER ? blockIdx.y : 0;
+    if constexpr (TOGETHER) {
+        head = (int)(blockIdx.x % a.c.heads);
+        const Item item = item_of(a.b, blockIdx.x / a.c.heads, a.group, 8);
+        if (item.sequence < 0) return;  // the whole cluster
+        b = item.sequence;
+        ct = item.column / 8;
+        seq = Sequence{item.first_token, item.tokens, item.length};
+        groups = tile_groups(a, seq, ct);
+        g0 = (int)((int64_t)groups.count * rank / a.splits);
+        run_end = (int64_t)groups.count * (rank + 1) / a.splits - g0;
+    } else {
+        // the whole cost, and the sequence in which this CTA's run begins
+        {
+            const int per = (a.b.batch + kWarps * 32 - 1) / (kWarps * 32), b0 = min((int)threadIdx.x * per, a.b.batch), b1 = min(b0 + per, a.b.batch);
+            int64_t mine = 0;
+            Sequence own{0, 0, 0};
+            for (int i = b0; i < b1; ++i) {
+                own = sequence_at(a.b, i);
+                mine += cost_of(a, own);
             }
-            at += cost;
+            int64_t upto = mine;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const int64_t v = __shfl_up_sync(~0u, upto, d);
+                if (lane >= d) upto += v;
+            }
+            if (lane == 31) scan[warp] = upto;
+            __syncthreads();
+            int64_t before = upto - mine;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) before += scan[w];
+                total += scan[w];
+            }
+            total *= a.c.heads;
+            const Cut cut = cut_of(total, a.splits);
+            ctas = cut.ctas;
+            if (total == 0 || blockIdx.x >= ctas) {
+                if (threadIdx.x == 0) a.cuts[blockIdx.x] = CutItem{0, 0, 0, 0, 0, 0};
+                return;
+            }
+            run = cut.first(blockIdx.x);
+            run_end = cut.first(blockIdx.x + 1);
+            int64_t at = before * a.c.heads;
+            for (int i = b0; i < b1; ++i) {
+                if (per > 1) own = sequence_at(a.b, i);
+                const int64_t cost = (per > 1 ? cost_of(a, own) : mine) * a.c.heads;
+                if (run >= at && run < at + cost) {
+                    found = i;
+                    found_before = at;
+                    found_sequence = own;
+                }
+                at += cost;
+            }
+            __syncthreads();
+            b = found;
+            start = found_before;
         }
-        __syncthreads();
-        b = found;
-        start = found_before;
+        seq = found_sequence;
+        groups = tile_groups(a, seq, 0);
+        while (run >= start + (int64_t)groups.count * a.c.heads) {
+            start += (int64_t)groups.count * a.c.heads;
+            groups = tile_groups(a, seq, ++ct);
+        }
+        head = (int)((run - start) / groups.count);
+        g0 = (int)((run - start) % groups.count);
     }
-    Sequence seq = found_sequence;
-    int ct = 0, head;
-    Groups groups = tile_groups(a, seq, 0);
-    while (run >= start + (int64_t)groups.count * a.c.heads) {
-        start += (int64_t)groups.count * a.c.heads;
-        groups = tile_groups(a, seq, ++ct);
-    }
-    head = (int)((run - start) / groups.count);
-    int g0 = (int)((run - start) % groups.count);
     const typename G::Base base = G::base_of(a.c, lane);
     constexpr float kSumLift = kLift + (FMT == kMxfp4 ? kMxLift : 0);
 
@@ -605,12 +627,18 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : WIDTH == 128 ?
                 f[w] = power2(s_M[w][col] - reference(M));
             }
             const bool any = before + (column0 + col) / a.group >= 0;
-            const bool complete = g0 == 0 && g1 == groups.count;
+            const bool complete = !TOGETHER && g0 == 0 && g1 == groups.count;
             const int64_t token = seq.first_token + (column0 + col) / a.group, h = head * a.group + (column0 + col) % a.group;
             const int64_t part = (2LL * blockIdx.x + (g0 == 0 ? 1 : 0)) * 8 + col;
             const Finish z = finish_of(m, M, l, kSumLift, any);
             T* out = static_cast<T*>(a.out) + token * a.ot + h * a.oh;
-            if (!complete && at == 0) a.part[part] = make_float4(m, M, l, any ? 1.0f : 0.0f);
+            float* const merged = sums + kWarps * 8 * ROW + col * ROW;
+            if (TOGETHER && at == 0) {
+                merged[WIDTH] = m;
+                merged[WIDTH + 1] = M;
+                merged[WIDTH + 2] = l;
+            }
+            if (!TOGETHER && !complete && at == 0) a.part[part] = make_float4(m, M, l, any ? 1.0f : 0.0f);
 #pragma unroll
             for (int d = at * 4; d < WIDTH; d += LANES * 4) {
                 float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -622,9 +650,46 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : WIDTH == 128 ?
                     y[2] = fmaf(x.z, f[w], y[2]);
                     y[3] = fmaf(x.w, f[w], y[3]);
                 }
-                if (complete) store4(out, d, a.c.dim, a.vec_out, z, y);
+                if (TOGETHER) *reinterpret_cast<float4*>(merged + d) = make_float4(y[0], y[1], y[2], y[3]);
+                else if (complete) store4(out, d, a.c.dim, a.vec_out, z, y);
                 else *reinterpret_cast<float4*>(a.sums + part * WIDTH + d) = make_float4(y[0], y[1], y[2], y[3]);
             }
+        }
+        if constexpr (TOGETHER) {
+            // CTA `rank` sums columns rank, rank + splits, ...
+            cluster_sync();
+            const uint32_t merged = smem_addr(sums + kWarps * 8 * ROW);
+            for (int col = rank; col < columns; col += a.splits) {
+                const uint32_t from = merged + col * ROW * 4;
+                float m = minus_infinity(), M = m, l = 0.0f, f[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (k >= a.splits) break;
+                    m = fmaxf(m, read_cluster(from + WIDTH * 4, k));
+                    M = fmaxf(M, f[k] = read_cluster(from + WIDTH * 4 + 4, k));
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (k >= a.splits) break;
+                    l += read_cluster(from + WIDTH * 4 + 8, k) * power2(read_cluster(from + WIDTH * 4, k) - reference(m));
+                    f[k] = power2(f[k] - reference(M));
+                }
+                const bool any = before + (column0 + col) / a.group >= 0;
+                const Finish z = finish_of(m, M, l, kSumLift, any);
+                T* out = static_cast<T*>(a.out) + (int64_t)(seq.first_token + (column0 + col) / a.group) * a.ot +
+                         (int64_t)(head * a.group + (column0 + col) % a.group) * a.oh;
+                for (int d = threadIdx.x; d < a.c.dim; d += kWarps * 32) {
+                    float y = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        if (k >= a.splits) break;
+                        y = fmaf(read_cluster(from + d * 4, k), f[k], y);
+                    }
+                    out[d] = from_float<T>(any ? y * z.x * z.x * z.inverse : 0.0f);
+                }
+            }
+            cluster_sync();  // nobody's memory goes while another reads it
+            break;
         }
         // the next item
         run += g1 - g0;
@@ -775,12 +840,29 @@ __global__ void __launch_bounds__(8 * PER * 32) join_cut_kernel(const AttendArgs
 
 template <int WIDTH, int FMT>
 constexpr size_t columns_smem() {
-    return std::max<size_t>(kWarps * 8 * (WIDTH + 4) * sizeof(float), (size_t)kWarps * Stage<WIDTH, FMT>::STAGES * 2 * Stage<WIDTH, FMT>::BYTES);
+    return std::max<size_t>((kWarps + 1) * 8 * (WIDTH + 4) * sizeof(float), (size_t)kWarps * Stage<WIDTH, FMT>::STAGES * 2 * Stage<WIDTH, FMT>::BYTES);
 }
 template <typename T, int WIDTH, int FMT>
 cudaError_t columns(const AttendArgs& a, cudaStream_t st) {
     const size_t smem = columns_smem<WIDTH, FMT>();
-    cudaError_t err = launch_pdl(attend_columns_kernel<T, WIDTH, FMT>, dim3((unsigned)a.splits), dim3(kWarps * 32), smem, st, a);
+    if (a.together) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(attend_tiles(a.b, a.group, 8) * a.c.heads), (unsigned)a.splits);
+        cfg.blockDim = dim3(kWarps * 32);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 1;
+        attr[0].val.clusterDim.y = (unsigned)a.splits;
+        attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, attend_columns_kernel<T, WIDTH, FMT, true>, a);
+    }
+    cudaError_t err = launch_pdl(attend_columns_kernel<T, WIDTH, FMT, false>, dim3((unsigned)a.splits), dim3(kWarps * 32), smem, st, a);
     if (err != cudaSuccess) return err;
     // few items for many CTAs: many parts of each
     const float lift = kLift + (FMT == kMxfp4 ? kMxLift : 0);
@@ -804,11 +886,12 @@ int resident() {
     if (n > 0) return n;
     const size_t smem = columns_smem<WIDTH, FMT>();
     if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(attend_columns_kernel<T, WIDTH, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+        (cudaFuncSetAttribute(attend_columns_kernel<T, WIDTH, FMT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+         cudaFuncSetAttribute(attend_columns_kernel<T, WIDTH, FMT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)) {
         (void)cudaGetLastError();
         return device_sms();
     }
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, attend_columns_kernel<T, WIDTH, FMT>, kWarps * 32, smem) != cudaSuccess || per < 1) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, attend_columns_kernel<T, WIDTH, FMT, false>, kWarps * 32, smem) != cudaSuccess || per < 1) {
         (void)cudaGetLastError();
         return device_sms();
     }
@@ -834,8 +917,17 @@ auto with_kernel(const AttendArgs& a, int type, F f) {
 
 }  // namespace
 
-int attend_columns_ctas(const AttendArgs& a, int type) {
-    return with_kernel(a, type, [](auto t, auto w, auto f) { return resident<decltype(t), decltype(w)::value, decltype(f)::value>(); });
+// Short sequences (as far as the page table and the window say) in few enough items: a
+// cluster for each, of up to 8 CTAs with 256 tokens or more, 512 at most, all on the SMs at
+// once.  (523 tokens, 8 heads: 9.8 us, 14.7 as runs and a second launch; 288 items of 1036
+// tokens 24 us in two rounds, 18.5 as runs.)
+void plan_attend_columns(AttendArgs& a, int type) {
+    const int ctas = with_kernel(a, type, [](auto t, auto w, auto f) { return resident<decltype(t), decltype(w)::value, decltype(f)::value>(); });
+    const int64_t table = (int64_t)a.b.table_pages * a.c.page_size, longest = a.window > 0 ? std::min<int64_t>(table, (int64_t)a.window + a.sinks + 32) : table;
+    const int64_t items = attend_tiles(a.b, a.group, 8) * a.c.heads;
+    const int64_t share = std::min<int64_t>({8, (longest + 255) / 256, ctas / std::max<int64_t>(1, items)});
+    a.together = share >= 1 && longest <= share * 512;
+    a.splits = a.together ? (int)share : ctas;
 }
 
 cudaError_t launch_attend_columns(const AttendArgs& a, int type, cudaStream_t st) {

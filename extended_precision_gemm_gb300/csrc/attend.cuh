@@ -29,7 +29,8 @@ struct AttendArgs {
     int window, sinks;       // window 0: none
     float scale;             // log2(e) times the scale of scores
     bool vec_q, vec_out;
-    int splits;    // attend_tile.cu: parts of every row; attend.cu: CTAs
+    int splits;    // attend_tile.cu: parts of every row; attend.cu: CTAs, or (together) CTAs of a cluster
+    bool together;
     float4* part;  // (m, M, l, 1 if any token is seen) of a part: by split and row (token, query head), or by CTA (attend.cu)
     float* sums;   // its o, `width` elements
     CutItem* cuts;  // attend.cu: one for each CTA
@@ -145,8 +146,9 @@ __device__ __forceinline__ void store4(T* out, int d, int dim, bool vec, const F
 inline int64_t attend_tiles(const BatchView& b, int group, int columns) { return b.tokens * group / columns + b.batch; }
 
 cudaError_t launch_attend_columns(const AttendArgs& a, int type, cudaStream_t st);
-// CTAs of that launch, and rows of the workspace: (part, sums) of two cut items each.
-int attend_columns_ctas(const AttendArgs& a, int type);
+// Sets `together` and `splits` for that launch; rows of its workspace unless together: (part, sums) of two cut items of
+// each CTA.
+void plan_attend_columns(AttendArgs& a, int type);
 inline int64_t attend_columns_rows(int ctas) { return 2LL * 8 * ctas; }
 // What a CTA says of the item that it begins and others end (0 columns: none): further CTAs, place of its columns,
 // the position of its sequence's first query.

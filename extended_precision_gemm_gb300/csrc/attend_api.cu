@@ -91,9 +91,12 @@ ddgemm_status check_rotary(const ddgemm_rotary* r, int64_t dim) {
     return DDGEMM_OK;
 }
 
-// Rows (query tokens times heads of a group) of a sequence on average up to which
-// the kernel for few queries runs.
-constexpr int64_t kColumnsMost = 16;
+// Rows (query tokens times heads of a group) of a sequence on average up to which the
+// kernel for few queries runs: it reads the cache once for each 8 of them, the other
+// once for 256.  Width 128, us, this kernel and the other: 32 sequences of 2048 to 4096
+// tokens with 8 heads, 32 rows 119 and 153, 48 rows 168 and 157, 64 rows 218 and 156;
+// one of 65536, 48 rows 105 and 118, 64 rows 132 and 116; one of 4096, 64 rows 24 and 23.
+constexpr int64_t kColumnsMost = 48;
 
 }  // namespace
 
@@ -212,15 +215,17 @@ ddgemm_status dd_mx4_attention(const ddgemm_mx4_cache* cache, const ddgemm_batch
     if (attend_tiles(a.b, a.group, 8) * cache->heads >= (1LL << 31)) return DDGEMM_ERR_UNSUPPORTED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool many = T * a.group > kColumnsMost * batch->batch && cache->pages > 0;
-    a.splits = many ? attend_tile_parts(a) : attend_columns_ctas(a, type);
+    if (many) a.splits = attend_tile_parts(a);
+    else plan_attend_columns(a, type);
+    const bool cut = !many && !a.together;
     Workspace ws(st);
-    const int64_t rows = many ? (a.splits > 1 ? a.splits * T * q_heads : 0) : attend_columns_rows(a.splits);
+    const int64_t rows = many ? (a.splits > 1 ? a.splits * T * q_heads : 0) : cut ? attend_columns_rows(a.splits) : 0;
     const int64_t parts = ws.reserve(rows * (int64_t)sizeof(float4)), sums = ws.reserve(rows * a.c.width * 4),
-                  cuts = ws.reserve(many ? 0 : a.splits * (int64_t)sizeof(CutItem));
+                  cuts = ws.reserve(cut ? a.splits * (int64_t)sizeof(CutItem) : 0);
     if (!ws.allocate()) return DDGEMM_ERR_ALLOC;
     a.part = rows ? ws.at<float4>(parts) : nullptr;
     a.sums = rows ? ws.at<float>(sums) : nullptr;
-    a.cuts = many ? nullptr : ws.at<CutItem>(cuts);
+    a.cuts = cut ? ws.at<CutItem>(cuts) : nullptr;
     return status_of(many ? launch_attend_tile(a, type, st) : launch_attend_columns(a, type, st));
 }
 
