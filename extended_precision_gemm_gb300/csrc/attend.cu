@@ -318,6 +318,9 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : WIDTH == 128 ?
         g0 = (int)((run - start) % groups.count);
     }
     const typename G::Base base = G::base_of(a.c, lane);
+    uint32_t inside[G::KB];  // blocks of the lane's keys that begin beyond the head's end take no part, whatever they hold
+#pragma unroll
+    for (int d = 0; d < G::KB; ++d) inside[d] = (c * (WIDTH / 4) / G::BLOCK + d) * G::BLOCK < a.c.dim ? ~0u : 0u;
     constexpr float kSumLift = kLift + (FMT == kMxfp4 ? kMxLift : 0);
 
     while (true) {
@@ -439,6 +442,8 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : WIDTH == 128 ?
                     ke[t] = reinterpret_cast<const int8_t*>(from + G::E0)[r + 8 * t];
                     load_words<G::KW>(from + (r + 8 * t) * G::ROW + c * (G::ROW / 4), k[t]);
                     half_scales<FMT, G::KB>(from + G::S0 + (r + 8 * t) * G::BLOCKS + c * (WIDTH / 4) / G::BLOCK, ke[t], ks[t]);
+#pragma unroll
+                    for (int d = 0; d < G::KB; ++d) ks[t][d] &= inside[d];
                 }
                 float x[4] = {0.0f, 0.0f, 0.0f, 0.0f}, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // two chains of MMAs
                 constexpr int PER = KS / G::KB;  // MMAs of a block of a lane's codes

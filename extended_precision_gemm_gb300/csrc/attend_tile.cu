@@ -606,6 +606,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             exponent = kNoToken;
             if (r >= 0 && j * 128 + et < tokens) exponent = fetch_signed1(exponent_base + (uint64_t)(uint32_t)r * 16);
         };
+        // blocks that begin beyond the head's end take no part, whatever they hold
+        const uint32_t inside = (part * 32 < a.c.dim ? 0xffffu : 0u) | (part * 32 + BLOCK % 32 < a.c.dim ? 0xffff0000u : 0u);
         const uint32_t place = base + part / 2 * S::BLOCK_BYTES + t * 128 + (uint32_t)(((part % 2 * 4) ^ (t % 8)) << 4);
         bool ok = true;
         int most_seen = kNoToken, key_exponent = 0, value_exponent = 0, next_value_exponent = 0;
@@ -628,6 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
                     if (o == kNoToken) s[0] = 0;
                     s[0] = mul_half2(s[0], half2_of(power, power));
                 }
+                s[0] &= inside;
                 if (value) {  // NaN: 0 here, and looked for at the end
                     const __half2 is = __hisnan2(*reinterpret_cast<const __half2*>(&s[0]));
                     const uint32_t nan = *reinterpret_cast<const uint32_t*>(&is);

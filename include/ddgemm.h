@@ -840,7 +840,7 @@ ddgemm_status dd_rotary(int type, int64_t tokens, int64_t heads, int64_t dim, co
  * A key/value cache in 4-bit microscaled form, in pages of page_size tokens (a
  * power of two, 16 to 65536).  A row is what one token has of one head, keys or
  * values: head_dim values (1 to 256) filled up with zeros to a width of 64, 128 or
- * 256, as codes (width / 2 bytes, the even element in the low nibble), scale bytes
+ * 256 (which no call looks at), as codes (width / 2 bytes, the even element in the low nibble), scale bytes
  * (width / 32 for mxfp4, width / 16 for nvfp4) and one exponent byte (int8): rows,
  * blocks and roundings are those of dd_mx4_quantize on the row; the exponent is
  * nvfp4's row exponent (-127 for a row without a finite value other than 0), and for

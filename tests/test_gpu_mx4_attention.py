@@ -296,3 +296,26 @@ def test_the_first_call_on_a_cold_cache():
     for i in range(5):
         other.fill_(i)
         assert torch.equal(ddg.mx4_attention(q, cache, *batch.dev), want)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim,n", ((96, 1), (96, 40), (32, 1), (32, 40), (30, 2), (200, 1), (200, 40), (130, 30)))
+def test_what_lies_beyond_the_head_does_not_matter(fmt, dtype, dim, n):
+    """Rows are filled up to 64, 128 or 256 elements: any bytes there, NaN scales among them, leave the result as it is."""
+    import torch
+    batch = Batch([(200, n), (77, n), (n, n)], 16)
+    cache, values = filled(batch, 2, dim, fmt)
+    q = queries(batch, 6, dim, dtype)
+    want = ddg.mx4_attention(q, cache, *batch.dev)
+    check(want, q, batch, values, dtype)
+    size = 32 if fmt == "mxfp4" else 16
+    first = -(-dim // size)  # the first block beyond the head
+    g = torch.Generator().manual_seed(0)
+    for byte in (255, 127, 254, 0):
+        cache.scales[..., first:] = byte
+        spoilt = torch.randint(0, 256, cache.codes.shape, generator=g, dtype=torch.uint8).cuda()
+        cache.codes[..., first * size // 2:] = spoilt[..., first * size // 2:]
+        assert torch.equal(ddg.mx4_attention(q, cache, *batch.dev), want)
+    k, _ = ddg.mx4_cache_read(cache, batch.tokens, *batch.dev, dtype=torch.float32)
+    assert torch.isfinite(k).all()
