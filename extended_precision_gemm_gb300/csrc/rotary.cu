@@ -137,7 +137,7 @@ cudaError_t launch(Rotary r, cudaStream_t st) {
     // few tokens: a block for as many heads as it has rows of threads; many: several heads for a thread, which share
     // the token's angles
     const bool many = r.T >= 8 * device_sms();
-    const int tokens = many ? kTokens : 1;
+    const int tokens = many && r.half <= 1024 ? kTokens : 1;  // 32 KB of angles at most
     const int heads = r.T >= 2 * device_sms() || r.H <= uy ? r.H : uy;
     const int most = many ? (uy + 1) / 2 : uy, rounds = (heads + most - 1) / most, rows = (heads + rounds - 1) / rounds;
     const int64_t blocks = (r.T + tokens - 1) / tokens;

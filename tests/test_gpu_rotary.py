@@ -112,3 +112,14 @@ def test_no_tokens():
     import torch
     x = torch.zeros(0, 3, 16).cuda()
     assert ddg.rotary(x, torch.zeros(0, dtype=torch.int32).cuda(), ddg.rotary_table(16)).shape == (0, 3, 16)
+
+
+@pytest.mark.parametrize("dtype", ("bfloat16", "float32"))
+@pytest.mark.parametrize("interleaved", (False, True))
+def test_the_widest_heads(dtype, interleaved):
+    import torch
+    x = torch.randn(1400, 2, 4096, generator=torch.Generator().manual_seed(0)).to(getattr(torch, dtype)).cuda()
+    p = torch.arange(1400).cuda() * 3
+    table = ddg.rotary_table(4096, interleaved=interleaved)
+    y = ddg.rotary(x, p, table)
+    check(x[::100], y[::100], p[::100], table)
