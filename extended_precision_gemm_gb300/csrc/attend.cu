@@ -196,10 +196,10 @@ __device__ __forceinline__ Cut cut_of(int64_t total, int ctas) {
 struct Sequence {
     int first_token, tokens, length;
 };
-__device__ __forceinline__ Sequence sequence_at(const BatchView& b, int i) {
-    const int s0 = b.starts[i], s1 = b.starts[i + 1];
-    if (s0 < 0 || s1 > b.tokens || s1 <= s0) return Sequence{0, 0, 0};
-    return Sequence{s0, s1 - s0, b.lengths[i]};
+__device__ __forceinline__ Sequence sequence_at(const AttendArgs& a, int i) {
+    const int s0 = a.b.starts[i], s1 = a.b.starts[i + 1];
+    if (s0 < 0 || s1 > a.b.tokens || s1 <= s0 || !a.takes(s1 - s0)) return Sequence{0, 0, 0};
+    return Sequence{s0, s1 - s0, a.b.lengths[i]};
 }
 // The groups of tile `ct` of 8 columns, and (with count at least 1) its cost.
 __device__ __forceinline__ Groups tile_groups(const AttendArgs& a, const Sequence& s, int ct) {
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : WIDTH == 128 ?
     const uint32_t rank = TOGETHER ? blockIdx.y : 0;
     if constexpr (TOGETHER) {
         head = (int)(blockIdx.x % a.c.heads);
-        const Item item = item_of(a.b, blockIdx.x / a.c.heads, a.group, 8);
+        const Item item = item_of(a, blockIdx.x / a.c.heads, 8);
         if (item.sequence < 0) return;  // the whole cluster
         b = item.sequence;
         ct = item.column / 8;
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : WIDTH == 128 ?
             int64_t mine = 0;
             Sequence own{0, 0, 0};
             for (int i = b0; i < b1; ++i) {
-                own = sequence_at(a.b, i);
+                own = sequence_at(a, i);
                 mine += cost_of(a, own);
             }
             int64_t upto = mine;
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : WIDTH == 128 ?
             run_end = cut.first(blockIdx.x + 1);
             int64_t at = before * a.c.heads;
             for (int i = b0; i < b1; ++i) {
-                if (per > 1) own = sequence_at(a.b, i);
+                if (per > 1) own = sequence_at(a, i);
                 const int64_t cost = (per > 1 ? cost_of(a, own) : mine) * a.c.heads;
                 if (run >= at && run < at + cost) {
                     found = i;
@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : WIDTH == 128 ?
             head = 0;
             if (++ct == tiles_of(a, seq)) {
                 ct = 0;
-                do seq = sequence_at(a.b, ++b);
+                do seq = sequence_at(a, ++b);
                 while (seq.tokens == 0);
             }
             groups = tile_groups(a, seq, ct);
@@ -732,8 +732,8 @@ __global__ void __launch_bounds__(128) join_kernel(const AttendArgs a, float lif
     const int64_t row = (int64_t)blockIdx.x * (4 / WARPS) + warp / WARPS;
     if (row >= rows) return;
     const int64_t token = row / a.heads, h = row % a.heads;
-    const int s = search(a.b, token, 1, 1, 0);
-    if (s < 0 || a.b.starts[s] < 0 || a.b.starts[s + 1] <= token || a.b.starts[s + 1] > a.b.tokens) return;
+    const int s = search(a.b, token, [&](int i) { return a.b.starts[i]; });
+    if (s < 0 || a.b.starts[s] < 0 || a.b.starts[s + 1] <= token || a.b.starts[s + 1] > a.b.tokens || !a.takes(a.b.starts[s + 1] - a.b.starts[s])) return;
     float m = minus_infinity(), M = m;
     float4 mine = make_float4(m, m, 0.0f, 0.0f);
     for (int i = lane; i < a.splits; i += 32) {
@@ -852,7 +852,7 @@ cudaError_t columns(const AttendArgs& a, cudaStream_t st) {
     const size_t smem = columns_smem<WIDTH, FMT>();
     if (a.together) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(attend_tiles(a.b, a.group, 8) * a.c.heads), (unsigned)a.splits);
+        cfg.gridDim = dim3((unsigned)(a.tiles(8) * a.c.heads), (unsigned)a.splits);
         cfg.blockDim = dim3(kWarps * 32);
         cfg.dynamicSmemBytes = smem;
         cfg.stream = st;
@@ -871,7 +871,7 @@ cudaError_t columns(const AttendArgs& a, cudaStream_t st) {
     if (err != cudaSuccess) return err;
     // few items for many CTAs: many parts of each
     const float lift = kLift + (FMT == kMxfp4 ? kMxLift : 0);
-    const bool long_items = attend_tiles(a.b, a.group, 8) * a.c.heads * 8 < a.splits;
+    const bool long_items = a.tiles(8) * a.c.heads * 8 < a.splits;
     return long_items ? launch_pdl(join_cut_kernel<T, WIDTH, WIDTH == 256 ? 2 : 4>, dim3((unsigned)a.splits), dim3(WIDTH == 256 ? 512 : 1024), 0, st, a, lift)
                       : launch_pdl(join_cut_kernel<T, WIDTH, 1>, dim3((unsigned)a.splits), dim3(256), 0, st, a, lift);
 }
@@ -929,7 +929,7 @@ auto with_kernel(const AttendArgs& a, int type, F f) {
 void plan_attend_columns(AttendArgs& a, int type) {
     const int ctas = with_kernel(a, type, [](auto t, auto w, auto f) { return resident<decltype(t), decltype(w)::value, decltype(f)::value>(); });
     const int64_t table = (int64_t)a.b.table_pages * a.c.page_size, longest = a.window > 0 ? std::min<int64_t>(table, (int64_t)a.window + a.sinks + 32) : table;
-    const int64_t items = attend_tiles(a.b, a.group, 8) * a.c.heads;
+    const int64_t items = a.tiles(8) * a.c.heads;
     const int64_t share = std::min<int64_t>({8, (longest + 255) / 256, ctas / std::max<int64_t>(1, items)});
     a.together = share >= 1 && longest <= share * 512;
     a.splits = a.together ? (int)share : ctas;

@@ -29,11 +29,23 @@ struct AttendArgs {
     int window, sinks;       // window 0: none
     float scale;             // log2(e) times the scale of scores
     bool vec_q, vec_out;
+    int64_t above, upto;  // sequences of so many rows (tokens times queries a key/value head) are taken, the others left out
+    int step;             // 0, or see first_tile
     int splits;    // attend_tile.cu: parts of every row; attend.cu: CTAs, or (together) CTAs of a cluster
     bool together;
     float4* part;  // (m, M, l, 1 if any token is seen) of a part: by split and row (token, query head), or by CTA (attend.cu)
     float* sums;   // its o, `width` elements
     CutItem* cuts;  // attend.cu: one for each CTA
+
+    __host__ __device__ bool takes(int64_t tokens) const { return tokens * group > above && tokens * group <= upto; }
+    // The number of the first tile of `columns` rows of sequence i, which starts at token `start`.  Its rows' own tiles
+    // have one more at most than start's difference gives: each sequence has a number more for it or, where only those
+    // of more than `above` rows are taken and the others are the most, every `step` tokens have, the fewest of such a
+    // sequence.  Numbers that are left over are of no tile.
+    __host__ __device__ int64_t first_tile(int i, int start, int columns) const {
+        return (int64_t)start * group / columns + (step > 0 ? (unsigned)start / (unsigned)step : i);
+    }
+    int64_t tiles(int columns) const { return first_tile((int)b.batch, (int)b.tokens, columns); }
 };
 
 #ifdef __CUDACC__
@@ -64,8 +76,8 @@ __device__ __forceinline__ Groups groups_of(const CacheView& c, const BatchView&
     if (p1 < 0) return g;
     const int end = (int)min((int64_t)p1 / 16 + 1, (int64_t)b.table_pages * c.page_size / 16 + 1);
     if (window > 0 && p0 >= window) {
-        g.low = min((p0 - window + 1) / 16, end - 1);
-        g.sink = min((min(sinks, p1 + 1) + 15) / 16, g.low);
+        g.low = min((p0 - window) / 16 + ((p0 - window) % 16 == 15 ? 1 : 0), end - 1);  // of token p0 - window + 1
+        g.sink = min((min(sinks, p1) + 15) / 16, g.low);
     }
     g.count = g.sink + end - g.low;
     return g;
@@ -77,22 +89,21 @@ __device__ __forceinline__ bool sees(int p, int j, int window, int sinks) {
 }
 
 // Work items are tiles of `columns` (query token, head of the group) pairs of one
-// sequence and key/value head.  Sequence b's tiles are numbered from
-// floor(starts[b] group / columns) + b on, which leaves room for all of them
-// whatever the sequences' sizes; numbers between are of no tile.
+// sequence and key/value head, numbered by first_tile.
 struct Item {
     int sequence, column, columns, first_token, tokens, length;
 };
-// The last sequence b with starts[b] group / columns + step b <= t, found by a whole
-// warp; -1 if there is none.
-__device__ __forceinline__ int search(const BatchView& b, int64_t t, int group, int columns, int step) {
+// The last sequence b with first(b) <= t, found by a whole warp, where first does not
+// fall; -1 if there is none.
+template <class F>
+__device__ __forceinline__ int search(const BatchView& b, int64_t t, F first) {
     const int lane = threadIdx.x & 31;
     int low = 0, high = b.batch;  // the answer is in [low, high)
     bool none = b.batch <= 0;
     while (!none && (high - low > 1 || low == 0)) {
         const int stride = (high - low + 31) / 32;
         const int i = low + lane * stride;
-        const bool at = i < high && (int64_t)b.starts[i] * group / columns + (int64_t)step * i <= t;
+        const bool at = i < high && first(i) <= t;
         const int n = __popc(__ballot_sync(~0u, at));
         none = n == 0;
         low += none ? 0 : (n - 1) * stride;
@@ -102,14 +113,15 @@ __device__ __forceinline__ int search(const BatchView& b, int64_t t, int group, 
     return none ? -1 : low;
 }
 // Tile t's part of the batch.
-__device__ __forceinline__ Item item_of(const BatchView& b, int64_t t, int group, int columns) {
+__device__ __forceinline__ Item item_of(const AttendArgs& a, int64_t t, int columns) {
     const Item nothing{-1, 0, 0, 0, 0, 0};
-    const int s = search(b, t, group, columns, 1);
+    const BatchView& b = a.b;
+    const int s = search(b, t, [&](int i) { return a.first_tile(i, b.starts[i], columns); });
     if (s < 0) return nothing;
     const int64_t s0 = b.starts[s], s1 = b.starts[s + 1];
-    const int64_t column = (t - (s0 * group / columns + s)) * columns;
-    if (s0 < 0 || s1 > b.tokens || column < 0 || column >= (s1 - s0) * group) return nothing;
-    return Item{s, (int)column, (int)min((int64_t)columns, (s1 - s0) * group - column), (int)s0, (int)(s1 - s0), b.lengths[s]};
+    const int64_t column = (t - a.first_tile(s, (int)s0, columns)) * columns;
+    if (s0 < 0 || s1 > b.tokens || !a.takes(s1 - s0) || column < 0 || column >= (s1 - s0) * a.group) return nothing;
+    return Item{s, (int)column, (int)min((int64_t)columns, (s1 - s0) * a.group - column), (int)s0, (int)(s1 - s0), b.lengths[s]};
 }
 
 // How a row's sums become its output: times x twice (half of the exponent each),
@@ -141,9 +153,6 @@ __device__ __forceinline__ void store4(T* out, int d, int dim, bool vec, const F
 }  // namespace
 
 #endif  // __CUDACC__
-
-// Tiles of `columns` that sequences of `tokens` tokens in all may have.
-inline int64_t attend_tiles(const BatchView& b, int group, int columns) { return b.tokens * group / columns + b.batch; }
 
 cudaError_t launch_attend_columns(const AttendArgs& a, int type, cudaStream_t st);
 // Sets `together` and `splits` for that launch; rows of its workspace unless together: (part, sums) of two cut items of

@@ -97,6 +97,34 @@ ddgemm_status check_rotary(const ddgemm_rotary* r, int64_t dim) {
 // tokens with 8 heads, 32 rows 119 and 153, 48 rows 168 and 157, 64 rows 218 and 156;
 // one of 65536, 48 rows 105 and 118, 64 rows 132 and 116; one of 4096, 64 rows 24 and 23.
 constexpr int64_t kColumnsMost = 48;
+// The host knows the sum of the sequences' rows alone.  Where their average is more, or
+// the tokens beyond one for each sequence could be more than 512 rows of one of them,
+// both kernels run, each on its sequences.  127 single tokens and 128 of one further
+// sequence, 4000 in the cache, 8 heads: 201 us, 310 by the kernel for few alone; 1024 of
+// that sequence: 321 us, 706 by the other alone.  What it costs where no sequence has
+// many: 32 of 5 tokens each 188 us, 170 by the kernel for few alone.
+constexpr int64_t kSurplus = 512;
+
+ddgemm_status attend_tiles_call(AttendArgs& a, int type, cudaStream_t st) {
+    a.splits = attend_tile_parts(a);
+    Workspace ws(st);
+    const int64_t rows = a.splits > 1 ? a.splits * a.b.tokens * a.heads : 0;
+    const int64_t parts = ws.reserve(rows * (int64_t)sizeof(float4)), sums = ws.reserve(rows * a.c.width * 4);
+    if (!ws.allocate()) return DDGEMM_ERR_ALLOC;
+    if (rows > 0) a.part = ws.at<float4>(parts), a.sums = ws.at<float>(sums);
+    return status_of(launch_attend_tile(a, type, st));
+}
+
+ddgemm_status attend_columns_call(AttendArgs& a, int type, cudaStream_t st) {
+    plan_attend_columns(a, type);
+    Workspace ws(st);
+    const int64_t rows = a.together ? 0 : attend_columns_rows(a.splits);
+    const int64_t parts = ws.reserve(rows * (int64_t)sizeof(float4)), sums = ws.reserve(rows * a.c.width * 4),
+                  cuts = ws.reserve(rows > 0 ? a.splits * (int64_t)sizeof(CutItem) : 0);
+    if (!ws.allocate()) return DDGEMM_ERR_ALLOC;
+    if (rows > 0) a.part = ws.at<float4>(parts), a.sums = ws.at<float>(sums), a.cuts = ws.at<CutItem>(cuts);
+    return status_of(launch_attend_columns(a, type, st));
+}
 
 }  // namespace
 
@@ -212,21 +240,25 @@ ddgemm_status dd_mx4_attention(const ddgemm_mx4_cache* cache, const ddgemm_batch
     const auto whole = [&](const void* p, int64_t t, int64_t h) { return aligned16(p) && (T <= 1 || t % 8 == 0) && (q_heads <= 1 || h % 8 == 0); };
     a.vec_q = whole(q, q_token, q_head);
     a.vec_out = whole(out, out_token, out_head);
-    if (attend_tiles(a.b, a.group, 8) * cache->heads >= (1LL << 31)) return DDGEMM_ERR_UNSUPPORTED;
+    if (a.tiles(8) * cache->heads >= (1LL << 31)) return DDGEMM_ERR_UNSUPPORTED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool many = T * a.group > kColumnsMost * batch->batch && cache->pages > 0;
-    if (many) a.splits = attend_tile_parts(a);
-    else plan_attend_columns(a, type);
-    const bool cut = !many && !a.together;
-    Workspace ws(st);
-    const int64_t rows = many ? (a.splits > 1 ? a.splits * T * q_heads : 0) : cut ? attend_columns_rows(a.splits) : 0;
-    const int64_t parts = ws.reserve(rows * (int64_t)sizeof(float4)), sums = ws.reserve(rows * a.c.width * 4),
-                  cuts = ws.reserve(cut ? a.splits * (int64_t)sizeof(CutItem) : 0);
-    if (!ws.allocate()) return DDGEMM_ERR_ALLOC;
-    a.part = rows ? ws.at<float4>(parts) : nullptr;
-    a.sums = rows ? ws.at<float>(sums) : nullptr;
-    a.cuts = cut ? ws.at<CutItem>(cuts) : nullptr;
-    return status_of(many ? launch_attend_tile(a, type, st) : launch_attend_columns(a, type, st));
+    const int64_t rows = T * a.group, surplus = (T - batch->batch) * a.group;
+    const bool tiles = cache->pages > 0 && (rows > kColumnsMost * batch->batch || surplus > kSurplus);
+    const bool columns = !tiles || (batch->batch > 1 && a.group <= kColumnsMost);
+    a.above = 0, a.upto = INT64_MAX;
+    for (const bool tile : {false, true}) {
+        if (!(tile ? tiles : columns)) continue;
+        AttendArgs c = a;
+        if (tile && columns) {
+            c.above = kColumnsMost;
+            const int64_t step = kColumnsMost / a.group + 1;
+            if (T / step < batch->batch) c.step = (int)step;
+        }
+        if (!tile && tiles) c.upto = kColumnsMost;
+        s = tile ? attend_tiles_call(c, type, st) : attend_columns_call(c, type, st);
+        if (s != DDGEMM_OK) return s;
+    }
+    return DDGEMM_OK;
 }
 
 }  // extern "C"

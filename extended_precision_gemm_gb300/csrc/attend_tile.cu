@@ -112,27 +112,27 @@ __device__ __forceinline__ void store_shared(uint32_t at, uint4 v) {
 // Loads that stay where they are written, ahead of the conversions of the tile before.
 __device__ __forceinline__ uint4 fetch16(const void* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
 __device__ __forceinline__ uint16_t fetch2(const void* p) {
     uint16_t v;
-    asm volatile("ld.global.nc.b16 %0, [%1];" : "=h"(v) : "l"(p));
+    asm volatile("ld.global.b16 %0, [%1];" : "=h"(v) : "l"(p));
     return v;
 }
 __device__ __forceinline__ uint16_t fetch1(const void* p) {
     uint16_t v;
-    asm volatile("ld.global.nc.u8 %0, [%1];" : "=h"(v) : "l"(p));
+    asm volatile("ld.global.u8 %0, [%1];" : "=h"(v) : "l"(p));
     return v;
 }
 __device__ __forceinline__ int fetch_signed1(const void* p) {
     int v;
-    asm volatile("ld.global.nc.s8 %0, [%1];" : "=r"(v) : "l"(p));
+    asm volatile("ld.global.s8 %0, [%1];" : "=r"(v) : "l"(p));
     return v;
 }
 __device__ __forceinline__ int fetch4(const void* p) {
     int v;
-    asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
     return v;
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
     const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const int head = (int)(blockIdx.x % a.c.heads);
     // the last rows of a sequence see the most tokens: they go first
-    const Item item = item_of(a.b, (int64_t)((gridDim.x - 1 - blockIdx.x) / a.c.heads), a.group, 128 * S::NQ);
+    const Item item = item_of(a, (int64_t)((gridDim.x - 1 - blockIdx.x) / a.c.heads), 128 * S::NQ);
     if (item.sequence < 0) return;
     const int before = item.length - item.tokens;
     const auto position = [&](int column) { return before + (item.column + column) / a.group; };
@@ -816,7 +816,7 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t st) {
         if (err != cudaSuccess) return err;
         asked[dev].store(true, std::memory_order_relaxed);
     }
-    const dim3 grid((unsigned)(a.c.heads * attend_tiles(a.b, a.group, 128 * S::NQ)), 1, (unsigned)a.splits);
+    const dim3 grid((unsigned)(a.c.heads * a.tiles(128 * S::NQ)), 1, (unsigned)a.splits);
     err = launch_pdl(kernel, grid, dim3(kThreads), S::SMEM, st, a);
     if (err != cudaSuccess || a.splits == 1) return err;
     return launch_attend_join(a, std::is_same_v<T, __half> ? DDGEMM_F16 : DDGEMM_BF16, kLift + lift_of<FMT>(), st);
@@ -834,7 +834,13 @@ cudaError_t by_width(const AttendArgs& a, cudaStream_t st) {
 // 3 us.
 int attend_tile_parts(const AttendArgs& a) {
     const int rows = a.c.width == 256 ? 128 : 256;
-    const int64_t items = std::max(a.b.tokens * a.group / rows, (int64_t)a.b.batch) * a.c.heads;
+    // sequences that may be taken, if each has a token at least
+    int64_t batch = a.b.batch, tokens = a.b.tokens;
+    if (a.above > a.group) {
+        batch = std::max<int64_t>(1, std::min(batch, (tokens - batch) * a.group / (a.above + 1 - a.group)));
+        tokens -= a.b.batch - batch;
+    }
+    const int64_t items = std::max(tokens * a.group / rows, batch) * a.c.heads;
     const int64_t longest = a.window > 0 ? (int64_t)a.window + a.sinks : (int64_t)a.b.table_pages * a.c.page_size;
     if (items >= 2 * device_sms()) return 1;
     return (int)std::max<int64_t>(1, std::min<int64_t>({4 * device_sms() / std::max<int64_t>(1, items), (longest + 511) / 512, 64}));

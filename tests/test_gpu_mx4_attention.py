@@ -319,3 +319,93 @@ def test_what_lies_beyond_the_head_does_not_matter(fmt, dtype, dim, n):
         assert torch.equal(ddg.mx4_attention(q, cache, *batch.dev), want)
     k, _ = ddg.mx4_cache_read(cache, batch.tokens, *batch.dev, dtype=torch.float32)
     assert torch.isfinite(k).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("scale", (-0.1, 0.0, 3.0))
+@pytest.mark.parametrize("n", (1, 60))
+def test_scales_of_either_sign(fmt, scale, n):
+    run([(90, n), (200, n)], 16, 2, 4, 64, fmt, "bfloat16", scale=scale, seed=3)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", (1, 60))
+def test_queries_that_are_not_finite_spoil_their_own_rows_only(dtype, n):
+    import torch
+    batch = Batch([(90, n), (200, n)], 16)
+    cache, values = filled(batch, 2, 64, "nvfp4")
+    q = queries(batch, 8, 64, dtype)
+    want = ddg.mx4_attention(q, cache, *batch.dev)
+    q[0, 1, 3], q[n, 2, 5] = float("nan"), float("inf")
+    y = ddg.mx4_attention(q, cache, *batch.dev)
+    bad = torch.zeros(y.shape[:2], dtype=torch.bool, device="cuda")
+    bad[0, 1] = bad[n, 2] = True
+    assert torch.isnan(y[0, 1]).all()  # NaN scores
+    assert not torch.isfinite(y[n, 2]).all()  # scores of plus infinity: NaN weights, as of the definition
+    assert torch.equal(y[~bad], want[~bad])
+
+
+def test_queries_of_any_size():
+    """Rows of 2^-100 to 2^60: scaled into the range of 16 bits by a power of two."""
+    import torch
+    batch = Batch([(90, 1), (200, 60)], 16)
+    cache, values = filled(batch, 1, 128, "mxfp4", 0, lambda rng, shape: 2.0**-20 * np.ones(shape))
+    q = queries(batch, 4, 128, "bfloat16")
+    powers = torch.tensor([-100, -60, 0, 60], device="cuda").float()
+    for scale in (1.0, 2.0**-50):
+        big = (q.double() * torch.exp2(powers.double())[None, :, None]).bfloat16()
+        small = (q.double() * torch.exp2(powers.double())[None, :, None] * scale).bfloat16()
+        y = ddg.mx4_attention(small, cache, *batch.dev, scale=2.0**-40 / scale)
+        assert torch.equal(y, ddg.mx4_attention(big, cache, *batch.dev, scale=2.0**-40))
+        check(y, big, batch, values, "bfloat16", scale=2.0**-40)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_long_and_short_parts_in_one_batch(fmt):
+    """Single tokens, some tokens and long parts together: each sequence takes the kernel that suits it."""
+    sizes = [(200 + 7 * b, 1) for b in range(40)] + [(900, 600)] + [(100 + b, 3) for b in range(30)] + [(300, 150), (64, 13)] + [(33, 1)] * 60
+    run(sizes, 16, 2, 4, 64, fmt, "float16", seed=1, lead=2, tail=3)
+    run(sizes, 16, 1, 8, 128, fmt, "bfloat16", 50, 3, seed=2)
+
+
+def test_an_empty_cache():
+    import torch
+    cache = ddg.mx4_cache(0, 16, 2, 64, "mxfp4")
+    for n in (1, 100):
+        starts, lengths = torch.tensor([0, n, n + 2], dtype=torch.int32).cuda(), torch.tensor([n, 0], dtype=torch.int32).cuda()
+        table = torch.zeros((2, 8), dtype=torch.int32, device="cuda")
+        x = torch.randn(n + 2, 2, 64, device="cuda").bfloat16()
+        ddg.mx4_cache_append(cache, x, x, starts, lengths, table)
+        y = ddg.mx4_attention(x, cache, starts, lengths, table)
+        assert torch.isnan(y[:n]).all() and not y[n:].any()
+        k, v = ddg.mx4_cache_read(cache, n + 2, starts, lengths, table)
+        assert torch.isnan(k).all() and torch.isnan(v).all()
+
+
+def test_no_tokens_and_no_sequences():
+    import torch
+    cache = ddg.mx4_cache(4, 16, 2, 64, "nvfp4")
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    q = torch.full((3, 4, 64), 2.0, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 5.0)
+    ddg.mx4_attention(q, cache, torch.zeros(1, dtype=torch.int32, device="cuda"), none, none.view(0, 4), out=out)
+    assert (out == 5).all()
+    assert ddg.mx4_attention(q[:0], cache, torch.zeros(2, dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda"),
+                             torch.zeros(1, 4, dtype=torch.int32, device="cuda")).shape == (0, 4, 64)
+
+
+def test_calls_on_two_streams_at_once():
+    import torch
+    batch = Batch([(6000, 1), (300, 1), (4, 3), (2000, 300)], 16)
+    cache, values = filled(batch, 2, 128, "mxfp4")
+    q = queries(batch, 8, 128, "bfloat16")
+    few = Batch([(3000, 1), (77, 2)], 16)
+    cache2, _ = filled(few, 4, 64, "nvfp4")
+    q2 = queries(few, 16, 64, "float16")
+    want, want2 = ddg.mx4_attention(q, cache, *batch.dev), ddg.mx4_attention(q2, cache2, *few.dev)
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(10):
+        got = [(ddg.mx4_attention(q, cache, *batch.dev, stream=a), ddg.mx4_attention(q2, cache2, *few.dev, stream=b)) for _ in range(5)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, want) and torch.equal(y, want2) for x, y in got)
