@@ -205,8 +205,6 @@ def test_streams_and_graphs():
     want = step(q, k, v)
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
-    assert torch.equal(step(q, k, v, side), want) or side.synchronize() or True
-    side.synchronize()
     got = step(q, k, v, side)
     side.synchronize()
     assert torch.equal(got, want)
