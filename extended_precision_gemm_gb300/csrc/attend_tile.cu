@@ -33,8 +33,6 @@ constexpr float kMost = 32768.0f;  // a row's reference follows where 32 weights
 constexpr int kShift = 3;      // ... and the values' exponent by more than 2^3 either way
 constexpr float kLift = 7.0f;  // the weight of a score equal to the reference is 2^(7 + up to 3 either way)
 constexpr int kFar = 64;       // values' exponents are at most so far below the largest seen
-constexpr int kThreads = 20 * 32;  // the last three warps only give up their registers
-constexpr int kConverters = 256;
 constexpr int kRing = 4;  // tiles whose rows, exponents and marks are kept
 constexpr int kNoToken = -4096;  // in the place of an exponent
 
@@ -46,6 +44,9 @@ template <int FMT> __host__ __device__ constexpr int lift_of() { return FMT == k
 template <int WIDTH>
 struct Shape {
     static constexpr int NQ = WIDTH == 256 ? 1 : 2;       // tiles of rows
+    // threads that convert: where one tile of rows shares them, twice as many (three chunks, see the end: 332 us for 363)
+    static constexpr int CONVERTERS = WIDTH == 256 ? 512 : 256;
+    static constexpr int MMA_WARP = 4 * NQ + CONVERTERS / 32, THREADS = (MMA_WARP + 4) * 32;  // the last three warps have no task
     static constexpr int STAGES = WIDTH == 256 ? 1 : 2;   // of keys, and of values
     static constexpr int BLOCK_BYTES = 128 * 128;         // 128 rows of 64 elements
     static constexpr int TILE_BYTES = WIDTH / 64 * BLOCK_BYTES;
@@ -53,13 +54,13 @@ struct Shape {
     static constexpr int SMEM = V0 + STAGES * TILE_BYTES + 1024;
     static constexpr int BUFFERS = 2 / NQ;                // of scores, of a tile of rows
     static constexpr int PIECES = WIDTH / 32;                     // of 32 codes, of a token
-    static constexpr int PER_PASS = kConverters / PIECES;         // tokens that the threads convert at once
+    static constexpr int PER_PASS = CONVERTERS / PIECES;          // tokens that the threads convert at once
     static constexpr int PASSES = 128 / PER_PASS;
     static constexpr uint32_t S_COL = 0, O_COL = 256;
-    // registers of a thread by role: of the 96 that each is launched with, five warps (two of the softmax,
-    // two that convert, one of the last four) share 480 on a part of the SM
-    static constexpr int SOFTMAX_REGS = NQ == 2 ? 136 : 168, IDLE_REGS = 24, CONVERT_REGS = NQ == 2 ? 80 : 120, MMA_REGS = 48;
-    static_assert(SOFTMAX_REGS + (NQ == 2 ? SOFTMAX_REGS : IDLE_REGS) + 2 * CONVERT_REGS + MMA_REGS <= 480, "registers of the launch");
+    // registers of a thread by role: of those that each is launched with, a part of the SM has 480 for its warps (one
+    // of each tile's softmax, two or four that convert, one of the last four)
+    static constexpr int SOFTMAX_REGS = NQ == 2 ? 136 : 176, CONVERT_REGS = NQ == 2 ? 80 : 64, MMA_REGS = 48;
+    static_assert(THREADS / 128 * (NQ == 2 ? 96 : 80) == 480 && NQ * SOFTMAX_REGS + CONVERTERS / 128 * CONVERT_REGS + MMA_REGS <= 480, "registers of the launch");
 };
 
 // What the softmax has to know of a tile.
@@ -244,7 +245,7 @@ __device__ __noinline__ void mark_nan(const AttendArgs& a, const Item& item, con
 }
 
 template <typename T, int WIDTH, int FMT>
-__global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(const AttendArgs a) {
     using S = Shape<WIDTH>;
     constexpr bool REST = std::is_same_v<T, __half>;  // what the rounding of weights leaves enters the sum too
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -287,8 +288,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
     if (threadIdx.x == 0) {
         mbar_init(q_full, 4 * S::NQ);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(bars.k_full, i), kConverters / 32);
-            mbar_init(bar(bars.v_full, i), kConverters / 32);
+            mbar_init(bar(bars.k_full, i), S::CONVERTERS / 32);
+            mbar_init(bar(bars.v_full, i), S::CONVERTERS / 32);
             mbar_init(bar(bars.k_empty, i), 1);
             mbar_init(bar(bars.v_empty, i), 1);
             mbar_init(bar(bars.s, i), 1);
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
         any_nan = 0;
         fence_barrier_init();
     }
-    if (warp == 16) {
+    if (warp == S::MMA_WARP) {
         tc5::tmem_alloc(smem_addr(&tmem_slot), 512);
         tc5::tmem_relinquish();
     }
@@ -549,14 +550,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             __syncwarp();
         }
         tc5::fence_before_sync();
-    } else if (warp < 8) {
-        fewer_registers<S::IDLE_REGS>();
-    } else if (warp < 16) {
+    } else if (warp < S::MMA_WARP) {
         // ---- codes to 16 bits ----
-        if constexpr (S::CONVERT_REGS < 96) fewer_registers<S::CONVERT_REGS>();
-        else more_registers<S::CONVERT_REGS>();
+        fewer_registers<S::CONVERT_REGS>();
         constexpr int PIECES = S::PIECES, PASSES = S::PASSES, BLOCK = mx4_block(FMT), BLOCKS = WIDTH / BLOCK;
-        const int thread = threadIdx.x - 8 * 32;
+        const int thread = threadIdx.x - 4 * S::NQ * 32;
         // In a pass the thread has 32 codes of token t, the part-th of it.  8 lanes in a row have 4 tokens and
         // 2 parts: their 16-byte pieces lie on different banks, and a warp's codes are contiguous all the same.
         constexpr int LOG = PIECES == 2 ? 1 : PIECES == 4 ? 2 : 3;
@@ -583,10 +581,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             rows[0][thread] = row_for(0, first_page);
             rows[1][thread] = row_for(1, second_page);
         }
-        asm volatile("bar.sync 1, %0;" ::"n"(kConverters) : "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(S::CONVERTERS) : "memory");
         const uint8_t* const code_base = a.c.codes + (t % 16) * (WIDTH / 2) + part * 16;
         const uint8_t* const scale_base = a.c.scales + (t % 16) * BLOCKS + part * (32 / BLOCK);
-        // of exponents a thread has one: a key's (threads 0 to 127) or a value's
+        // of exponents a thread has one: a key's (threads 0 to 127) or a value's (128 to 255)
         const int kv = thread / 128, et = thread % 128;
         const int8_t* const exponent_base = a.c.exponents + (kv ? (int64_t)to_values * 16 : 0) + et % 16;
         // tokens of the tiles from t0 on, up to the end of the sequence (only the last group reaches beyond it)
@@ -604,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
         const auto load_exponent = [&](int j) {
             const int r = rows[j & (kRing - 1)][et / 16];
             exponent = kNoToken;
-            if (r >= 0 && j * 128 + et < tokens) exponent = fetch_signed1(exponent_base + (uint64_t)(uint32_t)r * 16);
+            if (kv < 2 && r >= 0 && j * 128 + et < tokens) exponent = fetch_signed1(exponent_base + (uint64_t)(uint32_t)r * 16);
         };
         // blocks that begin beyond the head's end take no part, whatever they hold
         const uint32_t inside = (part * 32 < a.c.dim ? 0xffffu : 0u) | (part * 32 + BLOCK % 32 < a.c.dim ? 0xffff0000u : 0u);
@@ -662,10 +660,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             const int slot = j & (kRing - 1);
             ok = ok && warp_wait(bar(bars.k_empty, j % S::STAGES), ((j / S::STAGES) & 1) ^ 1, kWaitNs);
             // the scores of tile j - 2 are there: the softmax has done with tile j - 4, whose slot this is
-            exponents[slot][kv][et] = (int16_t)exponent;
-            const int top = __reduce_max_sync(~0u, exponent);
-            if (lane == 0) largest[j & 1][kv][et / 32] = top;
-            asm volatile("bar.sync 1, %0;" ::"n"(kConverters) : "memory");
+            if (kv < 2) {
+                exponents[slot][kv][et] = (int16_t)exponent;
+                const int top = __reduce_max_sync(~0u, exponent);
+                if (lane == 0) largest[j & 1][kv][et / 32] = top;
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(S::CONVERTERS) : "memory");
             if (with_values) load(j - 1, to_values, values);
             const int4 a0 = *reinterpret_cast<const int4*>(largest[j & 1][0]), a1 = *reinterpret_cast<const int4*>(largest[j & 1][1]);
             key_exponent = max(max(max(a0.x, a0.y), max(a0.z, a0.w)), -127);
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
             }
         }
         if (!ok && lane == 0) atomicAdd(&g_attend_timeouts, 1u);
-    } else if (fewer_registers<S::MMA_REGS>(); warp == 16 && n > 0) {
+    } else if (fewer_registers<S::MMA_REGS>(); warp == S::MMA_WARP && n > 0) {
         // ---- MMAs ----
         constexpr uint32_t S_DESC = tc5::idesc_f16(false, false, false, 128, 128);
         constexpr uint32_t O_DESC = tc5::idesc_f16(false, false, true, 128, WIDTH);
@@ -789,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tile_kernel(const AttendAr
     tc5::fence_before_sync();
     __syncthreads();
     tc5::fence_after_sync();
-    if (warp == 16) {
+    if (warp == S::MMA_WARP) {
         __syncwarp();
         tc5::tmem_dealloc(tmem, 512);
     }
@@ -817,7 +817,7 @@ cudaError_t launch(const AttendArgs& a, cudaStream_t st) {
         asked[dev].store(true, std::memory_order_relaxed);
     }
     const dim3 grid((unsigned)(a.c.heads * a.tiles(128 * S::NQ)), 1, (unsigned)a.splits);
-    err = launch_pdl(kernel, grid, dim3(kThreads), S::SMEM, st, a);
+    err = launch_pdl(kernel, grid, dim3(S::THREADS), S::SMEM, st, a);
     if (err != cudaSuccess || a.splits == 1) return err;
     return launch_attend_join(a, std::is_same_v<T, __half> ? DDGEMM_F16 : DDGEMM_BF16, kLift + lift_of<FMT>(), st);
 }
