@@ -76,8 +76,8 @@ __device__ __forceinline__ Groups groups_of(const CacheView& c, const BatchView&
     if (p1 < 0) return g;
     const int end = (int)min((int64_t)p1 / 16 + 1, (int64_t)b.table_pages * c.page_size / 16 + 1);
     if (window > 0 && p0 >= window) {
-        g.low = min((p0 - window) / 16 + ((p0 - window) % 16 == 15 ? 1 : 0), end - 1);  // of token p0 - window + 1
-        g.sink = min((min(sinks, p1) + 15) / 16, g.low);
+        g.low = min((p0 - window + 1) / 16, end - 1);
+        g.sink = min((int)(((unsigned)min(sinks, p1 + 1) + 15u) / 16u), g.low);
     }
     g.count = g.sink + end - g.low;
     return g;

@@ -586,6 +586,7 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
         const uint8_t* const scale_base = a.c.scales + (t % 16) * BLOCKS + part * (32 / BLOCK);
         // of exponents a thread has one: a key's (threads 0 to 127) or a value's (128 to 255)
         const int kv = thread / 128, et = thread % 128;
+        const bool has_exponent = S::CONVERTERS == 256 || kv < 2;
         const int8_t* const exponent_base = a.c.exponents + (kv ? (int64_t)to_values * 16 : 0) + et % 16;
         // tokens of the tiles from t0 on, up to the end of the sequence (only the last group reaches beyond it)
         const int tokens = groups.count > 0 ? (groups.count - 1) * 16 + min(16, item.length - group_token(groups, groups.count - 1)) - t0 * 128 : 0;
@@ -602,7 +603,7 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
         const auto load_exponent = [&](int j) {
             const int r = rows[j & (kRing - 1)][et / 16];
             exponent = kNoToken;
-            if (kv < 2 && r >= 0 && j * 128 + et < tokens) exponent = fetch_signed1(exponent_base + (uint64_t)(uint32_t)r * 16);
+            if (has_exponent && r >= 0 && j * 128 + et < tokens) exponent = fetch_signed1(exponent_base + (uint64_t)(uint32_t)r * 16);
         };
         // blocks that begin beyond the head's end take no part, whatever they hold
         const uint32_t inside = (part * 32 < a.c.dim ? 0xffffu : 0u) | (part * 32 + BLOCK % 32 < a.c.dim ? 0xffff0000u : 0u);
@@ -660,7 +661,7 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
             const int slot = j & (kRing - 1);
             ok = ok && warp_wait(bar(bars.k_empty, j % S::STAGES), ((j / S::STAGES) & 1) ^ 1, kWaitNs);
             // the scores of tile j - 2 are there: the softmax has done with tile j - 4, whose slot this is
-            if (kv < 2) {
+            if (has_exponent) {
                 exponents[slot][kv][et] = (int16_t)exponent;
                 const int top = __reduce_max_sync(~0u, exponent);
                 if (lane == 0) largest[j & 1][kv][et / 32] = top;
