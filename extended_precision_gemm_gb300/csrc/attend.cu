@@ -1,13 +1,27 @@
 // attend.cu -- attention over the 4-bit cache for few queries, and the sum of parts.
 //
 // Few queries of a key/value head (a token's group of heads, a few proposed tokens)
-// read the whole cache: the floor is its bytes.  A warp takes 16 tokens at a time,
-// straight from global memory into the registers of mma.sync fragments: scores as
-// S^T = K Q^T (16 tokens by 8 queries), the sum as O^T = V^T P^T, so that 8 queries
-// fill an instruction that 16 rows of queries would leave half empty, and the codes
-// of a row are contiguous in a thread.  (tcgen05 wants its operands in shared memory
-// and 128 rows: each 4-bit row would be written there in 16 bits and read again,
-// four times its bytes, for a product that uses 8 of the columns.)
+// read the whole cache: the floor is its bytes.  A warp takes 32 tokens a round, two
+// groups of 16 that are independent of each other, copied to its own part of shared
+// memory one or two rounds ahead (cp.async; no block waits for another warp), and makes
+// mma.sync fragments of them: scores as S^T = K Q^T (16 tokens by 8 queries), the sum as
+// O^T = V^T P^T, so that 8 queries fill an instruction that 16 rows of queries would
+// leave half empty, and the codes of a row are contiguous in a thread.  (tcgen05 wants
+// its operands in shared memory and 128 rows: each 4-bit row would be written there in
+// 16 bits and read again, four times its bytes, for a product that uses 8 of the
+// columns.)
+//
+// All groups of all (8 columns, key/value head) items in a row are cut into equal runs, one
+// for each CTA that the SMs hold: lengths may differ as they like.  An item that a run's
+// end cuts leaves parts, which join_cut_kernel adds.
+//
+// Measured (bfloat16): 64 sequences of 100 to 8192 tokens, 8 heads of 128, 8 queries each,
+// mxfp4: 101 us for 291 MB (2.9 TB/s); one of 131071, nvfp4: 47 us for 153 MB, 40 of them
+// here.  Bound by issue and the latency of its own instructions: a group takes 362
+// instructions, of which 140 run at half rate (conversions of codes, products with
+// scales, movmatrix), by 12 warps an SM (157 registers).  A fourth CTA costs more
+// instructions than its warps give, whole rows of codes at a time and 16 tokens a round
+// took 53 us for 47.
 //
 // The codes become 16-bit floating point by one conversion for two, the block's
 // scale one packed multiplication for two, exactly: E4M3 times E2M1 has 6 bits;

@@ -3,23 +3,35 @@
 //
 // A CTA takes tiles of 128 (query token, head of the group) rows of one sequence and
 // key/value head, two at a time (one of width 256), over the cache in tiles of 128
-// tokens, eight groups of 16 wherever their pages lie.  Warps: 0-3 and 4-7 the
-// softmax of a tile of rows each, 8-11 turn codes into 16-bit keys and values, 12
-// issues the MMAs:
+// tokens, eight groups of 16 wherever their pages lie.  Warps: four for the softmax of
+// each tile of rows, then 8 (16 of width 256) that turn codes into 16-bit keys and
+// values, then one that issues the MMAs:
 //   S = Q K^T       operands in shared memory, 128-byte swizzle, f32 in tensor memory;
 //   P = 2^(S f - m) a thread for a row, from tensor memory and back into it in 16
 //                   bits, over S;
 //   O += P V        P from tensor memory, V as it lies (tokens by head elements).
 // One tile's softmax overlaps the other's MMAs; O stays in tensor memory and is
-// multiplied only when a row's reference m has to follow (by more than 2^kLag).
+// multiplied only when a row's reference m has to follow: a row's weights are taken by
+// the m so far, in one pass, and only where 32 of them come to more than kMost does m
+// become the largest score, up to a whole number.
 //
-// The conversion is shared by the 256 rows: 256 codes a thread and tile.  Exponents of
-// rows become relative to the tile's largest, for keys a factor of all its scores
-// and for values one of all its weights: codes times scales are exact in 16 bits down
-// to 2^-18 of the tile's largest row, and rounded to 2^-40 of it.
+// The conversion is shared by the 256 rows.  Exponents of rows become relative to the
+// tile's largest, for keys a factor of all its scores and for values one of all its
+// weights: codes times scales are exact in 16 bits down to 2^-18 of the tile's largest
+// row, and rounded to 2^-40 of it.
 //
-// Bound: 4 * width operations a score on the tensor pipe, one 2^x a score, and about 5
-// instructions a score and 2 a code of issue.
+// Measured: a prompt of 8192 tokens, 32 heads over 8 of 128, mxfp4, bfloat16: 548 us, 1.0
+// PF/s (the simple kernel with mma.sync that was here first: 5008).  A pair of tiles takes
+// 4750 clocks for 128 tokens: each row's pass over its scores 2300 to 2550 (in four steps
+// of 32: wait for tensor memory, fma, 2^x, sum, round, store), then its products with V
+// and the next K, 1024, and the waits between; the tensor pipe is busy for 2048 of them, the
+// converters for 3000.  So the chain of one row's softmax and its MMAs bounds it.  Scores
+// of 64 tokens, in two buffers, would overlap them, but read Q from shared memory twice as
+// often: 593 us.  Three chunks of 100 to 700 tokens behind 2111 to 16000, 5 queries a head of
+// 256, nvfp4, float16: 332 us, 0.55 PF/s; the rest of the weights is a second product
+// there, K and V have one stage each, and the converters' stores (twice 64 KB a tile), the
+// MMAs' reads and the waits for each other's stage make 5900 clocks a tile.  Values in two
+// halves that come and go by themselves, or codes loaded a line at a time, changed nothing.
 #include <algorithm>
 
 #include "attend.cuh"
@@ -30,7 +42,7 @@ namespace {
 
 constexpr unsigned long long kWaitNs = 2000000000ULL;  // bounded waits: 2 s
 constexpr float kMost = 32768.0f;  // a row's reference follows where 32 weights are more than this in all
-constexpr int kShift = 3;      // ... and the values' exponent by more than 2^3 either way
+constexpr int kShift = 3;      // the values' exponent follows by more than 2^3 either way
 constexpr float kLift = 7.0f;  // the weight of a score equal to the reference is 2^(7 + up to 3 either way)
 constexpr int kFar = 64;       // values' exponents are at most so far below the largest seen
 constexpr int kRing = 4;  // tiles whose rows, exponents and marks are kept

@@ -2,10 +2,15 @@
 // places, and rows read back.
 //
 // Both move their bytes once (2 to 4 bytes a value on one side, 0.54 to 0.58 on the
-// other) and are bound by HBM, small batches by their launch.  A lane holds 8
-// consecutive values of a row; a row is 8, 16 or 32 lanes.  Keys may be rotated on
-// the way in: in 32 bits and what they leave (rotary.cuh), so that a value is rounded
-// once, to its code.
+// other), small batches in their launch.  A lane holds 8 consecutive values of a row; a
+// row is 8, 16 or 32 lanes, so that a block's largest value takes one or two exchanges
+// between lanes.  Keys may be rotated on the way in: in 32 bits and what they leave
+// (rotary.cuh), so that a value is rounded once, to its code.
+//
+// A prompt of 8192 tokens, 8 heads of 128, bfloat16, mxfp4: written with rotation 28 us,
+// without 18, read back 13 (42 MB each way, 6.3 us of a copy).  Bound by instructions: 22
+// million for a written batch, of which the rotation and what it leaves are 10 us; at 78
+// registers three blocks share an SM.  64 single tokens 3 us each way.
 #include "eight.cuh"
 #include "kv_cache.cuh"
 #include "rotary.cuh"
