@@ -107,6 +107,10 @@ constexpr int64_t kSurplus = 512;
 
 ddgemm_status attend_tiles_call(AttendArgs& a, int type, cudaStream_t st) {
     a.splits = attend_tile_parts(a);
+    if (a.above > 0) {  // every token has room in it, those of other sequences too: 256 MB at most
+        const int64_t row = a.c.width * 4 + (int64_t)sizeof(float4), most = (256LL << 20) / (row * a.b.tokens * a.heads);
+        a.splits = (int)std::max<int64_t>(1, std::min<int64_t>(a.splits, most));
+    }
     Workspace ws(st);
     const int64_t rows = a.splits > 1 ? a.splits * a.b.tokens * a.heads : 0;
     const int64_t parts = ws.reserve(rows * (int64_t)sizeof(float4)), sums = ws.reserve(rows * a.c.width * 4);
@@ -233,10 +237,11 @@ ddgemm_status dd_mx4_attention(const ddgemm_mx4_cache* cache, const ddgemm_batch
     a.out = out, a.ot = out_token, a.oh = out_head;
     a.heads = (int)q_heads;
     a.group = (int)(q_heads / cache->heads);
-    const int64_t far = 1LL << 30;  // beyond every position
-    a.window = (int)std::min(window, far);
-    a.sinks = (int)std::min(sinks, far);
+    const int64_t far = (1LL << 31) - 65536;  // a window or sinks of so many leave nothing out
+    a.window = window < far && sinks < far ? (int)window : 0;
+    a.sinks = a.window > 0 ? (int)sinks : 0;
     a.scale = scale * 1.4426950408889634f;
+    if (!std::isfinite(a.scale)) return DDGEMM_ERR_INVALID_ARG;
     const auto whole = [&](const void* p, int64_t t, int64_t h) { return aligned16(p) && (T <= 1 || t % 8 == 0) && (q_heads <= 1 || h % 8 == 0); };
     a.vec_q = whole(q, q_token, q_head);
     a.vec_out = whole(out, out_token, out_head);

@@ -898,7 +898,8 @@ ddgemm_status dd_mx4_cache_read(const ddgemm_mx4_cache* cache, const ddgemm_batc
 /*
  * Attention of the batch's tokens over the cache: out = softmax(scale q k^T) v, a
  * query at position p over the tokens j <= p of its sequence, with a window w > 0
- * those with j > p - w or j < sinks.  q and out: tokens x q_heads x head_dim of
+ * those with j > p - w or j < sinks (a window or sinks of 2^31 - 65536 and more are
+ * none).  The scale is finite.  q and out: tokens x q_heads x head_dim of
  * `type` (DDGEMM_BF16 or DDGEMM_F16), any strides of tokens and heads; q_heads is a
  * multiple of the cache's heads, and query head h uses head h / (q_heads / heads).
  * The cache's values enter exactly (of sequences with more than 48 rows of queries a

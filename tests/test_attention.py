@@ -343,3 +343,10 @@ def test_cache_and_batch_arguments(binding):
         with pytest.raises((ValueError, TypeError)):
             wrong()
     assert not calls
+
+
+@pytest.mark.parametrize("scale", (float("nan"), float("inf"), -float("inf"), 3e38))
+def test_attention_refuses_scales_that_are_not_finite(lib, scale):
+    """In base 2, too: 3e38 log2(e) is none."""
+    for tokens, window in ((4, 0), (400, 3)):
+        assert lib.dd_mx4_attention(ctypes.byref(cache()), ctypes.byref(batch(tokens=tokens)), 1, 4, P[7], 256, 64, window, 0, scale, P[9], 256, 64, None) == 1

@@ -407,3 +407,21 @@ def test_calls_on_two_streams_at_once():
         got = [(ddg.mx4_attention(q, cache, *batch.dev, stream=a), ddg.mx4_attention(q2, cache2, *few.dev, stream=b)) for _ in range(5)]
         torch.cuda.synchronize()
         assert all(torch.equal(x, want) and torch.equal(y, want2) for x, y in got)
+
+
+@pytest.mark.parametrize("n", (1, 60))
+def test_windows_and_sinks_beyond_every_position(n):
+    import torch
+    batch = Batch([(90, n), (200, n)], 16)
+    cache, _ = filled(batch, 2, 64, "mxfp4")
+    q = queries(batch, 4, 64, "bfloat16")
+    want = ddg.mx4_attention(q, cache, *batch.dev)
+    for window, sinks in ((2**31 - 65536, 0), (2**31 - 65537, 3), (2**62, 1), (5, 2**40), (5, 2**31 - 65537), (2**31 - 65537, 2**31 - 65537)):
+        assert torch.equal(ddg.mx4_attention(q, cache, *batch.dev, window=window, sinks=sinks), want), (window, sinks)
+
+
+def test_a_long_part_among_many_single_tokens():
+    """More sequences than the long parts' rows could be of: their tiles are numbered by tokens."""
+    sizes = [(30 + b % 50, 1) for b in range(300)] + [(400, 333)] + [(20 + b, 1) for b in range(200)] + [(260, 7), (90, 6), (150, 150)]
+    run(sizes, 16, 2, 8, 64, "nvfp4", "bfloat16", seed=4)
+    run(sizes, 16, 1, 1, 128, "mxfp4", "float16", 40, 2, seed=5, lead=3, tail=5)
