@@ -748,9 +748,15 @@ __global__ void __launch_bounds__(128) join_kernel(const AttendArgs a, float lif
     const int64_t token = row / a.heads, h = row % a.heads;
     const int s = search(a.b, token, [&](int i) { return a.b.starts[i]; });
     if (s < 0 || a.b.starts[s] < 0 || a.b.starts[s + 1] <= token || a.b.starts[s + 1] > a.b.tokens || !a.takes(a.b.starts[s + 1] - a.b.starts[s])) return;
+    // the item that the row is of, and its parts
+    constexpr int ROWS = WIDTH == 256 ? 128 : 256;
+    const int s0 = a.b.starts[s], tokens = a.b.starts[s + 1] - s0, before = a.b.lengths[s] - tokens;
+    const int column = ((int)token - s0) * a.group + (int)(h % a.group), first = column / ROWS * ROWS, last = min(first + ROWS, tokens * a.group) - 1;
+    const int splits = parts_of((groups_of(a.c, a.b, before + first / a.group, before + last / a.group, a.window, a.sinks).count + 7) / 8, a.splits);
+    if (splits == 1) return;  // written as a whole
     float m = minus_infinity(), M = m;
     float4 mine = make_float4(m, m, 0.0f, 0.0f);
-    for (int i = lane; i < a.splits; i += 32) {
+    for (int i = lane; i < splits; i += 32) {
         const float4 p = a.part[i * rows + row];
         if (i < 32) mine = p;
         m = fmaxf(m, p.x);
@@ -764,11 +770,11 @@ __global__ void __launch_bounds__(128) join_kernel(const AttendArgs a, float lif
     const bool any = __shfl_sync(~0u, mine.w, 0) != 0.0f;
     const int at = ((warp % WARPS) * 32 + lane) * 4;
     float y[4] = {0.0f, 0.0f, 0.0f, 0.0f}, l = 0.0f;
-    for (int i0 = 0; i0 < a.splits; i0 += 32) {
-        if (i0 > 0) mine = i0 + lane < a.splits ? a.part[(i0 + lane) * rows + row] : make_float4(minus_infinity(), minus_infinity(), 0.0f, 0.0f);
+    for (int i0 = 0; i0 < splits; i0 += 32) {
+        if (i0 > 0) mine = i0 + lane < splits ? a.part[(i0 + lane) * rows + row] : make_float4(minus_infinity(), minus_infinity(), 0.0f, 0.0f);
         l += mine.z * power2(mine.x - reference(m));
         const float f = power2(mine.y - reference(M));
-        const int n = min(32, a.splits - i0);
+        const int n = min(32, splits - i0);
 #pragma unroll 8
         for (int i = 0; i < n; ++i) {
             const float w = __shfl_sync(~0u, f, i);

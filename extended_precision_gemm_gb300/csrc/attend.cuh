@@ -31,7 +31,7 @@ struct AttendArgs {
     bool vec_q, vec_out;
     int64_t above, upto;  // sequences of so many rows (tokens times queries a key/value head) are taken, the others left out
     int step;             // 0, or see first_tile
-    int splits;    // attend_tile.cu: parts of every row; attend.cu: CTAs, or (together) CTAs of a cluster
+    int splits;    // attend_tile.cu: most parts of a row; attend.cu: CTAs, or (together) CTAs of a cluster
     bool together;
     float4* part;  // (m, M, l, 1 if any token is seen) of a part: by split and row (token, query head), or by CTA (attend.cu)
     float* sums;   // its o, `width` elements
@@ -82,6 +82,8 @@ __device__ __forceinline__ Groups groups_of(const CacheView& c, const BatchView&
     g.count = g.sink + end - g.low;
     return g;
 }
+// Parts of tiles of 128 tokens that an item is cut into (attend_tile.cu): of four tiles at least.
+__device__ __forceinline__ int parts_of(int tiles, int most) { return max(1, min(most, (tiles + 3) / 4)); }
 __device__ __forceinline__ int group_token(const Groups& g, int i) { return (i < g.sink ? i : i - g.sink + g.low) * 16; }
 
 __device__ __forceinline__ bool sees(int p, int j, int window, int sinks) {

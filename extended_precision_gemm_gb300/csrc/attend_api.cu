@@ -245,7 +245,7 @@ ddgemm_status dd_mx4_attention(const ddgemm_mx4_cache* cache, const ddgemm_batch
     const auto whole = [&](const void* p, int64_t t, int64_t h) { return aligned16(p) && (T <= 1 || t % 8 == 0) && (q_heads <= 1 || h % 8 == 0); };
     a.vec_q = whole(q, q_token, q_head);
     a.vec_out = whole(out, out_token, out_head);
-    if (a.tiles(8) * cache->heads >= (1LL << 31)) return DDGEMM_ERR_UNSUPPORTED;
+    if (a.tiles(8) * cache->heads >= (1LL << 31) || T * a.group >= (1LL << 31)) return DDGEMM_ERR_UNSUPPORTED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int64_t rows = T * a.group, surplus = (T - batch->batch) * a.group;
     const bool tiles = cache->pages > 0 && (rows > kColumnsMost * batch->batch || surplus > kSurplus);

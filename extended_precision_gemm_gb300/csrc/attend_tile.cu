@@ -28,7 +28,7 @@
 // converters for 3000.  So the chain of one row's softmax and its MMAs bounds it.  Scores
 // of 64 tokens, in two buffers, would overlap them, but read Q from shared memory twice as
 // often: 593 us.  Three chunks of 100 to 700 tokens behind 2111 to 16000, 5 queries a head of
-// 256, nvfp4, float16: 332 us, 0.55 PF/s; the rest of the weights is a second product
+// 256, nvfp4, float16: 336 us, 0.54 PF/s; the rest of the weights is a second product
 // there, K and V have one stage each, and the converters' stores (twice 64 KB a tile), the
 // MMAs' reads and the waits for each other's stage make 5900 clocks a tile.  Values in two
 // halves that come and go by themselves, or codes loaded a line at a time, changed nothing.
@@ -56,7 +56,7 @@ template <int FMT> __host__ __device__ constexpr int lift_of() { return FMT == k
 template <int WIDTH>
 struct Shape {
     static constexpr int NQ = WIDTH == 256 ? 1 : 2;       // tiles of rows
-    // threads that convert: where one tile of rows shares them, twice as many (three chunks, see the end: 332 us for 363)
+    // threads that convert: where one tile of rows shares them, twice as many (three chunks, see above: 336 us for 363)
     static constexpr int CONVERTERS = WIDTH == 256 ? 512 : 256;
     static constexpr int MMA_WARP = 4 * NQ + CONVERTERS / 32, THREADS = (MMA_WARP + 4) * 32;  // the last three warps have no task
     static constexpr int STAGES = WIDTH == 256 ? 1 : 2;   // of keys, and of values
@@ -232,7 +232,7 @@ struct Barriers {
 // of groups g0 .. g1 - 1 that the row sees.
 template <typename T, int WIDTH, int FMT>
 __device__ __noinline__ void mark_nan(const AttendArgs& a, const Item& item, const Groups& groups, int head, int p, int g0, int g1,
-                                      int64_t token, int64_t h) {
+                                      int64_t token, int64_t h, bool cut) {
     constexpr int BLOCK = mx4_block(FMT), BLOCKS = WIDTH / BLOCK;
     uint32_t blocks = 0;
     for (int g = g0; g < g1; ++g) {
@@ -251,7 +251,7 @@ __device__ __noinline__ void mark_nan(const AttendArgs& a, const Item& item, con
     T* out = static_cast<T*>(a.out) + token * a.ot + h * a.oh;
     for (int d = 0; d < a.c.dim; ++d) {
         if (!(blocks >> (d / BLOCK) & 1)) continue;
-        if (a.splits > 1) a.sums[part + d] = not_a_number();
+        if (cut) a.sums[part + d] = not_a_number();
         else out[d] = from_float<T>(not_a_number());
     }
 }
@@ -267,6 +267,7 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
     __shared__ int rows[kRing][8];  // of groups of keys, in 16s, -1 where there is no page
     __shared__ int16_t exponents[kRing][2][128];  // of keys and values
     __shared__ int any_nan;                       // in values
+    __shared__ bool cut;                          // the item has other parts (here, not in a register all the way: 547 us for 560 of 8192 tokens)
     __shared__ __align__(16) int largest[2][2][4];  // of the tiles in turn
 
     pdl_wait();
@@ -281,7 +282,11 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
     const int p0 = position(0), p1 = position(item.columns - 1);
     const Groups groups = groups_of(a.c, a.b, p0, p1, a.window, a.sinks);
     const int tiles = (groups.count + 7) / 8;
-    const int t0 = (int)((int64_t)tiles * blockIdx.z / a.splits), t1 = (int)((int64_t)tiles * (blockIdx.z + 1) / a.splits);
+    const int parts = parts_of(tiles, a.splits);
+    if ((int)blockIdx.z >= parts) return;
+    if (threadIdx.x == 0) cut = parts > 1;
+    // up to 2^24 tiles, 64 parts
+    const int t0 = (int)((unsigned)tiles * blockIdx.z / (unsigned)parts), t1 = (int)((unsigned)tiles * (blockIdx.z + 1) / (unsigned)parts);
     // tiles that the rows of tile x see, counted from t0
     int need[2] = {0, 0};
 #pragma unroll
@@ -526,7 +531,7 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
         const int64_t out_row = token * a.heads + h;
         const int64_t part = (int64_t)blockIdx.z * (a.b.tokens * a.heads) + out_row;
         const Finish z = finish_of(m, M, l, kLift + lift_of<FMT>(), p >= 0);
-        if (a.splits > 1 && have) a.part[part] = make_float4(m, M, l, p >= 0 ? 1.0f : 0.0f);
+        if (cut && have) a.part[part] = make_float4(m, M, l, p >= 0 ? 1.0f : 0.0f);
 #pragma unroll 1
         for (int c = 0; c < WIDTH; c += 32) {
             uint32_t v[32];
@@ -537,7 +542,7 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
                 for (int i = 0; i < 32; ++i) v[i] = 0;
             }
             if (have) {
-                if (a.splits > 1) {
+                if (cut) {
                     float4* to = reinterpret_cast<float4*>(a.sums + part * WIDTH + c);
     #pragma unroll
                     for (int i = 0; i < 8; ++i)
@@ -811,7 +816,7 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
         const int p = position(threadIdx.x), query = item.column + threadIdx.x;
         const int64_t token = item.first_token + query / a.group, h = head * a.group + query % a.group;
         const int x = threadIdx.x / 128;
-        mark_nan<T, WIDTH, FMT>(a, item, groups, head, p, t0 * 8, min(groups.count, (t0 + need[x]) * 8), token, h);
+        mark_nan<T, WIDTH, FMT>(a, item, groups, head, p, t0 * 8, min(groups.count, (t0 + need[x]) * 8), token, h, cut);
     }
 }
 
@@ -843,8 +848,10 @@ cudaError_t by_width(const AttendArgs& a, cudaStream_t st) {
 }  // namespace
 
 // Enough items for two rounds of the SMs are left whole; fewer are cut so that there are
-// four rounds of parts, of 512 tokens at least: lengths differ, and a part's start costs
-// 3 us.
+// up to four rounds of parts, of 512 tokens at least: lengths differ, and a part's start
+// costs 3 us.  The host knows the longest sequence that the page table has room for; how
+// many parts an item has goes by its own length, on the device (512 tokens of a prompt
+// with a table for 8192: 85 us in equal parts of every row).
 int attend_tile_parts(const AttendArgs& a) {
     const int rows = a.c.width == 256 ? 128 : 256;
     // sequences that may be taken, if each has a token at least

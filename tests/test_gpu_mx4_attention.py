@@ -425,3 +425,16 @@ def test_a_long_part_among_many_single_tokens():
     sizes = [(30 + b % 50, 1) for b in range(300)] + [(400, 333)] + [(20 + b, 1) for b in range(200)] + [(260, 7), (90, 6), (150, 150)]
     run(sizes, 16, 2, 8, 64, "nvfp4", "bfloat16", seed=4)
     run(sizes, 16, 1, 1, 128, "mxfp4", "float16", 40, 2, seed=5, lead=3, tail=5)
+
+
+@pytest.mark.parametrize("fmt,dim", (("mxfp4", 64), ("nvfp4", 128), ("mxfp4", 256)))
+def test_a_page_table_for_far_more_than_there_is(fmt, dim):
+    """How many parts a row has goes by its own sequence: none, one, some and the most of them."""
+    import torch
+    sizes = [(0, 0), (70, 70), (511, 100), (513, 90), (1100, 130), (2600, 70), (40, 60)]
+    for window, sinks in ((0, 0), (600, 20)):
+        batch, cache, values, q, y = run(sizes, 16, 1, 2, dim, fmt, "bfloat16", window, sinks, seed=6, lead=1, tail=2)
+        starts, lengths, table = batch.dev
+        wide = torch.nn.functional.pad(table, (0, 2000), value=-1)
+        z = ddg.mx4_attention(q, cache, starts, lengths, wide, window=window, sinks=sinks)
+        check(z, q, batch, values, "bfloat16", window, sinks)
