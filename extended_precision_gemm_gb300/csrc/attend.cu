@@ -177,7 +177,9 @@ __device__ __forceinline__ void half_scales(const uint8_t* bytes, int e, uint32_
             if (b + 1 < N) h[b + 1] = __byte_perm(h2, h2, 0x3232);
         } else {
             const auto half = [&](uint32_t byte) {
-                const int t = min(max((int)byte - e - 127 + kMxLift + 15, 0), 30);
+                // at most 2^kMxLift, which is what the row's own exponent gives its largest: bytes that do not belong
+                // together, of rows that no token has, stay finite (their weight is 0, and 0 times infinity is NaN)
+                const int t = min(max((int)byte - e - 127 + kMxLift + 15, 0), kMxLift + 15);
                 return byte == 255u ? 0x7fff7fffu : (uint32_t)t * 0x04000400u;
             };
             h[b] = half(two & 0xffu);

@@ -1,0 +1,58 @@
+"""What rows that no query sees hold does not matter to attention, whatever their
+bytes: rows behind a sequence's end, of pages that no sequence has, of later tokens."""
+import numpy as np
+import pytest
+
+import extended_precision_gemm_gb300 as ddg
+
+from attention_util import Batch, check, filled, queries
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = ("mxfp4", "nvfp4")
+DTYPES = ("bfloat16", "float16")
+
+
+def no_token(batch):
+    """Which rows (pages, page_size) of the cache no sequence has."""
+    free = np.ones((batch.pages, batch.page), dtype=bool)
+    for b, (length, _) in enumerate(batch.sizes):
+        for j in range(length):
+            free[batch.place(b, j)] = False
+    return free
+
+
+def bytes_of(kind, rng, shape):
+    if kind == "any":
+        return rng.integers(0, 256, shape)
+    return np.full(shape, kind)
+
+
+# (codes, scales, exponents) of the rows: memory that was not cleared, scales that do not belong to their exponent
+FILLS = ((0, 0, 0), (0xCD, 0xCD, 0xCD), ("any", 254, 0), ("any", 0x7E, 0x7F), ("any", "any", 0x81), ("any", "any", 0x80), ("any", "any", "any"), (0xFF, 0xFF, 0xFF))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", (64, 100, 128, 256))
+@pytest.mark.parametrize("n", (1, 3, 60))
+def test_rows_that_no_token_has(fmt, dtype, dim, n):
+    import torch
+    batch = Batch([(200, n), (77, n), (2500, 1), (65, n), (n, n)], 64, seed=dim)
+    cache, values = filled(batch, 2, dim, fmt, dim)
+    q = queries(batch, 8, dim, dtype)
+    free = torch.from_numpy(no_token(batch)).cuda()
+    rng = np.random.default_rng(n)
+    parts = (cache.codes, cache.scales, cache.exponents)
+    for window, sinks in ((0, 0), (50, 3)):
+        want = None
+        for kinds in FILLS:
+            for t, kind in zip(parts, kinds):
+                bytes_ = torch.from_numpy(bytes_of(kind, rng, tuple(t.shape)).astype(np.uint8)).cuda().view(t.dtype)
+                t.copy_(torch.where(free[:, None, None].reshape(free.shape[0], 1, 1, free.shape[1], *[1] * (t.dim() - 4)), bytes_, t))
+            y = ddg.mx4_attention(q, cache, *batch.dev, window=window, sinks=sinks)
+            if want is None:
+                check(y, q, batch, values, dtype, window, sinks)
+                want = y
+            assert torch.equal(y, want), (kinds, window)
+    assert ddg.wait_timeouts() == 0
