@@ -70,16 +70,19 @@ __device__ __forceinline__ float reference(float m) { return m == minus_infinity
 struct Groups {
     int sink, low, count;
 };
-// The last one is at most the first that the page table does not reach.
+// Beyond the page table the list goes on as far only as makes every query that lies there see a token without a page:
+// to the first group that the table does not reach, and with a window so far that each of an item's queries (of up to
+// 256 positions in a row) has the begin of its own window in the list: p - window is less than 16 low + 271.
 __device__ __forceinline__ Groups groups_of(const CacheView& c, const BatchView& b, int p0, int p1, int window, int sinks) {
     Groups g{0, 0, 0};
     if (p1 < 0) return g;
-    const int end = (int)min((int64_t)p1 / 16 + 1, (int64_t)b.table_pages * c.page_size / 16 + 1);
-    if (window > 0 && p0 >= window) {
-        g.low = min((p0 - window + 1) / 16, end - 1);
+    int64_t most = (int64_t)b.table_pages * c.page_size / 16 + 1;
+    if (window > 0) {
+        if (p0 >= window) g.low = (p0 - window + 1) / 16;
         g.sink = min((int)(((unsigned)min(sinks, p1 + 1) + 15u) / 16u), g.low);
+        most = max(most, (int64_t)g.low + 17);
     }
-    g.count = g.sink + end - g.low;
+    g.count = g.sink + (int)min((int64_t)p1 / 16 + 1, most) - g.low;
     return g;
 }
 // Parts of tiles of 128 tokens that an item is cut into (attend_tile.cu): of four tiles at least.

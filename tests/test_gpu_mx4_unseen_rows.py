@@ -5,7 +5,8 @@ import pytest
 
 import extended_precision_gemm_gb300 as ddg
 
-from attention_util import Batch, check, filled, queries
+from attention_bounds import near
+from attention_util import Batch, filled, queries
 
 pytestmark = pytest.mark.gpu
 
@@ -52,7 +53,31 @@ def test_rows_that_no_token_has(fmt, dtype, dim, n):
                 t.copy_(torch.where(free[:, None, None].reshape(free.shape[0], 1, 1, free.shape[1], *[1] * (t.dim() - 4)), bytes_, t))
             y = ddg.mx4_attention(q, cache, *batch.dev, window=window, sinks=sinks)
             if want is None:
-                check(y, q, batch, values, dtype, window, sinks)
+                near(y, q, batch, values, dtype, window, sinks)
                 want = y
             assert torch.equal(y, want), (kinds, window)
     assert ddg.wait_timeouts() == 0
+
+
+@pytest.mark.parametrize("group", (1, 4))
+@pytest.mark.parametrize("window,sinks", ((1, 0), (1, 4), (7, 3), (16, 4), (16, 40), (100, 0), (100, 4), (300, 20), (5000, 1)))
+@pytest.mark.parametrize("n", (1, 11, 40, 300))
+def test_page_tables_that_end_before_the_window(n, window, sinks, group):
+    """A query beyond the table does not see itself: NaN, sinks or none.  Those within it are what they are without."""
+    import torch
+    batch = Batch([(400, n), (3000, 1), (40, 1)], 16, table_pad=0)
+    cache, values = filled(batch, 1, 64, "mxfp4")
+    q = queries(batch, group, 64, "bfloat16")
+    want = ddg.mx4_attention(q, cache, *batch.dev, window=window, sinks=sinks)
+    near(want, q, batch, values, "bfloat16", window, sinks)
+    p = np.concatenate([batch.positions(b) for b in range(3)])
+    for pages in (1, 2, 4, 9, 18, 24):
+        y = ddg.mx4_attention(q, cache, *batch.dev[:2], batch.dev[2][:, :pages].contiguous(), window=window, sinks=sinks)
+        hit = torch.from_numpy(p >= 16 * pages)
+        assert torch.isnan(y[hit]).all(), pages
+        near(y, q, batch, values, "bfloat16", window, sinks, rows=~hit.numpy())  # parts may be others
+    far = batch.dev[1].clone()
+    for length in (10000, (1 << 31) - 1):
+        far[0] = length
+        y = ddg.mx4_attention(q, cache, batch.dev[0], far, batch.dev[2], window=window, sinks=sinks)
+        assert torch.isnan(y[:n]).all() and torch.equal(y[n:], want[n:]), length  # the same table, the same parts
