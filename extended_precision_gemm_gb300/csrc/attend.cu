@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : WIDTH == 128 ?
     constexpr int kStages = G::STAGES, kAhead = kStages - 1;
     extern __shared__ __align__(16) uint8_t shared[];  // [warp][stage], and [warp][8][ROW] floats behind an item's last group
     float* const sums = reinterpret_cast<float*>(shared);
-    __shared__ float s_m[kWarps][8], s_M[kWarps][8], s_l[kWarps][8];
+    __shared__ float s_m[kWarps][8], s_R[kWarps][8], s_l[kWarps][8];
     __shared__ int64_t scan[kWarps];
     __shared__ int64_t found_before;
     __shared__ int found;
@@ -429,8 +429,8 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : WIDTH == 128 ?
         float o[KS][4];
 #pragma unroll
         for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-        float ma = minus_infinity(), mb = ma, Ma = ma, Mb = ma, la = 0.0f, lb = 0.0f;
-        float ra = 0.0f, rb = 0.0f, Ra = -kLift, Rb = -kLift;  // what is subtracted from exponents
+        float ma = minus_infinity(), mb = ma, Ra = ma, Rb = ma, la = 0.0f, lb = 0.0f;
+        float sub_ma = 0.0f, sub_mb = 0.0f, sub_Ra = -kLift, sub_Rb = -kLift;  // what is subtracted from scores and exponents
 
         uint32_t stage = 0;
 #pragma unroll 1
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : WIDTH == 128 ?
             stage = stage == kAhead * 2 * G::BYTES ? 0 : stage + 2 * G::BYTES;
 
             // scores: of each group tokens r and r + 8 in rows r and r + 8
-            float s[2][4], u[2][4];
+            float s[2][4], e[2][2];
             const auto score_group = [&](auto N) {
                 constexpr int n = decltype(N)::value;
                 const uint8_t* const from = at + n * G::BYTES;
@@ -477,11 +477,12 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : WIDTH == 128 ?
                 s[n][1] = (x[1] + y[1]) * qf1 * k0;
                 s[n][2] = (x[2] + y[2]) * qf0 * k1;
                 s[n][3] = (x[3] + y[3]) * qf1 * k1;
-                float e0 = (float)reinterpret_cast<const int8_t*>(from + G::E0 + 16)[r], e1 = (float)reinterpret_cast<const int8_t*>(from + G::E0 + 16)[r + 8];
+                e[n][0] = (float)reinterpret_cast<const int8_t*>(from + G::E0 + 16)[r];
+                e[n][1] = (float)reinterpret_cast<const int8_t*>(from + G::E0 + 16)[r + 8];
                 if (!whole) {
                     if (bad >> n & 1) {
                         s[n][0] = s[n][1] = s[n][2] = s[n][3] = not_a_number();
-                        e0 = e1 = 0.0f;
+                        e[n][0] = e[n][1] = 0.0f;
                     }
                     const int t0 = group_token(groups, group + n) + r;
                     const bool there = group + n < g1;
@@ -490,30 +491,48 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : WIDTH == 128 ?
                     if (!there || !sees(pa, t0 + 8, a.window, a.sinks)) s[n][2] = minus_infinity();
                     if (!there || !sees(pb, t0 + 8, a.window, a.sinks)) s[n][3] = minus_infinity();
                 }
-                u[n][0] = s[n][0] + e0;
-                u[n][1] = s[n][1] + e0;
-                u[n][2] = s[n][2] + e1;
-                u[n][3] = s[n][3] + e1;
             };
             static_for<2>(score_group);
-            const float sa = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2])), sb = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
-            const float ua = fmaxf(fmaxf(u[0][0], u[0][2]), fmaxf(u[1][0], u[1][2])), ub = fmaxf(fmaxf(u[0][1], u[0][3]), fmaxf(u[1][1], u[1][3]));
-            if (__any_sync(~0u, sa > ma + kLag || sb > mb + kLag || ua > Ma + kLag || ub > Mb + kLag)) {
-                float na = sa, nb = sb, Na = ua, Nb = ub;
+            // what a weight in the sum and a token's weight are 2 to the power of
+            float x[2][4], t[2][4];
+            const auto exponents = [&]() {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        t[n][i] = s[n][i] - (i & 1 ? sub_mb : sub_ma);
+                        x[n][i] = t[n][i] + (e[n][i / 2] - (i & 1 ? sub_Rb : sub_Ra));
+                    }
+                }
+            };
+            exponents();
+            const auto most = [](const float (&v)[2][4], int i) { return fmaxf(fmaxf(v[0][i], v[0][i + 2]), fmaxf(v[1][i], v[1][i + 2])); };
+            const float sa = most(s, 0), sb = most(s, 1);
+            if (__any_sync(~0u, sa > ma + kLag || sb > mb + kLag || fmaxf(most(x, 0), most(x, 1)) > kLag + kLift)) {
+                float na = sa, nb = sb;
 #pragma unroll
                 for (int d = 4; d < 32; d *= 2) {
                     na = fmaxf(na, __shfl_xor_sync(~0u, na, d));
                     nb = fmaxf(nb, __shfl_xor_sync(~0u, nb, d));
-                    Na = fmaxf(Na, __shfl_xor_sync(~0u, Na, d));
-                    Nb = fmaxf(Nb, __shfl_xor_sync(~0u, Nb, d));
                 }
                 na = fmaxf(ma, na);
                 nb = fmaxf(mb, nb);
-                Na = fmaxf(Ma, Na);
-                Nb = fmaxf(Mb, Nb);
                 la *= power2(ma - reference(na));
                 lb *= power2(mb - reference(nb));
-                const float fa = power2(Ma - reference(Na)), fb = power2(Mb - reference(Nb));
+                Ra = relative(Ra, ma, na);
+                Rb = relative(Rb, mb, nb);
+                ma = na, mb = nb;
+                sub_ma = reference(ma), sub_mb = reference(mb), sub_Ra = 0.0f, sub_Rb = 0.0f;
+                exponents();
+                float Na = most(x, 0), Nb = most(x, 1);
+#pragma unroll
+                for (int d = 4; d < 32; d *= 2) {
+                    Na = fmaxf(Na, __shfl_xor_sync(~0u, Na, d));
+                    Nb = fmaxf(Nb, __shfl_xor_sync(~0u, Nb, d));
+                }
+                Na = fmaxf(Ra, Na);
+                Nb = fmaxf(Rb, Nb);
+                const float fa = power2(Ra - reference(Na)), fb = power2(Rb - reference(Nb));
 #pragma unroll
                 for (int d = 0; d < KS; ++d) {
                     o[d][0] *= fa;
@@ -521,16 +540,17 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : WIDTH == 128 ?
                     o[d][2] *= fa;
                     o[d][3] *= fb;
                 }
-                ma = na, mb = nb, Ma = Na, Mb = Nb;
-                ra = reference(ma), rb = reference(mb), Ra = reference(Ma) - kLift, Rb = reference(Mb) - kLift;
+                Ra = Na, Rb = Nb;
+                sub_Ra = reference(Ra) - kLift, sub_Rb = reference(Rb) - kLift;
+                exponents();
             }
-            la += (power2(s[0][0] - ra) + power2(s[0][2] - ra)) + (power2(s[1][0] - ra) + power2(s[1][2] - ra));
-            lb += (power2(s[0][1] - rb) + power2(s[0][3] - rb)) + (power2(s[1][1] - rb) + power2(s[1][3] - rb));
+            la += (power2(t[0][0]) + power2(t[0][2])) + (power2(t[1][0]) + power2(t[1][2]));
+            lb += (power2(t[0][1]) + power2(t[0][3])) + (power2(t[1][1]) + power2(t[1][3]));
 
             const auto weigh_group = [&](auto N) {
                 constexpr int n = decltype(N)::value;
                 const uint8_t* const from = at + n * G::BYTES;
-                const float w[4] = {power2(u[n][0] - Ra), power2(u[n][1] - Rb), power2(u[n][2] - Ra), power2(u[n][3] - Rb)};
+                const float w[4] = {power2(x[n][0]), power2(x[n][1]), power2(x[n][2]), power2(x[n][3])};
                 const uint32_t h0 = half2_of(w[0], w[1]), h1 = half2_of(w[2], w[3]);
                 const uint32_t w0 = transpose8x8(h0), w1 = transpose8x8(h1);
                 uint32_t x0 = 0, x1 = 0;
@@ -617,8 +637,8 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : WIDTH == 128 ?
         if (r == 0) {
             s_m[warp][2 * c] = ma;
             s_m[warp][2 * c + 1] = mb;
-            s_M[warp][2 * c] = Ma;
-            s_M[warp][2 * c + 1] = Mb;
+            s_R[warp][2 * c] = Ra;
+            s_R[warp][2 * c + 1] = Rb;
             s_l[warp][2 * c] = la;
             s_l[warp][2 * c + 1] = lb;
         }
@@ -635,31 +655,28 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : WIDTH == 128 ?
         constexpr int LANES = kWarps * 32 / 8;  // threads of a column
         const int col = threadIdx.x / LANES, at = threadIdx.x % LANES;
         if (col < columns) {
-            float m = s_m[0][col], M = s_M[0][col];
+            float m = s_m[0][col], R = s_R[0][col];
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) {
-                m = fmaxf(m, s_m[w][col]);
-                M = fmaxf(M, s_M[w][col]);
-            }
+            for (int w = 1; w < kWarps; ++w) join_references(m, R, s_m[w][col], s_R[w][col]);
             float l = 0.0f, f[kWarps];
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 l += s_l[w][col] * power2(s_m[w][col] - reference(m));
-                f[w] = power2(s_M[w][col] - reference(M));
+                f[w] = power2(relative(s_R[w][col], s_m[w][col], m) - reference(R));
             }
             const bool any = before + (column0 + col) / a.group >= 0;
             const bool complete = !TOGETHER && g0 == 0 && g1 == groups.count;
             const int64_t token = seq.first_token + (column0 + col) / a.group, h = head * a.group + (column0 + col) % a.group;
             const int64_t part = (2LL * blockIdx.x + (g0 == 0 ? 1 : 0)) * 8 + col;
-            const Finish z = finish_of(m, M, l, kSumLift, any);
+            const Finish z = finish_of(R, l, kSumLift, any);
             T* out = static_cast<T*>(a.out) + token * a.ot + h * a.oh;
             float* const merged = sums + kWarps * 8 * ROW + col * ROW;
             if (TOGETHER && at == 0) {
                 merged[WIDTH] = m;
-                merged[WIDTH + 1] = M;
+                merged[WIDTH + 1] = R;
                 merged[WIDTH + 2] = l;
             }
-            if (!TOGETHER && !complete && at == 0) a.part[part] = make_float4(m, M, l, any ? 1.0f : 0.0f);
+            if (!TOGETHER && !complete && at == 0) a.part[part] = make_float4(m, R, l, any ? 1.0f : 0.0f);
 #pragma unroll
             for (int d = at * 4; d < WIDTH; d += LANES * 4) {
                 float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -682,21 +699,21 @@ __global__ void __launch_bounds__(kWarps * 32, WIDTH == 256 ? 2 : WIDTH == 128 ?
             const uint32_t merged = smem_addr(sums + kWarps * 8 * ROW);
             for (int col = rank; col < columns; col += a.splits) {
                 const uint32_t from = merged + col * ROW * 4;
-                float m = minus_infinity(), M = m, l = 0.0f, f[8];
+                float m = minus_infinity(), R = m, l = 0.0f, f[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     if (k >= a.splits) break;
-                    m = fmaxf(m, read_cluster(from + WIDTH * 4, k));
-                    M = fmaxf(M, f[k] = read_cluster(from + WIDTH * 4 + 4, k));
+                    join_references(m, R, read_cluster(from + WIDTH * 4, k), f[k] = read_cluster(from + WIDTH * 4 + 4, k));
                 }
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     if (k >= a.splits) break;
-                    l += read_cluster(from + WIDTH * 4 + 8, k) * power2(read_cluster(from + WIDTH * 4, k) - reference(m));
-                    f[k] = power2(f[k] - reference(M));
+                    const float own = read_cluster(from + WIDTH * 4, k);
+                    l += read_cluster(from + WIDTH * 4 + 8, k) * power2(own - reference(m));
+                    f[k] = power2(relative(f[k], own, m) - reference(R));
                 }
                 const bool any = before + (column0 + col) / a.group >= 0;
-                const Finish z = finish_of(m, M, l, kSumLift, any);
+                const Finish z = finish_of(R, l, kSumLift, any);
                 T* out = static_cast<T*>(a.out) + (int64_t)(seq.first_token + (column0 + col) / a.group) * a.ot +
                          (int64_t)(head * a.group + (column0 + col) % a.group) * a.oh;
                 for (int d = threadIdx.x; d < a.c.dim; d += kWarps * 32) {
@@ -756,26 +773,22 @@ __global__ void __launch_bounds__(128) join_kernel(const AttendArgs a, float lif
     const int column = ((int)token - s0) * a.group + (int)(h % a.group), first = column / ROWS * ROWS, last = min(first + ROWS, tokens * a.group) - 1;
     const int splits = parts_of((groups_of(a.c, a.b, before + first / a.group, before + last / a.group, a.window, a.sinks).count + 7) / 8, a.splits);
     if (splits == 1) return;  // written as a whole
-    float m = minus_infinity(), M = m;
+    float m = minus_infinity(), R = m;
     float4 mine = make_float4(m, m, 0.0f, 0.0f);
     for (int i = lane; i < splits; i += 32) {
         const float4 p = a.part[i * rows + row];
         if (i < 32) mine = p;
-        m = fmaxf(m, p.x);
-        M = fmaxf(M, p.y);
+        join_references(m, R, p.x, p.y);
     }
 #pragma unroll
-    for (int d = 16; d > 0; d /= 2) {
-        m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-        M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
-    }
+    for (int d = 16; d > 0; d /= 2) join_references(m, R, __shfl_xor_sync(~0u, m, d), __shfl_xor_sync(~0u, R, d));
     const bool any = __shfl_sync(~0u, mine.w, 0) != 0.0f;
     const int at = ((warp % WARPS) * 32 + lane) * 4;
     float y[4] = {0.0f, 0.0f, 0.0f, 0.0f}, l = 0.0f;
     for (int i0 = 0; i0 < splits; i0 += 32) {
         if (i0 > 0) mine = i0 + lane < splits ? a.part[(i0 + lane) * rows + row] : make_float4(minus_infinity(), minus_infinity(), 0.0f, 0.0f);
         l += mine.z * power2(mine.x - reference(m));
-        const float f = power2(mine.y - reference(M));
+        const float f = power2(relative(mine.y, mine.x, m) - reference(R));
         const int n = min(32, splits - i0);
 #pragma unroll 8
         for (int i = 0; i < n; ++i) {
@@ -791,7 +804,7 @@ __global__ void __launch_bounds__(128) join_kernel(const AttendArgs a, float lif
     }
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) l += __shfl_xor_sync(~0u, l, d);
-    if (at < WIDTH) store4(static_cast<T*>(a.out) + token * a.ot + h * a.oh, at, a.c.dim, a.vec_out, finish_of(m, M, l, lift, any), y);
+    if (at < WIDTH) store4(static_cast<T*>(a.out) + token * a.ot + h * a.oh, at, a.c.dim, a.vec_out, finish_of(R, l, lift, any), y);
 }
 
 // The outputs of the items that were cut: block i that which CTA i began, PER warps for
@@ -809,20 +822,16 @@ __global__ void __launch_bounds__(8 * PER * 32) join_cut_kernel(const AttendArgs
     if (item.columns == 0) return;
     const int parts = item.others + 1;
     const auto slot = [&](int i) { return (2LL * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * 8 + column; };
-    float m = minus_infinity(), M = m, l = 0.0f, y[VALUES];
+    float m = minus_infinity(), R = m, l = 0.0f, y[VALUES];
 #pragma unroll
     for (int k = 0; k < VALUES; ++k) y[k] = 0.0f;
     if (column < item.columns) {
         for (int i = lane; i < parts; i += 32) {
             const float4 p = a.part[slot(i)];
-            m = fmaxf(m, p.x);
-            M = fmaxf(M, p.y);
+            join_references(m, R, p.x, p.y);
         }
 #pragma unroll
-        for (int d = 16; d > 0; d /= 2) {
-            m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-            M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
-        }
+        for (int d = 16; d > 0; d /= 2) join_references(m, R, __shfl_xor_sync(~0u, m, d), __shfl_xor_sync(~0u, R, d));
         for (int i0 = share; i0 < parts; i0 += BATCH * PER) {
             float x[BATCH][VALUES];
             float4 p[BATCH];
@@ -837,7 +846,7 @@ __global__ void __launch_bounds__(8 * PER * 32) join_cut_kernel(const AttendArgs
             for (int i = 0; i < BATCH; ++i) {
                 if (i0 + i * PER >= parts) continue;
                 l += p[i].z * power2(p[i].x - reference(m));
-                const float f = power2(p[i].y - reference(M));
+                const float f = power2(relative(p[i].y, p[i].x, m) - reference(R));
 #pragma unroll
                 for (int k = 0; k < VALUES; ++k) y[k] = fmaf(x[i][k], f, y[k]);
             }
@@ -858,7 +867,7 @@ __global__ void __launch_bounds__(8 * PER * 32) join_cut_kernel(const AttendArgs
     }
     const int col = item.column + column;
     const bool any = item.before + col / a.group >= 0;
-    const Finish z = finish_of(m, M, l, lift, any);
+    const Finish z = finish_of(R, l, lift, any);
     T* out = static_cast<T*>(a.out) + (int64_t)(item.first_token + col / a.group) * a.ot + (int64_t)(item.head * a.group + col % a.group) * a.oh;
 #pragma unroll
     for (int k = 0; k < VALUES; ++k)

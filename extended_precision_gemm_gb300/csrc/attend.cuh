@@ -4,9 +4,10 @@
 // o = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m) over the tokens j that a query sees,
 // with s_j = scale log2(e) q.k_j.  A cache row's value is its codes and block scales
 // (exact in 16-bit floating point) times 2^r, r the row's exponent: it joins s_j as
-// a factor for keys, and for values the weight is 2^(s_j + r_j - M) with a reference
-// M of its own, so rows of any size meet in range.  A part of the sum is (m, M, l, o):
-// l = sum 2^(s - m), o = sum 2^(s + r - M) (codes times scales).
+// a factor for keys, and for values the weight is 2^((s_j - m) + (r_j - R)) with a
+// reference R of its own, so rows of any size meet in range; R is relative to m, as a
+// sum of both would lose it where scores are 2^24 and more.  A part of the sum is
+// (m, R, l, o): l = sum 2^(s - m), o = sum 2^((s - m) + (r - R)) (codes times scales).
 #pragma once
 
 #include <cstdint>
@@ -33,7 +34,7 @@ struct AttendArgs {
     int step;             // 0, or see first_tile
     int splits;    // attend_tile.cu: most parts of a row; attend.cu: CTAs, or (together) CTAs of a cluster
     bool together;
-    float4* part;  // (m, M, l, 1 if any token is seen) of a part: by split and row (token, query head), or by CTA (attend.cu)
+    float4* part;  // (m, R, l, 1 if any token is seen) of a part: by split and row (token, query head), or by CTA (attend.cu)
     float* sums;   // its o, `width` elements
     CutItem* cuts;  // attend.cu: one for each CTA
 
@@ -129,14 +130,23 @@ __device__ __forceinline__ Item item_of(const AttendArgs& a, int64_t t, int colu
     return Item{s, (int)column, (int)min((int64_t)columns, (s1 - s0) * a.group - column), (int)s0, (int)(s1 - s0), b.lengths[s]};
 }
 
+// A part's R as one of the reference m (its own is m_of_part, and m is no less).
+__device__ __forceinline__ float relative(float R, float m_of_part, float m) { return R + (m_of_part - reference(m)); }
+// (m, R) becomes that of two parts: where every weight has its place in range.
+__device__ __forceinline__ void join_references(float& m, float& R, float other_m, float other_R) {
+    const float top = fmaxf(m, other_m);
+    R = fmaxf(relative(R, m, top), relative(other_R, other_m, top));
+    m = top;
+}
+
 // How a row's sums become its output: times x twice (half of the exponent each),
 // over l; 0 where no token is seen.
 struct Finish {
     float x, inverse;
 };
-__device__ __forceinline__ Finish finish_of(float m, float M, float l, float lift, bool any) {
+__device__ __forceinline__ Finish finish_of(float R, float l, float lift, bool any) {
     if (!any) return Finish{0.0f, 0.0f};
-    return Finish{power2(0.5f * (reference(M) - reference(m) - lift)), 1.0f / l};
+    return Finish{power2(0.5f * (reference(R) - lift)), 1.0f / l};
 }
 // Elements d .. d + 3 of an output row.
 template <typename T>

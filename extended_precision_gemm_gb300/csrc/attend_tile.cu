@@ -527,11 +527,11 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
             tc5::fence_after_sync();
         }
         if (!ok && lane == 0) atomicAdd(&g_attend_timeouts, 1u);
-        const float M = m + (float)reference_exponent;
+        const float R = (float)reference_exponent;
         const int64_t out_row = token * a.heads + h;
         const int64_t part = (int64_t)blockIdx.z * (a.b.tokens * a.heads) + out_row;
-        const Finish z = finish_of(m, M, l, kLift + lift_of<FMT>(), p >= 0);
-        if (cut && have) a.part[part] = make_float4(m, M, l, p >= 0 ? 1.0f : 0.0f);
+        const Finish z = finish_of(R, l, kLift + lift_of<FMT>(), p >= 0);
+        if (cut && have) a.part[part] = make_float4(m, R, l, p >= 0 ? 1.0f : 0.0f);
 #pragma unroll 1
         for (int c = 0; c < WIDTH; c += 32) {
             uint32_t v[32];
