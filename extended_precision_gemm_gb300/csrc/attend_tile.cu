@@ -17,8 +17,10 @@
 //
 // The conversion is shared by the 256 rows.  Exponents of rows become relative to the
 // tile's largest, for keys a factor of all its scores and for values one of all its
-// weights: codes times scales are exact in 16 bits down to 2^-18 of the tile's largest
-// row, and rounded to 2^-40 of it.
+// weights: codes times scales are exact in 16 bits while a tile's rows are within 2^9 of
+// one another (mxfp4: down to 2^-27 of the row's largest block).  One of the warps without
+// another task looks at the exponents; an item with rows further apart, or with scores of
+// 2^21 and more, is done again behind the loops, a step after the other.
 //
 // Measured: a prompt of 8192 tokens, 32 heads over 8 of 128, mxfp4, bfloat16: 548 us, 1.0
 // PF/s (the simple kernel with mma.sync that was here first: 5008).  A pair of tiles takes
@@ -44,9 +46,14 @@ constexpr unsigned long long kWaitNs = 2000000000ULL;  // bounded waits: 2 s
 constexpr float kMost = 32768.0f;  // a row's reference follows where 32 weights are more than this in all
 constexpr int kShift = 3;      // the values' exponent follows by more than 2^3 either way
 constexpr float kLift = 7.0f;  // the weight of a score equal to the reference is 2^(7 + up to 3 either way)
-constexpr int kFar = 64;       // values' exponents are at most so far below the largest seen
+// What the loops are for; an item beyond is done again by careful_item.
+constexpr int kSpread = 9;     // exponents of a tile's keys, and of its values, are so far apart at most: mxfp4 blocks down to
+                               // 2^-27 of their row's largest are exact then, as nvfp4 ones
+constexpr int kReach = 12;     // of all values of an item: one of 2^12 times another's size has a weight of 2^-24 or more where it counts
+constexpr float kMostScore = 2097152.0f;  // references are below 2^21, so that lifts and exponents are not lost beside them
 constexpr int kRing = 4;  // tiles whose rows, exponents and marks are kept
 constexpr int kNoToken = -4096;  // in the place of an exponent
+constexpr int kNone = 4096;      // of the least of no exponents
 
 __device__ unsigned int g_attend_timeouts = 0;
 
@@ -210,7 +217,7 @@ __device__ __forceinline__ void load_tmem16(uint32_t at, uint32_t (&v)[16]) {
 }
 // 32 weights (and what their rounding left) times a power of two.
 template <bool REST>
-__device__ __noinline__ void follow_weights(uint32_t at, uint32_t by) {
+__device__ __forceinline__ void follow_weights(uint32_t at, uint32_t by) {
     wait_tmem_stores();
 #pragma unroll
     for (int k = 0; k < (REST ? 2 : 1); ++k) {
@@ -222,8 +229,106 @@ __device__ __noinline__ void follow_weights(uint32_t at, uint32_t by) {
     }
 }
 
+template <bool REST>
+__device__ __noinline__ void call_follow_weights(uint32_t at, uint32_t by) { follow_weights<REST>(at, by); }
+
+// The scales of 32 codes (two blocks of nvfp4, in the halves of raw) as halves, each in both halves of a word, 2^add
+// (mxfp4: the byte joins it) or 2^(o + add) (nvfp4) times; o: the row's exponent, kNoToken for 0.  Those of values that
+// are NaN become 0, and the answer is whether there are any.
+template <int FMT>
+__device__ __forceinline__ bool piece_scales(uint32_t raw, int o, int add, uint32_t inside, bool value, uint32_t (&s)[2]) {
+    bool found = false;
+    if (FMT == kMxfp4) {
+        const float power = exp2_int(min(max((int)raw + add, -126), 15));
+        s[0] = raw == 255u ? 0x7fff7fffu : half2_of(power, power);
+        if (o == kNoToken) s[0] = 0;
+    } else {
+        const float power = exp2_int(min(max(o + add, -126), 15));  // 0 as a half where there is no token
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s[0]) : "h"((uint16_t)raw));
+        if (o == kNoToken) s[0] = 0;
+        s[0] = mul_half2(s[0], half2_of(power, power));
+    }
+    s[0] &= inside;
+    if (value) {  // NaN: 0 here, and looked for at the end
+        const __half2 is = __hisnan2(*reinterpret_cast<const __half2*>(&s[0]));
+        const uint32_t nan = *reinterpret_cast<const uint32_t*>(&is);
+        if (nan != 0) {
+            found = true;
+            s[0] &= (nan & 0xffffu ? 0u : 0xffffu) | (nan >> 16 ? 0u : 0xffff0000u);
+        }
+    }
+    s[1] = FMT == kMxfp4 ? s[0] : __byte_perm(s[0], s[0], 0x3232);
+    if (FMT == kNvfp4) s[0] = __byte_perm(s[0], s[0], 0x1010);
+    return found;
+}
+// 32 codes times their scales to a row of 128 bytes, 16 swizzled bytes at a time.
+__device__ __forceinline__ void store_piece(uint32_t to, const uint4& codes, const uint32_t (&s)[2]) {
+    const uint32_t words[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+    for (int k0 = 0; k0 < 4; ++k0) {
+        uint4 v = halves_of(words[k0]);
+        const uint32_t sc = s[k0 / 2];
+        v.x = mul_half2(v.x, sc);
+        v.y = mul_half2(v.y, sc);
+        v.z = mul_half2(v.z, sc);
+        v.w = mul_half2(v.w, sc);
+        store_shared(to ^ (uint32_t)(k0 << 4), v);
+    }
+}
+// Blocks of the part-th 32 elements that begin beyond the head's end take no part, whatever they hold.
+template <int BLOCK>
+__device__ __forceinline__ uint32_t inside_of(int part, int dim) {
+    return (part * 32 < dim ? 0xffffu : 0u) | (part * 32 + BLOCK % 32 < dim ? 0xffff0000u : 0u);
+}
+// Where they go: the token's row, swizzled.
+__device__ __forceinline__ uint32_t piece_place(int part, int t, uint32_t block_bytes) {
+    return part / 2 * block_bytes + t * 128 + (uint32_t)(((part % 2 * 4) ^ (t % 8)) << 4);
+}
+// What a tile's scores are times beside the row's own factor.
+template <int FMT>
+__device__ __forceinline__ float key_factor_of(int key_exponent) { return mxfp4_scale((uint32_t)(key_exponent + 127)) * exp2_int(-lift_of<FMT>()); }
+
+// Bits of the 32 tokens of groups g and g + 1: those that a query at p sees.
+__device__ __forceinline__ uint32_t seen_bits(const Groups& groups, int p, int window, int sinks, int g0) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int g = g0 + k, j0 = group_token(groups, g);
+        const uint32_t upto = (1u << min(max(p - j0 + 1, 0), 16)) - 1u;
+        uint32_t from = 0xffffu;
+        if (window > 0) from = ~((1u << min(max(p - window - j0 + 1, 0), 16)) - 1u) | ((1u << min(max(sinks - j0, 0), 16)) - 1u);
+        if (g < groups.count) bits |= (upto & from & 0xffffu) << (16 * k);
+    }
+    return bits;
+}
+
+// S = Q K^T of a tile of rows, and O = (O +) P V, issued by one thread; shared-memory addresses of the operands.
+template <int WIDTH>
+__device__ __forceinline__ void issue_scores(uint32_t s_at, uint32_t q, uint32_t k_tile) {
+    using S = Shape<WIDTH>;
+    constexpr uint32_t DESC = tc5::idesc_f16(false, false, false, 128, 128);
+    const uint64_t qd = tc5::desc_kmajor_sw128(q), kd = tc5::desc_kmajor_sw128(k_tile);
+#pragma unroll
+    for (int k = 0; k < WIDTH / 16; ++k) {
+        const uint64_t at = (uint64_t)(k / 4 * (S::BLOCK_BYTES / 16) + k % 4 * 2);
+        tc5::mma_f16_single(s_at, qd + at, kd + at, DESC, k > 0 ? 1u : 0u);
+    }
+}
+template <int WIDTH, bool REST>
+__device__ __forceinline__ void issue_sums(uint32_t o_at, uint32_t p_at, uint32_t v_tile, bool add) {
+    using S = Shape<WIDTH>;
+    constexpr uint32_t DESC = tc5::idesc_f16(false, false, true, 128, WIDTH);
+    const uint64_t vd = tc5::desc_mnmajor_sw128(v_tile, S::BLOCK_BYTES);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t from = p_at + k / 2 * 32 + k % 2 * 8;
+        mma_from_tmem(o_at, from, vd + k * (2048 / 16), DESC, add || k != 0 ? 1u : 0u);
+        if (REST) mma_from_tmem(o_at, from + 16, vd + k * (2048 / 16), DESC, 1u);
+    }
+}
+
 struct Barriers {
-    uint64_t q, k_full[2], k_empty[2], v_full[2], v_empty[2], done;
+    uint64_t q, k_full[2], k_empty[2], v_full[2], v_empty[2], done, careful;
     uint64_t s[2], p[2], o[2];
     uint64_t info[kRing];  // of tiles in turn
 };
@@ -256,6 +361,286 @@ __device__ __noinline__ void mark_nan(const AttendArgs& a, const Item& item, con
     }
 }
 
+// The power of two that a query row of bfloat16 is divided by: its largest element (0 where that is) comes to [2^11, 2^12).
+template <typename T>
+__device__ __forceinline__ int query_exponent(const T* src, int dim, bool vec, bool have) {
+    uint32_t most = 0;
+    if (have) {
+        if (vec) {
+            for (int d = 0; d + 8 <= dim; d += 8) {
+                const uint4 raw = *reinterpret_cast<const uint4*>(src + d);
+                const T* t = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t bits = __float_as_uint(to_float<T>(t[j])) & 0x7fffffffu;
+                    most = max(most, bits < kInfBits ? bits : 0u);
+                }
+            }
+        }
+        for (int d = vec ? dim / 8 * 8 : 0; d < dim; ++d) {
+            const uint32_t bits = __float_as_uint(to_float<T>(src[d])) & 0x7fffffffu;
+            most = max(most, bits < kInfBits ? bits : 0u);
+        }
+    }
+    return max((int)(most >> 23) - 127 - 11, -126);
+}
+
+// A row's softmax: l = sum 2^(s - m), and its sums in tensor memory are times 2^(m + exponent).
+struct RowState {
+    float m, l;
+    int exponent;
+};
+// The row's output, or its part.
+template <typename T, int WIDTH, int FMT>
+__device__ __forceinline__ void store_row(const AttendArgs& a, const RowState& row, int p, int64_t token, int64_t h, bool have, bool cut, bool summed, uint32_t o_at) {
+    const float R = (float)row.exponent;
+    const int64_t part = (int64_t)blockIdx.z * (a.b.tokens * a.heads) + token * a.heads + h;
+    const Finish z = finish_of(R, row.l, kLift + lift_of<FMT>(), p >= 0);
+    if (cut && have) a.part[part] = make_float4(row.m, R, row.l, p >= 0 ? 1.0f : 0.0f);
+#pragma unroll 1
+    for (int c = 0; c < WIDTH; c += 32) {
+        uint32_t v[32];
+        if (summed) {
+            tc5::ld32(o_at + c, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0;
+        }
+        if (have) {
+            if (cut) {
+                float4* to = reinterpret_cast<float4*>(a.sums + part * WIDTH + c);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    to[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+            } else {
+                T* out = static_cast<T*>(a.out) + token * a.ot + h * a.oh;
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    float y[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) y[k] = p < 0 ? 0.0f : __uint_as_float(v[i + k]) * z.x * z.x * z.inverse;
+                    if (a.vec_out && c + i + 8 <= a.c.dim) {
+                        store8(out + c + i, y);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (c + i + k < a.c.dim) out[c + i + k] = from_float<T>(y[k]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    }
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint32_t (&w)[4], int i) { return i < 2 ? i < 1 ? w[0] : w[1] : i < 3 ? w[2] : w[3]; }
+
+// A tile's step for a row of any scores and values.  Scores are rounded before the reference is subtracted, so that
+// nothing is lost beside large ones, and the references are of what the row sees: m follows its largest score, the
+// exponent its largest score with the tile's values, unless what O holds is far above it.  exponent: of the tile's
+// values; seen: bits of its tokens; lost: its groups without a page.
+template <int WIDTH, bool REST>
+__device__ __forceinline__ void careful_step(RowState& row, float f, int exponent, const uint32_t (&seen)[4], uint32_t lost, uint32_t s_at, uint32_t o_at, bool first) {
+    // 16 scores from the c-th on
+    const auto load_scores = [&](int c, float (&s)[16]) {
+        uint32_t v[16];
+        load_tmem16(s_at + c, v);
+        const uint32_t bits = word_of(seen, c / 32) >> (c % 32);
+        const bool gone = lost >> (c / 16) & 1u;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = bits >> i & 1u ? (gone ? not_a_number() : __uint_as_float(v[i]) * f) : minus_infinity();
+    };
+    float top = minus_infinity();
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 16) {
+        float s[16];
+        load_scores(c, s);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[i]);
+    }
+    top = ceilf(top);
+    const float m = fmaxf(row.m, top), sub = reference(m);
+    const float own = (top - sub) + (float)exponent, before = first ? minus_infinity() : relative((float)row.exponent, row.m, m);
+    float most = 0.0f;
+    if (!first) {
+#pragma unroll 1
+        for (int c = 0; c < WIDTH; c += 16) {
+            uint32_t v[16];
+            load_tmem16(o_at + c, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(__uint_as_float(v[i])));
+        }
+    }
+    // O stays below 2^100, beside which new terms (below 2^40) may vanish
+    const float least = most > 0.0f ? before + (float)((int)(__float_as_uint(most) >> 23) - 227) : minus_infinity();
+    float R = top == minus_infinity() ? before : fmaxf(own, least);
+    R = R > -0x1p20f ? R : top == minus_infinity() ? (float)exponent : -0x1p20f;  // (the former: nothing seen so far)
+    if (!first) {
+        const float2 turn = exp2_factors((int)fminf(fmaxf(before - R, -200.0f), 200.0f));
+#pragma unroll 1
+        for (int c = 0; c < WIDTH; c += 16) {
+            uint32_t v[16];
+            load_tmem16(o_at + c, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * turn.x * turn.y);
+            store_tmem16(o_at + c, v);
+        }
+    }
+    const float up = (float)exponent - R + kLift;
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+        uint32_t w[16], rest[16];
+#pragma unroll
+        for (int k = 0; k < 32; k += 16) {
+            float s[16];
+            load_scores(c + k, s);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                const float t0 = s[i] - sub, t1 = s[i + 1] - sub;
+                sum += power2(t0) + power2(t1);
+                const float u0 = power2(t0 + up), u1 = power2(t1 + up);
+                const uint32_t h = half2_of(u0, u1);
+                w[(k + i) / 2] = h;
+                if (REST) {
+                    const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                    rest[(k + i) / 2] = half2_of(u0 - back.x, u1 - back.y);
+                }
+            }
+        }
+        store_tmem16(s_at + c, w);
+        if (REST) store_tmem16(s_at + c + 16, rest);
+    }
+    row = RowState{m, fmaf(row.l, power2(row.m - sub), sum), (int)R};
+}
+
+// An item (or its part of n tiles) again from the start, of any scores and exponents of rows, by the softmax's warps
+// alone and one step after the other: a tile's tokens in as many passes as leave each pass keys, and values, within
+// 2^kSpread of one another, so that no row's bits depend on another's size, seen or not.  About three times the time
+// of the loops; a pass more a tile for each 2^kSpread.
+template <typename T, int WIDTH, int FMT>
+__device__ __forceinline__ void careful_item(const AttendArgs& a, const Item& item, const Groups& groups, int head, int t0, int n, uint32_t base, uint32_t tmem,
+                                          uint32_t done, int16_t (*exponents)[128], bool cut) {
+    using S = Shape<WIDTH>;
+    constexpr bool REST = std::is_same_v<T, __half>;
+    constexpr int THREADS = 128 * S::NQ, PIECES = S::PIECES, BLOCK = mx4_block(FMT), BLOCKS = WIDTH / BLOCK;
+    const int thread = threadIdx.x, warp = uniform_warp(), lane = thread & 31, x = warp / 4;
+    const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
+    const uint32_t s_at = tmem + S::S_COL + x * S::BUFFERS * 128 + lanes, o_at = tmem + S::O_COL + x * WIDTH + lanes;
+    const bool have = thread < item.columns;
+    const int query = item.column + thread, p = have ? item.length - item.tokens + query / a.group : -1;
+    float factor = fabsf(a.scale);
+    if (!REST) {
+        const T* const q = static_cast<const T*>(a.q) + (have ? (item.first_token + query / a.group) * a.qt + (int64_t)(head * a.group + query % a.group) * a.qh : 0);
+        factor = scale_by_exp2(factor, query_exponent(q, a.c.dim, a.vec_q, have));
+    }
+    RowState row{p >= 0 ? minus_infinity() : 0.0f, 0.0f, 0};
+    uint32_t phase = 0;
+    bool ok = true, first = true;
+    const auto meet = [] { asm volatile("bar.sync 2, %0;" ::"n"(THREADS) : "memory"); };
+    // MMAs of one thread behind everyone's writes, and everyone behind the MMAs.  Who gave up a wait once waits no more,
+    // and meets the others all the same.
+    const auto with_mmas = [&](auto issue) {
+        tc5::fence_before_sync();
+        meet();
+        if (warp == 0) {
+            tc5::fence_after_sync();
+            if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < S::NQ; ++i) issue(i);
+                tc5::commit(done);
+            }
+            __syncwarp();
+        }
+        ok = ok && warp_wait(done, phase, kWaitNs);
+        phase ^= 1;
+        tc5::fence_after_sync();
+    };
+    const auto row_of = [&](int tile, int t, int kv) -> int64_t {  // of a token in the cache, -1 where there is none
+        const int g = (t0 + tile) * 8 + t / 16, token = group_token(groups, g) + t % 16;
+        const int page = g < groups.count && token < item.length ? page_of(a.c, a.b, item.sequence, token) : -1;
+        return page < 0 ? -1 : cache_row(a.c, page, kv, head, token & (a.c.page_size - 1));
+    };
+    for (int tile = 0; tile < n; ++tile) {
+        for (int i = thread; i < 256; i += THREADS) {
+            const int64_t r = row_of(tile, i % 128, i / 128);
+            exponents[i / 128][i % 128] = r < 0 ? kNoToken : a.c.exponents[r];
+        }
+        const int g = (t0 + tile) * 8 + lane % 8;
+        const uint32_t bad = __ballot_sync(~0u, lane < 8 && g < groups.count && page_of(a.c, a.b, item.sequence, group_token(groups, g)) < 0);
+        meet();
+        int ke[4], ve[4];
+        uint32_t left[4], rest;  // tokens still to come; every warp finds the same
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ke[i] = exponents[0][32 * i + lane], ve[i] = exponents[1][32 * i + lane], left[i] = ~0u;
+        do {
+            const auto within = [](int e, int most) { return e <= -127 || most - e <= kSpread; };  // zeros and no tokens: with any
+            int key = kNoToken, value = kNoToken;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) key = max(key, left[i] >> lane & 1u ? ke[i] : kNoToken);
+            key = __reduce_max_sync(~0u, key);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) value = max(value, (left[i] >> lane & 1u) && within(ke[i], key) ? ve[i] : kNoToken);
+            value = __reduce_max_sync(~0u, value);
+            uint32_t now[4];
+            rest = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                now[i] = __ballot_sync(~0u, (left[i] >> lane & 1u) && within(ke[i], key) && within(ve[i], value));
+                left[i] &= ~now[i];
+                rest |= left[i];
+            }
+            key = max(key, -127);
+            value = max(value, -127);
+#pragma unroll 1
+            for (int i = thread; i < 256 * PIECES; i += THREADS) {
+                const int kv = i / (128 * PIECES), t = i / PIECES % 128, part = i % PIECES;
+                const int o = exponents[kv][t];
+                uint4 codes = make_uint4(0, 0, 0, 0);
+                uint32_t s[2] = {0, 0};
+                if (o != kNoToken && word_of(now, t / 32) >> (t % 32) & 1u) {
+                    const int64_t r = row_of(tile, t, kv);
+                    codes = fetch16(a.c.codes + r * (WIDTH / 2) + part * 16);
+                    const uint8_t* const scales = a.c.scales + r * BLOCKS + part * (32 / BLOCK);
+                    piece_scales<FMT>(FMT == kMxfp4 ? fetch1(scales) : fetch2(scales), o, lift_of<FMT>() - (kv ? value : key) - (FMT == kMxfp4 ? 127 : 0),
+                                      inside_of<BLOCK>(part, a.c.dim), kv, s);
+                }
+                store_piece(base + (kv ? S::V0 : S::K0) + piece_place(part, t, S::BLOCK_BYTES), codes, s);
+            }
+            fence_async();
+            with_mmas([&](int i) { issue_scores<WIDTH>(tmem + S::S_COL + i * S::BUFFERS * 128, base + i * S::TILE_BYTES, base + S::K0); });
+            uint32_t seen[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) seen[i] = now[i] & seen_bits(groups, p, a.window, a.sinks, (t0 + tile) * 8 + 2 * i);
+            careful_step<WIDTH, REST>(row, fmaxf(factor * key_factor_of<FMT>(key), 0x1p-120f), value, seen, bad, s_at, o_at, first);
+            wait_tmem_stores();
+            with_mmas([&](int i) { issue_sums<WIDTH, REST>(tmem + S::O_COL + i * WIDTH, tmem + S::S_COL + i * S::BUFFERS * 128, base + S::V0, !first); });
+            first = false;
+        } while (rest != 0);
+    }
+    if (!ok && lane == 0) atomicAdd(&g_attend_timeouts, 1u);
+    store_row<T, WIDTH, FMT>(a, row, p, item.first_token + query / a.group, head * a.group + query % a.group, have, cut, ok, o_at);
+}
+
+// The two ways in which the kernel calls it.  A call costs its loops registers, more or fewer by what is held over them
+// (us, against a copy without: 8192 tokens of width 128: 531; all found anew 543, handed over 550; chunks of width 256:
+// 339; 351 and 344; a kernel of its own behind this one: 5 us more for every call).
+template <typename T, int WIDTH, int FMT>
+__device__ __noinline__ void careful_item_anew(const AttendArgs& a, uint32_t smem, const uint32_t* tmem_slot, uint32_t done, int16_t (*exponents)[128]) {
+    const int head = (int)(blockIdx.x % a.c.heads);
+    const Item item = item_of(a, (int64_t)((gridDim.x - 1 - blockIdx.x) / a.c.heads), 128 * Shape<WIDTH>::NQ);
+    const int before = item.length - item.tokens;
+    const Groups groups = groups_of(a.c, a.b, before + item.column / a.group, before + (item.column + item.columns - 1) / a.group, a.window, a.sinks);
+    const int tiles = (groups.count + 7) / 8, parts = parts_of(tiles, a.splits);
+    const int t0 = (int)((unsigned)tiles * blockIdx.z / (unsigned)parts), t1 = (int)((unsigned)tiles * (blockIdx.z + 1) / (unsigned)parts);
+    careful_item<T, WIDTH, FMT>(a, item, groups, head, t0, t1 - t0, (smem + 1023u) & ~1023u, *tmem_slot, done, exponents, parts > 1);
+}
+template <typename T, int WIDTH, int FMT>
+__device__ __noinline__ void careful_item_handed(const AttendArgs& a, const Item& item, const Groups& groups, int head, int t0, int n, uint32_t base, uint32_t tmem,
+                                                 uint32_t done, int16_t (*exponents)[128], bool cut) {
+    careful_item<T, WIDTH, FMT>(a, item, groups, head, t0, n, base, tmem, done, exponents, cut);
+}
+
 template <typename T, int WIDTH, int FMT>
 __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(const AttendArgs a) {
     using S = Shape<WIDTH>;
@@ -269,6 +654,7 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
     __shared__ int any_nan;                       // in values
     __shared__ bool cut;                          // the item has other parts (here, not in a register all the way: 547 us for 560 of 8192 tokens)
     __shared__ __align__(16) int largest[2][2][4];  // of the tiles in turn
+    __shared__ bool far_rows, large_scores;         // what the loops are not for
 
     pdl_wait();
     pdl_launch_dependents();
@@ -317,7 +703,9 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
             mbar_init(bar(bars.info, i), 1);
         }
         mbar_init(done, 1);
+        mbar_init(smem_addr(&bars.careful), 1);
         any_nan = 0;
+        far_rows = large_scores = false;
         fence_barrier_init();
     }
     if (warp == S::MMA_WARP) {
@@ -344,26 +732,8 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
             const T* src = static_cast<const T*>(a.q) + (have ? token * a.qt + h * a.qh : 0);
             const float sign = a.scale < 0.0f ? -1.0f : 1.0f;
             float2 up = make_float2(sign, 1.0f);
-            if (!REST) {  // bfloat16: the row's largest to [2^11, 2^12)
-                uint32_t most = 0;
-                if (have) {
-                    if (a.vec_q) {
-                        for (int d = 0; d + 8 <= a.c.dim; d += 8) {
-                            const uint4 raw = *reinterpret_cast<const uint4*>(src + d);
-                            const T* t = reinterpret_cast<const T*>(&raw);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const uint32_t bits = __float_as_uint(to_float<T>(t[j])) & 0x7fffffffu;
-                                most = max(most, bits < kInfBits ? bits : 0u);
-                            }
-                        }
-                    }
-                    for (int d = a.vec_q ? a.c.dim / 8 * 8 : 0; d < a.c.dim; ++d) {
-                        const uint32_t bits = __float_as_uint(to_float<T>(src[d])) & 0x7fffffffu;
-                        most = max(most, bits < kInfBits ? bits : 0u);
-                    }
-                }
-                const int e = max((int)(most >> 23) - 127 - 11, -126);
+            if (!REST) {
+                const int e = query_exponent(src, a.c.dim, a.vec_q, have);
                 const float2 down = exp2_factors(e);
                 up = exp2_factors(-e);
                 up.x *= sign;
@@ -397,19 +767,6 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
         int reference_exponent = 0;
         bool ok = true;
         const int mine = need[x];
-        // bits of 32 tokens from the c-th of a tile of groups from g0 on: those that the row sees
-        const auto seen = [&](int g0, int c) {
-            uint32_t bits = 0;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int g = g0 + c / 16 + k, j0 = group_token(groups, g);
-                const uint32_t upto = (1u << min(max(p - j0 + 1, 0), 16)) - 1u;
-                uint32_t from = 0xffffu;
-                if (a.window > 0) from = ~((1u << min(max(p - a.window - j0 + 1, 0), 16)) - 1u) | ((1u << min(max(a.sinks - j0, 0), 16)) - 1u);
-                if (g < groups.count) bits |= (upto & from & 0xffffu) << (16 * k);
-            }
-            return bits;
-        };
         for (int j = 0; j < mine; ++j) {
             const int buffer = x * S::BUFFERS + j % S::BUFFERS;
             const uint32_t s_at = tmem + S::S_COL + buffer * 128 + lanes;
@@ -424,7 +781,7 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
             const bool whole = tile.bad == 0 && g0 + 8 <= groups.count && end <= first && (a.window == 0 || begin > last - a.window);
             // scores of what is not seen become minus infinity, of tokens without a page NaN
             const auto mask = [&](int c, uint32_t (&s)[32]) {
-                const uint32_t bits = seen(g0, c), lost = tile.bad >> (c / 16);
+                const uint32_t bits = seen_bits(groups, p, a.window, a.sinks, g0 + c / 16), lost = tile.bad >> (c / 16);
                 const uint32_t nan = (lost & 1u ? 0xffffu : 0u) | (lost & 2u ? 0xffff0000u : 0u);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) s[i] = bits >> i & 1u ? (nan >> i & 1u ? 0x7fc00000u : s[i]) : 0xff800000u;
@@ -484,6 +841,7 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
                     const float top = ceilf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * f);
                     const float by = top > m ? power2(m - top) : 1.0f;
                     m = top > m ? top : m;
+                    if (fabsf(m) >= kMostScore && fabsf(m) < -minus_infinity()) large_scores = true;
                     l *= by;
                     sum *= by;
                     turn *= by;
@@ -491,7 +849,12 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
                     if (c < 96) wait_tmem_loads(ring[c / 32 & 1 ^ 1]);  // no load is in flight over a call
                     const uint32_t half = half2_of(by, by);
 #pragma unroll 1
-                    for (int d = 0; d < c; d += 32) follow_weights<REST>(s_at + d, half);
+                    for (int d = 0; d < c; d += 32) {
+                        // a call costs the other loops registers (8192 tokens of width 128: 572 us, 535 so); of width 256
+                        // it is the other way round (chunks: 339, 346)
+                        if constexpr (S::NQ == 2) follow_weights<REST>(s_at + d, half);
+                        else call_follow_weights<REST>(s_at + d, half);
+                    }
                     weights();
                 }
                 sum += part;
@@ -527,45 +890,7 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
             tc5::fence_after_sync();
         }
         if (!ok && lane == 0) atomicAdd(&g_attend_timeouts, 1u);
-        const float R = (float)reference_exponent;
-        const int64_t out_row = token * a.heads + h;
-        const int64_t part = (int64_t)blockIdx.z * (a.b.tokens * a.heads) + out_row;
-        const Finish z = finish_of(R, l, kLift + lift_of<FMT>(), p >= 0);
-        if (cut && have) a.part[part] = make_float4(m, R, l, p >= 0 ? 1.0f : 0.0f);
-#pragma unroll 1
-        for (int c = 0; c < WIDTH; c += 32) {
-            uint32_t v[32];
-            if (mine > 0 && ok) {
-                tc5::ld32(o_at + c, v);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = 0;
-            }
-            if (have) {
-                if (cut) {
-                    float4* to = reinterpret_cast<float4*>(a.sums + part * WIDTH + c);
-    #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        to[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
-                } else {
-                    T* out = static_cast<T*>(a.out) + token * a.ot + h * a.oh;
-    #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        float y[8];
-    #pragma unroll
-                        for (int k = 0; k < 8; ++k) y[k] = p < 0 ? 0.0f : __uint_as_float(v[i + k]) * z.x * z.x * z.inverse;
-                        if (a.vec_out && c + i + 8 <= a.c.dim) {
-                            store8(out + c + i, y);
-                        } else {
-    #pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                if (c + i + k < a.c.dim) out[c + i + k] = from_float<T>(y[k]);
-                        }
-                    }
-                }
-            }
-            __syncwarp();
-        }
+        store_row<T, WIDTH, FMT>(a, RowState{m, l, reference_exponent}, p, token, h, have, cut, mine > 0 && ok, o_at);
         tc5::fence_before_sync();
     } else if (warp < S::MMA_WARP) {
         // ---- codes to 16 bits ----
@@ -622,11 +947,10 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
             exponent = kNoToken;
             if (has_exponent && r >= 0 && j * 128 + et < tokens) exponent = fetch_signed1(exponent_base + (uint64_t)(uint32_t)r * 16);
         };
-        // blocks that begin beyond the head's end take no part, whatever they hold
-        const uint32_t inside = (part * 32 < a.c.dim ? 0xffffu : 0u) | (part * 32 + BLOCK % 32 < a.c.dim ? 0xffff0000u : 0u);
-        const uint32_t place = base + part / 2 * S::BLOCK_BYTES + t * 128 + (uint32_t)(((part % 2 * 4) ^ (t % 8)) << 4);
+        const uint32_t inside = inside_of<BLOCK>(part, a.c.dim);
+        const uint32_t place = base + piece_place(part, t, S::BLOCK_BYTES);
         bool ok = true;
-        int most_seen = kNoToken, key_exponent = 0, value_exponent = 0, next_value_exponent = 0;
+        int key_exponent = 0, value_exponent = 0, next_value_exponent = -127;
         const auto convert = [&](int j, bool value, int e, const Raw<PASSES>& raw) {
             const int stage = j % S::STAGES;
             const int16_t* const own = exponents[j & (kRing - 1)][value ? 1 : 0];
@@ -634,40 +958,9 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
             const int add = lift_of<FMT>() - e - (FMT == kMxfp4 ? 127 : 0);
 #pragma unroll
             for (int i = 0; i < PASSES; ++i) {
-                const int o = own[i * S::PER_PASS + t];
                 uint32_t s[2];
-                if (FMT == kMxfp4) {
-                    const float power = exp2_int(min(max((int)raw.scales[i] + add, -126), 15));
-                    s[0] = raw.scales[i] == 255u ? 0x7fff7fffu : half2_of(power, power);
-                    if (o == kNoToken) s[0] = 0;
-                } else {
-                    const float power = exp2_int(min(max(o + add, -126), 15));  // 0 as a half where there is no token
-                    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s[0]) : "h"(raw.scales[i]));
-                    if (o == kNoToken) s[0] = 0;
-                    s[0] = mul_half2(s[0], half2_of(power, power));
-                }
-                s[0] &= inside;
-                if (value) {  // NaN: 0 here, and looked for at the end
-                    const __half2 is = __hisnan2(*reinterpret_cast<const __half2*>(&s[0]));
-                    const uint32_t nan = *reinterpret_cast<const uint32_t*>(&is);
-                    if (nan != 0) {
-                        any_nan = 1;
-                        s[0] &= (nan & 0xffffu ? 0u : 0xffffu) | (nan >> 16 ? 0u : 0xffff0000u);
-                    }
-                }
-                s[1] = FMT == kMxfp4 ? s[0] : __byte_perm(s[0], s[0], 0x3232);
-                if (FMT == kNvfp4) s[0] = __byte_perm(s[0], s[0], 0x1010);
-                const uint32_t words[4] = {raw.codes[i].x, raw.codes[i].y, raw.codes[i].z, raw.codes[i].w};
-#pragma unroll
-                for (int k0 = 0; k0 < 4; ++k0) {
-                    uint4 v = halves_of(words[k0]);
-                    const uint32_t sc = s[k0 / 2];
-                    v.x = mul_half2(v.x, sc);
-                    v.y = mul_half2(v.y, sc);
-                    v.z = mul_half2(v.z, sc);
-                    v.w = mul_half2(v.w, sc);
-                    store_shared((to + i * S::PER_PASS * 128) ^ (uint32_t)(k0 << 4), v);
-                }
+                if (piece_scales<FMT>(raw.scales[i], own[i * S::PER_PASS + t], add, inside, value, s)) any_nan = 1;
+                store_piece(to + i * S::PER_PASS * 128, raw.codes[i], s);
             }
             fence_async();
             __syncwarp();
@@ -688,13 +981,12 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
             const int4 a0 = *reinterpret_cast<const int4*>(largest[j & 1][0]), a1 = *reinterpret_cast<const int4*>(largest[j & 1][1]);
             key_exponent = max(max(max(a0.x, a0.y), max(a0.z, a0.w)), -127);
             const int v = max(max(a1.x, a1.y), max(a1.z, a1.w));
-            most_seen = max(most_seen, v);
             value_exponent = next_value_exponent;
-            next_value_exponent = max(max(v, most_seen - kFar), -127);
+            next_value_exponent = v > -127 ? v : value_exponent;  // zeros alone: as before
             if (thread / 32 == 1) {
                 const uint32_t bad = __ballot_sync(~0u, lane < 8 && (t0 + j) * 8 + lane < groups.count && rows[slot][lane % 8] < 0);
                 if (lane == 0) {
-                    info[slot].key_factor = mxfp4_scale((uint32_t)(key_exponent + 127)) * exp2_int(-lift_of<FMT>());
+                    info[slot].key_factor = key_factor_of<FMT>(key_exponent);
                     info[slot].value_exponent = next_value_exponent;
                     info[slot].bad = bad;
                     mbar_arrive(bar(bars.info, slot));
@@ -732,18 +1024,10 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
         if (!ok && lane == 0) atomicAdd(&g_attend_timeouts, 1u);
     } else if (fewer_registers<S::MMA_REGS>(); warp == S::MMA_WARP && n > 0) {
         // ---- MMAs ----
-        constexpr uint32_t S_DESC = tc5::idesc_f16(false, false, false, 128, 128);
-        constexpr uint32_t O_DESC = tc5::idesc_f16(false, false, true, 128, WIDTH);
         const auto score = [&](int x, int j) {
             if (elect_one()) {
                 const int buffer = x * S::BUFFERS + j % S::BUFFERS;
-                const uint64_t qd = tc5::desc_kmajor_sw128(base + x * S::TILE_BYTES);
-                const uint64_t kd = tc5::desc_kmajor_sw128(base + S::K0 + j % S::STAGES * S::TILE_BYTES);
-#pragma unroll
-                for (int k = 0; k < WIDTH / 16; ++k) {
-                    const uint64_t at = (uint64_t)(k / 4 * (S::BLOCK_BYTES / 16) + k % 4 * 2);
-                    tc5::mma_f16_single(tmem + S::S_COL + buffer * 128, qd + at, kd + at, S_DESC, k > 0 ? 1u : 0u);
-                }
+                issue_scores<WIDTH>(tmem + S::S_COL + buffer * 128, base + x * S::TILE_BYTES, base + S::K0 + j % S::STAGES * S::TILE_BYTES);
                 tc5::commit(bar(bars.s, buffer));
             }
             __syncwarp();
@@ -751,14 +1035,7 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
         const auto weigh = [&](int x, int j) {
             if (elect_one()) {
                 const int buffer = x * S::BUFFERS + j % S::BUFFERS;
-                const uint64_t vd = tc5::desc_mnmajor_sw128(base + S::V0 + j % S::STAGES * S::TILE_BYTES, S::BLOCK_BYTES);
-                const uint32_t p_at = tmem + S::S_COL + buffer * 128, o_at = tmem + S::O_COL + x * WIDTH;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t from = p_at + k / 2 * 32 + k % 2 * 8;
-                    mma_from_tmem(o_at, from, vd + k * (2048 / 16), O_DESC, (j | k) != 0 ? 1u : 0u);
-                    if (REST) mma_from_tmem(o_at, from + 16, vd + k * (2048 / 16), O_DESC, 1u);
-                }
+                issue_sums<WIDTH, REST>(tmem + S::O_COL + x * WIDTH, tmem + S::S_COL + buffer * 128, base + S::V0 + j % S::STAGES * S::TILE_BYTES, j != 0);
                 tc5::commit(bar(bars.o, x));
             }
             __syncwarp();
@@ -803,10 +1080,52 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
         __syncwarp();
         ok = warp_wait(done, 0, kWaitNs) && ok;
         if (!ok && lane == 0) atomicAdd(&g_attend_timeouts, 1u);
+    } else if (warp == S::MMA_WARP + 1) {
+        // ---- exponents far apart, which the loops are not for ----
+        // 16 lanes for a tile: groups of 16 tokens, keys and values
+        int most = -127, least = kNone, widest = 0;
+        for (int j = lane / 16; j < n + lane / 16; j += 2) {
+            const int kv = lane >> 3 & 1, g = (t0 + j) * 8 + lane % 8;
+            int top = -127, low = kNone;
+            if (j < n && g < groups.count) {
+                const int token = group_token(groups, g), page = page_of(a.c, a.b, item.sequence, token);
+                if (page >= 0) {
+                    const uint4 v = fetch16(a.c.exponents + cache_row(a.c, page, kv, head, token & (a.c.page_size - 1)));
+                    const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+                    const int here = item.length - token;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int e = (int8_t)(words[i / 4] >> (8 * (i % 4)));
+                        if (i < here && e > -127) {  // zeros are of any size
+                            top = max(top, e);
+                            low = min(low, e);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int d = 1; d < 8; d *= 2) {
+                top = max(top, __shfl_xor_sync(~0u, top, d));
+                low = min(low, __shfl_xor_sync(~0u, low, d));
+            }
+            widest = max(widest, top - low);
+            if (kv) most = max(most, top), least = min(least, low);
+        }
+        const bool far = __reduce_max_sync(~0u, widest) > kSpread || __reduce_max_sync(~0u, most) - __reduce_min_sync(~0u, least) > kReach;
+        if (far && lane == 0) far_rows = true;
     }
     tc5::fence_before_sync();
     __syncthreads();
     tc5::fence_after_sync();
+    if (far_rows || large_scores) {
+        if (threadIdx.x < 128 * S::NQ) {
+            if constexpr (S::NQ == 2) careful_item_anew<T, WIDTH, FMT>(a, smem_addr(smem_raw), &tmem_slot, smem_addr(&bars.careful), exponents[0]);
+            else careful_item_handed<T, WIDTH, FMT>(a, item, groups, head, t0, n, base, tmem, smem_addr(&bars.careful), exponents[0], cut);
+        }
+        tc5::fence_before_sync();
+        __syncthreads();
+        tc5::fence_after_sync();
+    }
     if (warp == S::MMA_WARP) {
         __syncwarp();
         tc5::tmem_dealloc(tmem, 512);

@@ -6,7 +6,7 @@ import pytest
 import extended_precision_gemm_gb300 as ddg
 from oracle import attention as oa
 
-from attention_bounds import UNIT
+from attention_bounds import UNIT, near
 from attention_util import Batch, filled, queries
 
 pytestmark = pytest.mark.gpu
@@ -17,7 +17,7 @@ DTYPES = ("bfloat16", "float16")
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("sizes,dim", (([(90, 1), (200, 1)], 64), ([(300, 3)], 256), ([(9001, 1)], 128)))
+@pytest.mark.parametrize("sizes,dim", (([(90, 1), (200, 1)], 64), ([(300, 3)], 256), ([(9001, 1)], 128), ([(90, 60), (600, 60)], 64), ([(300, 70)], 128), ([(4500, 80)], 64), ([(700, 50)], 256)))
 def test_scores_of_any_size(fmt, dtype, sizes, dim):
     """Where one score is further above the others than they are off by, its token's value is the answer, whatever the
     scores' size: 2^x counts lifts and exponents of rows beside them."""
@@ -43,6 +43,112 @@ def test_scores_of_any_size(fmt, dtype, sizes, dim):
                     assert (off[sure] <= 0).all(), (power, sign, b, i)
                     alone += sure.sum()
             assert alone > 0.8 * batch.tokens * 2 or power < 15, (power, alone)
+
+
+def stored(batch, heads, dim, fmt, factors, seed=0):
+    """(cache, values) of random rows times factors[b] (2, heads, length, dim or 1)."""
+    it = iter(factors)
+    return filled(batch, heads, dim, fmt, seed, lambda rng, shape: next(it))
+
+
+SIZES = {"few": [(300, 1), (900, 3), (70, 10)], "many": [(300, 300), (900, 120), (70, 70)], "long": [(5000, 30)]}
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("sizes,dim", (("few", 128), ("many", 64), ("many", 128), ("many", 256), ("long", 96)))
+@pytest.mark.parametrize("far", (12, 45, 100))
+def test_later_tokens_do_not_matter(fmt, dtype, sizes, dim, far):
+    """Keys, values or both of some tokens 2^far times the others': the queries before them are what they are without."""
+    batch = Batch(SIZES[sizes], 16)
+    low = 1.0 if far < 100 else 2.0**-50
+    factors, rows = [], []
+    for b, (length, n) in enumerate(batch.sizes):
+        f = np.full((2, 1, length, 1), low)
+        for i, j in enumerate(range(length - n // 2 - 1, length, 29)):
+            f[[0, 1] if i % 3 == 0 else i % 3 - 1, :, j] = low * 2.0**far
+        factors.append(f)
+        rows.append(batch.positions(b) < length - n // 2 - 1)
+    cache, values = stored(batch, 2, dim, fmt, factors)
+    q = queries(batch, 6, dim, dtype)
+    y = ddg.mx4_attention(q, cache, *batch.dev, scale=dim**-0.5 / low)
+    near(y, q, batch, values, dtype, scale=dim**-0.5 / low, rows=np.concatenate(rows))
+    if dtype == "float16" and low < 1:
+        assert not y[np.concatenate(rows)].any()  # 2^-50 in float16
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("sizes,dim", (("few", 128), ("many", 64), ("many", 128), ("many", 256), ("long", 96)))
+def test_tokens_that_the_window_has_left_do_not_matter(fmt, sizes, dim):
+    """Among the sinks' group, between sinks and window, just before it."""
+    batch = Batch(SIZES[sizes], 16)
+    window, sinks, factors = 64, 3, []
+    for b, (length, n) in enumerate(batch.sizes):
+        f = np.ones((2, 1, length, 1))
+        first = length - n
+        for j in (sinks, sinks + 1, 15, 16, first - window - 20, first - window):
+            if sinks <= j <= first - window:
+                f[:, :, j] = 2.0**70
+        factors.append(f)
+    cache, values = stored(batch, 2, dim, fmt, factors)
+    q = queries(batch, 6, dim, "bfloat16")
+    y = ddg.mx4_attention(q, cache, *batch.dev, window=window, sinks=sinks)
+    near(y, q, batch, values, "bfloat16", window, sinks)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("sizes,dim", (("few", 128), ("many", 64), ("many", 128), ("many", 256), ("long", 96)))
+@pytest.mark.parametrize("spread", (3, 10, 30, 60))
+def test_rows_of_any_size(fmt, dtype, sizes, dim, spread):
+    """Values over 2^+-spread, the larger ones with the smaller weights; keys of 2^-2 spread and more; rows of zeros."""
+    batch = Batch(SIZES[sizes], 16)
+    rng = np.random.default_rng(spread)
+    factors = []
+    for length, _ in batch.sizes:
+        f = np.stack((2.0 ** rng.integers(-2 * spread, 1, (2, length, 1)), 2.0 ** rng.integers(-spread, spread + 1, (2, length, 1))))
+        f[0, :, rng.integers(0, length, 9)] = 0
+        f[1, :, rng.integers(0, length, 9)] = 0
+        f[:, :, 128:256] *= rng.integers(0, 2)  # a tile of zeros or none
+        if dtype == "float16":
+            f[1] = np.minimum(f[1], 2.0**10)
+        factors.append(f)
+    cache, values = stored(batch, 2, dim, fmt, factors)
+    # keys that point away from every query where values are large: weights of about 2^-(their exponent) and less
+    q = queries(batch, 6, dim, dtype)
+    y = ddg.mx4_attention(q, cache, *batch.dev)
+    near(y, q, batch, values, dtype)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n", (1, 40, 300))
+def test_large_values_of_small_weight(fmt, n):
+    """A token of weight 2^-60 whose value is 2^60 or 2^64 times the others' counts as much as they do, or most."""
+    batch, dim = Batch([(300, n), (700, 2)], 16), 64
+    import torch
+    for power in (56, 60, 64):
+        cache = ddg.mx4_cache(batch.pages, 16, 1, dim, fmt)
+        values, x = [], np.zeros((batch.tokens, 1, dim))
+        k, v = [np.zeros((n_, 1, dim)) for n_, _ in batch.sizes], [np.zeros((n_, 1, dim)) for n_, _ in batch.sizes]
+        rng = np.random.default_rng(1)
+        for b, (length, _) in enumerate(batch.sizes):
+            v[b][:] = rng.choice((1.0, 1.5, 2.0, -3.0), v[b].shape)
+            k[b][:, 0, 0] = 0.0
+            for j in (0, 7, 130, 290):
+                if j < length:
+                    k[b][j, 0, 0] = -6.0  # scores 10 below the others' in the exponent of e, 6 times
+                    v[b][j] *= 2.0**power
+        starts = np.cumsum([0] + [len(a) for a in k]).astype(np.int32)
+        every = [torch.from_numpy(starts).cuda(), batch.dev[1], batch.dev[2]]
+        flat = [torch.from_numpy(np.concatenate(t)).float().cuda() for t in (k, v)]
+        ddg.mx4_cache_append(cache, *flat, *every)
+        kk, vv = (t.double().cpu().numpy() for t in ddg.mx4_cache_read(cache, int(starts[-1]), *every, dtype=torch.float32))
+        values = [np.stack((kk[a:e], vv[a:e])).transpose(0, 2, 1, 3) for a, e in zip(starts, starts[1:])]
+        x[..., 0] = 1.0
+        q = torch.from_numpy(x).bfloat16().cuda()
+        scale = 60 * np.log(2.0) / 6.0
+        y = ddg.mx4_attention(q, cache, *batch.dev, scale=scale)
+        near(y, q, batch, values, "bfloat16", scale=scale)
 
 
 def test_no_wait_gave_up_in_these():
