@@ -25,11 +25,12 @@
 //
 // The codes become 16-bit floating point by one conversion for two, the block's
 // scale one packed multiplication for two, exactly: E4M3 times E2M1 has 6 bits;
-// mxfp4 scales are relative to the row's largest, times 2^13 (a block 2^27 below it
-// counts as 0, below the rounding of the 32-bit sum).  Queries are scaled by a power
-// of two into the range of 16 bits; what they lose is 2^-36 of their row's largest.
-// Weights are rounded to 16 bits (11 significant) for bfloat16 outputs, and what that
-// leaves enters the sum too for float16 ones, whose own rounding is as small.
+// mxfp4 scales are relative to the row's largest, times 2^13, exact down to a block 2^36
+// below it and 0 from 2^38 on: what a channel of its own may show, for an output's elements
+// sum one block of each token.  Queries are scaled by a power of two into the range of 16
+// bits; what they lose is 2^-36 of their row's largest.  Weights are rounded to 16 bits
+// (11 significant) for bfloat16 outputs, and what that leaves enters the sum too for
+// float16 ones, whose own rounding is as small.
 #include <algorithm>
 #include <atomic>
 
@@ -164,7 +165,7 @@ struct Stage {
 };
 
 // The scale bytes of N blocks of a row with exponent e as halves, each in both halves
-// of a word.  (mxfp4: t 2^10 in both is one multiplication.)
+// of a word.
 template <int FMT, int N>
 __device__ __forceinline__ void half_scales(const uint8_t* bytes, int e, uint32_t (&h)[N]) {
 #pragma unroll
@@ -179,8 +180,8 @@ __device__ __forceinline__ void half_scales(const uint8_t* bytes, int e, uint32_
             const auto half = [&](uint32_t byte) {
                 // at most 2^kMxLift, which is what the row's own exponent gives its largest: bytes that do not belong
                 // together, of rows that no token has, stay finite (their weight is 0, and 0 times infinity is NaN)
-                const int t = min(max((int)byte - e - 127 + kMxLift + 15, 0), kMxLift + 15);
-                return byte == 255u ? 0x7fff7fffu : (uint32_t)t * 0x04000400u;
+                const float power = exp2_int(min(max((int)byte - e - 127 + kMxLift, -30), kMxLift));
+                return byte == 255u ? 0x7fff7fffu : half2_of(power, power);
             };
             h[b] = half(two & 0xffu);
             if (b + 1 < N) h[b + 1] = half(two >> 8);

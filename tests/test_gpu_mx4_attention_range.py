@@ -151,5 +151,30 @@ def test_large_values_of_small_weight(fmt, n):
         near(y, q, batch, values, "bfloat16", scale=scale)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("sizes,dim", (("few", 128), ("many", 64), ("many", 128), ("many", 256), ("long", 200)))
+def test_blocks_of_very_different_sizes(fmt, dtype, sizes, dim):
+    """Blocks of a row down to 2^-27 of its largest (nvfp4 has 2^-17): each channel to its own size, and keys whose
+    query looks at the small blocks only."""
+    batch = Batch(SIZES[sizes], 16)
+    block = 32 if fmt == "mxfp4" else 16
+    least = -27 if fmt == "mxfp4" else -12
+    rng = np.random.default_rng(3)
+    powers = np.linspace(0, least, -(-dim // block)).round()
+    factors = []
+    for length, _ in batch.sizes:
+        f = 2.0 ** np.broadcast_to(np.repeat(powers, block)[:dim], (2, 2, length, dim)) * 2.0 ** rng.integers(-4, 1, (2, 2, length, 1))
+        factors.append(f * (2.0**8 if dtype == "float16" else 1.0))
+    cache, values = stored(batch, 2, dim, fmt, factors)
+    q = queries(batch, 4, dim, dtype)
+    y = ddg.mx4_attention(q, cache, *batch.dev)
+    near(y, q, batch, values, dtype)
+    if dtype == "bfloat16":  # a query of the least block alone, as large as the keys there are small
+        q[..., : (len(powers) - 1) * block] = 0
+        q *= 2.0**-least
+        near(ddg.mx4_attention(q, cache, *batch.dev), q, batch, values, dtype)
+
+
 def test_no_wait_gave_up_in_these():
     assert ddg.wait_timeouts() == 0
