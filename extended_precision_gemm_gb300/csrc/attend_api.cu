@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <numeric>
 
 #include "attend.cuh"
 #include "entry.cuh"
@@ -33,7 +34,33 @@ struct Heads {
         return ((tokens - 1) * (tokens > 1 ? per_token : 0) + (heads - 1) * (heads > 1 ? per_head : 0) + dim) * elem;
     }
 };
-bool meet(const Heads& a, const Heads& b) { return overlap(a.p, a.bytes(), b.p, b.bytes()); }
+// Runs of `own` bytes from p on, every `period` bytes (0: one run) or at some of these places.
+struct Runs {
+    int64_t period, own;
+};
+// An array as runs of its heads' elements, or of what lies between two steps of its longer stride.
+Runs runs_of(const Heads& a, bool longer) {
+    const int64_t t = a.tokens > 1 ? a.per_token : 0, h = a.heads > 1 ? a.per_head : 0;
+    if (!longer) return Runs{std::gcd(t, h) * a.elem, a.dim * a.elem};
+    const bool token = t >= h;
+    return Runs{(token ? t : h) * a.elem, ((token ? (a.heads - 1) * h : (a.tokens - 1) * t) + a.dim) * a.elem};
+}
+// Whether two arrays have an element in common, or could have: parts of one array side by side, heads of a token or
+// halves of a head, have none although each reaches over the other.
+bool meet(const Heads& a, const Heads& b) {
+    if (!overlap(a.p, a.bytes(), b.p, b.bytes())) return false;
+    for (const bool la : {false, true}) {
+        for (const bool lb : {false, true}) {
+            const Runs x = runs_of(a, la), y = runs_of(b, lb);
+            const int64_t period = std::gcd(x.period, y.period);
+            if (period == 0) continue;
+            int64_t from_x = ((int64_t)((uintptr_t)b.p - (uintptr_t)a.p)) % period;
+            if (from_x < 0) from_x += period;
+            if (x.own <= from_x && from_x + y.own <= period) return false;
+        }
+    }
+    return true;
+}
 
 ddgemm_status check_cache(const ddgemm_mx4_cache* c, CacheView& v) {
     if (c == nullptr || !known_format(c->format) || c->pages < 0 || c->heads < 1 || c->head_dim < 1) return DDGEMM_ERR_INVALID_ARG;
@@ -205,11 +232,7 @@ ddgemm_status dd_mx4_cache_read(const ddgemm_mx4_cache* cache, const ddgemm_batc
     const Heads hk{k, T, H, D, k_token, k_head, type_bytes(type)}, hv{v, T, H, D, v_token, v_head, type_bytes(type)};
     if (!hk.sound() || !hv.sound()) return DDGEMM_ERR_INVALID_ARG;
     if (T == 0 || batch->batch == 0) return DDGEMM_OK;
-    if (meet(hk, hv)) {  // the two may be parts of one array: heads side by side
-        const bool same = k_token == v_token && k_head == v_head && T > 1;
-        const int64_t apart = std::abs((intptr_t)k - (intptr_t)v) / type_bytes(type), own = (H - 1) * (H > 1 ? k_head : 0) + D;
-        if (!same || apart < own || apart + own > k_token) return DDGEMM_ERR_INVALID_ARG;
-    }
+    if (meet(hk, hv)) return DDGEMM_ERR_INVALID_ARG;
     for (const Heads* h : {&hk, &hv})
         if (overlaps_cache(g.cache, h->p, h->bytes()) || overlaps_batch(g.batch, h->p, h->bytes())) return DDGEMM_ERR_INVALID_ARG;
     g.type = type;

@@ -826,7 +826,8 @@ typedef struct {
  * tokens and heads (elements; the head dimension is contiguous, heads and tokens
  * do not overlap), y likewise.  positions: one per token, int64 (wide = 1) or int32.
  * inverse = 1: the transposed rotation, dx from dy.  y may be x itself (the same
- * pointer and strides); otherwise they do not overlap.  Sums in 32 bits, cos and
+ * pointer and strides); otherwise they have no element in common (heads side by side or
+ * halves of heads of one array have none).  Sums in 32 bits, cos and
  * sin correctly rounded but for a few in 10^3, one rounding to `type`.
  */
 #define DDGEMM_MAX_HEADS 4096
