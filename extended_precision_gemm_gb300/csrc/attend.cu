@@ -216,7 +216,7 @@ struct Sequence {
 __device__ __forceinline__ Sequence sequence_at(const AttendArgs& a, int i) {
     const int s0 = a.b.starts[i], s1 = a.b.starts[i + 1];
     if (s0 < 0 || s1 > a.b.tokens || s1 <= s0 || !a.takes(s1 - s0)) return Sequence{0, 0, 0};
-    return Sequence{s0, s1 - s0, a.b.lengths[i]};
+    return Sequence{s0, s1 - s0, length_of(a.b, i)};
 }
 // The groups of tile `ct` of 8 columns, and (with count at least 1) its cost.
 __device__ __forceinline__ Groups tile_groups(const AttendArgs& a, const Sequence& s, int ct) {
@@ -770,7 +770,7 @@ __global__ void __launch_bounds__(128) join_kernel(const AttendArgs a, float lif
     if (s < 0 || a.b.starts[s] < 0 || a.b.starts[s + 1] <= token || a.b.starts[s + 1] > a.b.tokens || !a.takes(a.b.starts[s + 1] - a.b.starts[s])) return;
     // the item that the row is of, and its parts
     constexpr int ROWS = WIDTH == 256 ? 128 : 256;
-    const int s0 = a.b.starts[s], tokens = a.b.starts[s + 1] - s0, before = a.b.lengths[s] - tokens;
+    const int s0 = a.b.starts[s], tokens = a.b.starts[s + 1] - s0, before = length_of(a.b, s) - tokens;
     const int column = ((int)token - s0) * a.group + (int)(h % a.group), first = column / ROWS * ROWS, last = min(first + ROWS, tokens * a.group) - 1;
     const int splits = parts_of((groups_of(a.c, a.b, before + first / a.group, before + last / a.group, a.window, a.sinks).count + 7) / 8, a.splits);
     if (splits == 1) return;  // written as a whole

@@ -127,7 +127,7 @@ __device__ __forceinline__ Item item_of(const AttendArgs& a, int64_t t, int colu
     const int64_t s0 = b.starts[s], s1 = b.starts[s + 1];
     const int64_t column = (t - a.first_tile(s, (int)s0, columns)) * columns;
     if (s0 < 0 || s1 > b.tokens || !a.takes(s1 - s0) || column < 0 || column >= (s1 - s0) * a.group) return nothing;
-    return Item{s, (int)column, (int)min((int64_t)columns, (s1 - s0) * a.group - column), (int)s0, (int)(s1 - s0), b.lengths[s]};
+    return Item{s, (int)column, (int)min((int64_t)columns, (s1 - s0) * a.group - column), (int)s0, (int)(s1 - s0), length_of(b, s)};
 }
 
 // A part's R as one of the reference m (its own is m_of_part, and m is no less).

@@ -32,6 +32,9 @@ __device__ __forceinline__ int page_of(const CacheView& c, const BatchView& b, i
     return p >= 0 && p < c.pages ? p : -1;
 }
 
+// A sequence's tokens; any negative number as -1, so that no position behind it overflows.
+__device__ __forceinline__ int length_of(const BatchView& b, int sequence) { return max(b.lengths[sequence], -1); }
+
 // What a call's token is: its sequence (-1 for a token of none), position, and page (-1
 // where it has none in the cache).
 struct Place {
@@ -46,7 +49,7 @@ __device__ __forceinline__ Place place_of(const CacheView& c, const BatchView& b
         else high = mid;
     }
     if (low >= b.batch || starts[low] > t) return {-1, -1, -1};
-    const int position = b.lengths[low] - (starts[low + 1] - (int)t);
+    const int position = length_of(b, low) - (starts[low + 1] - (int)t);
     return {low, position, page_of(c, b, low, position)};
 }
 

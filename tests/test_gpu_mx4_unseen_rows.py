@@ -81,3 +81,25 @@ def test_page_tables_that_end_before_the_window(n, window, sinks, group):
         far[0] = length
         y = ddg.mx4_attention(q, cache, batch.dev[0], far, batch.dev[2], window=window, sinks=sinks)
         assert torch.isnan(y[:n]).all() and torch.equal(y[n:], want[n:]), length  # the same table, the same parts
+
+
+@pytest.mark.parametrize("n", (1, 5, 60, 700))
+@pytest.mark.parametrize("length", (-1, -5, -(1 << 28), -(1 << 31) + 3, -(1 << 31)))
+def test_lengths_far_below_zero(n, length):
+    """Every position is negative: nothing is written, read as NaN, and queries see nothing (lengths - n would overflow)."""
+    import torch
+    batch = Batch([(max(n, 40), n), (90, 2)], 16)
+    cache, values = filled(batch, 2, 64, "nvfp4")
+    before = [t.clone() for t in (cache.codes, cache.scales, cache.exponents)]
+    lengths = batch.dev[1].clone()
+    lengths[0] = length
+    plan = (batch.dev[0], lengths, batch.dev[2])
+    k, v = (torch.randn(batch.tokens, 2, 64, device="cuda").bfloat16() for _ in range(2))
+    got = torch.stack(ddg.mx4_cache_read(cache, batch.tokens, *plan))
+    assert torch.isnan(got[:, :n]).all() and torch.isfinite(got[:, n:]).all()
+    for window, sinks in ((0, 0), (20, 3)):
+        y = ddg.mx4_attention(queries(batch, 8, 64, "bfloat16"), cache, *plan, window=window, sinks=sinks)
+        assert not y[:n].any() and torch.isfinite(y[n:]).all() and y[n:].any()
+    starts = torch.tensor([0, n, n], dtype=torch.int32, device="cuda")  # of the first sequence alone
+    ddg.mx4_cache_append(cache, k[:n], v[:n], starts, lengths, batch.dev[2], rotary=ddg.rotary_table(64))
+    assert all(torch.equal(a, b) for a, b in zip(before, (cache.codes, cache.scales, cache.exponents)))
