@@ -149,7 +149,7 @@ def _rotate(x, name, positions, table, inverse, out, stream):
     code = _type(x.dtype, name)
     device = x.get_device()
     if not isinstance(positions, _lp._Tensor) or positions.dim() != 1 or positions.element_size() not in (4, 8) \
-            or positions.is_floating_point() or positions.is_complex():
+            or positions.is_floating_point() or positions.is_complex() or (positions.element_size() == 4 and positions.dtype is not _lp._int32):
         raise TypeError("positions must be a 1-D int32 or int64 CUDA tensor")
     if positions.shape[0] != T or not positions.is_contiguous():
         raise ValueError("positions must be contiguous, one for each token")
