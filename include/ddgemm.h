@@ -906,10 +906,11 @@ ddgemm_status dd_mx4_cache_read(const ddgemm_mx4_cache* cache, const ddgemm_batc
  * The cache's values enter exactly, whatever the sizes of other rows, but for mxfp4
  * blocks more than 2^27 below their row's largest and rows with the exponent -127 (values
  * below 2^-124), which may count as 0; elements of a bfloat16 query are rounded to 2^-36
- * of its largest.  Scores, softmax and sums are in 32 bits, weights have 11 significant
- * bits (bfloat16) or 22 (float16), where they are 2^-19 or more of what counts most.  What
- * a token holds that a query does not see, infinities, NaN and numbers of any size, does
- * not reach it.
+ * of its largest.  Scores, softmax and sums are in 32 bits.  Weights have 11 significant
+ * bits (bfloat16) or 22 (float16) while they, times the size of their value's row, are
+ * 2^-19 or more of the largest such product (a row of zeros as of any size); smaller ones
+ * lose bits, and below 2^-30 they may count as 0.  What a token holds that a query does
+ * not see, infinities, NaN and numbers of any size, does not reach it.
  */
 ddgemm_status dd_mx4_attention(const ddgemm_mx4_cache* cache, const ddgemm_batch* batch, int type, int64_t q_heads,
                                const void* q, int64_t q_token, int64_t q_head, int64_t window, int64_t sinks,

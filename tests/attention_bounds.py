@@ -17,7 +17,8 @@ def near(y, q, batch, values, dtype, window=0, sinks=0, scale=None, rows=None):
     sums over the tokens (2^-23 for each 16 of them, and the joining) and, where it is below 2^-14 of the 16-bit range,
     by 2^-25 of that: the token that counts most has 2^-6 at least (lifted by 2^7; references are rounded up, 2, values'
     exponents follow late, 2^3, and a tile's are within 2^9), so by 2^-19 of what that one adds, times the size of its
-    own element relative to its row.  Then the output's rounding."""
+    own element relative to its row.  (A row of zeros has no exponent: its weight counts as that of the largest row, as
+    what comes next to it has 2^-25 of the range below its weight.)  Then the output's rounding."""
     y = y.double().cpu().numpy()
     qn = q.double().cpu().numpy()
     heads, group, dim = values[0].shape[1], q.shape[1] // values[0].shape[1], q.shape[2]
@@ -44,7 +45,7 @@ def near(y, q, batch, values, dtype, window=0, sinks=0, scale=None, rows=None):
                 w, off = w / z, (up - w) / z
                 off = off + w * off.sum(1, keepdims=True) + w * (weight + 3 * 2.0**-21 + (length / 16 + 64) * 2.0**-23)
                 size = np.abs(v)
-                most = np.maximum(size.max(1), 1e-300)
+                most = np.where(size.any(1), size.max(1), max(size.max(), 1e-300))
                 want = w @ v
                 err = off @ size + 2.0**-19 * (w * most).max(1, keepdims=True) * (size / most[:, None]).sum(0)
                 bound = err * 1.01 + UNIT[dtype] * (np.abs(want) + err) + 2.0**-24 * (dtype == "float16") + 2.0**-133
