@@ -45,18 +45,8 @@ constexpr float kLag = 8.0f;    // references follow when they are exceeded by m
 constexpr float kLift = 7.0f;   // weights are up to 2^(8 + 7), below the largest float16
 constexpr int kMxLift = 13;     // mxfp4 scales relative to the row's largest, times 2^13
 
-__device__ __forceinline__ uint32_t half2_of(float a, float b) {  // a in the low half
-    uint32_t w;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
-    return w;
-}
 __device__ __forceinline__ float low_half(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(w & 0xffffu))); }
 __device__ __forceinline__ float high_half(uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(w >> 16))); }
-__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
 // Byte i of w, two codes, as two halves.
 template <int I>
 __device__ __forceinline__ uint32_t codes2(uint32_t w) {

@@ -63,6 +63,17 @@ __device__ __forceinline__ float power2(float x) {
     return y;
 }
 
+__device__ __forceinline__ uint32_t half2_of(float a, float b) {  // a in the low half
+    uint32_t w;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
+    return w;
+}
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // A reference that may be minus infinity (nothing seen yet) as a number to subtract.
 __device__ __forceinline__ float reference(float m) { return m == minus_infinity() ? 0.0f : m; }
 

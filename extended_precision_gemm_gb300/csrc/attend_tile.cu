@@ -96,16 +96,6 @@ struct Raw {
     uint16_t scales[PASSES];
 };
 
-__device__ __forceinline__ uint32_t half2_of(float a, float b) {  // a in the low half
-    uint32_t w;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(b), "f"(a));
-    return w;
-}
-__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
 // Eight codes as four pairs of halves.
 __device__ __forceinline__ uint4 halves_of(uint32_t w) {
     uint4 h;
