@@ -16,12 +16,12 @@
 // end cuts leaves parts, which join_cut_kernel adds.
 //
 // Measured (bfloat16): 64 sequences of 100 to 8192 tokens, 8 heads of 128, 8 queries each,
-// mxfp4: 101 us for 291 MB (2.9 TB/s); one of 131071, nvfp4: 47 us for 153 MB, 40 of them
-// here.  Bound by issue and the latency of its own instructions: a group takes 362
+// mxfp4: 103 us for 291 MB (2.8 TB/s); one of 131071, nvfp4: 48 us for 153 MB, 41 of them
+// here.  Bound by issue and the latency of its own instructions: a group takes 370
 // instructions, of which 140 run at half rate (conversions of codes, products with
-// scales, movmatrix), by 12 warps an SM (157 registers).  A fourth CTA costs more
+// scales, movmatrix), by 12 warps an SM (161 registers).  A fourth CTA costs more
 // instructions than its warps give, whole rows of codes at a time and 16 tokens a round
-// took 53 us for 47.
+// took 53 us where this form took 47.
 //
 // The codes become 16-bit floating point by one conversion for two, the block's
 // scale one packed multiplication for two, exactly: E4M3 times E2M1 has 6 bits;
@@ -30,7 +30,8 @@
 // sum one block of each token.  Queries are scaled by a power of two into the range of 16
 // bits; what they lose is 2^-36 of their row's largest.  Weights are rounded to 16 bits
 // (11 significant) for bfloat16 outputs, and what that leaves enters the sum too for
-// float16 ones, whose own rounding is as small.
+// float16 ones, whose own rounding is as small.  (22 bits for bfloat16 too: 108 and 51 us
+// for 103 and 48, and the error against 64 bits the same 0.0017, the output's rounding.)
 #include <algorithm>
 #include <atomic>
 
@@ -946,7 +947,7 @@ auto with_kernel(const AttendArgs& a, int type, F f) {
 
 // Short sequences (as far as the page table and the window say) in few enough items: a
 // cluster for each, of up to 8 CTAs with 256 tokens or more, 512 at most, all on the SMs at
-// once.  (523 tokens, 8 heads: 9.8 us, 14.7 as runs and a second launch; 288 items of 1036
+// once.  (523 tokens, 8 heads: 10.1 us, 14.7 as runs and a second launch; 288 items of 1036
 // tokens 24 us in two rounds, 18.5 as runs.)
 void plan_attend_columns(AttendArgs& a, int type) {
     const int ctas = with_kernel(a, type, [](auto t, auto w, auto f) { return resident<decltype(t), decltype(w)::value, decltype(f)::value>(); });

@@ -127,9 +127,9 @@ constexpr int64_t kColumnsMost = 48;
 // The host knows the sum of the sequences' rows alone.  Where their average is more, or
 // the tokens beyond one for each slot of the batch are more than 512 rows, both kernels run,
 // each on its sequences.  127 single tokens and 128 of one further sequence, 4000 in the
-// cache, 8 heads: 201 us, 310 by the kernel for few alone; 1024 of that sequence: 321 us,
+// cache, 8 heads: 208 us, 299 by the kernel for few alone; 1024 of that sequence: 320 us,
 // 706 by the other alone.  What it costs where no sequence has many: 32 of 5 tokens each
-// 188 us, 170 by the kernel for few alone.  Slots without tokens hide a part from this rule:
+// 194 us, 172 by the kernel for few alone.  Slots without tokens hide a part from this rule:
 // 255 tokens behind 4000, in 256 slots, are the kernel for few's, 353 us (112 in a slot of
 // their own).  To run both wherever all tokens could be of one sequence takes 138 us there,
 // but costs batches of single tokens more: 65 of 4000 105 us for 83, 1024 of 100 137 for 112.

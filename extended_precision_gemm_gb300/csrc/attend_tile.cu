@@ -22,18 +22,20 @@
 // another task looks at the exponents; an item with rows further apart, or with scores of
 // 2^21 and more, is done again behind the loops, a step after the other.
 //
-// Measured: a prompt of 8192 tokens, 32 heads over 8 of 128, mxfp4, bfloat16: 548 us, 1.0
+// Measured: a prompt of 8192 tokens, 32 heads over 8 of 128, mxfp4, bfloat16: 538 us, 1.0
 // PF/s (the simple kernel with mma.sync that was here first: 5008).  A pair of tiles takes
-// 4750 clocks for 128 tokens: each row's pass over its scores 2300 to 2550 (in four steps
+// 4700 clocks for 128 tokens: each row's pass over its scores about half of them (in four steps
 // of 32: wait for tensor memory, fma, 2^x, sum, round, store), then its products with V
 // and the next K, 1024, and the waits between; the tensor pipe is busy for 2048 of them, the
 // converters for 3000.  So the chain of one row's softmax and its MMAs bounds it.  Scores
 // of 64 tokens, in two buffers, would overlap them, but read Q from shared memory twice as
-// often: 593 us.  Three chunks of 100 to 700 tokens behind 2111 to 16000, 5 queries a head of
-// 256, nvfp4, float16: 336 us, 0.54 PF/s; the rest of the weights is a second product
-// there, K and V have one stage each, and the converters' stores (twice 64 KB a tile), the
-// MMAs' reads and the waits for each other's stage make 5900 clocks a tile.  Values in two
-// halves that come and go by themselves, or codes loaded a line at a time, changed nothing.
+// often: 593 us where this form took 548.  Three chunks of 100 to 700 tokens behind 2111 to
+// 16000, 5 queries a head of 256, nvfp4, float16: 340 us, 0.53 PF/s; the rest of the weights is a
+// second product there (22 bits for bfloat16 too: 8192 tokens in 711 us for 538, the error
+// against 64 bits the same, the output's rounding), K and V have one stage each, and the
+// converters' stores (twice 64 KB a tile), the MMAs' reads and the waits for each other's stage
+// make 5900 clocks a tile.  Values in two halves that come and go by themselves, or codes
+// loaded a line at a time, changed nothing.
 #include <algorithm>
 
 #include "attend.cuh"
@@ -613,8 +615,8 @@ __device__ __forceinline__ void careful_item(const AttendArgs& a, const Item& it
 }
 
 // The two ways in which the kernel calls it.  A call costs its loops registers, more or fewer by what is held over them
-// (us, against a copy without: 8192 tokens of width 128: 531; all found anew 543, handed over 550; chunks of width 256:
-// 339; 351 and 344; a kernel of its own behind this one: 5 us more for every call).
+// (us, against a copy without: 8192 tokens of width 128: 532; all found anew 539, handed over 550; chunks of width 256:
+// 339; 351 and 344; a kernel of its own behind this one: 5 us more for every call, 22 for 17 of 60 tokens).
 template <typename T, int WIDTH, int FMT>
 __device__ __noinline__ void careful_item_anew(const AttendArgs& a, uint32_t smem, const uint32_t* tmem_slot, uint32_t done, int16_t (*exponents)[128]) {
     const int head = (int)(blockIdx.x % a.c.heads);
@@ -642,7 +644,7 @@ __global__ void __launch_bounds__(Shape<WIDTH>::THREADS, 1) attend_tile_kernel(c
     __shared__ int rows[kRing][8];  // of groups of keys, in 16s, -1 where there is no page
     __shared__ int16_t exponents[kRing][2][128];  // of keys and values
     __shared__ int any_nan;                       // in values
-    __shared__ bool cut;                          // the item has other parts (here, not in a register all the way: 547 us for 560 of 8192 tokens)
+    __shared__ bool cut;                          // the item has other parts (here, not in a register all the way: 13 us less of 560, 8192 tokens)
     __shared__ __align__(16) int largest[2][2][4];  // of the tiles in turn
     __shared__ bool far_rows, large_scores;         // what the loops are not for
 

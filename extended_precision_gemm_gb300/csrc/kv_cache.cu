@@ -7,10 +7,10 @@
 // between lanes.  Keys may be rotated on the way in: in 32 bits and what they leave
 // (rotary.cuh), so that a value is rounded once, to its code.
 //
-// A prompt of 8192 tokens, 8 heads of 128, bfloat16, mxfp4: written with rotation 28 us,
-// without 18, read back 13 (42 MB each way, 6.3 us of a copy).  Bound by instructions: 22
+// A prompt of 8192 tokens, 8 heads of 128, bfloat16, mxfp4: written with rotation 29 us,
+// without 20, read back 13 (42 MB each way, 6.3 us of a copy).  Bound by instructions: 22
 // million for a written batch, of which the rotation and what it leaves are 10 us; at 78
-// registers three blocks share an SM.  64 single tokens 3 us each way.
+// registers three blocks share an SM.  32 single tokens, nvfp4: 3.7 us written with rotation, 2.7 read.
 #include "eight.cuh"
 #include "kv_cache.cuh"
 #include "rotary.cuh"
