@@ -176,5 +176,60 @@ def test_blocks_of_very_different_sizes(fmt, dtype, sizes, dim):
         near(ddg.mx4_attention(q, cache, *batch.dev), q, batch, values, dtype)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dim", (64, 96, 256))
+def test_what_else_such_items_have(fmt, dim):
+    """Items with rows far apart: NaN in values of a token and a page that is not there reach the queries that see them
+    alone, rows of no sequence stay, unaligned and strided operands, equal bits call for call and in a captured graph."""
+    import torch
+    batch = Batch([(300, 200), (1100, 90), (90, 60)], 16, lead=2, tail=3)
+    factors = []
+    for length, _ in batch.sizes:
+        f = np.ones((2, 1, length, 1))
+        f[:, :, length - 7] = 2.0**40
+        f[:, :, length // 2 :: 31] *= 2.0**-20
+        factors.append(f)
+    cache, values = stored(batch, 2, dim, fmt, factors)
+    q = queries(batch, 8, dim, "bfloat16")
+    p = np.concatenate([np.full(batch.starts[0], -1)] + [batch.positions(b) for b in range(3)] + [np.full(3, -1)])
+    b_of = np.concatenate([np.full(batch.starts[0], -1)] + [np.full(n, b) for b, (_, n) in enumerate(batch.sizes)] + [np.full(3, -1)])
+    before = np.concatenate([[False] * batch.starts[0]] + [batch.positions(b) < length - 7 for b, (length, _) in enumerate(batch.sizes)] + [[False] * 3])
+    want = torch.full_like(q, 5.0)
+    ddg.mx4_attention(q, cache, *batch.dev, out=want)
+    near(want, q, batch, values, "bfloat16", rows=before)
+    assert (want[: batch.starts[0]] == 5).all() and (want[-3:] == 5).all()
+    # strides, and one element off 16 bytes
+    odd = torch.zeros(batch.tokens * 8 * (dim + 1) + 1, dtype=torch.bfloat16, device="cuda")[1:].view(batch.tokens, 8, dim + 1)
+    odd[..., :dim] = q
+    out = torch.full((8, batch.tokens, dim), 5.0, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    assert torch.equal(ddg.mx4_attention(odd[..., :dim], cache, *batch.dev, out=out), want)
+    ddg.mx4_attention(q, cache, *batch.dev, out=odd[..., :dim])
+    mine = slice(batch.starts[0], batch.starts[-1])
+    assert torch.equal(odd[mine, :, :dim], want[mine]) and not odd[..., dim].any()
+    graph, again = torch.cuda.CUDAGraph(), torch.full_like(q, 5.0)
+    with torch.cuda.graph(graph):
+        ddg.mx4_attention(q, cache, *batch.dev, out=again)
+    for _ in range(3):
+        again.fill_(5.0)
+        graph.replay()
+        assert torch.equal(again, want)
+    # NaN in a block of a token's values
+    size = 32 if fmt == "mxfp4" else 16
+    page, off = batch.place(0, 150)
+    cache.scales[page, 1, 1, off, 1] = 255 if fmt == "mxfp4" else 127
+    y = ddg.mx4_attention(q, cache, *batch.dev)
+    bad = torch.zeros_like(y, dtype=torch.bool)
+    bad[torch.from_numpy((b_of == 0) & (p >= 150)).cuda(), 4:, size : 2 * size] = True
+    assert torch.equal(torch.isnan(y[mine]), bad[mine]) and torch.equal(torch.where(bad, 0.0, y)[mine], torch.where(bad, 0.0, want)[mine])
+    # a page that is not there
+    table = batch.dev[2].clone()
+    table[1, 64] = -1  # tokens 1024 to 1039
+    y = ddg.mx4_attention(q, cache, *batch.dev[:2], table)
+    lost = torch.from_numpy((b_of == 1) & (p >= 1024)).cuda()
+    assert torch.isnan(y[lost]).all()
+    kept = torch.from_numpy(b_of >= 0).cuda() & ~lost
+    assert torch.equal(torch.isnan(y[kept]), bad[kept])
+
+
 def test_no_wait_gave_up_in_these():
     assert ddg.wait_timeouts() == 0
